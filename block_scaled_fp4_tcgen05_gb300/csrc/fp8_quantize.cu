@@ -1,0 +1,332 @@
+// fp8_quantize.cu -- BF16 -> 8-bit floating point codes (E4M3 / E5M2) with one
+// fp32 scale per 128 elements: along the rows (the operand of a forward
+// product), along the columns and transposed (the operand of a weight
+// gradient), gathered into expert order, and per 128 x 128 block (weights).
+//
+// Per block, with top the type's largest magnitude and a = max(max|x|, 2^-100):
+//   s = a / top (or the smallest power of two not below it),
+//   code = RNE(x * top / a) (or x / s), saturating.
+// 2^-100 keeps both quotients and the scale normal numbers, so a block of
+// zeros needs no case of its own.
+//
+// One CTA takes a tile of TR rows x 128 columns.  Thread (i, c) of 16 x 16 (or
+// 8 rows fewer per thread for rows alone) holds R consecutive rows of eight
+// columns in registers: X is read once however many outputs are asked for.  A
+// row's amax is a shuffle over the 16 threads of the row, a column's one over
+// the rows a thread holds, then over the CTA through shared memory.  The
+// transposed codes go through a shared-memory tile so that both outputs leave
+// in whole 128-byte lines.  HBM-bound: 2 bytes read and 1 written per element
+// and direction.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "qfp4_common.cuh"
+#include "sm103_ptx.cuh"
+
+namespace qfp4 {
+
+__device__ uint32_t g_status_fp8_quant = 0;
+
+int read_clear_status_fp8_quant(cudaStream_t s, uint32_t *out)
+{
+    uint32_t zero = 0;
+    if (cudaMemcpyFromSymbolAsync(out, g_status_fp8_quant, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s) !=
+        cudaSuccess)
+        return QFP4_ERR_CUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return QFP4_ERR_CUDA;
+    if (cudaMemcpyToSymbolAsync(g_status_fp8_quant, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, s) !=
+        cudaSuccess)
+        return QFP4_ERR_CUDA;
+    return cudaStreamSynchronize(s) == cudaSuccess ? QFP4_OK : QFP4_ERR_CUDA;
+}
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kFloor = 0x1p-100f;
+
+struct QuantParams {
+    const uint4 *X;             // [X_rows, K] BF16, 8 per uint4
+    const int32_t *row_index;   // [M] or NULL
+    int64_t X_rows;
+    int32_t M, K;
+    int32_t Mt;                 // ceil16(M): row length of Q_t
+    int32_t tiles_k;            // 128-column tiles: ceil(K / 128)
+    uint8_t *Q, *Q_t;
+    float *SF, *SF_t;
+};
+
+template <int TYPE> struct Fp8;
+template <> struct Fp8<QFP4_E4M3> { static constexpr float top = 448.0f; };
+template <> struct Fp8<QFP4_E5M2> { static constexpr float top = 57344.0f; };
+
+// codes of lo (low byte) and hi (high byte), nearest even, saturating, NaN kept
+template <int TYPE>
+__device__ __forceinline__ uint32_t encode2(float lo, float hi)
+{
+    uint16_t r;
+    if (TYPE == QFP4_E4M3) asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+struct Scale {
+    float s;        // what a code stands for
+    float inv;      // what an element is multiplied by
+};
+
+template <int TYPE, bool POW2>
+__device__ __forceinline__ Scale block_scale(float amax)
+{
+    const float a = fmaxf(amax, kFloor);
+    const float t = __fdiv_rn(a, Fp8<TYPE>::top);
+    if (!POW2) return {t, __fdiv_rn(Fp8<TYPE>::top, a)};
+    // t is normal (or inf): the power of two not below it by its exponent field
+    const uint32_t u = __float_as_uint(t);
+    const uint32_t e = (u >> 23) + ((u & 0x7FFFFFu) != 0 ? 1u : 0u);
+    return {__uint_as_float(e << 23), e >= 254u ? 0.0f : __uint_as_float((254u - e) << 23)};
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+enum { kRows = 1, kCols = 2, kBlock = 4 };
+
+// R rows per thread: the tile is 16 R rows x 128 columns.  Thread 16 i + c
+// holds rows R i .. R i + R - 1 and columns 8 c .. 8 c + 7 of the tile.
+// WHAT: kRows and / or kCols, or kBlock with or without kCols (R = 8).
+template <int TYPE, bool POW2, int WHAT, int R>
+__global__ void __launch_bounds__(kThreads)
+fp8_quantize_kernel(const QuantParams p)
+{
+    constexpr bool ROWS = (WHAT & kRows) != 0, COLS = (WHAT & kCols) != 0, BLOCK = (WHAT & kBlock) != 0;
+    constexpr int TR = 16 * R;
+    static_assert(R == 8 || WHAT == kRows, "column and block scales need 128-row tiles");
+    // transposed tile: 128 columns of 16 units of eight rows' codes.  Unit i of
+    // column 8 c + j lies at i ^ c ^ (j & 1), so that neither the writes (16
+    // values of c at one j) nor the reads (four columns of one c) collide.
+    __shared__ __align__(16) uint2 s_t[COLS ? 128 * 16 : 1];
+    __shared__ float s_amax[COLS && !BLOCK ? 8 * 128 : 8];
+
+    const int tid = threadIdx.x;
+    const int c = tid & 15, i = tid >> 4, warp = tid >> 5, lane = tid & 31;
+    const int32_t mtile = blockIdx.x / p.tiles_k, kblock = blockIdx.x - mtile * p.tiles_k;
+    const int32_t m0 = mtile * TR + R * i;
+    const int32_t col = kblock * 128 + 8 * c;
+    const bool col_ok = col < p.K;          // K % 16 == 0: all eight or none
+    const int64_t group = blockIdx.y;       // kBlock: one matrix per group
+    const int64_t mat = BLOCK ? group * p.M * static_cast<int64_t>(p.K) : 0;
+
+    pdl_wait();
+    pdl_launch_dependents();
+
+    uint4 x[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int32_t m = m0 + r;
+        int64_t row = m;
+        bool ok = col_ok && m < p.M;
+        if (!BLOCK && p.row_index && ok) {
+            row = p.row_index[m];
+            if (row >= p.X_rows) {
+                if (c == 0) atomicOr(&g_status_fp8_quant, static_cast<uint32_t>(kStatusBadGroup));
+                ok = false;
+            }
+            if (row < 0) ok = false;
+        }
+        x[r] = make_uint4(0, 0, 0, 0);
+        if (ok) x[r] = ld_nc_v4(p.X + (mat + row * p.K + col) / 8);
+    }
+
+    float ra[R];            // amax of this thread's part of each row
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+        float a = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a = fmaxf(a, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
+        ra[r] = a;
+    }
+
+    Scale block{};
+    if (BLOCK) {
+        float a = 0.0f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) a = fmaxf(a, ra[r]);
+        for (int d = 16; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+        if (lane == 0) s_amax[warp] = a;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 8; ++w) a = fmaxf(a, s_amax[w]);
+        block = block_scale<TYPE, POW2>(a);
+        const int32_t tiles_m = gridDim.x / p.tiles_k;
+        if (tid == 0) {
+            p.SF[(group * tiles_m + mtile) * p.tiles_k + kblock] = block.s;
+            if (COLS) p.SF_t[(group * p.tiles_k + kblock) * tiles_m + mtile] = block.s;
+        }
+    }
+
+    if (ROWS || BLOCK) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            Scale s = block;
+            if (ROWS) {
+                float a = ra[r];
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+                s = block_scale<TYPE, POW2>(a);
+            }
+            const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+            uint32_t q[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                q[j] = encode2<TYPE>(__fmul_rn(bf16_lo(w[j]), s.inv), __fmul_rn(bf16_hi(w[j]), s.inv));
+            const int32_t m = m0 + r;
+            if (col_ok && m < p.M)
+                *reinterpret_cast<uint2 *>(p.Q + mat + static_cast<int64_t>(m) * p.K + col) =
+                    make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+            if (ROWS && c == 0 && m < p.M) p.SF[static_cast<int64_t>(kblock) * p.M + m] = s.s;
+        }
+    }
+
+    if (COLS) {
+        float inv[8];
+        if (BLOCK) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) inv[j] = block.inv;
+        } else {
+            float ca[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ca[j] = 0.0f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    ca[2 * j] = fmaxf(ca[2 * j], fabsf(bf16_lo(w[j])));
+                    ca[2 * j + 1] = fmaxf(ca[2 * j + 1], fabsf(bf16_hi(w[j])));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                ca[j] = fmaxf(ca[j], __shfl_xor_sync(0xffffffffu, ca[j], 16));
+                if (lane < 16) s_amax[warp * 128 + 8 * c + j] = ca[j];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float a = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) a = fmaxf(a, s_amax[w * 128 + 8 * c + j]);
+                const Scale s = block_scale<TYPE, POW2>(a);
+                inv[j] = s.inv;
+                if (i == 0 && col_ok) p.SF_t[static_cast<int64_t>(mtile) * p.K + col + j] = s.s;
+            }
+        }
+        // codes of column 8 c + j, rows R i .. R i + 7, as eight bytes of the
+        // transposed tile
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const uint32_t w = j < 2 ? x[r % R].x : j < 4 ? x[r % R].y : j < 6 ? x[r % R].z : x[r % R].w;
+                v[r] = __fmul_rn((j & 1) ? bf16_hi(w) : bf16_lo(w), inv[j]);
+            }
+            s_t[(8 * c + j) * 16 + (i ^ c ^ (j & 1))] =
+                make_uint2(encode2<TYPE>(v[0], v[1]) | encode2<TYPE>(v[2], v[3]) << 16,
+                           encode2<TYPE>(v[4], v[5]) | encode2<TYPE>(v[6], v[7]) << 16);
+        }
+        __syncthreads();
+        const int64_t mat_t = BLOCK ? group * p.K * static_cast<int64_t>(p.Mt) : 0;
+#pragma unroll
+        for (int f = tid; f < 128 * 8; f += kThreads) {
+            const int tc = f >> 3, part = f & 7;
+            const int32_t k = kblock * 128 + tc, m = mtile * 128 + 16 * part;
+            const int at = (2 * part) ^ (tc >> 3) ^ (tc & 1);
+            const uint2 lo = s_t[tc * 16 + at], hi = s_t[tc * 16 + (at ^ 1)];
+            if (k < p.K && m < p.Mt)
+                *reinterpret_cast<uint4 *>(p.Q_t + mat_t + static_cast<int64_t>(k) * p.Mt + m) =
+                    make_uint4(lo.x, lo.y, hi.x, hi.y);
+        }
+    }
+}
+
+template <int TYPE, bool POW2, int WHAT, int R>
+int launch(const QuantParams &p, int64_t groups, cudaStream_t s)
+{
+    const int64_t tiles = (static_cast<int64_t>(p.M) + 16 * R - 1) / (16 * R) * p.tiles_k;
+    if (tiles > INT32_MAX) return QFP4_ERR_UNSUPPORTED;
+    return launch_status(launch_pdl(fp8_quantize_kernel<TYPE, POW2, WHAT, R>,
+                                    dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(groups)), dim3(kThreads),
+                                    0, s, p));
+}
+
+template <int TYPE, bool POW2>
+int launch_what(const QuantParams &p, int what, int64_t groups, cudaStream_t s)
+{
+    switch (what) {
+    case kRows: return launch<TYPE, POW2, kRows, 8>(p, groups, s);
+    case kCols: return launch<TYPE, POW2, kCols, 8>(p, groups, s);
+    case kRows | kCols: return launch<TYPE, POW2, kRows | kCols, 8>(p, groups, s);
+    case kBlock: return launch<TYPE, POW2, kBlock, 8>(p, groups, s);
+    default: return launch<TYPE, POW2, kBlock | kCols, 8>(p, groups, s);
+    }
+}
+
+int launch_any(int type, int scale, const QuantParams &p, int what, int64_t groups, cudaStream_t s)
+{
+    const bool pow2 = scale == QFP4_SCALE_POW2;
+    if (type == QFP4_E4M3)
+        return pow2 ? launch_what<QFP4_E4M3, true>(p, what, groups, s)
+                    : launch_what<QFP4_E4M3, false>(p, what, groups, s);
+    return pow2 ? launch_what<QFP4_E5M2, true>(p, what, groups, s)
+                : launch_what<QFP4_E5M2, false>(p, what, groups, s);
+}
+
+bool types_ok(int type, int scale)
+{
+    return (type == QFP4_E4M3 || type == QFP4_E5M2) && (scale == QFP4_SCALE_FP32 || scale == QFP4_SCALE_POW2);
+}
+
+constexpr int64_t kMaxSize = int64_t{1} << 30;
+
+}  // namespace
+}  // namespace qfp4
+
+using namespace qfp4;
+
+extern "C" int qfp4_fp8_quantize(int type, int scale, const void *X_bf16, int64_t X_rows, const int32_t *row_index,
+                                 int64_t M, int64_t K, void *Q, float *SF, void *Q_t, float *SF_t, void *stream)
+{
+    if (!types_ok(type, scale) || M < 0 || K < 0 || X_rows < 0) return QFP4_ERR_INVALID_ARG;
+    if (!row_index && X_rows != M) return QFP4_ERR_INVALID_ARG;
+    if (K % 16 != 0 || M > kMaxSize || K > kMaxSize) return QFP4_ERR_UNSUPPORTED;
+    if (M == 0 || K == 0) return QFP4_OK;
+    if ((Q == nullptr) != (SF == nullptr) || (Q_t == nullptr) != (SF_t == nullptr) || (!Q && !Q_t) ||
+        (!X_bf16 && X_rows > 0))
+        return QFP4_ERR_INVALID_ARG;
+    if (!aligned16(X_bf16) || !aligned16(Q) || !aligned16(Q_t) || !aligned4(SF) || !aligned4(SF_t) ||
+        !aligned4(row_index))
+        return QFP4_ERR_MISALIGNED;
+    const QuantParams p{static_cast<const uint4 *>(X_bf16), row_index, X_rows, static_cast<int32_t>(M),
+                        static_cast<int32_t>(K), static_cast<int32_t>((M + 15) / 16 * 16), static_cast<int32_t>((K + 127) / 128),
+                        static_cast<uint8_t *>(Q), static_cast<uint8_t *>(Q_t), SF, SF_t};
+    return launch_any(type, scale, p, (Q ? kRows : 0) | (Q_t ? kCols : 0), 1, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int qfp4_fp8_quantize_weight(int type, int scale, int64_t groups, const void *W_bf16, int64_t N, int64_t K,
+                                        void *Q, float *SF, void *Q_t, float *SF_t, void *stream)
+{
+    if (!types_ok(type, scale) || groups < 1 || N < 0 || K < 0) return QFP4_ERR_INVALID_ARG;
+    if (K % 16 != 0 || N > kMaxSize || K > kMaxSize || groups > 65535) return QFP4_ERR_UNSUPPORTED;
+    if (N == 0 || K == 0) return QFP4_OK;
+    if (!W_bf16 || !Q || !SF || (Q_t == nullptr) != (SF_t == nullptr)) return QFP4_ERR_INVALID_ARG;
+    if (!aligned16(W_bf16) || !aligned16(Q) || !aligned16(Q_t) || !aligned4(SF) || !aligned4(SF_t))
+        return QFP4_ERR_MISALIGNED;
+    const QuantParams p{static_cast<const uint4 *>(W_bf16), nullptr, N, static_cast<int32_t>(N),
+                        static_cast<int32_t>(K), static_cast<int32_t>((N + 15) / 16 * 16), static_cast<int32_t>((K + 127) / 128),
+                        static_cast<uint8_t *>(Q), static_cast<uint8_t *>(Q_t), SF, SF_t};
+    return launch_any(type, scale, p, kBlock | (Q_t ? kCols : 0), groups, static_cast<cudaStream_t>(stream));
+}

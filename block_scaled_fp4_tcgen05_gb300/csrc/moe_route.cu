@@ -1,0 +1,471 @@
+// moe_route.cu -- expert router: top-k choice, gates, per-expert counts, the
+// row order of the experts' product, the balance loss, and its gradient.
+//
+// With p = softmax(l) per token, c_e the pairs that chose expert e, n the valid
+// tokens, P_e = sum_t p_te / n:
+//   loss = E / (k n) sum_e c_e P_e
+// and, choices held fixed, with s_e = dloss E c_e / (k n^2):
+//   dl_i = p_i (s_i - sum_e p_e s_e) + gates' part,
+//   gates' part, g = p / sum of the chosen p: g_i (dg_i - sum_j g_j dg_j) at the
+//   chosen experts; g = p: [chosen] p_i dg_i - p_i sum_j p_j dg_j.
+//
+// Forward, two launches.  route_rows_kernel: CTA c takes a contiguous range of
+// tokens, a warp one token at a time with its logits in registers (lane l holds
+// experts l, l + 32, ...): softmax, then k rounds of a warp-wide maximum over
+// order-preserving integer keys, ties to the lowest expert; a lane adds up its
+// experts' p over the warp's tokens in registers.  The CTA's counts and its sum
+// of p go to the workspace.  route_place_kernel: each CTA adds up the counts of
+// all ranges, so it knows where each expert's rows begin and how many of them
+// come from earlier ranges, and ranks its own pairs in order; CTA 0 also writes
+// the totals and the loss.  All sums run in a fixed order: results repeat bit
+// for bit.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "qfp4_common.cuh"
+
+namespace qfp4 {
+namespace {
+
+constexpr int kMaxExperts = 256;
+constexpr int kMaxTopk = 16;
+constexpr int kWarps = 16;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxChunks = 304;             // two CTAs on each of 152 SMs
+constexpr uint32_t kFull = 0xffffffffu;
+constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
+
+struct RouteParams {
+    const void *logits;         // [T, E] BF16 or fp32
+    const uint8_t *valid;       // [T] or NULL
+    int64_t T;
+    int32_t E, topk, renorm;
+    int64_t chunk;              // tokens per CTA
+    int32_t *ids;
+    float *gates;
+    int32_t *counts, *row_offsets, *dest, *src, *n_valid;
+    float *mean_prob, *loss;
+    // workspace: per chunk, counts [E] (int32), sums of p [E] (fp32); then
+    // valid tokens per chunk
+    int32_t *ws_counts;
+    float *ws_prob;
+    int32_t *ws_valid;
+};
+
+// Order-preserving key: larger float, larger key; NaN above everything.
+__device__ __forceinline__ uint32_t sort_key(float v)
+{
+    if (v != v) return 0xFFFFFFFFu;
+    const uint32_t u = __float_as_uint(v + 0.0f);       // -0 becomes +0
+    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float load_logit(const float *p) { return __ldg(p); }
+__device__ __forceinline__ float load_logit(const __nv_bfloat16 *p) { return __bfloat162float(__ldg(p)); }
+__device__ __forceinline__ void store_logit(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store_logit(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ float warp_max(float v)
+{
+    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v)
+{
+    for (int d = 16; d > 0; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, d));
+    return v;
+}
+
+// exp(l - max) of the lane's experts, and 1 / their sum over the row (0 for a
+// row with no open expert).  A NaN or +inf logit makes the sum NaN.
+template <int V>
+__device__ __forceinline__ float softmax_terms(const float (&l)[V], int E, int lane, float (&x)[V])
+{
+    float m = -INFINITY;
+    bool nan = false;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        m = fmaxf(m, l[v]);
+        nan |= l[v] != l[v];
+    }
+    m = warp_max(m);
+    if (__any_sync(kFull, nan)) m = NAN;
+    const float base = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        x[v] = lane + 32 * v < E ? expf(l[v] - base) : 0.0f;
+        sum += x[v];
+    }
+    sum = warp_sum(sum);
+    return sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+}
+
+template <typename L, int V>
+__global__ void __launch_bounds__(kThreads)
+route_rows_kernel(const RouteParams p)
+{
+    __shared__ int32_t s_counts[kMaxExperts];
+    __shared__ float s_prob[kWarps][kMaxExperts];
+    __shared__ int32_t s_valid;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int e = tid; e < kMaxExperts; e += kThreads) s_counts[e] = 0;
+    if (tid == 0) s_valid = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t t0 = blockIdx.x * p.chunk;
+    const int64_t t1 = min(p.T, t0 + p.chunk);
+    float psum[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) psum[v] = 0.0f;
+    int nvalid = 0;
+    for (int64_t t = t0 + warp; t < t1; t += kWarps) {
+        int32_t my_id = -1;
+        float my_gate = 0.0f;
+        if (!p.valid || p.valid[t] != 0) {
+            ++nvalid;
+            const L *row = static_cast<const L *>(p.logits) + t * p.E;
+            float l[V], x[V];
+            uint32_t key[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e = lane + 32 * v;
+                l[v] = e < p.E ? load_logit(row + e) : -INFINITY;
+                key[v] = e < p.E ? sort_key(l[v]) : 0u;
+            }
+            const float inv = softmax_terms<V>(l, p.E, lane, x);
+#pragma unroll
+            for (int v = 0; v < V; ++v) psum[v] = __fadd_rn(psum[v], x[v] * inv);
+            float my_x = 0.0f;
+            for (int j = 0; j < p.topk; ++j) {
+                uint32_t best = key[0];
+#pragma unroll
+                for (int v = 1; v < V; ++v) best = max(best, key[v]);
+                best = __reduce_max_sync(kFull, best);
+                if (best <= kKeyNegInf) break;
+                uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+                for (int v = V - 1; v >= 0; --v)
+                    if (key[v] == best) at = lane + 32 * v;
+                at = __reduce_min_sync(kFull, at);
+                float xv = 0.0f;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (at == lane + 32 * v) {
+                        key[v] = 0u;
+                        xv = x[v];
+                    }
+                xv = __shfl_sync(kFull, xv, at & 31);
+                if (lane == j) {
+                    my_id = static_cast<int32_t>(at);
+                    my_x = xv;
+                }
+            }
+            const float scale = p.renorm ? warp_sum(my_x) : 0.0f;
+            my_gate = my_id < 0 ? 0.0f : p.renorm ? (scale == 0.0f ? 0.0f : __fdiv_rn(my_x, scale)) : my_x * inv;
+            if (my_id >= 0) atomicAdd(&s_counts[my_id], 1);
+        }
+        if (lane < p.topk) {
+            p.ids[t * p.topk + lane] = my_id;
+            p.gates[t * p.topk + lane] = my_gate;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_prob[warp][lane + 32 * v] = psum[v];
+    if (lane == 0) atomicAdd(&s_valid, nvalid);
+    __syncthreads();
+    for (int e = tid; e < p.E; e += kThreads) {
+        float s = s_prob[0][e];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) s = __fadd_rn(s, s_prob[w][e]);
+        p.ws_prob[static_cast<int64_t>(blockIdx.x) * p.E + e] = s;
+        p.ws_counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = s_counts[e];
+    }
+    if (tid == 0) p.ws_valid[blockIdx.x] = s_valid;
+}
+
+__global__ void __launch_bounds__(kThreads)
+route_place_kernel(const RouteParams p, int chunks)
+{
+    __shared__ int32_t s_start[kMaxExperts];            // first row of each expert
+    __shared__ int32_t s_before[kMaxExperts];           // rows that earlier ranges put there
+    __shared__ int32_t s_total[kMaxExperts];
+    __shared__ int32_t s_warp[kWarps][kMaxExperts];     // then: next row of each warp's pairs
+    __shared__ float s_p[kMaxExperts];
+    __shared__ int32_t s_n;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int f = tid; f < kWarps * kMaxExperts; f += kThreads) s_warp[f / kMaxExperts][f % kMaxExperts] = 0;
+    pdl_wait();
+    pdl_launch_dependents();
+    for (int e = tid; e < p.E; e += kThreads) {
+        int32_t before = 0, total = 0;
+        for (int c = 0; c < chunks; ++c) {
+            const int32_t n = __ldcg(p.ws_counts + static_cast<int64_t>(c) * p.E + e);
+            if (c < static_cast<int>(blockIdx.x)) before += n;
+            total += n;
+        }
+        s_before[e] = before;
+        s_total[e] = total;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        int32_t at = 0;
+        for (int e = 0; e < p.E; ++e) {
+            s_start[e] = at;
+            at += s_total[e];
+        }
+        s_n = at;
+    }
+    // pairs of this range, warp by warp in order
+    const int64_t f0 = min(p.T, blockIdx.x * p.chunk) * p.topk, f1 = min(p.T, (blockIdx.x + 1) * p.chunk) * p.topk;
+    const int64_t per_warp = ((f1 - f0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+    const int64_t w0 = min(f1, f0 + warp * per_warp), w1 = min(f1, w0 + per_warp);
+    for (int64_t f = w0 + lane; f < w1; f += 32) {
+        const int32_t e = __ldcg(p.ids + f);
+        if (e >= 0) atomicAdd(&s_warp[warp][e], 1);
+    }
+    __syncthreads();
+    for (int e = tid; e < p.E; e += kThreads) {
+        int32_t at = s_start[e] + s_before[e];
+        for (int w = 0; w < kWarps; ++w) {
+            const int32_t n = s_warp[w][e];
+            s_warp[w][e] = at;
+            at += n;
+        }
+    }
+    __syncthreads();
+    for (int64_t f = w0; f < w1; f += 32) {
+        const int32_t e = f + lane < w1 ? __ldcg(p.ids + f + lane) : -1;
+        const uint32_t same = __match_any_sync(kFull, e);
+        const int rank = __popc(same & ((1u << lane) - 1u));
+        int32_t row = -1;
+        if (e >= 0) row = s_warp[warp][e] + rank;
+        __syncwarp();
+        if (e >= 0 && rank == 0) s_warp[warp][e] += __popc(same);
+        __syncwarp();
+        if (f + lane < w1) {
+            p.dest[f + lane] = row;
+            if (row >= 0) p.src[row] = static_cast<int32_t>((f + lane) / p.topk);
+        }
+    }
+    // rows that no pair takes
+    const int64_t pairs = p.T * p.topk;
+    for (int64_t r = s_n + static_cast<int64_t>(blockIdx.x) * kThreads + tid; r < pairs;
+         r += static_cast<int64_t>(gridDim.x) * kThreads)
+        p.src[r] = -1;
+    if (blockIdx.x != 0) return;
+    __shared__ int32_t s_valid;
+    if (tid == 0) {
+        int32_t n = 0;
+        for (int c = 0; c < chunks; ++c) n += __ldcg(p.ws_valid + c);
+        s_valid = n;
+    }
+    __syncthreads();
+    const float n = static_cast<float>(max(s_valid, 1));
+    for (int e = tid; e < p.E; e += kThreads) {
+        float s = 0.0f;
+        for (int c = 0; c < chunks; ++c) s = __fadd_rn(s, __ldcg(p.ws_prob + static_cast<int64_t>(c) * p.E + e));
+        s = __fdiv_rn(s, n);
+        p.mean_prob[e] = s;
+        p.counts[e] = s_total[e];
+        p.row_offsets[e] = s_start[e];
+        s_p[e] = s * static_cast<float>(s_total[e]);
+    }
+    __syncthreads();
+    if (tid == 0) {
+        float sum = 0.0f;
+        for (int e = 0; e < p.E; ++e) sum = __fadd_rn(sum, s_p[e]);
+        p.loss[0] = sum * __fdiv_rn(static_cast<float>(p.E), static_cast<float>(p.topk) * n);
+        p.row_offsets[p.E] = s_n;
+        p.n_valid[0] = s_valid;
+    }
+}
+
+struct BackParams {
+    const void *logits;
+    const uint8_t *valid;
+    int64_t T;
+    int32_t E, topk, renorm;
+    const int32_t *ids, *counts, *n_valid;
+    const float *dgates, *dloss;
+    void *dlogits;
+};
+
+template <typename L, int V>
+__global__ void __launch_bounds__(kThreads)
+route_backward_kernel(const BackParams p)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+    // s_e = dloss E c_e / (k n^2)
+    float s[V];
+    {
+        const float n = static_cast<float>(max(p.n_valid[0], 1));
+        const float f = p.dloss ? __fdiv_rn(__fdiv_rn(p.dloss[0] * static_cast<float>(p.E), n), static_cast<float>(p.topk) * n) : 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = lane + 32 * v;
+            s[v] = e < p.E ? f * static_cast<float>(p.counts[e]) : 0.0f;
+        }
+    }
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.T; t += stride) {
+        L *out = static_cast<L *>(p.dlogits) + t * p.E;
+        if (p.valid && p.valid[t] == 0) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (lane + 32 * v < p.E) store_logit(out + lane + 32 * v, 0.0f);
+            continue;
+        }
+        const L *row = static_cast<const L *>(p.logits) + t * p.E;
+        float l[V], x[V], h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = lane + 32 * v;
+            l[v] = e < p.E ? load_logit(row + e) : -INFINITY;
+        }
+        const float inv = softmax_terms<V>(l, p.E, lane, x);
+        float dot = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v] *= inv;
+            dot = fmaf(x[v], s[v], dot);
+            h[v] = 0.0f;
+        }
+        dot = warp_sum(dot);
+        if (p.dgates) {
+            // lane j < k: choice j
+            int32_t id = lane < p.topk ? p.ids[t * p.topk + lane] : -1;
+            if (id >= p.E) id = -1;
+            const float dg = id >= 0 ? p.dgates[t * p.topk + lane] : 0.0f;
+            float pj = 0.0f;
+            for (int j = 0; j < p.topk; ++j) {
+                const int32_t e = __shfl_sync(kFull, id, j);
+                if (e < 0) continue;
+                float mine = 0.0f;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (lane + 32 * v == e) mine = x[v];
+                mine = __shfl_sync(kFull, mine, e & 31);
+                if (lane == j) pj = mine;
+            }
+            float g = pj;
+            if (p.renorm) {
+                const float total = warp_sum(pj);
+                g = total == 0.0f ? 0.0f : __fdiv_rn(pj, total);
+            }
+            const float gd = warp_sum(g * dg);
+            const float hj = p.renorm ? g * (dg - gd) : g * dg;
+            if (!p.renorm) dot += gd;
+            for (int j = 0; j < p.topk; ++j) {
+                const int32_t e = __shfl_sync(kFull, id, j);
+                const float a = __shfl_sync(kFull, hj, j);
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (lane + 32 * v == e) h[v] += a;
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = lane + 32 * v;
+            if (e < p.E) store_logit(out + e, fmaf(x[v], s[v] - dot, h[v]));
+        }
+    }
+}
+
+template <typename L>
+int launch_rows(const RouteParams &p, unsigned chunks, cudaStream_t s)
+{
+    const dim3 g(chunks), b(kThreads);
+    if (p.E <= 32) return launch_status(launch_pdl(route_rows_kernel<L, 1>, g, b, 0, s, p));
+    if (p.E <= 64) return launch_status(launch_pdl(route_rows_kernel<L, 2>, g, b, 0, s, p));
+    if (p.E <= 128) return launch_status(launch_pdl(route_rows_kernel<L, 4>, g, b, 0, s, p));
+    return launch_status(launch_pdl(route_rows_kernel<L, 8>, g, b, 0, s, p));
+}
+
+template <typename L>
+int launch_back(const BackParams &p, unsigned ctas, cudaStream_t s)
+{
+    const dim3 g(ctas), b(kThreads);
+    if (p.E <= 32) return launch_status(launch_pdl(route_backward_kernel<L, 1>, g, b, 0, s, p));
+    if (p.E <= 64) return launch_status(launch_pdl(route_backward_kernel<L, 2>, g, b, 0, s, p));
+    if (p.E <= 128) return launch_status(launch_pdl(route_backward_kernel<L, 4>, g, b, 0, s, p));
+    return launch_status(launch_pdl(route_backward_kernel<L, 8>, g, b, 0, s, p));
+}
+
+bool sizes_ok(int64_t T, int64_t E, int64_t topk)
+{
+    return E <= kMaxExperts && topk <= kMaxTopk && topk <= E && T <= INT32_MAX / topk;
+}
+
+// Tokens go in ranges of whole warps' rows, at most kMaxChunks of them.
+int64_t chunk_count(int64_t T)
+{
+    const int64_t n = (T + kWarps - 1) / kWarps;
+    return n < 1 ? 1 : n > kMaxChunks ? kMaxChunks : n;
+}
+
+}  // namespace
+}  // namespace qfp4
+
+using namespace qfp4;
+
+extern "C" size_t qfp4_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t topk)
+{
+    if (T < 0 || E < 1 || topk < 1 || !sizes_ok(T, E, topk)) return 0;
+    const size_t chunks = static_cast<size_t>(chunk_count(T));
+    return chunks * static_cast<size_t>(E) * 8 + chunks * 4;
+}
+
+extern "C" int qfp4_moe_route(int logits_type, const void *logits, int64_t T, int64_t E, int64_t topk,
+                              const uint8_t *valid, int renorm, int32_t *ids, float *gates, int32_t *counts,
+                              int32_t *row_offsets, int32_t *dest, int32_t *src, int32_t *n_valid, float *mean_prob,
+                              float *loss, void *workspace, size_t ws_bytes, void *stream)
+{
+    if ((logits_type != QFP4_BF16 && logits_type != QFP4_FP32) || T < 0 || E < 1 || topk < 1)
+        return QFP4_ERR_INVALID_ARG;
+    if (!sizes_ok(T, E, topk)) return QFP4_ERR_UNSUPPORTED;
+    if (!counts || !row_offsets || !n_valid || !mean_prob || !loss || !workspace) return QFP4_ERR_INVALID_ARG;
+    if (T > 0 && (!logits || !ids || !gates || !dest || !src)) return QFP4_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned4(ids) || !aligned4(gates) || !aligned4(counts) || !aligned4(row_offsets) ||
+        !aligned4(dest) || !aligned4(src) || !aligned4(n_valid) || !aligned4(mean_prob) || !aligned4(loss) ||
+        !aligned16(workspace))
+        return QFP4_ERR_MISALIGNED;
+    if (ws_bytes < qfp4_moe_route_workspace_bytes(T, E, topk)) return QFP4_ERR_WORKSPACE;
+    const int64_t chunks = chunk_count(T);
+    RouteParams p{logits, valid, T, static_cast<int32_t>(E), static_cast<int32_t>(topk), renorm ? 1 : 0,
+                  (T + chunks - 1) / chunks, ids, gates, counts, row_offsets, dest, src, n_valid, mean_prob, loss};
+    p.ws_counts = static_cast<int32_t *>(workspace);
+    p.ws_prob = reinterpret_cast<float *>(p.ws_counts + chunks * E);
+    p.ws_valid = reinterpret_cast<int32_t *>(p.ws_prob + chunks * E);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int rc = logits_type == QFP4_BF16 ? launch_rows<__nv_bfloat16>(p, static_cast<unsigned>(chunks), s)
+                                            : launch_rows<float>(p, static_cast<unsigned>(chunks), s);
+    if (rc != QFP4_OK) return rc;
+    return launch_status(launch_pdl(route_place_kernel, dim3(static_cast<unsigned>(chunks)), dim3(kThreads), 0, s, p,
+                                    static_cast<int>(chunks)));
+}
+
+extern "C" int qfp4_moe_route_backward(int logits_type, const void *logits, int64_t T, int64_t E, int64_t topk,
+                                       const uint8_t *valid, int renorm, const int32_t *ids, const int32_t *counts,
+                                       const int32_t *n_valid, const float *dgates, const float *dloss,
+                                       void *dlogits, void *stream)
+{
+    if ((logits_type != QFP4_BF16 && logits_type != QFP4_FP32) || T < 0 || E < 1 || topk < 1)
+        return QFP4_ERR_INVALID_ARG;
+    if (!sizes_ok(T, E, topk)) return QFP4_ERR_UNSUPPORTED;
+    if (T == 0) return QFP4_OK;
+    if (!logits || !ids || !counts || !n_valid || !dlogits) return QFP4_ERR_INVALID_ARG;
+    if (!aligned16(logits) || !aligned4(ids) || !aligned4(counts) || !aligned4(n_valid) || !aligned4(dgates) ||
+        !aligned4(dloss) || !aligned16(dlogits))
+        return QFP4_ERR_MISALIGNED;
+    const BackParams p{logits, valid, T, static_cast<int32_t>(E), static_cast<int32_t>(topk), renorm ? 1 : 0,
+                       ids, counts, n_valid, dgates, dloss, dlogits};
+    const int64_t want = (T + kWarps - 1) / kWarps;
+    const unsigned ctas = static_cast<unsigned>(want < 4 * 152 ? want : 4 * 152);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return logits_type == QFP4_BF16 ? launch_back<__nv_bfloat16>(p, ctas, s) : launch_back<float>(p, ctas, s);
+}

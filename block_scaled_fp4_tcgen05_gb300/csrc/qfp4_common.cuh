@@ -100,5 +100,7 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
 int read_clear_status_quant(cudaStream_t s, uint32_t *out);
 int read_clear_status_gemm(cudaStream_t s, uint32_t *out);
 int read_clear_status_gemm_sparse(cudaStream_t s, uint32_t *out);
+int read_clear_status_gemm_fp8(cudaStream_t s, uint32_t *out);
+int read_clear_status_fp8_quant(cudaStream_t s, uint32_t *out);
 
 }  // namespace qfp4

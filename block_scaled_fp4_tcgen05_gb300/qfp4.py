@@ -17,6 +17,12 @@ import torch
 MXFP4 = 0
 NVFP4 = 1
 NVFP4_B32 = 2
+E4M3 = 0
+E5M2 = 1
+SCALE_FP32 = 0
+SCALE_POW2 = 1
+OUT_BF16 = 0
+OUT_FP32 = 1
 SF_ROWMAJOR = 0
 SF_MMA = 1
 
@@ -63,6 +69,15 @@ SIGNATURES = {
     "qfp4_gemm_nt_noalloc": (_i32, [_i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "qfp4_gemm_nt_grouped": (_i32, [_i32, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp,
                                     _vp, _vp, _vp, _vp, _sz, _vp]),
+    "qfp4_fp8_quantize": (_i32, [_i32, _i32, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "qfp4_fp8_quantize_weight": (_i32, [_i32, _i32, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "qfp4_gemm_nt_fp8": (_i32, [_i32, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]),
+    "qfp4_gemm_nt_fp8_grouped": (_i32, [_i32, _i32, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _vp,
+                                        _vp]),
+    "qfp4_moe_route_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "qfp4_moe_route": (_i32, [_i32, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                              _vp, _sz, _vp]),
+    "qfp4_moe_route_backward": (_i32, [_i32, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
 
 
@@ -320,3 +335,113 @@ def gemm_swiglu_quantize_grouped(fmt, row_offsets, total_rows, I, K, A, A_sf, W,
            load().qfp4_gemm_swiglu_quantize_grouped(fmt, groups, _p(row_offsets), total_rows, I, K, _p(A),
                                                     _p(A_sf), _p(W), _p(W_sf), _p(gs_a), _p(gs_w), _p(gs_out),
                                                     _p(Q_out), _p(SF_out), _stream(stream)))
+
+
+def _dense(*tensors) -> None:
+    """The C ABI takes whole row-major matrices on the GPU: a strided view or a
+    host tensor would be read as something else."""
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and not (t.is_cuda and t.is_contiguous()):
+            raise ValueError("qfp4: tensors must be contiguous and on the GPU")
+
+
+def _typed(dtype, *tensors) -> None:
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.dtype != dtype:
+            raise ValueError(f"qfp4: expected {dtype}, got {t.dtype}")
+
+
+def fp8_quantize(type, X, Q=None, SF=None, Q_t=None, SF_t=None, scale=SCALE_FP32, row_index=None, stream=None) -> None:
+    """BF16 X -> 8-bit codes with a scale per 128 elements: along the rows
+    (Q [M, K], SF [ceil(K/128), M]) and / or along the columns, transposed
+    (Q_t [K, ceil16(M)], SF_t [ceil(M/128), K]).  row_index (int32 [M]) gathers
+    rows of X."""
+    _dense(X, Q, SF, Q_t, SF_t, row_index)
+    _typed(torch.bfloat16, X)
+    _typed(torch.float32, SF, SF_t)
+    _typed(torch.int32, row_index)
+    rows, K = X.shape
+    M = rows if row_index is None else row_index.numel()
+    _check("qfp4_fp8_quantize",
+           load().qfp4_fp8_quantize(type, scale, _p(X), rows, _p(row_index), M, K, _p(Q), _p(SF), _p(Q_t), _p(SF_t),
+                                    _stream(stream)))
+
+
+def fp8_quantize_weight(type, W, Q, SF, Q_t=None, SF_t=None, scale=SCALE_FP32, stream=None) -> None:
+    """Weights W [N, K] or [groups, N, K] -> codes with a scale per 128 x 128
+    block, and optionally their transpose (Q_t [.., K, ceil16(N)])."""
+    _dense(W, Q, SF, Q_t, SF_t)
+    _typed(torch.bfloat16, W)
+    _typed(torch.float32, SF, SF_t)
+    groups, (N, K) = (1 if W.dim() == 2 else W.shape[0]), W.shape[-2:]
+    _check("qfp4_fp8_quantize_weight",
+           load().qfp4_fp8_quantize_weight(type, scale, groups, _p(W), N, K, _p(Q), _p(SF), _p(Q_t), _p(SF_t),
+                                           _stream(stream)))
+
+
+def gemm_nt_fp8(a_type, b_type, M, N, K, A, A_sf, B, B_sf, D, b_rows=128, out=OUT_BF16, accumulate=False,
+                stream=None) -> None:
+    """D = A B^T with a scale per 128 elements of K: A_sf [ceil(K/128), M], B_sf
+    per 128 x 128 block (b_rows=128) or [ceil(K/128), N] (b_rows=1)."""
+    _dense(A, A_sf, B, B_sf, D)
+    _typed(torch.float32, A_sf, B_sf)
+    _typed(torch.float32 if out == OUT_FP32 else torch.bfloat16, D)
+    _check("qfp4_gemm_nt_fp8",
+           load().qfp4_gemm_nt_fp8(a_type, b_type, M, N, K, _p(A), _p(A_sf), _p(B), _p(B_sf), b_rows, out,
+                                   1 if accumulate else 0, _p(D), _stream(stream)))
+
+
+def gemm_nt_fp8_grouped(a_type, b_type, row_offsets, total_rows, max_group_rows, N, K, A, A_sf, B, B_sf, D,
+                        out=OUT_BF16, stream=None) -> None:
+    """One product per expert: rows [row_offsets[e], row_offsets[e+1]) with B[e]."""
+    _dense(row_offsets, A, A_sf, B, B_sf, D)
+    _typed(torch.int32, row_offsets)
+    _typed(torch.float32, A_sf, B_sf)
+    _typed(torch.float32 if out == OUT_FP32 else torch.bfloat16, D)
+    groups = row_offsets.numel() - 1
+    _check("qfp4_gemm_nt_fp8_grouped",
+           load().qfp4_gemm_nt_fp8_grouped(a_type, b_type, groups, _p(row_offsets), total_rows, max_group_rows, N, K,
+                                           _p(A), _p(A_sf), _p(B), _p(B_sf), out, _p(D), _stream(stream)))
+
+
+def moe_route_workspace_bytes(T: int, E: int, topk: int) -> int:
+    return int(load().qfp4_moe_route_workspace_bytes(T, E, topk))
+
+
+def _logits_type(logits) -> int:
+    if logits.dtype == torch.float32:
+        return OUT_FP32
+    _typed(torch.bfloat16, logits)
+    return OUT_BF16
+
+
+def moe_route(logits, topk, ids, gates, counts, row_offsets, dest, src, n_valid, mean_prob, loss, workspace,
+              valid=None, renorm=True, stream=None) -> None:
+    """Top-k experts of each token, gates, per-expert counts and row order, and
+    the balance loss; valid is uint8 [T] or None."""
+    _dense(logits, ids, gates, counts, row_offsets, dest, src, n_valid, mean_prob, loss, workspace, valid)
+    _typed(torch.int32, ids, counts, row_offsets, dest, src, n_valid)
+    _typed(torch.float32, gates, mean_prob, loss)
+    _typed(torch.uint8, valid)
+    T, E = logits.shape
+    _check("qfp4_moe_route",
+           load().qfp4_moe_route(_logits_type(logits), _p(logits), T, E, topk, _p(valid), 1 if renorm else 0, _p(ids),
+                                 _p(gates), _p(counts), _p(row_offsets), _p(dest), _p(src), _p(n_valid),
+                                 _p(mean_prob), _p(loss), _p(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def moe_route_backward(logits, ids, counts, n_valid, dgates, dloss, dlogits, valid=None, renorm=True,
+                       stream=None) -> None:
+    """dlogits of (gates . dgates + dloss * loss), choices and counts held fixed;
+    dgates and dloss may be None."""
+    _dense(logits, ids, counts, n_valid, dgates, dloss, dlogits, valid)
+    _typed(torch.int32, ids, counts, n_valid)
+    _typed(torch.float32, dgates, dloss)
+    _typed(torch.uint8, valid)
+    _typed(logits.dtype, dlogits)
+    T, E = logits.shape
+    _check("qfp4_moe_route_backward",
+           load().qfp4_moe_route_backward(_logits_type(logits), _p(logits), T, E, ids.shape[1], _p(valid),
+                                          1 if renorm else 0, _p(ids), _p(counts), _p(n_valid), _p(dgates),
+                                          _p(dloss), _p(dlogits), _stream(stream)))

@@ -491,6 +491,143 @@ int qfp4_gemm_swiglu_quantize_grouped(int fmt, int64_t groups, const int32_t *ro
                                       const float *gs_a, const float *gs_w, const float *gs_out,
                                       void *Q_out, void *SF_out, void *stream);
 
+/* ---------------------------------------------------------------------- */
+/* 8-bit floating point with a scale per 128 elements                       */
+/* ---------------------------------------------------------------------- */
+
+/* Code types: OCP FP8 E4M3 (largest 448, NaN, no infinities) and E5M2
+ * (largest 57344).  The quantiser saturates and never writes an infinity. */
+enum { QFP4_E4M3 = 0, QFP4_E5M2 = 1 };
+
+/* How a block's scale is taken from its largest magnitude. */
+enum { QFP4_SCALE_FP32 = 0, QFP4_SCALE_POW2 = 1 };
+
+/* Element types of the product's output and of the router's logits. */
+enum { QFP4_BF16 = 0, QFP4_FP32 = 1 };
+
+/* BF16 -> 8-bit codes with one fp32 scale per 128 consecutive elements of a
+ * row, and / or of a column.  Per block, in IEEE fp32 with
+ * round-to-nearest-even, top = 448 (E4M3) or 57344 (E5M2):
+ *   a = max(max |x|, 2^-100)
+ *   QFP4_SCALE_FP32: s = a / top, code = RNE(x * (top / a))
+ *   QFP4_SCALE_POW2: s = smallest power of two >= a / top, code = RNE(x / s)
+ * saturating at top.  A NaN encodes as NaN and does not count in max |x|; an
+ * infinity gives s = inf and codes whose product with it is NaN.  The output is
+ * bit-exact to this rule.
+ *   X_bf16     [X_rows, K] row-major
+ *   row_index  NULL: row m of the operand is row m of X (X_rows == M).  Else a
+ *              DEVICE int32 [M]: row m is X[row_index[m]] (tokens gathered into
+ *              expert order); a negative index gives a row of zero codes (and
+ *              the scale of a zero block), one of X_rows or more does too
+ *              and makes the next qfp4_poll_device_status return
+ *              QFP4_ERR_INVALID_ARG.
+ *   Q, SF      codes [M, K] and scales [ceil(K/128)][M] of the blocks along
+ *              the rows (the last block of a row may be short): an operand of
+ *              qfp4_gemm_nt_fp8 whose K is this K.  Both or neither NULL.
+ *   Q_t, SF_t  codes of the transpose, [K][ceil16(M)] with ceil16(M) the next
+ *              multiple of 16 and zero codes beyond M, and scales
+ *              [ceil(M/128)][K] of the blocks of 128 rows along each column:
+ *              an operand of the weight gradient, whose K is ceil16(M).  Both
+ *              or neither NULL.  X is read once for both outputs.
+ * Requirements: K % 16 == 0, M, K <= 2^30, X / Q / Q_t 16-byte aligned, the
+ * rest 4-byte.  M == 0 or K == 0 launches nothing. */
+int qfp4_fp8_quantize(int type, int scale, const void *X_bf16, int64_t X_rows, const int32_t *row_index,
+                      int64_t M, int64_t K, void *Q, float *SF, void *Q_t, float *SF_t, void *stream);
+
+/* The same with one scale per 128 x 128 block: weights W [groups, N, K]
+ * (groups = 1, or one matrix per expert).
+ *   Q, SF      codes [groups][N][K], scales [groups][ceil(N/128)][ceil(K/128)]:
+ *              the B operand of qfp4_gemm_nt_fp8 (b_rows = 128)
+ *   Q_t, SF_t  (both NULL for none) the same codes transposed,
+ *              [groups][K][ceil16(N)] with zero codes beyond N, and scales
+ *              [groups][ceil(K/128)][ceil(N/128)]: B of the input gradient
+ *              dX = dY W.
+ * Requirements: K % 16 == 0, 1 <= groups <= 65535, alignment as above. */
+int qfp4_fp8_quantize_weight(int type, int scale, int64_t groups, const void *W_bf16, int64_t N, int64_t K,
+                             void *Q, float *SF, void *Q_t, float *SF_t, void *stream);
+
+/* D[m,n] = sum over blocks j of 128 along K of
+ *            sa[j][m] * sb(j,n) * sum_{k in block j} a[m,k] * b[n,k]
+ * with A [M,K], B [N,K] 8-bit codes (types may differ), K-major.
+ *   A_sf     fp32 [ceil(K/128)][M]
+ *   b_rows   128: B_sf fp32 [ceil(N/128)][ceil(K/128)] (weights);
+ *            1: B_sf fp32 [ceil(K/128)][N] (both operands activations or
+ *            gradients: the weight gradient dW = dY^T X)
+ *   out_type QFP4_BF16: D BF16 [M,N], one rounding at the end; QFP4_FP32
+ *   accumulate  1: D += (QFP4_FP32 only: gradients summed over micro batches)
+ * Training: forward A = X, B = W; input gradient A = dY, B = W's transpose
+ * (Q_t, SF_t of qfp4_fp8_quantize_weight, K = ceil16(N): quantise dY with
+ * zero columns beyond N); weight gradient A = dY's and B = X's transpose
+ * (Q_t, SF_t of qfp4_fp8_quantize, b_rows = 1).
+ * The products of one block are accumulated by the tensor cores, the blocks
+ * in fp32 registers with the scales applied in fp32.  Every result repeats bit
+ * for bit.
+ * Requirements: K % 16 == 0; M, N, K <= 2^30; A, B, D 16-byte aligned, scales
+ * 4-byte.  M == 0 or N == 0 launches nothing; K == 0 gives D = 0 (accumulate:
+ * D unchanged).
+ * Accuracy: |D - exact| <= u |exact| + (ceil(K/128) + 18) 2^-24 T, with T the
+ * sum of the terms' magnitudes and u = 2^-8 (BF16) or 2^-24 (FP32, where the
+ * accumulated D counts as part of exact). */
+int qfp4_gemm_nt_fp8(int a_type, int b_type, int64_t M, int64_t N, int64_t K,
+                     const void *A, const float *A_sf, const void *B, const float *B_sf, int b_rows,
+                     int out_type, int accumulate, void *D, void *stream);
+
+/* One product per expert: rows [row_offsets[e], row_offsets[e+1]) of A and D
+ * with B[e].  B [groups][N][K], B_sf [groups][ceil(N/128)][ceil(K/128)].
+ * row_offsets, total_rows and max_group_rows as in qfp4_gemm_nt_grouped, but
+ * row_offsets[groups] may be below total_rows (tokens that the router dropped
+ * leave the last rows unused): the rows of D beyond it are left untouched.
+ * Requirements as qfp4_gemm_nt_fp8, 1 <= groups <= 256, groups * N <= 2^30. */
+int qfp4_gemm_nt_fp8_grouped(int a_type, int b_type, int64_t groups, const int32_t *row_offsets,
+                             int64_t total_rows, int64_t max_group_rows, int64_t N, int64_t K,
+                             const void *A, const float *A_sf, const void *B, const float *B_sf,
+                             int out_type, void *D, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Expert router                                                            */
+/* ---------------------------------------------------------------------- */
+
+/* Routes T tokens to topk of E experts each and takes the balance loss, in
+ * fp32.  Per token t with valid[t] != 0 (valid NULL: all): p = softmax(logits[t])
+ * and the topk experts of largest logit, ties to the lowest index; an expert
+ * whose logit is -inf is never chosen (a token with fewer open experts gets
+ * fewer; one with none has p = 0).  NaN ranks above +inf, and either makes the
+ * row's p NaN.
+ *   ids    int32 [T, topk] in falling order of logit, -1 where none
+ *   gates  fp32 [T, topk]: p of the expert (renorm: divided by the sum of the
+ *          token's chosen p), 0 where none
+ *   counts int32 [E]: (token, choice) pairs per expert
+ *   row_offsets int32 [E + 1]: its running sum, for the grouped calls
+ *   dest   int32 [T, topk]: row of the pair in expert order (by expert, then
+ *          token, then choice), -1 where none
+ *   src    int32 [T * topk]: token of each row, -1 beyond row_offsets[E]: the
+ *          row_index of qfp4_fp8_quantize
+ *   n_valid int32 [1];  mean_prob fp32 [E]: P_e = sum_t p_te / max(n_valid, 1)
+ *   loss   fp32 [1]: E / (topk * max(n_valid, 1)) * sum_e counts[e] * P_e
+ *          (1 when both are uniform)
+ *   workspace  DEVICE scratch, 16-byte aligned, of ws_bytes >=
+ *          qfp4_moe_route_workspace_bytes(...) (never above 1 MiB); need not be
+ *          cleared.  One call at a time per workspace.
+ * Results repeat bit for bit.  Requirements: 1 <= E <= 256, 1 <= topk <=
+ * min(E, 16), T >= 0, T * topk <= 2^31 - 1, logits 16-byte aligned, the rest
+ * 4-byte.  T == 0 writes zero counts, offsets, n_valid, mean_prob and loss. */
+size_t qfp4_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t topk);
+int qfp4_moe_route(int logits_type, const void *logits, int64_t T, int64_t E, int64_t topk, const uint8_t *valid,
+                   int renorm, int32_t *ids, float *gates, int32_t *counts, int32_t *row_offsets, int32_t *dest,
+                   int32_t *src, int32_t *n_valid, float *mean_prob, float *loss, void *workspace, size_t ws_bytes,
+                   void *stream);
+
+/* Gradient of qfp4_moe_route: with the choices and counts held fixed,
+ *   dlogits = d/dlogits (sum_tj dgates[t,j] gates[t,j] + dloss * loss)
+ * written in the type of the logits (0 for tokens that are not valid).
+ * dgates fp32 [T, topk] or NULL (zeros), dloss DEVICE fp32 [1] or NULL (0);
+ * logits, valid, renorm, ids, counts and n_valid as given to and written by the
+ * forward call.  An id outside [-1, E) counts as -1. */
+int qfp4_moe_route_backward(int logits_type, const void *logits, int64_t T, int64_t E, int64_t topk,
+                            const uint8_t *valid, int renorm, const int32_t *ids, const int32_t *counts,
+                            const int32_t *n_valid, const float *dgates, const float *dloss, void *dlogits,
+                            void *stream);
+
 #ifdef __cplusplus
 }
 #endif
