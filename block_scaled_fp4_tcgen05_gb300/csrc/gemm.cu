@@ -485,6 +485,30 @@ int make_map(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows, 
                       [&](CUtensorMap *m) { return encode_map(m, base, inner, rows, box_inner, box_rows); });
 }
 
+int make_map_direct(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows, uint32_t box_inner,
+                    uint32_t box_rows)
+{
+    const int rc = ensure_thread_context();
+    return rc == QFP4_OK ? encode_map(map, base, inner, rows, box_inner, box_rows) : rc;
+}
+
+int make_map_store(CUtensorMap *map, void *base, bool fp32, uint64_t cols, uint64_t rows, uint32_t box_cols,
+                   uint32_t box_rows)
+{
+    const int rc = ensure_thread_context();
+    if (rc != QFP4_OK) return rc;
+    auto enc = get_encode_fn();
+    if (!enc) return QFP4_ERR_CUDA;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {cols * (fp32 ? 4 : 2)};
+    cuuint32_t box[2] = {box_cols, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims,
+                     strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_32B,
+                     CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? QFP4_OK : QFP4_ERR_CUDA;
+}
+
 int make_map_kpairs(CUtensorMap *map, const void *base, uint64_t K, uint64_t rows)
 {
     return cached_map(MapKey{1, 0, 0, base, K, rows}, map,

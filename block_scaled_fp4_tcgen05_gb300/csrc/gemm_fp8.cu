@@ -1,14 +1,39 @@
 // gemm_fp8.cu -- product of 8-bit floating point operands with one fp32 scale
-// per 128 elements of K (see qfp4_gemm_nt_fp8).
+// per 128 elements of K (see qfp4_gemm_nt_fp8), on CTA pairs.
 //
-// First form: 64 x 64 tiles on the CUDA cores, codes decoded to fp32 in shared
-// memory, one block of 128 accumulated at a time and added under its scales.
+// D[m,n] = sum_j sa[j][m] sb(j,n) sum_{k in block j} a b: the tensor cores
+// (tcgen05 kind::f8f6f4) sum one block of 128, and because its scale differs
+// from the next one's, each block's sum leaves tensor memory for registers,
+// where it is added under the fp32 product of its two scales.
+//
+// A cluster of two CTAs computes a 256 x 256 tile.  CTA r holds 128 rows of A
+// and 128 rows of B per K block (16 KB each, a ring of five); the leader issues
+// four M=256 N=256 K=32 MMAs per K block into one of two accumulator slots of
+// 256 columns, so that one is summed while the other is drained.  Eight
+// epilogue warps per CTA each keep 32 rows x 128 columns of D in registers
+// (128 per thread; the producer warps give theirs up with setmaxnreg).  A
+// thread owns one row, and its 128 columns are one block of B's scales, so the
+// scale is one number per thread and K block (COLSCALE: one per column).
+//
+// What bounds it is the epilogue's chain per K block: 32768 multiply-adds per
+// SM are 256 issue cycles of the 512 the MMAs take, beside four tensor-memory
+// loads per warp (72 cycles each alone) and the hand-overs (about 95 cycles for
+// a look at an mbarrier that is already complete).  So: loads of the next 32
+// columns run under the additions of the last; the next slot is looked at
+// before the last additions and judged after them; slots are given back with
+// relaxed arrivals straight at the leader; scales come through shared memory
+// from a warp of their own, eight K blocks at a time (loading them in the
+// epilogue warps themselves cost a global latency per K block: 1.7x slower);
+// plain multiply-adds, as the packed ones need more cycles per element
+// (measured 1.4 per element of a warp against 1.1: 278 us against 216 at
+// 4096 x 4096 x 14336); one slot per K block (two half as wide: 281 us).
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include "qfp4_common.cuh"
+#include "qfp4_gemm_internal.cuh"
 #include "sm103_ptx.cuh"
 
 namespace qfp4 {
@@ -43,6 +68,7 @@ struct Fp8Params {
     int32_t max_group_rows;         // grouped: 0 = no bound
     int32_t a_type, b_type, b_rows;
     int32_t fp32, accumulate;
+    int32_t store_map;              // D can be written by TMA (rows 16-byte aligned)
 };
 
 // Row offsets a grouped product can use: from 0, never decreasing, at most
@@ -58,85 +84,410 @@ __device__ __forceinline__ bool fp8_offsets_valid(const int32_t *offs, int group
     return true;
 }
 
-__device__ __forceinline__ float decode(uint8_t c, int type)
+// ---------------------------------------------------------------- CTA pairs, 256 x 256 tiles
+
+constexpr int kPairThreads = 384;       // 12 warps
+constexpr int kEpiWarps = 8;            // per slot: set h of eight warps drains part h of every K block
+constexpr int kStages = 5;
+constexpr int kOpBytes = 128 * 128;     // 128 rows x 128 elements of K
+constexpr int kStageBytes = 2 * kOpBytes;
+constexpr int kSlotCols = 256;          // columns of an accumulator slot
+constexpr int kSlots = 512 / kSlotCols;
+constexpr int kParts = 256 / kSlotCols; // slots per K block
+constexpr int kWarpCols = kSlotCols / 2;        // columns of a slot that one epilogue warp reads
+constexpr int kBatch = 8;               // K blocks per hand-over of scales
+constexpr int kScaleFloats = 128 + 256; // per K block: the CTA's rows, then the tile's columns (or its two blocks)
+constexpr int kOffScale = kStages * kStageBytes;    // two batches
+constexpr int kBoxBytes = 32 * 32;      // output staging box: 32 rows x 32 bytes; two per epilogue warp
+constexpr int kOffOut = kOffScale + 2 * kBatch * kScaleFloats * 4;
+constexpr int kOffBar = kOffOut + kEpiWarps * 2 * kBoxBytes;
+constexpr int kPairBars = 2 * kStages + 2 * kSlots + 4;  // full, empty [stage]; acc_full, acc_empty [slot]; sc_full, sc_empty [2]
+constexpr int kPairSmem = kOffBar + kPairBars * 8 + 16 + 1024;
+static_assert(kPairSmem + 4096 <= 232448, "shared memory overflow");
+
+__device__ __forceinline__ void record_timeout()
 {
-    __nv_fp8_storage_t v = c;
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, type == QFP4_E4M3 ? __NV_E4M3 : __NV_E5M2)));
+    atomicOr(&g_status_gemm_fp8, static_cast<uint32_t>(kStatusTimeout));
 }
 
-__global__ void __launch_bounds__(256)
-gemm_fp8_simple_kernel(const Fp8Params p)
+
+
+// Writes a warp's 32 rows x kWarpCols columns of D; lane i holds row i.  Box
+// q's 16-byte halves are staged in the 32-byte swizzle of the store map.
+template <bool FP32>
+__device__ __forceinline__ void store_boxes(const float (&acc)[128], uint8_t *out, const CUtensorMap &map,
+                                            const Fp8Params &p, bool by_tma, int32_t row0, int32_t rows, int32_t c0,
+                                            int lane)
 {
-    __shared__ float sa[32][65], sb[32][65];
-    __shared__ int32_t s_row[3];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    if (tid == 0) {
-        int32_t t = blockIdx.x, e = 0, lo = 0, hi = p.M;
-        if (p.groups) {
-            lo = hi = 0;
-            if (!fp8_offsets_valid(p.row_offsets, p.groups, p.M, p.max_group_rows)) {
-                if (blockIdx.x == 0 && blockIdx.y == 0)
-                    atomicOr(&g_status_gemm_fp8, static_cast<uint32_t>(kStatusBadGroup));
+    constexpr int kCols = FP32 ? 8 : 16;        // columns of a box
+#pragma unroll
+    for (int q = 0; q < 128 / kCols; ++q) {
+        const int32_t col = c0 + q * kCols;
+        if (col >= p.N) break;
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float lo, hi;
+            if (FP32) {
+                lo = acc[q * 8 + (i & ~1)]; hi = acc[q * 8 + (i | 1)];
+                w[i] = __float_as_uint(i & 1 ? hi : lo);
             } else {
-                for (; e < p.groups; ++e) {
-                    const int32_t tiles = (p.row_offsets[e + 1] - p.row_offsets[e] + 63) / 64;
-                    if (t < tiles) {
-                        lo = p.row_offsets[e];
-                        hi = p.row_offsets[e + 1];
-                        break;
-                    }
-                    t -= tiles;
+                lo = acc[q * 16 + 2 * i]; hi = acc[q * 16 + 2 * i + 1];
+                __nv_bfloat162 pr = __floats2bfloat162_rn(lo, hi);
+                w[i] = *reinterpret_cast<uint32_t *>(&pr);
+            }
+        }
+        uint8_t *box = out + (q & 1) * kBoxBytes;
+        // the box is free once the copy engine has read the store of two boxes ago
+        if (lane == 0) bulk_wait_group_read<1>();
+        __syncwarp();
+        const int flip = (lane >> 2) & 1;
+        *reinterpret_cast<uint4 *>(box + lane * 32 + 16 * flip) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(box + lane * 32 + 16 * (flip ^ 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+        if (by_tma) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (p.accumulate) tma_reduce_add_2d(&map, smem_u32(box), col, row0);
+                else tma_store_2d(&map, smem_u32(box), col, row0);
+                bulk_commit_group();
+            }
+            continue;
+        }
+        __syncwarp();
+        // four rows at a time, lane = 8 row + word
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), word = lane & 7;
+            const uint32_t v = *reinterpret_cast<const uint32_t *>(
+                box + r * 32 + 16 * ((word >> 2) ^ ((r >> 2) & 1)) + 4 * (word & 3));
+            if (r >= rows) break;
+            const int64_t at = static_cast<int64_t>(row0 + r) * p.N;
+            if (FP32) {
+                if (col + word < p.N) {
+                    float *d = static_cast<float *>(p.D) + at + col + word;
+                    *d = p.accumulate ? *d + __uint_as_float(v) : __uint_as_float(v);
+                }
+            } else {
+                uint16_t *d = static_cast<uint16_t *>(p.D) + at + col + 2 * word;
+                if (p.N % 2 == 0) {
+                    if (col + 2 * word < p.N) *reinterpret_cast<uint32_t *>(d) = v;
+                } else {
+                    if (col + 2 * word < p.N) d[0] = static_cast<uint16_t>(v);
+                    if (col + 2 * word + 1 < p.N) d[1] = static_cast<uint16_t>(v >> 16);
                 }
             }
         }
-        s_row[0] = lo + t * 64;
-        s_row[1] = hi;
-        s_row[2] = e;
+        __syncwarp();
     }
+}
+
+struct Tile {
+    int32_t row0, row_end, n0, group;
+};
+
+template <bool GROUPED, bool COLSCALE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                     const __grid_constant__ CUtensorMap tmD, const Fp8Params p)
+{
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar);   // leader: bytes of both CTAs
+    uint64_t *empty = full + kStages;                                // stage free again (MMA commit, both CTAs)
+    uint64_t *acc_full = empty + kStages;                            // slot's sum complete (both CTAs)
+    uint64_t *acc_empty = acc_full + kSlots;                         // leader: slot drained by both CTAs
+    uint64_t *sc_full = acc_empty + kSlots;                          // [2] batch of scales written
+    uint64_t *sc_empty = sc_full + 2;                                // [2] batch of scales read
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sc_empty + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    __shared__ int32_t s_offs[GROUPED ? kMaxGroups + 1 : 1];
+    __shared__ int32_t s_ptile[GROUPED ? kMaxGroups + 1 : 1];        // prefix of 256-row tiles
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int32_t kblocks = (p.K + 127) / 128;
+    const int32_t ntiles_n = (p.N + 255) / 256;
+    const int32_t pair_id = blockIdx.x >> 1;
+    const int32_t npairs = gridDim.x >> 1;
+
+    if (GROUPED) pdl_wait();
+    int32_t total_tiles;
+    if (GROUPED) {
+        __shared__ int s_bad;
+        for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) s_offs[i] = p.row_offsets[i];
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            s_bad = fp8_offsets_valid(s_offs, p.groups, p.M, p.max_group_rows) ? 0 : 1;
+            if (s_bad && blockIdx.x == 0) atomicOr(&g_status_gemm_fp8, static_cast<uint32_t>(kStatusBadGroup));
+            int32_t pt = 0;
+            for (int e = 0; e < p.groups; ++e) {
+                s_ptile[e] = pt;
+                const int32_t rows = s_offs[e + 1] - s_offs[e];
+                pt += !s_bad && rows > 0 ? (rows + 255) / 256 : 0;
+            }
+            s_ptile[p.groups] = pt;
+        }
+        __syncthreads();
+        total_tiles = s_ptile[p.groups] * ntiles_n;
+    } else {
+        total_tiles = ((p.M + 255) / 256) * ntiles_n;
+    }
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int b = 0; b < kSlots; ++b) {
+            mbar_init(smem_u32(&acc_full[b]), 1);
+            mbar_init(smem_u32(&acc_empty[b]), 2 * kEpiWarps);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&sc_full[b]), 32);
+            mbar_init(smem_u32(&sc_empty[b]), kEpiWarps);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmA);
+        prefetch_tensormap(&tmB);
+        prefetch_tensormap(&tmD);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
     __syncthreads();
-    const int32_t m0 = s_row[0], m_end = s_row[1], e = s_row[2], n0 = blockIdx.y * 64;
-    if (m0 >= m_end) return;
-    const uint8_t *B = p.B + static_cast<int64_t>(e) * p.N * p.K;
-    const int32_t kb = (p.K + 127) / 128;
-    const float *B_sf = p.B_sf + static_cast<int64_t>(e) * ((p.N + 127) / 128) * kb;
-    float acc[4][4] = {};
-    for (int32_t b = 0; b < kb; ++b) {
-        float part[4][4] = {};
-        for (int k0 = b * 128; k0 < min(p.K, b * 128 + 128); k0 += 32) {
-            __syncthreads();
-            for (int f = tid; f < 64 * 32; f += 256) {
-                const int r = f >> 5, k = k0 + (f & 31);
-                sa[f & 31][r] = m0 + r < m_end && k < p.K ? decode(p.A[static_cast<int64_t>(m0 + r) * p.K + k], p.a_type) : 0.0f;
-                sb[f & 31][r] = n0 + r < p.N && k < p.K ? decode(B[static_cast<int64_t>(n0 + r) * p.K + k], p.b_type) : 0.0f;
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    if (!GROUPED) pdl_wait();
+    pdl_launch_dependents();
+
+    auto tile_info = [&](int32_t t) {
+        Tile ti;
+        ti.group = 0;
+        int32_t lt = t, mtiles = (p.M + 255) / 256, base = 0;
+        ti.row_end = p.M;
+        if (GROUPED) {
+            const int32_t mt_all = t / ntiles_n;
+            int lo = 0, hi = p.groups - 1;
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (s_ptile[mid] <= mt_all) lo = mid; else hi = mid - 1;
             }
-            __syncthreads();
-            for (int k = 0; k < 32; ++k)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j) part[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], part[i][j]);
+            lt = t - s_ptile[lo] * ntiles_n;
+            mtiles = s_ptile[lo + 1] - s_ptile[lo];
+            base = s_offs[lo];
+            ti.group = lo;
+            ti.row_end = s_offs[lo + 1];
         }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int32_t m = min(m0 + ty * 4 + i, p.M - 1), n = min(n0 + tx * 4 + j, p.N - 1);
-                const float s = p.A_sf[static_cast<int64_t>(b) * p.M + m] *
-                                (p.b_rows == 1 ? B_sf[static_cast<int64_t>(b) * p.N + n]
-                                               : B_sf[static_cast<int64_t>(n / 128) * kb + b]);
-                acc[i][j] = fmaf(s, part[i][j], acc[i][j]);
+        // groups of up to eight row tiles walk the column tiles together, so
+        // that the pairs of one round share operand tiles in L2
+        constexpr int32_t GM = 8;
+        const int32_t per_group = GM * ntiles_n;
+        const int32_t first_m = (lt / per_group) * GM;
+        const int32_t rows_here = min(GM, mtiles - first_m);
+        const int32_t idx = lt % per_group;
+        ti.row0 = base + (first_m + idx % rows_here) * 256;
+        ti.n0 = (idx / rows_here) * 256;
+        return ti;
+    };
+
+    if (warp < 4) {
+        setmaxnreg_dec<40>();
+        if (warp == 0 || warp == 2) {
+            // ------------------------------------------------ A (warp 0) and B (warp 2) TMA producers
+            if (lane == 0) {
+                const bool is_a = warp == 0;
+                const uint32_t full0_leader = mapa_shared(smem_u32(&full[0]), 0);
+                const CUtensorMap *map = is_a ? &tmA : &tmB;
+                uint32_t s = 0, phase = 1;
+                bool ok = true;
+                for (int32_t t = pair_id; t < total_tiles && ok; t += npairs) {
+                    const Tile ti = tile_info(t);
+                    const int32_t row = (is_a ? ti.row0 : ti.group * p.N + ti.n0) + 128 * static_cast<int32_t>(rank);
+                    for (int32_t kb = 0; kb < kblocks; ++kb) {
+                        if (!mbar_wait(smem_u32(&empty[s]), phase)) { ok = false; break; }
+                        if (is_a && rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * kStageBytes);
+                        tma_load_2d_pair(smem_u32(smem + s * kStageBytes + (is_a ? 0 : kOpBytes)), map,
+                                         full0_leader + s * 8, kb * 128, row);
+                        if (++s == kStages) { s = 0; phase ^= 1; }
+                    }
+                }
+                if (!ok) { record_timeout(); *abort_flag = 1; }
             }
+        } else if (warp == 3) {
+            // ------------------------------------------------ scales: kBatch K blocks at a time, copied
+            // straight into one of two halves (4-byte copies: a row of scales need not be aligned)
+            uint32_t b = 0, phase = 1;
+            bool ok = true;
+            const int32_t nb = (p.N + 127) / 128;
+            for (int32_t t = pair_id; t < total_tiles && ok; t += npairs) {
+                const Tile ti = tile_info(t);
+                const int32_t row = ti.row0 + 128 * static_cast<int32_t>(rank) + lane;
+                for (int32_t kb0 = 0; kb0 < kblocks; kb0 += kBatch) {
+                    if (!mbar_wait_warp(smem_u32(&sc_empty[b]), phase)) { ok = false; break; }
+                    uint32_t dst = smem_u32(smem + kOffScale) + b * (kBatch * kScaleFloats * 4);
+                    if (!COLSCALE && lane < 2 * kBatch && kb0 + (lane >> 1) < kblocks) {
+                        // lane 2 u + h: half h's block of B at K block u
+                        cp_async4(dst + ((lane >> 1) * kScaleFloats + 128 + (lane & 1)) * 4,
+                                  p.B_sf + (static_cast<int64_t>(ti.group) * nb + min(ti.n0 / 128 + (lane & 1), nb - 1)) * kblocks +
+                                      kb0 + (lane >> 1));
+                    }
+                    dst += lane * 4;
+                    for (int32_t kb = kb0; kb < min(kb0 + kBatch, kblocks); ++kb, dst += kScaleFloats * 4) {
+                        const float *a = p.A_sf + static_cast<int64_t>(kb) * p.M;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) cp_async4(dst + i * 128, a + min(row + 32 * i, p.M - 1));
+                        if (COLSCALE) {
+                            const float *c = p.B_sf + static_cast<int64_t>(kb) * p.N;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                cp_async4(dst + 512 + i * 128, c + min(ti.n0 + lane + 32 * i, p.N - 1));
+                        }
+                    }
+                    cp_async_arrive(smem_u32(&sc_full[b]));     // every lane, once its copies have landed
+                    b ^= 1;
+                    if (b == 0) phase ^= 1;
+                }
+            }
+            if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
+        } else if (warp == 1) {
+            // ------------------------------------------------ MMA issuer (leader).  Part h of a K block
+            // multiplies with rows [slot columns / 2 * h, ..) of each CTA's 128 rows of B: its slot's
+            // columns are that many of each 128-column half of the tile.
+            if (rank == 0) {
+                // the whole warp keeps count, one lane issues: descriptors stay in uniform registers
+                const uint64_t a_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+                const uint64_t b_desc0 = smem_desc(smem_u32(smem) + kOpBytes, 16, 1024, kSwizzle128B);
+                const uint32_t idesc = idesc_f8(256, kSlotCols, p.a_type, p.b_type);
+                uint32_t s = 0, phase = 0, slot = 0, acc_phase = 1;
+                bool ok = true;
+                for (int32_t t = pair_id; t < total_tiles && ok; t += npairs) {
+                    for (int32_t kb = 0; kb < kblocks && ok; ++kb) {
+                        if (!mbar_wait_warp(smem_u32(&full[s]), phase)) { ok = false; break; }
+                        const uint64_t ad = a_desc0 + s * static_cast<uint64_t>(kStageBytes >> 4);
+                        const uint64_t bd = b_desc0 + s * static_cast<uint64_t>(kStageBytes >> 4);
+#pragma unroll
+                        for (int h = 0; h < kParts; ++h) {
+                            if (!mbar_wait_warp(smem_u32(&acc_empty[slot]), acc_phase)) { ok = false; break; }
+                            tc_fence_after();
+                            if (elect_one_sync()) {
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    tc_mma_f8_pair(tmem_base + slot * kSlotCols, ad + 2 * kk,
+                                                   bd + h * ((kWarpCols * 128) >> 4) + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+                                tc_commit_pair(smem_u32(&acc_full[slot]), 0x3);
+                                if (h == kParts - 1) tc_commit_pair(smem_u32(&empty[s]), 0x3);
+                            }
+                            __syncwarp();
+                            if (++slot == kSlots) { slot = 0; acc_phase ^= 1; }
+                        }
+                        if (++s == kStages) { s = 0; phase ^= 1; }
+                    }
+                }
+                if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
+            }
+        }
+    } else {
+        setmaxnreg_inc<232>();
+        // ------------------------------------------------ epilogue: eight warps, each 32 rows x 128 columns
+        const int quad = warp & 3;
+        const int half = (warp - 4) >> 2;
+        const uint32_t release = mapa_shared(smem_u32(&acc_empty[0]), 0);
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + half * kWarpCols;
+        uint8_t *out = smem + kOffOut + (warp - 4) * 2 * kBoxBytes;
+        const float *s_scale = reinterpret_cast<const float *>(smem + kOffScale);
+        uint32_t slot = 0, phase = 0, b = 0, sc_phase = 0;
+        bool ok = true;
+        for (int32_t t = pair_id; t < total_tiles && ok; t += npairs) {
+            const Tile ti = tile_info(t);
+            const int32_t c0 = ti.n0 + half * 128;
+            float acc[128];
+#pragma unroll
+            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+            bool ready = false;         // the next slot's sum is known to be complete
+            int u = 0;
+            for (int32_t kb = 0; kb < kblocks; ++kb) {
+                if (u == 0 && !mbar_wait_warp(smem_u32(&sc_full[b]), sc_phase)) { ok = false; break; }
+                if (!ready && !mbar_wait_warp(smem_u32(&acc_full[slot]), phase)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t src = taddr + slot * kSlotCols;
+                bool done = false;
+                uint32_t v[2][32];
+                tmem_ld_32x32b_x32(src, v[0]);
+                const float *sc = s_scale + (b * kBatch + u) * kScaleFloats;
+                const float sm = COLSCALE ? sc[quad * 32 + lane] : sc[quad * 32 + lane] * sc[128 + half];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    tmem_ld_wait();
+                    tmem_regs_after_wait(v[c & 1]);
+                    if (c < 3) {
+                        tmem_ld_32x32b_x32(src + (c + 1) * 32, v[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster_relaxed(release + slot * 8);
+                        if (++slot == kSlots) { slot = 0; phase ^= 1; }
+                        done = mbar_test(smem_u32(&acc_full[slot]), phase);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x0 = __uint_as_float(v[c & 1][2 * i]), x1 = __uint_as_float(v[c & 1][2 * i + 1]);
+                        if (COLSCALE) {
+                            const float2 f = *reinterpret_cast<const float2 *>(sc + 128 + half * 128 + c * 32 + 2 * i);
+                            x0 *= f.x; x1 *= f.y;
+                        }
+                        acc[c * 32 + 2 * i] = fmaf(sm, x0, acc[c * 32 + 2 * i]);
+                        acc[c * 32 + 2 * i + 1] = fmaf(sm, x1, acc[c * 32 + 2 * i + 1]);
+                    }
+                }
+                ready = __all_sync(0xffffffffu, done) && kb + 1 < kblocks;
+                if (++u == kBatch || kb == kblocks - 1) {
+                    u = 0;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sc_empty[b]));
+                    b ^= 1;
+                    if (b == 0) sc_phase ^= 1;
+                }
+            }
+            if (!ok) break;
+            // D leaves in boxes of 32 rows x 32 bytes through two staging boxes of the warp's own: by
+            // TMA where D's rows are 16-byte aligned and the box's rows are all this tile's (rows
+            // beyond M are clipped by the map), else in four-byte or single pieces
+            const int32_t wrow0 = ti.row0 + 128 * static_cast<int32_t>(rank) + quad * 32;
+            const int32_t rows = ti.row_end - wrow0;
+            if (rows > 0 && c0 < p.N) {
+                const bool by_tma = p.store_map && (!GROUPED || rows >= 32);
+                if (p.fp32) store_boxes<true>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
+                else store_boxes<false>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
+            }
+            __syncwarp();
+        }
+        if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
+        // the staging boxes must outlive the stores issued from them
+        if (lane == 0) bulk_wait_group<0>();
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int32_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-            if (m >= m_end || n >= p.N) continue;
-            const int64_t at = static_cast<int64_t>(m) * p.N + n;
-            if (p.fp32) {
-                float *d = static_cast<float *>(p.D) + at;
-                *d = p.accumulate ? *d + acc[i][j] : acc[i][j];
-            } else {
-                static_cast<__nv_bfloat16 *>(p.D)[at] = __float2bfloat16_rn(acc[i][j]);
-            }
-        }
+
+    // teardown: lanes that skipped a single-lane role wait for their warp
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (*abort_flag) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) { }
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
 }
 
 bool types_ok(int a_type, int b_type, int out_type)
@@ -145,13 +496,39 @@ bool types_ok(int a_type, int b_type, int out_type)
            (out_type == QFP4_BF16 || out_type == QFP4_FP32);
 }
 
+template <bool GROUPED, bool COLSCALE>
+int launch_pair(Fp8Params p, int64_t tiles, cudaStream_t s)
+{
+    auto kern = gemm_fp8_pair_kernel<GROUPED, COLSCALE>;
+    CUtensorMap ma, mb, md;
+    int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), kPairSmem);
+    if (rc == QFP4_OK) rc = make_map_direct(&ma, p.A, p.K, p.M, 128, 128);
+    if (rc == QFP4_OK) rc = make_map_direct(&mb, p.B, p.K, static_cast<uint64_t>(GROUPED ? p.groups : 1) * p.N, 128, 128);
+    p.store_map = p.N % (p.fp32 ? 4 : 8) == 0;
+    if (rc == QFP4_OK && p.store_map) rc = make_map_store(&md, p.D, p.fp32 != 0, p.N, p.M, p.fp32 ? 8 : 16, 32);
+    else md = ma;       // never used
+    if (rc != QFP4_OK) return rc;
+    const int sms = sm_count();
+    if (sms < 2) return QFP4_ERR_CUDA;
+    const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
+    return launch_status(launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kPairThreads), kPairSmem, s,
+                                    ma, mb, md, p));
+}
+
 int launch_gemm_fp8(const Fp8Params &p, cudaStream_t s)
 {
-    const int64_t tiles = (static_cast<int64_t>(p.M) + 63) / 64 + p.groups;
-    const int64_t tiles_n = (static_cast<int64_t>(p.N) + 63) / 64;
-    if (tiles_n > 65535) return QFP4_ERR_UNSUPPORTED;
-    return launch_status(launch_pdl(gemm_fp8_simple_kernel,
-                                    dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(tiles_n)), dim3(256), 0, s, p));
+    const int64_t tiles_n = (static_cast<int64_t>(p.N) + 255) / 256;
+    int64_t tiles_m = (static_cast<int64_t>(p.M) + 255) / 256;
+    if (p.groups) {
+        // every group may add one partial tile, and none has more than max_group_rows rows
+        tiles_m += p.groups;
+        const int64_t by_max = static_cast<int64_t>(p.groups) * ((p.max_group_rows + 255) / 256);
+        if (p.max_group_rows > 0 && by_max < tiles_m) tiles_m = by_max;
+    }
+    const int64_t tiles = tiles_m * tiles_n;
+    if (tiles > INT32_MAX) return QFP4_ERR_UNSUPPORTED;
+    if (p.groups) return launch_pair<true, false>(p, tiles, s);
+    return p.b_rows == 1 ? launch_pair<false, true>(p, tiles, s) : launch_pair<false, false>(p, tiles, s);
 }
 
 }  // namespace

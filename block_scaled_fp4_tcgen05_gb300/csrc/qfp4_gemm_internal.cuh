@@ -48,6 +48,17 @@ struct GemmParams {
 int make_map(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows, uint32_t box_inner,
              uint32_t box_rows);
 
+// The same map encoded anew, without the record of earlier maps (encoding
+// takes well under a microsecond).
+int make_map_direct(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows, uint32_t box_inner,
+                    uint32_t box_rows);
+
+// Store map of a BF16 or fp32 matrix [rows, cols] with boxes of 32 bytes x
+// box_rows rows in the 32-byte swizzle (the 16-byte halves of rows 4..7 of
+// every eight change places); also encoded anew.
+int make_map_store(CUtensorMap *map, void *base, bool fp32, uint64_t cols, uint64_t rows, uint32_t box_cols,
+                   uint32_t box_rows);
+
 // Packed FP4 matrix [rows, K/2 bytes] viewed as {128 bytes, rows, K/256 blocks}
 // (strides K/2 and 128 bytes), 128-byte swizzle, box {128, 128, 2}: one
 // request brings two consecutive 256-K blocks of 128 rows, laid out as two
