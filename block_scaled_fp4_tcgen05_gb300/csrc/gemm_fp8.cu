@@ -88,7 +88,7 @@ __device__ __forceinline__ bool fp8_offsets_valid(const int32_t *offs, int group
 
 constexpr int kPairThreads = 384;       // 12 warps
 constexpr int kEpiWarps = 8;            // per slot: set h of eight warps drains part h of every K block
-constexpr int kStages = 5;
+constexpr int kStages = 4;
 constexpr int kOpBytes = 128 * 128;     // 128 rows x 128 elements of K
 constexpr int kStageBytes = 2 * kOpBytes;
 constexpr int kSlotCols = 256;          // columns of an accumulator slot
@@ -98,9 +98,10 @@ constexpr int kWarpCols = kSlotCols / 2;        // columns of a slot that one ep
 constexpr int kBatch = 8;               // K blocks per hand-over of scales
 constexpr int kScaleFloats = 128 + 256; // per K block: the CTA's rows, then the tile's columns (or its two blocks)
 constexpr int kOffScale = kStages * kStageBytes;    // two batches
-constexpr int kBoxBytes = 32 * 32;      // output staging box: 32 rows x 32 bytes; two per epilogue warp
+constexpr int kBoxBytes = 32 * 128;     // output staging box: 32 rows x 128 bytes
+constexpr int kBoxes = 2;               // per epilogue warp
 constexpr int kOffOut = kOffScale + 2 * kBatch * kScaleFloats * 4;
-constexpr int kOffBar = kOffOut + kEpiWarps * 2 * kBoxBytes;
+constexpr int kOffBar = kOffOut + kEpiWarps * kBoxes * kBoxBytes;
 constexpr int kPairBars = 2 * kStages + 2 * kSlots + 4;  // full, empty [stage]; acc_full, acc_empty [slot]; sc_full, sc_empty [2]
 constexpr int kPairSmem = kOffBar + kPairBars * 8 + 16 + 1024;
 static_assert(kPairSmem + 4096 <= 232448, "shared memory overflow");
@@ -112,69 +113,76 @@ __device__ __forceinline__ void record_timeout()
 
 
 
-// Writes a warp's 32 rows x kWarpCols columns of D; lane i holds row i.  Box
-// q's 16-byte halves are staged in the 32-byte swizzle of the store map.
+// Writes a warp's 32 rows x 128 columns of D; lane i holds row i.  The rows
+// are staged as boxes of 128 bytes x 32 rows in the 128-byte swizzle of the
+// store map (16-byte piece c of row r at c ^ (r % 8)), up to kBoxes of them at
+// a time, and leave together behind one fence.
 template <bool FP32>
-__device__ __forceinline__ void store_boxes(const float (&acc)[128], uint8_t *out, const CUtensorMap &map,
-                                            const Fp8Params &p, bool by_tma, int32_t row0, int32_t rows, int32_t c0,
-                                            int lane)
+__device__ __forceinline__ void store_tile(const float (&acc)[128], uint8_t *out, const CUtensorMap &map,
+                                           const Fp8Params &p, bool by_tma, int32_t row0, int32_t rows, int32_t c0,
+                                           int lane)
 {
-    constexpr int kCols = FP32 ? 8 : 16;        // columns of a box
+    constexpr int kCols = FP32 ? 32 : 64;       // columns of a box
 #pragma unroll
-    for (int q = 0; q < 128 / kCols; ++q) {
-        const int32_t col = c0 + q * kCols;
-        if (col >= p.N) break;
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float lo, hi;
-            if (FP32) {
-                lo = acc[q * 8 + (i & ~1)]; hi = acc[q * 8 + (i | 1)];
-                w[i] = __float_as_uint(i & 1 ? hi : lo);
-            } else {
-                lo = acc[q * 16 + 2 * i]; hi = acc[q * 16 + 2 * i + 1];
-                __nv_bfloat162 pr = __floats2bfloat162_rn(lo, hi);
-                w[i] = *reinterpret_cast<uint32_t *>(&pr);
-            }
-        }
-        uint8_t *box = out + (q & 1) * kBoxBytes;
-        // the box is free once the copy engine has read the store of two boxes ago
-        if (lane == 0) bulk_wait_group_read<1>();
+    for (int q0 = 0; q0 < 128 / kCols; q0 += kBoxes) {
+        if (c0 + q0 * kCols >= p.N) break;
+        // the boxes are free once the copy engine has read what left them last
+        if (lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
-        const int flip = (lane >> 2) & 1;
-        *reinterpret_cast<uint4 *>(box + lane * 32 + 16 * flip) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4 *>(box + lane * 32 + 16 * (flip ^ 1)) = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+        for (int q = 0; q < kBoxes; ++q)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (FP32) {
+                        w[i] = __float_as_uint(acc[(q0 + q) * 32 + 4 * c + i]);
+                    } else {
+                        const int a = (q0 + q) * 64 + 8 * c + 2 * i;
+                        __nv_bfloat162 pr = __floats2bfloat162_rn(acc[a], acc[a + 1]);
+                        w[i] = *reinterpret_cast<uint32_t *>(&pr);
+                    }
+                }
+                *reinterpret_cast<uint4 *>(out + q * kBoxBytes + lane * 128 + 16 * (c ^ (lane & 7))) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
         if (by_tma) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                if (p.accumulate) tma_reduce_add_2d(&map, smem_u32(box), col, row0);
-                else tma_store_2d(&map, smem_u32(box), col, row0);
+#pragma unroll
+                for (int q = 0; q < kBoxes; ++q) {
+                    const int32_t col = c0 + (q0 + q) * kCols;
+                    if (col >= p.N) break;
+                    if (p.accumulate) tma_reduce_add_2d(&map, smem_u32(out + q * kBoxBytes), col, row0);
+                    else tma_store_2d(&map, smem_u32(out + q * kBoxBytes), col, row0);
+                }
                 bulk_commit_group();
             }
             continue;
         }
         __syncwarp();
-        // four rows at a time, lane = 8 row + word
+        // a row's 128 bytes of a box at a time, a word per lane
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (lane >> 3), word = lane & 7;
-            const uint32_t v = *reinterpret_cast<const uint32_t *>(
-                box + r * 32 + 16 * ((word >> 2) ^ ((r >> 2) & 1)) + 4 * (word & 3));
-            if (r >= rows) break;
-            const int64_t at = static_cast<int64_t>(row0 + r) * p.N;
-            if (FP32) {
-                if (col + word < p.N) {
-                    float *d = static_cast<float *>(p.D) + at + col + word;
-                    *d = p.accumulate ? *d + __uint_as_float(v) : __uint_as_float(v);
-                }
-            } else {
-                uint16_t *d = static_cast<uint16_t *>(p.D) + at + col + 2 * word;
-                if (p.N % 2 == 0) {
-                    if (col + 2 * word < p.N) *reinterpret_cast<uint32_t *>(d) = v;
+        for (int q = 0; q < kBoxes; ++q) {
+            const int32_t col = c0 + (q0 + q) * kCols + (FP32 ? lane : 2 * lane);
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r) {
+                const uint32_t v = *reinterpret_cast<const uint32_t *>(
+                    out + q * kBoxBytes + r * 128 + 16 * ((lane >> 2) ^ (r & 7)) + 4 * (lane & 3));
+                const int64_t at = static_cast<int64_t>(row0 + r) * p.N + col;
+                if (FP32) {
+                    float *d = static_cast<float *>(p.D) + at;
+                    if (col < p.N) *d = p.accumulate ? *d + __uint_as_float(v) : __uint_as_float(v);
                 } else {
-                    if (col + 2 * word < p.N) d[0] = static_cast<uint16_t>(v);
-                    if (col + 2 * word + 1 < p.N) d[1] = static_cast<uint16_t>(v >> 16);
+                    uint16_t *d = static_cast<uint16_t *>(p.D) + at;
+                    if (p.N % 2 == 0) {
+                        if (col < p.N) *reinterpret_cast<uint32_t *>(d) = v;
+                    } else {
+                        if (col < p.N) d[0] = static_cast<uint16_t>(v);
+                        if (col + 1 < p.N) d[1] = static_cast<uint16_t>(v >> 16);
+                    }
                 }
             }
         }
@@ -402,7 +410,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         const int half = (warp - 4) >> 2;
         const uint32_t release = mapa_shared(smem_u32(&acc_empty[0]), 0);
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + half * kWarpCols;
-        uint8_t *out = smem + kOffOut + (warp - 4) * 2 * kBoxBytes;
+        uint8_t *out = smem + kOffOut + (warp - 4) * kBoxes * kBoxBytes;
         const float *s_scale = reinterpret_cast<const float *>(smem + kOffScale);
         uint32_t slot = 0, phase = 0, b = 0, sc_phase = 0;
         bool ok = true;
@@ -422,32 +430,40 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 bool done = false;
                 uint32_t v[2][32];
                 tmem_ld_32x32b_x32(src, v[0]);
+                tmem_ld_32x32b_x32(src + 32, v[1]);
                 const float *sc = s_scale + (b * kBatch + u) * kScaleFloats;
                 const float sm = COLSCALE ? sc[quad * 32 + lane] : sc[quad * 32 + lane] * sc[128 + half];
+                auto add32 = [&](const uint32_t (&x)[32], int c) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    tmem_ld_wait();
-                    tmem_regs_after_wait(v[c & 1]);
-                    if (c < 3) {
-                        tmem_ld_32x32b_x32(src + (c + 1) * 32, v[(c + 1) & 1]);
-                    } else {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster_relaxed(release + slot * 8);
-                        if (++slot == kSlots) { slot = 0; phase ^= 1; }
-                        done = mbar_test(smem_u32(&acc_full[slot]), phase);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float x0 = __uint_as_float(v[c & 1][2 * i]), x1 = __uint_as_float(v[c & 1][2 * i + 1]);
+                    for (int i = 0; i < 8; ++i) {
+                        float f[4] = {sm, sm, sm, sm};
                         if (COLSCALE) {
-                            const float2 f = *reinterpret_cast<const float2 *>(sc + 128 + half * 128 + c * 32 + 2 * i);
-                            x0 *= f.x; x1 *= f.y;
+                            const float4 q = *reinterpret_cast<const float4 *>(sc + 128 + half * 128 + c * 32 + 4 * i);
+                            unpack_f32x2(mul_f32x2(pack_f32x2(q.x, q.y), pack_f32x2(sm, sm)), f[0], f[1]);
+                            unpack_f32x2(mul_f32x2(pack_f32x2(q.z, q.w), pack_f32x2(sm, sm)), f[2], f[3]);
                         }
-                        acc[c * 32 + 2 * i] = fmaf(sm, x0, acc[c * 32 + 2 * i]);
-                        acc[c * 32 + 2 * i + 1] = fmaf(sm, x1, acc[c * 32 + 2 * i + 1]);
+#pragma unroll
+                        for (int z = 0; z < 4; ++z)
+                            acc[c * 32 + 4 * i + z] = fmaf(f[z], __uint_as_float(x[4 * i + z]), acc[c * 32 + 4 * i + z]);
                     }
-                }
+                };
+                tmem_ld_wait();
+                tmem_regs_after_wait(v[0]);
+                tmem_regs_after_wait(v[1]);
+                add32(v[0], 0);
+                tmem_ld_32x32b_x32(src + 64, v[0]);
+                add32(v[1], 1);
+                tmem_ld_32x32b_x32(src + 96, v[1]);
+                tmem_ld_wait();
+                tmem_regs_after_wait(v[0]);
+                tmem_regs_after_wait(v[1]);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(release + slot * 8);
+                if (++slot == kSlots) { slot = 0; phase ^= 1; }
+                done = mbar_test(smem_u32(&acc_full[slot]), phase);
+                add32(v[0], 2);
+                add32(v[1], 3);
                 ready = __all_sync(0xffffffffu, done) && kb + 1 < kblocks;
                 if (++u == kBatch || kb == kblocks - 1) {
                     u = 0;
@@ -465,8 +481,8 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             const int32_t rows = ti.row_end - wrow0;
             if (rows > 0 && c0 < p.N) {
                 const bool by_tma = p.store_map && (!GROUPED || rows >= 32);
-                if (p.fp32) store_boxes<true>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
-                else store_boxes<false>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
+                if (p.fp32) store_tile<true>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
+                else store_tile<false>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
             }
             __syncwarp();
         }
@@ -505,7 +521,7 @@ int launch_pair(Fp8Params p, int64_t tiles, cudaStream_t s)
     if (rc == QFP4_OK) rc = make_map_direct(&ma, p.A, p.K, p.M, 128, 128);
     if (rc == QFP4_OK) rc = make_map_direct(&mb, p.B, p.K, static_cast<uint64_t>(GROUPED ? p.groups : 1) * p.N, 128, 128);
     p.store_map = p.N % (p.fp32 ? 4 : 8) == 0;
-    if (rc == QFP4_OK && p.store_map) rc = make_map_store(&md, p.D, p.fp32 != 0, p.N, p.M, p.fp32 ? 8 : 16, 32);
+    if (rc == QFP4_OK && p.store_map) rc = make_map_store(&md, p.D, p.fp32 != 0, p.N, p.M, p.fp32 ? 32 : 64, 32);
     else md = ma;       // never used
     if (rc != QFP4_OK) return rc;
     const int sms = sm_count();

@@ -53,9 +53,8 @@ int make_map(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows, 
 int make_map_direct(CUtensorMap *map, const void *base, uint64_t inner, uint64_t rows, uint32_t box_inner,
                     uint32_t box_rows);
 
-// Store map of a BF16 or fp32 matrix [rows, cols] with boxes of 32 bytes x
-// box_rows rows in the 32-byte swizzle (the 16-byte halves of rows 4..7 of
-// every eight change places); also encoded anew.
+// Store map of a BF16 or fp32 matrix [rows, cols] with boxes of up to 128 bytes
+// x box_rows rows in the 128-byte swizzle; also encoded anew.
 int make_map_store(CUtensorMap *map, void *base, bool fp32, uint64_t cols, uint64_t rows, uint32_t box_cols,
                    uint32_t box_rows);
 
