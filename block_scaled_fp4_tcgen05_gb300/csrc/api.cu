@@ -7,6 +7,7 @@
 #include <utility>
 
 #include "qfp4_common.cuh"
+#include "qfp4_gemm_fp8.cuh"
 #include "qfp4_gemm_internal.cuh"
 
 namespace qfp4 {
@@ -74,16 +75,17 @@ extern "C" int qfp4_device_check(void)
 extern "C" int qfp4_poll_device_status(void *stream)
 {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    uint32_t q = 0, g = 0, gp = 0, gd = 0, gs = 0, g8 = 0, q8 = 0;
+    uint32_t q = 0, g = 0, gp = 0, gd = 0, gs = 0, g8 = 0, s8 = 0, q8 = 0;
     int rc = qfp4::read_clear_status_quant(s, &q);
     if (rc == QFP4_OK) rc = qfp4::read_clear_status_gemm(s, &g);
     if (rc == QFP4_OK) rc = qfp4::read_clear_status_gemm_pair(s, &gp);
     if (rc == QFP4_OK) rc = qfp4::read_clear_status_gemm_decode(s, &gd);
     if (rc == QFP4_OK) rc = qfp4::read_clear_status_gemm_sparse(s, &gs);
     if (rc == QFP4_OK) rc = qfp4::read_clear_status_gemm_fp8(s, &g8);
+    if (rc == QFP4_OK) rc = qfp4::read_clear_status_gemm_fp8_small(s, &s8);
     if (rc == QFP4_OK) rc = qfp4::read_clear_status_fp8_quant(s, &q8);
     if (rc != QFP4_OK) return rc;
-    const uint32_t all = q | g | gp | gd | gs | g8 | q8;
+    const uint32_t all = q | g | gp | gd | gs | g8 | s8 | q8;
     if (all & qfp4::kStatusTimeout) return QFP4_ERR_TIMEOUT;
     if (all & (qfp4::kStatusBadGroup | qfp4::kStatusBadSparsity)) return QFP4_ERR_INVALID_ARG;
     return QFP4_OK;

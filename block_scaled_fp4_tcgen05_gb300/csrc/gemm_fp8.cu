@@ -33,6 +33,7 @@
 #include <cuda_runtime.h>
 
 #include "qfp4_common.cuh"
+#include "qfp4_gemm_fp8.cuh"
 #include "qfp4_gemm_internal.cuh"
 #include "sm103_ptx.cuh"
 
@@ -58,19 +59,6 @@ namespace {
 constexpr int kMaxGroups = 256;
 constexpr int64_t kMaxSize = int64_t{1} << 30;
 
-struct Fp8Params {
-    const uint8_t *A, *B;
-    const float *A_sf, *B_sf;
-    void *D;
-    const int32_t *row_offsets;     // grouped: DEVICE [groups + 1]
-    int32_t M, N, K;                // grouped: M = total_rows
-    int32_t groups;                 // 0: dense
-    int32_t max_group_rows;         // grouped: 0 = no bound
-    int32_t a_type, b_type, b_rows;
-    int32_t fp32, accumulate;
-    int32_t store_map;              // D can be written by TMA (rows 16-byte aligned)
-};
-
 // Row offsets a grouped product can use: from 0, never decreasing, at most
 // total_rows, no group above max_rows (0 = no bound).
 __device__ __forceinline__ bool fp8_offsets_valid(const int32_t *offs, int groups, int32_t total_rows,
@@ -91,10 +79,7 @@ constexpr int kEpiWarps = 8;            // per slot: set h of eight warps drains
 constexpr int kStages = 4;
 constexpr int kOpBytes = 128 * 128;     // 128 rows x 128 elements of K
 constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kSlotCols = 256;          // columns of an accumulator slot
-constexpr int kSlots = 512 / kSlotCols;
-constexpr int kParts = 256 / kSlotCols; // slots per K block
-constexpr int kWarpCols = kSlotCols / 2;        // columns of a slot that one epilogue warp reads
+constexpr int kSlots = 2;               // accumulator slots of 256 columns
 constexpr int kBatch = 8;               // K blocks per hand-over of scales
 constexpr int kScaleFloats = 128 + 256; // per K block: the CTA's rows, then the tile's columns (or its two blocks)
 constexpr int kOffScale = kStages * kStageBytes;    // two batches
@@ -367,37 +352,33 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             }
             if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
         } else if (warp == 1) {
-            // ------------------------------------------------ MMA issuer (leader).  Part h of a K block
-            // multiplies with rows [slot columns / 2 * h, ..) of each CTA's 128 rows of B: its slot's
-            // columns are that many of each 128-column half of the tile.
+            // ------------------------------------------------ MMA issuer (leader): a K block's sum into each
+            // slot in turn
             if (rank == 0) {
                 // the whole warp keeps count, one lane issues: descriptors stay in uniform registers
                 const uint64_t a_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
                 const uint64_t b_desc0 = smem_desc(smem_u32(smem) + kOpBytes, 16, 1024, kSwizzle128B);
-                const uint32_t idesc = idesc_f8(256, kSlotCols, p.a_type, p.b_type);
+                const uint32_t idesc = idesc_f8(256, 256, p.a_type, p.b_type);
                 uint32_t s = 0, phase = 0, slot = 0, acc_phase = 1;
-                bool ok = true;
+                bool ok = true, loaded = false;     // loaded: the next stage is known to have landed
                 for (int32_t t = pair_id; t < total_tiles && ok; t += npairs) {
-                    for (int32_t kb = 0; kb < kblocks && ok; ++kb) {
-                        if (!mbar_wait_warp(smem_u32(&full[s]), phase)) { ok = false; break; }
+                    for (int32_t kb = 0; kb < kblocks; ++kb) {
+                        if (!loaded && !mbar_wait_warp(smem_u32(&full[s]), phase)) { ok = false; break; }
                         const uint64_t ad = a_desc0 + s * static_cast<uint64_t>(kStageBytes >> 4);
                         const uint64_t bd = b_desc0 + s * static_cast<uint64_t>(kStageBytes >> 4);
+                        if (!mbar_wait_warp(smem_u32(&acc_empty[slot]), acc_phase)) { ok = false; break; }
+                        tc_fence_after();
+                        if (elect_one_sync()) {
 #pragma unroll
-                        for (int h = 0; h < kParts; ++h) {
-                            if (!mbar_wait_warp(smem_u32(&acc_empty[slot]), acc_phase)) { ok = false; break; }
-                            tc_fence_after();
-                            if (elect_one_sync()) {
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    tc_mma_f8_pair(tmem_base + slot * kSlotCols, ad + 2 * kk,
-                                                   bd + h * ((kWarpCols * 128) >> 4) + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-                                tc_commit_pair(smem_u32(&acc_full[slot]), 0x3);
-                                if (h == kParts - 1) tc_commit_pair(smem_u32(&empty[s]), 0x3);
-                            }
-                            __syncwarp();
-                            if (++slot == kSlots) { slot = 0; acc_phase ^= 1; }
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc_mma_f8_pair(tmem_base + slot * 256, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+                            tc_commit_pair(smem_u32(&acc_full[slot]), 0x3);
+                            tc_commit_pair(smem_u32(&empty[s]), 0x3);
                         }
+                        __syncwarp();
+                        if (++slot == kSlots) { slot = 0; acc_phase ^= 1; }
                         if (++s == kStages) { s = 0; phase ^= 1; }
+                        loaded = __all_sync(0xffffffffu, mbar_test(smem_u32(&full[s]), phase));
                     }
                 }
                 if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
@@ -409,7 +390,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         const int quad = warp & 3;
         const int half = (warp - 4) >> 2;
         const uint32_t release = mapa_shared(smem_u32(&acc_empty[0]), 0);
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + half * kWarpCols;
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
         uint8_t *out = smem + kOffOut + (warp - 4) * kBoxes * kBoxBytes;
         const float *s_scale = reinterpret_cast<const float *>(smem + kOffScale);
         uint32_t slot = 0, phase = 0, b = 0, sc_phase = 0;
@@ -426,7 +407,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 if (u == 0 && !mbar_wait_warp(smem_u32(&sc_full[b]), sc_phase)) { ok = false; break; }
                 if (!ready && !mbar_wait_warp(smem_u32(&acc_full[slot]), phase)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t src = taddr + slot * kSlotCols;
+                const uint32_t src = taddr + slot * 256;
                 bool done = false;
                 uint32_t v[2][32];
                 tmem_ld_32x32b_x32(src, v[0]);
@@ -533,6 +514,7 @@ int launch_pair(Fp8Params p, int64_t tiles, cudaStream_t s)
 
 int launch_gemm_fp8(const Fp8Params &p, cudaStream_t s)
 {
+    if (gemm_fp8_small_pays(p)) return launch_gemm_fp8_small(p, s);
     const int64_t tiles_n = (static_cast<int64_t>(p.N) + 255) / 256;
     int64_t tiles_m = (static_cast<int64_t>(p.M) + 255) / 256;
     if (p.groups) {

@@ -1,0 +1,394 @@
+// gemm_fp8_small.cu -- the product of gemm_fp8.cu for few rows of A (decoding
+// tokens, short prompts), where 256 x 256 tiles would leave most SMs idle and
+// the weights' bytes bound the time.
+//
+// Swap AB: 128 rows of B take the MMA's M slot and up to NT rows of A its N
+// slot, so a CTA (tcgen05 cta_group::1) computes D^T for one 128 x NT tile.  K
+// is split over the S CTAs of a cluster, each streaming its own K blocks (16 KB
+// of B and NT x 128 bytes of A per block) through a ring; as in gemm_fp8.cu the
+// block sums leave tensor memory (two slots of NT columns) for registers, here
+// with a row scale per thread (B's) and a column scale per token (A's).  At the
+// end every CTA leaves its sums in its shared memory, the cluster meets, and
+// CTA r adds up tokens r, r + S, ... over the S CTAs in order (the results
+// repeat bit for bit, and no scratch in global memory is needed).
+//
+// Warps: 0 TMA producer, 1 tensor-memory owner and MMA issuer, 2 scales, 4..
+// epilogue (four, or eight for NT = 128, each 32 rows of B).
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "qfp4_common.cuh"
+#include "qfp4_gemm_fp8.cuh"
+#include "qfp4_gemm_internal.cuh"
+#include "sm103_ptx.cuh"
+
+namespace qfp4 {
+
+__device__ uint32_t g_status_gemm_fp8_small = 0;
+
+int read_clear_status_gemm_fp8_small(cudaStream_t s, uint32_t *out)
+{
+    uint32_t zero = 0;
+    if (cudaMemcpyFromSymbolAsync(out, g_status_gemm_fp8_small, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s) !=
+        cudaSuccess)
+        return QFP4_ERR_CUDA;
+    if (cudaStreamSynchronize(s) != cudaSuccess) return QFP4_ERR_CUDA;
+    if (cudaMemcpyToSymbolAsync(g_status_gemm_fp8_small, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, s) !=
+        cudaSuccess)
+        return QFP4_ERR_CUDA;
+    return cudaStreamSynchronize(s) == cudaSuccess ? QFP4_OK : QFP4_ERR_CUDA;
+}
+
+namespace {
+
+constexpr int kMaxSplits = 8;       // CTAs of a cluster (the portable limit)
+constexpr int kBatch = 4;           // K blocks per hand-over of scales
+
+template <int NT>
+struct SmallCfg {
+    static constexpr int EPI = NT == 128 ? 8 : 4;               // epilogue warps
+    static constexpr int THREADS = 128 + 32 * EPI;
+    static constexpr int COLS = NT == 128 ? 64 : NT;            // token columns per epilogue warp
+    static constexpr int CTAS = NT == 128 ? 1 : 2;              // resident CTAs per SM that the ring is sized for
+    static constexpr int W_BYTES = 128 * 128;
+    static constexpr int STAGE = W_BYTES + NT * 128;
+    static constexpr int STAGES = NT == 128 ? 5 : NT == 64 ? 4 : 5;
+    static constexpr int SCALES = NT + 128;                     // floats per K block: tokens, then rows of B
+    static constexpr int OFF_SCALE = STAGES * STAGE;
+    static constexpr int OFF_BAR = OFF_SCALE + 2 * kBatch * SCALES * 4;
+    static constexpr int NBAR = 2 * STAGES + 4 + 4;             // full, empty; acc_full, acc_empty [2]; sc_full, sc_empty [2]
+    static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
+    static constexpr int TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
+    static_assert(NT * 128 * 4 <= OFF_SCALE, "the sums must fit in the ring");
+    static_assert(CTAS * (SMEM + 1024) <= 233472, "shared memory overflow");
+};
+
+__device__ __forceinline__ void record_timeout()
+{
+    atomicOr(&g_status_gemm_fp8_small, static_cast<uint32_t>(kStatusTimeout));
+}
+
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// PER_ROW: B has one scale per row (b_rows = 1), else one per 128 rows.
+template <int NT, bool PER_ROW>
+__global__ void __launch_bounds__(SmallCfg<NT>::THREADS, SmallCfg<NT>::CTAS)
+gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
+                      const Fp8Params p, const int splits)
+{
+    using C = SmallCfg<NT>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
+    uint64_t *empty = full + C::STAGES;
+    uint64_t *acc_full = empty + C::STAGES;
+    uint64_t *acc_empty = acc_full + 2;
+    uint64_t *sc_full = acc_empty + 2;
+    uint64_t *sc_empty = sc_full + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sc_empty + 2);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    const int32_t tiles_n = (p.N + 127) / 128;
+    const int32_t tile = blockIdx.x / splits;
+    const int32_t n0 = (tile % tiles_n) * 128, m0 = (tile / tiles_n) * NT;
+    const int32_t kblocks = (p.K + 127) / 128;
+    const int32_t kb0 = static_cast<int32_t>(static_cast<int64_t>(rank) * kblocks / splits);
+    const int32_t nkb = static_cast<int32_t>(static_cast<int64_t>(rank + 1) * kblocks / splits) - kb0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&acc_full[b]), 1);
+            mbar_init(smem_u32(&acc_empty[b]), C::EPI);
+            mbar_init(smem_u32(&sc_full[b]), 32);
+            mbar_init(smem_u32(&sc_empty[b]), C::EPI);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmT);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            uint32_t s = 0, phase = 1;
+            bool ok = true;
+            for (int32_t j = 0; j < nkb; ++j) {
+                if (!mbar_wait(smem_u32(&empty[s]), phase)) { ok = false; break; }
+                const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(smem + s * C::STAGE);
+                mbar_arrive_expect_tx(bar, C::STAGE);
+                tma_load_2d(dst, &tmW, bar, (kb0 + j) * 128, n0);
+                tma_load_2d(dst + C::W_BYTES, &tmT, bar, (kb0 + j) * 128, m0);
+                if (++s == C::STAGES) { s = 0; phase ^= 1; }
+            }
+            if (!ok) { record_timeout(); *abort_flag = 1; }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer
+        const uint64_t w_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+        const uint64_t t_desc0 = smem_desc(smem_u32(smem) + C::W_BYTES, 16, 1024, kSwizzle128B);
+        const uint32_t idesc = idesc_f8(128, NT, p.b_type, p.a_type);
+        uint32_t s = 0, phase = 0, slot = 0, acc_phase = 1;
+        bool ok = true;
+        for (int32_t j = 0; j < nkb; ++j) {
+            if (!mbar_wait_warp(smem_u32(&full[s]), phase) || !mbar_wait_warp(smem_u32(&acc_empty[slot]), acc_phase)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (elect_one_sync()) {
+                const uint64_t wd = w_desc0 + s * static_cast<uint64_t>(C::STAGE >> 4);
+                const uint64_t td = t_desc0 + s * static_cast<uint64_t>(C::STAGE >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc_mma_f8(tmem_base + slot * NT, wd + 2 * kk, td + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+                tc_commit(smem_u32(&acc_full[slot]));
+                tc_commit(smem_u32(&empty[s]));
+            }
+            __syncwarp();
+            slot ^= 1;
+            if (slot == 0) acc_phase ^= 1;
+            if (++s == C::STAGES) { s = 0; phase ^= 1; }
+        }
+        if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
+    } else if (warp == 2) {
+        // ------------------------------------------------ scales, kBatch K blocks at a time
+        uint32_t b = 0, phase = 1;
+        bool ok = true;
+        for (int32_t j0 = 0; j0 < nkb; j0 += kBatch) {
+            if (!mbar_wait_warp(smem_u32(&sc_empty[b]), phase)) { ok = false; break; }
+            const uint32_t dst0 = smem_u32(smem + C::OFF_SCALE) + b * (kBatch * C::SCALES * 4);
+            for (int u = 0; u < kBatch && j0 + u < nkb; ++u) {
+                const int64_t kb = kb0 + j0 + u;
+                const uint32_t dst = dst0 + u * (C::SCALES * 4) + lane * 4;
+#pragma unroll
+                for (int i = 0; i < (NT + 31) / 32; ++i)
+                    if (32 * i + lane < NT) cp_async4(dst + 128 * i, p.A_sf + kb * p.M + min(m0 + lane + 32 * i, p.M - 1));
+                if (PER_ROW) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        cp_async4(dst + NT * 4 + 128 * i, p.B_sf + kb * p.N + min(n0 + lane + 32 * i, p.N - 1));
+                } else if (lane == 0) {
+                    cp_async4(dst + NT * 4, p.B_sf + static_cast<int64_t>(n0 / 128) * kblocks + kb);
+                }
+            }
+            cp_async_arrive(smem_u32(&sc_full[b]));
+            b ^= 1;
+            if (b == 0) phase ^= 1;
+        }
+        if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
+    } else if (warp >= 4) {
+        // ------------------------------------------------ epilogue: 32 rows of B x COLS tokens per warp
+        const int quad = warp & 3, c0 = ((warp - 4) >> 2) * C::COLS;
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c0;
+        constexpr int kLd = C::COLS < 32 ? 16 : 32;      // columns per load
+        float acc[C::COLS];
+#pragma unroll
+        for (int i = 0; i < C::COLS; ++i) acc[i] = 0.0f;
+        uint32_t slot = 0, phase = 0, b = 0, sc_phase = 0;
+        int u = 0;
+        bool ok = true;
+        for (int32_t j = 0; j < nkb; ++j) {
+            if (u == 0 && !mbar_wait_warp(smem_u32(&sc_full[b]), sc_phase)) { ok = false; break; }
+            const float *sc = reinterpret_cast<const float *>(smem + C::OFF_SCALE) + (b * kBatch + u) * C::SCALES;
+            const float row = sc[NT + (PER_ROW ? quad * 32 + lane : 0)];
+            if (!mbar_wait_warp(smem_u32(&acc_full[slot]), phase)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < C::COLS / kLd; ++c) {
+                uint32_t v[kLd];
+                if constexpr (kLd == 16) tmem_ld_32x32b_x16(taddr + slot * NT, v);
+                else tmem_ld_32x32b_x32(taddr + slot * NT + c * 32, v);
+                tmem_ld_wait();
+                tmem_regs_after_wait(v);
+                if (c == C::COLS / kLd - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&acc_empty[slot]));
+                }
+#pragma unroll
+                for (int i = 0; i < kLd; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(sc + c0 + c * kLd + i);
+                    float *a = acc + c * kLd + i;
+                    a[0] = fmaf(__fmul_rn(f.x, row), __uint_as_float(v[i]), a[0]);
+                    a[1] = fmaf(__fmul_rn(f.y, row), __uint_as_float(v[i + 1]), a[1]);
+                    a[2] = fmaf(__fmul_rn(f.z, row), __uint_as_float(v[i + 2]), a[2]);
+                    a[3] = fmaf(__fmul_rn(f.w, row), __uint_as_float(v[i + 3]), a[3]);
+                }
+            }
+            slot ^= 1;
+            if (slot == 0) phase ^= 1;
+            if (++u == kBatch || j == nkb - 1) {
+                u = 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sc_empty[b]));
+                b ^= 1;
+                if (b == 0) sc_phase ^= 1;
+            }
+        }
+        if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
+        // the last block's MMAs have read the ring and every copy into it was
+        // waited for by one of them: it now takes the sums, [token][row of B]
+        if (ok) {
+            float *red = reinterpret_cast<float *>(smem) + c0 * 128 + quad * 32 + lane;
+#pragma unroll
+            for (int i = 0; i < C::COLS; ++i) red[i * 128] = acc[i];
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    if (splits > 1) cluster_sync_all(); else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, C::TMEM_COLS);
+    }
+    // a CTA that gave up leaves undefined sums; the status word says so
+    const int32_t tokens = min(NT, p.M - m0);
+    const uint32_t red0 = smem_u32(smem) + lane * 16;
+    const int32_t n = n0 + 4 * lane;
+    for (int32_t t = rank + splits * warp; t < tokens; t += splits * (C::THREADS / 32)) {
+        float4 a;
+        if (splits == 1) {
+            a = reinterpret_cast<const float4 *>(smem + t * 512)[lane];
+        } else {
+            a = ld_cluster_v4(mapa_shared(red0 + t * 512, 0));
+            for (int q = 1; q < splits; ++q) {
+                const float4 o = ld_cluster_v4(mapa_shared(red0 + t * 512, q));
+                a = make_float4(a.x + o.x, a.y + o.y, a.z + o.z, a.w + o.w);
+            }
+        }
+        const float o[4] = {a.x, a.y, a.z, a.w};
+        const int64_t at = static_cast<int64_t>(m0 + t) * p.N + n;
+        if (p.fp32) {
+            float *d = static_cast<float *>(p.D) + at;
+            if (p.N % 4 == 0) {
+                if (n < p.N) {
+                    if (p.accumulate) {
+                        const float4 old = *reinterpret_cast<const float4 *>(d);
+                        a = make_float4(a.x + old.x, a.y + old.y, a.z + old.z, a.w + old.w);
+                    }
+                    *reinterpret_cast<float4 *>(d) = a;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n + i < p.N) d[i] = p.accumulate ? o[i] + d[i] : o[i];
+            }
+        } else {
+            __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(p.D) + at;
+            if (p.N % 4 == 0) {
+                if (n < p.N) {
+                    __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
+                    *reinterpret_cast<uint2 *>(d) = make_uint2(*reinterpret_cast<uint32_t *>(&lo),
+                                                               *reinterpret_cast<uint32_t *>(&hi));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (n + i < p.N) d[i] = __float2bfloat16_rn(o[i]);
+            }
+        }
+    }
+    // no CTA may leave while another still reads its sums
+    __syncwarp();
+    if (splits > 1) cluster_sync_all();
+    if (*abort_flag) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) { }
+    }
+}
+
+template <int NT, bool PER_ROW>
+int launch(const Fp8Params &p, int splits, cudaStream_t s)
+{
+    using C = SmallCfg<NT>;
+    auto kern = gemm_fp8_small_kernel<NT, PER_ROW>;
+    CUtensorMap mw, mt;
+    int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM);
+    if (rc == QFP4_OK) rc = make_map_direct(&mw, p.B, p.K, p.N, 128, 128);
+    if (rc == QFP4_OK) rc = make_map_direct(&mt, p.A, p.K, p.M, 128, NT);
+    if (rc != QFP4_OK) return rc;
+    const int64_t tiles = static_cast<int64_t>((p.N + 127) / 128) * ((p.M + NT - 1) / NT);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = splits > 1 ? 2 : 1;
+    return launch_status(cudaLaunchKernelEx(&cfg, kern, mw, mt, p, splits));
+}
+
+template <int NT>
+int launch_nt(const Fp8Params &p, int splits, cudaStream_t s)
+{
+    return p.b_rows == 1 ? launch<NT, true>(p, splits, s) : launch<NT, false>(p, splits, s);
+}
+
+int tokens_of(const Fp8Params &p) { return p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128; }
+
+}  // namespace
+
+bool gemm_fp8_small_pays(const Fp8Params &p)
+{
+    if (p.groups) return false;
+    if (p.M <= 128) return true;
+    const int64_t pairs = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + 255) / 256);
+    return pairs < sm_count() / 4;
+}
+
+int launch_gemm_fp8_small(const Fp8Params &p, cudaStream_t s)
+{
+    const int nt = tokens_of(p);
+    const int64_t tiles = static_cast<int64_t>((p.N + 127) / 128) * ((p.M + nt - 1) / nt);
+    const int64_t kblocks = (static_cast<int64_t>(p.K) + 127) / 128;
+    const int64_t room = static_cast<int64_t>(sm_count()) * (nt == 128 ? 1 : 2);
+    if (tiles > INT32_MAX / kMaxSplits) return QFP4_ERR_UNSUPPORTED;
+    int splits = 1;
+    while (splits < kMaxSplits && tiles * splits * 2 <= room && kblocks >= 2 * splits) splits *= 2;
+    switch (nt) {
+    case 16: return launch_nt<16>(p, splits, s);
+    case 32: return launch_nt<32>(p, splits, s);
+    case 64: return launch_nt<64>(p, splits, s);
+    default: return launch_nt<128>(p, splits, s);
+    }
+}
+
+}  // namespace qfp4
