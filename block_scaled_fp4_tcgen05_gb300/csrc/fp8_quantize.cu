@@ -107,7 +107,7 @@ fp8_quantize_kernel(const QuantParams p)
     // column 8 c + j lies at i ^ c ^ (j & 1), so that neither the writes (16
     // values of c at one j) nor the reads (four columns of one c) collide.
     __shared__ __align__(16) uint2 s_t[COLS ? 128 * 16 : 1];
-    __shared__ float s_amax[COLS && !BLOCK ? 8 * 128 : 8];
+    __shared__ __align__(16) float s_amax[COLS && !BLOCK ? 8 * 128 : 8];
 
     const int tid = threadIdx.x;
     const int c = tid & 15, i = tid >> 4, warp = tid >> 5, lane = tid & 31;
@@ -168,25 +168,53 @@ fp8_quantize_kernel(const QuantParams p)
     }
 
     if (ROWS || BLOCK) {
+        // Row scales.  Each halving exchange leaves a thread half as many rows
+        // and the maximum over twice as many threads, so that after three of
+        // them (and one plain one) lanes 2 r, 2 r + 1 of the 16 that share R
+        // rows hold row r's maximum, and every scale is computed once or
+        // twice, not sixteen times; the threads then fetch theirs back.
+        float mine = 0.0f;
+        Scale s = block;
+        if (ROWS) {
+            if (R == 8) {
+                float h[4], q[2];
+                const bool b3 = (c & 8) != 0, b2 = (c & 4) != 0, b1 = (c & 2) != 0;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float keep = b3 ? ra[(r + 4) % R] : ra[r % R], give = b3 ? ra[r % R] : ra[(r + 4) % R];
+                    h[r] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 8));
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float keep = b2 ? h[r + 2] : h[r], give = b2 ? h[r] : h[r + 2];
+                    q[r] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+                }
+                mine = fmaxf(b1 ? q[1] : q[0], __shfl_xor_sync(0xffffffffu, b1 ? q[0] : q[1], 2));
+                mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
+            } else {
+                float h = 0.0f;
+                const bool b3 = (c & 8) != 0;
+                h = fmaxf(b3 ? ra[R - 1] : ra[0], __shfl_xor_sync(0xffffffffu, b3 ? ra[0] : ra[R - 1], 8));
+                h = fmaxf(h, __shfl_xor_sync(0xffffffffu, h, 4));
+                h = fmaxf(h, __shfl_xor_sync(0xffffffffu, h, 2));
+                mine = fmaxf(h, __shfl_xor_sync(0xffffffffu, h, 1));
+            }
+            s = block_scale<TYPE, POW2>(mine);
+            constexpr int kPer = 16 / R;            // lanes that hold one row's scale
+            const int32_t m = m0 + c / kPer;
+            if (c % kPer == 0 && m < p.M) p.SF[static_cast<int64_t>(kblock) * p.M + m] = s.s;
+        }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            Scale s = block;
-            if (ROWS) {
-                float a = ra[r];
-#pragma unroll
-                for (int d = 8; d > 0; d >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
-                s = block_scale<TYPE, POW2>(a);
-            }
+            const float inv = ROWS ? __shfl_sync(0xffffffffu, s.inv, (lane & 16) + r * (16 / R)) : s.inv;
             const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
             uint32_t q[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                q[j] = encode2<TYPE>(__fmul_rn(bf16_lo(w[j]), s.inv), __fmul_rn(bf16_hi(w[j]), s.inv));
+            for (int j = 0; j < 4; ++j) q[j] = encode2<TYPE>(__fmul_rn(bf16_lo(w[j]), inv), __fmul_rn(bf16_hi(w[j]), inv));
             const int32_t m = m0 + r;
             if (col_ok && m < p.M)
                 *reinterpret_cast<uint2 *>(p.Q + mat + static_cast<int64_t>(m) * p.K + col) =
                     make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
-            if (ROWS && c == 0 && m < p.M) p.SF[static_cast<int64_t>(kblock) * p.M + m] = s.s;
         }
     }
 
@@ -208,20 +236,32 @@ fp8_quantize_kernel(const QuantParams p)
                     ca[2 * j + 1] = fmaxf(ca[2 * j + 1], fabsf(bf16_hi(w[j])));
                 }
             }
+            // the warp's two row groups: each lane keeps four of the columns
+            float4 half;
+            {
+                const bool up = (lane & 16) != 0;
+                float *h = &half.x;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                ca[j] = fmaxf(ca[j], __shfl_xor_sync(0xffffffffu, ca[j], 16));
-                if (lane < 16) s_amax[warp * 128 + 8 * c + j] = ca[j];
+                for (int j = 0; j < 4; ++j)
+                    h[j] = fmaxf(up ? ca[j + 4] : ca[j], __shfl_xor_sync(0xffffffffu, up ? ca[j] : ca[j + 4], 16));
+                reinterpret_cast<float4 *>(s_amax + warp * 128)[2 * c + (up ? 1 : 0)] = half;
+            }
+            __syncthreads();
+            // one column per thread of the first half: its scale, its factor for the others
+            if (tid < 128) {
+                float a = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) a = fmaxf(a, s_amax[w * 128 + tid]);
+                const Scale s = block_scale<TYPE, POW2>(a);
+                s_amax[tid] = s.inv;            // (only this thread read it: warp 0's row of the table)
+                const int32_t k = kblock * 128 + tid;
+                if (k < p.K) p.SF_t[static_cast<int64_t>(mtile) * p.K + k] = s.s;
             }
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float a = 0.0f;
-#pragma unroll
-                for (int w = 0; w < 8; ++w) a = fmaxf(a, s_amax[w * 128 + 8 * c + j]);
-                const Scale s = block_scale<TYPE, POW2>(a);
-                inv[j] = s.inv;
-                if (i == 0 && col_ok) p.SF_t[static_cast<int64_t>(mtile) * p.K + col + j] = s.s;
+            for (int j = 0; j < 2; ++j) {
+                const float4 f = reinterpret_cast<const float4 *>(s_amax)[2 * c + j];
+                inv[4 * j] = f.x; inv[4 * j + 1] = f.y; inv[4 * j + 2] = f.z; inv[4 * j + 3] = f.w;
             }
         }
         // codes of column 8 c + j, rows R i .. R i + 7, as eight bytes of the
@@ -267,7 +307,7 @@ template <int TYPE, bool POW2>
 int launch_what(const QuantParams &p, int what, int64_t groups, cudaStream_t s)
 {
     switch (what) {
-    case kRows: return launch<TYPE, POW2, kRows, 8>(p, groups, s);
+    case kRows: return launch<TYPE, POW2, kRows, 2>(p, groups, s);
     case kCols: return launch<TYPE, POW2, kCols, 8>(p, groups, s);
     case kRows | kCols: return launch<TYPE, POW2, kRows | kCols, 8>(p, groups, s);
     case kBlock: return launch<TYPE, POW2, kBlock, 8>(p, groups, s);

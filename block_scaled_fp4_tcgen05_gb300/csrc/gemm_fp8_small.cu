@@ -44,7 +44,7 @@ int read_clear_status_gemm_fp8_small(cudaStream_t s, uint32_t *out)
 namespace {
 
 constexpr int kMaxSplits = 8;       // CTAs of a cluster (the portable limit)
-constexpr int kBatch = 4;           // K blocks per hand-over of scales
+constexpr int kBatch = 8;           // K blocks per hand-over of scales
 
 template <int NT>
 struct SmallCfg {
@@ -158,9 +158,10 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         const uint64_t t_desc0 = smem_desc(smem_u32(smem) + C::W_BYTES, 16, 1024, kSwizzle128B);
         const uint32_t idesc = idesc_f8(128, NT, p.b_type, p.a_type);
         uint32_t s = 0, phase = 0, slot = 0, acc_phase = 1;
-        bool ok = true;
+        bool ok = true, loaded = false;      // loaded: the next stage is known to have landed
         for (int32_t j = 0; j < nkb; ++j) {
-            if (!mbar_wait_warp(smem_u32(&full[s]), phase) || !mbar_wait_warp(smem_u32(&acc_empty[slot]), acc_phase)) {
+            if ((!loaded && !mbar_wait_warp(smem_u32(&full[s]), phase)) ||
+                !mbar_wait_warp(smem_u32(&acc_empty[slot]), acc_phase)) {
                 ok = false;
                 break;
             }
@@ -178,6 +179,7 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             slot ^= 1;
             if (slot == 0) acc_phase ^= 1;
             if (++s == C::STAGES) { s = 0; phase ^= 1; }
+            loaded = __all_sync(0xffffffffu, mbar_test(smem_u32(&full[s]), phase));
         }
         if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
     } else if (warp == 2) {
@@ -216,37 +218,45 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         for (int i = 0; i < C::COLS; ++i) acc[i] = 0.0f;
         uint32_t slot = 0, phase = 0, b = 0, sc_phase = 0;
         int u = 0;
-        bool ok = true;
+        bool ok = true, ready = false;      // ready: the next slot's sum is known to be complete
         for (int32_t j = 0; j < nkb; ++j) {
             if (u == 0 && !mbar_wait_warp(smem_u32(&sc_full[b]), sc_phase)) { ok = false; break; }
             const float *sc = reinterpret_cast<const float *>(smem + C::OFF_SCALE) + (b * kBatch + u) * C::SCALES;
-            const float row = sc[NT + (PER_ROW ? quad * 32 + lane : 0)];
-            if (!mbar_wait_warp(smem_u32(&acc_full[slot]), phase)) { ok = false; break; }
+            if (!ready && !mbar_wait_warp(smem_u32(&acc_full[slot]), phase)) { ok = false; break; }
             tc_fence_after();
+            uint32_t v[C::COLS / kLd][kLd];
 #pragma unroll
             for (int c = 0; c < C::COLS / kLd; ++c) {
-                uint32_t v[kLd];
-                if constexpr (kLd == 16) tmem_ld_32x32b_x16(taddr + slot * NT, v);
-                else tmem_ld_32x32b_x32(taddr + slot * NT + c * 32, v);
-                tmem_ld_wait();
-                tmem_regs_after_wait(v);
-                if (c == C::COLS / kLd - 1) {
+                if constexpr (kLd == 16) tmem_ld_32x32b_x16(taddr + slot * NT, v[c]);
+                else tmem_ld_32x32b_x32(taddr + slot * NT + c * 32, v[c]);
+            }
+            const float row = sc[NT + (PER_ROW ? quad * 32 + lane : 0)];
+            bool done = false;
+#pragma unroll
+            for (int c = 0; c < C::COLS / kLd; ++c) {
+                // the products of the scales (the first ones while the loads are under way)
+                float f[kLd];
+#pragma unroll
+                for (int i = 0; i < kLd; i += 4) {
+                    const float4 q = *reinterpret_cast<const float4 *>(sc + c0 + c * kLd + i);
+                    unpack_f32x2(mul_f32x2(pack_f32x2(q.x, q.y), pack_f32x2(row, row)), f[i], f[i + 1]);
+                    unpack_f32x2(mul_f32x2(pack_f32x2(q.z, q.w), pack_f32x2(row, row)), f[i + 2], f[i + 3]);
+                }
+                if (c == 0) {
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int d = 0; d < C::COLS / kLd; ++d) tmem_regs_after_wait(v[d]);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&acc_empty[slot]));
+                    slot ^= 1;
+                    if (slot == 0) phase ^= 1;
+                    done = mbar_test(smem_u32(&acc_full[slot]), phase);
                 }
 #pragma unroll
-                for (int i = 0; i < kLd; i += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(sc + c0 + c * kLd + i);
-                    float *a = acc + c * kLd + i;
-                    a[0] = fmaf(__fmul_rn(f.x, row), __uint_as_float(v[i]), a[0]);
-                    a[1] = fmaf(__fmul_rn(f.y, row), __uint_as_float(v[i + 1]), a[1]);
-                    a[2] = fmaf(__fmul_rn(f.z, row), __uint_as_float(v[i + 2]), a[2]);
-                    a[3] = fmaf(__fmul_rn(f.w, row), __uint_as_float(v[i + 3]), a[3]);
-                }
+                for (int i = 0; i < kLd; ++i) acc[c * kLd + i] = fmaf(f[i], __uint_as_float(v[c][i]), acc[c * kLd + i]);
             }
-            slot ^= 1;
-            if (slot == 0) phase ^= 1;
+            ready = __all_sync(0xffffffffu, done);
             if (++u == kBatch || j == nkb - 1) {
                 u = 0;
                 __syncwarp();

@@ -90,6 +90,8 @@ class Qfp4Error(RuntimeError):
 def load() -> ctypes.CDLL:
     """Open libqfp4.so (built by build.py / __graft_entry__.build())."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -137,6 +139,12 @@ def status_string(status: int) -> str:
     return load().qfp4_status_string(int(status)).decode()
 
 
+# The current stream's handle, without building a torch Stream around it
+# (0.1 us instead of 3).
+_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 def _p(t) -> int | None:
     if t is None:
         return None
@@ -147,7 +155,7 @@ def _p(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -337,18 +345,19 @@ def gemm_swiglu_quantize_grouped(fmt, row_offsets, total_rows, I, K, A, A_sf, W,
                                                     _p(Q_out), _p(SF_out), _stream(stream)))
 
 
-def _dense(*tensors) -> None:
-    """The C ABI takes whole row-major matrices on the GPU: a strided view or a
-    host tensor would be read as something else."""
-    for t in tensors:
-        if t is not None and not isinstance(t, int) and not (t.is_cuda and t.is_contiguous()):
-            raise ValueError("qfp4: tensors must be contiguous and on the GPU")
+def _at(t, dtype=None):
+    """Address of a whole row-major matrix on the GPU (a strided view or a host
+    tensor would be read as something else), of the given type."""
+    if t is None or isinstance(t, int):
+        return t
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError("qfp4: tensors must be contiguous and on the GPU")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"qfp4: expected {dtype}, got {t.dtype}")
+    return t.data_ptr()
 
 
-def _typed(dtype, *tensors) -> None:
-    for t in tensors:
-        if t is not None and not isinstance(t, int) and t.dtype != dtype:
-            raise ValueError(f"qfp4: expected {dtype}, got {t.dtype}")
+_F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 
 
 def fp8_quantize(type, X, Q=None, SF=None, Q_t=None, SF_t=None, scale=SCALE_FP32, row_index=None, stream=None) -> None:
@@ -356,92 +365,69 @@ def fp8_quantize(type, X, Q=None, SF=None, Q_t=None, SF_t=None, scale=SCALE_FP32
     (Q [M, K], SF [ceil(K/128), M]) and / or along the columns, transposed
     (Q_t [K, ceil16(M)], SF_t [ceil(M/128), K]).  row_index (int32 [M]) gathers
     rows of X."""
-    _dense(X, Q, SF, Q_t, SF_t, row_index)
-    _typed(torch.bfloat16, X)
-    _typed(torch.float32, SF, SF_t)
-    _typed(torch.int32, row_index)
     rows, K = X.shape
     M = rows if row_index is None else row_index.numel()
     _check("qfp4_fp8_quantize",
-           load().qfp4_fp8_quantize(type, scale, _p(X), rows, _p(row_index), M, K, _p(Q), _p(SF), _p(Q_t), _p(SF_t),
-                                    _stream(stream)))
+           load().qfp4_fp8_quantize(type, scale, _at(X, _BF16), rows, _at(row_index, _I32), M, K, _at(Q), _at(SF, _F32),
+                                    _at(Q_t), _at(SF_t, _F32), _stream(stream)))
 
 
 def fp8_quantize_weight(type, W, Q, SF, Q_t=None, SF_t=None, scale=SCALE_FP32, stream=None) -> None:
     """Weights W [N, K] or [groups, N, K] -> codes with a scale per 128 x 128
     block, and optionally their transpose (Q_t [.., K, ceil16(N)])."""
-    _dense(W, Q, SF, Q_t, SF_t)
-    _typed(torch.bfloat16, W)
-    _typed(torch.float32, SF, SF_t)
     groups, (N, K) = (1 if W.dim() == 2 else W.shape[0]), W.shape[-2:]
     _check("qfp4_fp8_quantize_weight",
-           load().qfp4_fp8_quantize_weight(type, scale, groups, _p(W), N, K, _p(Q), _p(SF), _p(Q_t), _p(SF_t),
-                                           _stream(stream)))
+           load().qfp4_fp8_quantize_weight(type, scale, groups, _at(W, _BF16), N, K, _at(Q), _at(SF, _F32), _at(Q_t),
+                                           _at(SF_t, _F32), _stream(stream)))
 
 
 def gemm_nt_fp8(a_type, b_type, M, N, K, A, A_sf, B, B_sf, D, b_rows=128, out=OUT_BF16, accumulate=False,
                 stream=None) -> None:
     """D = A B^T with a scale per 128 elements of K: A_sf [ceil(K/128), M], B_sf
     per 128 x 128 block (b_rows=128) or [ceil(K/128), N] (b_rows=1)."""
-    _dense(A, A_sf, B, B_sf, D)
-    _typed(torch.float32, A_sf, B_sf)
-    _typed(torch.float32 if out == OUT_FP32 else torch.bfloat16, D)
     _check("qfp4_gemm_nt_fp8",
-           load().qfp4_gemm_nt_fp8(a_type, b_type, M, N, K, _p(A), _p(A_sf), _p(B), _p(B_sf), b_rows, out,
-                                   1 if accumulate else 0, _p(D), _stream(stream)))
+           load().qfp4_gemm_nt_fp8(a_type, b_type, M, N, K, _at(A), _at(A_sf, _F32), _at(B), _at(B_sf, _F32), b_rows,
+                                   out, 1 if accumulate else 0, _at(D, _F32 if out == OUT_FP32 else _BF16),
+                                   _stream(stream)))
 
 
 def gemm_nt_fp8_grouped(a_type, b_type, row_offsets, total_rows, max_group_rows, N, K, A, A_sf, B, B_sf, D,
                         out=OUT_BF16, stream=None) -> None:
     """One product per expert: rows [row_offsets[e], row_offsets[e+1]) with B[e]."""
-    _dense(row_offsets, A, A_sf, B, B_sf, D)
-    _typed(torch.int32, row_offsets)
-    _typed(torch.float32, A_sf, B_sf)
-    _typed(torch.float32 if out == OUT_FP32 else torch.bfloat16, D)
     groups = row_offsets.numel() - 1
     _check("qfp4_gemm_nt_fp8_grouped",
-           load().qfp4_gemm_nt_fp8_grouped(a_type, b_type, groups, _p(row_offsets), total_rows, max_group_rows, N, K,
-                                           _p(A), _p(A_sf), _p(B), _p(B_sf), out, _p(D), _stream(stream)))
+           load().qfp4_gemm_nt_fp8_grouped(a_type, b_type, groups, _at(row_offsets, _I32), total_rows, max_group_rows,
+                                           N, K, _at(A), _at(A_sf, _F32), _at(B), _at(B_sf, _F32), out,
+                                           _at(D, _F32 if out == OUT_FP32 else _BF16), _stream(stream)))
 
 
 def moe_route_workspace_bytes(T: int, E: int, topk: int) -> int:
     return int(load().qfp4_moe_route_workspace_bytes(T, E, topk))
 
 
-def _logits_type(logits) -> int:
-    if logits.dtype == torch.float32:
-        return OUT_FP32
-    _typed(torch.bfloat16, logits)
-    return OUT_BF16
+def _logits(t):
+    """(type, address)"""
+    return (OUT_FP32, _at(t, _F32)) if t.dtype == _F32 else (OUT_BF16, _at(t, _BF16))
 
 
 def moe_route(logits, topk, ids, gates, counts, row_offsets, dest, src, n_valid, mean_prob, loss, workspace,
               valid=None, renorm=True, stream=None) -> None:
     """Top-k experts of each token, gates, per-expert counts and row order, and
     the balance loss; valid is uint8 [T] or None."""
-    _dense(logits, ids, gates, counts, row_offsets, dest, src, n_valid, mean_prob, loss, workspace, valid)
-    _typed(torch.int32, ids, counts, row_offsets, dest, src, n_valid)
-    _typed(torch.float32, gates, mean_prob, loss)
-    _typed(torch.uint8, valid)
     T, E = logits.shape
     _check("qfp4_moe_route",
-           load().qfp4_moe_route(_logits_type(logits), _p(logits), T, E, topk, _p(valid), 1 if renorm else 0, _p(ids),
-                                 _p(gates), _p(counts), _p(row_offsets), _p(dest), _p(src), _p(n_valid),
-                                 _p(mean_prob), _p(loss), _p(workspace),
-                                 workspace.numel() * workspace.element_size(), _stream(stream)))
+           load().qfp4_moe_route(*_logits(logits), T, E, topk, _at(valid, _U8), 1 if renorm else 0, _at(ids, _I32),
+                                 _at(gates, _F32), _at(counts, _I32), _at(row_offsets, _I32), _at(dest, _I32),
+                                 _at(src, _I32), _at(n_valid, _I32), _at(mean_prob, _F32), _at(loss, _F32),
+                                 _at(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def moe_route_backward(logits, ids, counts, n_valid, dgates, dloss, dlogits, valid=None, renorm=True,
                        stream=None) -> None:
     """dlogits of (gates . dgates + dloss * loss), choices and counts held fixed;
     dgates and dloss may be None."""
-    _dense(logits, ids, counts, n_valid, dgates, dloss, dlogits, valid)
-    _typed(torch.int32, ids, counts, n_valid)
-    _typed(torch.float32, dgates, dloss)
-    _typed(torch.uint8, valid)
-    _typed(logits.dtype, dlogits)
     T, E = logits.shape
     _check("qfp4_moe_route_backward",
-           load().qfp4_moe_route_backward(_logits_type(logits), _p(logits), T, E, ids.shape[1], _p(valid),
-                                          1 if renorm else 0, _p(ids), _p(counts), _p(n_valid), _p(dgates),
-                                          _p(dloss), _p(dlogits), _stream(stream)))
+           load().qfp4_moe_route_backward(*_logits(logits), T, E, ids.shape[1], _at(valid, _U8), 1 if renorm else 0,
+                                          _at(ids, _I32), _at(counts, _I32), _at(n_valid, _I32), _at(dgates, _F32),
+                                          _at(dloss, _F32), _at(dlogits, logits.dtype), _stream(stream)))
