@@ -12,7 +12,7 @@
 // CTA r adds up tokens r, r + S, ... over the S CTAs in order (the results
 // repeat bit for bit, and no scratch in global memory is needed).
 //
-// Warps: 0 TMA producer, 1 tensor-memory owner and MMA issuer, 2 scales, 4..
+// Warps: 0 and 3 TMA producers, 1 tensor-memory owner and MMA issuer, 2 scales, 4..
 // epilogue (four, or eight for NT = 128, each 32 rows of B).
 #include <cstdint>
 #include <cuda.h>
@@ -137,17 +137,22 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     pdl_wait();
     pdl_launch_dependents();
 
-    if (warp == 0) {
-        // ------------------------------------------------ TMA producer
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------ B (warp 0) and A (warp 3) TMA producers: the copy
+        // engine takes one thread's requests one after another
         if (lane == 0) {
+            const bool is_w = warp == 0;
             uint32_t s = 0, phase = 1;
             bool ok = true;
             for (int32_t j = 0; j < nkb; ++j) {
                 if (!mbar_wait(smem_u32(&empty[s]), phase)) { ok = false; break; }
                 const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(smem + s * C::STAGE);
-                mbar_arrive_expect_tx(bar, C::STAGE);
-                tma_load_2d(dst, &tmW, bar, (kb0 + j) * 128, n0);
-                tma_load_2d(dst + C::W_BYTES, &tmT, bar, (kb0 + j) * 128, m0);
+                if (is_w) {
+                    mbar_arrive_expect_tx(bar, C::STAGE);
+                    tma_load_2d(dst, &tmW, bar, (kb0 + j) * 128, n0);
+                } else {
+                    tma_load_2d(dst + C::W_BYTES, &tmT, bar, (kb0 + j) * 128, m0);
+                }
                 if (++s == C::STAGES) { s = 0; phase ^= 1; }
             }
             if (!ok) { record_timeout(); *abort_flag = 1; }

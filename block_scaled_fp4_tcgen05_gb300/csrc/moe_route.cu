@@ -9,16 +9,17 @@
 //   gates' part, g = p / sum of the chosen p: g_i (dg_i - sum_j g_j dg_j) at the
 //   chosen experts; g = p: [chosen] p_i dg_i - p_i sum_j p_j dg_j.
 //
-// Forward, two launches.  route_rows_kernel: CTA c takes a contiguous range of
-// tokens, a warp one token at a time with its logits in registers (lane l holds
-// experts l, l + 32, ...): softmax, then k rounds of a warp-wide maximum over
-// order-preserving integer keys, ties to the lowest expert; a lane adds up its
-// experts' p over the warp's tokens in registers.  The CTA's counts and its sum
-// of p go to the workspace.  route_place_kernel: each CTA adds up the counts of
-// all ranges, so it knows where each expert's rows begin and how many of them
-// come from earlier ranges, and ranks its own pairs in order; CTA 0 also writes
-// the totals and the loss.  All sums run in a fixed order: results repeat bit
-// for bit.
+// Forward, two launches (one for few tokens).  route_rows_kernel: CTA c takes a
+// contiguous range of tokens, a warp one token at a time with its logits in
+// registers (lane l holds experts l, l + 32, ...): softmax, then k rounds of
+// top-k on order-preserving integer keys.  A lane keeps the best of its own
+// keys, so a round is one warp-wide maximum, a vote for the lane that holds it
+// and that lane's next best.  A lane adds up its experts' p over the warp's
+// tokens in registers.  The CTA's counts and its sum of p go to the workspace.
+// route_place_kernel: each CTA adds up the counts of all ranges, so it knows
+// where each expert's rows begin and how many of them come from earlier
+// ranges, and ranks its own pairs in order; one more CTA writes the totals and
+// the loss.  All sums run in a fixed order: results repeat bit for bit.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -30,9 +31,10 @@ namespace {
 
 constexpr int kMaxExperts = 256;
 constexpr int kMaxTopk = 16;
-constexpr int kWarps = 16;
+constexpr int kWarps = 32;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxChunks = 304;             // two CTAs on each of 152 SMs
+constexpr int kMaxChunks = 152;             // one CTA on each SM
+constexpr int64_t kOneCta = 128;            // tokens that one CTA takes in one launch
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
 
@@ -77,10 +79,11 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// exp(l - max) of the lane's experts, and 1 / their sum over the row (0 for a
-// row with no open expert).  A NaN or +inf logit makes the sum NaN.
+// exp(l - max) of the lane's experts; returns 1 / their sum over the row (0 for
+// a row with no open expert) and the subtracted maximum.  A NaN or +inf logit
+// makes the sum NaN.
 template <int V>
-__device__ __forceinline__ float softmax_terms(const float (&l)[V], int E, int lane, float (&x)[V])
+__device__ __forceinline__ float softmax_terms(const float (&l)[V], int E, int lane, float (&x)[V], float &base)
 {
     float m = -INFINITY;
     bool nan = false;
@@ -91,7 +94,7 @@ __device__ __forceinline__ float softmax_terms(const float (&l)[V], int E, int l
     }
     m = warp_max(m);
     if (__any_sync(kFull, nan)) m = NAN;
-    const float base = m == -INFINITY ? 0.0f : m;
+    base = m == -INFINITY ? 0.0f : m;
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -102,21 +105,26 @@ __device__ __forceinline__ float softmax_terms(const float (&l)[V], int E, int l
     return sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
 }
 
+struct RouteShared {
+    int32_t counts[kMaxExperts];                    // of this range
+    int32_t start[kMaxExperts];                     // first row of each expert, all ranges
+    int32_t before[kMaxExperts];                    // rows of it that earlier ranges fill
+    int32_t total[kMaxExperts];
+    union {
+        float prob[kWarps][kMaxExperts];            // sums of p per warp
+        int32_t row[kWarps][kMaxExperts];           // counts, then next row, of each warp's pairs
+        int32_t part[2][kThreads];                  // partial sums over ranges
+        float ppart[kThreads];
+    };
+    int32_t valid;
+    int32_t rows;                                   // rows of all experts
+};
+
+// Choices, gates and counts of tokens [t0, t1), and the warps' sums of p.
 template <typename L, int V>
-__global__ void __launch_bounds__(kThreads)
-route_rows_kernel(const RouteParams p)
+__device__ __forceinline__ void route_rows(const RouteParams &p, int64_t t0, int64_t t1, RouteShared &sh)
 {
-    __shared__ int32_t s_counts[kMaxExperts];
-    __shared__ float s_prob[kWarps][kMaxExperts];
-    __shared__ int32_t s_valid;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int e = tid; e < kMaxExperts; e += kThreads) s_counts[e] = 0;
-    if (tid == 0) s_valid = 0;
-    __syncthreads();
-    pdl_wait();
-    pdl_launch_dependents();
-    const int64_t t0 = blockIdx.x * p.chunk;
-    const int64_t t1 = min(p.T, t0 + p.chunk);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float psum[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) psum[v] = 0.0f;
@@ -127,7 +135,7 @@ route_rows_kernel(const RouteParams p)
         if (!p.valid || p.valid[t] != 0) {
             ++nvalid;
             const L *row = static_cast<const L *>(p.logits) + t * p.E;
-            float l[V], x[V];
+            float l[V], x[V], base;
             uint32_t key[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -135,37 +143,46 @@ route_rows_kernel(const RouteParams p)
                 l[v] = e < p.E ? load_logit(row + e) : -INFINITY;
                 key[v] = e < p.E ? sort_key(l[v]) : 0u;
             }
-            const float inv = softmax_terms<V>(l, p.E, lane, x);
+            const float inv = softmax_terms<V>(l, p.E, lane, x, base);
 #pragma unroll
             for (int v = 0; v < V; ++v) psum[v] = __fadd_rn(psum[v], x[v] * inv);
-            float my_x = 0.0f;
-            for (int j = 0; j < p.topk; ++j) {
-                uint32_t best = key[0];
+            // the lane's best key and its place, lowest expert first
+            uint32_t best = key[0];
+            int at = 0;
+            auto find = [&]() {
+                best = key[0];
+                at = 0;
 #pragma unroll
-                for (int v = 1; v < V; ++v) best = max(best, key[v]);
-                best = __reduce_max_sync(kFull, best);
-                if (best <= kKeyNegInf) break;
-                uint32_t at = 0xFFFFFFFFu;
-#pragma unroll
-                for (int v = V - 1; v >= 0; --v)
-                    if (key[v] == best) at = lane + 32 * v;
-                at = __reduce_min_sync(kFull, at);
-                float xv = 0.0f;
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (at == lane + 32 * v) {
-                        key[v] = 0u;
-                        xv = x[v];
+                for (int v = 1; v < V; ++v)
+                    if (key[v] > best) {
+                        best = key[v];
+                        at = v;
                     }
-                xv = __shfl_sync(kFull, xv, at & 31);
-                if (lane == j) {
-                    my_id = static_cast<int32_t>(at);
-                    my_x = xv;
+            };
+            find();
+            for (int j = 0; j < p.topk; ++j) {
+                const uint32_t top = __reduce_max_sync(kFull, best);
+                if (top <= kKeyNegInf) break;
+                uint32_t who = __ballot_sync(kFull, best == top);
+                uint32_t e = lane + 32 * at;
+                if (who & (who - 1)) {          // equal keys on several lanes: the lowest expert
+                    const uint32_t low = __reduce_min_sync(kFull, best == top ? e : 0xFFFFFFFFu);
+                    who = 1u << (low & 31u);
+                }
+                const int src = __ffs(who) - 1;
+                e = __shfl_sync(kFull, e, src);
+                if (lane == j) my_id = static_cast<int32_t>(e);
+                if (lane == src) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        if (v == at) key[v] = 0u;
+                    find();
                 }
             }
+            const float my_x = my_id >= 0 ? expf(load_logit(row + my_id) - base) : 0.0f;
             const float scale = p.renorm ? warp_sum(my_x) : 0.0f;
             my_gate = my_id < 0 ? 0.0f : p.renorm ? (scale == 0.0f ? 0.0f : __fdiv_rn(my_x, scale)) : my_x * inv;
-            if (my_id >= 0) atomicAdd(&s_counts[my_id], 1);
+            if (my_id >= 0) atomicAdd(&sh.counts[my_id], 1);
         }
         if (lane < p.topk) {
             p.ids[t * p.topk + lane] = my_id;
@@ -173,65 +190,66 @@ route_rows_kernel(const RouteParams p)
         }
     }
 #pragma unroll
-    for (int v = 0; v < V; ++v) s_prob[warp][lane + 32 * v] = psum[v];
-    if (lane == 0) atomicAdd(&s_valid, nvalid);
-    __syncthreads();
-    for (int e = tid; e < p.E; e += kThreads) {
-        float s = s_prob[0][e];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) s = __fadd_rn(s, s_prob[w][e]);
-        p.ws_prob[static_cast<int64_t>(blockIdx.x) * p.E + e] = s;
-        p.ws_counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = s_counts[e];
-    }
-    if (tid == 0) p.ws_valid[blockIdx.x] = s_valid;
+    for (int v = 0; v < V; ++v) sh.prob[warp][lane + 32 * v] = psum[v];
+    if (lane == 0) atomicAdd(&sh.valid, nvalid);
 }
 
-__global__ void __launch_bounds__(kThreads)
-route_place_kernel(const RouteParams p, int chunks)
+// Sum of expert e's p over the warps of this CTA.
+__device__ __forceinline__ float route_prob(const RouteShared &sh, int e)
 {
-    __shared__ int32_t s_start[kMaxExperts];            // first row of each expert
-    __shared__ int32_t s_before[kMaxExperts];           // rows that earlier ranges put there
-    __shared__ int32_t s_total[kMaxExperts];
-    __shared__ int32_t s_warp[kWarps][kMaxExperts];     // then: next row of each warp's pairs
-    __shared__ float s_p[kMaxExperts];
-    __shared__ int32_t s_n;
+    float s = sh.prob[0][e];
+#pragma unroll 8
+    for (int w = 1; w < kWarps; ++w) s = __fadd_rn(s, sh.prob[w][e]);
+    return s;
+}
+
+// First row of each expert from the totals; by the first warp.
+__device__ __forceinline__ void route_starts(const RouteParams &p, RouteShared &sh)
+{
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x < 32) {
+        int32_t n[kMaxExperts / 32], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kMaxExperts / 32; ++i) {
+            const int e = lane * (kMaxExperts / 32) + i;
+            n[i] = mine;
+            mine += e < p.E ? sh.total[e] : 0;
+        }
+        int32_t up = mine;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(kFull, up, d);
+            if (lane >= d) up += o;
+        }
+#pragma unroll
+        for (int i = 0; i < kMaxExperts / 32; ++i) {
+            const int e = lane * (kMaxExperts / 32) + i;
+            if (e < p.E) sh.start[e] = up - mine + n[i];
+        }
+        if (lane == 31) sh.rows = up;
+    }
+}
+
+// Rows of the pairs of tokens [t0, t1): after the experts' starts and the rows
+// that earlier ranges fill, in the pairs' order.  All threads; sh.row is free.
+__device__ __forceinline__ void route_place(const RouteParams &p, int64_t t0, int64_t t1, RouteShared &sh)
+{
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int f = tid; f < kWarps * kMaxExperts; f += kThreads) s_warp[f / kMaxExperts][f % kMaxExperts] = 0;
-    pdl_wait();
-    pdl_launch_dependents();
-    for (int e = tid; e < p.E; e += kThreads) {
-        int32_t before = 0, total = 0;
-        for (int c = 0; c < chunks; ++c) {
-            const int32_t n = __ldcg(p.ws_counts + static_cast<int64_t>(c) * p.E + e);
-            if (c < static_cast<int>(blockIdx.x)) before += n;
-            total += n;
-        }
-        s_before[e] = before;
-        s_total[e] = total;
-    }
+    for (int f = tid; f < kWarps * kMaxExperts; f += kThreads) (&sh.row[0][0])[f] = 0;
     __syncthreads();
-    if (tid == 0) {
-        int32_t at = 0;
-        for (int e = 0; e < p.E; ++e) {
-            s_start[e] = at;
-            at += s_total[e];
-        }
-        s_n = at;
-    }
-    // pairs of this range, warp by warp in order
-    const int64_t f0 = min(p.T, blockIdx.x * p.chunk) * p.topk, f1 = min(p.T, (blockIdx.x + 1) * p.chunk) * p.topk;
+    const int64_t f0 = t0 * p.topk, f1 = t1 * p.topk;
     const int64_t per_warp = ((f1 - f0 + kWarps - 1) / kWarps + 31) / 32 * 32;
     const int64_t w0 = min(f1, f0 + warp * per_warp), w1 = min(f1, w0 + per_warp);
     for (int64_t f = w0 + lane; f < w1; f += 32) {
         const int32_t e = __ldcg(p.ids + f);
-        if (e >= 0) atomicAdd(&s_warp[warp][e], 1);
+        if (e >= 0) atomicAdd(&sh.row[warp][e], 1);
     }
     __syncthreads();
     for (int e = tid; e < p.E; e += kThreads) {
-        int32_t at = s_start[e] + s_before[e];
+        int32_t at = sh.start[e] + sh.before[e];
+#pragma unroll 8
         for (int w = 0; w < kWarps; ++w) {
-            const int32_t n = s_warp[w][e];
-            s_warp[w][e] = at;
+            const int32_t n = sh.row[w][e];
+            sh.row[w][e] = at;
             at += n;
         }
     }
@@ -241,46 +259,161 @@ route_place_kernel(const RouteParams p, int chunks)
         const uint32_t same = __match_any_sync(kFull, e);
         const int rank = __popc(same & ((1u << lane) - 1u));
         int32_t row = -1;
-        if (e >= 0) row = s_warp[warp][e] + rank;
+        if (e >= 0) row = sh.row[warp][e] + rank;
         __syncwarp();
-        if (e >= 0 && rank == 0) s_warp[warp][e] += __popc(same);
+        if (e >= 0 && rank == 0) sh.row[warp][e] += __popc(same);
         __syncwarp();
         if (f + lane < w1) {
             p.dest[f + lane] = row;
             if (row >= 0) p.src[row] = static_cast<int32_t>((f + lane) / p.topk);
         }
     }
+}
+
+// Totals, offsets, mean p and loss; prob = sum of expert tid's p over all tokens.
+__device__ __forceinline__ void route_totals(const RouteParams &p, RouteShared &sh, int32_t valid, float prob)
+{
+    const int tid = threadIdx.x;
+    const float n = static_cast<float>(max(valid, 1));
+    float s = 0.0f;
+    if (tid < p.E) {
+        const float mean = __fdiv_rn(prob, n);
+        p.mean_prob[tid] = mean;
+        p.counts[tid] = sh.total[tid];
+        p.row_offsets[tid] = sh.start[tid];
+        s = mean * static_cast<float>(sh.total[tid]);
+    }
+    __shared__ float part[kMaxExperts / 32];
+    if (tid < kMaxExperts) {
+        s = warp_sum(s);
+        if ((tid & 31) == 0) part[tid >> 5] = s;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        float sum = part[0];
+#pragma unroll
+        for (int w = 1; w < kMaxExperts / 32; ++w) sum = __fadd_rn(sum, part[w]);
+        p.loss[0] = sum * __fdiv_rn(static_cast<float>(p.E), static_cast<float>(p.topk) * n);
+        p.row_offsets[p.E] = sh.rows;
+        p.n_valid[0] = valid;
+    }
+}
+
+template <typename L, int V>
+__global__ void __launch_bounds__(kThreads)
+route_rows_kernel(const RouteParams p)
+{
+    __shared__ RouteShared sh;
+    const int tid = threadIdx.x;
+    if (tid < kMaxExperts) sh.counts[tid] = 0;
+    if (tid == 0) sh.valid = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t t0 = min(p.T, blockIdx.x * p.chunk), t1 = min(p.T, t0 + p.chunk);
+    route_rows<L, V>(p, t0, t1, sh);
+    __syncthreads();
+    if (tid < p.E) {
+        p.ws_prob[static_cast<int64_t>(blockIdx.x) * p.E + tid] = route_prob(sh, tid);
+        p.ws_counts[static_cast<int64_t>(blockIdx.x) * p.E + tid] = sh.counts[tid];
+    }
+    if (tid == 0) p.ws_valid[blockIdx.x] = sh.valid;
+}
+
+// CTA c < chunks places range c; the last one writes the totals.
+__global__ void __launch_bounds__(kThreads)
+route_place_kernel(const RouteParams p, int chunks)
+{
+    __shared__ RouteShared sh;
+    const int tid = threadIdx.x;
+    const bool totals = static_cast<int>(blockIdx.x) == chunks;
+    // every expert's counts are added up by `parts` threads
+    const int width = p.E <= 32 ? 32 : p.E <= 64 ? 64 : p.E <= 128 ? 128 : 256;
+    const int parts = kThreads / width, part = tid / width, e = tid % width;
+    pdl_wait();
+    pdl_launch_dependents();
+    int32_t before = 0, total = 0;
+    if (e < p.E) {
+#pragma unroll 8
+        for (int c = part; c < chunks; c += parts) {
+            const int32_t n = __ldcg(p.ws_counts + static_cast<int64_t>(c) * p.E + e);
+            if (c < static_cast<int>(blockIdx.x)) before += n;
+            total += n;
+        }
+    }
+    sh.part[0][tid] = before;
+    sh.part[1][tid] = total;
+    __syncthreads();
+    if (tid < p.E) {
+        before = total = 0;
+        for (int i = 0; i < parts; ++i) {
+            before += sh.part[0][i * width + tid];
+            total += sh.part[1][i * width + tid];
+        }
+        sh.before[tid] = before;
+        sh.total[tid] = total;
+    }
+    __syncthreads();
+    route_starts(p, sh);
+    __syncthreads();
     // rows that no pair takes
     const int64_t pairs = p.T * p.topk;
-    for (int64_t r = s_n + static_cast<int64_t>(blockIdx.x) * kThreads + tid; r < pairs;
+    for (int64_t r = sh.rows + static_cast<int64_t>(blockIdx.x) * kThreads + tid; r < pairs;
          r += static_cast<int64_t>(gridDim.x) * kThreads)
         p.src[r] = -1;
-    if (blockIdx.x != 0) return;
-    __shared__ int32_t s_valid;
-    if (tid == 0) {
+    if (!totals) {
+        const int64_t t0 = min(p.T, blockIdx.x * p.chunk);
+        route_place(p, t0, min(p.T, t0 + p.chunk), sh);
+        return;
+    }
+    float s = 0.0f;
+    if (e < p.E) {
+#pragma unroll 8
+        for (int c = part; c < chunks; c += parts) s = __fadd_rn(s, __ldcg(p.ws_prob + static_cast<int64_t>(c) * p.E + e));
+    }
+    __syncthreads();
+    sh.ppart[tid] = s;
+    if (tid < 32) {
         int32_t n = 0;
-        for (int c = 0; c < chunks; ++c) n += __ldcg(p.ws_valid + c);
-        s_valid = n;
+        for (int c = tid; c < chunks; c += 32) n += __ldcg(p.ws_valid + c);
+        n = __reduce_add_sync(kFull, n);
+        if (tid == 0) sh.valid = n;
     }
     __syncthreads();
-    const float n = static_cast<float>(max(s_valid, 1));
-    for (int e = tid; e < p.E; e += kThreads) {
-        float s = 0.0f;
-        for (int c = 0; c < chunks; ++c) s = __fadd_rn(s, __ldcg(p.ws_prob + static_cast<int64_t>(c) * p.E + e));
-        s = __fdiv_rn(s, n);
-        p.mean_prob[e] = s;
-        p.counts[e] = s_total[e];
-        p.row_offsets[e] = s_start[e];
-        s_p[e] = s * static_cast<float>(s_total[e]);
+    s = 0.0f;
+    if (tid < p.E)
+        for (int i = 0; i < parts; ++i) s = __fadd_rn(s, sh.ppart[i * width + tid]);
+    route_totals(p, sh, sh.valid, s);
+}
+
+// Few tokens: the whole of it in one CTA.
+template <typename L, int V>
+__global__ void __launch_bounds__(kThreads)
+route_one_kernel(const RouteParams p)
+{
+    __shared__ RouteShared sh;
+    const int tid = threadIdx.x;
+    if (tid < kMaxExperts) {
+        sh.counts[tid] = 0;
+        sh.before[tid] = 0;
+    }
+    if (tid == 0) sh.valid = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    route_rows<L, V>(p, 0, p.T, sh);
+    __syncthreads();
+    float prob = 0.0f;
+    if (tid < p.E) {
+        prob = route_prob(sh, tid);
+        sh.total[tid] = sh.counts[tid];
     }
     __syncthreads();
-    if (tid == 0) {
-        float sum = 0.0f;
-        for (int e = 0; e < p.E; ++e) sum = __fadd_rn(sum, s_p[e]);
-        p.loss[0] = sum * __fdiv_rn(static_cast<float>(p.E), static_cast<float>(p.topk) * n);
-        p.row_offsets[p.E] = s_n;
-        p.n_valid[0] = s_valid;
-    }
+    route_starts(p, sh);
+    __syncthreads();
+    for (int64_t r = sh.rows + tid; r < p.T * p.topk; r += kThreads) p.src[r] = -1;
+    route_place(p, 0, p.T, sh);     // (the ids it reads were written before the barriers above)
+    route_totals(p, sh, sh.valid, prob);
 }
 
 struct BackParams {
@@ -327,7 +460,8 @@ route_backward_kernel(const BackParams p)
             const int e = lane + 32 * v;
             l[v] = e < p.E ? load_logit(row + e) : -INFINITY;
         }
-        const float inv = softmax_terms<V>(l, p.E, lane, x);
+        float base;
+        const float inv = softmax_terms<V>(l, p.E, lane, x, base);
         float dot = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -376,14 +510,22 @@ route_backward_kernel(const BackParams p)
     }
 }
 
-template <typename L>
-int launch_rows(const RouteParams &p, unsigned chunks, cudaStream_t s)
+template <typename L, int V>
+int launch_route(const RouteParams &p, int chunks, cudaStream_t s)
 {
-    const dim3 g(chunks), b(kThreads);
-    if (p.E <= 32) return launch_status(launch_pdl(route_rows_kernel<L, 1>, g, b, 0, s, p));
-    if (p.E <= 64) return launch_status(launch_pdl(route_rows_kernel<L, 2>, g, b, 0, s, p));
-    if (p.E <= 128) return launch_status(launch_pdl(route_rows_kernel<L, 4>, g, b, 0, s, p));
-    return launch_status(launch_pdl(route_rows_kernel<L, 8>, g, b, 0, s, p));
+    if (p.T <= kOneCta) return launch_status(launch_pdl(route_one_kernel<L, V>, dim3(1), dim3(kThreads), 0, s, p));
+    const int rc = launch_status(launch_pdl(route_rows_kernel<L, V>, dim3(chunks), dim3(kThreads), 0, s, p));
+    if (rc != QFP4_OK) return rc;
+    return launch_status(launch_pdl(route_place_kernel, dim3(chunks + 1), dim3(kThreads), 0, s, p, chunks));
+}
+
+template <typename L>
+int launch_forward(const RouteParams &p, int chunks, cudaStream_t s)
+{
+    if (p.E <= 32) return launch_route<L, 1>(p, chunks, s);
+    if (p.E <= 64) return launch_route<L, 2>(p, chunks, s);
+    if (p.E <= 128) return launch_route<L, 4>(p, chunks, s);
+    return launch_route<L, 8>(p, chunks, s);
 }
 
 template <typename L>
@@ -442,11 +584,8 @@ extern "C" int qfp4_moe_route(int logits_type, const void *logits, int64_t T, in
     p.ws_prob = reinterpret_cast<float *>(p.ws_counts + chunks * E);
     p.ws_valid = reinterpret_cast<int32_t *>(p.ws_prob + chunks * E);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int rc = logits_type == QFP4_BF16 ? launch_rows<__nv_bfloat16>(p, static_cast<unsigned>(chunks), s)
-                                            : launch_rows<float>(p, static_cast<unsigned>(chunks), s);
-    if (rc != QFP4_OK) return rc;
-    return launch_status(launch_pdl(route_place_kernel, dim3(static_cast<unsigned>(chunks)), dim3(kThreads), 0, s, p,
-                                    static_cast<int>(chunks)));
+    return logits_type == QFP4_BF16 ? launch_forward<__nv_bfloat16>(p, static_cast<int>(chunks), s)
+                                    : launch_forward<float>(p, static_cast<int>(chunks), s);
 }
 
 extern "C" int qfp4_moe_route_backward(int logits_type, const void *logits, int64_t T, int64_t E, int64_t topk,
@@ -465,7 +604,7 @@ extern "C" int qfp4_moe_route_backward(int logits_type, const void *logits, int6
     const BackParams p{logits, valid, T, static_cast<int32_t>(E), static_cast<int32_t>(topk), renorm ? 1 : 0,
                        ids, counts, n_valid, dgates, dloss, dlogits};
     const int64_t want = (T + kWarps - 1) / kWarps;
-    const unsigned ctas = static_cast<unsigned>(want < 4 * 152 ? want : 4 * 152);
+    const unsigned ctas = static_cast<unsigned>(want < 2 * 152 ? want : 2 * 152);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return logits_type == QFP4_BF16 ? launch_back<__nv_bfloat16>(p, ctas, s) : launch_back<float>(p, ctas, s);
 }
