@@ -91,13 +91,20 @@ __device__ __forceinline__ Scale block_scale(float amax)
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 enum { kRows = 1, kCols = 2, kBlock = 4 };
 
 // R rows per thread: the tile is 16 R rows x 128 columns.  Thread 16 i + c
 // holds rows R i .. R i + R - 1 and columns 8 c .. 8 c + 7 of the tile.
 // WHAT: kRows and / or kCols, or kBlock with or without kCols (R = 8).
 template <int TYPE, bool POW2, int WHAT, int R>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, R == 8 ? 3 : 6)
 fp8_quantize_kernel(const QuantParams p)
 {
     constexpr bool ROWS = (WHAT & kRows) != 0, COLS = (WHAT & kCols) != 0, BLOCK = (WHAT & kBlock) != 0;
@@ -139,14 +146,20 @@ fp8_quantize_kernel(const QuantParams p)
         if (ok) x[r] = ld_nc_v4(p.X + (mat + row * p.K + col) / 8);
     }
 
-    float ra[R];            // amax of this thread's part of each row
+    // amax of this thread's part of each row and, two columns per word, of each
+    // column; BF16 maxima are exact (a NaN gives way to the other operand)
+    float ra[R];
+    uint32_t cw[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
-        float a = 0.0f;
+        uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a = fmaxf(a, fmaxf(fabsf(bf16_lo(w[j])), fabsf(bf16_hi(w[j]))));
-        ra[r] = a;
+        for (int j = 0; j < 4; ++j) {
+            w[j] &= 0x7FFF7FFFu;
+            if (COLS && !BLOCK) cw[j] = max_bf16x2(cw[j], w[j]);
+        }
+        const uint32_t a = max_bf16x2(max_bf16x2(w[0], w[1]), max_bf16x2(w[2], w[3]));
+        ra[r] = fmaxf(fmaxf(bf16_lo(a), bf16_hi(a)), 0.0f);
     }
 
     Scale block{};
@@ -226,15 +239,9 @@ fp8_quantize_kernel(const QuantParams p)
         } else {
             float ca[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) ca[j] = 0.0f;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const uint32_t w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    ca[2 * j] = fmaxf(ca[2 * j], fabsf(bf16_lo(w[j])));
-                    ca[2 * j + 1] = fmaxf(ca[2 * j + 1], fabsf(bf16_hi(w[j])));
-                }
+            for (int j = 0; j < 4; ++j) {
+                ca[2 * j] = bf16_lo(cw[j]);
+                ca[2 * j + 1] = bf16_hi(cw[j]);
             }
             // the warp's two row groups: each lane keeps four of the columns
             float4 half;

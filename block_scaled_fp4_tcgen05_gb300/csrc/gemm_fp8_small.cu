@@ -2,18 +2,21 @@
 // tokens, short prompts), where 256 x 256 tiles would leave most SMs idle and
 // the weights' bytes bound the time.
 //
-// Swap AB: 128 rows of B take the MMA's M slot and up to NT rows of A its N
-// slot, so a CTA (tcgen05 cta_group::1) computes D^T for one 128 x NT tile.  K
-// is split over the S CTAs of a cluster, each streaming its own K blocks (16 KB
-// of B and NT x 128 bytes of A per block) through a ring; as in gemm_fp8.cu the
-// block sums leave tensor memory (two slots of NT columns) for registers, here
-// with a row scale per thread (B's) and a column scale per token (A's).  At the
-// end every CTA leaves its sums in its shared memory, the cluster meets, and
-// CTA r adds up tokens r, r + S, ... over the S CTAs in order (the results
-// repeat bit for bit, and no scratch in global memory is needed).
+// A CTA (tcgen05 cta_group::1) takes one tile.  Up to 64 rows of A (NT): swap
+// AB, 128 rows of B in the MMA's M slot and the tokens in its N slot, D^T.
+// More: 128 rows of A in the M slot and 128 of B in the N slot; a thread's
+// block sums then share one scale, where the swapped form needs one per token
+// from shared memory, whose bandwidth the wider MMAs use up (128 tokens x
+// 14336 x 4096: 1500 cycles per K block swapped, twice the streaming time).
+// K is split over the S CTAs of a cluster, each streaming its own K blocks
+// through a ring; as in gemm_fp8.cu the block sums leave tensor memory (two
+// slots) for registers.  At the end every CTA leaves its sums in its shared
+// memory, the cluster meets, and CTA r adds up tokens r, r + S, ... over the S
+// CTAs in order (the results repeat bit for bit, and no scratch in global
+// memory is needed).
 //
-// Warps: 0 and 3 TMA producers, 1 tensor-memory owner and MMA issuer, 2 scales, 4..
-// epilogue (four, or eight for NT = 128, each 32 rows of B).
+// Warps: 0 and 3 TMA producers, 1 tensor-memory owner and MMA issuer, 2 scales,
+// 4.. epilogue (four of all columns, or sixteen of 32 each).
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -48,14 +51,16 @@ constexpr int kBatch = 8;           // K blocks per hand-over of scales
 
 template <int NT>
 struct SmallCfg {
-    static constexpr int EPI = NT == 128 ? 8 : 4;               // epilogue warps
+    static constexpr bool SWAP = NT < 128;                      // rows of B in the MMA's M slot
+    static constexpr int GROUPS = SWAP ? 1 : NT / 32;           // column groups of the epilogue
+    static constexpr int EPI = 4 * GROUPS;                      // epilogue warps
     static constexpr int THREADS = 128 + 32 * EPI;
-    static constexpr int COLS = NT == 128 ? 64 : NT;            // token columns per epilogue warp
-    static constexpr int CTAS = NT == 128 ? 1 : 2;              // resident CTAs per SM that the ring is sized for
-    static constexpr int W_BYTES = 128 * 128;
-    static constexpr int STAGE = W_BYTES + NT * 128;
-    static constexpr int STAGES = NT == 128 ? 5 : NT == 64 ? 4 : 5;
-    static constexpr int SCALES = NT + 128;                     // floats per K block: tokens, then rows of B
+    static constexpr int COLS = NT / GROUPS;                    // columns per epilogue warp
+    static constexpr int CTAS = SWAP ? 2 : 1;                   // resident CTAs per SM that the ring is sized for
+    static constexpr int M_BYTES = 128 * 128;                   // the M slot's 128 rows x 128 elements of K
+    static constexpr int STAGE = M_BYTES + NT * 128;
+    static constexpr int STAGES = NT == 64 ? 4 : 5;
+    static constexpr int SCALES = 128 + NT;                     // floats per K block: the M slot's rows, then the N slot's
     static constexpr int OFF_SCALE = STAGES * STAGE;
     static constexpr int OFF_BAR = OFF_SCALE + 2 * kBatch * SCALES * 4;
     static constexpr int NBAR = 2 * STAGES + 4 + 4;             // full, empty; acc_full, acc_empty [2]; sc_full, sc_empty [2]
@@ -81,9 +86,10 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr)
 }
 
 // PER_ROW: B has one scale per row (b_rows = 1), else one per 128 rows.
+// tmM, tmN: maps of the operands in the MMA's M and N slots.
 template <int NT, bool PER_ROW>
 __global__ void __launch_bounds__(SmallCfg<NT>::THREADS, SmallCfg<NT>::CTAS)
-gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmT,
+gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_constant__ CUtensorMap tmN,
                       const Fp8Params p, const int splits)
 {
     using C = SmallCfg<NT>;
@@ -123,8 +129,8 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
-        prefetch_tensormap(&tmW);
-        prefetch_tensormap(&tmT);
+        prefetch_tensormap(&tmM);
+        prefetch_tensormap(&tmN);
     }
     if (warp == 1) {
         tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
@@ -138,20 +144,21 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     pdl_launch_dependents();
 
     if (warp == 0 || warp == 3) {
-        // ------------------------------------------------ B (warp 0) and A (warp 3) TMA producers: the copy
-        // engine takes one thread's requests one after another
+        // ------------------------------------------------ TMA producers of the M slot's (warp 0) and the N
+        // slot's (warp 3) operand: the copy engine takes one thread's requests one after another
         if (lane == 0) {
-            const bool is_w = warp == 0;
+            const bool is_m = warp == 0;
+            const int32_t row = is_m == C::SWAP ? n0 : m0;
             uint32_t s = 0, phase = 1;
             bool ok = true;
             for (int32_t j = 0; j < nkb; ++j) {
                 if (!mbar_wait(smem_u32(&empty[s]), phase)) { ok = false; break; }
                 const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(smem + s * C::STAGE);
-                if (is_w) {
+                if (is_m) {
                     mbar_arrive_expect_tx(bar, C::STAGE);
-                    tma_load_2d(dst, &tmW, bar, (kb0 + j) * 128, n0);
+                    tma_load_2d(dst, &tmM, bar, (kb0 + j) * 128, row);
                 } else {
-                    tma_load_2d(dst + C::W_BYTES, &tmT, bar, (kb0 + j) * 128, m0);
+                    tma_load_2d(dst + C::M_BYTES, &tmN, bar, (kb0 + j) * 128, row);
                 }
                 if (++s == C::STAGES) { s = 0; phase ^= 1; }
             }
@@ -159,9 +166,9 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         }
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
-        const uint64_t w_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-        const uint64_t t_desc0 = smem_desc(smem_u32(smem) + C::W_BYTES, 16, 1024, kSwizzle128B);
-        const uint32_t idesc = idesc_f8(128, NT, p.b_type, p.a_type);
+        const uint64_t m_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+        const uint64_t n_desc0 = smem_desc(smem_u32(smem) + C::M_BYTES, 16, 1024, kSwizzle128B);
+        const uint32_t idesc = C::SWAP ? idesc_f8(128, NT, p.b_type, p.a_type) : idesc_f8(128, NT, p.a_type, p.b_type);
         uint32_t s = 0, phase = 0, slot = 0, acc_phase = 1;
         bool ok = true, loaded = false;      // loaded: the next stage is known to have landed
         for (int32_t j = 0; j < nkb; ++j) {
@@ -172,11 +179,11 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             }
             tc_fence_after();
             if (elect_one_sync()) {
-                const uint64_t wd = w_desc0 + s * static_cast<uint64_t>(C::STAGE >> 4);
-                const uint64_t td = t_desc0 + s * static_cast<uint64_t>(C::STAGE >> 4);
+                const uint64_t md = m_desc0 + s * static_cast<uint64_t>(C::STAGE >> 4);
+                const uint64_t nd = n_desc0 + s * static_cast<uint64_t>(C::STAGE >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    tc_mma_f8(tmem_base + slot * NT, wd + 2 * kk, td + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+                    tc_mma_f8(tmem_base + slot * NT, md + 2 * kk, nd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
                 tc_commit(smem_u32(&acc_full[slot]));
                 tc_commit(smem_u32(&empty[s]));
             }
@@ -188,7 +195,10 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         }
         if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
     } else if (warp == 2) {
-        // ------------------------------------------------ scales, kBatch K blocks at a time
+        // ------------------------------------------------ scales, kBatch K blocks at a time: A's rows and B's
+        // rows (or B's one block) where the slot that holds them expects its own
+        constexpr int kAt = C::SWAP ? 512 : 0, kBt = C::SWAP ? 0 : 512;      // byte offsets in a K block's scales
+        constexpr int kArows = C::SWAP ? NT : 128, kBrows = C::SWAP ? 128 : NT;
         uint32_t b = 0, phase = 1;
         bool ok = true;
         for (int32_t j0 = 0; j0 < nkb; j0 += kBatch) {
@@ -198,14 +208,15 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 const int64_t kb = kb0 + j0 + u;
                 const uint32_t dst = dst0 + u * (C::SCALES * 4) + lane * 4;
 #pragma unroll
-                for (int i = 0; i < (NT + 31) / 32; ++i)
-                    if (32 * i + lane < NT) cp_async4(dst + 128 * i, p.A_sf + kb * p.M + min(m0 + lane + 32 * i, p.M - 1));
+                for (int i = 0; i < (kArows + 31) / 32; ++i)
+                    if (32 * i + lane < kArows)
+                        cp_async4(dst + kAt + 128 * i, p.A_sf + kb * p.M + min(m0 + lane + 32 * i, p.M - 1));
                 if (PER_ROW) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        cp_async4(dst + NT * 4 + 128 * i, p.B_sf + kb * p.N + min(n0 + lane + 32 * i, p.N - 1));
+                    for (int i = 0; i < kBrows / 32; ++i)
+                        cp_async4(dst + kBt + 128 * i, p.B_sf + kb * p.N + min(n0 + lane + 32 * i, p.N - 1));
                 } else if (lane == 0) {
-                    cp_async4(dst + NT * 4, p.B_sf + static_cast<int64_t>(n0 / 128) * kblocks + kb);
+                    cp_async4(dst + kBt, p.B_sf + static_cast<int64_t>(n0 / 128) * kblocks + kb);
                 }
             }
             cp_async_arrive(smem_u32(&sc_full[b]));
@@ -214,10 +225,11 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
         }
         if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
     } else if (warp >= 4) {
-        // ------------------------------------------------ epilogue: 32 rows of B x COLS tokens per warp
+        // ------------------------------------------------ epilogue: 32 rows of the M slot x COLS columns per warp
         const int quad = warp & 3, c0 = ((warp - 4) >> 2) * C::COLS;
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c0;
-        constexpr int kLd = C::COLS < 32 ? 16 : 32;      // columns per load
+        constexpr int kLd = C::COLS < 32 ? 16 : 32;             // columns per load
+        constexpr bool kColumns = C::SWAP || PER_ROW;           // the N slot has a scale per column
         float acc[C::COLS];
 #pragma unroll
         for (int i = 0; i < C::COLS; ++i) acc[i] = 0.0f;
@@ -235,7 +247,8 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 if constexpr (kLd == 16) tmem_ld_32x32b_x16(taddr + slot * NT, v[c]);
                 else tmem_ld_32x32b_x32(taddr + slot * NT + c * 32, v[c]);
             }
-            const float row = sc[NT + (PER_ROW ? quad * 32 + lane : 0)];
+            float row = sc[C::SWAP && !PER_ROW ? 0 : quad * 32 + lane];
+            if (!kColumns) row = row * sc[128];
             bool done = false;
 #pragma unroll
             for (int c = 0; c < C::COLS / kLd; ++c) {
@@ -243,9 +256,12 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
                 float f[kLd];
 #pragma unroll
                 for (int i = 0; i < kLd; i += 4) {
-                    const float4 q = *reinterpret_cast<const float4 *>(sc + c0 + c * kLd + i);
-                    unpack_f32x2(mul_f32x2(pack_f32x2(q.x, q.y), pack_f32x2(row, row)), f[i], f[i + 1]);
-                    unpack_f32x2(mul_f32x2(pack_f32x2(q.z, q.w), pack_f32x2(row, row)), f[i + 2], f[i + 3]);
+                    f[i] = f[i + 1] = f[i + 2] = f[i + 3] = row;
+                    if (kColumns) {
+                        const float4 q = *reinterpret_cast<const float4 *>(sc + 128 + c0 + c * kLd + i);
+                        unpack_f32x2(mul_f32x2(pack_f32x2(q.x, q.y), pack_f32x2(row, row)), f[i], f[i + 1]);
+                        unpack_f32x2(mul_f32x2(pack_f32x2(q.z, q.w), pack_f32x2(row, row)), f[i + 2], f[i + 3]);
+                    }
                 }
                 if (c == 0) {
                     tmem_ld_wait();
@@ -271,12 +287,22 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
             }
         }
         if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
-        // the last block's MMAs have read the ring and every copy into it was
-        // waited for by one of them: it now takes the sums, [token][row of B]
+        // The last block's MMAs have read the ring and every copy into it was
+        // waited for by one of them: it now takes the sums, 128 columns of D
+        // per token.  Swapped, a thread holds one column of every token;
+        // else a part of one token's row, in 16-byte pieces whose place is
+        // turned by the token so that a warp's pieces do not collide.
         if (ok) {
-            float *red = reinterpret_cast<float *>(smem) + c0 * 128 + quad * 32 + lane;
+            if (C::SWAP) {
+                float *red = reinterpret_cast<float *>(smem) + quad * 32 + lane;
 #pragma unroll
-            for (int i = 0; i < C::COLS; ++i) red[i * 128] = acc[i];
+                for (int i = 0; i < C::COLS; ++i) red[i * 128] = acc[i];
+            } else {
+                float4 *red = reinterpret_cast<float4 *>(smem) + (quad * 32 + lane) * 32;
+#pragma unroll
+                for (int i = 0; i < C::COLS / 4; ++i)
+                    red[(c0 / 4 + i) ^ lane] = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+            }
         }
     }
 
@@ -289,16 +315,16 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_cons
     }
     // a CTA that gave up leaves undefined sums; the status word says so
     const int32_t tokens = min(NT, p.M - m0);
-    const uint32_t red0 = smem_u32(smem) + lane * 16;
     const int32_t n = n0 + 4 * lane;
     for (int32_t t = rank + splits * warp; t < tokens; t += splits * (C::THREADS / 32)) {
+        const uint32_t piece = (t * 32 + (C::SWAP ? lane : lane ^ (t & 31))) * 16;
         float4 a;
         if (splits == 1) {
-            a = reinterpret_cast<const float4 *>(smem + t * 512)[lane];
+            a = *reinterpret_cast<const float4 *>(smem + piece);
         } else {
-            a = ld_cluster_v4(mapa_shared(red0 + t * 512, 0));
+            a = ld_cluster_v4(mapa_shared(smem_u32(smem) + piece, 0));
             for (int q = 1; q < splits; ++q) {
-                const float4 o = ld_cluster_v4(mapa_shared(red0 + t * 512, q));
+                const float4 o = ld_cluster_v4(mapa_shared(smem_u32(smem) + piece, q));
                 a = make_float4(a.x + o.x, a.y + o.y, a.z + o.z, a.w + o.w);
             }
         }
@@ -348,10 +374,10 @@ int launch(const Fp8Params &p, int splits, cudaStream_t s)
 {
     using C = SmallCfg<NT>;
     auto kern = gemm_fp8_small_kernel<NT, PER_ROW>;
-    CUtensorMap mw, mt;
+    CUtensorMap mm, mn;
     int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM);
-    if (rc == QFP4_OK) rc = make_map_direct(&mw, p.B, p.K, p.N, 128, 128);
-    if (rc == QFP4_OK) rc = make_map_direct(&mt, p.A, p.K, p.M, 128, NT);
+    if (rc == QFP4_OK) rc = make_map_direct(C::SWAP ? &mm : &mn, p.B, p.K, p.N, 128, 128);
+    if (rc == QFP4_OK) rc = make_map_direct(C::SWAP ? &mn : &mm, p.A, p.K, p.M, 128, NT);
     if (rc != QFP4_OK) return rc;
     const int64_t tiles = static_cast<int64_t>((p.N + 127) / 128) * ((p.M + NT - 1) / NT);
     cudaLaunchConfig_t cfg = {};
@@ -368,7 +394,7 @@ int launch(const Fp8Params &p, int splits, cudaStream_t s)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = splits > 1 ? 2 : 1;
-    return launch_status(cudaLaunchKernelEx(&cfg, kern, mw, mt, p, splits));
+    return launch_status(cudaLaunchKernelEx(&cfg, kern, mm, mn, p, splits));
 }
 
 template <int NT>

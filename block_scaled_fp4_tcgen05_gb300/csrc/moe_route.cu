@@ -50,17 +50,22 @@ struct RouteParams {
     float *mean_prob, *loss;
     // workspace: per chunk, counts [E] (int32), sums of p [E] (fp32); then
     // valid tokens per chunk
-    int32_t *ws_counts;
+    int32_t *ws_counts;         // rows of E4 = E rounded up to 4
     float *ws_prob;
     int32_t *ws_valid;
 };
 
-// Order-preserving key: larger float, larger key; NaN above everything.
+// Order-preserving key: larger float, larger key.  Adding +0 turns -0 into +0
+// and every NaN into the one whose key is above all others.
 __device__ __forceinline__ uint32_t sort_key(float v)
 {
-    if (v != v) return 0xFFFFFFFFu;
-    const uint32_t u = __float_as_uint(v + 0.0f);       // -0 becomes +0
-    return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+    const uint32_t u = __float_as_uint(__fadd_rn(v, 0.0f));
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
 __device__ __forceinline__ float load_logit(const float *p) { return __ldg(p); }
@@ -68,52 +73,41 @@ __device__ __forceinline__ float load_logit(const __nv_bfloat16 *p) { return __b
 __device__ __forceinline__ void store_logit(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-__device__ __forceinline__ float warp_max(float v)
-{
-    for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, d));
-    return v;
-}
 __device__ __forceinline__ float warp_sum(float v)
 {
     for (int d = 16; d > 0; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, d));
     return v;
 }
 
-// exp(l - max) of the lane's experts; returns 1 / their sum over the row (0 for
-// a row with no open expert) and the subtracted maximum.  A NaN or +inf logit
-// makes the sum NaN.
+// x = exp(l - base) of the lane's experts, base the row's largest logit (0 for
+// a row with no open expert); returns 1 / their sum over the row (0 for such a
+// row).  A NaN or +inf logit makes base, or a difference with it, and so the
+// sum, NaN.  exp is 2^(x log2 e) by the hardware's exponential: the rounded
+// product costs |x| 2^-24 relative, the exponential 2^-22.
 template <int V>
-__device__ __forceinline__ float softmax_terms(const float (&l)[V], int E, int lane, float (&x)[V], float &base)
+__device__ __forceinline__ float softmax_terms(const float (&l)[V], int E, int lane, float base, float (&x)[V])
 {
-    float m = -INFINITY;
-    bool nan = false;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        m = fmaxf(m, l[v]);
-        nan |= l[v] != l[v];
-    }
-    m = warp_max(m);
-    if (__any_sync(kFull, nan)) m = NAN;
-    base = m == -INFINITY ? 0.0f : m;
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        x[v] = lane + 32 * v < E ? expf(l[v] - base) : 0.0f;
+        x[v] = lane + 32 * v < E ? __expf(l[v] - base) : 0.0f;
         sum += x[v];
     }
     sum = warp_sum(sum);
     return sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
 }
 
+__device__ __forceinline__ float softmax_base(uint32_t top) { return top <= kKeyNegInf ? 0.0f : key_value(top); }
+
 struct RouteShared {
-    int32_t counts[kMaxExperts];                    // of this range
+    alignas(16) int32_t counts[kMaxExperts];        // of this range
     int32_t start[kMaxExperts];                     // first row of each expert, all ranges
     int32_t before[kMaxExperts];                    // rows of it that earlier ranges fill
     int32_t total[kMaxExperts];
     union {
         float prob[kWarps][kMaxExperts];            // sums of p per warp
         int32_t row[kWarps][kMaxExperts];           // counts, then next row, of each warp's pairs
-        int32_t part[2][kThreads];                  // partial sums over ranges
+        int4 part[2][kThreads];                     // partial sums over ranges, four experts each
         float ppart[kThreads];
     };
     int32_t valid;
@@ -125,43 +119,51 @@ template <typename L, int V>
 __device__ __forceinline__ void route_rows(const RouteParams &p, int64_t t0, int64_t t1, RouteShared &sh)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float psum[V];
+    float psum[V], l[V], ahead[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) psum[v] = 0.0f;
     int nvalid = 0;
+    auto load_row = [&](int64_t t, float (&d)[V]) {
+        if (t < t1) {
+            const L *row = static_cast<const L *>(p.logits) + t * p.E;
+#pragma unroll
+            for (int v = 0; v < V; ++v) d[v] = lane + 32 * v < p.E ? load_logit(row + lane + 32 * v) : -INFINITY;
+        }
+    };
+    load_row(t0 + warp, ahead);
     for (int64_t t = t0 + warp; t < t1; t += kWarps) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[v] = ahead[v];
+        load_row(t + kWarps, ahead);        // the next token's logits come while this one is worked on
         int32_t my_id = -1;
         float my_gate = 0.0f;
         if (!p.valid || p.valid[t] != 0) {
             ++nvalid;
-            const L *row = static_cast<const L *>(p.logits) + t * p.E;
-            float l[V], x[V], base;
-            uint32_t key[V];
+            // the lane's best and second best key and their places (equal keys: the lowest expert first)
+            uint32_t key[V], best = 0u, second = 0u;
+            int at = 0, then = 0;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int e = lane + 32 * v;
-                l[v] = e < p.E ? load_logit(row + e) : -INFINITY;
-                key[v] = e < p.E ? sort_key(l[v]) : 0u;
+                key[v] = sort_key(l[v]);
+                if (key[v] > best) {
+                    second = best;
+                    then = at;
+                    best = key[v];
+                    at = v;
+                } else if (V > 1 && key[v] > second) {
+                    second = key[v];
+                    then = v;
+                }
             }
-            const float inv = softmax_terms<V>(l, p.E, lane, x, base);
+            bool known = true;              // second is the lane's next best
+            uint32_t top = __reduce_max_sync(kFull, best);
+            const float base = softmax_base(top);
+            float x[V];
+            const float inv = softmax_terms<V>(l, p.E, lane, base, x);
 #pragma unroll
-            for (int v = 0; v < V; ++v) psum[v] = __fadd_rn(psum[v], x[v] * inv);
-            // the lane's best key and its place, lowest expert first
-            uint32_t best = key[0];
-            int at = 0;
-            auto find = [&]() {
-                best = key[0];
-                at = 0;
-#pragma unroll
-                for (int v = 1; v < V; ++v)
-                    if (key[v] > best) {
-                        best = key[v];
-                        at = v;
-                    }
-            };
-            find();
+            for (int v = 0; v < V; ++v) psum[v] = fmaf(x[v], inv, psum[v]);
             for (int j = 0; j < p.topk; ++j) {
-                const uint32_t top = __reduce_max_sync(kFull, best);
+                if (j > 0) top = __reduce_max_sync(kFull, best);
                 if (top <= kKeyNegInf) break;
                 uint32_t who = __ballot_sync(kFull, best == top);
                 uint32_t e = lane + 32 * at;
@@ -173,13 +175,26 @@ __device__ __forceinline__ void route_rows(const RouteParams &p, int64_t t0, int
                 e = __shfl_sync(kFull, e, src);
                 if (lane == j) my_id = static_cast<int32_t>(e);
                 if (lane == src) {
+                    if (V == 1) {
+                        best = 0u;
+                    } else {
+                        if (!known) {           // the lane's third and later: the largest after (best, at)
+                            second = 0u;
 #pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        if (v == at) key[v] = 0u;
-                    find();
+                            for (int v = 0; v < V; ++v)
+                                if ((key[v] < best || (key[v] == best && v > at)) && key[v] > second) {
+                                    second = key[v];
+                                    then = v;
+                                }
+                        }
+                        known = false;
+                        best = second;
+                        at = then;
+                    }
                 }
             }
-            const float my_x = my_id >= 0 ? expf(load_logit(row + my_id) - base) : 0.0f;
+            float my_x = 0.0f;
+            if (my_id >= 0) my_x = __expf(load_logit(static_cast<const L *>(p.logits) + t * p.E + my_id) - base);
             const float scale = p.renorm ? warp_sum(my_x) : 0.0f;
             my_gate = my_id < 0 ? 0.0f : p.renorm ? (scale == 0.0f ? 0.0f : __fdiv_rn(my_x, scale)) : my_x * inv;
             if (my_id >= 0) atomicAdd(&sh.counts[my_id], 1);
@@ -315,8 +330,9 @@ route_rows_kernel(const RouteParams p)
     __syncthreads();
     if (tid < p.E) {
         p.ws_prob[static_cast<int64_t>(blockIdx.x) * p.E + tid] = route_prob(sh, tid);
-        p.ws_counts[static_cast<int64_t>(blockIdx.x) * p.E + tid] = sh.counts[tid];
     }
+    if (tid < (p.E + 3) / 4)
+        reinterpret_cast<int4 *>(p.ws_counts)[blockIdx.x * ((p.E + 3) / 4) + tid] = reinterpret_cast<const int4 *>(sh.counts)[tid];
     if (tid == 0) p.ws_valid[blockIdx.x] = sh.valid;
 }
 
@@ -327,31 +343,43 @@ route_place_kernel(const RouteParams p, int chunks)
     __shared__ RouteShared sh;
     const int tid = threadIdx.x;
     const bool totals = static_cast<int>(blockIdx.x) == chunks;
-    // every expert's counts are added up by `parts` threads
-    const int width = p.E <= 32 ? 32 : p.E <= 64 ? 64 : p.E <= 128 ? 128 : 256;
+    // four experts' counts are added up by `parts` threads, ten ranges or fewer each
+    const int e4 = (p.E + 3) / 4;
+    const int width = e4 <= 8 ? 8 : e4 <= 16 ? 16 : e4 <= 32 ? 32 : 64;
     const int parts = kThreads / width, part = tid / width, e = tid % width;
     pdl_wait();
     pdl_launch_dependents();
-    int32_t before = 0, total = 0;
-    if (e < p.E) {
-#pragma unroll 8
-        for (int c = part; c < chunks; c += parts) {
-            const int32_t n = __ldcg(p.ws_counts + static_cast<int64_t>(c) * p.E + e);
-            if (c < static_cast<int>(blockIdx.x)) before += n;
-            total += n;
+    int4 before = make_int4(0, 0, 0, 0), total = make_int4(0, 0, 0, 0);
+    if (e < e4) {
+        constexpr int kLoads = (kMaxChunks + 15) / 16;          // (16 parts at 64 threads of width)
+        int4 n[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int c = part + i * parts;
+            n[i] = c < chunks ? __ldcg(reinterpret_cast<const int4 *>(p.ws_counts) + c * e4 + e) : make_int4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            if (part + i * parts < static_cast<int>(blockIdx.x)) {
+                before.x += n[i].x; before.y += n[i].y; before.z += n[i].z; before.w += n[i].w;
+            }
+            total.x += n[i].x; total.y += n[i].y; total.z += n[i].z; total.w += n[i].w;
         }
     }
     sh.part[0][tid] = before;
     sh.part[1][tid] = total;
     __syncthreads();
     if (tid < p.E) {
-        before = total = 0;
+        int32_t b = 0, n = 0;
+        const int32_t *pb = reinterpret_cast<const int32_t *>(sh.part[0]) + tid;
+        const int32_t *pn = reinterpret_cast<const int32_t *>(sh.part[1]) + tid;
+#pragma unroll 16
         for (int i = 0; i < parts; ++i) {
-            before += sh.part[0][i * width + tid];
-            total += sh.part[1][i * width + tid];
+            b += pb[i * width * 4];
+            n += pn[i * width * 4];
         }
-        sh.before[tid] = before;
-        sh.total[tid] = total;
+        sh.before[tid] = b;
+        sh.total[tid] = n;
     }
     __syncthreads();
     route_starts(p, sh);
@@ -366,10 +394,11 @@ route_place_kernel(const RouteParams p, int chunks)
         route_place(p, t0, min(p.T, t0 + p.chunk), sh);
         return;
     }
+    const int pwidth = 4 * width, pparts = kThreads / pwidth, pp = tid / pwidth, pe = tid % pwidth;
     float s = 0.0f;
-    if (e < p.E) {
+    if (pe < p.E) {
 #pragma unroll 8
-        for (int c = part; c < chunks; c += parts) s = __fadd_rn(s, __ldcg(p.ws_prob + static_cast<int64_t>(c) * p.E + e));
+        for (int c = pp; c < chunks; c += pparts) s = __fadd_rn(s, __ldcg(p.ws_prob + static_cast<int64_t>(c) * p.E + pe));
     }
     __syncthreads();
     sh.ppart[tid] = s;
@@ -382,7 +411,7 @@ route_place_kernel(const RouteParams p, int chunks)
     __syncthreads();
     s = 0.0f;
     if (tid < p.E)
-        for (int i = 0; i < parts; ++i) s = __fadd_rn(s, sh.ppart[i * width + tid]);
+        for (int i = 0; i < pparts; ++i) s = __fadd_rn(s, sh.ppart[i * pwidth + tid]);
     route_totals(p, sh, sh.valid, s);
 }
 
@@ -455,13 +484,20 @@ route_backward_kernel(const BackParams p)
         }
         const L *row = static_cast<const L *>(p.logits) + t * p.E;
         float l[V], x[V], h[V];
+        uint32_t best = 0u;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int e = lane + 32 * v;
             l[v] = e < p.E ? load_logit(row + e) : -INFINITY;
+            best = max(best, sort_key(l[v]));
         }
-        float base;
-        const float inv = softmax_terms<V>(l, p.E, lane, x, base);
+        // lane j < k: choice j
+        int32_t id = p.dgates && lane < p.topk ? p.ids[t * p.topk + lane] : -1;
+        if (id >= p.E) id = -1;
+        const float dg = id >= 0 ? p.dgates[t * p.topk + lane] : 0.0f;
+        const float lj = id >= 0 ? load_logit(row + id) : 0.0f;
+        const float base = softmax_base(__reduce_max_sync(kFull, best));
+        const float inv = softmax_terms<V>(l, p.E, lane, base, x);
         float dot = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -471,21 +507,7 @@ route_backward_kernel(const BackParams p)
         }
         dot = warp_sum(dot);
         if (p.dgates) {
-            // lane j < k: choice j
-            int32_t id = lane < p.topk ? p.ids[t * p.topk + lane] : -1;
-            if (id >= p.E) id = -1;
-            const float dg = id >= 0 ? p.dgates[t * p.topk + lane] : 0.0f;
-            float pj = 0.0f;
-            for (int j = 0; j < p.topk; ++j) {
-                const int32_t e = __shfl_sync(kFull, id, j);
-                if (e < 0) continue;
-                float mine = 0.0f;
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (lane + 32 * v == e) mine = x[v];
-                mine = __shfl_sync(kFull, mine, e & 31);
-                if (lane == j) pj = mine;
-            }
+            const float pj = id >= 0 ? __expf(lj - base) * inv : 0.0f;
             float g = pj;
             if (p.renorm) {
                 const float total = warp_sum(pj);
@@ -559,7 +581,8 @@ extern "C" size_t qfp4_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t t
 {
     if (T < 0 || E < 1 || topk < 1 || !sizes_ok(T, E, topk)) return 0;
     const size_t chunks = static_cast<size_t>(chunk_count(T));
-    return chunks * static_cast<size_t>(E) * 8 + chunks * 4;
+    const size_t E4 = static_cast<size_t>((E + 3) / 4 * 4);
+    return chunks * (E4 + static_cast<size_t>(E)) * 4 + chunks * 4;
 }
 
 extern "C" int qfp4_moe_route(int logits_type, const void *logits, int64_t T, int64_t E, int64_t topk,
@@ -581,7 +604,7 @@ extern "C" int qfp4_moe_route(int logits_type, const void *logits, int64_t T, in
     RouteParams p{logits, valid, T, static_cast<int32_t>(E), static_cast<int32_t>(topk), renorm ? 1 : 0,
                   (T + chunks - 1) / chunks, ids, gates, counts, row_offsets, dest, src, n_valid, mean_prob, loss};
     p.ws_counts = static_cast<int32_t *>(workspace);
-    p.ws_prob = reinterpret_cast<float *>(p.ws_counts + chunks * E);
+    p.ws_prob = reinterpret_cast<float *>(p.ws_counts + chunks * ((E + 3) / 4 * 4));
     p.ws_valid = reinterpret_cast<int32_t *>(p.ws_prob + chunks * E);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return logits_type == QFP4_BF16 ? launch_forward<__nv_bfloat16>(p, static_cast<int>(chunks), s)
