@@ -294,22 +294,21 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
 
     if (warp < 4) {
         setmaxnreg_dec<40>();
-        if (warp == 0 || warp == 2) {
-            // ------------------------------------------------ A (warp 0) and B (warp 2) TMA producers
+        if (warp == 0) {
+            // ------------------------------------------------ TMA producer
             if (lane == 0) {
-                const bool is_a = warp == 0;
                 const uint32_t full0_leader = mapa_shared(smem_u32(&full[0]), 0);
-                const CUtensorMap *map = is_a ? &tmA : &tmB;
                 uint32_t s = 0, phase = 1;
                 bool ok = true;
                 for (int32_t t = pair_id; t < total_tiles && ok; t += npairs) {
                     const Tile ti = tile_info(t);
-                    const int32_t row = (is_a ? ti.row0 : ti.group * p.N + ti.n0) + 128 * static_cast<int32_t>(rank);
+                    const int32_t arow = ti.row0 + 128 * static_cast<int32_t>(rank);
+                    const int32_t brow = ti.group * p.N + ti.n0 + 128 * static_cast<int32_t>(rank);
                     for (int32_t kb = 0; kb < kblocks; ++kb) {
                         if (!mbar_wait(smem_u32(&empty[s]), phase)) { ok = false; break; }
-                        if (is_a && rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * kStageBytes);
-                        tma_load_2d_pair(smem_u32(smem + s * kStageBytes + (is_a ? 0 : kOpBytes)), map,
-                                         full0_leader + s * 8, kb * 128, row);
+                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * kStageBytes);
+                        tma_load_2d_pair(smem_u32(smem + s * kStageBytes), &tmA, full0_leader + s * 8, kb * 128, arow);
+                        tma_load_2d_pair(smem_u32(smem + s * kStageBytes + kOpBytes), &tmB, full0_leader + s * 8, kb * 128, brow);
                         if (++s == kStages) { s = 0; phase ^= 1; }
                     }
                 }
@@ -351,38 +350,37 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 }
             }
             if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
-        } else if (warp == 1) {
-            // ------------------------------------------------ MMA issuer (leader): a K block's sum into each
-            // slot in turn
-            if (rank == 0) {
-                // the whole warp keeps count, one lane issues: descriptors stay in uniform registers
-                const uint64_t a_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-                const uint64_t b_desc0 = smem_desc(smem_u32(smem) + kOpBytes, 16, 1024, kSwizzle128B);
-                const uint32_t idesc = idesc_f8(256, 256, p.a_type, p.b_type);
-                uint32_t s = 0, phase = 0, slot = 0, acc_phase = 1;
-                bool ok = true, loaded = false;     // loaded: the next stage is known to have landed
-                for (int32_t t = pair_id; t < total_tiles && ok; t += npairs) {
-                    for (int32_t kb = 0; kb < kblocks; ++kb) {
-                        if (!loaded && !mbar_wait_warp(smem_u32(&full[s]), phase)) { ok = false; break; }
-                        const uint64_t ad = a_desc0 + s * static_cast<uint64_t>(kStageBytes >> 4);
-                        const uint64_t bd = b_desc0 + s * static_cast<uint64_t>(kStageBytes >> 4);
-                        if (!mbar_wait_warp(smem_u32(&acc_empty[slot]), acc_phase)) { ok = false; break; }
-                        tc_fence_after();
-                        if (elect_one_sync()) {
+        } else if (rank == 0) {
+            // ------------------------------------------------ MMA issuers (leader): warp 1 sums the even K
+            // blocks of the whole sequence into slot 0, warp 2 the odd ones into slot 1
+            // the whole warp keeps count, one lane issues: descriptors stay in uniform registers
+            const uint32_t slot = warp - 1;
+            const uint64_t a_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+            const uint64_t b_desc0 = smem_desc(smem_u32(smem) + kOpBytes, 16, 1024, kSwizzle128B);
+            const uint32_t idesc = idesc_f8(256, 256, p.a_type, p.b_type);
+            uint32_t s = slot, phase = 0, acc_phase = 1;
+            bool ok = true;
+            const int64_t mine = pair_id < total_tiles ? (total_tiles - pair_id + npairs - 1) / npairs : 0;
+            const int64_t count = mine * kblocks;
+            for (int64_t j = slot; j < count; j += 2) {
+                if (!mbar_wait_warp(smem_u32(&full[s]), phase) ||
+                    !mbar_wait_warp(smem_u32(&acc_empty[slot]), acc_phase)) { ok = false; break; }
+                tc_fence_after();
+                if (elect_one_sync()) {
+                    const uint64_t ad = a_desc0 + s * static_cast<uint64_t>(kStageBytes >> 4);
+                    const uint64_t bd = b_desc0 + s * static_cast<uint64_t>(kStageBytes >> 4);
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                tc_mma_f8_pair(tmem_base + slot * 256, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-                            tc_commit_pair(smem_u32(&acc_full[slot]), 0x3);
-                            tc_commit_pair(smem_u32(&empty[s]), 0x3);
-                        }
-                        __syncwarp();
-                        if (++slot == kSlots) { slot = 0; acc_phase ^= 1; }
-                        if (++s == kStages) { s = 0; phase ^= 1; }
-                        loaded = __all_sync(0xffffffffu, mbar_test(smem_u32(&full[s]), phase));
-                    }
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_f8_pair(tmem_base + slot * 256, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+                    tc_commit_pair(smem_u32(&acc_full[slot]), 0x3);
+                    tc_commit_pair(smem_u32(&empty[s]), 0x3);
                 }
-                if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
+                __syncwarp();
+                acc_phase ^= 1;
+                s += 2;
+                if (s >= kStages) { s -= kStages; phase ^= 1; }
             }
+            if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
         }
     } else {
         setmaxnreg_inc<232>();

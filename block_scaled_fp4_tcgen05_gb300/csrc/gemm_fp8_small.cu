@@ -2,7 +2,7 @@
 // tokens, short prompts), where 256 x 256 tiles would leave most SMs idle and
 // the weights' bytes bound the time.
 //
-// A CTA (tcgen05 cta_group::1) takes one tile.  Up to 64 rows of A (NT): swap
+// A CTA (tcgen05 cta_group::1) takes one tile.  Up to 32 rows of A (NT): swap
 // AB, 128 rows of B in the MMA's M slot and the tokens in its N slot, D^T.
 // More: 128 rows of A in the M slot and 128 of B in the N slot; a thread's
 // block sums then share one scale, where the swapped form needs one per token
@@ -15,7 +15,7 @@
 // CTAs in order (the results repeat bit for bit, and no scratch in global
 // memory is needed).
 //
-// Warps: 0 and 3 TMA producers, 1 tensor-memory owner and MMA issuer, 2 scales,
+// Warps: 0 TMA producer, 1 and 3 MMA issuers (1 owns tensor memory), 2 scales,
 // 4.. epilogue (four of all columns, or sixteen of 32 each).
 #include <cstdint>
 #include <cuda.h>
@@ -59,7 +59,7 @@ struct SmallCfg {
     static constexpr int CTAS = SWAP ? 2 : 1;                   // resident CTAs per SM that the ring is sized for
     static constexpr int M_BYTES = 128 * 128;                   // the M slot's 128 rows x 128 elements of K
     static constexpr int STAGE = M_BYTES + NT * 128;
-    static constexpr int STAGES = NT == 64 ? 4 : 5;
+    static constexpr int STAGES = 5;
     static constexpr int SCALES = 128 + NT;                     // floats per K block: the M slot's rows, then the N slot's
     static constexpr int OFF_SCALE = STAGES * STAGE;
     static constexpr int OFF_BAR = OFF_SCALE + 2 * kBatch * SCALES * 4;
@@ -143,37 +143,32 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
     pdl_wait();
     pdl_launch_dependents();
 
-    if (warp == 0 || warp == 3) {
-        // ------------------------------------------------ TMA producers of the M slot's (warp 0) and the N
-        // slot's (warp 3) operand: the copy engine takes one thread's requests one after another
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
         if (lane == 0) {
-            const bool is_m = warp == 0;
-            const int32_t row = is_m == C::SWAP ? n0 : m0;
             uint32_t s = 0, phase = 1;
             bool ok = true;
             for (int32_t j = 0; j < nkb; ++j) {
                 if (!mbar_wait(smem_u32(&empty[s]), phase)) { ok = false; break; }
                 const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(smem + s * C::STAGE);
-                if (is_m) {
-                    mbar_arrive_expect_tx(bar, C::STAGE);
-                    tma_load_2d(dst, &tmM, bar, (kb0 + j) * 128, row);
-                } else {
-                    tma_load_2d(dst + C::M_BYTES, &tmN, bar, (kb0 + j) * 128, row);
-                }
+                mbar_arrive_expect_tx(bar, C::STAGE);
+                tma_load_2d(dst, &tmM, bar, (kb0 + j) * 128, C::SWAP ? n0 : m0);
+                tma_load_2d(dst + C::M_BYTES, &tmN, bar, (kb0 + j) * 128, C::SWAP ? m0 : n0);
                 if (++s == C::STAGES) { s = 0; phase ^= 1; }
             }
             if (!ok) { record_timeout(); *abort_flag = 1; }
         }
-    } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer
+    } else if (warp == 1 || warp == 3) {
+        // ------------------------------------------------ MMA issuers: warp 1 sums the even K blocks into slot
+        // 0, warp 3 the odd ones into slot 1, so that one looks at its barriers while the other's MMAs run
+        const uint32_t slot = warp >> 1;
         const uint64_t m_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
         const uint64_t n_desc0 = smem_desc(smem_u32(smem) + C::M_BYTES, 16, 1024, kSwizzle128B);
         const uint32_t idesc = C::SWAP ? idesc_f8(128, NT, p.b_type, p.a_type) : idesc_f8(128, NT, p.a_type, p.b_type);
-        uint32_t s = 0, phase = 0, slot = 0, acc_phase = 1;
-        bool ok = true, loaded = false;      // loaded: the next stage is known to have landed
-        for (int32_t j = 0; j < nkb; ++j) {
-            if ((!loaded && !mbar_wait_warp(smem_u32(&full[s]), phase)) ||
-                !mbar_wait_warp(smem_u32(&acc_empty[slot]), acc_phase)) {
+        uint32_t s = slot, phase = 0, acc_phase = 1;
+        bool ok = true;
+        for (int32_t j = slot; j < nkb; j += 2) {
+            if (!mbar_wait_warp(smem_u32(&full[s]), phase) || !mbar_wait_warp(smem_u32(&acc_empty[slot]), acc_phase)) {
                 ok = false;
                 break;
             }
@@ -188,10 +183,9 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
                 tc_commit(smem_u32(&empty[s]));
             }
             __syncwarp();
-            slot ^= 1;
-            if (slot == 0) acc_phase ^= 1;
-            if (++s == C::STAGES) { s = 0; phase ^= 1; }
-            loaded = __all_sync(0xffffffffu, mbar_test(smem_u32(&full[s]), phase));
+            acc_phase ^= 1;
+            s += 2;
+            if (s >= C::STAGES) { s -= C::STAGES; phase ^= 1; }
         }
         if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
     } else if (warp == 2) {
@@ -322,11 +316,15 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
         if (splits == 1) {
             a = *reinterpret_cast<const float4 *>(smem + piece);
         } else {
-            a = ld_cluster_v4(mapa_shared(smem_u32(smem) + piece, 0));
-            for (int q = 1; q < splits; ++q) {
-                const float4 o = ld_cluster_v4(mapa_shared(smem_u32(smem) + piece, q));
-                a = make_float4(a.x + o.x, a.y + o.y, a.z + o.z, a.w + o.w);
-            }
+            // all CTAs' pieces on their way, then added in order
+            float4 o[kMaxSplits];
+#pragma unroll
+            for (int q = 0; q < kMaxSplits; ++q)
+                if (q < splits) o[q] = ld_cluster_v4(mapa_shared(smem_u32(smem) + piece, q));
+            a = o[0];
+#pragma unroll
+            for (int q = 1; q < kMaxSplits; ++q)
+                if (q < splits) a = make_float4(a.x + o[q].x, a.y + o[q].y, a.z + o[q].z, a.w + o[q].w);
         }
         const float o[4] = {a.x, a.y, a.z, a.w};
         const int64_t at = static_cast<int64_t>(m0 + t) * p.N + n;
@@ -403,7 +401,7 @@ int launch_nt(const Fp8Params &p, int splits, cudaStream_t s)
     return p.b_rows == 1 ? launch<NT, true>(p, splits, s) : launch<NT, false>(p, splits, s);
 }
 
-int tokens_of(const Fp8Params &p) { return p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128; }
+int tokens_of(const Fp8Params &p) { return p.M <= 16 ? 16 : p.M <= 32 ? 32 : 128; }
 
 }  // namespace
 
@@ -427,7 +425,6 @@ int launch_gemm_fp8_small(const Fp8Params &p, cudaStream_t s)
     switch (nt) {
     case 16: return launch_nt<16>(p, splits, s);
     case 32: return launch_nt<32>(p, splits, s);
-    case 64: return launch_nt<64>(p, splits, s);
     default: return launch_nt<128>(p, splits, s);
     }
 }
