@@ -56,40 +56,34 @@ int read_clear_status_gemm_fp8(cudaStream_t s, uint32_t *out)
 
 namespace {
 
-constexpr int kMaxGroups = 256;
 constexpr int64_t kMaxSize = int64_t{1} << 30;
 
-// Row offsets a grouped product can use: from 0, never decreasing, at most
-// total_rows, no group above max_rows (0 = no bound).
-__device__ __forceinline__ bool fp8_offsets_valid(const int32_t *offs, int groups, int32_t total_rows,
-                                                  int32_t max_rows)
-{
-    if (offs[0] != 0 || offs[groups] > total_rows) return false;
-    for (int e = 0; e < groups; ++e) {
-        const int64_t rows = static_cast<int64_t>(offs[e + 1]) - offs[e];
-        if (rows < 0 || (max_rows > 0 && rows > max_rows)) return false;
-    }
-    return true;
-}
-
-// ---------------------------------------------------------------- CTA pairs, 256 x 256 tiles
+// ---------------------------------------------------------------- CTA pairs, 256 x TN tiles
 
 constexpr int kPairThreads = 384;       // 12 warps
-constexpr int kEpiWarps = 8;            // per slot: set h of eight warps drains part h of every K block
-constexpr int kStages = 4;
-constexpr int kOpBytes = 128 * 128;     // 128 rows x 128 elements of K
-constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kSlots = 2;               // accumulator slots of 256 columns
+constexpr int kEpiWarps = 8;
 constexpr int kBatch = 8;               // K blocks per hand-over of scales
-constexpr int kScaleFloats = 128 + 256; // per K block: the CTA's rows, then the tile's columns (or its two blocks)
-constexpr int kOffScale = kStages * kStageBytes;    // two batches
+constexpr int kABytes = 128 * 128;      // a CTA's 128 rows of A x 128 elements of K
 constexpr int kBoxBytes = 32 * 128;     // output staging box: 32 rows x 128 bytes
-constexpr int kBoxes = 2;               // per epilogue warp
-constexpr int kOffOut = kOffScale + 2 * kBatch * kScaleFloats * 4;
-constexpr int kOffBar = kOffOut + kEpiWarps * kBoxes * kBoxBytes;
-constexpr int kPairBars = 2 * kStages + 2 * kSlots + 4;  // full, empty [stage]; acc_full, acc_empty [slot]; sc_full, sc_empty [2]
-constexpr int kPairSmem = kOffBar + kPairBars * 8 + 16 + 1024;
-static_assert(kPairSmem + 4096 <= 232448, "shared memory overflow");
+
+template <int TN>
+struct PairCfg {
+    static constexpr int STAGES = TN == 256 ? 4 : 7;
+    static constexpr int STAGE = kABytes + TN / 2 * 128;        // and TN / 2 rows of B
+    static constexpr int SLOTS = 512 / TN;                      // accumulator slots of TN columns
+    static constexpr int COLS = TN / 2;                         // columns per epilogue warp
+    static constexpr int SCALES = 128 + TN;                     // floats per K block: the CTA's rows, then the tile's
+                                                                // columns (or its blocks of 128)
+    static constexpr int BOXES = TN / 128;                      // staging boxes per epilogue warp
+    static constexpr int OFF_SCALE = STAGES * STAGE;            // two batches
+    static constexpr int OFF_OUT = OFF_SCALE + 2 * kBatch * SCALES * 4;
+    static constexpr int OFF_BAR = OFF_OUT + kEpiWarps * BOXES * kBoxBytes;
+    // full, empty [stage]; acc_full, acc_empty [slot]; sc_full, sc_empty [2]
+    static constexpr int NBAR = 2 * STAGES + 2 * SLOTS + 4;
+    static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16 + 1024;
+    static_assert(SMEM + 4096 <= 232448, "shared memory overflow");
+    static_assert(OFF_OUT % 1024 == 0, "swizzled boxes start on 1 KB");
+};
 
 __device__ __forceinline__ void record_timeout()
 {
@@ -98,24 +92,24 @@ __device__ __forceinline__ void record_timeout()
 
 
 
-// Writes a warp's 32 rows x 128 columns of D; lane i holds row i.  The rows
+// Writes a warp's 32 rows x COLS columns of D; lane i holds row i.  The rows
 // are staged as boxes of 128 bytes x 32 rows in the 128-byte swizzle of the
-// store map (16-byte piece c of row r at c ^ (r % 8)), up to kBoxes of them at
+// store map (16-byte piece c of row r at c ^ (r % 8)), up to BOXES of them at
 // a time, and leave together behind one fence.
-template <bool FP32>
-__device__ __forceinline__ void store_tile(const float (&acc)[128], uint8_t *out, const CUtensorMap &map,
+template <bool FP32, int COLS, int BOXES>
+__device__ __forceinline__ void store_tile(const float (&acc)[COLS], uint8_t *out, const CUtensorMap &map,
                                            const Fp8Params &p, bool by_tma, int32_t row0, int32_t rows, int32_t c0,
                                            int lane)
 {
     constexpr int kCols = FP32 ? 32 : 64;       // columns of a box
 #pragma unroll
-    for (int q0 = 0; q0 < 128 / kCols; q0 += kBoxes) {
+    for (int q0 = 0; q0 < COLS / kCols; q0 += BOXES) {
         if (c0 + q0 * kCols >= p.N) break;
         // the boxes are free once the copy engine has read what left them last
         if (lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
 #pragma unroll
-        for (int q = 0; q < kBoxes; ++q)
+        for (int q = 0; q < BOXES; ++q)
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 uint32_t w[4];
@@ -137,7 +131,7 @@ __device__ __forceinline__ void store_tile(const float (&acc)[128], uint8_t *out
             __syncwarp();
             if (lane == 0) {
 #pragma unroll
-                for (int q = 0; q < kBoxes; ++q) {
+                for (int q = 0; q < BOXES; ++q) {
                     const int32_t col = c0 + (q0 + q) * kCols;
                     if (col >= p.N) break;
                     if (p.accumulate) tma_reduce_add_2d(&map, smem_u32(out + q * kBoxBytes), col, row0);
@@ -150,7 +144,7 @@ __device__ __forceinline__ void store_tile(const float (&acc)[128], uint8_t *out
         __syncwarp();
         // a row's 128 bytes of a box at a time, a word per lane
 #pragma unroll
-        for (int q = 0; q < kBoxes; ++q) {
+        for (int q = 0; q < BOXES; ++q) {
             const int32_t col = c0 + (q0 + q) * kCols + (FP32 ? lane : 2 * lane);
 #pragma unroll 4
             for (int r = 0; r < rows; ++r) {
@@ -179,19 +173,22 @@ struct Tile {
     int32_t row0, row_end, n0, group;
 };
 
-template <bool GROUPED, bool COLSCALE>
+// GROUPED: one product per expert.  COLSCALE: B has one scale per row
+// (b_rows = 1), else one per 128 rows.
+template <bool GROUPED, bool COLSCALE, int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmD, const Fp8Params p)
 {
+    using C = PairCfg<TN>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + kOffBar);   // leader: bytes of both CTAs
-    uint64_t *empty = full + kStages;                                // stage free again (MMA commit, both CTAs)
-    uint64_t *acc_full = empty + kStages;                            // slot's sum complete (both CTAs)
-    uint64_t *acc_empty = acc_full + kSlots;                         // leader: slot drained by both CTAs
-    uint64_t *sc_full = acc_empty + kSlots;                          // [2] batch of scales written
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);   // leader: bytes of both CTAs
+    uint64_t *empty = full + C::STAGES;                                // stage free again (MMA commit, both CTAs)
+    uint64_t *acc_full = empty + C::STAGES;                            // slot's sum complete (both CTAs)
+    uint64_t *acc_empty = acc_full + C::SLOTS;                         // leader: slot drained by both CTAs
+    uint64_t *sc_full = acc_empty + C::SLOTS;                          // [2] batch of scales written
     uint64_t *sc_empty = sc_full + 2;                                // [2] batch of scales read
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sc_empty + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -202,26 +199,40 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int32_t kblocks = (p.K + 127) / 128;
-    const int32_t ntiles_n = (p.N + 255) / 256;
+    const int32_t ntiles_n = (p.N + TN - 1) / TN;
     const int32_t pair_id = blockIdx.x >> 1;
     const int32_t npairs = gridDim.x >> 1;
 
     if (GROUPED) pdl_wait();
     int32_t total_tiles;
     if (GROUPED) {
-        __shared__ int s_bad;
         for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) s_offs[i] = p.row_offsets[i];
         __syncthreads();
-        if (threadIdx.x == 0) {
-            s_bad = fp8_offsets_valid(s_offs, p.groups, p.M, p.max_group_rows) ? 0 : 1;
-            if (s_bad && blockIdx.x == 0) atomicOr(&g_status_gemm_fp8, static_cast<uint32_t>(kStatusBadGroup));
-            int32_t pt = 0;
-            for (int e = 0; e < p.groups; ++e) {
-                s_ptile[e] = pt;
-                const int32_t rows = s_offs[e + 1] - s_offs[e];
-                pt += !s_bad && rows > 0 ? (rows + 255) / 256 : 0;
+        const bool bad = __syncthreads_or(threadIdx.x < p.groups &&
+                                          !fp8_offsets_valid(s_offs, threadIdx.x, p.groups, p.M, p.max_group_rows));
+        if (bad && threadIdx.x == 0 && blockIdx.x == 0)
+            atomicOr(&g_status_gemm_fp8, static_cast<uint32_t>(kStatusBadGroup));
+        // running sum of the groups' 256-row tiles, eight groups a lane
+        if (warp == 0) {
+            constexpr int kPer = kMaxGroups / 32;
+            int32_t before[kPer], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int e = lane * kPer + i;
+                before[i] = sum;
+                sum += !bad && e < p.groups ? (s_offs[e + 1] - s_offs[e] + 255) / 256 : 0;
             }
-            s_ptile[p.groups] = pt;
+            int32_t up = sum;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int32_t o = __shfl_up_sync(0xffffffffu, up, d);
+                if (lane >= d) up += o;
+            }
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int e = lane * kPer + i;
+                if (e < p.groups) s_ptile[e] = up - sum + before[i];
+            }
+            if (lane == 31) s_ptile[p.groups] = up;
         }
         __syncthreads();
         total_tiles = s_ptile[p.groups] * ntiles_n;
@@ -230,11 +241,11 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     }
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
-        for (int b = 0; b < kSlots; ++b) {
+        for (int b = 0; b < C::SLOTS; ++b) {
             mbar_init(smem_u32(&acc_full[b]), 1);
             mbar_init(smem_u32(&acc_empty[b]), 2 * kEpiWarps);
         }
@@ -288,7 +299,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         const int32_t rows_here = min(GM, mtiles - first_m);
         const int32_t idx = lt % per_group;
         ti.row0 = base + (first_m + idx % rows_here) * 256;
-        ti.n0 = (idx / rows_here) * 256;
+        ti.n0 = (idx / rows_here) * TN;
         return ti;
     };
 
@@ -303,13 +314,13 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 for (int32_t t = pair_id; t < total_tiles && ok; t += npairs) {
                     const Tile ti = tile_info(t);
                     const int32_t arow = ti.row0 + 128 * static_cast<int32_t>(rank);
-                    const int32_t brow = ti.group * p.N + ti.n0 + 128 * static_cast<int32_t>(rank);
+                    const int32_t brow = ti.group * p.N + ti.n0 + TN / 2 * static_cast<int32_t>(rank);
                     for (int32_t kb = 0; kb < kblocks; ++kb) {
                         if (!mbar_wait(smem_u32(&empty[s]), phase)) { ok = false; break; }
-                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * kStageBytes);
-                        tma_load_2d_pair(smem_u32(smem + s * kStageBytes), &tmA, full0_leader + s * 8, kb * 128, arow);
-                        tma_load_2d_pair(smem_u32(smem + s * kStageBytes + kOpBytes), &tmB, full0_leader + s * 8, kb * 128, brow);
-                        if (++s == kStages) { s = 0; phase ^= 1; }
+                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * C::STAGE);
+                        tma_load_2d_pair(smem_u32(smem + s * C::STAGE), &tmA, full0_leader + s * 8, kb * 128, arow);
+                        tma_load_2d_pair(smem_u32(smem + s * C::STAGE + kABytes), &tmB, full0_leader + s * 8, kb * 128, brow);
+                        if (++s == C::STAGES) { s = 0; phase ^= 1; }
                     }
                 }
                 if (!ok) { record_timeout(); *abort_flag = 1; }
@@ -325,22 +336,22 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 const int32_t row = ti.row0 + 128 * static_cast<int32_t>(rank) + lane;
                 for (int32_t kb0 = 0; kb0 < kblocks; kb0 += kBatch) {
                     if (!mbar_wait_warp(smem_u32(&sc_empty[b]), phase)) { ok = false; break; }
-                    uint32_t dst = smem_u32(smem + kOffScale) + b * (kBatch * kScaleFloats * 4);
+                    uint32_t dst = smem_u32(smem + C::OFF_SCALE) + b * (kBatch * C::SCALES * 4);
                     if (!COLSCALE && lane < 2 * kBatch && kb0 + (lane >> 1) < kblocks) {
-                        // lane 2 u + h: half h's block of B at K block u
-                        cp_async4(dst + ((lane >> 1) * kScaleFloats + 128 + (lane & 1)) * 4,
+                        // lane 2 u + h: the h-th block of 128 columns at K block u
+                        cp_async4(dst + ((lane >> 1) * C::SCALES + 128 + (lane & 1)) * 4,
                                   p.B_sf + (static_cast<int64_t>(ti.group) * nb + min(ti.n0 / 128 + (lane & 1), nb - 1)) * kblocks +
                                       kb0 + (lane >> 1));
                     }
                     dst += lane * 4;
-                    for (int32_t kb = kb0; kb < min(kb0 + kBatch, kblocks); ++kb, dst += kScaleFloats * 4) {
+                    for (int32_t kb = kb0; kb < min(kb0 + kBatch, kblocks); ++kb, dst += C::SCALES * 4) {
                         const float *a = p.A_sf + static_cast<int64_t>(kb) * p.M;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) cp_async4(dst + i * 128, a + min(row + 32 * i, p.M - 1));
                         if (COLSCALE) {
                             const float *c = p.B_sf + static_cast<int64_t>(kb) * p.N;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
+                            for (int i = 0; i < TN / 32; ++i)
                                 cp_async4(dst + 512 + i * 128, c + min(ti.n0 + lane + 32 * i, p.N - 1));
                         }
                     }
@@ -351,98 +362,106 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             }
             if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
         } else if (rank == 0) {
-            // ------------------------------------------------ MMA issuers (leader): warp 1 sums the even K
-            // blocks of the whole sequence into slot 0, warp 2 the odd ones into slot 1
-            // the whole warp keeps count, one lane issues: descriptors stay in uniform registers
-            const uint32_t slot = warp - 1;
+            // ------------------------------------------------ MMA issuers (leader): warp 1 takes the even K
+            // blocks of the whole sequence, warp 2 the odd ones, the slots in turn, so that one looks at
+            // its barriers while the other's MMAs run.  The whole warp keeps count and one lane issues:
+            // descriptors stay in uniform registers.
+            const uint32_t first = warp - 1;
             const uint64_t a_desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
-            const uint64_t b_desc0 = smem_desc(smem_u32(smem) + kOpBytes, 16, 1024, kSwizzle128B);
-            const uint32_t idesc = idesc_f8(256, 256, p.a_type, p.b_type);
-            uint32_t s = slot, phase = 0, acc_phase = 1;
+            const uint64_t b_desc0 = smem_desc(smem_u32(smem) + kABytes, 16, 1024, kSwizzle128B);
+            const uint32_t idesc = idesc_f8(256, TN, p.a_type, p.b_type);
+            uint32_t s = first, phase = 0, slot = first, acc_phase = 1;
             bool ok = true;
             const int64_t mine = pair_id < total_tiles ? (total_tiles - pair_id + npairs - 1) / npairs : 0;
             const int64_t count = mine * kblocks;
-            for (int64_t j = slot; j < count; j += 2) {
+            for (int64_t j = first; j < count; j += 2) {
                 if (!mbar_wait_warp(smem_u32(&full[s]), phase) ||
                     !mbar_wait_warp(smem_u32(&acc_empty[slot]), acc_phase)) { ok = false; break; }
                 tc_fence_after();
                 if (elect_one_sync()) {
-                    const uint64_t ad = a_desc0 + s * static_cast<uint64_t>(kStageBytes >> 4);
-                    const uint64_t bd = b_desc0 + s * static_cast<uint64_t>(kStageBytes >> 4);
+                    const uint64_t ad = a_desc0 + s * static_cast<uint64_t>(C::STAGE >> 4);
+                    const uint64_t bd = b_desc0 + s * static_cast<uint64_t>(C::STAGE >> 4);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_f8_pair(tmem_base + slot * 256, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+                        tc_mma_f8_pair(tmem_base + slot * TN, ad + 2 * kk, bd + 2 * kk, idesc, kk > 0 ? 1u : 0u);
                     tc_commit_pair(smem_u32(&acc_full[slot]), 0x3);
                     tc_commit_pair(smem_u32(&empty[s]), 0x3);
                 }
                 __syncwarp();
-                acc_phase ^= 1;
+                slot += 2;
+                if (slot >= C::SLOTS) { slot = first; acc_phase ^= 1; }
                 s += 2;
-                if (s >= kStages) { s -= kStages; phase ^= 1; }
+                if (s >= C::STAGES) { s -= C::STAGES; phase ^= 1; }
             }
             if (!ok && lane == 0) { record_timeout(); *abort_flag = 1; }
         }
     } else {
         setmaxnreg_inc<232>();
-        // ------------------------------------------------ epilogue: eight warps, each 32 rows x 128 columns
+        // ------------------------------------------------ epilogue: eight warps, each 32 rows x TN / 2 columns
         const int quad = warp & 3;
         const int half = (warp - 4) >> 2;
         const uint32_t release = mapa_shared(smem_u32(&acc_empty[0]), 0);
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
-        uint8_t *out = smem + kOffOut + (warp - 4) * kBoxes * kBoxBytes;
-        const float *s_scale = reinterpret_cast<const float *>(smem + kOffScale);
+        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + half * C::COLS;
+        uint8_t *out = smem + C::OFF_OUT + (warp - 4) * C::BOXES * kBoxBytes;
+        const float *s_scale = reinterpret_cast<const float *>(smem + C::OFF_SCALE);
         uint32_t slot = 0, phase = 0, b = 0, sc_phase = 0;
         bool ok = true;
         for (int32_t t = pair_id; t < total_tiles && ok; t += npairs) {
             const Tile ti = tile_info(t);
-            const int32_t c0 = ti.n0 + half * 128;
-            float acc[128];
+            const int32_t c0 = ti.n0 + half * C::COLS;
+            float acc[C::COLS];
 #pragma unroll
-            for (int i = 0; i < 128; ++i) acc[i] = 0.0f;
+            for (int i = 0; i < C::COLS; ++i) acc[i] = 0.0f;
             bool ready = false;         // the next slot's sum is known to be complete
             int u = 0;
             for (int32_t kb = 0; kb < kblocks; ++kb) {
                 if (u == 0 && !mbar_wait_warp(smem_u32(&sc_full[b]), sc_phase)) { ok = false; break; }
                 if (!ready && !mbar_wait_warp(smem_u32(&acc_full[slot]), phase)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t src = taddr + slot * 256;
+                const uint32_t src = taddr + slot * TN;
                 bool done = false;
+                const float *sc = s_scale + (b * kBatch + u) * C::SCALES;
+                auto give_back = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(release + slot * 8);
+                    if (++slot == C::SLOTS) { slot = 0; phase ^= 1; }
+                    done = mbar_test(smem_u32(&acc_full[slot]), phase);
+                };
                 uint32_t v[2][32];
                 tmem_ld_32x32b_x32(src, v[0]);
                 tmem_ld_32x32b_x32(src + 32, v[1]);
-                const float *sc = s_scale + (b * kBatch + u) * kScaleFloats;
-                const float sm = COLSCALE ? sc[quad * 32 + lane] : sc[quad * 32 + lane] * sc[128 + half];
+                const float sm = COLSCALE ? sc[quad * 32 + lane] : sc[quad * 32 + lane] * sc[128 + (TN == 256 ? half : 0)];
                 auto add32 = [&](const uint32_t (&x)[32], int c) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 32; i += 4) {
                         float f[4] = {sm, sm, sm, sm};
                         if (COLSCALE) {
-                            const float4 q = *reinterpret_cast<const float4 *>(sc + 128 + half * 128 + c * 32 + 4 * i);
+                            const float4 q = *reinterpret_cast<const float4 *>(sc + 128 + half * C::COLS + c * 32 + i);
                             unpack_f32x2(mul_f32x2(pack_f32x2(q.x, q.y), pack_f32x2(sm, sm)), f[0], f[1]);
                             unpack_f32x2(mul_f32x2(pack_f32x2(q.z, q.w), pack_f32x2(sm, sm)), f[2], f[3]);
                         }
 #pragma unroll
                         for (int z = 0; z < 4; ++z)
-                            acc[c * 32 + 4 * i + z] = fmaf(f[z], __uint_as_float(x[4 * i + z]), acc[c * 32 + 4 * i + z]);
+                            acc[c * 32 + i + z] = fmaf(f[z], __uint_as_float(x[i + z]), acc[c * 32 + i + z]);
                     }
                 };
                 tmem_ld_wait();
                 tmem_regs_after_wait(v[0]);
                 tmem_regs_after_wait(v[1]);
-                add32(v[0], 0);
-                tmem_ld_32x32b_x32(src + 64, v[0]);
-                add32(v[1], 1);
-                tmem_ld_32x32b_x32(src + 96, v[1]);
-                tmem_ld_wait();
-                tmem_regs_after_wait(v[0]);
-                tmem_regs_after_wait(v[1]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(release + slot * 8);
-                if (++slot == kSlots) { slot = 0; phase ^= 1; }
-                done = mbar_test(smem_u32(&acc_full[slot]), phase);
-                add32(v[0], 2);
-                add32(v[1], 3);
+                if constexpr (TN == 256) {
+                    // the second half's loads run under the first half's additions
+                    add32(v[0], 0);
+                    tmem_ld_32x32b_x32(src + 64, v[0]);
+                    add32(v[1], 1);
+                    tmem_ld_32x32b_x32(src + 96, v[1]);
+                    tmem_ld_wait();
+                    tmem_regs_after_wait(v[0]);
+                    tmem_regs_after_wait(v[1]);
+                }
+                give_back();
+                add32(v[0], TN == 256 ? 2 : 0);
+                add32(v[1], TN == 256 ? 3 : 1);
                 ready = __all_sync(0xffffffffu, done) && kb + 1 < kblocks;
                 if (++u == kBatch || kb == kblocks - 1) {
                     u = 0;
@@ -453,15 +472,14 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 }
             }
             if (!ok) break;
-            // D leaves in boxes of 32 rows x 32 bytes through two staging boxes of the warp's own: by
-            // TMA where D's rows are 16-byte aligned and the box's rows are all this tile's (rows
-            // beyond M are clipped by the map), else in four-byte or single pieces
+            // D leaves by TMA where its rows are 16-byte aligned and the warp's 32 rows are all this
+            // tile's (rows beyond M are clipped by the map), else in four-byte or single pieces
             const int32_t wrow0 = ti.row0 + 128 * static_cast<int32_t>(rank) + quad * 32;
             const int32_t rows = ti.row_end - wrow0;
             if (rows > 0 && c0 < p.N) {
                 const bool by_tma = p.store_map && (!GROUPED || rows >= 32);
-                if (p.fp32) store_tile<true>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
-                else store_tile<false>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
+                if (p.fp32) store_tile<true, C::COLS, C::BOXES>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
+                else store_tile<false, C::COLS, C::BOXES>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
             }
             __syncwarp();
         }
@@ -491,14 +509,15 @@ bool types_ok(int a_type, int b_type, int out_type)
            (out_type == QFP4_BF16 || out_type == QFP4_FP32);
 }
 
-template <bool GROUPED, bool COLSCALE>
+template <bool GROUPED, bool COLSCALE, int TN>
 int launch_pair(Fp8Params p, int64_t tiles, cudaStream_t s)
 {
-    auto kern = gemm_fp8_pair_kernel<GROUPED, COLSCALE>;
+    using C = PairCfg<TN>;
+    auto kern = gemm_fp8_pair_kernel<GROUPED, COLSCALE, TN>;
     CUtensorMap ma, mb, md;
-    int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), kPairSmem);
+    int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM);
     if (rc == QFP4_OK) rc = make_map_direct(&ma, p.A, p.K, p.M, 128, 128);
-    if (rc == QFP4_OK) rc = make_map_direct(&mb, p.B, p.K, static_cast<uint64_t>(GROUPED ? p.groups : 1) * p.N, 128, 128);
+    if (rc == QFP4_OK) rc = make_map_direct(&mb, p.B, p.K, static_cast<uint64_t>(GROUPED ? p.groups : 1) * p.N, 128, TN / 2);
     p.store_map = p.N % (p.fp32 ? 4 : 8) == 0;
     if (rc == QFP4_OK && p.store_map) rc = make_map_store(&md, p.D, p.fp32 != 0, p.N, p.M, p.fp32 ? 32 : 64, 32);
     else md = ma;       // never used
@@ -506,14 +525,20 @@ int launch_pair(Fp8Params p, int64_t tiles, cudaStream_t s)
     const int sms = sm_count();
     if (sms < 2) return QFP4_ERR_CUDA;
     const int64_t pairs = tiles < sms / 2 ? tiles : sms / 2;
-    return launch_status(launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kPairThreads), kPairSmem, s,
+    return launch_status(launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kPairThreads), C::SMEM, s,
                                     ma, mb, md, p));
+}
+
+template <int TN>
+int launch_width(const Fp8Params &p, int64_t tiles, cudaStream_t s)
+{
+    if (p.groups) return launch_pair<true, false, TN>(p, tiles, s);
+    return p.b_rows == 1 ? launch_pair<false, true, TN>(p, tiles, s) : launch_pair<false, false, TN>(p, tiles, s);
 }
 
 int launch_gemm_fp8(const Fp8Params &p, cudaStream_t s)
 {
     if (gemm_fp8_small_pays(p)) return launch_gemm_fp8_small(p, s);
-    const int64_t tiles_n = (static_cast<int64_t>(p.N) + 255) / 256;
     int64_t tiles_m = (static_cast<int64_t>(p.M) + 255) / 256;
     if (p.groups) {
         // every group may add one partial tile, and none has more than max_group_rows rows
@@ -521,10 +546,18 @@ int launch_gemm_fp8(const Fp8Params &p, cudaStream_t s)
         const int64_t by_max = static_cast<int64_t>(p.groups) * ((p.max_group_rows + 255) / 256);
         if (p.max_group_rows > 0 && by_max < tiles_m) tiles_m = by_max;
     }
-    const int64_t tiles = tiles_m * tiles_n;
-    if (tiles > INT32_MAX) return QFP4_ERR_UNSUPPORTED;
-    if (p.groups) return launch_pair<true, false>(p, tiles, s);
-    return p.b_rows == 1 ? launch_pair<false, true>(p, tiles, s) : launch_pair<false, false>(p, tiles, s);
+    const int64_t wide = tiles_m * ((static_cast<int64_t>(p.N) + 255) / 256);
+    const int64_t narrow = tiles_m * ((static_cast<int64_t>(p.N) + 127) / 128);
+    if (narrow > INT32_MAX / 2) return QFP4_ERR_UNSUPPORTED;
+    const int64_t pairs = sm_count() / 2;
+    if (pairs < 1) return QFP4_ERR_CUDA;
+    // Tiles 128 columns wide cost 0.55 to 0.6 of the time of one 256 wide (0.7
+    // with column scales), so they pay where they fill the last round better:
+    // 1531 x 4100 x 2000 takes 21.1 us in three rounds of narrow tiles and
+    // 22.6 in two of wide ones; 4096 x 4096 x 14336 223 in seven, 210 in four.
+    const int64_t narrow_cost = (narrow + pairs - 1) / pairs * (p.b_rows == 1 ? 7 : 6);
+    return narrow_cost < (wide + pairs - 1) / pairs * 10 ? launch_width<128>(p, narrow, s)
+                                                         : launch_width<256>(p, wide, s);
 }
 
 }  // namespace

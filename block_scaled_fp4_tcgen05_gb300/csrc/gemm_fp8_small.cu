@@ -86,11 +86,14 @@ __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr)
 }
 
 // PER_ROW: B has one scale per row (b_rows = 1), else one per 128 rows.
+// GROUPED: one product per expert, each with its own tiles of up to max_rows
+// rows; a CTA (a whole cluster) whose tile its expert does not reach leaves at
+// once.
 // tmM, tmN: maps of the operands in the MMA's M and N slots.
-template <int NT, bool PER_ROW>
+template <int NT, bool PER_ROW, bool GROUPED>
 __global__ void __launch_bounds__(SmallCfg<NT>::THREADS, SmallCfg<NT>::CTAS)
 gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_constant__ CUtensorMap tmN,
-                      const Fp8Params p, const int splits)
+                      const Fp8Params p, const int splits, const int32_t max_rows)
 {
     using C = SmallCfg<NT>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -109,7 +112,24 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
     const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int32_t tiles_n = (p.N + 127) / 128;
     const int32_t tile = blockIdx.x / splits;
-    const int32_t n0 = (tile % tiles_n) * 128, m0 = (tile / tiles_n) * NT;
+    const int32_t n0 = (tile % tiles_n) * 128;
+    // rows [m0, m_end) of A, and where B's row and block n0 lie
+    int32_t m0 = (tile / tiles_n) * NT, m_end = p.M, group = 0;
+    if (GROUPED) {
+        const int32_t tiles_m = (max_rows + NT - 1) / NT;
+        group = tile / (tiles_n * tiles_m);
+        m0 = (tile / tiles_n % tiles_m) * NT;
+        pdl_wait();
+        const bool bad = __syncthreads_or(threadIdx.x < p.groups &&
+                                          !fp8_offsets_valid(p.row_offsets, threadIdx.x, p.groups, p.M, p.max_group_rows));
+        if (bad && threadIdx.x == 0 && blockIdx.x == 0)
+            atomicOr(&g_status_gemm_fp8_small, static_cast<uint32_t>(kStatusBadGroup));
+        m0 += p.row_offsets[group];
+        m_end = p.row_offsets[group + 1];
+        if (bad || m0 >= m_end) return;
+    }
+    const int32_t wrow = group * p.N + n0;
+    const float *b_sf = p.B_sf + (PER_ROW ? 0 : (static_cast<int64_t>(group) * tiles_n + n0 / 128) * ((p.K + 127) / 128));
     const int32_t kblocks = (p.K + 127) / 128;
     const int32_t kb0 = static_cast<int32_t>(static_cast<int64_t>(rank) * kblocks / splits);
     const int32_t nkb = static_cast<int32_t>(static_cast<int64_t>(rank + 1) * kblocks / splits) - kb0;
@@ -140,7 +160,7 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
-    pdl_wait();
+    if (!GROUPED) pdl_wait();
     pdl_launch_dependents();
 
     if (warp == 0) {
@@ -152,8 +172,8 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
                 if (!mbar_wait(smem_u32(&empty[s]), phase)) { ok = false; break; }
                 const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(smem + s * C::STAGE);
                 mbar_arrive_expect_tx(bar, C::STAGE);
-                tma_load_2d(dst, &tmM, bar, (kb0 + j) * 128, C::SWAP ? n0 : m0);
-                tma_load_2d(dst + C::M_BYTES, &tmN, bar, (kb0 + j) * 128, C::SWAP ? m0 : n0);
+                tma_load_2d(dst, &tmM, bar, (kb0 + j) * 128, C::SWAP ? wrow : m0);
+                tma_load_2d(dst + C::M_BYTES, &tmN, bar, (kb0 + j) * 128, C::SWAP ? m0 : wrow);
                 if (++s == C::STAGES) { s = 0; phase ^= 1; }
             }
             if (!ok) { record_timeout(); *abort_flag = 1; }
@@ -210,7 +230,7 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
                     for (int i = 0; i < kBrows / 32; ++i)
                         cp_async4(dst + kBt + 128 * i, p.B_sf + kb * p.N + min(n0 + lane + 32 * i, p.N - 1));
                 } else if (lane == 0) {
-                    cp_async4(dst + kBt, p.B_sf + static_cast<int64_t>(n0 / 128) * kblocks + kb);
+                    cp_async4(dst + kBt, b_sf + kb);
                 }
             }
             cp_async_arrive(smem_u32(&sc_full[b]));
@@ -308,7 +328,7 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
         tmem_dealloc(tmem_base, C::TMEM_COLS);
     }
     // a CTA that gave up leaves undefined sums; the status word says so
-    const int32_t tokens = min(NT, p.M - m0);
+    const int32_t tokens = min(NT, m_end - m0);
     const int32_t n = n0 + 4 * lane;
     for (int32_t t = rank + splits * warp; t < tokens; t += splits * (C::THREADS / 32)) {
         const uint32_t piece = (t * 32 + (C::SWAP ? lane : lane ^ (t & 31))) * 16;
@@ -367,17 +387,17 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
     }
 }
 
-template <int NT, bool PER_ROW>
-int launch(const Fp8Params &p, int splits, cudaStream_t s)
+template <int NT, bool PER_ROW, bool GROUPED>
+int launch(const Fp8Params &p, int64_t tiles, int splits, int32_t max_rows, cudaStream_t s)
 {
     using C = SmallCfg<NT>;
-    auto kern = gemm_fp8_small_kernel<NT, PER_ROW>;
+    auto kern = gemm_fp8_small_kernel<NT, PER_ROW, GROUPED>;
     CUtensorMap mm, mn;
     int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM);
-    if (rc == QFP4_OK) rc = make_map_direct(C::SWAP ? &mm : &mn, p.B, p.K, p.N, 128, 128);
+    const uint64_t b_rows = static_cast<uint64_t>(GROUPED ? p.groups : 1) * p.N;
+    if (rc == QFP4_OK) rc = make_map_direct(C::SWAP ? &mm : &mn, p.B, p.K, b_rows, 128, 128);
     if (rc == QFP4_OK) rc = make_map_direct(C::SWAP ? &mn : &mm, p.A, p.K, p.M, 128, NT);
     if (rc != QFP4_OK) return rc;
-    const int64_t tiles = static_cast<int64_t>((p.N + 127) / 128) * ((p.M + NT - 1) / NT);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
     cfg.blockDim = dim3(C::THREADS);
@@ -392,40 +412,52 @@ int launch(const Fp8Params &p, int splits, cudaStream_t s)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = splits > 1 ? 2 : 1;
-    return launch_status(cudaLaunchKernelEx(&cfg, kern, mm, mn, p, splits));
+    return launch_status(cudaLaunchKernelEx(&cfg, kern, mm, mn, p, splits, max_rows));
 }
 
 template <int NT>
-int launch_nt(const Fp8Params &p, int splits, cudaStream_t s)
+int launch_nt(const Fp8Params &p, int64_t tiles, int splits, int32_t max_rows, cudaStream_t s)
 {
-    return p.b_rows == 1 ? launch<NT, true>(p, splits, s) : launch<NT, false>(p, splits, s);
+    if (p.groups) return launch<NT, false, true>(p, tiles, splits, max_rows, s);
+    return p.b_rows == 1 ? launch<NT, true, false>(p, tiles, splits, max_rows, s)
+                         : launch<NT, false, false>(p, tiles, splits, max_rows, s);
 }
 
-int tokens_of(const Fp8Params &p) { return p.M <= 16 ? 16 : p.M <= 32 ? 32 : 128; }
+// Rows of A (of any group) that the launch has to cover.
+int64_t most_rows(const Fp8Params &p)
+{
+    return p.groups && p.max_group_rows > 0 && p.max_group_rows < p.M ? p.max_group_rows : p.M;
+}
 
 }  // namespace
 
+// Up to 128 rows always (per group, as far as the host can tell); more where
+// the 256 x 256 tiles would take up less than half of the SMs (512 x 4096 x
+// 4096, 32 such tiles on 76 pairs: 13.8 us here; 64 tiles: 19 us there).
 bool gemm_fp8_small_pays(const Fp8Params &p)
 {
-    if (p.groups) return false;
-    if (p.M <= 128) return true;
+    if (most_rows(p) <= 128) return true;
     const int64_t pairs = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + 255) / 256);
-    return pairs < sm_count() / 4;
+    return !p.groups && pairs < sm_count() / 4;
 }
 
 int launch_gemm_fp8_small(const Fp8Params &p, cudaStream_t s)
 {
-    const int nt = tokens_of(p);
-    const int64_t tiles = static_cast<int64_t>((p.N + 127) / 128) * ((p.M + nt - 1) / nt);
+    const int64_t rows = most_rows(p);
+    const int nt = rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+    const int64_t tiles = static_cast<int64_t>((p.N + 127) / 128) * ((rows + nt - 1) / nt) * (p.groups ? p.groups : 1);
     const int64_t kblocks = (static_cast<int64_t>(p.K) + 127) / 128;
+    // split K while the CTAs still fit on the GPU at once (two per SM for few
+    // rows) and each keeps two K blocks or more
     const int64_t room = static_cast<int64_t>(sm_count()) * (nt == 128 ? 1 : 2);
     if (tiles > INT32_MAX / kMaxSplits) return QFP4_ERR_UNSUPPORTED;
     int splits = 1;
-    while (splits < kMaxSplits && tiles * splits * 2 <= room && kblocks >= 2 * splits) splits *= 2;
+    while (splits < kMaxSplits && tiles * splits * 2 <= room && kblocks >= 4 * splits) splits *= 2;
+    const int32_t max_rows = static_cast<int32_t>(rows);
     switch (nt) {
-    case 16: return launch_nt<16>(p, splits, s);
-    case 32: return launch_nt<32>(p, splits, s);
-    default: return launch_nt<128>(p, splits, s);
+    case 16: return launch_nt<16>(p, tiles, splits, max_rows, s);
+    case 32: return launch_nt<32>(p, tiles, splits, max_rows, s);
+    default: return launch_nt<128>(p, tiles, splits, max_rows, s);
     }
 }
 

@@ -6,6 +6,8 @@
 
 namespace qfp4 {
 
+constexpr int kMaxGroups = 256;
+
 struct Fp8Params {
     const uint8_t *A, *B;
     const float *A_sf, *B_sf;
@@ -19,8 +21,18 @@ struct Fp8Params {
     int32_t store_map;              // D can be written by TMA (rows 16-byte aligned)
 };
 
+// Row offsets a grouped product can use: from 0, never decreasing, at most
+// total_rows, no group above max_rows (0 = no bound).  Group e's part of that.
+__device__ __forceinline__ bool fp8_offsets_valid(const int32_t *offs, int e, int groups, int32_t total_rows,
+                                                  int32_t max_rows)
+{
+    const int64_t rows = static_cast<int64_t>(offs[e + 1]) - offs[e];
+    return (e > 0 || offs[0] == 0) && (e < groups - 1 || offs[groups] <= total_rows) && rows >= 0 &&
+           (max_rows == 0 || rows <= max_rows);
+}
+
 // Small products (few tiles of 256 x 256): tiles of 128 rows of B x up to 128
-// rows of A, K split over the CTAs of a cluster.  Dense only.
+// rows of A, K split over the CTAs of a cluster.
 bool gemm_fp8_small_pays(const Fp8Params &p);
 int launch_gemm_fp8_small(const Fp8Params &p, cudaStream_t s);
 int read_clear_status_gemm_fp8_small(cudaStream_t s, uint32_t *out);
