@@ -10,12 +10,15 @@
 //   chosen experts; g = p: [chosen] p_i dg_i - p_i sum_j p_j dg_j.
 //
 // Forward, two launches (one for few tokens).  route_rows_kernel: CTA c takes a
-// contiguous range of tokens, a warp one token at a time with its logits in
-// registers (lane l holds experts l, l + 32, ...): softmax, then k rounds of
-// top-k on order-preserving integer keys.  A lane keeps the best of its own
-// keys, so a round is one warp-wide maximum, a vote for the lane that holds it
-// and that lane's next best.  A lane adds up its experts' p over the warp's
-// tokens in registers.  The CTA's counts and its sum of p go to the workspace.
+// contiguous range of tokens.  Instructions bound it, and most of them would be
+// the k rounds of top-k, so a round serves several tokens at once: G lanes (4,
+// 8 or 16) share a token, each with up to 16 of its logits in registers.  Keys
+// are integers in the order of the logits; a lane keeps its best and second
+// best, so a round is a maximum over the G lanes, a vote for the lane that
+// holds it and that lane's next best (757 instructions per token of 256 experts
+// with a warp to itself, 18 us for 16384 of them).  A lane adds up its experts'
+// p over its tokens in registers.  The CTA's counts and its sum of p go to the
+// workspace.
 // route_place_kernel: each CTA adds up the counts of all ranges, so it knows
 // where each expert's rows begin and how many of them come from earlier
 // ranges, and ranks its own pairs in order; one more CTA writes the totals and
@@ -31,10 +34,10 @@ namespace {
 
 constexpr int kMaxExperts = 256;
 constexpr int kMaxTopk = 16;
-constexpr int kWarps = 32;
+constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxRowWarps = 32;            // of the CTAs that read the logits: 16, or 32 where a warp has one token
 constexpr int kMaxChunks = 152;             // one CTA on each SM
-constexpr int64_t kOneCta = 128;            // tokens that one CTA takes in one launch
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;
 
@@ -105,116 +108,168 @@ struct RouteShared {
     int32_t before[kMaxExperts];                    // rows of it that earlier ranges fill
     int32_t total[kMaxExperts];
     union {
-        float prob[kWarps][kMaxExperts];            // sums of p per warp
-        int32_t row[kWarps][kMaxExperts];           // counts, then next row, of each warp's pairs
-        int4 part[2][kThreads];                     // partial sums over ranges, four experts each
-        float ppart[kThreads];
+        float prob[kMaxRowWarps][kMaxExperts];      // sums of p per warp
+        struct {
+            int32_t row[kWarps][kMaxExperts];       // counts, then next row, of each warp's pairs
+            union {
+                int4 part[2][kThreads];             // partial sums over ranges, four experts each
+                float ppart[kThreads];
+            };
+        };
     };
     int32_t valid;
     int32_t rows;                                   // rows of all experts
 };
 
-// Choices, gates and counts of tokens [t0, t1), and the warps' sums of p.
-template <typename L, int V>
+// Choices, gates and counts of tokens [t0, t1), and the warps' sums of p; by
+// WARPS warps.  G lanes per token, V experts per lane: lane l of the G has
+// experts l, l + G, ...
+template <typename L, int G, int V, int WARPS>
 __device__ __forceinline__ void route_rows(const RouteParams &p, int64_t t0, int64_t t1, RouteShared &sh)
 {
+    constexpr int kTokens = 32 / G;                     // tokens of a warp at a time
+    constexpr int kHold = (kMaxTopk + G - 1) / G;       // choices that a lane keeps: l, l + G, ...
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float psum[V], l[V], ahead[V];
+    const int l = lane % G, first = lane - l;
+    float psum[V], ahead[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) psum[v] = 0.0f;
     int nvalid = 0;
-    auto load_row = [&](int64_t t, float (&d)[V]) {
-        if (t < t1) {
-            const L *row = static_cast<const L *>(p.logits) + t * p.E;
+    auto load_row = [&](int64_t t) {
+        const L *row = static_cast<const L *>(p.logits) + t * p.E + l;
 #pragma unroll
-            for (int v = 0; v < V; ++v) d[v] = lane + 32 * v < p.E ? load_logit(row + lane + 32 * v) : -INFINITY;
-        }
+        for (int v = 0; v < V; ++v) ahead[v] = t < t1 && l + G * v < p.E ? load_logit(row + G * v) : -INFINITY;
     };
-    load_row(t0 + warp, ahead);
-    for (int64_t t = t0 + warp; t < t1; t += kWarps) {
+    auto group_sum = [](float x) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) l[v] = ahead[v];
-        load_row(t + kWarps, ahead);        // the next token's logits come while this one is worked on
-        int32_t my_id = -1;
-        float my_gate = 0.0f;
-        if (!p.valid || p.valid[t] != 0) {
-            ++nvalid;
-            // the lane's best and second best key and their places (equal keys: the lowest expert first)
-            uint32_t key[V], best = 0u, second = 0u;
-            int at = 0, then = 0;
+        for (int d = G / 2; d > 0; d >>= 1) x = __fadd_rn(x, __shfl_xor_sync(kFull, x, d));
+        return x;
+    };
+    load_row(t0 + warp * kTokens + lane / G);
+    for (int64_t tw = t0 + warp * kTokens; tw < t1; tw += WARPS * kTokens) {
+        const int64_t t = tw + lane / G;
+        const bool here = t < t1;
+        const bool valid = here && (!p.valid || p.valid[t] != 0);
+        if (valid && l == 0) ++nvalid;
+        float x[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = __fadd_rn(ahead[v], 0.0f);
+        load_row(t + WARPS * kTokens);      // the next tokens' logits come while these are worked on
+        // the lane's best and second best key and their places (equal keys: the lowest expert first)
+        uint32_t best = 0u, second = 0u;
+        int at = 0, then = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t key = sort_key(x[v]);
+            const bool b = key > best, c = key > second;
+            second = b ? best : c ? key : second;
+            then = b ? at : c ? v : then;
+            best = b ? key : best;
+            at = b ? v : at;
+        }
+        bool known = true;                      // second is the lane's next best
+        auto group_max = [](uint32_t k) {
+            if constexpr (G == 32) {
+                k = __reduce_max_sync(kFull, k);
+            } else {
+#pragma unroll
+                for (int d = G / 2; d > 0; d >>= 1) k = max(k, __shfl_xor_sync(kFull, k, d));
+            }
+            return k;
+        };
+        uint32_t top = group_max(best);
+        const float base = softmax_base(top);
+        float sum = 0.0f, chosen = 0.0f;
+        {
+            float e[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                key[v] = sort_key(l[v]);
-                if (key[v] > best) {
-                    second = best;
-                    then = at;
-                    best = key[v];
-                    at = v;
-                } else if (V > 1 && key[v] > second) {
-                    second = key[v];
-                    then = v;
-                }
+                e[v] = __expf(x[v] - base);     // (0 where there is no expert: its logit is -inf)
+                sum += e[v];
             }
-            bool known = true;              // second is the lane's next best
-            uint32_t top = __reduce_max_sync(kFull, best);
-            const float base = softmax_base(top);
-            float x[V];
-            const float inv = softmax_terms<V>(l, p.E, lane, base, x);
+            sum = group_sum(sum);
+            // tokens that are not valid add nothing, whatever their logits hold
+            const float inv = !valid || sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
 #pragma unroll
-            for (int v = 0; v < V; ++v) psum[v] = fmaf(x[v], inv, psum[v]);
-            for (int j = 0; j < p.topk; ++j) {
-                if (j > 0) top = __reduce_max_sync(kFull, best);
-                if (top <= kKeyNegInf) break;
-                uint32_t who = __ballot_sync(kFull, best == top);
-                uint32_t e = lane + 32 * at;
-                if (who & (who - 1)) {          // equal keys on several lanes: the lowest expert
-                    const uint32_t low = __reduce_min_sync(kFull, best == top ? e : 0xFFFFFFFFu);
-                    who = 1u << (low & 31u);
+            for (int v = 0; v < V; ++v) psum[v] = valid ? fmaf(e[v], inv, psum[v]) : psum[v];
+            sum = inv;
+        }
+        int32_t my_id[kHold];
+        float my_x[kHold];
+#pragma unroll
+        for (int h = 0; h < kHold; ++h) {
+            my_id[h] = -1;
+            my_x[h] = 0.0f;
+#pragma unroll 1
+            for (int i = 0; i < G; ++i) {
+                if (h * G + i >= p.topk) break;
+                if (h + i > 0) top = group_max(best);
+                const bool open = valid && top > kKeyNegInf;
+                if (G == 32 && !open) break;        // (the whole warp's token)
+                uint32_t who = __ballot_sync(kFull, best == top) >> first & (kFull >> (32 - G));
+                uint32_t e = l + G * at;
+                const bool several = open && (who & (who - 1u)) != 0;
+                if (G == 32 ? several : __any_sync(kFull, several)) {
+                    // equal keys on several lanes: the lowest expert
+                    uint32_t low = best == top ? e : 0xFFFFFFFFu;
+#pragma unroll
+                    for (int d = G / 2; d > 0; d >>= 1) low = min(low, __shfl_xor_sync(kFull, low, d));
+                    who = 1u << (low % G);
                 }
                 const int src = __ffs(who) - 1;
-                e = __shfl_sync(kFull, e, src);
-                if (lane == j) my_id = static_cast<int32_t>(e);
-                if (lane == src) {
-                    if (V == 1) {
-                        best = 0u;
-                    } else {
-                        if (!known) {           // the lane's third and later: the largest after (best, at)
-                            second = 0u;
+                e = __shfl_sync(kFull, e, src, G);
+                const float xe = open ? __expf(key_value(top) - base) : 0.0f;
+                chosen = __fadd_rn(chosen, xe);
+                if (l == i) {
+                    my_id[h] = open ? static_cast<int32_t>(e) : -1;
+                    my_x[h] = xe;
+                }
+                const bool mine = l == src;
+                if (mine && !known) {           // the lane's third and later: the largest after (best, at)
+                    second = 0u;
 #pragma unroll
-                            for (int v = 0; v < V; ++v)
-                                if ((key[v] < best || (key[v] == best && v > at)) && key[v] > second) {
-                                    second = key[v];
-                                    then = v;
-                                }
+                    for (int v = 0; v < V; ++v) {
+                        const uint32_t key = sort_key(x[v]);
+                        if ((key < best || (key == best && v > at)) && key > second) {
+                            second = key;
+                            then = v;
                         }
-                        known = false;
-                        best = second;
-                        at = then;
                     }
                 }
+                best = mine ? second : best;
+                at = mine ? then : at;
+                known = known && !mine;
             }
-            float my_x = 0.0f;
-            if (my_id >= 0) my_x = __expf(load_logit(static_cast<const L *>(p.logits) + t * p.E + my_id) - base);
-            const float scale = p.renorm ? warp_sum(my_x) : 0.0f;
-            my_gate = my_id < 0 ? 0.0f : p.renorm ? (scale == 0.0f ? 0.0f : __fdiv_rn(my_x, scale)) : my_x * inv;
-            if (my_id >= 0) atomicAdd(&sh.counts[my_id], 1);
         }
-        if (lane < p.topk) {
-            p.ids[t * p.topk + lane] = my_id;
-            p.gates[t * p.topk + lane] = my_gate;
+        const float scale = !p.renorm ? sum : chosen == 0.0f ? 0.0f : __fdiv_rn(1.0f, chosen);
+#pragma unroll
+        for (int h = 0; h < kHold; ++h) {
+            const int j = h * G + l;
+            if (here && j < p.topk) {
+                p.ids[t * p.topk + j] = my_id[h];
+                p.gates[t * p.topk + j] = my_x[h] * scale;
+                if (my_id[h] >= 0) atomicAdd(&sh.counts[my_id[h]], 1);
+            }
         }
     }
+    // the warp's tokens side by side, in order
 #pragma unroll
-    for (int v = 0; v < V; ++v) sh.prob[warp][lane + 32 * v] = psum[v];
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int d = G; d < 32; d <<= 1) psum[v] = __fadd_rn(psum[v], __shfl_xor_sync(kFull, psum[v], d));
+        if (lane < G && l + G * v < kMaxExperts) sh.prob[warp][l + G * v] = psum[v];
+    }
+    nvalid = __reduce_add_sync(kFull, nvalid);
     if (lane == 0) atomicAdd(&sh.valid, nvalid);
 }
 
 // Sum of expert e's p over the warps of this CTA.
+template <int WARPS>
 __device__ __forceinline__ float route_prob(const RouteShared &sh, int e)
 {
     float s = sh.prob[0][e];
 #pragma unroll 8
-    for (int w = 1; w < kWarps; ++w) s = __fadd_rn(s, sh.prob[w][e]);
+    for (int w = 1; w < WARPS; ++w) s = __fadd_rn(s, sh.prob[w][e]);
     return s;
 }
 
@@ -245,12 +300,10 @@ __device__ __forceinline__ void route_starts(const RouteParams &p, RouteShared &
 }
 
 // Rows of the pairs of tokens [t0, t1): after the experts' starts and the rows
-// that earlier ranges fill, in the pairs' order.  All threads; sh.row is free.
+// that earlier ranges fill, in the pairs' order.  All threads; sh.row is zero.
 __device__ __forceinline__ void route_place(const RouteParams &p, int64_t t0, int64_t t1, RouteShared &sh)
 {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    for (int f = tid; f < kWarps * kMaxExperts; f += kThreads) (&sh.row[0][0])[f] = 0;
-    __syncthreads();
     const int64_t f0 = t0 * p.topk, f1 = t1 * p.topk;
     const int64_t per_warp = ((f1 - f0 + kWarps - 1) / kWarps + 31) / 32 * 32;
     const int64_t w0 = min(f1, f0 + warp * per_warp), w1 = min(f1, w0 + per_warp);
@@ -314,8 +367,8 @@ __device__ __forceinline__ void route_totals(const RouteParams &p, RouteShared &
     }
 }
 
-template <typename L, int V>
-__global__ void __launch_bounds__(kThreads)
+template <typename L, int G, int V, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 1)
 route_rows_kernel(const RouteParams p)
 {
     __shared__ RouteShared sh;
@@ -326,10 +379,10 @@ route_rows_kernel(const RouteParams p)
     pdl_wait();
     pdl_launch_dependents();
     const int64_t t0 = min(p.T, blockIdx.x * p.chunk), t1 = min(p.T, t0 + p.chunk);
-    route_rows<L, V>(p, t0, t1, sh);
+    route_rows<L, G, V, WARPS>(p, t0, t1, sh);
     __syncthreads();
     if (tid < p.E) {
-        p.ws_prob[static_cast<int64_t>(blockIdx.x) * p.E + tid] = route_prob(sh, tid);
+        p.ws_prob[static_cast<int64_t>(blockIdx.x) * p.E + tid] = route_prob<WARPS>(sh, tid);
     }
     if (tid < (p.E + 3) / 4)
         reinterpret_cast<int4 *>(p.ws_counts)[blockIdx.x * ((p.E + 3) / 4) + tid] = reinterpret_cast<const int4 *>(sh.counts)[tid];
@@ -347,11 +400,12 @@ route_place_kernel(const RouteParams p, int chunks)
     const int e4 = (p.E + 3) / 4;
     const int width = e4 <= 8 ? 8 : e4 <= 16 ? 16 : e4 <= 32 ? 32 : 64;
     const int parts = kThreads / width, part = tid / width, e = tid % width;
+    for (int f = tid; f < kWarps * kMaxExperts; f += kThreads) (&sh.row[0][0])[f] = 0;
     pdl_wait();
     pdl_launch_dependents();
     int4 before = make_int4(0, 0, 0, 0), total = make_int4(0, 0, 0, 0);
     if (e < e4) {
-        constexpr int kLoads = (kMaxChunks + 15) / 16;          // (16 parts at 64 threads of width)
+        constexpr int kLoads = (kMaxChunks + 7) / 8;            // (8 parts at 64 threads of width)
         int4 n[kLoads];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -416,8 +470,8 @@ route_place_kernel(const RouteParams p, int chunks)
 }
 
 // Few tokens: the whole of it in one CTA.
-template <typename L, int V>
-__global__ void __launch_bounds__(kThreads)
+template <typename L, int G, int V>
+__global__ void __launch_bounds__(kThreads, 1)
 route_one_kernel(const RouteParams p)
 {
     __shared__ RouteShared sh;
@@ -430,14 +484,15 @@ route_one_kernel(const RouteParams p)
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
-    route_rows<L, V>(p, 0, p.T, sh);
+    route_rows<L, G, V, kWarps>(p, 0, p.T, sh);
     __syncthreads();
     float prob = 0.0f;
     if (tid < p.E) {
-        prob = route_prob(sh, tid);
+        prob = route_prob<kWarps>(sh, tid);
         sh.total[tid] = sh.counts[tid];
     }
     __syncthreads();
+    for (int f = tid; f < kWarps * kMaxExperts; f += kThreads) (&sh.row[0][0])[f] = 0;
     route_starts(p, sh);
     __syncthreads();
     for (int64_t r = sh.rows + tid; r < p.T * p.topk; r += kThreads) p.src[r] = -1;
@@ -532,11 +587,13 @@ route_backward_kernel(const BackParams p)
     }
 }
 
-template <typename L, int V>
+template <typename L, int G, int V>
 int launch_route(const RouteParams &p, int chunks, cudaStream_t s)
 {
-    if (p.T <= kOneCta) return launch_status(launch_pdl(route_one_kernel<L, V>, dim3(1), dim3(kThreads), 0, s, p));
-    const int rc = launch_status(launch_pdl(route_rows_kernel<L, V>, dim3(chunks), dim3(kThreads), 0, s, p));
+    constexpr int W = G == 32 ? 32 : 16;
+    // one CTA while each warp has two rounds of tokens at most
+    if (p.T <= 2 * kWarps * (32 / G)) return launch_status(launch_pdl(route_one_kernel<L, G, V>, dim3(1), dim3(kThreads), 0, s, p));
+    const int rc = launch_status(launch_pdl(route_rows_kernel<L, G, V, W>, dim3(chunks), dim3(32 * W), 0, s, p));
     if (rc != QFP4_OK) return rc;
     return launch_status(launch_pdl(route_place_kernel, dim3(chunks + 1), dim3(kThreads), 0, s, p, chunks));
 }
@@ -544,10 +601,11 @@ int launch_route(const RouteParams &p, int chunks, cudaStream_t s)
 template <typename L>
 int launch_forward(const RouteParams &p, int chunks, cudaStream_t s)
 {
-    if (p.E <= 32) return launch_route<L, 1>(p, chunks, s);
-    if (p.E <= 64) return launch_route<L, 2>(p, chunks, s);
-    if (p.E <= 128) return launch_route<L, 4>(p, chunks, s);
-    return launch_route<L, 8>(p, chunks, s);
+    if (p.E <= 16) return launch_route<L, 4, 4>(p, chunks, s);
+    if (p.E <= 32) return launch_route<L, 4, 8>(p, chunks, s);
+    if (p.E <= 64) return launch_route<L, 4, 16>(p, chunks, s);
+    if (p.E <= 128) return launch_route<L, 8, 16>(p, chunks, s);
+    return launch_route<L, 32, 8>(p, chunks, s);
 }
 
 template <typename L>
@@ -565,7 +623,7 @@ bool sizes_ok(int64_t T, int64_t E, int64_t topk)
     return E <= kMaxExperts && topk <= kMaxTopk && topk <= E && T <= INT32_MAX / topk;
 }
 
-// Tokens go in ranges of whole warps' rows, at most kMaxChunks of them.
+// Ranges of tokens: at least 32 each, at most kMaxChunks of them.
 int64_t chunk_count(int64_t T)
 {
     const int64_t n = (T + kWarps - 1) / kWarps;
@@ -627,7 +685,7 @@ extern "C" int qfp4_moe_route_backward(int logits_type, const void *logits, int6
     const BackParams p{logits, valid, T, static_cast<int32_t>(E), static_cast<int32_t>(topk), renorm ? 1 : 0,
                        ids, counts, n_valid, dgates, dloss, dlogits};
     const int64_t want = (T + kWarps - 1) / kWarps;
-    const unsigned ctas = static_cast<unsigned>(want < 2 * 152 ? want : 2 * 152);
+    const unsigned ctas = static_cast<unsigned>(want < 4 * 152 ? want : 4 * 152);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return logits_type == QFP4_BF16 ? launch_back<__nv_bfloat16>(p, ctas, s) : launch_back<float>(p, ctas, s);
 }
