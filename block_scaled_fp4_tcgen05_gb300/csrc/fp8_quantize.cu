@@ -55,7 +55,11 @@ struct QuantParams {
     int32_t tiles_k;            // 128-column tiles: ceil(K / 128)
     uint8_t *Q, *Q_t;
     float *SF, *SF_t;
+    const int32_t *row_offsets; // grouped: DEVICE [groups + 1]
+    int32_t groups;
 };
+
+constexpr int kMaxGroups = 256;
 
 template <int TYPE> struct Fp8;
 template <> struct Fp8<QFP4_E4M3> { static constexpr float top = 448.0f; };
@@ -103,13 +107,16 @@ enum { kRows = 1, kCols = 2, kBlock = 4 };
 // R rows per thread: the tile is 16 R rows x 128 columns.  Thread 16 i + c
 // holds rows R i .. R i + R - 1 and columns 8 c .. 8 c + 7 of the tile.
 // WHAT: kRows and / or kCols, or kBlock with or without kCols (R = 8).
-template <int TYPE, bool POW2, int WHAT, int R>
+// GROUPED: every group's rows begin a row tile of their own (WHAT has kCols).
+template <int TYPE, bool POW2, int WHAT, int R, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, R == 8 ? 3 : 6)
 fp8_quantize_kernel(const QuantParams p)
 {
     constexpr bool ROWS = (WHAT & kRows) != 0, COLS = (WHAT & kCols) != 0, BLOCK = (WHAT & kBlock) != 0;
     constexpr int TR = 16 * R;
     static_assert(R == 8 || WHAT == kRows, "column and block scales need 128-row tiles");
+    static_assert(!GROUPED || (COLS && !BLOCK), "groups matter to blocks of rows only");
+    __shared__ int32_t s_rows[GROUPED ? 2 : 1];
     // transposed tile: 128 columns of 16 units of eight rows' codes.  Unit i of
     // column 8 c + j lies at i ^ c ^ (j & 1), so that neither the writes (16
     // values of c at one j) nor the reads (four columns of one c) collide.
@@ -119,7 +126,7 @@ fp8_quantize_kernel(const QuantParams p)
     const int tid = threadIdx.x;
     const int c = tid & 15, i = tid >> 4, warp = tid >> 5, lane = tid & 31;
     const int32_t mtile = blockIdx.x / p.tiles_k, kblock = blockIdx.x - mtile * p.tiles_k;
-    const int32_t m0 = mtile * TR + R * i;
+    int32_t m0 = mtile * TR, m_end = p.M;
     const int32_t col = kblock * 128 + 8 * c;
     const bool col_ok = col < p.K;          // K % 16 == 0: all eight or none
     const int64_t group = blockIdx.y;       // kBlock: one matrix per group
@@ -128,12 +135,45 @@ fp8_quantize_kernel(const QuantParams p)
     pdl_wait();
     pdl_launch_dependents();
 
+    if (GROUPED) {
+        // the group whose row tiles this one is among: a thread per group, and
+        // a running sum over the CTA's eight warps
+        __shared__ int32_t s_sum[8];
+        const bool mine = tid < p.groups;
+        const int32_t lo = mine ? p.row_offsets[tid] : 0, hi = mine ? p.row_offsets[tid + 1] : 0;
+        const bool bad = __syncthreads_or(mine && ((tid == 0 && lo != 0) || hi < lo || (tid == p.groups - 1 && hi > p.M)));
+        if (bad) {
+            if (blockIdx.x == 0 && tid == 0) atomicOr(&g_status_fp8_quant, static_cast<uint32_t>(kStatusBadGroup));
+            return;
+        }
+        const int32_t n = (hi - lo + 127) / 128;
+        int32_t up = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int32_t o = __shfl_up_sync(0xffffffffu, up, d);
+            if (lane >= d) up += o;
+        }
+        if (lane == 31) s_sum[warp] = up;
+        if (tid == 0) s_rows[0] = s_rows[1] = 0;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) up += s_sum[w];
+        if (mtile >= up - n && mtile < up) {
+            s_rows[0] = lo + (mtile - (up - n)) * 128;
+            s_rows[1] = hi;
+        }
+        __syncthreads();
+        m0 = s_rows[0];
+        m_end = s_rows[1];
+        if (m0 >= m_end) return;        // beyond the last group's tiles
+    }
+    m0 += R * i;
+
     uint4 x[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int32_t m = m0 + r;
         int64_t row = m;
-        bool ok = col_ok && m < p.M;
+        bool ok = col_ok && m < m_end;
         if (!BLOCK && p.row_index && ok) {
             row = p.row_index[m];
             if (row >= p.X_rows) {
@@ -215,7 +255,7 @@ fp8_quantize_kernel(const QuantParams p)
             s = block_scale<TYPE, POW2>(mine);
             constexpr int kPer = 16 / R;            // lanes that hold one row's scale
             const int32_t m = m0 + c / kPer;
-            if (c % kPer == 0 && m < p.M) p.SF[static_cast<int64_t>(kblock) * p.M + m] = s.s;
+            if (c % kPer == 0 && m < m_end) p.SF[static_cast<int64_t>(kblock) * p.M + m] = s.s;
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -225,7 +265,7 @@ fp8_quantize_kernel(const QuantParams p)
 #pragma unroll
             for (int j = 0; j < 4; ++j) q[j] = encode2<TYPE>(__fmul_rn(bf16_lo(w[j]), inv), __fmul_rn(bf16_hi(w[j]), inv));
             const int32_t m = m0 + r;
-            if (col_ok && m < p.M)
+            if (col_ok && m < m_end)
                 *reinterpret_cast<uint2 *>(p.Q + mat + static_cast<int64_t>(m) * p.K + col) =
                     make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
         }
@@ -300,12 +340,13 @@ fp8_quantize_kernel(const QuantParams p)
     }
 }
 
-template <int TYPE, bool POW2, int WHAT, int R>
+template <int TYPE, bool POW2, int WHAT, int R, bool GROUPED = false>
 int launch(const QuantParams &p, int64_t groups, cudaStream_t s)
 {
-    const int64_t tiles = (static_cast<int64_t>(p.M) + 16 * R - 1) / (16 * R) * p.tiles_k;
+    const int64_t tiles =
+        ((static_cast<int64_t>(p.M) + 16 * R - 1) / (16 * R) + (GROUPED ? p.groups : 0)) * p.tiles_k;
     if (tiles > INT32_MAX) return QFP4_ERR_UNSUPPORTED;
-    return launch_status(launch_pdl(fp8_quantize_kernel<TYPE, POW2, WHAT, R>,
+    return launch_status(launch_pdl(fp8_quantize_kernel<TYPE, POW2, WHAT, R, GROUPED>,
                                     dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(groups)), dim3(kThreads),
                                     0, s, p));
 }
@@ -313,6 +354,9 @@ int launch(const QuantParams &p, int64_t groups, cudaStream_t s)
 template <int TYPE, bool POW2>
 int launch_what(const QuantParams &p, int what, int64_t groups, cudaStream_t s)
 {
+    if (p.groups)
+        return what & kRows ? launch<TYPE, POW2, kRows | kCols, 8, true>(p, groups, s)
+                            : launch<TYPE, POW2, kCols, 8, true>(p, groups, s);
     switch (what) {
     case kRows: return launch<TYPE, POW2, kRows, 2>(p, groups, s);
     case kCols: return launch<TYPE, POW2, kCols, 8>(p, groups, s);
@@ -359,7 +403,7 @@ extern "C" int qfp4_fp8_quantize(int type, int scale, const void *X_bf16, int64_
         return QFP4_ERR_MISALIGNED;
     const QuantParams p{static_cast<const uint4 *>(X_bf16), row_index, X_rows, static_cast<int32_t>(M),
                         static_cast<int32_t>(K), static_cast<int32_t>((M + 15) / 16 * 16), static_cast<int32_t>((K + 127) / 128),
-                        static_cast<uint8_t *>(Q), static_cast<uint8_t *>(Q_t), SF, SF_t};
+                        static_cast<uint8_t *>(Q), static_cast<uint8_t *>(Q_t), SF, SF_t, nullptr, 0};
     return launch_any(type, scale, p, (Q ? kRows : 0) | (Q_t ? kCols : 0), 1, static_cast<cudaStream_t>(stream));
 }
 
@@ -374,6 +418,33 @@ extern "C" int qfp4_fp8_quantize_weight(int type, int scale, int64_t groups, con
         return QFP4_ERR_MISALIGNED;
     const QuantParams p{static_cast<const uint4 *>(W_bf16), nullptr, N, static_cast<int32_t>(N),
                         static_cast<int32_t>(K), static_cast<int32_t>((N + 15) / 16 * 16), static_cast<int32_t>((K + 127) / 128),
-                        static_cast<uint8_t *>(Q), static_cast<uint8_t *>(Q_t), SF, SF_t};
+                        static_cast<uint8_t *>(Q), static_cast<uint8_t *>(Q_t), SF, SF_t, nullptr, 0};
     return launch_any(type, scale, p, kBlock | (Q_t ? kCols : 0), groups, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" size_t qfp4_fp8_grouped_cols(int64_t total_rows, int64_t groups)
+{
+    if (total_rows < 0 || groups < 1) return 0;
+    return 128 * (static_cast<size_t>((total_rows + 127) / 128) + static_cast<size_t>(groups));
+}
+
+extern "C" int qfp4_fp8_quantize_grouped(int type, int scale, const void *X_bf16, int64_t X_rows,
+                                         const int32_t *row_index, int64_t groups, const int32_t *row_offsets,
+                                         int64_t total_rows, int64_t K, void *Q, float *SF, void *Q_t, float *SF_t,
+                                         void *stream)
+{
+    if (!types_ok(type, scale) || total_rows < 0 || K < 0 || X_rows < 0 || groups < 1 || !row_offsets)
+        return QFP4_ERR_INVALID_ARG;
+    if (!row_index && X_rows != total_rows) return QFP4_ERR_INVALID_ARG;
+    if (K % 16 != 0 || total_rows > kMaxSize || K > kMaxSize || groups > kMaxGroups) return QFP4_ERR_UNSUPPORTED;
+    if (total_rows == 0 || K == 0) return QFP4_OK;
+    if ((Q == nullptr) != (SF == nullptr) || !Q_t || !SF_t || (!X_bf16 && X_rows > 0)) return QFP4_ERR_INVALID_ARG;
+    if (!aligned16(X_bf16) || !aligned16(Q) || !aligned16(Q_t) || !aligned4(SF) || !aligned4(SF_t) ||
+        !aligned4(row_index) || !aligned4(row_offsets))
+        return QFP4_ERR_MISALIGNED;
+    const QuantParams p{static_cast<const uint4 *>(X_bf16), row_index, X_rows, static_cast<int32_t>(total_rows),
+                        static_cast<int32_t>(K), static_cast<int32_t>(qfp4_fp8_grouped_cols(total_rows, groups)),
+                        static_cast<int32_t>((K + 127) / 128), static_cast<uint8_t *>(Q), static_cast<uint8_t *>(Q_t),
+                        SF, SF_t, row_offsets, static_cast<int32_t>(groups)};
+    return launch_any(type, scale, p, (Q ? kRows : 0) | kCols, 1, static_cast<cudaStream_t>(stream));
 }

@@ -170,17 +170,25 @@ __device__ __forceinline__ void store_tile(const float (&acc)[COLS], uint8_t *ou
 }
 
 struct Tile {
-    int32_t row0, row_end, n0, group;
+    int32_t row0, row_end;      // rows of A and D: the tile's first, the end of its product's
+    int32_t n0, group;
+    int32_t kb0, kblocks;       // K blocks of its product
 };
 
-// GROUPED: one product per expert.  COLSCALE: B has one scale per row
-// (b_rows = 1), else one per 128 rows.
-template <bool GROUPED, bool COLSCALE, int TN>
+// kRowGroups: the groups' rows of A and D, each with its own B.
+// kBlockGroups: the groups' K blocks, each with its own D (weight gradients per expert).
+enum Grouping { kDense, kRowGroups, kBlockGroups };
+
+// COLSCALE: B has one scale per row (b_rows = 1), else one per 128 rows.
+template <Grouping GROUPING, bool COLSCALE, int TN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmD, const Fp8Params p)
 {
     using C = PairCfg<TN>;
+    constexpr bool GROUPED = GROUPING != kDense;
+    // rows of one of s_ptile's tiles: row tiles of D, or blocks of K
+    constexpr int kTileRows = GROUPING == kBlockGroups ? 128 : 256;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -193,7 +201,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sc_empty + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     __shared__ int32_t s_offs[GROUPED ? kMaxGroups + 1 : 1];
-    __shared__ int32_t s_ptile[GROUPED ? kMaxGroups + 1 : 1];        // prefix of 256-row tiles
+    __shared__ int32_t s_ptile[GROUPED ? kMaxGroups + 1 : 1];        // running sum of the groups' tiles
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -209,10 +217,10 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         for (int i = threadIdx.x; i <= p.groups; i += blockDim.x) s_offs[i] = p.row_offsets[i];
         __syncthreads();
         const bool bad = __syncthreads_or(threadIdx.x < p.groups &&
-                                          !fp8_offsets_valid(s_offs, threadIdx.x, p.groups, p.M, p.max_group_rows));
+                                          !fp8_offsets_valid(s_offs, threadIdx.x, p.groups, p.total_rows, p.max_group_rows));
         if (bad && threadIdx.x == 0 && blockIdx.x == 0)
             atomicOr(&g_status_gemm_fp8, static_cast<uint32_t>(kStatusBadGroup));
-        // running sum of the groups' 256-row tiles, eight groups a lane
+        // running sum of the groups' tiles, eight groups a lane
         if (warp == 0) {
             constexpr int kPer = kMaxGroups / 32;
             int32_t before[kPer], sum = 0;
@@ -220,7 +228,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             for (int i = 0; i < kPer; ++i) {
                 const int e = lane * kPer + i;
                 before[i] = sum;
-                sum += !bad && e < p.groups ? (s_offs[e + 1] - s_offs[e] + 255) / 256 : 0;
+                sum += !bad && e < p.groups ? (s_offs[e + 1] - s_offs[e] + kTileRows - 1) / kTileRows : 0;
             }
             int32_t up = sum;
             for (int d = 1; d < 32; d <<= 1) {
@@ -235,7 +243,9 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             if (lane == 31) s_ptile[p.groups] = up;
         }
         __syncthreads();
-        total_tiles = s_ptile[p.groups] * ntiles_n;
+        total_tiles = GROUPING == kRowGroups ? s_ptile[p.groups] * ntiles_n
+                      : bad                ? 0
+                                             : p.groups * ((p.M + 255) / 256) * ntiles_n;
     } else {
         total_tiles = ((p.M + 255) / 256) * ntiles_n;
     }
@@ -278,7 +288,17 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
         ti.group = 0;
         int32_t lt = t, mtiles = (p.M + 255) / 256, base = 0;
         ti.row_end = p.M;
-        if (GROUPED) {
+        ti.kb0 = 0;
+        ti.kblocks = kblocks;
+        if (GROUPING == kBlockGroups) {
+            ti.group = t / (mtiles * ntiles_n);
+            lt = t - ti.group * mtiles * ntiles_n;
+            base = ti.group * p.M;
+            ti.row_end = base + p.M;
+            ti.kb0 = s_ptile[ti.group];
+            ti.kblocks = s_ptile[ti.group + 1] - ti.kb0;
+        }
+        if (GROUPING == kRowGroups) {
             const int32_t mt_all = t / ntiles_n;
             int lo = 0, hi = p.groups - 1;
             while (lo < hi) {
@@ -313,9 +333,11 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 bool ok = true;
                 for (int32_t t = pair_id; t < total_tiles && ok; t += npairs) {
                     const Tile ti = tile_info(t);
-                    const int32_t arow = ti.row0 + 128 * static_cast<int32_t>(rank);
-                    const int32_t brow = ti.group * p.N + ti.n0 + TN / 2 * static_cast<int32_t>(rank);
-                    for (int32_t kb = 0; kb < kblocks; ++kb) {
+                    const int32_t arow = ti.row0 - (GROUPING == kBlockGroups ? ti.group * p.M : 0) +
+                                         128 * static_cast<int32_t>(rank);
+                    const int32_t brow = (GROUPING == kRowGroups ? ti.group * p.N : 0) + ti.n0 +
+                                         TN / 2 * static_cast<int32_t>(rank);
+                    for (int32_t kb = ti.kb0; kb < ti.kb0 + ti.kblocks; ++kb) {
                         if (!mbar_wait(smem_u32(&empty[s]), phase)) { ok = false; break; }
                         if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * C::STAGE);
                         tma_load_2d_pair(smem_u32(smem + s * C::STAGE), &tmA, full0_leader + s * 8, kb * 128, arow);
@@ -333,18 +355,20 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             const int32_t nb = (p.N + 127) / 128;
             for (int32_t t = pair_id; t < total_tiles && ok; t += npairs) {
                 const Tile ti = tile_info(t);
-                const int32_t row = ti.row0 + 128 * static_cast<int32_t>(rank) + lane;
-                for (int32_t kb0 = 0; kb0 < kblocks; kb0 += kBatch) {
+                const int32_t row = ti.row0 - (GROUPING == kBlockGroups ? ti.group * p.M : 0) +
+                                    128 * static_cast<int32_t>(rank) + lane;
+                const int32_t kb_end = ti.kb0 + ti.kblocks;
+                for (int32_t kb0 = ti.kb0; kb0 < kb_end; kb0 += kBatch) {
                     if (!mbar_wait_warp(smem_u32(&sc_empty[b]), phase)) { ok = false; break; }
                     uint32_t dst = smem_u32(smem + C::OFF_SCALE) + b * (kBatch * C::SCALES * 4);
-                    if (!COLSCALE && lane < 2 * kBatch && kb0 + (lane >> 1) < kblocks) {
+                    if (!COLSCALE && lane < 2 * kBatch && kb0 + (lane >> 1) < kb_end) {
                         // lane 2 u + h: the h-th block of 128 columns at K block u
                         cp_async4(dst + ((lane >> 1) * C::SCALES + 128 + (lane & 1)) * 4,
                                   p.B_sf + (static_cast<int64_t>(ti.group) * nb + min(ti.n0 / 128 + (lane & 1), nb - 1)) * kblocks +
                                       kb0 + (lane >> 1));
                     }
                     dst += lane * 4;
-                    for (int32_t kb = kb0; kb < min(kb0 + kBatch, kblocks); ++kb, dst += C::SCALES * 4) {
+                    for (int32_t kb = kb0; kb < min(kb0 + kBatch, kb_end); ++kb, dst += C::SCALES * 4) {
                         const float *a = p.A_sf + static_cast<int64_t>(kb) * p.M;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) cp_async4(dst + i * 128, a + min(row + 32 * i, p.M - 1));
@@ -372,8 +396,12 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             const uint32_t idesc = idesc_f8(256, TN, p.a_type, p.b_type);
             uint32_t s = first, phase = 0, slot = first, acc_phase = 1;
             bool ok = true;
-            const int64_t mine = pair_id < total_tiles ? (total_tiles - pair_id + npairs - 1) / npairs : 0;
-            const int64_t count = mine * kblocks;
+            int64_t count = 0;
+            if (GROUPING == kBlockGroups) {
+                for (int32_t t = pair_id; t < total_tiles; t += npairs) count += tile_info(t).kblocks;
+            } else if (pair_id < total_tiles) {
+                count = static_cast<int64_t>((total_tiles - pair_id + npairs - 1) / npairs) * kblocks;
+            }
             for (int64_t j = first; j < count; j += 2) {
                 if (!mbar_wait_warp(smem_u32(&full[s]), phase) ||
                     !mbar_wait_warp(smem_u32(&acc_empty[slot]), acc_phase)) { ok = false; break; }
@@ -414,7 +442,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             for (int i = 0; i < C::COLS; ++i) acc[i] = 0.0f;
             bool ready = false;         // the next slot's sum is known to be complete
             int u = 0;
-            for (int32_t kb = 0; kb < kblocks; ++kb) {
+            for (int32_t kb = 0; kb < ti.kblocks; ++kb) {
                 if (u == 0 && !mbar_wait_warp(smem_u32(&sc_full[b]), sc_phase)) { ok = false; break; }
                 if (!ready && !mbar_wait_warp(smem_u32(&acc_full[slot]), phase)) { ok = false; break; }
                 tc_fence_after();
@@ -462,8 +490,8 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 give_back();
                 add32(v[0], TN == 256 ? 2 : 0);
                 add32(v[1], TN == 256 ? 3 : 1);
-                ready = __all_sync(0xffffffffu, done) && kb + 1 < kblocks;
-                if (++u == kBatch || kb == kblocks - 1) {
+                ready = __all_sync(0xffffffffu, done) && kb + 1 < ti.kblocks;
+                if (++u == kBatch || kb == ti.kblocks - 1) {
                     u = 0;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sc_empty[b]));
@@ -509,17 +537,18 @@ bool types_ok(int a_type, int b_type, int out_type)
            (out_type == QFP4_BF16 || out_type == QFP4_FP32);
 }
 
-template <bool GROUPED, bool COLSCALE, int TN>
+template <Grouping GROUPING, bool COLSCALE, int TN>
 int launch_pair(Fp8Params p, int64_t tiles, cudaStream_t s)
 {
     using C = PairCfg<TN>;
-    auto kern = gemm_fp8_pair_kernel<GROUPED, COLSCALE, TN>;
+    auto kern = gemm_fp8_pair_kernel<GROUPING, COLSCALE, TN>;
     CUtensorMap ma, mb, md;
     int rc = ensure_smem_attr(reinterpret_cast<const void *>(kern), C::SMEM);
     if (rc == QFP4_OK) rc = make_map_direct(&ma, p.A, p.K, p.M, 128, 128);
-    if (rc == QFP4_OK) rc = make_map_direct(&mb, p.B, p.K, static_cast<uint64_t>(GROUPED ? p.groups : 1) * p.N, 128, TN / 2);
+    const uint64_t b_groups = GROUPING == kRowGroups ? p.groups : 1, d_groups = GROUPING == kBlockGroups ? p.groups : 1;
+    if (rc == QFP4_OK) rc = make_map_direct(&mb, p.B, p.K, b_groups * p.N, 128, TN / 2);
     p.store_map = p.N % (p.fp32 ? 4 : 8) == 0;
-    if (rc == QFP4_OK && p.store_map) rc = make_map_store(&md, p.D, p.fp32 != 0, p.N, p.M, p.fp32 ? 32 : 64, 32);
+    if (rc == QFP4_OK && p.store_map) rc = make_map_store(&md, p.D, p.fp32 != 0, p.N, d_groups * p.M, p.fp32 ? 32 : 64, 32);
     else md = ma;       // never used
     if (rc != QFP4_OK) return rc;
     const int sms = sm_count();
@@ -532,15 +561,18 @@ int launch_pair(Fp8Params p, int64_t tiles, cudaStream_t s)
 template <int TN>
 int launch_width(const Fp8Params &p, int64_t tiles, cudaStream_t s)
 {
-    if (p.groups) return launch_pair<true, false, TN>(p, tiles, s);
-    return p.b_rows == 1 ? launch_pair<false, true, TN>(p, tiles, s) : launch_pair<false, false, TN>(p, tiles, s);
+    if (p.groups) return p.b_rows == 1 ? launch_pair<kBlockGroups, true, TN>(p, tiles, s)
+                                       : launch_pair<kRowGroups, false, TN>(p, tiles, s);
+    return p.b_rows == 1 ? launch_pair<kDense, true, TN>(p, tiles, s) : launch_pair<kDense, false, TN>(p, tiles, s);
 }
 
 int launch_gemm_fp8(const Fp8Params &p, cudaStream_t s)
 {
-    if (gemm_fp8_small_pays(p)) return launch_gemm_fp8_small(p, s);
+    if (!(p.groups && p.b_rows == 1) && gemm_fp8_small_pays(p)) return launch_gemm_fp8_small(p, s);
     int64_t tiles_m = (static_cast<int64_t>(p.M) + 255) / 256;
-    if (p.groups) {
+    if (p.groups && p.b_rows == 1) {
+        tiles_m *= p.groups;
+    } else if (p.groups) {
         // every group may add one partial tile, and none has more than max_group_rows rows
         tiles_m += p.groups;
         const int64_t by_max = static_cast<int64_t>(p.groups) * ((p.max_group_rows + 255) / 256);
@@ -610,6 +642,28 @@ extern "C" int qfp4_gemm_nt_fp8_grouped(int a_type, int b_type, int64_t groups, 
     const Fp8Params p{static_cast<const uint8_t *>(A), static_cast<const uint8_t *>(B), A_sf, B_sf, D, row_offsets,
                       static_cast<int32_t>(total_rows), static_cast<int32_t>(N), static_cast<int32_t>(K),
                       static_cast<int32_t>(groups), static_cast<int32_t>(max_group_rows),
-                      a_type, b_type, 128, out_type == QFP4_FP32, 0};
+                      a_type, b_type, 128, out_type == QFP4_FP32, 0, 0, static_cast<int32_t>(total_rows)};
+    return launch_gemm_fp8(p, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int qfp4_gemm_nt_fp8_kgrouped(int a_type, int b_type, int64_t groups, const int32_t *row_offsets,
+                                         int64_t total_rows, int64_t M, int64_t N, const void *A, const float *A_sf,
+                                         const void *B, const float *B_sf, int accumulate, float *D, void *stream)
+{
+    if (!types_ok(a_type, b_type, QFP4_FP32)) return QFP4_ERR_INVALID_ARG;
+    if (groups < 1 || !row_offsets || total_rows < 0 || M < 0 || N < 0) return QFP4_ERR_INVALID_ARG;
+    if (groups > kMaxGroups || total_rows > kMaxSize || M > kMaxSize || N > kMaxSize || groups * M > kMaxSize)
+        return QFP4_ERR_UNSUPPORTED;
+    if (M == 0 || N == 0) return QFP4_OK;            // empty D: nothing to do, nothing launched
+    if (!D || !A || !A_sf || !B || !B_sf) return QFP4_ERR_INVALID_ARG;
+    if (!aligned16(A) || !aligned16(B) || !aligned16(D) || !aligned4(A_sf) || !aligned4(B_sf) ||
+        !aligned4(row_offsets))
+        return QFP4_ERR_MISALIGNED;
+    // K of the operands: every group's rows from a block of 128 of their own
+    const int64_t K = static_cast<int64_t>(qfp4_fp8_grouped_cols(total_rows, groups));
+    const Fp8Params p{static_cast<const uint8_t *>(A), static_cast<const uint8_t *>(B), A_sf, B_sf, D, row_offsets,
+                      static_cast<int32_t>(M), static_cast<int32_t>(N), static_cast<int32_t>(K),
+                      static_cast<int32_t>(groups), 0, a_type, b_type, 1, 1, accumulate ? 1 : 0, 0,
+                      static_cast<int32_t>(total_rows)};
     return launch_gemm_fp8(p, static_cast<cudaStream_t>(stream));
 }

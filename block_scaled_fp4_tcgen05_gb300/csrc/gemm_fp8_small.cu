@@ -121,7 +121,7 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
         m0 = (tile / tiles_n % tiles_m) * NT;
         pdl_wait();
         const bool bad = __syncthreads_or(threadIdx.x < p.groups &&
-                                          !fp8_offsets_valid(p.row_offsets, threadIdx.x, p.groups, p.M, p.max_group_rows));
+                                          !fp8_offsets_valid(p.row_offsets, threadIdx.x, p.groups, p.total_rows, p.max_group_rows));
         if (bad && threadIdx.x == 0 && blockIdx.x == 0)
             atomicOr(&g_status_gemm_fp8_small, static_cast<uint32_t>(kStatusBadGroup));
         m0 += p.row_offsets[group];

@@ -13,12 +13,13 @@ struct Fp8Params {
     const float *A_sf, *B_sf;
     void *D;
     const int32_t *row_offsets;     // grouped: DEVICE [groups + 1]
-    int32_t M, N, K;                // grouped: M = total_rows
-    int32_t groups;                 // 0: dense
+    int32_t M, N, K;                // grouped by rows: M = total_rows
+    int32_t groups;                 // 0: dense; with b_rows = 1, grouped by blocks of K
     int32_t max_group_rows;         // grouped: 0 = no bound
     int32_t a_type, b_type, b_rows;
     int32_t fp32, accumulate;
     int32_t store_map;              // D can be written by TMA (rows 16-byte aligned)
+    int32_t total_rows;             // grouped: what row_offsets may reach
 };
 
 // Row offsets a grouped product can use: from 0, never decreasing, at most

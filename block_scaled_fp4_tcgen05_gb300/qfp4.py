@@ -74,6 +74,10 @@ SIGNATURES = {
     "qfp4_gemm_nt_fp8": (_i32, [_i32, _i32, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp]),
     "qfp4_gemm_nt_fp8_grouped": (_i32, [_i32, _i32, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _vp,
                                         _vp]),
+    "qfp4_fp8_grouped_cols": (_sz, [_i64, _i64]),
+    "qfp4_fp8_quantize_grouped": (_i32, [_i32, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "qfp4_gemm_nt_fp8_kgrouped": (_i32, [_i32, _i32, _i64, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _vp,
+                                         _vp]),
     "qfp4_moe_route_workspace_bytes": (_sz, [_i64, _i64, _i64]),
     "qfp4_moe_route": (_i32, [_i32, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                               _vp, _sz, _vp]),
@@ -372,6 +376,24 @@ def fp8_quantize(type, X, Q=None, SF=None, Q_t=None, SF_t=None, scale=SCALE_FP32
                                     _at(Q_t), _at(SF_t, _F32), _stream(stream)))
 
 
+def fp8_grouped_cols(total_rows: int, groups: int) -> int:
+    """Columns of Q_t when every group's rows begin a block of 128 of their own."""
+    return int(load().qfp4_fp8_grouped_cols(total_rows, groups))
+
+
+def fp8_quantize_grouped(type, X, row_offsets, Q_t, SF_t, Q=None, SF=None, scale=SCALE_FP32, row_index=None,
+                         stream=None) -> None:
+    """fp8_quantize for one product per expert: Q_t [K, cols], SF_t [cols/128, K]
+    with cols = fp8_grouped_cols(rows, groups)."""
+    rows, K = X.shape
+    M = rows if row_index is None else row_index.numel()
+    groups = row_offsets.numel() - 1
+    _check("qfp4_fp8_quantize_grouped",
+           load().qfp4_fp8_quantize_grouped(type, scale, _at(X, _BF16), rows, _at(row_index, _I32), groups,
+                                            _at(row_offsets, _I32), M, K, _at(Q), _at(SF, _F32), _at(Q_t),
+                                            _at(SF_t, _F32), _stream(stream)))
+
+
 def fp8_quantize_weight(type, W, Q, SF, Q_t=None, SF_t=None, scale=SCALE_FP32, stream=None) -> None:
     """Weights W [N, K] or [groups, N, K] -> codes with a scale per 128 x 128
     block, and optionally their transpose (Q_t [.., K, ceil16(N)])."""
@@ -399,6 +421,17 @@ def gemm_nt_fp8_grouped(a_type, b_type, row_offsets, total_rows, max_group_rows,
            load().qfp4_gemm_nt_fp8_grouped(a_type, b_type, groups, _at(row_offsets, _I32), total_rows, max_group_rows,
                                            N, K, _at(A), _at(A_sf, _F32), _at(B), _at(B_sf, _F32), out,
                                            _at(D, _F32 if out == OUT_FP32 else _BF16), _stream(stream)))
+
+
+def gemm_nt_fp8_kgrouped(a_type, b_type, row_offsets, total_rows, M, N, A, A_sf, B, B_sf, D, accumulate=False,
+                         stream=None) -> None:
+    """Every expert's weight gradient: D[e] (+)= A_e B_e^T over the columns that
+    fp8_quantize_grouped gave group e; D fp32 [groups, M, N]."""
+    groups = row_offsets.numel() - 1
+    _check("qfp4_gemm_nt_fp8_kgrouped",
+           load().qfp4_gemm_nt_fp8_kgrouped(a_type, b_type, groups, _at(row_offsets, _I32), total_rows, M, N, _at(A),
+                                            _at(A_sf, _F32), _at(B), _at(B_sf, _F32), 1 if accumulate else 0,
+                                            _at(D, _F32), _stream(stream)))
 
 
 def moe_route_workspace_bytes(T: int, E: int, topk: int) -> int:

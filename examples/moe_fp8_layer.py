@@ -5,9 +5,8 @@ weighted sum, then the gradients of the router, of the weights and of the input.
     python examples/moe_fp8_layer.py [--tokens 4096] [--experts 8] [--topk 2]
 
 Every product and quantiser and the router are the library's kernels; the
-elementwise steps between them (SwiGLU, the weighted sum) are torch.  The
-weight gradients are taken expert by expert with the dense product, whose
-operands are the transposed codes of qfp4.fp8_quantize.
+elementwise steps between them (SwiGLU, the weighted sum) are torch.  No step
+needs the experts' loads on the host.
 """
 from __future__ import annotations
 
@@ -65,18 +64,20 @@ class Experts:
         qfp4.gemm_nt_fp8_grouped(qfp4.E5M2, qfp4.E4M3, offsets, dy.shape[0], 0, K, N, q, sf, self.qt, self.sft, d)
         return d
 
-    def weight_gradient(self, dy, x, cuts):
-        """dW[e] = dY_e^T X_e, fp32, both operands scaled along the tokens."""
+    def weight_gradient(self, dy, x, offsets, index=None):
+        """dW[e] = dY_e^T X_e, fp32, both operands scaled along the tokens; index
+        gathers the rows of x into expert order."""
         E, N, K = self.shape
-        dw = torch.zeros(E, N, K, device=x.device)
-        for e in range(E):
-            lo, hi = cuts[e], cuts[e + 1]
-            if lo == hi:
-                continue
-            _, _, dq, dsf = quantize(dy[lo:hi], qfp4.E5M2, rows=False, cols=True)
-            _, _, xq, xsf = quantize(x[lo:hi], qfp4.E4M3, rows=False, cols=True)
-            qfp4.gemm_nt_fp8(qfp4.E5M2, qfp4.E4M3, N, K, up16(hi - lo), dq, dsf, xq, xsf, dw[e], b_rows=1,
-                             out=qfp4.OUT_FP32)
+        rows = dy.shape[0]
+        cols = qfp4.fp8_grouped_cols(rows, E)
+        operands = []
+        for t, kind, ix in ((dy, qfp4.E5M2, None), (x, qfp4.E4M3, index)):
+            qt = torch.empty(t.shape[1], cols, dtype=torch.uint8, device=t.device)
+            sft = torch.empty(cols // BLOCK, t.shape[1], device=t.device)
+            qfp4.fp8_quantize_grouped(kind, t, offsets, qt, sft, row_index=ix)
+            operands += [qt, sft]
+        dw = torch.empty(E, N, K, device=x.device)
+        qfp4.gemm_nt_fp8_kgrouped(qfp4.E5M2, qfp4.E4M3, offsets, rows, N, K, *operands, dw)
         return dw
 
 
@@ -106,7 +107,6 @@ def layer(x, logits, up, down, topk, dy=None, balance=0.01, valid=None):
     y = (rows * gates[..., None]).sum(1)
     if dy is None:
         return y, loss
-    cuts = offsets.tolist()
     dgates = (rows * dy[:, None]).sum(-1)
     at = dest.view(-1).long()
     keep = at >= 0
@@ -118,11 +118,10 @@ def layer(x, logits, up, down, topk, dy=None, balance=0.01, valid=None):
     dh = torch.cat([da * uph * s * (1 + gate * (1 - s)), da * gate * s], -1).bfloat16()
     dxe = up.input_gradient(dh, offsets)
     dx = (dxe[dest.clamp(min=0).long().view(-1)].view(T, topk, -1).float() * chosen).sum(1)
-    xe = x[src.clamp(min=0).long()]
     dlogits = torch.empty_like(logits)
     qfp4.moe_route_backward(logits, ids, counts, n, dgates, torch.full((1,), balance, device=dev), dlogits, valid=valid)
-    return y, loss, {"x": dx, "logits": dlogits, "up": up.weight_gradient(dh, xe, cuts),
-                     "down": down.weight_gradient(do, a, cuts)}
+    return y, loss, {"x": dx, "logits": dlogits, "up": up.weight_gradient(dh, x, offsets, src),
+                     "down": down.weight_gradient(do, a, offsets)}
 
 
 def plain(x, logits, w_up, w_down, topk, dy, balance):

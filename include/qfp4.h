@@ -534,6 +534,23 @@ enum { QFP4_BF16 = 0, QFP4_FP32 = 1 };
 int qfp4_fp8_quantize(int type, int scale, const void *X_bf16, int64_t X_rows, const int32_t *row_index,
                       int64_t M, int64_t K, void *Q, float *SF, void *Q_t, float *SF_t, void *stream);
 
+/* Both directions for one product per expert: rows [row_offsets[e],
+ * row_offsets[e+1]) of the operand (gathered by row_index or not) are group e,
+ * and the blocks of 128 rows along the columns begin anew with each group.
+ *   Q, SF      as above, both or neither NULL; rows beyond row_offsets[groups]
+ *              are left unwritten
+ *   Q_t, SF_t  [K][cols] and [cols / 128][K] with cols =
+ *              qfp4_fp8_grouped_cols(total_rows, groups): group e's columns
+ *              start at 128 * sum_{e' < e} ceil(rows_e' / 128), zero codes
+ *              beyond its rows; columns beyond the last group's are left
+ *              unwritten.  Operands of qfp4_gemm_nt_fp8_kgrouped.
+ * row_offsets is checked on the device as for qfp4_gemm_nt_fp8_grouped (unusable
+ * ones: nothing is written).  Requirements as above, 1 <= groups <= 256. */
+size_t qfp4_fp8_grouped_cols(int64_t total_rows, int64_t groups);
+int qfp4_fp8_quantize_grouped(int type, int scale, const void *X_bf16, int64_t X_rows, const int32_t *row_index,
+                              int64_t groups, const int32_t *row_offsets, int64_t total_rows, int64_t K, void *Q,
+                              float *SF, void *Q_t, float *SF_t, void *stream);
+
 /* The same with one scale per 128 x 128 block: weights W [groups, N, K]
  * (groups = 1, or one matrix per expert).
  *   Q, SF      codes [groups][N][K], scales [groups][ceil(N/128)][ceil(K/128)]:
@@ -582,6 +599,19 @@ int qfp4_gemm_nt_fp8_grouped(int a_type, int b_type, int64_t groups, const int32
                              int64_t total_rows, int64_t max_group_rows, int64_t N, int64_t K,
                              const void *A, const float *A_sf, const void *B, const float *B_sf,
                              int out_type, void *D, void *stream);
+
+/* Weight gradients of every expert in one launch: for each group e
+ *   D[e][m,n] = (accumulate ? D[e][m,n] : 0) + sum over e's blocks j along K of
+ *               sa[j][m] * sb[j][n] * sum_{k in block j} a[m,k] * b[n,k]
+ * with A [M][cols] and B [N][cols] the transposed codes of
+ * qfp4_fp8_quantize_grouped (of the output's gradient and of the input), A_sf
+ * [cols / 128][M], B_sf [cols / 128][N], cols = qfp4_fp8_grouped_cols(total_rows,
+ * groups), D fp32 [groups][M][N].  A group without rows gives zeros (accumulate:
+ * its D stays).  row_offsets as in qfp4_gemm_nt_fp8_grouped.  Requirements as
+ * there, groups * M <= 2^30. */
+int qfp4_gemm_nt_fp8_kgrouped(int a_type, int b_type, int64_t groups, const int32_t *row_offsets,
+                              int64_t total_rows, int64_t M, int64_t N, const void *A, const float *A_sf,
+                              const void *B, const float *B_sf, int accumulate, float *D, void *stream);
 
 /* ---------------------------------------------------------------------- */
 /* Expert router                                                            */

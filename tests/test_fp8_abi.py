@@ -54,6 +54,35 @@ def test_quantize_weight(lib):
     assert call(N=0) == OK
 
 
+def test_quantize_grouped(lib):
+    call = caller(lib.qfp4_fp8_quantize_grouped, type=0, scale=0, X=FAKE, X_rows=16, row_index=None, groups=4, offs=FAKE,
+                  rows=16, K=256, Q=FAKE, SF=FAKE, Q_t=FAKE, SF_t=FAKE, stream=None)
+    for bad in (dict(type=2), dict(scale=5), dict(groups=0), dict(offs=None), dict(rows=-1, X_rows=-1), dict(K=-16),
+                dict(X=None), dict(X_rows=15), dict(Q=None), dict(SF=None), dict(Q_t=None), dict(SF_t=None)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(K=40), dict(groups=257), dict(rows=1 << 31, X_rows=1 << 31)):
+        assert call(**bad) == UNSUPPORTED, bad
+    for bad in (dict(X=FAKE + 8), dict(Q_t=FAKE + 4), dict(offs=FAKE + 2), dict(row_index=FAKE + 1), dict(SF_t=FAKE + 2)):
+        assert call(**bad) == MISALIGNED, bad
+    assert call(rows=0, X_rows=0) == OK
+    assert qfp4.fp8_grouped_cols(0, 3) == 384 and qfp4.fp8_grouped_cols(129, 2) == 512
+    assert qfp4.fp8_grouped_cols(-1, 2) == 0 and qfp4.fp8_grouped_cols(5, 0) == 0
+
+
+def test_kgrouped(lib):
+    call = caller(lib.qfp4_gemm_nt_fp8_kgrouped, ta=1, tb=0, groups=4, offs=FAKE, rows=64, M=128, N=256, A=FAKE, A_sf=FAKE,
+                  B=FAKE, B_sf=FAKE, accumulate=0, D=FAKE, stream=None)
+    for bad in (dict(ta=2), dict(tb=9), dict(groups=0), dict(offs=None), dict(rows=-1), dict(M=-1), dict(N=-1),
+                dict(A=None), dict(A_sf=None), dict(B=None), dict(B_sf=None), dict(D=None)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(groups=257), dict(M=1 << 29), dict(N=1 << 31), dict(rows=1 << 31)):
+        assert call(**bad) == UNSUPPORTED, bad
+    for bad in (dict(offs=FAKE + 2), dict(A=FAKE + 4), dict(B=FAKE + 8), dict(D=FAKE + 8), dict(A_sf=FAKE + 1),
+                dict(B_sf=FAKE + 3)):
+        assert call(**bad) == MISALIGNED, bad
+    assert call(M=0) == OK and call(N=0) == OK
+
+
 def test_gemm(lib):
     call = caller(lib.qfp4_gemm_nt_fp8, ta=0, tb=1, M=16, N=128, K=256, A=FAKE, A_sf=FAKE, B=FAKE, B_sf=FAKE, b_rows=128,
                   out=0, accumulate=0, D=FAKE, stream=None)

@@ -144,6 +144,52 @@ def test_quantize_gathers_rows():
     assert settled() == 0
 
 
+def group_tiles(offsets):
+    """First 128-column tile of each group, and how many there are."""
+    at = [0]
+    for lo, hi in zip(offsets, offsets[1:]):
+        at.append(at[-1] + -(-(hi - lo) // BLOCK))
+    return at
+
+
+@pytest.mark.parametrize("offsets,K", [([0, 5], 144), ([0, 0, 128, 128, 257, 300], 272), ([0, 1, 2, 3], 16),
+                                       ([0, 0, 0], 32), ([0] + [3 * i for i in range(1, 257)], 48), ([0, 700, 1500], 640)])
+@pytest.mark.parametrize("pow2,rows,gather", [(False, True, False), (True, False, True)])
+def test_quantize_grouped(offsets, K, pow2, rows, gather):
+    """Each group's blocks along the columns begin anew; what no group reaches
+    stays as it was."""
+    kind, G, used = qfp4.E4M3, len(offsets) - 1, offsets[-1]
+    M = used + 20
+    x = values(M, K, 3 * M)
+    index = torch.randperm(M, generator=torch.Generator().manual_seed(1)) if gather else torch.arange(M)
+    cols = qfp4.fp8_grouped_cols(M, G)
+    seven = torch.full((1,), 7.0).to(TYPES[kind][0])
+    q = seven.expand(M, K).contiguous().cuda() if rows else None
+    sf = torch.full((-(-K // BLOCK), M), -1.0, device="cuda") if rows else None
+    qt, sft = seven.expand(K, cols).contiguous().cuda(), torch.full((cols // BLOCK, K), -1.0, device="cuda")
+    offs = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    qfp4.fp8_quantize_grouped(kind, x.cuda(), offs, qt, sft, q, sf, scale=qfp4.SCALE_POW2 if pow2 else qfp4.SCALE_FP32,
+                              row_index=index.int().cuda() if gather else None)
+    assert settled() == 0
+    want = x[index]
+    tiles = group_tiles(offsets)
+    qt, sft = qt.cpu(), sft.cpu()
+    for e in range(G):
+        lo, hi = offsets[e], offsets[e + 1]
+        if lo == hi:
+            continue
+        codes, scale = rows_rule(want[lo:hi].t().contiguous(), kind, pow2)
+        at = tiles[e] * BLOCK
+        assert same(qt[:, at:at + hi - lo].double().numpy(), codes)
+        assert not qt[:, at + hi - lo:tiles[e + 1] * BLOCK].view(torch.uint8).any()
+        assert same(sft[tiles[e]:tiles[e + 1]].numpy(), scale)
+    assert bool((qt[:, tiles[-1] * BLOCK:].float() == 7.0).all()) and bool((sft[tiles[-1]:] == -1.0).all())
+    if rows:
+        codes, scale = rows_rule(want[:used], kind, pow2)
+        assert same(q[:used].cpu().double().numpy(), codes) and same(sf[:, :used].cpu().numpy(), scale)
+        assert bool((q[used:].float() == 7.0).all()) and bool((sf[:, used:] == -1.0).all())
+
+
 @pytest.mark.parametrize("kind", [qfp4.E4M3, qfp4.E5M2])
 @pytest.mark.parametrize("pow2", [False, True])
 @pytest.mark.parametrize("G,N,K", [(1, 1, 16), (1, 128, 128), (3, 200, 272), (2, 16, 1040), (1, 385, 144)])
@@ -330,6 +376,44 @@ def test_grouped_refuses_bad_offsets(offsets, most):
     qfp4.gemm_nt_fp8_grouped(qfp4.E4M3, qfp4.E4M3, offs, rows, most, N, K, *(t.cuda() for t in (qa, sa, qb, sb)), d)
     assert settled() == -1
     assert bool((d == 7.0).all())
+    assert settled() == 0
+
+
+@pytest.mark.parametrize("offsets,M,N", [([0, 5], 136, 24), ([0, 0, 128, 128, 257, 300], 264, 130), ([0, 1, 2, 3], 16, 256),
+                                         ([0, 0, 0], 40, 128), ([0] + [3 * i for i in range(1, 257)], 48, 64),
+                                         ([0, 700, 1500], 300, 515), ([0, 900, 900, 2500], 512, 256)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_kgrouped(offsets, M, N, accumulate):
+    """Each expert's weight gradient; none where no row came to it."""
+    G, used = len(offsets) - 1, offsets[-1]
+    rows = used + 9
+    cols, tiles = qfp4.fp8_grouped_cols(rows, G), group_tiles(offsets)
+    qa, sa = operand(M, cols, qfp4.E5M2, 3)
+    qb, sb = operand(N, cols, qfp4.E4M3, 4)
+    for t in (qa, qb):          # what no group reaches may hold anything
+        t.view(torch.uint8)[:, tiles[-1] * BLOCK:] = 0x7F
+    start = torch.randn(G, M, N, generator=torch.Generator().manual_seed(1)) * 10
+    d = start.cuda() if accumulate else torch.full((G, M, N), float("nan"), device="cuda")
+    offs = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    qfp4.gemm_nt_fp8_kgrouped(qfp4.E5M2, qfp4.E4M3, offs, rows, M, N, qa.cuda(), sa.cuda(), qb.cuda(), sb.cuda(), d,
+                              accumulate=accumulate)
+    assert settled() == 0
+    a, b = decoded(qa, sa, False), decoded(qb, sb, False)
+    for e in range(G):
+        k = slice(tiles[e] * BLOCK, tiles[e + 1] * BLOCK)
+        check_product(d[e], a[:, k], b[:, k], (tiles[e + 1] - tiles[e]) * BLOCK, True, start[e].double() if accumulate else None)
+
+
+@pytest.mark.parametrize("offsets", [[1, 4, 8], [0, 6, 4], [0, 4, 9], [0, -2, 8]])
+def test_grouped_training_refuses_bad_offsets(offsets):
+    offs = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    qt = torch.full((64, qfp4.fp8_grouped_cols(8, 2)), 9, dtype=torch.uint8, device="cuda")
+    sft = torch.full((qt.shape[1] // BLOCK, 64), -1.0, device="cuda")
+    qfp4.fp8_quantize_grouped(qfp4.E4M3, values(8, 64, 1).cuda(), offs, qt, sft)
+    assert settled() == -1 and bool((qt == 9).all()) and bool((sft == -1.0).all())
+    d = torch.full((2, 64, 64), 7.0, device="cuda")
+    qfp4.gemm_nt_fp8_kgrouped(qfp4.E4M3, qfp4.E4M3, offs, 8, 64, 64, qt, sft, qt, sft, d)
+    assert settled() == -1 and bool((d == 7.0).all())
     assert settled() == 0
 
 
