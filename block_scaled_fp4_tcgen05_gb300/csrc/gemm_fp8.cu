@@ -41,6 +41,16 @@ namespace qfp4 {
 
 __device__ uint32_t g_status_gemm_fp8 = 0;
 
+#ifdef QFP4_FAULT_INJECTION
+// Test build only: when set, one epilogue warp of the first pair's leader never
+// gives back the slot of its first K block, so that the issuer's next wait for
+// that slot runs out.  No copy completes on that barrier.
+__device__ int g_inject_fp8_pair = 0;
+__device__ __forceinline__ bool inject_skip(bool here) { return here && g_inject_fp8_pair != 0; }
+#else
+__device__ __forceinline__ bool inject_skip(bool) { return false; }
+#endif
+
 int read_clear_status_gemm_fp8(cudaStream_t s, uint32_t *out)
 {
     uint32_t zero = 0;
@@ -452,7 +462,8 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 auto give_back = [&]() {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster_relaxed(release + slot * 8);
+                    if (lane == 0 && !inject_skip(blockIdx.x == 0 && warp == 4 && t == pair_id && kb == 0))
+                        mbar_arrive_cluster_relaxed(release + slot * 8);
                     if (++slot == C::SLOTS) { slot = 0; phase ^= 1; }
                     done = mbar_test(smem_u32(&acc_full[slot]), phase);
                 };
@@ -667,3 +678,13 @@ extern "C" int qfp4_gemm_nt_fp8_kgrouped(int a_type, int b_type, int64_t groups,
                       static_cast<int32_t>(total_rows)};
     return launch_gemm_fp8(p, static_cast<cudaStream_t>(stream));
 }
+
+#ifdef QFP4_FAULT_INJECTION
+// Test build only (not declared in the public header): arm (1) or disarm (0)
+// the missing releases of the 8-bit products.
+extern "C" int qfp4_test_inject_fp8_skip_release(int on)
+{
+    if (cudaMemcpyToSymbol(qfp4::g_inject_fp8_pair, &on, sizeof(int)) != cudaSuccess) return QFP4_ERR_CUDA;
+    return qfp4::set_inject_fp8_small(on);
+}
+#endif

@@ -31,6 +31,19 @@ namespace qfp4 {
 
 __device__ uint32_t g_status_gemm_fp8_small = 0;
 
+#ifdef QFP4_FAULT_INJECTION
+// Test build only: one epilogue warp of the first CTA never gives back the
+// slot of its first K block.
+__device__ int g_inject_fp8_small = 0;
+__device__ __forceinline__ bool inject_skip(bool here) { return here && g_inject_fp8_small != 0; }
+int set_inject_fp8_small(int on)
+{
+    return cudaMemcpyToSymbol(g_inject_fp8_small, &on, sizeof(int)) == cudaSuccess ? QFP4_OK : QFP4_ERR_CUDA;
+}
+#else
+__device__ __forceinline__ bool inject_skip(bool) { return false; }
+#endif
+
 int read_clear_status_gemm_fp8_small(cudaStream_t s, uint32_t *out)
 {
     uint32_t zero = 0;
@@ -283,7 +296,8 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
                     for (int d = 0; d < C::COLS / kLd; ++d) tmem_regs_after_wait(v[d]);
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&acc_empty[slot]));
+                    if (lane == 0 && !inject_skip(blockIdx.x == 0 && warp == 4 && j == 0))
+                        mbar_arrive(smem_u32(&acc_empty[slot]));
                     slot ^= 1;
                     if (slot == 0) phase ^= 1;
                     done = mbar_test(smem_u32(&acc_full[slot]), phase);

@@ -116,7 +116,8 @@ _faultinj = None
 def load_fault_injection() -> ctypes.CDLL:
     """Open the test build (libqfp4_faultinj.so, built by
     build.build(variant="faultinj")): the same entry points with a 5 ms wait
-    limit, plus qfp4_test_inject_skip_release(int) and the encoder probes
+    limit, plus qfp4_test_inject_skip_release(int), its counterpart for the
+    8-bit products qfp4_test_inject_fp8_skip_release(int) and the encoder probes
     qfp4_test_scale_codes / qfp4_test_element_codes.  For tests only; the
     product path always uses load()."""
     global _faultinj
@@ -129,8 +130,9 @@ def load_fault_injection() -> ctypes.CDLL:
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
-            lib.qfp4_test_inject_skip_release.restype = _i32
-            lib.qfp4_test_inject_skip_release.argtypes = [_i32]
+            for name in ("qfp4_test_inject_skip_release", "qfp4_test_inject_fp8_skip_release"):
+                getattr(lib, name).restype = _i32
+                getattr(lib, name).argtypes = [_i32]
             for name in ("qfp4_test_scale_codes", "qfp4_test_element_codes"):
                 fn = getattr(lib, name)
                 fn.restype = _i32
