@@ -43,7 +43,6 @@ int read_clear_status_fp8_quant(cudaStream_t s, uint32_t *out)
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr float kFloor = 0x1p-100f;
 
 struct QuantParams {
@@ -104,24 +103,32 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
 
 enum { kRows = 1, kCols = 2, kBlock = 4 };
 
-// R rows per thread: the tile is 16 R rows x 128 columns.  Thread 16 i + c
-// holds rows R i .. R i + R - 1 and columns 8 c .. 8 c + 7 of the tile.
-// WHAT: kRows and / or kCols, or kBlock with or without kCols (R = 8).
+// R rows per thread.  Thread 16 i + c holds rows R i .. R i + R - 1 and columns
+// 8 c .. 8 c + 7 of the tile: 128 rows, or the 16 R of 256 threads for rows alone.
+// WHAT: kRows and / or kCols, or kBlock with or without kCols.
+template <int WHAT, int R>
+struct QuantCfg {
+    static constexpr int ROWS = WHAT == kRows ? 16 * R : 128;
+    static constexpr int THREADS = 16 * (ROWS / R);
+    static constexpr int CTAS = (WHAT == kRows ? 1536 : 768) / THREADS;      // resident CTAs per SM that the registers are sized for
+};
+
 // GROUPED: every group's rows begin a row tile of their own (WHAT has kCols).
 template <int TYPE, bool POW2, int WHAT, int R, bool GROUPED>
-__global__ void __launch_bounds__(kThreads, R == 8 ? 3 : 6)
+__global__ void __launch_bounds__(QuantCfg<WHAT, R>::THREADS, QuantCfg<WHAT, R>::CTAS)
 fp8_quantize_kernel(const QuantParams p)
 {
     constexpr bool ROWS = (WHAT & kRows) != 0, COLS = (WHAT & kCols) != 0, BLOCK = (WHAT & kBlock) != 0;
-    constexpr int TR = 16 * R;
-    static_assert(R == 8 || WHAT == kRows, "column and block scales need 128-row tiles");
+    constexpr int TR = QuantCfg<WHAT, R>::ROWS, THREADS = QuantCfg<WHAT, R>::THREADS, WARPS = THREADS / 32;
+    static_assert(R == 2 || R == 4 || R == 8, "the exchange between rows halves them");
     static_assert(!GROUPED || (COLS && !BLOCK), "groups matter to blocks of rows only");
     __shared__ int32_t s_rows[GROUPED ? 2 : 1];
-    // transposed tile: 128 columns of 16 units of eight rows' codes.  Unit i of
-    // column 8 c + j lies at i ^ c ^ (j & 1), so that neither the writes (16
-    // values of c at one j) nor the reads (four columns of one c) collide.
-    __shared__ __align__(16) uint2 s_t[COLS ? 128 * 16 : 1];
-    __shared__ __align__(16) float s_amax[COLS && !BLOCK ? 8 * 128 : 8];
+    // transposed tile: 128 columns of 32 words of four rows' codes.  Word u of
+    // column 8 c + j lies at u ^ 2 c: the writes of a warp (16 values of c, two
+    // neighbouring words) and the reads (16 bytes of four columns) then spread
+    // over all banks.
+    __shared__ __align__(16) uint32_t s_t[COLS ? 128 * 32 : 4];
+    __shared__ __align__(16) float s_amax[COLS && !BLOCK ? WARPS * 128 : WARPS];
 
     const int tid = threadIdx.x;
     const int c = tid & 15, i = tid >> 4, warp = tid >> 5, lane = tid & 31;
@@ -137,8 +144,9 @@ fp8_quantize_kernel(const QuantParams p)
 
     if (GROUPED) {
         // the group whose row tiles this one is among: a thread per group, and
-        // a running sum over the CTA's eight warps
-        __shared__ int32_t s_sum[8];
+        // a running sum over the CTA's warps
+        __shared__ int32_t s_sum[WARPS];
+        static_assert(!GROUPED || THREADS >= kMaxGroups, "a thread per group");
         const bool mine = tid < p.groups;
         const int32_t lo = mine ? p.row_offsets[tid] : 0, hi = mine ? p.row_offsets[tid + 1] : 0;
         const bool bad = __syncthreads_or(mine && ((tid == 0 && lo != 0) || hi < lo || (tid == p.groups - 1 && hi > p.M)));
@@ -211,7 +219,7 @@ fp8_quantize_kernel(const QuantParams p)
         if (lane == 0) s_amax[warp] = a;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < 8; ++w) a = fmaxf(a, s_amax[w]);
+        for (int w = 0; w < WARPS; ++w) a = fmaxf(a, s_amax[w]);
         block = block_scale<TYPE, POW2>(a);
         const int32_t tiles_m = gridDim.x / p.tiles_k;
         if (tid == 0) {
@@ -222,36 +230,24 @@ fp8_quantize_kernel(const QuantParams p)
 
     if (ROWS || BLOCK) {
         // Row scales.  Each halving exchange leaves a thread half as many rows
-        // and the maximum over twice as many threads, so that after three of
-        // them (and one plain one) lanes 2 r, 2 r + 1 of the 16 that share R
-        // rows hold row r's maximum, and every scale is computed once or
-        // twice, not sixteen times; the threads then fetch theirs back.
-        float mine = 0.0f;
+        // and the maximum over twice as many threads, so that in the end 16 / R
+        // of the 16 threads that share R rows hold each row's maximum, and a
+        // scale is computed that often, not sixteen times; the threads then
+        // fetch theirs back.
         Scale s = block;
         if (ROWS) {
-            if (R == 8) {
-                float h[4], q[2];
-                const bool b3 = (c & 8) != 0, b2 = (c & 4) != 0, b1 = (c & 2) != 0;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const float keep = b3 ? ra[(r + 4) % R] : ra[r % R], give = b3 ? ra[r % R] : ra[(r + 4) % R];
-                    h[r] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 8));
-                }
+            for (int n = R / 2, d = 8; d > 0; d >>= 1, n /= 2) {
+                if (n > 0) {
+                    const bool up = (c & d) != 0;
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float keep = b2 ? h[r + 2] : h[r], give = b2 ? h[r] : h[r + 2];
-                    q[r] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, 4));
+                    for (int r = 0; r < n; ++r)
+                        ra[r] = fmaxf(up ? ra[r + n] : ra[r], __shfl_xor_sync(0xffffffffu, up ? ra[r] : ra[r + n], d));
+                } else {
+                    ra[0] = fmaxf(ra[0], __shfl_xor_sync(0xffffffffu, ra[0], d));
                 }
-                mine = fmaxf(b1 ? q[1] : q[0], __shfl_xor_sync(0xffffffffu, b1 ? q[0] : q[1], 2));
-                mine = fmaxf(mine, __shfl_xor_sync(0xffffffffu, mine, 1));
-            } else {
-                float h = 0.0f;
-                const bool b3 = (c & 8) != 0;
-                h = fmaxf(b3 ? ra[R - 1] : ra[0], __shfl_xor_sync(0xffffffffu, b3 ? ra[0] : ra[R - 1], 8));
-                h = fmaxf(h, __shfl_xor_sync(0xffffffffu, h, 4));
-                h = fmaxf(h, __shfl_xor_sync(0xffffffffu, h, 2));
-                mine = fmaxf(h, __shfl_xor_sync(0xffffffffu, h, 1));
             }
+            const float mine = ra[0];
             s = block_scale<TYPE, POW2>(mine);
             constexpr int kPer = 16 / R;            // lanes that hold one row's scale
             const int32_t m = m0 + c / kPer;
@@ -298,7 +294,7 @@ fp8_quantize_kernel(const QuantParams p)
             if (tid < 128) {
                 float a = 0.0f;
 #pragma unroll
-                for (int w = 0; w < 8; ++w) a = fmaxf(a, s_amax[w * 128 + tid]);
+                for (int w = 0; w < WARPS; ++w) a = fmaxf(a, s_amax[w * 128 + tid]);
                 const Scale s = block_scale<TYPE, POW2>(a);
                 s_amax[tid] = s.inv;            // (only this thread read it: warp 0's row of the table)
                 const int32_t k = kblock * 128 + tid;
@@ -311,31 +307,31 @@ fp8_quantize_kernel(const QuantParams p)
                 inv[4 * j] = f.x; inv[4 * j + 1] = f.y; inv[4 * j + 2] = f.z; inv[4 * j + 3] = f.w;
             }
         }
-        // codes of column 8 c + j, rows R i .. R i + 7, as eight bytes of the
-        // transposed tile
+        // codes of column 8 c + j, four rows to a word of the transposed tile
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float v[8];
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const uint32_t w = j < 2 ? x[r % R].x : j < 4 ? x[r % R].y : j < 6 ? x[r % R].z : x[r % R].w;
-                v[r] = __fmul_rn((j & 1) ? bf16_hi(w) : bf16_lo(w), inv[j]);
+            for (int u = 0; u < R / 4; ++u) {
+                float v[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint4 &q = x[(4 * u + r) % R];
+                    const uint32_t w = j < 2 ? q.x : j < 4 ? q.y : j < 6 ? q.z : q.w;
+                    v[r] = __fmul_rn((j & 1) ? bf16_hi(w) : bf16_lo(w), inv[j]);
+                }
+                s_t[(8 * c + j) * 32 + ((R / 4 * i + u) ^ (2 * c))] =
+                    encode2<TYPE>(v[0], v[1]) | encode2<TYPE>(v[2], v[3]) << 16;
             }
-            s_t[(8 * c + j) * 16 + (i ^ c ^ (j & 1))] =
-                make_uint2(encode2<TYPE>(v[0], v[1]) | encode2<TYPE>(v[2], v[3]) << 16,
-                           encode2<TYPE>(v[4], v[5]) | encode2<TYPE>(v[6], v[7]) << 16);
-        }
         __syncthreads();
         const int64_t mat_t = BLOCK ? group * p.K * static_cast<int64_t>(p.Mt) : 0;
 #pragma unroll
-        for (int f = tid; f < 128 * 8; f += kThreads) {
-            const int tc = f >> 3, part = f & 7;
+        for (int f = tid; f < 128 * 8; f += THREADS) {
+            const int tc = f >> 3, part = f & 7, tcc = tc >> 3;
             const int32_t k = kblock * 128 + tc, m = mtile * 128 + 16 * part;
-            const int at = (2 * part) ^ (tc >> 3) ^ (tc & 1);
-            const uint2 lo = s_t[tc * 16 + at], hi = s_t[tc * 16 + (at ^ 1)];
+            uint4 q = reinterpret_cast<const uint4 *>(s_t)[tc * 8 + (part ^ (tcc >> 1))];
+            if (tcc & 1) q = make_uint4(q.z, q.w, q.x, q.y);
             if (k < p.K && m < p.Mt)
-                *reinterpret_cast<uint4 *>(p.Q_t + mat_t + static_cast<int64_t>(k) * p.Mt + m) =
-                    make_uint4(lo.x, lo.y, hi.x, hi.y);
+                *reinterpret_cast<uint4 *>(p.Q_t + mat_t + static_cast<int64_t>(k) * p.Mt + m) = q;
         }
     }
 }
@@ -343,11 +339,12 @@ fp8_quantize_kernel(const QuantParams p)
 template <int TYPE, bool POW2, int WHAT, int R, bool GROUPED = false>
 int launch(const QuantParams &p, int64_t groups, cudaStream_t s)
 {
+    using C = QuantCfg<WHAT, R>;
     const int64_t tiles =
-        ((static_cast<int64_t>(p.M) + 16 * R - 1) / (16 * R) + (GROUPED ? p.groups : 0)) * p.tiles_k;
+        ((static_cast<int64_t>(p.M) + C::ROWS - 1) / C::ROWS + (GROUPED ? p.groups : 0)) * p.tiles_k;
     if (tiles > INT32_MAX) return QFP4_ERR_UNSUPPORTED;
     return launch_status(launch_pdl(fp8_quantize_kernel<TYPE, POW2, WHAT, R, GROUPED>,
-                                    dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(groups)), dim3(kThreads),
+                                    dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(groups)), dim3(C::THREADS),
                                     0, s, p));
 }
 
@@ -355,8 +352,8 @@ template <int TYPE, bool POW2>
 int launch_what(const QuantParams &p, int what, int64_t groups, cudaStream_t s)
 {
     if (p.groups)
-        return what & kRows ? launch<TYPE, POW2, kRows | kCols, 8, true>(p, groups, s)
-                            : launch<TYPE, POW2, kCols, 8, true>(p, groups, s);
+        return what & kRows ? launch<TYPE, POW2, kRows | kCols, 4, true>(p, groups, s)
+                            : launch<TYPE, POW2, kCols, 4, true>(p, groups, s);
     switch (what) {
     case kRows: return launch<TYPE, POW2, kRows, 2>(p, groups, s);
     case kCols: return launch<TYPE, POW2, kCols, 8>(p, groups, s);
