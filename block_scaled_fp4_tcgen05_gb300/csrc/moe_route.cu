@@ -54,7 +54,7 @@ struct RouteParams {
     // workspace: per chunk, counts [E] (int32), sums of p [E] (fp32); then
     // valid tokens per chunk
     int32_t *ws_counts;         // rows of E4 = E rounded up to 4
-    float *ws_prob;
+    float *ws_prob;             // the same
     int32_t *ws_valid;
 };
 
@@ -113,7 +113,7 @@ struct RouteShared {
             int32_t row[kWarps][kMaxExperts];       // counts, then next row, of each warp's pairs
             union {
                 int4 part[2][kThreads];             // partial sums over ranges, four experts each
-                float ppart[kThreads];
+                float4 ppart[kThreads];
             };
         };
     };
@@ -179,7 +179,7 @@ __device__ __forceinline__ void route_rows(const RouteParams &p, int64_t t0, int
         };
         uint32_t top = group_max(best);
         const float base = softmax_base(top);
-        float sum = 0.0f, chosen = 0.0f;
+        float sum = 0.0f;
         {
             float e[V];
 #pragma unroll
@@ -195,11 +195,11 @@ __device__ __forceinline__ void route_rows(const RouteParams &p, int64_t t0, int
             sum = inv;
         }
         int32_t my_id[kHold];
-        float my_x[kHold];
+        uint32_t my_key[kHold];
 #pragma unroll
         for (int h = 0; h < kHold; ++h) {
             my_id[h] = -1;
-            my_x[h] = 0.0f;
+            my_key[h] = 0u;
 #pragma unroll 1
             for (int i = 0; i < G; ++i) {
                 if (h * G + i >= p.topk) break;
@@ -218,11 +218,9 @@ __device__ __forceinline__ void route_rows(const RouteParams &p, int64_t t0, int
                 }
                 const int src = __ffs(who) - 1;
                 e = __shfl_sync(kFull, e, src, G);
-                const float xe = open ? __expf(key_value(top) - base) : 0.0f;
-                chosen = __fadd_rn(chosen, xe);
-                if (l == i) {
-                    my_id[h] = open ? static_cast<int32_t>(e) : -1;
-                    my_x[h] = xe;
+                if (l == i && open) {
+                    my_id[h] = static_cast<int32_t>(e);
+                    my_key[h] = top;
                 }
                 const bool mine = l == src;
                 if (mine && !known) {           // the lane's third and later: the largest after (best, at)
@@ -241,7 +239,15 @@ __device__ __forceinline__ void route_rows(const RouteParams &p, int64_t t0, int
                 known = known && !mine;
             }
         }
-        const float scale = !p.renorm ? sum : chosen == 0.0f ? 0.0f : __fdiv_rn(1.0f, chosen);
+        // the chosen experts' terms, and their sum where the gates are shares of it
+        float my_x[kHold], scale = 0.0f;
+#pragma unroll
+        for (int h = 0; h < kHold; ++h) {
+            my_x[h] = my_id[h] >= 0 ? __expf(key_value(my_key[h]) - base) : 0.0f;
+            scale = __fadd_rn(scale, my_x[h]);
+        }
+        scale = p.renorm ? group_sum(scale) : 0.0f;
+        scale = !p.renorm ? sum : scale == 0.0f ? 0.0f : __fdiv_rn(1.0f, scale);
 #pragma unroll
         for (int h = 0; h < kHold; ++h) {
             const int j = h * G + l;
@@ -307,7 +313,18 @@ __device__ __forceinline__ void route_place(const RouteParams &p, int64_t t0, in
     const int64_t f0 = t0 * p.topk, f1 = t1 * p.topk;
     const int64_t per_warp = ((f1 - f0 + kWarps - 1) / kWarps + 31) / 32 * 32;
     const int64_t w0 = min(f1, f0 + warp * per_warp), w1 = min(f1, w0 + per_warp);
-    for (int64_t f = w0 + lane; f < w1; f += 32) {
+    // the first pairs' experts stay in registers for the second pass
+    constexpr int kKeep = 4;
+    int32_t kept[kKeep];
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i) {
+        const int64_t f = w0 + 32 * i + lane;
+        kept[i] = f < w1 ? __ldcg(p.ids + f) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+        if (kept[i] >= 0) atomicAdd(&sh.row[warp][kept[i]], 1);
+    for (int64_t f = w0 + 32 * kKeep + lane; f < w1; f += 32) {
         const int32_t e = __ldcg(p.ids + f);
         if (e >= 0) atomicAdd(&sh.row[warp][e], 1);
     }
@@ -322,8 +339,7 @@ __device__ __forceinline__ void route_place(const RouteParams &p, int64_t t0, in
         }
     }
     __syncthreads();
-    for (int64_t f = w0; f < w1; f += 32) {
-        const int32_t e = f + lane < w1 ? __ldcg(p.ids + f + lane) : -1;
+    auto place = [&](int64_t f, int32_t e) {
         const uint32_t same = __match_any_sync(kFull, e);
         const int rank = __popc(same & ((1u << lane) - 1u));
         int32_t row = -1;
@@ -333,9 +349,13 @@ __device__ __forceinline__ void route_place(const RouteParams &p, int64_t t0, in
         __syncwarp();
         if (f + lane < w1) {
             p.dest[f + lane] = row;
-            if (row >= 0) p.src[row] = static_cast<int32_t>((f + lane) / p.topk);
+            if (row >= 0) p.src[row] = static_cast<int32_t>(static_cast<uint32_t>(f + lane) / static_cast<uint32_t>(p.topk));
         }
-    }
+    };
+#pragma unroll
+    for (int i = 0; i < kKeep; ++i)
+        if (w0 + 32 * i < w1) place(w0 + 32 * i, kept[i]);
+    for (int64_t f = w0 + 32 * kKeep; f < w1; f += 32) place(f, f + lane < w1 ? __ldcg(p.ids + f + lane) : -1);
 }
 
 // Totals, offsets, mean p and loss; prob = sum of expert tid's p over all tokens.
@@ -381,9 +401,7 @@ route_rows_kernel(const RouteParams p)
     const int64_t t0 = min(p.T, blockIdx.x * p.chunk), t1 = min(p.T, t0 + p.chunk);
     route_rows<L, G, V, WARPS>(p, t0, t1, sh);
     __syncthreads();
-    if (tid < p.E) {
-        p.ws_prob[static_cast<int64_t>(blockIdx.x) * p.E + tid] = route_prob<WARPS>(sh, tid);
-    }
+    if (tid < p.E) p.ws_prob[blockIdx.x * ((p.E + 3) / 4 * 4) + tid] = route_prob<WARPS>(sh, tid);
     if (tid < (p.E + 3) / 4)
         reinterpret_cast<int4 *>(p.ws_counts)[blockIdx.x * ((p.E + 3) / 4) + tid] = reinterpret_cast<const int4 *>(sh.counts)[tid];
     if (tid == 0) p.ws_valid[blockIdx.x] = sh.valid;
@@ -404,8 +422,25 @@ route_place_kernel(const RouteParams p, int chunks)
     pdl_wait();
     pdl_launch_dependents();
     int4 before = make_int4(0, 0, 0, 0), total = make_int4(0, 0, 0, 0);
+    float4 prob = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    constexpr int kLoads = (kMaxChunks + 7) / 8;                // (8 parts at 64 threads of width)
+    if (totals && e < e4) {
+        float4 n[kLoads];
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int c = part + i * parts;
+            n[i] = c < chunks ? __ldcg(reinterpret_cast<const float4 *>(p.ws_prob) + c * e4 + e)
+                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            prob.x = __fadd_rn(prob.x, n[i].x);
+            prob.y = __fadd_rn(prob.y, n[i].y);
+            prob.z = __fadd_rn(prob.z, n[i].z);
+            prob.w = __fadd_rn(prob.w, n[i].w);
+        }
+    }
     if (e < e4) {
-        constexpr int kLoads = (kMaxChunks + 7) / 8;            // (8 parts at 64 threads of width)
         int4 n[kLoads];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -448,14 +483,8 @@ route_place_kernel(const RouteParams p, int chunks)
         route_place(p, t0, min(p.T, t0 + p.chunk), sh);
         return;
     }
-    const int pwidth = 4 * width, pparts = kThreads / pwidth, pp = tid / pwidth, pe = tid % pwidth;
-    float s = 0.0f;
-    if (pe < p.E) {
-#pragma unroll 8
-        for (int c = pp; c < chunks; c += pparts) s = __fadd_rn(s, __ldcg(p.ws_prob + static_cast<int64_t>(c) * p.E + pe));
-    }
     __syncthreads();
-    sh.ppart[tid] = s;
+    sh.ppart[tid] = prob;
     if (tid < 32) {
         int32_t n = 0;
         for (int c = tid; c < chunks; c += 32) n += __ldcg(p.ws_valid + c);
@@ -463,9 +492,12 @@ route_place_kernel(const RouteParams p, int chunks)
         if (tid == 0) sh.valid = n;
     }
     __syncthreads();
-    s = 0.0f;
-    if (tid < p.E)
-        for (int i = 0; i < pparts; ++i) s = __fadd_rn(s, sh.ppart[i * pwidth + tid]);
+    float s = 0.0f;
+    if (tid < p.E) {
+        const float *pp = reinterpret_cast<const float *>(sh.ppart) + tid;
+#pragma unroll 8
+        for (int i = 0; i < parts; ++i) s = __fadd_rn(s, pp[i * width * 4]);
+    }
     route_totals(p, sh, sh.valid, s);
 }
 
@@ -640,7 +672,7 @@ extern "C" size_t qfp4_moe_route_workspace_bytes(int64_t T, int64_t E, int64_t t
     if (T < 0 || E < 1 || topk < 1 || !sizes_ok(T, E, topk)) return 0;
     const size_t chunks = static_cast<size_t>(chunk_count(T));
     const size_t E4 = static_cast<size_t>((E + 3) / 4 * 4);
-    return chunks * (E4 + static_cast<size_t>(E)) * 4 + chunks * 4;
+    return chunks * E4 * 8 + chunks * 4;
 }
 
 extern "C" int qfp4_moe_route(int logits_type, const void *logits, int64_t T, int64_t E, int64_t topk,
@@ -663,7 +695,7 @@ extern "C" int qfp4_moe_route(int logits_type, const void *logits, int64_t T, in
                   (T + chunks - 1) / chunks, ids, gates, counts, row_offsets, dest, src, n_valid, mean_prob, loss};
     p.ws_counts = static_cast<int32_t *>(workspace);
     p.ws_prob = reinterpret_cast<float *>(p.ws_counts + chunks * ((E + 3) / 4 * 4));
-    p.ws_valid = reinterpret_cast<int32_t *>(p.ws_prob + chunks * E);
+    p.ws_valid = reinterpret_cast<int32_t *>(p.ws_prob + chunks * ((E + 3) / 4 * 4));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return logits_type == QFP4_BF16 ? launch_forward<__nv_bfloat16>(p, static_cast<int>(chunks), s)
                                     : launch_forward<float>(p, static_cast<int>(chunks), s);
