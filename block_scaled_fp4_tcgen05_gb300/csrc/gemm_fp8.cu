@@ -6,27 +6,38 @@
 // from the next one's, each block's sum leaves tensor memory for registers,
 // where it is added under the fp32 product of its two scales.
 //
-// A cluster of two CTAs computes a 256 x 256 tile.  CTA r holds 128 rows of A
-// and 128 rows of B per K block (16 KB each, a ring of five); the leader issues
-// four M=256 N=256 K=32 MMAs per K block into one of two accumulator slots of
-// 256 columns, so that one is summed while the other is drained.  Eight
-// epilogue warps per CTA each keep 32 rows x 128 columns of D in registers
-// (128 per thread; the producer warps give theirs up with setmaxnreg).  A
-// thread owns one row, and its 128 columns are one block of B's scales, so the
-// scale is one number per thread and K block (COLSCALE: one per column).
+// A cluster of two CTAs computes a tile of 256 rows x TN = 256 columns (128
+// where that fills the last round of tiles better).  CTA r holds 128 rows of A
+// and TN / 2 rows of B per K block (a ring of four stages of 32 KB, or seven of
+// 24); the leader issues four M=256 N=TN K=32 MMAs per K block into one of 512 /
+// TN accumulator slots, so that one is summed while another is drained.  Two
+// warps issue them, for even and odd K blocks, so that one looks at its
+// barriers while the other's MMAs run (experts' product 490 -> 474 us).
+// Eight epilogue warps per CTA each keep 32 rows x TN / 2 columns of D in
+// registers (128 per thread; the producer warps give theirs up with
+// setmaxnreg).  A thread owns one row and its columns lie in one block of B's
+// scales, so the scale is one number per thread and K block (COLSCALE: one per
+// column).  D is staged in shared memory behind one fence and leaves by TMA.
 //
-// What bounds it is the epilogue's chain per K block: 32768 multiply-adds per
-// SM are 256 issue cycles of the 512 the MMAs take, beside four tensor-memory
-// loads per warp (72 cycles each alone) and the hand-overs (about 95 cycles for
-// a look at an mbarrier that is already complete).  So: loads of the next 32
-// columns run under the additions of the last; the next slot is looked at
-// before the last additions and judged after them; slots are given back with
-// relaxed arrivals straight at the leader; scales come through shared memory
-// from a warp of their own, eight K blocks at a time (loading them in the
-// epilogue warps themselves cost a global latency per K block: 1.7x slower);
-// plain multiply-adds, as the packed ones need more cycles per element
-// (measured 1.4 per element of a warp against 1.1: 278 us against 216 at
-// 4096 x 4096 x 14336); one slot per K block (two half as wide: 281 us).
+// What bounds it is the epilogue's chain per K block (about 870 cycles at TN =
+// 256, where the MMAs take 512) and, on long products, the power limit: 4096 x
+// 4096 x 14336 takes 211 us (2.28 PFLOP/s at 1.96 GHz and 1.36 kW); with the
+// multiply-adds left out 180, and with all of K summed in tensor memory, so
+// without any epilogue per block, 173 (at 1.75 GHz, the same power).  An SM's
+// 32768 multiply-adds per K block are 256 issue cycles, beside four
+// tensor-memory loads per warp (72 cycles each alone) and the hand-overs (about
+// 95 cycles for a look at an mbarrier that is already complete).  So: the second
+// half's loads run under the first half's additions; the next slot is looked
+// at before the last additions and judged after them; slots are given back
+// with relaxed arrivals straight at the leader; scales come through shared
+// memory from a warp of their own, eight K blocks at a time (loading them in
+// the epilogue warps themselves cost a global latency per K block).  Slower,
+// at the same product: packed multiply-adds (2.8 cycles for the two elements
+// of a pair against 1.1 each: 278 us where the plain ones took 216), sixteen
+// epilogue warps of 64 columns (230), two slots of 128 columns per K block
+// (281 where one of 256 took 241).  COLSCALE adds a multiply per element and
+// shared-memory reads of the columns' scales: 14336 x 4096 x 4096 with fp32
+// output takes 313 us, 197 without the multiply-adds.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>

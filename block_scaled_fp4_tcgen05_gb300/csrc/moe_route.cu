@@ -10,19 +10,25 @@
 //   chosen experts; g = p: [chosen] p_i dg_i - p_i sum_j p_j dg_j.
 //
 // Forward, two launches (one for few tokens).  route_rows_kernel: CTA c takes a
-// contiguous range of tokens.  Instructions bound it, and most of them would be
-// the k rounds of top-k, so a round serves several tokens at once: G lanes (4,
-// 8 or 16) share a token, each with up to 16 of its logits in registers.  Keys
-// are integers in the order of the logits; a lane keeps its best and second
-// best, so a round is a maximum over the G lanes, a vote for the lane that
-// holds it and that lane's next best (757 instructions per token of 256 experts
-// with a warp to itself, 18 us for 16384 of them).  A lane adds up its experts'
-// p over its tokens in registers.  The CTA's counts and its sum of p go to the
-// workspace.
+// contiguous range of tokens.  Instructions bound it, most of them in the k
+// rounds of top-k, so where experts are few a round serves several tokens: G
+// lanes (4, 8 or 32) share a token, each with up to 16 of its logits in
+// registers.  Keys are integers in the order of the logits; a lane keeps its
+// best and second best, so a round is a maximum over the G lanes, a vote for
+// the lane that holds it and that lane's next best.  A lane adds up its
+// experts' p over its tokens in registers.  The CTA's counts and its sum of p
+// go to the workspace.
 // route_place_kernel: each CTA adds up the counts of all ranges, so it knows
 // where each expert's rows begin and how many of them come from earlier
 // ranges, and ranks its own pairs in order; one more CTA writes the totals and
 // the loss.  All sums run in a fixed order: results repeat bit for bit.
+//
+// 16384 tokens x 256 experts, top 8, take 21 us (58 with keys searched anew in
+// every round and the ranges' counts added one after another), about 12 of
+// them in the first kernel at 0.75 of the issue slots; the second is a chain of
+// latencies (8 us together for 512 tokens).  64 tokens x 8 experts: 3.9 us in
+// one launch.  The gradient reads the logits once more and writes as much:
+// 16384 x 256 in 12 us (2.8 TB/s), its instructions likewise.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
