@@ -113,11 +113,13 @@ __device__ __forceinline__ void record_timeout()
 
 
 
-// Writes a warp's 32 rows x COLS columns of D; lane i holds row i.  The rows
-// are staged as boxes of 128 bytes x 32 rows in the 128-byte swizzle of the
-// store map (16-byte piece c of row r at c ^ (r % 8)), up to BOXES of them at
-// a time, and leave together behind one fence.
-template <bool FP32, int COLS, int BOXES>
+// Writes a warp's 32 rows x COLS columns of D.  Lane i holds row i, or with
+// PAIRS what tmem_ld_16x256b_x8 gives it: acc[32 (2 c + h) ..] are columns 64 c
+// .. 64 c + 63 of rows 16 h .. 16 h + 15.  The rows are staged as boxes of 128
+// bytes x 32 rows in the 128-byte swizzle of the store map (16-byte piece c of
+// row r at c ^ (r % 8)), up to BOXES of them at a time, and leave together
+// behind one fence.
+template <bool FP32, int COLS, int BOXES, bool PAIRS>
 __device__ __forceinline__ void store_tile(const float (&acc)[COLS], uint8_t *out, const CUtensorMap &map,
                                            const Fp8Params &p, bool by_tma, int32_t row0, int32_t rows, int32_t c0,
                                            int lane)
@@ -129,6 +131,29 @@ __device__ __forceinline__ void store_tile(const float (&acc)[COLS], uint8_t *ou
         // the boxes are free once the copy engine has read what left them last
         if (lane == 0) bulk_wait_group_read<0>();
         __syncwarp();
+        if constexpr (PAIRS) {
+#pragma unroll
+            for (int q = 0; q < BOXES; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int g = 0; g < kCols / 8; ++g)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            // two neighbouring columns of row r: eight or four bytes of a piece
+                            const int r = 16 * h + 8 * u + (lane >> 2);
+                            const int a = FP32 ? ((q0 + q) / 2 * 2 + h) * 32 + ((q0 + q) % 2 * 4 + g) * 4 + 2 * u
+                                               : ((q0 + q) * 2 + h) * 32 + g * 4 + 2 * u;
+                            uint8_t *row = out + q * kBoxBytes + r * 128;
+                            if (FP32) {
+                                *reinterpret_cast<float2 *>(row + 16 * ((2 * g + ((lane >> 1) & 1)) ^ (r & 7)) +
+                                                            8 * (lane & 1)) = make_float2(acc[a], acc[a + 1]);
+                            } else {
+                                *reinterpret_cast<__nv_bfloat162 *>(row + 16 * (g ^ (r & 7)) + 4 * (lane & 3)) =
+                                    __floats2bfloat162_rn(acc[a], acc[a + 1]);
+                            }
+                        }
+        } else {
 #pragma unroll
         for (int q = 0; q < BOXES; ++q)
 #pragma unroll
@@ -147,6 +172,7 @@ __device__ __forceinline__ void store_tile(const float (&acc)[COLS], uint8_t *ou
                 *reinterpret_cast<uint4 *>(out + q * kBoxBytes + lane * 128 + 16 * (c ^ (lane & 7))) =
                     make_uint4(w[0], w[1], w[2], w[3]);
             }
+        }
         if (by_tma) {
             fence_proxy_async_smem();
             __syncwarp();
@@ -479,39 +505,71 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                     done = mbar_test(smem_u32(&acc_full[slot]), phase);
                 };
                 uint32_t v[2][32];
-                tmem_ld_32x32b_x32(src, v[0]);
-                tmem_ld_32x32b_x32(src + 32, v[1]);
-                const float sm = COLSCALE ? sc[quad * 32 + lane] : sc[quad * 32 + lane] * sc[128 + (TN == 256 ? half : 0)];
-                auto add32 = [&](const uint32_t (&x)[32], int c) {
+                if constexpr (COLSCALE) {
+                    // 64 columns of 16 rows at a time: a thread then needs the scales of four rows and of a
+                    // quarter of the columns (all of them, for one row: the reads of shared memory alone
+                    // take longer than the MMAs)
+                    const uint32_t upper = src + (16u << 16);
+                    tmem_ld_16x256b_x8(src, v[0]);
+                    tmem_ld_16x256b_x8(upper, v[1]);
+                    const float *sr = sc + quad * 32 + (lane >> 2);
+                    const float rs[4] = {sr[0], sr[8], sr[16], sr[24]};
+                    auto add64 = [&](const uint32_t (&x)[32], int c, int h) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        float f[4] = {sm, sm, sm, sm};
-                        if (COLSCALE) {
-                            const float4 q = *reinterpret_cast<const float4 *>(sc + 128 + half * C::COLS + c * 32 + i);
-                            unpack_f32x2(mul_f32x2(pack_f32x2(q.x, q.y), pack_f32x2(sm, sm)), f[0], f[1]);
-                            unpack_f32x2(mul_f32x2(pack_f32x2(q.z, q.w), pack_f32x2(sm, sm)), f[2], f[3]);
+                        for (int g = 0; g < 8; ++g) {
+                            const float2 f = *reinterpret_cast<const float2 *>(sc + 128 + half * C::COLS + c * 64 + 8 * g +
+                                                                               2 * (lane & 3));
+                            float *y = acc + (2 * c + h) * 32 + 4 * g;
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                float lo, hi;
+                                unpack_f32x2(mul_f32x2(pack_b32x2(x[4 * g + 2 * u], x[4 * g + 2 * u + 1]),
+                                                       pack_f32x2(f.x, f.y)), lo, hi);
+                                y[2 * u] = fmaf(rs[2 * h + u], lo, y[2 * u]);
+                                y[2 * u + 1] = fmaf(rs[2 * h + u], hi, y[2 * u + 1]);
+                            }
                         }
-#pragma unroll
-                        for (int z = 0; z < 4; ++z)
-                            acc[c * 32 + i + z] = fmaf(f[z], __uint_as_float(x[i + z]), acc[c * 32 + i + z]);
-                    }
-                };
-                tmem_ld_wait();
-                tmem_regs_after_wait(v[0]);
-                tmem_regs_after_wait(v[1]);
-                if constexpr (TN == 256) {
-                    // the second half's loads run under the first half's additions
-                    add32(v[0], 0);
-                    tmem_ld_32x32b_x32(src + 64, v[0]);
-                    add32(v[1], 1);
-                    tmem_ld_32x32b_x32(src + 96, v[1]);
+                    };
                     tmem_ld_wait();
                     tmem_regs_after_wait(v[0]);
                     tmem_regs_after_wait(v[1]);
+                    if constexpr (TN == 256) {
+                        add64(v[0], 0, 0);
+                        tmem_ld_16x256b_x8(src + 64, v[0]);
+                        add64(v[1], 0, 1);
+                        tmem_ld_16x256b_x8(upper + 64, v[1]);
+                        tmem_ld_wait();
+                        tmem_regs_after_wait(v[0]);
+                        tmem_regs_after_wait(v[1]);
+                    }
+                    give_back();
+                    add64(v[0], TN == 256 ? 1 : 0, 0);
+                    add64(v[1], TN == 256 ? 1 : 0, 1);
+                } else {
+                    tmem_ld_32x32b_x32(src, v[0]);
+                    tmem_ld_32x32b_x32(src + 32, v[1]);
+                    const float sm = sc[quad * 32 + lane] * sc[128 + (TN == 256 ? half : 0)];
+                    auto add32 = [&](const uint32_t (&x)[32], int c) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(sm, __uint_as_float(x[i]), acc[c * 32 + i]);
+                    };
+                    tmem_ld_wait();
+                    tmem_regs_after_wait(v[0]);
+                    tmem_regs_after_wait(v[1]);
+                    if constexpr (TN == 256) {
+                        // the second half's loads run under the first half's additions
+                        add32(v[0], 0);
+                        tmem_ld_32x32b_x32(src + 64, v[0]);
+                        add32(v[1], 1);
+                        tmem_ld_32x32b_x32(src + 96, v[1]);
+                        tmem_ld_wait();
+                        tmem_regs_after_wait(v[0]);
+                        tmem_regs_after_wait(v[1]);
+                    }
+                    give_back();
+                    add32(v[0], TN == 256 ? 2 : 0);
+                    add32(v[1], TN == 256 ? 3 : 1);
                 }
-                give_back();
-                add32(v[0], TN == 256 ? 2 : 0);
-                add32(v[1], TN == 256 ? 3 : 1);
                 ready = __all_sync(0xffffffffu, done) && kb + 1 < ti.kblocks;
                 if (++u == kBatch || kb == ti.kblocks - 1) {
                     u = 0;
@@ -528,8 +586,8 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             const int32_t rows = ti.row_end - wrow0;
             if (rows > 0 && c0 < p.N) {
                 const bool by_tma = p.store_map && (!GROUPED || rows >= 32);
-                if (p.fp32) store_tile<true, C::COLS, C::BOXES>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
-                else store_tile<false, C::COLS, C::BOXES>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
+                if (p.fp32) store_tile<true, C::COLS, C::BOXES, COLSCALE>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
+                else store_tile<false, C::COLS, C::BOXES, COLSCALE>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
             }
             __syncwarp();
         }
