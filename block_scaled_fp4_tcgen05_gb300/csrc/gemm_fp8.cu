@@ -35,9 +35,15 @@
 // at the same product: packed multiply-adds (2.8 cycles for the two elements
 // of a pair against 1.1 each: 278 us where the plain ones took 216), sixteen
 // epilogue warps of 64 columns (230), two slots of 128 columns per K block
-// (281 where one of 256 took 241).  COLSCALE adds a multiply per element and
-// shared-memory reads of the columns' scales: 14336 x 4096 x 4096 with fp32
-// output takes 313 us, 197 without the multiply-adds.
+// (281 where one of 256 took 241).
+//
+// COLSCALE adds a multiply per element and reads of the columns' scales from
+// shared memory.  With a thread per row those reads alone, a wavefront's worth
+// of returned data per column and warp, take longer than the MMAs; reading
+// tensor memory 16 rows x 64 columns at a time a thread needs the scales of a
+// quarter of the columns, and packed arithmetic then pays (fewer instructions
+// bound it): 14336 x 4096 x 4096 with fp32 output takes 279 us (314 with a thread
+// per row, 296 with plain multiply-adds, 251 without the stores).
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -514,22 +520,25 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                     tmem_ld_16x256b_x8(upper, v[1]);
                     const float *sr = sc + quad * 32 + (lane >> 2);
                     const float rs[4] = {sr[0], sr[8], sr[16], sr[24]};
+                    uint64_t cs[8];             // scales of column pairs of 64 columns
+                    auto columns = [&](int c) {
+#pragma unroll
+                        for (int g = 0; g < 8; ++g)
+                            cs[g] = *reinterpret_cast<const uint64_t *>(sc + 128 + half * C::COLS + c * 64 + 8 * g +
+                                                                        2 * (lane & 3));
+                    };
                     auto add64 = [&](const uint32_t (&x)[32], int c, int h) {
 #pragma unroll
-                        for (int g = 0; g < 8; ++g) {
-                            const float2 f = *reinterpret_cast<const float2 *>(sc + 128 + half * C::COLS + c * 64 + 8 * g +
-                                                                               2 * (lane & 3));
-                            float *y = acc + (2 * c + h) * 32 + 4 * g;
+                        for (int g = 0; g < 8; ++g)
 #pragma unroll
                             for (int u = 0; u < 2; ++u) {
-                                float lo, hi;
-                                unpack_f32x2(mul_f32x2(pack_b32x2(x[4 * g + 2 * u], x[4 * g + 2 * u + 1]),
-                                                       pack_f32x2(f.x, f.y)), lo, hi);
-                                y[2 * u] = fmaf(rs[2 * h + u], lo, y[2 * u]);
-                                y[2 * u + 1] = fmaf(rs[2 * h + u], hi, y[2 * u + 1]);
+                                const int a = (2 * c + h) * 32 + 4 * g + 2 * u;
+                                const uint64_t t = mul_f32x2(pack_b32x2(x[4 * g + 2 * u], x[4 * g + 2 * u + 1]), cs[g]);
+                                const uint64_t r = pack_f32x2(rs[2 * h + u], rs[2 * h + u]);
+                                unpack_f32x2(fma_f32x2(r, t, pack_f32x2(acc[a], acc[a + 1])), acc[a], acc[a + 1]);
                             }
-                        }
                     };
+                    columns(0);
                     tmem_ld_wait();
                     tmem_regs_after_wait(v[0]);
                     tmem_regs_after_wait(v[1]);
@@ -538,6 +547,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                         tmem_ld_16x256b_x8(src + 64, v[0]);
                         add64(v[1], 0, 1);
                         tmem_ld_16x256b_x8(upper + 64, v[1]);
+                        columns(1);
                         tmem_ld_wait();
                         tmem_regs_after_wait(v[0]);
                         tmem_regs_after_wait(v[1]);
