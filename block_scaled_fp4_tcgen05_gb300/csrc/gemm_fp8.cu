@@ -21,29 +21,29 @@
 //
 // What bounds it is the epilogue's chain per K block (about 870 cycles at TN =
 // 256, where the MMAs take 512) and, on long products, the power limit: 4096 x
-// 4096 x 14336 takes 211 us (2.28 PFLOP/s at 1.96 GHz and 1.36 kW); with the
-// multiply-adds left out 180, and with all of K summed in tensor memory, so
-// without any epilogue per block, 173 (at 1.75 GHz, the same power).  An SM's
-// 32768 multiply-adds per K block are 256 issue cycles, beside four
-// tensor-memory loads per warp (72 cycles each alone) and the hand-overs (about
-// 95 cycles for a look at an mbarrier that is already complete).  So: the second
-// half's loads run under the first half's additions; the next slot is looked
-// at before the last additions and judged after them; slots are given back
-// with relaxed arrivals straight at the leader; scales come through shared
+// 4096 x 14336 takes 207 us (2.33 PFLOP/s; 1.36 kW); with the multiply-adds
+// left out 180, and with all of K summed in tensor memory, so without any
+// epilogue per block, 173 (at 1.75 GHz, the same power).  An SM's 32768
+// multiply-adds per K block are 128 packed instructions per scheduler, beside
+// four tensor-memory loads per warp (72 cycles each alone) and the hand-overs
+// (about 95 cycles for a look at an mbarrier that is already complete).  So:
+// the second half's loads run under the first half's additions; the next slot
+// is looked at before the last additions and judged after them; slots are given
+// back with relaxed arrivals straight at the leader; scales come through shared
 // memory from a warp of their own, eight K blocks at a time (loading them in
-// the epilogue warps themselves cost a global latency per K block).  Slower,
-// at the same product: packed multiply-adds (2.8 cycles for the two elements
-// of a pair against 1.1 each: 278 us where the plain ones took 216), sixteen
-// epilogue warps of 64 columns (230), two slots of 128 columns per K block
-// (281 where one of 256 took 241).
+// the epilogue warps themselves cost a global latency per K block); the
+// multiply-adds are packed in pairs (212 us with single ones).  Slower, at the
+// same product: the next block's first load ahead of the last additions (214
+// against 207), sixteen epilogue warps of 64 columns (230 against 216), two
+// slots of 128 columns per K block (281 where one of 256 took 241).
 //
 // COLSCALE adds a multiply per element and reads of the columns' scales from
 // shared memory.  With a thread per row those reads alone, a wavefront's worth
 // of returned data per column and warp, take longer than the MMAs; reading
 // tensor memory 16 rows x 64 columns at a time a thread needs the scales of a
-// quarter of the columns, and packed arithmetic then pays (fewer instructions
-// bound it): 14336 x 4096 x 4096 with fp32 output takes 279 us (314 with a thread
-// per row, 296 with plain multiply-adds, 251 without the stores).
+// quarter of the columns, and packed arithmetic then pays (fewer
+// instructions): 14336 x 4096 x 4096 with fp32 output takes 280 us (314 with a
+// thread per row, 296 with plain multiply-adds, 251 without the stores).
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -559,9 +559,12 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                     tmem_ld_32x32b_x32(src, v[0]);
                     tmem_ld_32x32b_x32(src + 32, v[1]);
                     const float sm = sc[quad * 32 + lane] * sc[128 + (TN == 256 ? half : 0)];
+                    const uint64_t sm2 = pack_f32x2(sm, sm);
                     auto add32 = [&](const uint32_t (&x)[32], int c) {
+                        float *d = acc + c * 32;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) acc[c * 32 + i] = fmaf(sm, __uint_as_float(x[i]), acc[c * 32 + i]);
+                        for (int i = 0; i < 32; i += 2)
+                            unpack_f32x2(fma_f32x2(sm2, pack_b32x2(x[i], x[i + 1]), pack_f32x2(d[i], d[i + 1])), d[i], d[i + 1]);
                     };
                     tmem_ld_wait();
                     tmem_regs_after_wait(v[0]);
@@ -673,12 +676,14 @@ int launch_gemm_fp8(const Fp8Params &p, cudaStream_t s)
     if (narrow > INT32_MAX / 2) return QFP4_ERR_UNSUPPORTED;
     const int64_t pairs = sm_count() / 2;
     if (pairs < 1) return QFP4_ERR_CUDA;
-    // Tiles 128 columns wide cost 0.55 to 0.6 of the time of one 256 wide (0.7
-    // with column scales), so they pay where they fill the last round better:
-    // 1531 x 4100 x 2000 takes 21.1 us in three rounds of narrow tiles and
-    // 22.6 in two of wide ones; 4096 x 4096 x 14336 223 in seven, 210 in four.
-    const int64_t narrow_cost = (narrow + pairs - 1) / pairs * (p.b_rows == 1 ? 7 : 6);
-    return narrow_cost < (wide + pairs - 1) / pairs * 10 ? launch_width<128>(p, narrow, s)
+    // Tiles 128 columns wide cost 0.65 of the time of one 256 wide, with either
+    // form of B's scales (4096 x 4864 x 4096: 78.8 us in eight rounds of narrow
+    // tiles, 62.6 in four of wide ones; fp32 with column scales 123.6 and 96.5),
+    // so they pay where they fill the last round better: 1536 x 4864 x 4096 takes
+    // 32.2 us in three rounds of narrow tiles and 33.0 in two of wide ones (49.0
+    // and 50.1), 768 x 4864 x 4096 22.6 in two and 18.8 in one (33.7 and 27.4).
+    const int64_t narrow_cost = (narrow + pairs - 1) / pairs * 13;
+    return narrow_cost < (wide + pairs - 1) / pairs * 20 ? launch_width<128>(p, narrow, s)
                                                          : launch_width<256>(p, wide, s);
 }
 
