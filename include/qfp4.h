@@ -87,7 +87,8 @@ int qfp4_device_check(void);
  * QFP4_OK; QFP4_ERR_TIMEOUT if any kernel of this library gave up on a
  * bounded wait since the last poll (its outputs are then undefined); or
  * QFP4_ERR_INVALID_ARG if a grouped call found its device row_offsets
- * unusable (see qfp4_global_scale_grouped) and wrote nothing. */
+ * unusable (see qfp4_global_scale_grouped) and wrote nothing, or a gathering
+ * call met a row index beyond its input (see qfp4_fp8_quantize). */
 int qfp4_poll_device_status(void *stream);
 
 /* ---------------------------------------------------------------------- */
@@ -580,8 +581,9 @@ int qfp4_fp8_quantize_weight(int type, int scale, int64_t groups, const void *W_
  * in fp32 registers with the scales applied in fp32.  Every result repeats bit
  * for bit.
  * Requirements: K % 16 == 0; M, N, K <= 2^30; A, B, D 16-byte aligned, scales
- * 4-byte.  M == 0 or N == 0 launches nothing; K == 0 gives D = 0 (accumulate:
- * D unchanged).
+ * 4-byte; D of no more than about 2^30 tiles of 256 x 128 (QFP4_ERR_UNSUPPORTED).
+ * M == 0 or N == 0 launches nothing; K == 0 gives D = 0 (accumulate: D
+ * unchanged).
  * Accuracy: |D - exact| <= u |exact| + (ceil(K/128) + 18) 2^-24 T, with T the
  * sum of the terms' magnitudes and u = 2^-8 (BF16) or 2^-24 (FP32, where the
  * accumulated D counts as part of exact). */
