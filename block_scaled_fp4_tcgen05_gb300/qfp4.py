@@ -353,17 +353,33 @@ def gemm_swiglu_quantize_grouped(fmt, row_offsets, total_rows, I, K, A, A_sf, W,
 
 def _at(t, dtype=None):
     """Address of a whole row-major matrix on the GPU (a strided view or a host
-    tensor would be read as something else), of the given type."""
-    if t is None or isinstance(t, int):
-        return t
+    tensor would be read as something else), of the given type.  A router call
+    has fifteen of these: the usual path asks each question once."""
+    if t is None:
+        return None
+    try:
+        if t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):
+            return t
+        raise
     if not (t.is_cuda and t.is_contiguous()):
         raise ValueError("qfp4: tensors must be contiguous and on the GPU")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"qfp4: expected {dtype}, got {t.dtype}")
-    return t.data_ptr()
+    raise ValueError(f"qfp4: expected {dtype}, got {t.dtype}")
 
 
 _F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+_CODES = {E4M3: (torch.float8_e4m3fn, torch.uint8), E5M2: (torch.float8_e5m2, torch.uint8)}
+
+
+def _codes(t, kind):
+    """Address of a matrix of 8-bit codes: of that type, or plain bytes."""
+    if t is None or isinstance(t, int):
+        return t
+    if kind in _CODES and t.dtype not in _CODES[kind]:
+        raise ValueError(f"qfp4: expected codes of {_CODES[kind][0]}, got {t.dtype}")
+    return _at(t)
 
 
 def fp8_quantize(type, X, Q=None, SF=None, Q_t=None, SF_t=None, scale=SCALE_FP32, row_index=None, stream=None) -> None:
@@ -374,8 +390,9 @@ def fp8_quantize(type, X, Q=None, SF=None, Q_t=None, SF_t=None, scale=SCALE_FP32
     rows, K = X.shape
     M = rows if row_index is None else row_index.numel()
     _check("qfp4_fp8_quantize",
-           load().qfp4_fp8_quantize(type, scale, _at(X, _BF16), rows, _at(row_index, _I32), M, K, _at(Q), _at(SF, _F32),
-                                    _at(Q_t), _at(SF_t, _F32), _stream(stream)))
+           load().qfp4_fp8_quantize(type, scale, _at(X, _BF16), rows, _at(row_index, _I32), M, K,
+                                    _codes(Q, type), _at(SF, _F32), _codes(Q_t, type), _at(SF_t, _F32),
+                                    _stream(stream)))
 
 
 def fp8_grouped_cols(total_rows: int, groups: int) -> int:
@@ -392,8 +409,8 @@ def fp8_quantize_grouped(type, X, row_offsets, Q_t, SF_t, Q=None, SF=None, scale
     groups = row_offsets.numel() - 1
     _check("qfp4_fp8_quantize_grouped",
            load().qfp4_fp8_quantize_grouped(type, scale, _at(X, _BF16), rows, _at(row_index, _I32), groups,
-                                            _at(row_offsets, _I32), M, K, _at(Q), _at(SF, _F32), _at(Q_t),
-                                            _at(SF_t, _F32), _stream(stream)))
+                                            _at(row_offsets, _I32), M, K, _codes(Q, type), _at(SF, _F32),
+                                            _codes(Q_t, type), _at(SF_t, _F32), _stream(stream)))
 
 
 def fp8_quantize_weight(type, W, Q, SF, Q_t=None, SF_t=None, scale=SCALE_FP32, stream=None) -> None:
@@ -401,8 +418,8 @@ def fp8_quantize_weight(type, W, Q, SF, Q_t=None, SF_t=None, scale=SCALE_FP32, s
     block, and optionally their transpose (Q_t [.., K, ceil16(N)])."""
     groups, (N, K) = (1 if W.dim() == 2 else W.shape[0]), W.shape[-2:]
     _check("qfp4_fp8_quantize_weight",
-           load().qfp4_fp8_quantize_weight(type, scale, groups, _at(W, _BF16), N, K, _at(Q), _at(SF, _F32), _at(Q_t),
-                                           _at(SF_t, _F32), _stream(stream)))
+           load().qfp4_fp8_quantize_weight(type, scale, groups, _at(W, _BF16), N, K, _codes(Q, type),
+                                           _at(SF, _F32), _codes(Q_t, type), _at(SF_t, _F32), _stream(stream)))
 
 
 def gemm_nt_fp8(a_type, b_type, M, N, K, A, A_sf, B, B_sf, D, b_rows=128, out=OUT_BF16, accumulate=False,
@@ -410,9 +427,9 @@ def gemm_nt_fp8(a_type, b_type, M, N, K, A, A_sf, B, B_sf, D, b_rows=128, out=OU
     """D = A B^T with a scale per 128 elements of K: A_sf [ceil(K/128), M], B_sf
     per 128 x 128 block (b_rows=128) or [ceil(K/128), N] (b_rows=1)."""
     _check("qfp4_gemm_nt_fp8",
-           load().qfp4_gemm_nt_fp8(a_type, b_type, M, N, K, _at(A), _at(A_sf, _F32), _at(B), _at(B_sf, _F32), b_rows,
-                                   out, 1 if accumulate else 0, _at(D, _F32 if out == OUT_FP32 else _BF16),
-                                   _stream(stream)))
+           load().qfp4_gemm_nt_fp8(a_type, b_type, M, N, K, _codes(A, a_type), _at(A_sf, _F32), _codes(B, b_type),
+                                   _at(B_sf, _F32), b_rows, out, 1 if accumulate else 0,
+                                   _at(D, _F32 if out == OUT_FP32 else _BF16), _stream(stream)))
 
 
 def gemm_nt_fp8_grouped(a_type, b_type, row_offsets, total_rows, max_group_rows, N, K, A, A_sf, B, B_sf, D,
@@ -421,8 +438,9 @@ def gemm_nt_fp8_grouped(a_type, b_type, row_offsets, total_rows, max_group_rows,
     groups = row_offsets.numel() - 1
     _check("qfp4_gemm_nt_fp8_grouped",
            load().qfp4_gemm_nt_fp8_grouped(a_type, b_type, groups, _at(row_offsets, _I32), total_rows, max_group_rows,
-                                           N, K, _at(A), _at(A_sf, _F32), _at(B), _at(B_sf, _F32), out,
-                                           _at(D, _F32 if out == OUT_FP32 else _BF16), _stream(stream)))
+                                           N, K, _codes(A, a_type), _at(A_sf, _F32), _codes(B, b_type),
+                                           _at(B_sf, _F32), out, _at(D, _F32 if out == OUT_FP32 else _BF16),
+                                           _stream(stream)))
 
 
 def gemm_nt_fp8_kgrouped(a_type, b_type, row_offsets, total_rows, M, N, A, A_sf, B, B_sf, D, accumulate=False,
@@ -431,9 +449,9 @@ def gemm_nt_fp8_kgrouped(a_type, b_type, row_offsets, total_rows, M, N, A, A_sf,
     fp8_quantize_grouped gave group e; D fp32 [groups, M, N]."""
     groups = row_offsets.numel() - 1
     _check("qfp4_gemm_nt_fp8_kgrouped",
-           load().qfp4_gemm_nt_fp8_kgrouped(a_type, b_type, groups, _at(row_offsets, _I32), total_rows, M, N, _at(A),
-                                            _at(A_sf, _F32), _at(B), _at(B_sf, _F32), 1 if accumulate else 0,
-                                            _at(D, _F32), _stream(stream)))
+           load().qfp4_gemm_nt_fp8_kgrouped(a_type, b_type, groups, _at(row_offsets, _I32), total_rows, M, N,
+                                            _codes(A, a_type), _at(A_sf, _F32), _codes(B, b_type), _at(B_sf, _F32),
+                                            1 if accumulate else 0, _at(D, _F32), _stream(stream)))
 
 
 def moe_route_workspace_bytes(T: int, E: int, topk: int) -> int:

@@ -157,3 +157,11 @@ def test_binding_refuses_what_the_abi_cannot_see(lib):
         qfp4.fp8_quantize(qfp4.E4M3, x, x, x)                       # on the host
     with pytest.raises(ValueError):
         qfp4.moe_route_backward(x.t(), x, x, x, None, None, x)      # strided
+
+
+def test_binding_refuses_codes_of_another_type(lib):
+    x = torch.zeros(32, 64, dtype=torch.bfloat16)
+    e4m3, e5m2 = (torch.zeros(32, 64, dtype=t) for t in (torch.float8_e4m3fn, torch.float8_e5m2))
+    for a_type, a in ((qfp4.E4M3, e5m2), (qfp4.E5M2, e4m3), (qfp4.E4M3, x)):
+        with pytest.raises(ValueError, match="codes"):      # the other arguments are addresses
+            qfp4.gemm_nt_fp8(a_type, qfp4.E4M3, 32, 32, 64, a, 16, 16, 16, 16)
