@@ -28,7 +28,8 @@
 // them in the first kernel at 0.75 of the issue slots; the second is a chain of
 // latencies (8 us together for 512 tokens).  64 tokens x 8 experts: 3.9 us in
 // one launch.  The gradient reads the logits once more and writes as much:
-// 16384 x 256 in 12 us (2.8 TB/s), its instructions likewise.
+// 16384 x 256 in 8.5 us (3.9 TB/s), 16384 x 64 BF16 in 4.2 (12.6 and 8.0 with a
+// warp per token); its instructions bound it likewise.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -42,6 +43,7 @@ constexpr int kMaxExperts = 256;
 constexpr int kMaxTopk = 16;
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kBackThreads = 256;
 constexpr int kMaxRowWarps = 32;            // of the CTAs that read the logits: 16, or 32 where a warp has one token
 constexpr int kMaxChunks = 152;             // one CTA on each SM
 constexpr uint32_t kFull = 0xffffffffu;
@@ -77,6 +79,14 @@ __device__ __forceinline__ float key_value(uint32_t k)
     return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
+// The larger one; NaN where either is.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 __device__ __forceinline__ float load_logit(const float *p) { return __ldg(p); }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16 *p) { return __bfloat162float(__ldg(p)); }
 __device__ __forceinline__ void store_logit(float *p, float v) { *p = v; }
@@ -88,24 +98,10 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// x = exp(l - base) of the lane's experts, base the row's largest logit (0 for
-// a row with no open expert); returns 1 / their sum over the row (0 for such a
-// row).  A NaN or +inf logit makes base, or a difference with it, and so the
-// sum, NaN.  exp is 2^(x log2 e) by the hardware's exponential: the rounded
-// product costs |x| 2^-24 relative, the exponential 2^-22.
-template <int V>
-__device__ __forceinline__ float softmax_terms(const float (&l)[V], int E, int lane, float base, float (&x)[V])
-{
-    float sum = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        x[v] = lane + 32 * v < E ? __expf(l[v] - base) : 0.0f;
-        sum += x[v];
-    }
-    sum = warp_sum(sum);
-    return sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
-}
-
+// base of exp(l - base): the row's largest logit, 0 for a row with no open
+// expert.  A NaN or +inf logit makes base, or a difference with it, and so the
+// row's sum, NaN.  exp is 2^(x log2 e) by the hardware's exponential: the
+// rounded product costs |x| 2^-24 relative, the exponential 2^-22.
 __device__ __forceinline__ float softmax_base(uint32_t top) { return top <= kKeyNegInf ? 0.0f : key_value(top); }
 
 struct RouteShared {
@@ -548,79 +544,134 @@ struct BackParams {
     void *dlogits;
 };
 
-template <typename L, int V>
-__global__ void __launch_bounds__(kThreads)
+// G lanes per token, V experts per lane, in runs of P (pairs of BF16 logits
+// move as one word: 16384 x 64 in 4.2 us, 4.6 one by one; not for an odd E,
+// whose rows are not aligned to them).  The chosen experts' elements are
+// written twice: with the others, then by the lane that holds the choice and
+// knows its p.  Adding the gates' part to the owner's register instead takes
+// top-k rounds of V comparisons.
+template <typename L, int G, int V, int P>
+__global__ void __launch_bounds__(kBackThreads)
 route_backward_kernel(const BackParams p)
 {
+    constexpr int kTokens = 32 / G;
+    constexpr int kHold = (kMaxTopk + G - 1) / G;
+    __shared__ float share[kMaxExperts];        // s_e
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int l = lane % G;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kBackThreads / 32) * kTokens;
+    int64_t tw = (static_cast<int64_t>(blockIdx.x) * (kBackThreads / 32) + warp) * kTokens;
     pdl_wait();
     pdl_launch_dependents();
-    // s_e = dloss E c_e / (k n^2)
-    float s[V];
+    float x[V];
+    bool here, valid;
+    int64_t t;
+    auto load_row = [&]() {
+        t = tw + lane / G;
+        here = t < p.T;
+        valid = here && (!p.valid || p.valid[t] != 0);
+        const L *row = static_cast<const L *>(p.logits) + t * p.E + l * P;
+#pragma unroll
+        for (int v = 0; v < V; v += P) {
+            const bool open = valid && l * P + G * v < p.E;
+            if constexpr (P == 2) {
+                const float2 two = open ? __bfloat1622float2(__ldg(reinterpret_cast<const __nv_bfloat162 *>(row + G * v)))
+                                        : make_float2(-INFINITY, -INFINITY);
+                x[v] = two.x;
+                x[v + 1] = two.y;
+            } else {
+                x[v] = open ? load_logit(row + G * v) : -INFINITY;
+            }
+        }
+    };
+    load_row();
     {
+        // s_e = dloss E c_e / (k n^2)
         const float n = static_cast<float>(max(p.n_valid[0], 1));
         const float f = p.dloss ? __fdiv_rn(__fdiv_rn(p.dloss[0] * static_cast<float>(p.E), n), static_cast<float>(p.topk) * n) : 0.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = lane + 32 * v;
-            s[v] = e < p.E ? f * static_cast<float>(p.counts[e]) : 0.0f;
-        }
+        for (int e = threadIdx.x; e < kMaxExperts; e += kBackThreads)
+            share[e] = e < p.E ? f * static_cast<float>(p.counts[e]) : 0.0f;
     }
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kWarps;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < p.T; t += stride) {
-        L *out = static_cast<L *>(p.dlogits) + t * p.E;
-        if (p.valid && p.valid[t] == 0) {
+    __syncthreads();
+    float s[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (lane + 32 * v < p.E) store_logit(out + lane + 32 * v, 0.0f);
-            continue;
+    for (int v = 0; v < V; ++v) s[v] = share[l * P + G * (v / P * P) + v % P];
+    auto group_sum = [](float a) {
+#pragma unroll
+        for (int d = G / 2; d > 0; d >>= 1) a = __fadd_rn(a, __shfl_xor_sync(kFull, a, d));
+        return a;
+    };
+    for (; tw < p.T; tw += stride, load_row()) {
+        // choices l, l + G, ... of the token
+        int32_t id[kHold];
+        float dg[kHold], chosen[kHold];
+#pragma unroll
+        for (int h = 0; h < kHold; ++h) {
+            const int j = h * G + l;
+            id[h] = valid && p.dgates && j < p.topk ? p.ids[t * p.topk + j] : -1;
+            if (id[h] >= p.E) id[h] = -1;
+            dg[h] = id[h] >= 0 ? p.dgates[t * p.topk + j] : 0.0f;
+            chosen[h] = id[h] >= 0 ? load_logit(static_cast<const L *>(p.logits) + t * p.E + id[h]) : -INFINITY;
         }
-        const L *row = static_cast<const L *>(p.logits) + t * p.E;
-        float l[V], x[V], h[V];
-        uint32_t best = 0u;
+        float top = x[0];
+#pragma unroll
+        for (int v = 1; v < V; ++v) top = max_nan(top, x[v]);
+        uint32_t best = sort_key(top);
+        if constexpr (G == 32) {
+            best = __reduce_max_sync(kFull, best);
+        } else {
+#pragma unroll
+            for (int d = G / 2; d > 0; d >>= 1) best = max(best, __shfl_xor_sync(kFull, best, d));
+        }
+        const float base = softmax_base(best);
+        float sum = 0.0f, dot = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = lane + 32 * v;
-            l[v] = e < p.E ? load_logit(row + e) : -INFINITY;
-            best = max(best, sort_key(l[v]));
+            x[v] = __expf(x[v] - base);         // (0 where there is no expert)
+            sum += x[v];
         }
-        // lane j < k: choice j
-        int32_t id = p.dgates && lane < p.topk ? p.ids[t * p.topk + lane] : -1;
-        if (id >= p.E) id = -1;
-        const float dg = id >= 0 ? p.dgates[t * p.topk + lane] : 0.0f;
-        const float lj = id >= 0 ? load_logit(row + id) : 0.0f;
-        const float base = softmax_base(__reduce_max_sync(kFull, best));
-        const float inv = softmax_terms<V>(l, p.E, lane, base, x);
-        float dot = 0.0f;
+        sum = group_sum(sum);
+        const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             x[v] *= inv;
             dot = fmaf(x[v], s[v], dot);
-            h[v] = 0.0f;
         }
-        dot = warp_sum(dot);
+        dot = group_sum(dot);
         if (p.dgates) {
-            const float pj = id >= 0 ? __expf(lj - base) * inv : 0.0f;
-            float g = pj;
-            if (p.renorm) {
-                const float total = warp_sum(pj);
-                g = total == 0.0f ? 0.0f : __fdiv_rn(pj, total);
+            float total = 0.0f, gd = 0.0f, g[kHold];
+#pragma unroll
+            for (int h = 0; h < kHold; ++h) {
+                chosen[h] = __expf(chosen[h] - base) * inv;
+                total = __fadd_rn(total, id[h] >= 0 ? chosen[h] : 0.0f);
             }
-            const float gd = warp_sum(g * dg);
-            const float hj = p.renorm ? g * (dg - gd) : g * dg;
+            if (p.renorm) total = group_sum(total);
+#pragma unroll
+            for (int h = 0; h < kHold; ++h) {
+                g[h] = id[h] < 0 ? 0.0f : !p.renorm ? chosen[h] : total == 0.0f ? 0.0f : __fdiv_rn(chosen[h], total);
+                gd = fmaf(g[h], dg[h], gd);
+            }
+            gd = group_sum(gd);
             if (!p.renorm) dot += gd;
-            for (int j = 0; j < p.topk; ++j) {
-                const int32_t e = __shfl_sync(kFull, id, j);
-                const float a = __shfl_sync(kFull, hj, j);
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (lane + 32 * v == e) h[v] += a;
-            }
+            for (int h = 0; h < kHold; ++h) dg[h] = p.renorm ? g[h] * (dg[h] - gd) : g[h] * dg[h];
         }
+        L *out = static_cast<L *>(p.dlogits) + t * p.E;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = lane + 32 * v;
-            if (e < p.E) store_logit(out + e, fmaf(x[v], s[v] - dot, h[v]));
+        for (int v = 0; v < V; v += P) {
+            if (!here || l * P + G * v >= p.E) continue;
+            const float a = valid ? fmaf(x[v], s[v] - dot, 0.0f) : 0.0f;
+            if constexpr (P == 2)
+                *reinterpret_cast<__nv_bfloat162 *>(out + l * P + G * v) =
+                    __floats2bfloat162_rn(a, valid ? fmaf(x[v + 1], s[v + 1] - dot, 0.0f) : 0.0f);
+            else
+                store_logit(out + l + G * v, a);
+        }
+        if (p.dgates) {
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < kHold; ++h)
+                if (id[h] >= 0) store_logit(out + id[h], fmaf(chosen[h], share[id[h]] - dot, dg[h]));
         }
     }
 }
@@ -646,14 +697,25 @@ int launch_forward(const RouteParams &p, int chunks, cudaStream_t s)
     return launch_route<L, 32, 8>(p, chunks, s);
 }
 
-template <typename L>
-int launch_back(const BackParams &p, unsigned ctas, cudaStream_t s)
+template <typename L, int G, int V>
+int launch_back_width(const BackParams &p, cudaStream_t s)
 {
-    const dim3 g(ctas), b(kThreads);
-    if (p.E <= 32) return launch_status(launch_pdl(route_backward_kernel<L, 1>, g, b, 0, s, p));
-    if (p.E <= 64) return launch_status(launch_pdl(route_backward_kernel<L, 2>, g, b, 0, s, p));
-    if (p.E <= 128) return launch_status(launch_pdl(route_backward_kernel<L, 4>, g, b, 0, s, p));
-    return launch_status(launch_pdl(route_backward_kernel<L, 8>, g, b, 0, s, p));
+    const int64_t tokens = kBackThreads / G;
+    const int64_t want = (p.T + tokens - 1) / tokens, most = static_cast<int64_t>(kMaxChunks) * (2048 / kBackThreads);
+    const dim3 g(static_cast<unsigned>(want < most ? want : most)), b(kBackThreads);
+    if constexpr (sizeof(L) == 2)
+        if (p.E % 2 == 0) return launch_status(launch_pdl(route_backward_kernel<L, G, V, 2>, g, b, 0, s, p));
+    return launch_status(launch_pdl(route_backward_kernel<L, G, V, 1>, g, b, 0, s, p));
+}
+
+template <typename L>
+int launch_back(const BackParams &p, cudaStream_t s)
+{
+    if (p.E <= 16) return launch_back_width<L, 4, 4>(p, s);
+    if (p.E <= 32) return launch_back_width<L, 4, 8>(p, s);
+    if (p.E <= 64) return launch_back_width<L, 8, 8>(p, s);
+    if (p.E <= 128) return launch_back_width<L, 16, 8>(p, s);
+    return launch_back_width<L, 32, 8>(p, s);
 }
 
 bool sizes_ok(int64_t T, int64_t E, int64_t topk)
@@ -722,8 +784,6 @@ extern "C" int qfp4_moe_route_backward(int logits_type, const void *logits, int6
         return QFP4_ERR_MISALIGNED;
     const BackParams p{logits, valid, T, static_cast<int32_t>(E), static_cast<int32_t>(topk), renorm ? 1 : 0,
                        ids, counts, n_valid, dgates, dloss, dlogits};
-    const int64_t want = (T + kWarps - 1) / kWarps;
-    const unsigned ctas = static_cast<unsigned>(want < 4 * 152 ? want : 4 * 152);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return logits_type == QFP4_BF16 ? launch_back<__nv_bfloat16>(p, ctas, s) : launch_back<float>(p, ctas, s);
+    return logits_type == QFP4_BF16 ? launch_back<__nv_bfloat16>(p, s) : launch_back<float>(p, s);
 }
