@@ -15,14 +15,15 @@
 // CTAs in order (the results repeat bit for bit, and no scratch in global
 // memory is needed).
 //
-// The weights' bytes are the floor.  One token x 14336 x 4096 takes 11.9 us
-// (4.9 TB/s) and 4096 x 4096 4.7 to 6.1; 128 tokens x 14336 x 4096 take 14.9 us
+// The weights' bytes are the floor.  One token x 14336 x 4096 takes 11.8 us
+// (4.9 TB/s) and 4096 x 4096 5.8 (5.1 from L2); 128 tokens x 14336 x 4096 15.0
 // (4.2 TB/s): there a K block's 128 x 128 MMAs, whose operands take all of
 // shared memory's bandwidth (about 115 cycles each), set the pace.  Grouped,
 // 8 experts x 14336 x 4096: 74 us with 2 rows each (6.4 TB/s), 97 with 16.
 //
 // Warps: 0 TMA producer, 1 and 3 MMA issuers (1 owns tensor memory), 2 scales,
 // 4.. epilogue (four of all columns, or sixteen of 32 each).
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -449,30 +450,86 @@ int64_t most_rows(const Fp8Params &p)
     return p.groups && p.max_group_rows > 0 && p.max_group_rows < p.M ? p.max_group_rows : p.M;
 }
 
+// Clusters of `splits` CTAs of the 128 x 128 form that the current device holds
+// at once (0 where it cannot say), asked once per device and size.
+int clusters_at_once(int splits)
+{
+    static std::atomic<int> known[64][kMaxSplits + 1];      // the answer + 1
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    const int seen = known[dev][splits].load(std::memory_order_relaxed);
+    if (seen > 0) return seen - 1;
+    using C = SmallCfg<128>;
+    const void *kern = reinterpret_cast<const void *>(gemm_fp8_small_kernel<128, false, false>);
+    int n = 0;
+    if (ensure_smem_attr(kern, C::SMEM) == QFP4_OK) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(splits);
+        cfg.blockDim = dim3(C::THREADS);
+        cfg.dynamicSmemBytes = C::SMEM;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = static_cast<unsigned>(splits);
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            n = 0;
+            cudaGetLastError();
+        }
+    }
+    known[dev][splits].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
+struct Plan {
+    int nt, splits;
+    int64_t tiles;
+};
+
+// K is split while each CTA keeps two K blocks or more and the CTAs run at
+// once.  128 x 128: one per SM, and the clusters have to fit as such (16 of
+// eight do not: 128 x 2048 x 2048 took 12.8 us with eight splits, 6.4 with
+// four).  Few rows: a second CTA per SM pays with eight K blocks for each (1 x
+// 7168 x 4096 6.4 us in 224 CTAs, 6.9 in 112; 1 x 4096 x 4096 5.4 us in 256, 5.1
+// in 128).
+Plan plan(const Fp8Params &p)
+{
+    const int64_t rows = most_rows(p), sms = sm_count();
+    Plan r;
+    r.nt = rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
+    r.tiles = static_cast<int64_t>((p.N + 127) / 128) * ((rows + r.nt - 1) / r.nt) * (p.groups ? p.groups : 1);
+    r.splits = 1;
+    const int64_t kblocks = (static_cast<int64_t>(p.K) + 127) / 128;
+    while (r.splits < kMaxSplits && kblocks >= 4 * r.splits) {
+        const int64_t ctas = r.tiles * 2 * r.splits;
+        if (r.nt == 128 ? ctas > sms || r.tiles > clusters_at_once(2 * r.splits)
+                        : ctas > (kblocks >= 16 * r.splits ? 2 * sms : sms))
+            break;
+        r.splits *= 2;
+    }
+    return r;
+}
+
 }  // namespace
 
-// Up to 128 rows always (per group, as far as the host can tell); more where
-// the 256 x 256 tiles would take up less than half of the SMs (512 x 4096 x
-// 4096, 32 such tiles on 76 pairs: 13.8 us here; 64 tiles: 19 us there).
+// Up to 128 rows always (per group, as far as the host can tell).  More where K
+// is split: a CTA then has half the K blocks of a pair's 256 x 128 tile (256 x
+// 4096 x 14336 takes 23 us here and 34 there).  Unsplit the pair is as fast or
+// faster (512 x 4096 x 14336 39 us here, 35 there; fp32 with column scales 76
+// and 54).
 bool gemm_fp8_small_pays(const Fp8Params &p)
 {
-    if (most_rows(p) <= 128) return true;
-    const int64_t pairs = static_cast<int64_t>((p.M + 255) / 256) * ((p.N + 255) / 256);
-    return !p.groups && pairs < sm_count() / 4;
+    return most_rows(p) <= 128 || (!p.groups && plan(p).splits > 1);
 }
 
 int launch_gemm_fp8_small(const Fp8Params &p, cudaStream_t s)
 {
-    const int64_t rows = most_rows(p);
-    const int nt = rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
-    const int64_t tiles = static_cast<int64_t>((p.N + 127) / 128) * ((rows + nt - 1) / nt) * (p.groups ? p.groups : 1);
-    const int64_t kblocks = (static_cast<int64_t>(p.K) + 127) / 128;
-    // split K while the CTAs still fit on the GPU at once (two per SM for few
-    // rows) and each keeps two K blocks or more
-    const int64_t room = static_cast<int64_t>(sm_count()) * (nt == 128 ? 1 : 2);
-    if (tiles > INT32_MAX / kMaxSplits) return QFP4_ERR_UNSUPPORTED;
-    int splits = 1;
-    while (splits < kMaxSplits && tiles * splits * 2 <= room && kblocks >= 4 * splits) splits *= 2;
+    const Plan plan = qfp4::plan(p);
+    if (plan.tiles > INT32_MAX / kMaxSplits) return QFP4_ERR_UNSUPPORTED;
+    const int64_t rows = most_rows(p), tiles = plan.tiles;
+    const int nt = plan.nt, splits = plan.splits;
     const int32_t max_rows = static_cast<int32_t>(rows);
     switch (nt) {
     case 16: return launch_nt<16>(p, tiles, splits, max_rows, s);
