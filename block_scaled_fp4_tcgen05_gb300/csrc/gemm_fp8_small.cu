@@ -514,14 +514,22 @@ Plan plan(const Fp8Params &p)
 
 }  // namespace
 
-// Up to 128 rows always (per group, as far as the host can tell).  More where K
-// is split: a CTA then has half the K blocks of a pair's 256 x 128 tile (256 x
+// Up to 32 rows always (per group, as far as the host can tell).  Up to 128 but
+// for many tiles of a short K, whose beginnings and ends the pairs' persistent
+// loop hides (64 groups of 128 rows x 2048 x 768: 51 us here, 39 there; 128 x
+// 131072 x 512: 39 and 25; with fewer rounds or a longer K the pairs' tiles,
+// half of them padding, lose: 128 x 65536 x 4096 63 and 68, 8 groups of 128 rows
+// x 4096 x 2048 20 and 24).  More where K is split: a CTA then has half the K blocks of a pair's 256 x 128 tile (256 x
 // 4096 x 14336 takes 23 us here and 34 there).  Unsplit the pair is as fast or
 // faster (512 x 4096 x 14336 39 us here, 35 there; fp32 with column scales 76
 // and 54).
 bool gemm_fp8_small_pays(const Fp8Params &p)
 {
-    return most_rows(p) <= 128 || (!p.groups && plan(p).splits > 1);
+    const int64_t rows = most_rows(p);
+    if (rows <= 32) return true;
+    const Plan r = plan(p);
+    if (rows <= 128) return r.tiles <= 3 * sm_count() || p.K > 16 * 128;
+    return !p.groups && r.splits > 1;
 }
 
 int launch_gemm_fp8_small(const Fp8Params &p, cudaStream_t s)

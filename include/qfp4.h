@@ -595,7 +595,9 @@ int qfp4_gemm_nt_fp8(int a_type, int b_type, int64_t M, int64_t N, int64_t K,
  * with B[e].  B [groups][N][K], B_sf [groups][ceil(N/128)][ceil(K/128)].
  * row_offsets, total_rows and max_group_rows as in qfp4_gemm_nt_grouped, but
  * row_offsets[groups] may be below total_rows (tokens that the router dropped
- * leave the last rows unused): the rows of D beyond it are left untouched.
+ * leave the last rows unused): the rows of D beyond it are left untouched.  A
+ * bound on the groups' rows (T after qfp4_moe_route, whose choices of a token
+ * differ) lets small batches take the kernel for few rows.
  * Requirements as qfp4_gemm_nt_fp8, 1 <= groups <= 256, groups * N <= 2^30. */
 int qfp4_gemm_nt_fp8_grouped(int a_type, int b_type, int64_t groups, const int32_t *row_offsets,
                              int64_t total_rows, int64_t max_group_rows, int64_t N, int64_t K,

@@ -284,7 +284,7 @@ def test_product(M, N, K, b_rows):
 
 
 # sixteen tiles of 128 x 128 (their clusters of eight do not run at once), K split in two and not split, both widths
-@pytest.mark.parametrize("M,N,K", [(128, 2048, 2048), (512, 512, 2048), (300, 1664, 512), (384, 4096, 256), (600, 2560, 384)])
+@pytest.mark.parametrize("M,N,K", [(128, 2048, 2048), (512, 512, 2048), (300, 1664, 512), (384, 4096, 256), (600, 2560, 384), (40, 60000, 256)])
 @pytest.mark.parametrize("b_rows", [128, 1])
 def test_product_however_k_is_split(M, N, K, b_rows):
     product(qfp4.E4M3, qfp4.E4M3, M, N, K, b_rows, b_rows == 1, N)
