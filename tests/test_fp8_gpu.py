@@ -373,6 +373,13 @@ def test_grouped(offsets, N, K, fp32, unused):
         assert bool((d[used:] == 7.0).all())
 
 
+@pytest.mark.parametrize("fp32", [False, True])
+def test_grouped_many_tiles_of_a_short_sum(fp32):
+    """Groups of up to 128 rows, more tiles than three rounds: bounded, by pairs of CTAs."""
+    rows = [(37 * i) % 129 for i in range(64)]
+    test_grouped([sum(rows[:i]) for i in range(65)], 1100, 272, fp32, 5)
+
+
 @pytest.mark.parametrize("offsets,most", [([1, 4, 8], 0), ([0, 6, 4], 0), ([0, 4, 9], 0), ([0, -2, 8], 0), ([0, 2, 8], 5)])
 def test_grouped_refuses_bad_offsets(offsets, most):
     K, N, rows = 128, 128, 8
