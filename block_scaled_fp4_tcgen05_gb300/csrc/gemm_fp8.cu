@@ -558,6 +558,10 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
                 } else {
                     tmem_ld_32x32b_x32(src, v[0]);
                     tmem_ld_32x32b_x32(src + 32, v[1]);
+                    // The product of the scales has to be a normal number (the header says so).  Taking them
+                    // one after the other costs a multiply per element; to do so only where the product is
+                    // none, decided by a vote per K block here or by the scales' warp, 3 to 5% of the time of
+                    // every product (4096 x 4096 x 14336: 207 us instead of 201)
                     const float sm = sc[quad * 32 + lane] * sc[128 + (TN == 256 ? half : 0)];
                     const uint64_t sm2 = pack_f32x2(sm, sm);
                     auto add32 = [&](const uint32_t (&x)[32], int c) {

@@ -286,15 +286,13 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
             bool done = false;
 #pragma unroll
             for (int c = 0; c < C::COLS / kLd; ++c) {
-                // the products of the scales (the first ones while the loads are under way)
-                float f[kLd];
+                // the columns' scales (the first ones while the loads are under way)
+                float q[kLd];
+                if constexpr (kColumns) {
 #pragma unroll
-                for (int i = 0; i < kLd; i += 4) {
-                    f[i] = f[i + 1] = f[i + 2] = f[i + 3] = row;
-                    if (kColumns) {
-                        const float4 q = *reinterpret_cast<const float4 *>(sc + 128 + c0 + c * kLd + i);
-                        unpack_f32x2(mul_f32x2(pack_f32x2(q.x, q.y), pack_f32x2(row, row)), f[i], f[i + 1]);
-                        unpack_f32x2(mul_f32x2(pack_f32x2(q.z, q.w), pack_f32x2(row, row)), f[i + 2], f[i + 3]);
+                    for (int i = 0; i < kLd; i += 4) {
+                        const float4 four = *reinterpret_cast<const float4 *>(sc + 128 + c0 + c * kLd + i);
+                        q[i] = four.x; q[i + 1] = four.y; q[i + 2] = four.z; q[i + 3] = four.w;
                     }
                 }
                 if (c == 0) {
@@ -309,8 +307,20 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
                     if (slot == 0) phase ^= 1;
                     done = mbar_test(smem_u32(&acc_full[slot]), phase);
                 }
+                if constexpr (kColumns) {
+                    // the column's scale meets the sum first, the row's the result: their product alone need
+                    // not be a normal number where the term is one.  It costs nothing (100 rows x 4096 x 4096
+                    // with a scale per row 9.7 us, 11.0 with the scales multiplied ahead of the loads' end)
 #pragma unroll
-                for (int i = 0; i < kLd; ++i) acc[c * kLd + i] = fmaf(f[i], __uint_as_float(v[c][i]), acc[c * kLd + i]);
+                    for (int i = 0; i < kLd; i += 2) {
+                        float lo, hi;
+                        unpack_f32x2(mul_f32x2(pack_b32x2(v[c][i], v[c][i + 1]), pack_f32x2(q[i], q[i + 1])), lo, hi);
+                        v[c][i] = __float_as_uint(lo);
+                        v[c][i + 1] = __float_as_uint(hi);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kLd; ++i) acc[c * kLd + i] = fmaf(row, __uint_as_float(v[c][i]), acc[c * kLd + i]);
             }
             ready = __all_sync(0xffffffffu, done);
             if (++u == kBatch || j == nkb - 1) {

@@ -584,9 +584,16 @@ int qfp4_fp8_quantize_weight(int type, int scale, int64_t groups, const void *W_
  * 4-byte; D of no more than about 2^30 tiles of 256 x 128 (QFP4_ERR_UNSUPPORTED).
  * M == 0 or N == 0 launches nothing; K == 0 gives D = 0 (accumulate: D
  * unchanged).
- * Accuracy: |D - exact| <= u |exact| + (ceil(K/128) + 18) 2^-24 T, with T the
- * sum of the terms' magnitudes and u = 2^-8 (BF16) or 2^-24 (FP32, where the
- * accumulated D counts as part of exact). */
+ * Accuracy: |D - exact| <= u |exact| + (ceil(K/128) + 18) 2^-24 T + z, with T
+ * the sum of the terms' magnitudes, u = 2^-8 (BF16) or 2^-24 (FP32, where the
+ * accumulated D counts as part of exact) and z the steps of numbers below
+ * 2^-126: 2^-134 (BF16) or (ceil(K/128) + 2) 2^-149 (FP32).  It holds where the
+ * magnitudes of a block's scales lie in [2^-94, 2^88] and, with b_rows = 128,
+ * that of their product in [2^-126, 2^128): the quantisers' scales do for blocks
+ * whose largest magnitude lies in [2^-47, 2^72].  With b_rows = 128 a smaller
+ * product keeps fewer bits or is zero, and a larger one gives infinities (NaN
+ * where the block's sum is zero).  A block of zero codes adds nothing under any
+ * scales whose product is finite. */
 int qfp4_gemm_nt_fp8(int a_type, int b_type, int64_t M, int64_t N, int64_t K,
                      const void *A, const float *A_sf, const void *B, const float *B_sf, int b_rows,
                      int out_type, int accumulate, void *D, void *stream);
