@@ -354,6 +354,11 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
     __syncwarp();
     tc_fence_before();
     if (splits > 1) cluster_sync_all(); else __syncthreads();
+    if (*abort_flag) {
+        // let copies and MMAs already in flight drain before the memory goes
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) { }
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, C::TMEM_COLS);
@@ -412,10 +417,6 @@ gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmM, const __grid_cons
     // no CTA may leave while another still reads its sums
     __syncwarp();
     if (splits > 1) cluster_sync_all();
-    if (*abort_flag) {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 1000000ull) { }
-    }
 }
 
 template <int NT, bool PER_ROW, bool GROUPED>
