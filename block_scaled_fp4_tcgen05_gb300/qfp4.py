@@ -351,14 +351,16 @@ def gemm_swiglu_quantize_grouped(fmt, row_offsets, total_rows, I, K, A, A_sf, W,
                                                     _p(Q_out), _p(SF_out), _stream(stream)))
 
 
-def _at(t, dtype=None):
+def _at(t, dtype, least=0):
     """Address of a whole row-major matrix on the GPU (a strided view or a host
-    tensor would be read as something else), of the given type.  A router call
-    has fifteen of these: the usual path asks each question once."""
+    tensor would be read as something else), of the given type and with at least
+    so many elements (the C ABI sees an address and cannot tell: a kernel would
+    write past a shorter one's end).  A router call has fifteen of these: the
+    usual path asks each question once."""
     if t is None:
         return None
     try:
-        if t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        if t.dtype is dtype and t.is_cuda and t.numel() >= least and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         if isinstance(t, int):
@@ -366,20 +368,28 @@ def _at(t, dtype=None):
         raise
     if not (t.is_cuda and t.is_contiguous()):
         raise ValueError("qfp4: tensors must be contiguous and on the GPU")
-    raise ValueError(f"qfp4: expected {dtype}, got {t.dtype}")
+    if t.dtype is not dtype:
+        raise ValueError(f"qfp4: expected {dtype}, got {t.dtype}")
+    raise ValueError(f"qfp4: expected at least {least} elements, got {t.numel()} ({tuple(t.shape)})")
 
 
 _F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
 _CODES = {E4M3: (torch.float8_e4m3fn, torch.uint8), E5M2: (torch.float8_e5m2, torch.uint8)}
 
 
-def _codes(t, kind):
+def _codes(t, kind, least=0):
     """Address of a matrix of 8-bit codes: of that type, or plain bytes."""
-    if t is None or isinstance(t, int):
-        return t
+    if t is None:
+        return None
+    try:
+        if t.dtype in _CODES[kind] and t.is_cuda and t.numel() >= least and t.is_contiguous():
+            return t.data_ptr()
+    except (AttributeError, KeyError):      # an address; a type that the library refuses
+        if isinstance(t, int):
+            return t
     if kind in _CODES and t.dtype not in _CODES[kind]:
         raise ValueError(f"qfp4: expected codes of {_CODES[kind][0]}, got {t.dtype}")
-    return _at(t)
+    return _at(t, t.dtype, least)
 
 
 def fp8_quantize(type, X, Q=None, SF=None, Q_t=None, SF_t=None, scale=SCALE_FP32, row_index=None, stream=None) -> None:
@@ -391,7 +401,8 @@ def fp8_quantize(type, X, Q=None, SF=None, Q_t=None, SF_t=None, scale=SCALE_FP32
     M = rows if row_index is None else row_index.numel()
     _check("qfp4_fp8_quantize",
            load().qfp4_fp8_quantize(type, scale, _at(X, _BF16), rows, _at(row_index, _I32), M, K,
-                                    _codes(Q, type), _at(SF, _F32), _codes(Q_t, type), _at(SF_t, _F32),
+                                    _codes(Q, type, M * K), _at(SF, _F32, (K + 127) // 128 * M),
+                                    _codes(Q_t, type, K * ((M + 15) // 16 * 16)), _at(SF_t, _F32, (M + 127) // 128 * K),
                                     _stream(stream)))
 
 
@@ -407,40 +418,49 @@ def fp8_quantize_grouped(type, X, row_offsets, Q_t, SF_t, Q=None, SF=None, scale
     rows, K = X.shape
     M = rows if row_index is None else row_index.numel()
     groups = row_offsets.numel() - 1
+    cols = fp8_grouped_cols(M, groups)
     _check("qfp4_fp8_quantize_grouped",
            load().qfp4_fp8_quantize_grouped(type, scale, _at(X, _BF16), rows, _at(row_index, _I32), groups,
-                                            _at(row_offsets, _I32), M, K, _codes(Q, type), _at(SF, _F32),
-                                            _codes(Q_t, type), _at(SF_t, _F32), _stream(stream)))
+                                            _at(row_offsets, _I32), M, K, _codes(Q, type, M * K),
+                                            _at(SF, _F32, (K + 127) // 128 * M), _codes(Q_t, type, K * cols),
+                                            _at(SF_t, _F32, cols // 128 * K), _stream(stream)))
 
 
 def fp8_quantize_weight(type, W, Q, SF, Q_t=None, SF_t=None, scale=SCALE_FP32, stream=None) -> None:
     """Weights W [N, K] or [groups, N, K] -> codes with a scale per 128 x 128
     block, and optionally their transpose (Q_t [.., K, ceil16(N)])."""
     groups, (N, K) = (1 if W.dim() == 2 else W.shape[0]), W.shape[-2:]
+    blocks = groups * ((N + 127) // 128) * ((K + 127) // 128)
     _check("qfp4_fp8_quantize_weight",
-           load().qfp4_fp8_quantize_weight(type, scale, groups, _at(W, _BF16), N, K, _codes(Q, type),
-                                           _at(SF, _F32), _codes(Q_t, type), _at(SF_t, _F32), _stream(stream)))
+           load().qfp4_fp8_quantize_weight(type, scale, groups, _at(W, _BF16, groups * N * K), N, K,
+                                           _codes(Q, type, groups * N * K), _at(SF, _F32, blocks),
+                                           _codes(Q_t, type, groups * K * ((N + 15) // 16 * 16)),
+                                           _at(SF_t, _F32, blocks), _stream(stream)))
 
 
 def gemm_nt_fp8(a_type, b_type, M, N, K, A, A_sf, B, B_sf, D, b_rows=128, out=OUT_BF16, accumulate=False,
                 stream=None) -> None:
     """D = A B^T with a scale per 128 elements of K: A_sf [ceil(K/128), M], B_sf
     per 128 x 128 block (b_rows=128) or [ceil(K/128), N] (b_rows=1)."""
+    blocks = (K + 127) // 128
     _check("qfp4_gemm_nt_fp8",
-           load().qfp4_gemm_nt_fp8(a_type, b_type, M, N, K, _codes(A, a_type), _at(A_sf, _F32), _codes(B, b_type),
-                                   _at(B_sf, _F32), b_rows, out, 1 if accumulate else 0,
-                                   _at(D, _F32 if out == OUT_FP32 else _BF16), _stream(stream)))
+           load().qfp4_gemm_nt_fp8(a_type, b_type, M, N, K, _codes(A, a_type, M * K), _at(A_sf, _F32, blocks * M),
+                                   _codes(B, b_type, N * K), _at(B_sf, _F32, blocks * (N if b_rows == 1 else (N + 127) // 128)),
+                                   b_rows, out, 1 if accumulate else 0,
+                                   _at(D, _F32 if out == OUT_FP32 else _BF16, M * N), _stream(stream)))
 
 
 def gemm_nt_fp8_grouped(a_type, b_type, row_offsets, total_rows, max_group_rows, N, K, A, A_sf, B, B_sf, D,
                         out=OUT_BF16, stream=None) -> None:
     """One product per expert: rows [row_offsets[e], row_offsets[e+1]) with B[e]."""
     groups = row_offsets.numel() - 1
+    blocks = (K + 127) // 128
     _check("qfp4_gemm_nt_fp8_grouped",
            load().qfp4_gemm_nt_fp8_grouped(a_type, b_type, groups, _at(row_offsets, _I32), total_rows, max_group_rows,
-                                           N, K, _codes(A, a_type), _at(A_sf, _F32), _codes(B, b_type),
-                                           _at(B_sf, _F32), out, _at(D, _F32 if out == OUT_FP32 else _BF16),
-                                           _stream(stream)))
+                                           N, K, _codes(A, a_type, total_rows * K), _at(A_sf, _F32, blocks * total_rows),
+                                           _codes(B, b_type, groups * N * K),
+                                           _at(B_sf, _F32, groups * ((N + 127) // 128) * blocks), out,
+                                           _at(D, _F32 if out == OUT_FP32 else _BF16, total_rows * N), _stream(stream)))
 
 
 def gemm_nt_fp8_kgrouped(a_type, b_type, row_offsets, total_rows, M, N, A, A_sf, B, B_sf, D, accumulate=False,
@@ -448,10 +468,12 @@ def gemm_nt_fp8_kgrouped(a_type, b_type, row_offsets, total_rows, M, N, A, A_sf,
     """Every expert's weight gradient: D[e] (+)= A_e B_e^T over the columns that
     fp8_quantize_grouped gave group e; D fp32 [groups, M, N]."""
     groups = row_offsets.numel() - 1
+    cols = fp8_grouped_cols(total_rows, groups)
     _check("qfp4_gemm_nt_fp8_kgrouped",
            load().qfp4_gemm_nt_fp8_kgrouped(a_type, b_type, groups, _at(row_offsets, _I32), total_rows, M, N,
-                                            _codes(A, a_type), _at(A_sf, _F32), _codes(B, b_type), _at(B_sf, _F32),
-                                            1 if accumulate else 0, _at(D, _F32), _stream(stream)))
+                                            _codes(A, a_type, M * cols), _at(A_sf, _F32, cols // 128 * M),
+                                            _codes(B, b_type, N * cols), _at(B_sf, _F32, cols // 128 * N),
+                                            1 if accumulate else 0, _at(D, _F32, groups * M * N), _stream(stream)))
 
 
 def moe_route_workspace_bytes(T: int, E: int, topk: int) -> int:
@@ -468,11 +490,13 @@ def moe_route(logits, topk, ids, gates, counts, row_offsets, dest, src, n_valid,
     """Top-k experts of each token, gates, per-expert counts and row order, and
     the balance loss; valid is uint8 [T] or None."""
     T, E = logits.shape
+    pairs = T * topk
     _check("qfp4_moe_route",
-           load().qfp4_moe_route(*_logits(logits), T, E, topk, _at(valid, _U8), 1 if renorm else 0, _at(ids, _I32),
-                                 _at(gates, _F32), _at(counts, _I32), _at(row_offsets, _I32), _at(dest, _I32),
-                                 _at(src, _I32), _at(n_valid, _I32), _at(mean_prob, _F32), _at(loss, _F32),
-                                 _at(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+           load().qfp4_moe_route(*_logits(logits), T, E, topk, _at(valid, _U8, T), 1 if renorm else 0,
+                                 _at(ids, _I32, pairs), _at(gates, _F32, pairs), _at(counts, _I32, E),
+                                 _at(row_offsets, _I32, E + 1), _at(dest, _I32, pairs), _at(src, _I32, pairs),
+                                 _at(n_valid, _I32, 1), _at(mean_prob, _F32, E), _at(loss, _F32, 1),
+                                 _at(workspace, workspace.dtype), workspace.nbytes, _stream(stream)))
 
 
 def moe_route_backward(logits, ids, counts, n_valid, dgates, dloss, dlogits, valid=None, renorm=True,
@@ -480,7 +504,10 @@ def moe_route_backward(logits, ids, counts, n_valid, dgates, dloss, dlogits, val
     """dlogits of (gates . dgates + dloss * loss), choices and counts held fixed;
     dgates and dloss may be None."""
     T, E = logits.shape
+    topk = ids.shape[1]
+    pairs = T * topk
     _check("qfp4_moe_route_backward",
-           load().qfp4_moe_route_backward(*_logits(logits), T, E, ids.shape[1], _at(valid, _U8), 1 if renorm else 0,
-                                          _at(ids, _I32), _at(counts, _I32), _at(n_valid, _I32), _at(dgates, _F32),
-                                          _at(dloss, _F32), _at(dlogits, logits.dtype), _stream(stream)))
+           load().qfp4_moe_route_backward(*_logits(logits), T, E, topk, _at(valid, _U8, T), 1 if renorm else 0,
+                                          _at(ids, _I32, pairs), _at(counts, _I32, E), _at(n_valid, _I32, 1),
+                                          _at(dgates, _F32, pairs), _at(dloss, _F32, 1), _at(dlogits, logits.dtype, T * E),
+                                          _stream(stream)))
