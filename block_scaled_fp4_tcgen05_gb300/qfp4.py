@@ -145,10 +145,15 @@ def status_string(status: int) -> str:
     return load().qfp4_status_string(int(status)).decode()
 
 
+def _torch_stream(device) -> int:
+    return torch.cuda.current_stream().cuda_stream      # on a torch without CUDA: its own error
+
+
 # The current stream's handle, without building a torch Stream around it
-# (0.1 us instead of 3).
-_current_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# (0.1 us instead of 3).  A torch built without CUDA has neither lookup, and
+# what needs no GPU (sizes, refusals, status texts) works there too.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _torch_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", lambda: 0)
 
 
 def _p(t) -> int | None:
