@@ -1,9 +1,11 @@
 // api.cu -- library-wide entry points of libqfp4: version, status text,
 // device check and the device status poll.
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 #include <mutex>
 #include <set>
+#include <thread>
 #include <utility>
 
 #include "qfp4_common.cuh"
@@ -43,6 +45,59 @@ int ensure_smem_attr(const void *kern, int bytes)
     return QFP4_OK;
 }
 
+namespace {
+
+// The status poll: one launch takes every kernel's word and leaves zero (in one
+// atomic step: a word set once is reported once, whichever poll meets it), and
+// one copy brings the result back: 19 us instead of 142 with a copy and a wait to
+// read and as much to clear each word.
+constexpr int kWords = 8;
+constexpr int (*kWordOf[kWords])(uint32_t **) = {
+    status_word_quant,       status_word_gemm,     status_word_gemm_pair,      status_word_gemm_decode,
+    status_word_gemm_sparse, status_word_gemm_fp8, status_word_gemm_fp8_small, status_word_fp8_quant};
+
+struct StatusWords {
+    uint32_t *word[kWords];
+};
+
+constexpr int kPollSlots = 32;
+__device__ uint32_t g_poll_results[kPollSlots];
+
+__global__ void gather_status_kernel(const StatusWords w, uint32_t *result)
+{
+    const int i = threadIdx.x;
+    uint32_t v = 0;
+#pragma unroll
+    for (int k = 0; k < kWords; ++k)
+        if (i == k) v = atomicExch(w.word[k], 0u);
+    v = __reduce_or_sync(0xffffffffu, v);
+    if (i == 0) *result = v;
+}
+
+// Where a poll's result waits to be copied: one of its own for each poll under
+// way (another thread's would overwrite it).
+struct PollSlot {
+    int index = 0;
+
+    PollSlot()
+    {
+        while (taken()[index].exchange(true, std::memory_order_acquire)) {
+            if (++index == kPollSlots) {
+                index = 0;
+                std::this_thread::yield();
+            }
+        }
+    }
+    ~PollSlot() { taken()[index].store(false, std::memory_order_release); }
+
+    static std::atomic<bool> *taken()
+    {
+        static std::atomic<bool> t[kPollSlots];
+        return t;
+    }
+};
+
+}  // namespace
 }  // namespace qfp4
 
 extern "C" int qfp4_version(void) { return 100; }   // 0.1.0
@@ -74,19 +129,26 @@ extern "C" int qfp4_device_check(void)
 
 extern "C" int qfp4_poll_device_status(void *stream)
 {
+    using namespace qfp4;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    uint32_t q = 0, g = 0, gp = 0, gd = 0, gs = 0, g8 = 0, s8 = 0, q8 = 0;
-    int rc = qfp4::read_clear_status_quant(s, &q);
-    if (rc == QFP4_OK) rc = qfp4::read_clear_status_gemm(s, &g);
-    if (rc == QFP4_OK) rc = qfp4::read_clear_status_gemm_pair(s, &gp);
-    if (rc == QFP4_OK) rc = qfp4::read_clear_status_gemm_decode(s, &gd);
-    if (rc == QFP4_OK) rc = qfp4::read_clear_status_gemm_sparse(s, &gs);
-    if (rc == QFP4_OK) rc = qfp4::read_clear_status_gemm_fp8(s, &g8);
-    if (rc == QFP4_OK) rc = qfp4::read_clear_status_gemm_fp8_small(s, &s8);
-    if (rc == QFP4_OK) rc = qfp4::read_clear_status_fp8_quant(s, &q8);
+    StatusWords words;
+    int rc = QFP4_OK;
+    for (int i = 0; i < kWords && rc == QFP4_OK; ++i) rc = kWordOf[i](&words.word[i]);
+    uint32_t *results = nullptr;
+    if (rc == QFP4_OK) rc = status_word(g_poll_results, &results);
     if (rc != QFP4_OK) return rc;
-    const uint32_t all = q | g | gp | gd | gs | g8 | s8 | q8;
-    if (all & qfp4::kStatusTimeout) return QFP4_ERR_TIMEOUT;
-    if (all & (qfp4::kStatusBadGroup | qfp4::kStatusBadSparsity)) return QFP4_ERR_INVALID_ARG;
+    PollSlot slot;
+    // without programmatic launch: it starts once all earlier work on the stream is complete
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(32);
+    cfg.stream = s;
+    uint32_t all = 0;
+    if (cudaLaunchKernelEx(&cfg, gather_status_kernel, words, results + slot.index) != cudaSuccess ||
+        cudaMemcpyAsync(&all, results + slot.index, sizeof(all), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+        return QFP4_ERR_CUDA;
+    if (all & kStatusTimeout) return QFP4_ERR_TIMEOUT;
+    if (all & (kStatusBadGroup | kStatusBadSparsity)) return QFP4_ERR_INVALID_ARG;
     return QFP4_OK;
 }

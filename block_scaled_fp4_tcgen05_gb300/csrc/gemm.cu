@@ -38,18 +38,7 @@ namespace qfp4 {
 
 __device__ uint32_t g_status_gemm = 0;
 
-int read_clear_status_gemm(cudaStream_t s, uint32_t *out)
-{
-    uint32_t zero = 0;
-    if (cudaMemcpyFromSymbolAsync(out, g_status_gemm, sizeof(uint32_t), 0,
-                                  cudaMemcpyDeviceToHost, s) != cudaSuccess)
-        return QFP4_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return QFP4_ERR_CUDA;
-    if (cudaMemcpyToSymbolAsync(g_status_gemm, &zero, sizeof(uint32_t), 0,
-                                cudaMemcpyHostToDevice, s) != cudaSuccess)
-        return QFP4_ERR_CUDA;
-    return cudaStreamSynchronize(s) == cudaSuccess ? QFP4_OK : QFP4_ERR_CUDA;
-}
+int status_word_gemm(uint32_t **word) { return status_word(g_status_gemm, word); }
 
 namespace {
 

@@ -68,18 +68,7 @@ __device__ __forceinline__ bool inject_skip(bool here) { return here && g_inject
 __device__ __forceinline__ bool inject_skip(bool) { return false; }
 #endif
 
-int read_clear_status_gemm_fp8(cudaStream_t s, uint32_t *out)
-{
-    uint32_t zero = 0;
-    if (cudaMemcpyFromSymbolAsync(out, g_status_gemm_fp8, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s) !=
-        cudaSuccess)
-        return QFP4_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return QFP4_ERR_CUDA;
-    if (cudaMemcpyToSymbolAsync(g_status_gemm_fp8, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, s) !=
-        cudaSuccess)
-        return QFP4_ERR_CUDA;
-    return cudaStreamSynchronize(s) == cudaSuccess ? QFP4_OK : QFP4_ERR_CUDA;
-}
+int status_word_gemm_fp8(uint32_t **word) { return status_word(g_status_gemm_fp8, word); }
 
 namespace {
 

@@ -51,18 +51,7 @@ int set_inject_fp8_small(int on)
 __device__ __forceinline__ bool inject_skip(bool) { return false; }
 #endif
 
-int read_clear_status_gemm_fp8_small(cudaStream_t s, uint32_t *out)
-{
-    uint32_t zero = 0;
-    if (cudaMemcpyFromSymbolAsync(out, g_status_gemm_fp8_small, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s) !=
-        cudaSuccess)
-        return QFP4_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return QFP4_ERR_CUDA;
-    if (cudaMemcpyToSymbolAsync(g_status_gemm_fp8_small, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, s) !=
-        cudaSuccess)
-        return QFP4_ERR_CUDA;
-    return cudaStreamSynchronize(s) == cudaSuccess ? QFP4_OK : QFP4_ERR_CUDA;
-}
+int status_word_gemm_fp8_small(uint32_t **word) { return status_word(g_status_gemm_fp8_small, word); }
 
 namespace {
 

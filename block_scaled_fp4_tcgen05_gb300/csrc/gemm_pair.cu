@@ -70,18 +70,7 @@ __device__ __forceinline__ bool inject_skip_release(int32_t pair_id, uint32_t ra
 __device__ __forceinline__ bool inject_skip_release(int32_t, uint32_t, int32_t) { return false; }
 #endif
 
-int read_clear_status_gemm_pair(cudaStream_t s, uint32_t *out)
-{
-    uint32_t zero = 0;
-    if (cudaMemcpyFromSymbolAsync(out, g_status_gemm_pair, sizeof(uint32_t), 0,
-                                  cudaMemcpyDeviceToHost, s) != cudaSuccess)
-        return QFP4_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return QFP4_ERR_CUDA;
-    if (cudaMemcpyToSymbolAsync(g_status_gemm_pair, &zero, sizeof(uint32_t), 0,
-                                cudaMemcpyHostToDevice, s) != cudaSuccess)
-        return QFP4_ERR_CUDA;
-    return cudaStreamSynchronize(s) == cudaSuccess ? QFP4_OK : QFP4_ERR_CUDA;
-}
+int status_word_gemm_pair(uint32_t **word) { return status_word(g_status_gemm_pair, word); }
 
 namespace {
 

@@ -96,11 +96,21 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-// Per-unit status readers (defined in each .cu that owns a status word).
-int read_clear_status_quant(cudaStream_t s, uint32_t *out);
-int read_clear_status_gemm(cudaStream_t s, uint32_t *out);
-int read_clear_status_gemm_sparse(cudaStream_t s, uint32_t *out);
-int read_clear_status_gemm_fp8(cudaStream_t s, uint32_t *out);
-int read_clear_status_fp8_quant(cudaStream_t s, uint32_t *out);
+// Address on the current device of a translation unit's status word.
+template <typename T>
+inline int status_word(T &symbol, uint32_t **word)
+{
+    void *p = nullptr;
+    if (cudaGetSymbolAddress(&p, symbol) != cudaSuccess) return QFP4_ERR_CUDA;
+    *word = static_cast<uint32_t *>(p);
+    return QFP4_OK;
+}
+
+// Of each .cu that owns one.
+int status_word_quant(uint32_t **word);
+int status_word_gemm(uint32_t **word);
+int status_word_gemm_sparse(uint32_t **word);
+int status_word_gemm_fp8(uint32_t **word);
+int status_word_fp8_quant(uint32_t **word);
 
 }  // namespace qfp4

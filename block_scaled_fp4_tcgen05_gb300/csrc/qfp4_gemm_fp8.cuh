@@ -36,7 +36,7 @@ __device__ __forceinline__ bool fp8_offsets_valid(const int32_t *offs, int e, in
 // rows of A, K split over the CTAs of a cluster.
 bool gemm_fp8_small_pays(const Fp8Params &p);
 int launch_gemm_fp8_small(const Fp8Params &p, cudaStream_t s);
-int read_clear_status_gemm_fp8_small(cudaStream_t s, uint32_t *out);
+int status_word_gemm_fp8_small(uint32_t **word);
 #ifdef QFP4_FAULT_INJECTION
 int set_inject_fp8_small(int on);
 #endif

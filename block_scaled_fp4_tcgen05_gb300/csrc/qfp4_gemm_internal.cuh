@@ -78,7 +78,7 @@ int launch_gemm_pair(int fmt, bool grouped, const CUtensorMap &ma, const CUtenso
 int launch_gemm_pair_swiglu(int fmt, bool grouped, const CUtensorMap &ma, const CUtensorMap &mb,
                             const GemmParams &prm, int64_t pair_tiles, cudaStream_t s);
 
-int read_clear_status_gemm_pair(cudaStream_t s, uint32_t *out);
+int status_word_gemm_pair(uint32_t **word);
 
 // Decode GEMM for M <= 128 (N % 128 == 0), swap AB on CTA pairs: the
 // weights (B, map mw with 128-row boxes) fill the MMA's M slot, the tokens
@@ -99,6 +99,6 @@ size_t decode_counter_bytes(int64_t N);
 // box_cols x box_rows elements, no swizzle: the TMA store map of D.
 int make_map_bf16(CUtensorMap *map, void *base, uint64_t cols, uint64_t rows, uint32_t box_cols,
                   uint32_t box_rows);
-int read_clear_status_gemm_decode(cudaStream_t s, uint32_t *out);
+int status_word_gemm_decode(uint32_t **word);
 
 }  // namespace qfp4
