@@ -590,7 +590,9 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
             // tile's (rows beyond M are clipped by the map), else in four-byte or single pieces
             const int32_t wrow0 = ti.row0 + 128 * static_cast<int32_t>(rank) + quad * 32;
             const int32_t rows = ti.row_end - wrow0;
-            if (rows > 0 && c0 < p.N) {
+            // (a group without rows adds nothing: its D is not even read, and a -0 in it stays)
+            const bool nothing = GROUPING == kBlockGroups && p.accumulate && ti.kblocks == 0;
+            if (rows > 0 && c0 < p.N && !nothing) {
                 const bool by_tma = p.store_map && (!GROUPED || rows >= 32);
                 if (p.fp32) store_tile<true, C::COLS, C::BOXES, COLSCALE>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
                 else store_tile<false, C::COLS, C::BOXES, COLSCALE>(acc, out, tmD, p, by_tma, wrow0, min(rows, 32), c0, lane);
