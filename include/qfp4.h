@@ -132,7 +132,8 @@ int qfp4_global_scale(const void *X_bf16, int64_t rows, int64_t cols, float *gs_
  * 1 <= groups <= 256.
  * Every grouped call of this library checks its row_offsets on the device
  * (row_offsets[0] == 0, non-decreasing, row_offsets[groups] == the row count
- * passed on the host, and for the GEMMs no group above max_group_rows).
+ * passed on the host, or no more than it for the 8-bit calls, and for the GEMMs
+ * no group above max_group_rows).
  * Offsets that fail make the kernels skip all work and make the next
  * qfp4_poll_device_status return QFP4_ERR_INVALID_ARG: the GEMMs and the
  * quantiser's codes are left untouched, the grouped quantiser's scale buffer
@@ -638,7 +639,10 @@ int qfp4_gemm_nt_fp8_kgrouped(int a_type, int b_type, int64_t groups, const int3
  *   gates  fp32 [T, topk]: p of the expert (renorm: divided by the sum of the
  *          token's chosen p), 0 where none
  *   counts int32 [E]: (token, choice) pairs per expert
- *   row_offsets int32 [E + 1]: its running sum, for the grouped calls
+ *   row_offsets int32 [E + 1]: its running sum, for the grouped 8-bit calls,
+ *          and for the grouped FP4 calls where every pair has a row (no token
+ *          is padding, each has topk open experts): those want
+ *          row_offsets[groups] == total_rows, and report anything else
  *   dest   int32 [T, topk]: row of the pair in expert order (by expert, then
  *          token, then choice), -1 where none
  *   src    int32 [T * topk]: token of each row, -1 beyond row_offsets[E]: the
