@@ -23,7 +23,9 @@
 // 90 with every thread computing its scales, 60 without packed BF16 maxima and
 // with two CTAs per SM instead of three), a 14336 x 4096 weight with its
 // transpose 37 us (6.3 TB/s, 0.93).  Tiles of 512 threads with four rows each
-// are slower (53 and 41 us).
+// are slower (53 and 41 us), grouped ones too: 8 groups of 1024 rows x 4096 take
+// 34 us in both directions and 21 along the columns alone (52 and 27).  16384 x
+// 4096 takes 34 us along the rows alone (6.1 TB/s) and 39 along the columns (5.3).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -117,7 +119,7 @@ fp8_quantize_kernel(const QuantParams p)
 {
     constexpr bool ROWS = (WHAT & kRows) != 0, COLS = (WHAT & kCols) != 0, BLOCK = (WHAT & kBlock) != 0;
     constexpr int TR = QuantCfg<WHAT, R>::ROWS, THREADS = QuantCfg<WHAT, R>::THREADS, WARPS = THREADS / 32;
-    static_assert(R == 2 || R == 4 || R == 8, "the exchange between rows halves them");
+    static_assert(R == 2 || R == 8, "the exchange between rows halves them");
     static_assert(!GROUPED || (COLS && !BLOCK), "groups matter to blocks of rows only");
     __shared__ int32_t s_rows[GROUPED ? 2 : 1];
     // transposed tile: 128 columns of 32 words of four rows' codes.  Word u of
@@ -349,8 +351,8 @@ template <int TYPE, bool POW2>
 int launch_what(const QuantParams &p, int what, int64_t groups, cudaStream_t s)
 {
     if (p.groups)
-        return what & kRows ? launch<TYPE, POW2, kRows | kCols, 4, true>(p, groups, s)
-                            : launch<TYPE, POW2, kCols, 4, true>(p, groups, s);
+        return what & kRows ? launch<TYPE, POW2, kRows | kCols, 8, true>(p, groups, s)
+                            : launch<TYPE, POW2, kCols, 8, true>(p, groups, s);
     switch (what) {
     case kRows: return launch<TYPE, POW2, kRows, 2>(p, groups, s);
     case kCols: return launch<TYPE, POW2, kCols, 8>(p, groups, s);
