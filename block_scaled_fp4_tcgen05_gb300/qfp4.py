@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -85,6 +86,13 @@ SIGNATURES = {
 }
 
 
+# Calls with many arguments, which take them as one array of 64-bit words:
+# (function, packer), filled by load().
+_WORDS = ("qfp4_fp8_quantize", "qfp4_fp8_quantize_grouped", "qfp4_fp8_quantize_weight", "qfp4_gemm_nt_fp8",
+          "qfp4_gemm_nt_fp8_grouped", "qfp4_gemm_nt_fp8_kgrouped", "qfp4_moe_route", "qfp4_moe_route_backward")
+_words = {}
+
+
 class Qfp4Error(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -105,6 +113,11 @@ def load() -> ctypes.CDLL:
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
+            for name in _WORDS:
+                fn = getattr(lib, name + "_words")
+                fn.restype = _i32
+                fn.argtypes = [ctypes.c_char_p]
+                _words[name] = fn, struct.Struct(f"{len(SIGNATURES[name][1])}q").pack
             _lib = lib
         return _lib
 
@@ -173,6 +186,15 @@ def _stream(stream) -> int | None:
 
 
 def _check(fn: str, rc: int) -> None:
+    if rc != 0:
+        raise Qfp4Error(fn, rc)
+
+
+def _call(fn: str, *args) -> None:
+    if _lib is None:
+        load()
+    function, pack = _words[fn]
+    rc = function(pack(*args))
     if rc != 0:
         raise Qfp4Error(fn, rc)
 
@@ -363,7 +385,7 @@ def _at(t, dtype, least=0):
     write past a shorter one's end).  A router call has fifteen of these: the
     usual path asks each question once."""
     if t is None:
-        return None
+        return 0
     try:
         if t.dtype is dtype and t.is_cuda and t.numel() >= least and t.is_contiguous():
             return t.data_ptr()
@@ -385,7 +407,7 @@ _CODES = {E4M3: (torch.float8_e4m3fn, torch.uint8), E5M2: (torch.float8_e5m2, to
 def _codes(t, kind, least=0):
     """Address of a matrix of 8-bit codes: of that type, or plain bytes."""
     if t is None:
-        return None
+        return 0
     try:
         if t.dtype in _CODES[kind] and t.is_cuda and t.numel() >= least and t.is_contiguous():
             return t.data_ptr()
@@ -404,11 +426,9 @@ def fp8_quantize(type, X, Q=None, SF=None, Q_t=None, SF_t=None, scale=SCALE_FP32
     rows of X."""
     rows, K = X.shape
     M = rows if row_index is None else row_index.numel()
-    _check("qfp4_fp8_quantize",
-           load().qfp4_fp8_quantize(type, scale, _at(X, _BF16), rows, _at(row_index, _I32), M, K,
-                                    _codes(Q, type, M * K), _at(SF, _F32, (K + 127) // 128 * M),
-                                    _codes(Q_t, type, K * ((M + 15) // 16 * 16)), _at(SF_t, _F32, (M + 127) // 128 * K),
-                                    _stream(stream)))
+    _call("qfp4_fp8_quantize", type, scale, _at(X, _BF16), rows, _at(row_index, _I32), M, K,
+          _codes(Q, type, M * K), _at(SF, _F32, (K + 127) // 128 * M),
+          _codes(Q_t, type, K * ((M + 15) // 16 * 16)), _at(SF_t, _F32, (M + 127) // 128 * K), _stream(stream))
 
 
 def fp8_grouped_cols(total_rows: int, groups: int) -> int:
@@ -424,11 +444,9 @@ def fp8_quantize_grouped(type, X, row_offsets, Q_t, SF_t, Q=None, SF=None, scale
     M = rows if row_index is None else row_index.numel()
     groups = row_offsets.numel() - 1
     cols = fp8_grouped_cols(M, groups)
-    _check("qfp4_fp8_quantize_grouped",
-           load().qfp4_fp8_quantize_grouped(type, scale, _at(X, _BF16), rows, _at(row_index, _I32), groups,
-                                            _at(row_offsets, _I32), M, K, _codes(Q, type, M * K),
-                                            _at(SF, _F32, (K + 127) // 128 * M), _codes(Q_t, type, K * cols),
-                                            _at(SF_t, _F32, cols // 128 * K), _stream(stream)))
+    _call("qfp4_fp8_quantize_grouped", type, scale, _at(X, _BF16), rows, _at(row_index, _I32), groups,
+          _at(row_offsets, _I32), M, K, _codes(Q, type, M * K), _at(SF, _F32, (K + 127) // 128 * M),
+          _codes(Q_t, type, K * cols), _at(SF_t, _F32, cols // 128 * K), _stream(stream))
 
 
 def fp8_quantize_weight(type, W, Q, SF, Q_t=None, SF_t=None, scale=SCALE_FP32, stream=None) -> None:
@@ -436,11 +454,9 @@ def fp8_quantize_weight(type, W, Q, SF, Q_t=None, SF_t=None, scale=SCALE_FP32, s
     block, and optionally their transpose (Q_t [.., K, ceil16(N)])."""
     groups, (N, K) = (1 if W.dim() == 2 else W.shape[0]), W.shape[-2:]
     blocks = groups * ((N + 127) // 128) * ((K + 127) // 128)
-    _check("qfp4_fp8_quantize_weight",
-           load().qfp4_fp8_quantize_weight(type, scale, groups, _at(W, _BF16, groups * N * K), N, K,
-                                           _codes(Q, type, groups * N * K), _at(SF, _F32, blocks),
-                                           _codes(Q_t, type, groups * K * ((N + 15) // 16 * 16)),
-                                           _at(SF_t, _F32, blocks), _stream(stream)))
+    _call("qfp4_fp8_quantize_weight", type, scale, groups, _at(W, _BF16, groups * N * K), N, K,
+          _codes(Q, type, groups * N * K), _at(SF, _F32, blocks),
+          _codes(Q_t, type, groups * K * ((N + 15) // 16 * 16)), _at(SF_t, _F32, blocks), _stream(stream))
 
 
 def gemm_nt_fp8(a_type, b_type, M, N, K, A, A_sf, B, B_sf, D, b_rows=128, out=OUT_BF16, accumulate=False,
@@ -448,11 +464,9 @@ def gemm_nt_fp8(a_type, b_type, M, N, K, A, A_sf, B, B_sf, D, b_rows=128, out=OU
     """D = A B^T with a scale per 128 elements of K: A_sf [ceil(K/128), M], B_sf
     per 128 x 128 block (b_rows=128) or [ceil(K/128), N] (b_rows=1)."""
     blocks = (K + 127) // 128
-    _check("qfp4_gemm_nt_fp8",
-           load().qfp4_gemm_nt_fp8(a_type, b_type, M, N, K, _codes(A, a_type, M * K), _at(A_sf, _F32, blocks * M),
-                                   _codes(B, b_type, N * K), _at(B_sf, _F32, blocks * (N if b_rows == 1 else (N + 127) // 128)),
-                                   b_rows, out, 1 if accumulate else 0,
-                                   _at(D, _F32 if out == OUT_FP32 else _BF16, M * N), _stream(stream)))
+    _call("qfp4_gemm_nt_fp8", a_type, b_type, M, N, K, _codes(A, a_type, M * K), _at(A_sf, _F32, blocks * M),
+          _codes(B, b_type, N * K), _at(B_sf, _F32, blocks * (N if b_rows == 1 else (N + 127) // 128)), b_rows, out,
+          1 if accumulate else 0, _at(D, _F32 if out == OUT_FP32 else _BF16, M * N), _stream(stream))
 
 
 def gemm_nt_fp8_grouped(a_type, b_type, row_offsets, total_rows, max_group_rows, N, K, A, A_sf, B, B_sf, D,
@@ -460,12 +474,10 @@ def gemm_nt_fp8_grouped(a_type, b_type, row_offsets, total_rows, max_group_rows,
     """One product per expert: rows [row_offsets[e], row_offsets[e+1]) with B[e]."""
     groups = row_offsets.numel() - 1
     blocks = (K + 127) // 128
-    _check("qfp4_gemm_nt_fp8_grouped",
-           load().qfp4_gemm_nt_fp8_grouped(a_type, b_type, groups, _at(row_offsets, _I32), total_rows, max_group_rows,
-                                           N, K, _codes(A, a_type, total_rows * K), _at(A_sf, _F32, blocks * total_rows),
-                                           _codes(B, b_type, groups * N * K),
-                                           _at(B_sf, _F32, groups * ((N + 127) // 128) * blocks), out,
-                                           _at(D, _F32 if out == OUT_FP32 else _BF16, total_rows * N), _stream(stream)))
+    _call("qfp4_gemm_nt_fp8_grouped", a_type, b_type, groups, _at(row_offsets, _I32), total_rows, max_group_rows, N, K,
+          _codes(A, a_type, total_rows * K), _at(A_sf, _F32, blocks * total_rows),
+          _codes(B, b_type, groups * N * K), _at(B_sf, _F32, groups * ((N + 127) // 128) * blocks), out,
+          _at(D, _F32 if out == OUT_FP32 else _BF16, total_rows * N), _stream(stream))
 
 
 def gemm_nt_fp8_kgrouped(a_type, b_type, row_offsets, total_rows, M, N, A, A_sf, B, B_sf, D, accumulate=False,
@@ -474,11 +486,10 @@ def gemm_nt_fp8_kgrouped(a_type, b_type, row_offsets, total_rows, M, N, A, A_sf,
     fp8_quantize_grouped gave group e; D fp32 [groups, M, N]."""
     groups = row_offsets.numel() - 1
     cols = fp8_grouped_cols(total_rows, groups)
-    _check("qfp4_gemm_nt_fp8_kgrouped",
-           load().qfp4_gemm_nt_fp8_kgrouped(a_type, b_type, groups, _at(row_offsets, _I32), total_rows, M, N,
-                                            _codes(A, a_type, M * cols), _at(A_sf, _F32, cols // 128 * M),
-                                            _codes(B, b_type, N * cols), _at(B_sf, _F32, cols // 128 * N),
-                                            1 if accumulate else 0, _at(D, _F32, groups * M * N), _stream(stream)))
+    _call("qfp4_gemm_nt_fp8_kgrouped", a_type, b_type, groups, _at(row_offsets, _I32), total_rows, M, N,
+          _codes(A, a_type, M * cols), _at(A_sf, _F32, cols // 128 * M),
+          _codes(B, b_type, N * cols), _at(B_sf, _F32, cols // 128 * N),
+          1 if accumulate else 0, _at(D, _F32, groups * M * N), _stream(stream))
 
 
 def moe_route_workspace_bytes(T: int, E: int, topk: int) -> int:
@@ -496,12 +507,10 @@ def moe_route(logits, topk, ids, gates, counts, row_offsets, dest, src, n_valid,
     the balance loss; valid is uint8 [T] or None."""
     T, E = logits.shape
     pairs = T * topk
-    _check("qfp4_moe_route",
-           load().qfp4_moe_route(*_logits(logits), T, E, topk, _at(valid, _U8, T), 1 if renorm else 0,
-                                 _at(ids, _I32, pairs), _at(gates, _F32, pairs), _at(counts, _I32, E),
-                                 _at(row_offsets, _I32, E + 1), _at(dest, _I32, pairs), _at(src, _I32, pairs),
-                                 _at(n_valid, _I32, 1), _at(mean_prob, _F32, E), _at(loss, _F32, 1),
-                                 _at(workspace, workspace.dtype), workspace.nbytes, _stream(stream)))
+    _call("qfp4_moe_route", *_logits(logits), T, E, topk, _at(valid, _U8, T), 1 if renorm else 0,
+          _at(ids, _I32, pairs), _at(gates, _F32, pairs), _at(counts, _I32, E), _at(row_offsets, _I32, E + 1),
+          _at(dest, _I32, pairs), _at(src, _I32, pairs), _at(n_valid, _I32, 1), _at(mean_prob, _F32, E),
+          _at(loss, _F32, 1), _at(workspace, workspace.dtype), workspace.nbytes, _stream(stream))
 
 
 def moe_route_backward(logits, ids, counts, n_valid, dgates, dloss, dlogits, valid=None, renorm=True,
@@ -511,8 +520,6 @@ def moe_route_backward(logits, ids, counts, n_valid, dgates, dloss, dlogits, val
     T, E = logits.shape
     topk = ids.shape[1]
     pairs = T * topk
-    _check("qfp4_moe_route_backward",
-           load().qfp4_moe_route_backward(*_logits(logits), T, E, topk, _at(valid, _U8, T), 1 if renorm else 0,
-                                          _at(ids, _I32, pairs), _at(counts, _I32, E), _at(n_valid, _I32, 1),
-                                          _at(dgates, _F32, pairs), _at(dloss, _F32, 1), _at(dlogits, logits.dtype, T * E),
-                                          _stream(stream)))
+    _call("qfp4_moe_route_backward", *_logits(logits), T, E, topk, _at(valid, _U8, T), 1 if renorm else 0,
+          _at(ids, _I32, pairs), _at(counts, _I32, E), _at(n_valid, _I32, 1), _at(dgates, _F32, pairs),
+          _at(dloss, _F32, 1), _at(dlogits, logits.dtype, T * E), _stream(stream))

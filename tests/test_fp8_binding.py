@@ -44,16 +44,11 @@ def calls(monkeypatch):
     made = []
 
     class Library:
-        def __getattr__(self, name):
-            def call(*a):
-                made.append(name)
-                return 0
-            return call
-
         def qfp4_fp8_grouped_cols(self, rows, groups):
             return 128 * (-(-rows // 128) + groups)
 
     monkeypatch.setattr(qfp4, "load", lambda: Library())
+    monkeypatch.setattr(qfp4, "_call", lambda name, *a: made.append(name))
     monkeypatch.setattr(qfp4, "_stream", lambda s: None)
     return made
 
@@ -125,3 +120,36 @@ def test_other_refusals_say_what_they_are(calls):
         qfp4.gemm_nt_fp8(**{**a, "D": strided})
     qfp4.gemm_nt_fp8(**{**a, "A": 1 << 40, "D": 1 << 40})       # addresses stand as they are
     assert calls == ["qfp4_gemm_nt_fp8"]
+
+
+def test_arguments_reach_the_library_as_they_are():
+    """Every call that takes its arguments as packed words, against the C entry
+    itself: each argument is made bad in turn, and both refuse it alike."""
+    if torch.cuda.is_available():
+        pytest.skip("a call that is not refused would be launched with these addresses")
+    lib = qfp4.load()
+    fake = 1 << 40
+    values = {
+        "qfp4_fp8_quantize": (0, 0, fake, 16, None, 16, 256, fake, fake, fake, fake, None),
+        "qfp4_fp8_quantize_grouped": (0, 0, fake, 16, None, 4, fake, 16, 256, fake, fake, fake, fake, None),
+        "qfp4_fp8_quantize_weight": (0, 0, 1, fake, 128, 256, fake, fake, fake, fake, None),
+        "qfp4_gemm_nt_fp8": (0, 1, 16, 128, 256, fake, fake, fake, fake, 128, 0, 0, fake, None),
+        "qfp4_gemm_nt_fp8_grouped": (0, 0, 4, fake, 64, 0, 128, 256, fake, fake, fake, fake, 0, fake, None),
+        "qfp4_gemm_nt_fp8_kgrouped": (1, 0, 4, fake, 64, 128, 256, fake, fake, fake, fake, 0, fake, None),
+        "qfp4_moe_route": (1, fake, 64, 8, 2, None, 1, *[fake] * 9, fake, 1 << 20, None),
+        "qfp4_moe_route_backward": (0, fake, 64, 8, 2, None, 0, fake, fake, fake, fake, fake, fake, None),
+    }
+    assert set(values) == set(qfp4._WORDS)
+    for name, good in values.items():
+        function, pack = qfp4._words[name]
+        assert len(good) == len(qfp4.SIGNATURES[name][1])
+        refused = 0
+        for i, v in enumerate(good):
+            for bad in (-(1 << 40) - 7, -1, 0, fake + 1):
+                args = (*good[:i], bad, *good[i + 1:])
+                want = getattr(lib, name)(*[None if a is None else a for a in args])
+                if want in (0, -4):     # not refused (there is no GPU to launch it on)
+                    continue
+                refused += 1
+                assert function(pack(*(0 if a is None else a for a in args))) == want, (name, i, bad)
+        assert refused >= len(good), name
