@@ -16,10 +16,12 @@
 // memory is needed).
 //
 // The weights' bytes are the floor.  One token x 14336 x 4096 takes 11.8 us
-// (4.9 TB/s) and 4096 x 4096 5.8 (5.1 from L2); 128 tokens x 14336 x 4096 15.0
-// (4.2 TB/s): there a K block's 128 x 128 MMAs, whose operands take all of
-// shared memory's bandwidth (about 115 cycles each), set the pace.  Grouped,
-// 8 experts x 14336 x 4096: 74 us with 2 rows each (6.4 TB/s), 97 with 16.
+// (4.9 TB/s) and 4096 x 4096 5.8 (5.1 from L2); 128 tokens x 14336 x 4096 15.7
+// (4.0 TB/s; 14.2 with the weights in L2).  There a CTA's pace, about 0.31 us
+// per K block, and the 112 CTAs on 152 SMs bound it: 152 of them (N = 19456)
+// take the same time.  Grouped, 8 experts x 14336 x 4096, with a bound on the
+// groups' rows: 72 us with 2 rows each (6.5 TB/s), 73 with 16, 98 with 48 (and
+// with 16 where no bound says so).
 //
 // Warps: 0 TMA producer, 1 and 3 MMA issuers (1 owns tensor memory), 2 scales,
 // 4.. epilogue (four of all columns, or sixteen of 32 each).
@@ -516,13 +518,20 @@ Plan plan(const Fp8Params &p)
 
 // Up to 32 rows always (per group, as far as the host can tell).  Up to 128 but
 // for many tiles of a short K, whose beginnings and ends the pairs' persistent
-// loop hides (64 groups of 128 rows x 2048 x 768: 51 us here, 39 there; 128 x
-// 131072 x 512: 39 and 25; with fewer rounds or a longer K the pairs' tiles,
-// half of them padding, lose: 128 x 65536 x 4096 63 and 68, 8 groups of 128 rows
-// x 4096 x 2048 20 and 24).  More where K is split: a CTA then has half the K blocks of a pair's 256 x 128 tile (256 x
-// 4096 x 14336 takes 23 us here and 34 there).  Unsplit the pair is as fast or
-// faster (512 x 4096 x 14336 39 us here, 35 there; fp32 with column scales 76
-// and 54).
+// loop hides; with a longer K the pairs' tiles, half of them padding, lose.  Both
+// forms over K = 512, 1024, 1536, 2048, 2560, 4096 (us, here / pairs):
+//   128 x 40960 (2.1 rounds)   13.9/12.3  18.2/17.9  22.0/22.6  25.9/27.9  33.9/35.8  46.4/52.3
+//   128 x 65536 (3.4)          18.7/15.4  25.1/22.8  34.4/32.4  39.9/39.5  46.4/47.5  63.3/68.5
+//   128 x 98304 (5.1)          27.8/20.9  42.1/33.8  50.0/45.3  57.7/55.7  67.7/67.8  92.8/99.8
+//   64 groups of 128 x 2048    44.5/31.6  56.8/46.2  66.9/61.0  76.9/75.6  89.3/92.3  121/141
+//   64 groups of 48 x 2048     36.8/33.1  51.9/48.4  61.7/62.4  71.5/75.9  82.9/91.4  114/139
+//   8 groups of 128 x 8192     22.1/18.8  28.7/26.4             43.9/44.7  50.4/53.1  67.6/76.1
+// The two are even near K = 2048 from three rounds on (fewer rows a little
+// earlier); with two rounds the pairs gain little anywhere.
+// More than 128 where K is split: a CTA then has half the K blocks of a pair's
+// 256 x 128 tile (256 x 4096 x 14336 takes 23 us here and 34 there).  Unsplit the
+// pair is as fast or faster (512 x 4096 x 14336 39 us here, 35 there; fp32 with
+// column scales 76 and 54).
 bool gemm_fp8_small_pays(const Fp8Params &p)
 {
     const int64_t rows = most_rows(p);

@@ -416,7 +416,7 @@ route_place_kernel(const RouteParams p, int chunks)
     __shared__ RouteShared sh;
     const int tid = threadIdx.x;
     const bool totals = static_cast<int>(blockIdx.x) == chunks;
-    // four experts' counts are added up by `parts` threads, ten ranges or fewer each
+    // four experts' counts are added up by `parts` threads, up to 19 ranges each (E > 128; fewer experts, fewer)
     const int e4 = (p.E + 3) / 4;
     const int width = e4 <= 8 ? 8 : e4 <= 16 ? 16 : e4 <= 32 ? 32 : 64;
     const int parts = kThreads / width, part = tid / width, e = tid % width;
@@ -723,7 +723,7 @@ bool sizes_ok(int64_t T, int64_t E, int64_t topk)
     return E <= kMaxExperts && topk <= kMaxTopk && topk <= E && T <= INT32_MAX / topk;
 }
 
-// Ranges of tokens: at least 32 each, at most kMaxChunks of them.
+// Ranges of tokens: 16 each, or more where that would make over kMaxChunks of them.
 int64_t chunk_count(int64_t T)
 {
     const int64_t n = (T + kWarps - 1) / kWarps;
