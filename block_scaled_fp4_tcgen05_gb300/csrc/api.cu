@@ -51,10 +51,11 @@ namespace {
 // atomic step: a word set once is reported once, whichever poll meets it), and
 // one copy brings the result back: 19 us instead of 142 with a copy and a wait to
 // read and as much to clear each word.
-constexpr int kWords = 8;
+constexpr int kWords = 10;
 constexpr int (*kWordOf[kWords])(uint32_t **) = {
     status_word_quant,       status_word_gemm,     status_word_gemm_pair,      status_word_gemm_decode,
-    status_word_gemm_sparse, status_word_gemm_fp8, status_word_gemm_fp8_small, status_word_fp8_quant};
+    status_word_gemm_sparse, status_word_gemm_fp8, status_word_gemm_fp8_small, status_word_fp8_quant,
+    status_word_heads,       status_word_attention};
 
 struct StatusWords {
     uint32_t *word[kWords];

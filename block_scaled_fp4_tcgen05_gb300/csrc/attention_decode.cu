@@ -1,0 +1,94 @@
+// attention_decode.cu -- entry points of the attention of one new token per
+// sequence over the paged cache (kernel: qfp4_attention.cuh).
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "qfp4_attention.cuh"
+
+namespace qfp4 {
+
+__device__ uint32_t g_status_attention = 0;
+
+int status_word_attention(uint32_t **word) { return status_word(g_status_attention, word); }
+
+namespace {
+
+// CTAs that the workspace is sized for: 152 SMs, at most this many on each.
+constexpr int kMaxPerSm = 4, kMaxCtas = 152 * kMaxPerSm;
+constexpr size_t kCounterBytes = 4096;
+static_assert(kMaxCtas * sizeof(uint32_t) <= kCounterBytes, "a counter per CTA");
+
+constexpr int64_t kMaxHeads = 4096, kMaxBatch = 1 << 20, kMaxLength = int64_t{1} << 30;
+
+bool sizes_ok(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D)
+{
+    return (D == 64 || D == 128 || D == 256) && q_heads <= kMaxHeads && B <= kMaxBatch && q_heads % kv_heads == 0;
+}
+
+size_t workspace_bytes(int64_t group, int D)
+{
+    return kCounterBytes + static_cast<size_t>(kMaxCtas) * 2 * attn_piece_floats(8 * attn_tiles(group, D), D) * sizeof(float);
+}
+
+}  // namespace
+}  // namespace qfp4
+
+using namespace qfp4;
+
+extern "C" size_t qfp4_attention_decode_workspace_bytes(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim)
+{
+    if (B < 0 || q_heads < 1 || kv_heads < 1 || !sizes_ok(B, q_heads, kv_heads, head_dim)) return 0;
+    return workspace_bytes(q_heads / kv_heads, static_cast<int>(head_dim));
+}
+
+extern "C" int qfp4_attention_decode(int type, const void *Q_bf16, int64_t ldq, int64_t B, int64_t q_heads,
+                                     int64_t kv_heads, int64_t head_dim, const void *cache, int64_t pages,
+                                     int64_t page_size, const int32_t *page_table, int64_t max_pages,
+                                     const int32_t *lengths, int64_t window, float scale, const float *gs_k,
+                                     const float *gs_v, void *O_bf16, float *lse, void *workspace, size_t ws_bytes,
+                                     void *stream)
+{
+    if (!cache_type_ok(type) || B < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1 || pages < 0 || page_size < 1 ||
+        max_pages < 0 || window < 0 || ldq < q_heads * head_dim || !(scale > -3.0e38f && scale < 3.0e38f))
+        return QFP4_ERR_INVALID_ARG;
+    if (!sizes_ok(B, q_heads, kv_heads, head_dim) || page_size % 16 != 0 || page_size > 65536 || pages > INT32_MAX ||
+        max_pages > kMaxLength / page_size || ldq % 8 != 0)
+        return QFP4_ERR_UNSUPPORTED;
+    if (B == 0) return QFP4_OK;
+    if (!Q_bf16 || !lengths || !O_bf16 || (max_pages > 0 && (!page_table || !cache || pages < 1)) ||
+        (type == QFP4_CACHE_NVFP4 && (!gs_k || !gs_v)))
+        return QFP4_ERR_INVALID_ARG;
+    if (!aligned16(Q_bf16) || !aligned16(cache) || !aligned16(O_bf16) || !aligned16(workspace) ||
+        !aligned4(page_table) || !aligned4(lengths) || !aligned4(gs_k) || !aligned4(gs_v) || !aligned4(lse))
+        return QFP4_ERR_MISALIGNED;
+    const int D = static_cast<int>(head_dim), nt = attn_tiles(q_heads / kv_heads, D);
+    if (!workspace || ws_bytes < workspace_bytes(q_heads / kv_heads, D)) return QFP4_ERR_WORKSPACE;
+    AttnParams p = {};
+    p.q = static_cast<const __nv_bfloat16 *>(Q_bf16);
+    p.ldq = ldq;
+    p.B = static_cast<int32_t>(B);
+    p.kv_heads = static_cast<int32_t>(kv_heads);
+    p.group = static_cast<int32_t>(q_heads / kv_heads);
+    p.blocks = (p.group + 8 * nt - 1) / (8 * nt);
+    p.cache = static_cast<const uint8_t *>(cache);
+    p.pages = pages;
+    p.page_size = static_cast<int32_t>(page_size);
+    p.max_pages = static_cast<int32_t>(max_pages);
+    p.window = static_cast<int32_t>(window < kMaxLength ? window : 0);
+    p.page_table = page_table;
+    p.lengths = lengths;
+    p.scale_log2 = scale * 1.44269504088896341f;
+    p.gs_k = gs_k;
+    p.gs_v = gs_v;
+    p.out = static_cast<__nv_bfloat16 *>(O_bf16);
+    p.lse = lse;
+    p.counters = static_cast<uint32_t *>(workspace);
+    p.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kCounterBytes);
+    if (status_word_attention(&p.status) != QFP4_OK) return QFP4_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    switch (type) {
+    case QFP4_CACHE_BF16: return attn_launch_bf16(p, D, nt, kMaxPerSm, s);
+    case QFP4_CACHE_E4M3: return attn_launch_e4m3(p, D, nt, kMaxPerSm, s);
+    default: return attn_launch_nvfp4(p, D, nt, kMaxPerSm, s);
+    }
+}

@@ -5,6 +5,7 @@
 // router's nineteen, where packing them and converting one takes 0.9.
 #include <cstddef>
 #include <cstdint>
+#include <cstring>
 #include <type_traits>
 #include <utility>
 
@@ -15,7 +16,11 @@ namespace {
 template <typename T>
 T from_word(int64_t w)
 {
-    if constexpr (std::is_pointer_v<T>) return reinterpret_cast<T>(static_cast<uintptr_t>(w));
+    if constexpr (std::is_same_v<T, float>) {       // its 32 bits, in the first half of the word
+        T v;
+        std::memcpy(&v, &w, sizeof(v));
+        return v;
+    } else if constexpr (std::is_pointer_v<T>) return reinterpret_cast<T>(static_cast<uintptr_t>(w));
     else return static_cast<T>(w);
 }
 
@@ -44,3 +49,10 @@ QFP4_WORDS(qfp4_gemm_nt_fp8_grouped)
 QFP4_WORDS(qfp4_gemm_nt_fp8_kgrouped)
 QFP4_WORDS(qfp4_moe_route)
 QFP4_WORDS(qfp4_moe_route_backward)
+QFP4_WORDS(qfp4_qk_norm_rope)
+QFP4_WORDS(qfp4_qk_norm_rope_cache)
+QFP4_WORDS(qfp4_qk_norm_rope_backward)
+QFP4_WORDS(qfp4_kv_cache_write)
+QFP4_WORDS(qfp4_kv_cache_read)
+QFP4_WORDS(qfp4_attention_decode)
+QFP4_WORDS(qfp4_gemv_nt)

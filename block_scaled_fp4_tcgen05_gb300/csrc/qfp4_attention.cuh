@@ -1,0 +1,881 @@
+// qfp4_attention.cuh -- attention of one new token per sequence over the paged
+// cache (see qfp4_kv_cache.cuh for the cache's layout).  One translation unit
+// per cache type instantiates the kernel.
+//
+//   x_j = scale q . k_j (in units of log 2),  p_j = 2^(x_j - m),  m = max x_j,
+//   o = sum p_j v_j / sum p_j,  lse = ln 2 (m + log2 sum p_j)
+// in one pass over the cache, with the running m, sums and o in fp32 registers.
+//
+// Bound by the cache's bytes.  A warp takes 16 tokens as the rows of a tensor
+// core product with up to 8 (or 16) query heads that share the key head as its
+// columns: S^T = K Q^T, then O^T = V^T P^T, so a group of 8 heads fills the
+// columns and the cache is read once for all of them.  The codes go from shared
+// memory to the operand registers as they lie, 16 bytes per lane and free of bank
+// conflicts, and become FP16 there: E2M1 and E4M3 values and their products with
+// UE4M3 scales have at most 6 significant bits and are exact in FP16.  Queries
+// become FP16 too, each multiplied by the power of two that takes its largest
+// element to [2^14, 2^15): what lies 2^28 below that loses bits, 2^-39 of the
+// largest at most.  p is rounded to FP16 (2^-11 of it at most); an E4M3 token's value
+// scale s joins it as 2^(x + log2 s - m'), m' the maximum of that exponent, so
+// that no range of scales is lost.  With a BF16 cache the operands are BF16 and p is the sum
+// of two (2^-16).
+//
+// The tokens of all sequences and heads are one line of tiles; each CTA takes an
+// equal piece of it, whatever the lengths, and the pieces of a head that lies
+// across CTAs are joined by the one that finishes last, in the order of the
+// pieces: results repeat bit for bit.  Each warp brings its own tokens with bulk
+// copies into a ring of stages of its own, ahead of the tile that it works on and
+// across the heads' borders; no other warp waits for it until a head ends.
+#pragma once
+
+#include <atomic>
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "qfp4_common.cuh"
+#include "qfp4_kv_cache.cuh"
+#include "sm103_ptx.cuh"
+
+namespace qfp4 {
+
+struct AttnParams {
+    const __nv_bfloat16 *q;     // [B, q_heads, D], ldq elements from sequence to sequence
+    int64_t ldq;
+    int32_t B, kv_heads, group; // group: query heads of a key head
+    int32_t blocks;             // blocks of query heads in a group
+    const uint8_t *cache;
+    int64_t pages;
+    int32_t page_size, max_pages, window;
+    const int32_t *page_table, *lengths;
+    float scale_log2;           // scale * log2(e)
+    const float *gs_k, *gs_v;
+    __nv_bfloat16 *out;         // [B, q_heads, D]
+    float *lse;                 // [B, q_heads] or NULL
+    uint32_t *counters;         // [grid], zero before and after
+    float *partial;             // [grid][2] pieces
+    uint32_t *status;
+};
+
+// Space of a piece in the workspace: o, then m and l of each query.
+__host__ __device__ constexpr int attn_piece_floats(int queries, int D) { return queries * (D + 2); }
+
+constexpr int kAttnWarps = 4, kAttnThreads = 32 * kAttnWarps;
+// tokens of a warp's stage, and stages of its ring
+constexpr int attn_stage_tokens(int type, int D)
+{
+    return type == QFP4_CACHE_NVFP4 ? (D == 64 ? 64 : D == 128 ? 32 : 16)
+         : type == QFP4_CACHE_E4M3  ? (D == 64 ? 32 : 16) : 16;
+}
+constexpr int attn_stages(int type, int D) { return type == QFP4_CACHE_BF16 && D == 256 ? 2 : 3; }
+
+template <int TYPE, int D, int NT>
+struct AttnCfg {
+    static constexpr int TOKENS = attn_stage_tokens(TYPE, D), STAGES = attn_stages(TYPE, D), UNITS = TOKENS / 16;
+    static constexpr int UNIT = cache_unit_bytes(TYPE, D), STAGE = UNITS * UNIT;
+    static constexpr int TILE = TOKENS * kAttnWarps;
+    static constexpr int QUERIES = 8 * NT;
+    static constexpr int RING = kAttnWarps * STAGES * STAGE;
+    static constexpr int JOIN = QUERIES * (D + 4) * 4 + kAttnWarps * QUERIES * 8;
+    static constexpr int BARS = kAttnWarps * STAGES * 8;
+    static constexpr int SMEM = RING + JOIN + BARS;
+};
+
+namespace attn {
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int TYPE>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if constexpr (TYPE == QFP4_CACHE_BF16) mma_bf16(c, a, b0, b1);
+    else mma_f16(c, a, b0, b1);
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// Two E2M1 codes (byte I of w) as FP16, the low code in the low half.
+template <int I>
+__device__ __forceinline__ uint32_t fp4x2(uint32_t w)
+{
+    uint32_t r;
+    if constexpr (I == 0)
+        asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %1;\ncvt.rn.f16x2.e2m1x2 %0, a;\n}" : "=r"(r) : "r"(w));
+    else if constexpr (I == 1)
+        asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %1;\ncvt.rn.f16x2.e2m1x2 %0, b;\n}" : "=r"(r) : "r"(w));
+    else if constexpr (I == 2)
+        asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %1;\ncvt.rn.f16x2.e2m1x2 %0, c;\n}" : "=r"(r) : "r"(w));
+    else
+        asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %1;\ncvt.rn.f16x2.e2m1x2 %0, d;\n}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+// Two E4M3 codes (half I of w) as FP16.
+template <int I>
+__device__ __forceinline__ uint32_t fp8x2(uint32_t w)
+{
+    uint32_t r;
+    if constexpr (I == 0)
+        asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %1;\ncvt.rn.f16x2.e4m3x2 %0, a;\n}" : "=r"(r) : "r"(w));
+    else
+        asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %1;\ncvt.rn.f16x2.e4m3x2 %0, b;\n}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float log2_fast(float x)
+{
+    float r;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The larger one; NaN where either is: a NaN must not pass for "no token".
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// 2^e for -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Where a CTA stands on the line of tiles: sequence, (key head, query block) and tile.
+struct Cursor {
+    int b, item, tile, tiles;
+    int first, len;             // tokens that the sequence's tiles begin at (a multiple of 16) and end before
+
+    template <int TILE>
+    __device__ __forceinline__ void load(const AttnParams &p)
+    {
+        first = tiles = len = 0;
+        if (b >= p.B) return;
+        extent(p, p.lengths[b], first, len);
+        tiles = count<TILE>(first, len);
+    }
+    __device__ static __forceinline__ void extent(const AttnParams &p, int length, int &first, int &len)
+    {
+        const int64_t most = static_cast<int64_t>(p.max_pages) * p.page_size;
+        len = length < 0 ? 0 : length > most ? static_cast<int>(most) : length;
+        first = p.window > 0 && len > p.window ? (len - p.window) & ~15 : 0;
+    }
+    // an empty sequence has one tile, which writes its zeros
+    template <int TILE>
+    __device__ static __forceinline__ int count(int first, int len)
+    {
+        const int n = (len - first + TILE - 1) / TILE;
+        return n > 0 ? n : 1;
+    }
+    template <int TILE>
+    __device__ __forceinline__ void next(const AttnParams &p)
+    {
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++item < p.kv_heads * p.blocks) return;
+        item = 0;
+        ++b;
+        load<TILE>(p);
+    }
+};
+
+}  // namespace attn
+
+template <int TYPE, int D, int NT>
+__global__ void __launch_bounds__(kAttnThreads) attention_decode_kernel(const AttnParams p)
+{
+    using namespace attn;
+    using C = AttnCfg<TYPE, D, NT>;
+    constexpr CacheUnit U(TYPE, D);
+    constexpr int UNITS = C::UNITS, STAGES = C::STAGES, TILE = C::TILE, QUERIES = C::QUERIES;
+    constexpr int KSTEPS = D / 16, MTILES = D / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t s_sum[kAttnWarps];
+    __shared__ int64_t s_start[2];      // the CTA's first tile: sequence, tile within it
+    __shared__ uint32_t s_last;
+    float *s_o = reinterpret_cast<float *>(smem + C::RING);                     // [QUERIES][D + 4]
+    float2 *s_ml = reinterpret_cast<float2 *>(s_o + QUERIES * (D + 4));         // [warps][QUERIES]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t bars = smem_u32(smem + C::RING + C::JOIN) + warp * STAGES * 8;
+    uint8_t *ring = smem + warp * STAGES * C::STAGE;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 1);
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // ---- the CTA's piece of the line of tiles
+    const int items = p.kv_heads * p.blocks;
+    int64_t mine = 0;
+    for (int b = tid; b < p.B; b += kAttnThreads) {
+        int first, len;
+        const int length = p.lengths[b];
+        Cursor::extent(p, length, first, len);
+        if (length != len && blockIdx.x == 0) atomicOr(p.status, kStatusBadGroup);
+        mine += static_cast<int64_t>(items) * Cursor::count<TILE>(first, len);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) s_sum[warp] = mine;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int i = 0; i < kAttnWarps; ++i) total += s_sum[i];
+    const int64_t ctas = total < gridDim.x ? total : gridDim.x;
+    if (blockIdx.x >= ctas) return;
+    const int64_t lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
+    if (warp == 0) {
+        int64_t before = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const int b = b0 + lane;
+            int64_t n = 0;
+            if (b < p.B) {
+                int first, len;
+                Cursor::extent(p, p.lengths[b], first, len);
+                n = static_cast<int64_t>(items) * Cursor::count<TILE>(first, len);
+            }
+            int64_t upto = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            upto += before;
+            if (n > 0 && lo >= upto - n && lo < upto) {
+                s_start[0] = b;
+                s_start[1] = lo - (upto - n);
+            }
+            before = __shfl_sync(0xffffffffu, upto, 31);
+            if (before > lo) break;
+        }
+    }
+    __syncthreads();
+    Cursor cur;
+    cur.b = static_cast<int>(s_start[0]);
+    cur.load<TILE>(p);
+    cur.item = static_cast<int>(s_start[1] / cur.tiles);
+    cur.tile = static_cast<int>(s_start[1] - static_cast<int64_t>(cur.item) * cur.tiles);
+
+    // ---- the warp's ring
+    Cursor ahead = cur;
+    int64_t to_issue = hi - lo;
+    // page of this lane's unit in the tile that `ahead` stands at
+    auto page_of = [&](const Cursor &c) {
+        const int token = c.first + c.tile * TILE + warp * C::TOKENS + 16 * lane;
+        int page = -1;
+        if (lane < UNITS && token < c.len) page = p.page_table[static_cast<int64_t>(c.b) * p.max_pages + token / p.page_size];
+        return page;
+    };
+    auto issue = [&](const Cursor &c, int page, int stage) {
+        const int token = c.first + c.tile * TILE + warp * C::TOKENS + 16 * lane;
+        const bool has = lane < UNITS && token < c.len;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, has));
+        if (has && (page < 0 || page >= p.pages)) {
+            atomicOr(p.status, kStatusBadGroup);
+            page = 0;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, n * C::UNIT);
+        __syncwarp();
+        if (has) {
+            const int64_t unit = (static_cast<int64_t>(page) * p.kv_heads + c.item / p.blocks) * (p.page_size / 16) +
+                                 token % p.page_size / 16;
+            bulk_load(smem_u32(ring + stage * C::STAGE + lane * C::UNIT), p.cache + unit * C::UNIT, C::UNIT, bars + 8 * stage);
+        }
+    };
+    {
+        Cursor c[STAGES];
+        int page[STAGES];
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i) {
+            c[i] = ahead;
+            page[i] = -1;
+            if (i < to_issue) {
+                page[i] = page_of(ahead);
+                ahead.next<TILE>(p);
+                n = i + 1;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < STAGES; ++i)
+            if (i < n) issue(c[i], page[i], i);
+        to_issue -= n;
+    }
+    int page_next = to_issue > 0 ? page_of(ahead) : -1;
+
+    int stage = 0;
+    uint32_t phase = 0;
+    bool dead = false;
+    const float gs_k = TYPE == QFP4_CACHE_NVFP4 ? *p.gs_k : 1.0f, gs_v = TYPE == QFP4_CACHE_NVFP4 ? *p.gs_v : 1.0f;
+    int64_t at = lo;
+
+    while (at < hi) {
+        // ---- a segment: the CTA's tiles of one (sequence, key head, query block)
+        const int b = cur.b, item = cur.item, seg_first = cur.tile, seg_tiles = cur.tiles, len = cur.len, first = cur.first;
+        const int head = item / p.blocks, qblock = item - head * p.blocks;
+        const int visible = p.window > 0 && len > p.window ? len - p.window : 0;      // first token that counts
+        const int queries = min(QUERIES, p.group - qblock * QUERIES);
+        const int64_t q_head0 = static_cast<int64_t>(head) * p.group + qblock * QUERIES;
+
+        uint32_t qf[NT][KSTEPS][2];
+        float qmul[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const bool has = 8 * n + g < queries;
+            const __nv_bfloat16 *src = p.q + b * p.ldq + (q_head0 + 8 * n + g) * D;
+            // k step (chunk i, u): lane t's dims are four of chunk 4 i + t of the row
+            constexpr int EC = U.row / 4 >= 16 ? 16 * D / U.row : D / 4;    // elements of a chunk
+            float amax = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < KSTEPS; ++ks) {
+                const int i = ks / (EC / 4), u = ks % (EC / 4);
+                uint2 v = make_uint2(0, 0);
+                if (has) v = *reinterpret_cast<const uint2 *>(src + (4 * i + t) * EC + 4 * u);
+                qf[n][ks][0] = v.x;
+                qf[n][ks][1] = v.y;
+                if (TYPE != QFP4_CACHE_BF16) {
+                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v.x << 16)), fabsf(__uint_as_float(v.x & 0xFFFF0000u))));
+                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v.y << 16)), fabsf(__uint_as_float(v.y & 0xFFFF0000u))));
+                }
+            }
+            float back = 1.0f;      // what the products of this lane's query are multiplied by
+            if (TYPE != QFP4_CACHE_BF16) {
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                // the exponent that takes amax to [2^14, 2^15); none for zeros and infinities
+                int e = 14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127);
+                e = amax == 0.0f || !(amax < 3.4e38f) ? 0 : max(-126, min(126, e));
+                const float up = pow2(e);
+                back = pow2(-e);
+#pragma unroll
+                for (int ks = 0; ks < KSTEPS; ++ks)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t v = qf[n][ks][r];
+                        qf[n][ks][r] = pack_f16(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+                    }
+            }
+            back *= p.scale_log2 * gs_k;
+            // the products' columns 2t, 2t + 1
+            qmul[n][0] = __shfl_sync(0xffffffffu, back, 8 * t);
+            qmul[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+        }
+
+        float o[NT][MTILES][4], m[NT][2], mw[NT][2], l[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int i = 0; i < MTILES; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[n][i][k] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                m[n][k] = mw[n][k] = -INFINITY;
+                l[n][k] = 0.0f;
+            }
+        }
+
+        do {
+            const int token0 = first + cur.tile * TILE + warp * C::TOKENS;
+            if (!mbar_wait(bars + 8 * stage, phase)) {
+                if (lane == 0) atomicOr(p.status, kStatusTimeout);
+                dead = true;
+            }
+            const uint8_t *buf = ring + stage * C::STAGE;
+            const int units = min(UNITS, max(0, (len - token0 + 15) >> 4));
+            if (units > 0) {
+                // ---- logits: rows are tokens g and g + 8 of each unit, columns the queries 2t and 2t + 1
+                float x[UNITS][NT][4];
+                float ls[UNITS][2];     // E4M3: log2 of the value scales
+#pragma unroll
+                for (int un = 0; un < UNITS; ++un) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[un][n][k] = 0.0f;
+                    ls[un][0] = ls[un][1] = 0.0f;
+                    if (un < units) {
+                        const uint8_t *unit = buf + un * C::UNIT;
+                        constexpr int CB = U.row / 4 >= 16 ? 16 : U.row / 4;    // bytes of a chunk
+                        constexpr int CHUNKS = U.row / (4 * CB), KPC = KSTEPS / CHUNKS;
+#pragma unroll
+                        for (int i = 0; i < CHUNKS; ++i) {
+                            uint32_t w[2][4];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint8_t *src = unit + U.k_code(8 * h, (4 * i) * CB) + g * (4 * CB) + t * CB;
+                                if constexpr (CB == 16) {
+                                    const uint4 v = *reinterpret_cast<const uint4 *>(src);
+                                    w[h][0] = v.x, w[h][1] = v.y, w[h][2] = v.z, w[h][3] = v.w;
+                                } else {
+                                    const uint2 v = *reinterpret_cast<const uint2 *>(src);
+                                    w[h][0] = v.x, w[h][1] = v.y, w[h][2] = w[h][3] = 0;
+                                }
+                            }
+                            uint32_t sc[2][2] = {};     // NVFP4: a block's scale, twice
+                            if constexpr (TYPE == QFP4_CACHE_NVFP4) {
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    if constexpr (CB == 16) {
+                                        const uint32_t v = fp8x2<0>(*reinterpret_cast<const uint16_t *>(
+                                            unit + U.k_scales + (8 * h + g) * U.scale + 2 * (4 * i + t)));
+                                        sc[h][0] = __byte_perm(v, 0, 0x1010);
+                                        sc[h][1] = __byte_perm(v, 0, 0x3232);
+                                    } else {
+                                        const uint32_t v = fp8x2<0>(unit[U.k_scales + (8 * h + g) * U.scale + t]);
+                                        sc[h][0] = __byte_perm(v, 0, 0x1010);
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int u = 0; u < KPC; ++u) {
+                                uint32_t a[4];
+                                if constexpr (TYPE == QFP4_CACHE_NVFP4) {
+                                    const int word = u / 2;
+                                    const uint32_t s0 = sc[0][u / 4], s1 = sc[1][u / 4];
+                                    if (u & 1) {
+                                        a[0] = mul_f16x2(fp4x2<2>(w[0][word]), s0);
+                                        a[1] = mul_f16x2(fp4x2<2>(w[1][word]), s1);
+                                        a[2] = mul_f16x2(fp4x2<3>(w[0][word]), s0);
+                                        a[3] = mul_f16x2(fp4x2<3>(w[1][word]), s1);
+                                    } else {
+                                        a[0] = mul_f16x2(fp4x2<0>(w[0][word]), s0);
+                                        a[1] = mul_f16x2(fp4x2<0>(w[1][word]), s1);
+                                        a[2] = mul_f16x2(fp4x2<1>(w[0][word]), s0);
+                                        a[3] = mul_f16x2(fp4x2<1>(w[1][word]), s1);
+                                    }
+                                } else if constexpr (TYPE == QFP4_CACHE_E4M3) {
+                                    a[0] = fp8x2<0>(w[0][u]);
+                                    a[1] = fp8x2<0>(w[1][u]);
+                                    a[2] = fp8x2<1>(w[0][u]);
+                                    a[3] = fp8x2<1>(w[1][u]);
+                                } else {
+                                    a[0] = w[0][2 * u];
+                                    a[1] = w[1][2 * u];
+                                    a[2] = w[0][2 * u + 1];
+                                    a[3] = w[1][2 * u + 1];
+                                }
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) mma<TYPE>(x[un][n], a, qf[n][i * KPC + u][0], qf[n][i * KPC + u][1]);
+                            }
+                        }
+                        float ks0 = 1.0f, ks1 = 1.0f;
+                        if constexpr (TYPE == QFP4_CACHE_E4M3) {
+                            ks0 = *reinterpret_cast<const float *>(unit + U.k_token_scale(0) + 4 * g);
+                            ks1 = *reinterpret_cast<const float *>(unit + U.k_token_scale(8) + 4 * g);
+                            ls[un][0] = log2_fast(*reinterpret_cast<const float *>(unit + U.v_token_scale(0) + 4 * g));
+                            ls[un][1] = log2_fast(*reinterpret_cast<const float *>(unit + U.v_token_scale(8) + 4 * g));
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            x[un][n][0] *= qmul[n][0] * ks0;
+                            x[un][n][1] *= qmul[n][1] * ks0;
+                            x[un][n][2] *= qmul[n][0] * ks1;
+                            x[un][n][3] *= qmul[n][1] * ks1;
+                        }
+                    }
+                }
+                // tokens outside the sequence or its window: whatever lies there does not count
+                if (token0 < visible || token0 + C::TOKENS > len) {
+#pragma unroll
+                    for (int un = 0; un < UNITS; ++un)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int token = token0 + 16 * un + 8 * h + g;
+                            if (token < visible || token >= len) {
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) x[un][n][2 * h] = x[un][n][2 * h + 1] = -INFINITY;
+                                ls[un][h] = 0.0f;
+                            }
+                        }
+                }
+                // ---- running maxima; with value scales, those of x + log2 s as well
+                float base[NT][2], base_w[NT][2];
+                bool moved = false;
+                float alpha[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float top = -INFINITY, top_w = -INFINITY;
+#pragma unroll
+                        for (int un = 0; un < UNITS; ++un) {
+                            top = max_nan(top, max_nan(x[un][n][k], x[un][n][2 + k]));
+                            if (TYPE == QFP4_CACHE_E4M3)
+                                top_w = max_nan(top_w, max_nan(x[un][n][k] + ls[un][0], x[un][n][2 + k] + ls[un][1]));
+                        }
+#pragma unroll
+                        for (int s = 4; s < 32; s <<= 1) {
+                            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, s));
+                            if (TYPE == QFP4_CACHE_E4M3) top_w = max_nan(top_w, __shfl_xor_sync(0xffffffffu, top_w, s));
+                        }
+                        const float m_new = max_nan(m[n][k], top);
+                        base[n][k] = m_new == -INFINITY ? 0.0f : m_new;
+                        const float a = exp2_fast(m[n][k] - base[n][k]);
+                        l[n][k] *= a;
+                        m[n][k] = m_new;
+                        alpha[n][k] = a;
+                        if (TYPE == QFP4_CACHE_E4M3) {
+                            const float w_new = max_nan(mw[n][k], top_w);
+                            base_w[n][k] = w_new == -INFINITY ? 0.0f : w_new;
+                            alpha[n][k] = exp2_fast(mw[n][k] - base_w[n][k]);
+                            mw[n][k] = w_new;
+                        }
+                        moved |= alpha[n][k] != 1.0f;
+                    }
+                if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < MTILES; ++i) {
+                            o[n][i][0] *= alpha[n][0];
+                            o[n][i][1] *= alpha[n][1];
+                            o[n][i][2] *= alpha[n][0];
+                            o[n][i][3] *= alpha[n][1];
+                        }
+                }
+                // ---- weights and their products with the values
+#pragma unroll
+                for (int un = 0; un < UNITS; ++un) {
+                    if (un >= units) continue;
+                    const uint8_t *unit = buf + un * C::UNIT;
+                    uint32_t pf[NT][2], pl[NT][2];      // operand P^T, and what BF16 leaves of it
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float x0 = x[un][n][2 * h], x1 = x[un][n][2 * h + 1];
+                            const float p0 = exp2_fast(x0 - base[n][0]), p1 = exp2_fast(x1 - base[n][1]);
+                            l[n][0] += p0;
+                            l[n][1] += p1;
+                            pl[n][h] = 0;
+                            if constexpr (TYPE == QFP4_CACHE_BF16) {
+                                const uint32_t v = pack_bf16(p0, p1);
+                                pf[n][h] = transpose8x8(v);
+                                pl[n][h] = transpose8x8(pack_bf16(p0 - __uint_as_float(v << 16), p1 - __uint_as_float(v & 0xFFFF0000u)));
+                            } else if constexpr (TYPE == QFP4_CACHE_E4M3) {
+                                pf[n][h] = transpose8x8(pack_f16(exp2_fast(x0 + ls[un][h] - base_w[n][0]),
+                                                                 exp2_fast(x1 + ls[un][h] - base_w[n][1])));
+                            } else {
+                                pf[n][h] = transpose8x8(pack_f16(p0, p1));
+                            }
+                        }
+                    // this lane's tokens s = 2 h + e: 8 h + 2 t + e
+                    const int tok = token0 + 16 * un + 2 * t;
+                    const bool part = token0 + 16 * un < visible || token0 + 16 * un + 16 > len;
+                    uint32_t live = 0xF;
+                    if (part) {
+                        live = 0;
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) {
+                            const int token = tok + 8 * (s >> 1) + (s & 1);
+                            if (token >= visible && token < len) live |= 1u << s;
+                        }
+                    }
+                    constexpr int W = U.row / 8;                        // bytes of a token that a lane holds
+                    constexpr int STEP = W >= 16 ? 4 : W / 4;           // words of a token per round
+#pragma unroll
+                    for (int y0 = 0; y0 < W / 4; y0 += STEP) {
+                        uint32_t w[4][STEP];
+                        const uint4 *src = reinterpret_cast<const uint4 *>(unit + U.v_codes) + lane;
+                        if constexpr (W >= 16) {
+#pragma unroll
+                            for (int s = 0; s < 4; ++s) {
+                                const uint4 v = src[(s * (W / 16) + y0 / 4) * 32];
+                                w[s][0] = v.x, w[s][1] = v.y, w[s][2] = v.z, w[s][3] = v.w;
+                            }
+                        } else if constexpr (W == 8) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint4 v = src[h * 32];
+                                w[2 * h][0] = v.x, w[2 * h][1] = v.y, w[2 * h + 1][0] = v.z, w[2 * h + 1][1] = v.w;
+                            }
+                        } else {
+                            const uint4 v = src[0];
+                            w[0][0] = v.x, w[1][0] = v.y, w[2][0] = v.z, w[3][0] = v.w;
+                        }
+                        if (part) {
+#pragma unroll
+                            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                                for (int y = 0; y < STEP; ++y) w[s][y] = live >> s & 1 ? w[s][y] : 0u;
+                        }
+#pragma unroll
+                        for (int y = 0; y < STEP; ++y) {
+                            if constexpr (TYPE == QFP4_CACHE_NVFP4) {
+                                // block of these eight dims; the scales of the lane's four tokens lie together
+                                const int blk = (g * (D / 8) + 8 * (y0 + y)) / 16;
+                                uint32_t sw = *reinterpret_cast<const uint32_t *>(unit + U.v_scales + blk * 16 + 4 * t);
+                                if (part) sw &= __byte_perm(0x0000FF00u, 0, (live & 1) | (live & 2) << 3 | (live & 4) << 6 | (live & 8) << 9);
+                                const uint32_t s01 = fp8x2<0>(sw), s23 = fp8x2<1>(sw);
+                                const uint32_t sc[4] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
+                                                        __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
+                                uint32_t v[4][4];       // [token][pair of dims]
+#pragma unroll
+                                for (int s = 0; s < 4; ++s) {
+                                    v[s][0] = mul_f16x2(fp4x2<0>(w[s][y]), sc[s]);
+                                    v[s][1] = mul_f16x2(fp4x2<1>(w[s][y]), sc[s]);
+                                    v[s][2] = mul_f16x2(fp4x2<2>(w[s][y]), sc[s]);
+                                    v[s][3] = mul_f16x2(fp4x2<3>(w[s][y]), sc[s]);
+                                }
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const uint32_t a[4] = {__byte_perm(v[0][k], v[1][k], 0x5410), __byte_perm(v[0][k], v[1][k], 0x7632),
+                                                           __byte_perm(v[2][k], v[3][k], 0x5410), __byte_perm(v[2][k], v[3][k], 0x7632)};
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * (y0 + y) + k], a, pf[n][0], pf[n][1]);
+                                }
+                            } else if constexpr (TYPE == QFP4_CACHE_E4M3) {
+                                const uint32_t lo0 = __byte_perm(w[0][y], w[1][y], 0x5140), hi0 = __byte_perm(w[0][y], w[1][y], 0x7362);
+                                const uint32_t lo1 = __byte_perm(w[2][y], w[3][y], 0x5140), hi1 = __byte_perm(w[2][y], w[3][y], 0x7362);
+                                const uint32_t a0[4] = {fp8x2<0>(lo0), fp8x2<1>(lo0), fp8x2<0>(lo1), fp8x2<1>(lo1)};
+                                const uint32_t a1[4] = {fp8x2<0>(hi0), fp8x2<1>(hi0), fp8x2<0>(hi1), fp8x2<1>(hi1)};
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    mma_f16(o[n][2 * (y0 + y)], a0, pf[n][0], pf[n][1]);
+                                    mma_f16(o[n][2 * (y0 + y) + 1], a1, pf[n][0], pf[n][1]);
+                                }
+                            } else {
+                                const uint32_t a[4] = {__byte_perm(w[0][y], w[1][y], 0x5410), __byte_perm(w[0][y], w[1][y], 0x7632),
+                                                       __byte_perm(w[2][y], w[3][y], 0x5410), __byte_perm(w[2][y], w[3][y], 0x7632)};
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    mma_bf16(o[n][y0 + y], a, pf[n][0], pf[n][1]);
+                                    mma_bf16(o[n][y0 + y], a, pl[n][0], pl[n][1]);
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (to_issue > 0) {
+                issue(ahead, page_next, stage);
+                ahead.next<TILE>(p);
+                page_next = --to_issue > 0 ? page_of(ahead) : -1;
+            }
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1;
+            }
+            ++at;
+            cur.next<TILE>(p);
+        } while (at < hi && cur.b == b && cur.item == item);
+
+        // ---- the warps' results joined: o relative to the CTA's maximum, added up in the warps' order
+        const int seg_n = static_cast<int>(cur.b == b && cur.item == item ? cur.tile : seg_tiles) - seg_first;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int s = 4; s < 32; s <<= 1) l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], s);
+                if (g == 0) s_ml[warp * QUERIES + 8 * n + 2 * t + k] = make_float2(m[n][k], l[n][k]);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int turn = 0; turn < kAttnWarps; ++turn) {
+            if (turn == warp) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int q = 8 * n + 2 * t + k;
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int w = 0; w < kAttnWarps; ++w) top = max_nan(top, s_ml[w * QUERIES + q].x);
+                        const float own = TYPE == QFP4_CACHE_E4M3 ? mw[n][k] : m[n][k];
+                        const float f = own == -INFINITY ? 0.0f : exp2_fast(own - top);
+                        // dims g D / 8 + 2 i and the next
+                        float *dst = s_o + q * (D + 4) + g * (D / 8);
+#pragma unroll
+                        for (int i = 0; i < MTILES; ++i) {
+                            float2 v = make_float2(o[n][i][k] * f, o[n][i][2 + k] * f);
+                            if (turn > 0) {
+                                const float2 old = *reinterpret_cast<const float2 *>(dst + 2 * i);
+                                v.x += old.x;
+                                v.y += old.y;
+                            }
+                            *reinterpret_cast<float2 *>(dst + 2 * i) = v;
+                        }
+                    }
+            }
+            __syncthreads();
+        }
+        const bool whole = seg_first == 0 && seg_n == seg_tiles;
+        constexpr int PIECE = attn_piece_floats(QUERIES, D);
+        float *piece = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (seg_first == 0)) * PIECE;
+        // thread -> query tid / (threads per query), dims
+        constexpr int PER = kAttnThreads / QUERIES, DIMS = D / PER;     // 16 or 8 threads per query
+        const int q = tid / PER, d0 = (tid % PER) * 4;
+        float m_all = -INFINITY, l_all = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) m_all = max_nan(m_all, s_ml[w * QUERIES + q].x);
+#pragma unroll
+        for (int w = 0; w < kAttnWarps; ++w) {
+            const float2 v = s_ml[w * QUERIES + q];
+            if (v.x != -INFINITY) l_all += v.y * exp2_fast(v.x - m_all);
+        }
+        float acc[DIMS];
+#pragma unroll
+        for (int i = 0; i < DIMS / 4; ++i) {
+            const float4 v = *reinterpret_cast<const float4 *>(s_o + q * (D + 4) + d0 + 4 * PER * i);
+            acc[4 * i] = v.x, acc[4 * i + 1] = v.y, acc[4 * i + 2] = v.z, acc[4 * i + 3] = v.w;
+        }
+        bool write = whole;
+        if (!whole) {
+#pragma unroll
+            for (int i = 0; i < DIMS / 4; ++i)
+                *reinterpret_cast<float4 *>(piece + q * D + d0 + 4 * PER * i) =
+                    make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+            if (tid % PER == 0) *reinterpret_cast<float2 *>(piece + QUERIES * D + 2 * q) = make_float2(m_all, l_all);
+            // CTAs that hold the item's first and last tile
+            const int64_t i0 = at - seg_n - seg_first, i1 = i0 + seg_tiles - 1;
+            const int64_t c0 = ((i0 + 1) * ctas - 1) / total, c1 = ((i1 + 1) * ctas - 1) / total;
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) s_last = atom_add_acq_rel_gpu(p.counters + c0, 1u) == static_cast<uint32_t>(c1 - c0);
+            __syncthreads();
+            write = s_last != 0;
+            if (write) {
+                __threadfence();
+                if (tid == 0) p.counters[c0] = 0;
+                m_all = -INFINITY;
+                l_all = 0.0f;
+#pragma unroll
+                for (int i = 0; i < DIMS; ++i) acc[i] = 0.0f;
+                for (int64_t c = c0; c <= c1; ++c) {
+                    const float *from = p.partial + (2 * c + (c == c0)) * PIECE;
+                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(from + QUERIES * D + 2 * q));
+                    const float top = max_nan(m_all, ml.x);
+                    const float fa = m_all == -INFINITY ? 0.0f : exp2_fast(m_all - top);
+                    const float fb = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - top);
+                    m_all = top;
+                    l_all = l_all * fa + ml.y * fb;
+#pragma unroll
+                    for (int i = 0; i < DIMS / 4; ++i) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(from + q * D + d0 + 4 * PER * i));
+                        acc[4 * i] = acc[4 * i] * fa + v.x * fb;
+                        acc[4 * i + 1] = acc[4 * i + 1] * fa + v.y * fb;
+                        acc[4 * i + 2] = acc[4 * i + 2] * fa + v.z * fb;
+                        acc[4 * i + 3] = acc[4 * i + 3] * fa + v.w * fb;
+                    }
+                }
+            }
+        }
+        if (write && q < queries) {
+            // no token: zeros
+            const float inv = m_all == -INFINITY ? 0.0f : gs_v / l_all;
+            const int64_t row = static_cast<int64_t>(b) * p.kv_heads * p.group + q_head0 + q;
+#pragma unroll
+            for (int i = 0; i < DIMS / 4; ++i)
+                *reinterpret_cast<uint2 *>(p.out + row * D + d0 + 4 * PER * i) =
+                    make_uint2(pack_bf16(acc[4 * i] * inv, acc[4 * i + 1] * inv), pack_bf16(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
+            if (p.lse && tid % PER == 0)
+                p.lse[row] = m_all == -INFINITY ? -INFINITY : (m_all + log2f(l_all)) * 0.693147180559945309f;
+        }
+        __syncthreads();
+    }
+    if (dead) {     // copies in flight have time to land before the shared memory goes to another CTA
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {
+        }
+    }
+}
+
+// CTAs of this kernel that an SM holds, no more than `most`; asked once.
+template <int TYPE, int D, int NT>
+int attn_per_sm(int most)
+{
+    static std::atomic<int> known{0};
+    int n = known.load(std::memory_order_relaxed);
+    if (n == 0) {
+        using C = AttnCfg<TYPE, D, NT>;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attention_decode_kernel<TYPE, D, NT>, kAttnThreads,
+                                                          C::SMEM) != cudaSuccess ||
+            n < 1)
+            return 0;
+        known.store(n, std::memory_order_relaxed);
+    }
+    return n < most ? n : most;
+}
+
+// The grid is what the GPU holds at once, whatever the lengths, which only the
+// device knows: 152 SMs times the CTAs of each, at most per_sm.
+template <int TYPE, int D, int NT>
+int attn_launch(const AttnParams &p, int per_sm, cudaStream_t s)
+{
+    using C = AttnCfg<TYPE, D, NT>;
+    auto kernel = attention_decode_kernel<TYPE, D, NT>;
+    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(kernel), C::SMEM);
+    if (rc != QFP4_OK) return rc;
+    const int n = attn_per_sm<TYPE, D, NT>(per_sm);
+    if (n == 0) return QFP4_ERR_CUDA;
+    return launch_status(launch_pdl(kernel, dim3(152 * n), dim3(kAttnThreads), C::SMEM, s, p));
+}
+
+// Of attention_decode_<type>.cu.
+int attn_launch_bf16(const AttnParams &p, int D, int nt, int per_sm, cudaStream_t s);
+int attn_launch_e4m3(const AttnParams &p, int D, int nt, int per_sm, cudaStream_t s);
+int attn_launch_nvfp4(const AttnParams &p, int D, int nt, int per_sm, cudaStream_t s);
+
+// Query heads of a block: those of a group, 8 or 16; 8 where 16 would not fit
+// in the registers (D = 256).
+inline int attn_tiles(int64_t group, int D) { return group > 8 && D <= 128 ? 2 : 1; }
+
+template <int TYPE>
+int attn_launch_type(const AttnParams &p, int D, int nt, int per_sm, cudaStream_t s)
+{
+    if (D == 64) return nt == 1 ? attn_launch<TYPE, 64, 1>(p, per_sm, s) : attn_launch<TYPE, 64, 2>(p, per_sm, s);
+    if (D == 128) return nt == 1 ? attn_launch<TYPE, 128, 1>(p, per_sm, s) : attn_launch<TYPE, 128, 2>(p, per_sm, s);
+    return attn_launch<TYPE, 256, 1>(p, per_sm, s);
+}
+
+}  // namespace qfp4

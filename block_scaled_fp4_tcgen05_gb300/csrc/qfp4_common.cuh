@@ -112,5 +112,7 @@ int status_word_gemm(uint32_t **word);
 int status_word_gemm_sparse(uint32_t **word);
 int status_word_gemm_fp8(uint32_t **word);
 int status_word_fp8_quant(uint32_t **word);
+int status_word_heads(uint32_t **word);
+int status_word_attention(uint32_t **word);
 
 }  // namespace qfp4

@@ -22,6 +22,9 @@ E4M3 = 0
 E5M2 = 1
 SCALE_FP32 = 0
 SCALE_POW2 = 1
+CACHE_BF16 = 0
+CACHE_E4M3 = 1
+CACHE_NVFP4 = 2
 OUT_BF16 = 0
 OUT_FP32 = 1
 SF_ROWMAJOR = 0
@@ -34,6 +37,7 @@ _lib = None
 
 # (restype, argtypes) per exported symbol, mirroring include/qfp4.h
 _i32, _i64, _sz, _vp, _cp = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_char_p
+_f32 = ctypes.c_float
 SIGNATURES = {
     "qfp4_version": (_i32, []),
     "qfp4_status_string": (_cp, [_i32]),
@@ -83,6 +87,22 @@ SIGNATURES = {
     "qfp4_moe_route": (_i32, [_i32, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                               _vp, _sz, _vp]),
     "qfp4_moe_route_backward": (_i32, [_i32, _vp, _i64, _i64, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "qfp4_gemv_nt": (_i32, [_i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "qfp4_qk_norm_rope": (_i32, [_vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _f32, _vp, _i64, _i64, _i32, _vp, _vp,
+                                 _i64, _vp, _i64, _vp]),
+    "qfp4_qk_norm_rope_cache": (_i32, [_vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _f32, _vp, _i64, _i64, _i32, _vp,
+                                       _vp, _i64, _i32, _vp, _i64, _i64, _vp, _vp, _vp, _vp]),
+    "qfp4_qk_norm_rope_backward_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "qfp4_qk_norm_rope_backward": (_i32, [_vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _f32, _vp, _i64, _i64, _i32,
+                                          _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "qfp4_kv_cache_page_bytes": (_sz, [_i32, _i64, _i64, _i64]),
+    "qfp4_kv_cache_write": (_i32, [_i32, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _i64,
+                                   _vp]),
+    "qfp4_kv_cache_read": (_i32, [_i32, _vp, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64,
+                                  _vp]),
+    "qfp4_attention_decode_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
+    "qfp4_attention_decode": (_i32, [_i32, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64,
+                                     _f32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -90,6 +110,8 @@ SIGNATURES = {
 # (function, packer), filled by load().
 _WORDS = ("qfp4_fp8_quantize", "qfp4_fp8_quantize_grouped", "qfp4_fp8_quantize_weight", "qfp4_gemm_nt_fp8",
           "qfp4_gemm_nt_fp8_grouped", "qfp4_gemm_nt_fp8_kgrouped", "qfp4_moe_route", "qfp4_moe_route_backward")
+_LAYER_WORDS = ("qfp4_gemv_nt", "qfp4_qk_norm_rope", "qfp4_qk_norm_rope_cache", "qfp4_qk_norm_rope_backward",
+                "qfp4_kv_cache_write", "qfp4_kv_cache_read", "qfp4_attention_decode")
 _words = {}
 
 
@@ -113,11 +135,12 @@ def load() -> ctypes.CDLL:
                 fn = getattr(lib, name)
                 fn.restype = res
                 fn.argtypes = args
-            for name in _WORDS:
+            for name in _WORDS + _LAYER_WORDS:
                 fn = getattr(lib, name + "_words")
                 fn.restype = _i32
                 fn.argtypes = [ctypes.c_char_p]
-                _words[name] = fn, struct.Struct(f"{len(SIGNATURES[name][1])}q").pack
+                form = "".join("f4x" if a is _f32 else "q" for a in SIGNATURES[name][1])
+                _words[name] = fn, struct.Struct("=" + form).pack
             _lib = lib
         return _lib
 
@@ -523,3 +546,163 @@ def moe_route_backward(logits, ids, counts, n_valid, dgates, dloss, dlogits, val
     _call("qfp4_moe_route_backward", *_logits(logits), T, E, topk, _at(valid, _U8, T), 1 if renorm else 0,
           _at(ids, _I32, pairs), _at(counts, _I32, E), _at(n_valid, _I32, 1), _at(dgates, _F32, pairs),
           _at(dloss, _F32, 1), _at(dlogits, logits.dtype, T * E), _stream(stream))
+
+
+def _rows(t, width, rows, dtype=torch.bfloat16):
+    """(address, elements from row to row) of `rows` rows of `width` elements
+    that lie together: a contiguous matrix, or some columns of one (the heads of
+    one kind in a projection's output)."""
+    if t is None:
+        return 0, width
+    if t.dtype is not dtype or not t.is_cuda:
+        raise ValueError(f"qfp4: expected {dtype} on the GPU, got {t.dtype} on {t.device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        if shape[2] != 1 and stride[2] != 1 or shape[1] != 1 and stride[1] != shape[2]:
+            raise ValueError("qfp4: the heads of a row must lie together")
+        got = shape[1] * shape[2]
+    elif len(shape) == 2:
+        if shape[1] != 1 and stride[1] != 1:
+            raise ValueError("qfp4: the elements of a row must lie together")
+        got = shape[1]
+    else:
+        raise ValueError(f"qfp4: expected rows, got {tuple(shape)}")
+    if shape[0] != rows or got != width:
+        raise ValueError(f"qfp4: expected {rows} rows of {width} elements, got {tuple(shape)}")
+    return t.data_ptr(), stride[0] if rows > 1 and width > 0 else width
+
+
+def gemv_nt(fmt, X, W, W_sf, gs_w, D, stream=None) -> None:
+    """D = X W^T: up to 16 BF16 rows X [M, K] times 4-bit weights W [N, K/2] with
+    scales in the MMA layout (B of gemm_nt); gs_w may be None."""
+    M, K = X.shape
+    N = W.shape[0]
+    if W.shape[1] * 2 != K:
+        raise ValueError(f"qfp4: W has {W.shape[1] * 2} columns, X {K}")
+    x, ldx = _rows(X, K, M)
+    d, ldd = _rows(D, N, M)
+    g = 16 if fmt == NVFP4 else 32
+    _call("qfp4_gemv_nt", fmt, M, N, K, x, ldx, _at(W, _U8, N * K // 2),
+          _at(W_sf, _U8, (N + 127) // 128 * 128 * ((K // g + 3) // 4 * 4)), _at(gs_w, _F32, 1), d, ldd, _stream(stream))
+
+
+def _head_args(QKV, q_heads, kv_heads, head_dim, value_heads, q_weight, k_weight, cos_sin, positions, eps,
+               interleaved):
+    """What the calls on query and key heads share, in the C ABI's order."""
+    T, width = QKV.shape
+    if width < (q_heads + kv_heads + value_heads) * head_dim:
+        raise ValueError(f"qfp4: {q_heads} + {kv_heads} heads of {head_dim} do not fit in rows of {width}")
+    x, ld = _rows(QKV, width, T)
+    rows, rotary = (0, 0) if cos_sin is None else cos_sin.shape
+    return (x, ld, T, q_heads, kv_heads, head_dim, _at(q_weight, _BF16, head_dim), _at(k_weight, _BF16, head_dim), eps,
+            _at(cos_sin, _F32), rows, rotary, 1 if interleaved else 0, _at(positions, _I32, T))
+
+
+def qk_norm_rope(QKV, q_heads, kv_heads, Q_out, K_out, q_weight=None, k_weight=None, cos_sin=None, positions=None,
+                 eps=1e-6, interleaved=False, stream=None) -> None:
+    """RMS norms of the query and key heads (weights None: none) and the rotation
+    by cos_sin [positions, rotary_dim] (None: none), from the QKV projection's
+    output [T, (q_heads + kv_heads + ...) * head_dim].  Q_out [T, q_heads,
+    head_dim] and K_out [T, kv_heads, head_dim] may be views of QKV itself."""
+    T, D = QKV.shape[0], Q_out.shape[2]
+    args = _head_args(QKV, q_heads, kv_heads, D, 0, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    q, ldq = _rows(Q_out, q_heads * D, T)
+    k, ldk = _rows(K_out, kv_heads * D, T)
+    _call("qfp4_qk_norm_rope", *args, q, ldq, k, ldk, _stream(stream))
+
+
+def qk_norm_rope_backward_workspace_bytes(T: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(load().qfp4_qk_norm_rope_backward_workspace_bytes(T, q_heads, kv_heads, head_dim))
+
+
+def qk_norm_rope_backward(QKV, q_heads, kv_heads, dQ, dK, dQKV, dq_weight, dk_weight, workspace, q_weight=None,
+                          k_weight=None, cos_sin=None, positions=None, eps=1e-6, interleaved=False,
+                          stream=None) -> None:
+    """Gradient of qk_norm_rope: the query and key heads of dQKV (its value heads
+    stay) and, fp32 [head_dim], those of the weights; without weights they and
+    the workspace may be None."""
+    T, D = QKV.shape[0], dQ.shape[2]
+    args = _head_args(QKV, q_heads, kv_heads, D, 0, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    q, ldq = _rows(dQ, q_heads * D, T)
+    k, ldk = _rows(dK, kv_heads * D, T)
+    if dQKV.shape != QKV.shape:
+        raise ValueError(f"qfp4: dQKV is {tuple(dQKV.shape)}, QKV {tuple(QKV.shape)}")
+    dx, ldx = _rows(dQKV, QKV.shape[1], T)
+    ws, nbytes = (0, 0) if workspace is None else (_at(workspace, workspace.dtype), workspace.nbytes)
+    _call("qfp4_qk_norm_rope_backward", *args, q, ldq, k, ldk, dx, ldx, _at(dq_weight, _F32, D),
+          _at(dk_weight, _F32, D), ws, nbytes, _stream(stream))
+
+
+def kv_cache_page_bytes(type: int, kv_heads: int, head_dim: int, page_size: int) -> int:
+    """Bytes of a page; a cache is a uint8 tensor of that many per page."""
+    return int(load().qfp4_kv_cache_page_bytes(type, kv_heads, head_dim, page_size))
+
+
+_CACHE_TOKEN_BITS = {CACHE_BF16: lambda D: 32 * D, CACHE_E4M3: lambda D: 16 * D + 64, CACHE_NVFP4: lambda D: 9 * D}
+
+
+def _cache(type, cache, kv_heads, D, page_size):
+    """(address, pages) of a cache whose pages have that layout's size."""
+    token = _CACHE_TOKEN_BITS[type](D) // 8 if type in _CACHE_TOKEN_BITS else 1
+    pages, page = cache.shape[0], token * kv_heads * page_size
+    if type in _CACHE_TOKEN_BITS and cache.numel() != pages * page:
+        raise ValueError(f"qfp4: a page of this cache has {page} bytes, got {tuple(cache.shape)}")
+    return _at(cache, _U8), pages
+
+
+def kv_cache_write(type, K, V, slots, cache, page_size, gs_k=None, gs_v=None, stream=None) -> None:
+    """Quantises K and V [T, kv_heads, head_dim] (BF16; heads of a projection's
+    output, or whole) into the slots (int32 [T], negative: skipped) of the cache
+    [pages, ...] (uint8, kv_cache_page_bytes per page)."""
+    T, H, D = K.shape
+    k, ldk = _rows(K, H * D, T)
+    v, ldv = _rows(V, H * D, T)
+    c, pages = _cache(type, cache, H, D, page_size)
+    _call("qfp4_kv_cache_write", type, k, ldk, v, ldv, T, H, D, _at(slots, _I32, T), _at(gs_k, _F32, 1),
+          _at(gs_v, _F32, 1), c, pages, page_size, _stream(stream))
+
+
+def kv_cache_read(type, cache, page_size, slots, K_out, V_out, gs_k=None, gs_v=None, stream=None) -> None:
+    """The tokens at these slots in BF16, K_out and V_out [T, kv_heads, head_dim]
+    (either may be None); a negative slot gives zeros."""
+    T, H, D = (V_out if K_out is None else K_out).shape
+    k, ldk = _rows(K_out, H * D, T)
+    v, ldv = _rows(V_out, H * D, T)
+    c, pages = _cache(type, cache, H, D, page_size)
+    _call("qfp4_kv_cache_read", type, c, pages, page_size, H, D, _at(slots, _I32, T), T, _at(gs_k, _F32, 1),
+          _at(gs_v, _F32, 1), k, ldk, v, ldv, _stream(stream))
+
+
+def qk_norm_rope_cache(QKV, q_heads, kv_heads, Q_out, type, cache, page_size, slots, q_weight=None, k_weight=None,
+                       cos_sin=None, positions=None, gs_k=None, gs_v=None, eps=1e-6, interleaved=False,
+                       stream=None) -> None:
+    """qk_norm_rope with the keys and the value heads behind them quantised
+    straight into the cache."""
+    T, D = QKV.shape[0], Q_out.shape[2]
+    args = _head_args(QKV, q_heads, kv_heads, D, kv_heads, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    q, ldq = _rows(Q_out, q_heads * D, T)
+    c, pages = _cache(type, cache, kv_heads, D, page_size)
+    _call("qfp4_qk_norm_rope_cache", *args, q, ldq, type, c, pages, page_size, _at(slots, _I32, T),
+          _at(gs_k, _F32, 1), _at(gs_v, _F32, 1), _stream(stream))
+
+
+def attention_decode_workspace_bytes(B: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(load().qfp4_attention_decode_workspace_bytes(B, q_heads, kv_heads, head_dim))
+
+
+def attention_decode(type, Q, cache, page_size, page_table, lengths, scale, O, workspace, gs_k=None, gs_v=None,
+                     kv_heads=None, lse=None, window=0, stream=None) -> None:
+    """Attention of one new token per sequence, Q and O [B, q_heads, head_dim],
+    over the paged cache [pages, kv_heads, ...] (kv_heads: where the cache has
+    another shape); page_table int32 [B, max_pages], lengths int32 [B].  The
+    workspace is zeroed once, before its first use."""
+    B, H, D = Q.shape
+    heads = cache.shape[1] if kv_heads is None else kv_heads
+    q, ldq = _rows(Q, H * D, B)
+    c, pages = _cache(type, cache, heads, D, page_size)
+    if page_table.shape[0] != B:
+        raise ValueError(f"qfp4: page_table has {page_table.shape[0]} rows for {B} sequences")
+    _call("qfp4_attention_decode", type, q, ldq, B, H, heads, D, c, pages, page_size, _at(page_table, _I32),
+          page_table.shape[1], _at(lengths, _I32, B), window, scale, _at(gs_k, _F32, 1), _at(gs_v, _F32, 1),
+          _at(O, _BF16, B * H * D), _at(lse, _F32, B * H), _at(workspace, workspace.dtype), workspace.nbytes,
+          _stream(stream))

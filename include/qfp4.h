@@ -87,8 +87,10 @@ int qfp4_device_check(void);
  * QFP4_OK; QFP4_ERR_TIMEOUT if any kernel of this library gave up on a
  * bounded wait since the last poll (its outputs are then undefined); or
  * QFP4_ERR_INVALID_ARG if a grouped call found its device row_offsets
- * unusable (see qfp4_global_scale_grouped) and wrote nothing, or a gathering
- * call met a row index beyond its input (see qfp4_fp8_quantize). */
+ * unusable (see qfp4_global_scale_grouped) and wrote nothing, or a call met a
+ * row index, position, slot, page or length beyond what it was given (see
+ * qfp4_fp8_quantize, qfp4_qk_norm_rope, qfp4_kv_cache_write,
+ * qfp4_attention_decode). */
 int qfp4_poll_device_status(void *stream);
 
 /* ---------------------------------------------------------------------- */
@@ -672,6 +674,184 @@ int qfp4_moe_route_backward(int logits_type, const void *logits, int64_t T, int6
                             const uint8_t *valid, int renorm, const int32_t *ids, const int32_t *counts,
                             const int32_t *n_valid, const float *dgates, const float *dloss, void *dlogits,
                             void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Few rows times 4-bit weights                                             */
+/* ---------------------------------------------------------------------- */
+
+/* D[m,n] = bf16_rne(gs_w * sum_k x[m,k] * w[n,k]) with x in BF16 and 4-bit
+ * weights w = E2M1(W) * SF_W: the decode product of a few tokens whose
+ * activations stay unquantised.
+ *   X_bf16    [M, K], ldx elements from row to row
+ *   W_packed  [N, K/2], W_sf MMA layout for [N, K/g]: B of qfp4_gemm_nt
+ *   gs_w      DEVICE fp32 (NULL = 1.0; MXFP4 ignores it)
+ *   D_bf16    [M, N], ldd elements from row to row
+ * Requirements: M <= 16 (more rows: qfp4_gemm_nt), any N, K % 128 == 0,
+ * ldx >= K, ldx % 8 == 0, ldd >= N, N and K <= 2^30, X / W / W_sf 16-byte
+ * aligned.  M == 0 or N == 0 launches nothing; K == 0 gives D = 0.  Results
+ * repeat bit for bit.
+ * Accuracy: |D - exact| <= 2^-8 |exact| + (K/16 + 16) 2^-23 sum_k |x_k w_k| +
+ * 2^-33 max|x| sum_k |w_k| (elements of x below 2^-22 of their row's largest in
+ * a slice of 1024 lose bits), where no sum leaves fp32's range (scales up to
+ * 2^100). */
+int qfp4_gemv_nt(int fmt, int64_t M, int64_t N, int64_t K, const void *X_bf16, int64_t ldx,
+                 const void *W_packed, const void *W_sf, const float *gs_w, void *D_bf16, int64_t ldd,
+                 void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Norms of queries and keys with the position rotation                     */
+/* ---------------------------------------------------------------------- */
+
+/* From the QKV projection's output, in fp32 with one rounding at the end:
+ *   z = x / sqrt(mean(x^2) + eps) * weight       per head vector x of head_dim
+ *   (a, b) -> (a c - b s, b c + a s)             for each pair of the first
+ *                                                rotary_dim elements of z
+ * with c, s the cosine and sine that the table has for the token's position.
+ *   QKV_bf16   [T, ld]: a token's q_heads query heads, its kv_heads key heads
+ *              (and its value heads, which this call leaves alone)
+ *   q_weight, k_weight  BF16 [head_dim]; both NULL: no norm
+ *   cos_sin    fp32 [table_rows, rotary_dim]: rotary_dim / 2 cosines, then as
+ *              many sines; may be NULL with rotary_dim = 0 (no rotation)
+ *   interleaved  0: pairs (j, j + rotary_dim / 2); 1: pairs (2j, 2j + 1)
+ *   positions  DEVICE int32 [T], the token's row of the table.  A negative one
+ *              marks a row that belongs to no sequence: its outputs stay as
+ *              they are.  One of table_rows or more is treated the same and
+ *              makes the next qfp4_poll_device_status return
+ *              QFP4_ERR_INVALID_ARG.  NULL (rotary_dim = 0 only): every row
+ *              counts.
+ *   Q_out, K_out  BF16, rows of q_heads (kv_heads) x head_dim, ldq (ldk)
+ *              elements from token to token; they may be the heads' own places
+ *              in QKV
+ * Requirements: head_dim and rotary_dim multiples of 16, rotary_dim <= head_dim
+ * <= 256, at most 4096 heads of a kind, T <= 2^30, eps >= 0 and finite, ld, ldq,
+ * ldk multiples of 8, the last a row's length at least; positions 4-byte
+ * aligned, the rest 16-byte.  T == 0 launches nothing.
+ * Accuracy: |y - exact| <= 2^-8 |exact| + 2^-20 (|z_a| + |z_b|) of the pair. */
+int qfp4_qk_norm_rope(const void *QKV_bf16, int64_t ld, int64_t T, int64_t q_heads, int64_t kv_heads,
+                      int64_t head_dim, const void *q_weight, const void *k_weight, float eps,
+                      const float *cos_sin, int64_t table_rows, int64_t rotary_dim, int interleaved,
+                      const int32_t *positions, void *Q_out, int64_t ldq, void *K_out, int64_t ldk,
+                      void *stream);
+
+/* Its gradient, with the weights': for dQ, dK [T, heads x head_dim] (lddq, lddk
+ * elements from token to token)
+ *   dQKV        the query and key heads of rows of lddqkv elements; the value
+ *               heads' places stay as they are.  Rows without a position get
+ *               zeros.  dQKV may be QKV, and dQ and dK may be their heads'
+ *               places in it.
+ *   dq_weight, dk_weight  fp32 [head_dim], overwritten (NULL without weights)
+ *   workspace   DEVICE scratch, 16-byte aligned, of ws_bytes >=
+ *               qfp4_qk_norm_rope_backward_workspace_bytes(...); need not be
+ *               cleared.  One call at a time per workspace.  Not used without
+ *               weights.
+ * QKV is the forward call's input (before the norm).  Other arguments and
+ * requirements as there.  T == 0 writes zero weight gradients.  Results repeat
+ * bit for bit. */
+size_t qfp4_qk_norm_rope_backward_workspace_bytes(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+int qfp4_qk_norm_rope_backward(const void *QKV_bf16, int64_t ld, int64_t T, int64_t q_heads, int64_t kv_heads,
+                               int64_t head_dim, const void *q_weight, const void *k_weight, float eps,
+                               const float *cos_sin, int64_t table_rows, int64_t rotary_dim, int interleaved,
+                               const int32_t *positions, const void *dQ, int64_t lddq, const void *dK, int64_t lddk,
+                               void *dQKV, int64_t lddqkv, float *dq_weight, float *dk_weight, void *workspace,
+                               size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Paged key-value cache                                                    */
+/* ---------------------------------------------------------------------- */
+
+/* Element types of a cache: BF16 as it is; E4M3 codes with one fp32 scale per
+ * head vector (rule of qfp4_fp8_quantize, QFP4_SCALE_FP32, over head_dim
+ * elements); NVFP4 (rule of qfp4_quantize) with global scales of K and of V that
+ * the caller has calibrated. */
+enum { QFP4_CACHE_BF16 = 0, QFP4_CACHE_E4M3 = 1, QFP4_CACHE_NVFP4 = 2 };
+
+/* A cache is [pages][kv_heads][page_size / 16] units of 16 tokens of one head.
+ * A page is one contiguous piece of qfp4_kv_cache_page_bytes(...) bytes and may
+ * be copied as such.  A token's slot is page * page_size + its place in the page.
+ * A unit holds K codes, K scales, V codes, V scales.  With row the code bytes of
+ * a head vector, token j = 8 h + 2 t + e of the unit (e in {0, 1}, t in 0..3) and
+ * byte x of its row:
+ *   K codes   at ((h * (row / p) + x / p) * 8 + j % 8) * p + x % p, p = min(64, row)
+ *   V codes   w = row / 8, a = (2 h + e) * w + x % w:
+ *             at ((a / 16) * 32 + 4 * (x / w) + t) * 16 + a % 16
+ *   scales    E4M3: fp32 [token]; NVFP4: K [token][head_dim / 16], V
+ *             [head_dim / 16][t][h][e]
+ * so that a warp reads them as operands of the tensor cores' products.
+ * head_dim is 64, 128 or 256, page_size a multiple of 16 up to 65536, and
+ * pages * page_size <= 2^31 - 1.  0 for sizes that no cache has. */
+size_t qfp4_kv_cache_page_bytes(int type, int64_t kv_heads, int64_t head_dim, int64_t page_size);
+
+/* Quantises K and V [T, kv_heads, head_dim] (BF16, ldk and ldv elements from
+ * token to token) into their slots.
+ *   slots   DEVICE int32 [T]; a negative one skips the token; one beyond the
+ *           cache does too and makes the next qfp4_poll_device_status return
+ *           QFP4_ERR_INVALID_ARG.  Two tokens of a call must not have the same
+ *           slot (it would keep a mixture of both).
+ *   gs_k, gs_v  DEVICE fp32 (NVFP4 only)
+ * Bit-exact to the types' rules.  Requirements: ldk, ldv multiples of 8, T <=
+ * 2^30, K / V / cache 16-byte aligned, the rest 4-byte.  T == 0 launches
+ * nothing. */
+int qfp4_kv_cache_write(int type, const void *K_bf16, int64_t ldk, const void *V_bf16, int64_t ldv, int64_t T,
+                        int64_t kv_heads, int64_t head_dim, const int32_t *slots, const float *gs_k,
+                        const float *gs_v, void *cache, int64_t pages, int64_t page_size, void *stream);
+
+/* The tokens at these slots back in BF16 (code * scale in fp32, rounded), into
+ * K_out and V_out [T, kv_heads, head_dim]; either may be NULL.  A negative slot
+ * gives zeros, one beyond the cache too, and reports.  Requirements as
+ * qfp4_kv_cache_write. */
+int qfp4_kv_cache_read(int type, const void *cache, int64_t pages, int64_t page_size, int64_t kv_heads,
+                       int64_t head_dim, const int32_t *slots, int64_t T, const float *gs_k, const float *gs_v,
+                       void *K_out, int64_t ldk, void *V_out, int64_t ldv, void *stream);
+
+/* qfp4_qk_norm_rope with the keys and the values (the heads behind the keys in
+ * QKV, unchanged) quantised straight into the cache, from the fp32 values
+ * without a rounding to BF16 between.  A row without a position writes nothing;
+ * one whose slot is negative or beyond the cache writes its queries only (and
+ * reports the latter). */
+int qfp4_qk_norm_rope_cache(const void *QKV_bf16, int64_t ld, int64_t T, int64_t q_heads, int64_t kv_heads,
+                            int64_t head_dim, const void *q_weight, const void *k_weight, float eps,
+                            const float *cos_sin, int64_t table_rows, int64_t rotary_dim, int interleaved,
+                            const int32_t *positions, void *Q_out, int64_t ldq, int type, void *cache,
+                            int64_t pages, int64_t page_size, const int32_t *slots, const float *gs_k,
+                            const float *gs_v, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Attention of one new token over the paged cache                          */
+/* ---------------------------------------------------------------------- */
+
+/* For each sequence b and query head h, over the tokens j that it sees,
+ *   O[b,h] = sum_j softmax_j(scale * q . k_j) v_j
+ * with key head h / (q_heads / kv_heads).  The sequence's new token is the last
+ * of its length and already in the cache.
+ *   Q_bf16     [B, q_heads, head_dim], ldq elements from sequence to sequence
+ *   page_table DEVICE int32 [B, max_pages]: pages of the sequence's tokens in
+ *              order.  One outside the cache counts as page 0 and makes the next
+ *              qfp4_poll_device_status return QFP4_ERR_INVALID_ARG.
+ *   lengths    DEVICE int32 [B] in [0, max_pages * page_size]; others are cut to
+ *              that range and report.  What the pages hold beyond a sequence's
+ *              length does not count, whatever it is.
+ *   window     0, or how many of the last tokens are seen
+ *   O_bf16     [B, q_heads, head_dim]; a sequence without tokens gets zeros
+ *   lse        fp32 [B, q_heads] or NULL: ln sum_j exp(scale * q . k_j), -inf
+ *              without tokens
+ *   workspace  DEVICE scratch, 16-byte aligned, of ws_bytes >=
+ *              qfp4_attention_decode_workspace_bytes(...), ZERO-FILLED before
+ *              its first use; every call leaves its counters at zero again.
+ *              One call at a time per workspace, graphs that captured one
+ *              included.
+ * Products and sums in fp32.  The queries enter the products in FP16 (E4M3,
+ * NVFP4 cache), scaled so that an element loses bits only 2^28 below the largest
+ * of its head; the weights are rounded to FP16 (2^-11 of each, 2^-25 of the
+ * largest at least) or, with a BF16 cache, to 16 bits.  Results repeat bit for bit.
+ * Requirements: cache sizes as above, q_heads a multiple of kv_heads, at most
+ * 4096, B <= 2^20, max_pages * page_size <= 2^30, ldq a multiple of 8, Q / cache /
+ * O / workspace 16-byte aligned, the rest 4-byte.  B == 0 launches nothing. */
+size_t qfp4_attention_decode_workspace_bytes(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim);
+int qfp4_attention_decode(int type, const void *Q_bf16, int64_t ldq, int64_t B, int64_t q_heads, int64_t kv_heads,
+                          int64_t head_dim, const void *cache, int64_t pages, int64_t page_size,
+                          const int32_t *page_table, int64_t max_pages, const int32_t *lengths, int64_t window,
+                          float scale, const float *gs_k, const float *gs_v, void *O_bf16, float *lse,
+                          void *workspace, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }
