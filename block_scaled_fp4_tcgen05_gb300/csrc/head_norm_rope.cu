@@ -11,12 +11,12 @@
 // reciprocal root, h = x r and dz = dy turned back:
 //   dw = sum dz h,   dx = r (dz w - h mean(dz w h)).
 //
-// HBM-bound.  8, 16 or 32 lanes hold a vector, 16 bytes each, so every access
-// is a whole 16-byte piece of a row; a warp takes one token and four vectors per
-// group of lanes, so that their loads are in flight together and the angles and
-// weights are read once for all of them.  A pair's other element comes from a
-// lane R/16 away, as the packed BF16 words that were loaded (half the exchanges
-// of fp32 values); w is folded into the cosines and sines.
+// HBM-bound, with the instructions per element close behind, so they are few:
+// 8, 16 or 32 lanes hold a vector, eight elements each, in two pieces of four
+// that hold both elements of their pairs (4 g .. and R/2 + 4 g .., or eight
+// neighbours): no lane needs another's elements but for the sums.  The arithmetic
+// is on packed pairs of fp32.  A warp takes one token's heads of a kind one after
+// the other, the next ones' loads ahead, with the angles and weights in registers.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -25,6 +25,7 @@
 #include "qfp4_common.cuh"
 #include "qfp4_fp4_codes.cuh"
 #include "qfp4_kv_cache.cuh"
+#include "sm103_ptx.cuh"
 
 namespace qfp4 {
 
@@ -57,24 +58,15 @@ struct HeadParams {
     const float *table;         // [table_rows, R]: cos, then sin
     const int32_t *positions;   // [T] or NULL
     int64_t T, table_rows;
-    int32_t heads[3], blocks[3];
+    int32_t heads[3];
+    int32_t blocks[3];          // of each kind in a token; a block is what a warp works on at a time
     int32_t D, R, interleaved, norm;
-    float eps;
+    float eps, inv_D;
     CacheParams c;
 };
 
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-__device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8])
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = bf16_lo(w[i]);
-        x[2 * i + 1] = bf16_hi(w[i]);
-    }
-}
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
@@ -103,66 +95,103 @@ __device__ __forceinline__ float group_max(float v)
     return v;
 }
 
-// What the rotation does to a lane's eight elements: y = a x + b x', with x' the
-// pairs' other elements.
-struct Turn {
-    int partner;        // lane that holds x'
-    bool in;            // these elements turn (all eight or none: R is a multiple of 16)
-    float c[8], s[8];   // s with the sign that x' gets
+// A lane's eight elements of a vector: two pieces of four, as packed pairs that
+// the rotation mixes, (a[i], b[i]) -> (a c - b s, b c + a s).
+struct Eight {
+    uint64_t a[2], b[2];
+};
 
-    template <int LANES>
-    __device__ __forceinline__ void load(const HeadParams &p, int64_t position, int lane)
+struct Raw {
+    uint2 v[2];     // the pieces as they lie in memory
+};
+
+// Interleaved pairs are the low and high halves of a piece's words, the others
+// the two pieces' elements in the same place.
+template <bool INTER>
+__device__ __forceinline__ Eight unpack(const Raw &r)
+{
+    const uint64_t lo0 = f2_pack(bf16_lo(r.v[0].x), bf16_lo(r.v[0].y)), hi0 = f2_pack(bf16_hi(r.v[0].x), bf16_hi(r.v[0].y));
+    const uint64_t lo1 = f2_pack(bf16_lo(r.v[1].x), bf16_lo(r.v[1].y)), hi1 = f2_pack(bf16_hi(r.v[1].x), bf16_hi(r.v[1].y));
+    return INTER ? Eight{{lo0, lo1}, {hi0, hi1}} : Eight{{lo0, hi0}, {lo1, hi1}};
+}
+
+// Back to the pieces' elements in memory's order.
+template <bool INTER>
+__device__ __forceinline__ void elements(const Eight &y, float (&e)[8])
+{
+    f2_unpack(y.a[0], e[0], e[2]);
+    f2_unpack(INTER ? y.b[0] : y.a[1], e[1], e[3]);
+    f2_unpack(INTER ? y.a[1] : y.b[0], e[4], e[6]);
+    f2_unpack(y.b[1], e[5], e[7]);
+}
+
+template <bool INTER>
+__device__ __forceinline__ Raw pack(const Eight &y)
+{
+    float e[8];
+    elements<INTER>(y, e);
+    Raw r;
+    r.v[0] = make_uint2(pack2(e[0], e[1]), pack2(e[2], e[3]));
+    r.v[1] = make_uint2(pack2(e[4], e[5]), pack2(e[6], e[7]));
+    return r;
+}
+
+// Where a lane's pieces lie in a vector, and whether they turn.
+struct Place {
+    int at[2];
+    bool turns;
+
+    template <int LANES, bool INTER>
+    __device__ __forceinline__ static Place of(const HeadParams &p, int g, bool value)
     {
-        const int g = lane % LANES, i0 = 8 * g, half = p.R / 2;
-        in = i0 < p.R;
-        partner = lane;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            c[e] = 1.0f;
-            s[e] = 0.0f;
-        }
-        if (in && !p.interleaved) partner = i0 < half ? lane + half / 8 : lane - half / 8;
-        if (!in) return;
-        const float *row = p.table + position * p.R;
-        if (p.interleaved) {
-            const float4 cv = __ldg(reinterpret_cast<const float4 *>(row + i0 / 2));
-            const float4 sv = __ldg(reinterpret_cast<const float4 *>(row + half + i0 / 2));
-            const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                c[2 * e] = c[2 * e + 1] = cc[e];
-                s[2 * e] = -ss[e];
-                s[2 * e + 1] = ss[e];
-            }
-        } else {
-            const int j = i0 < half ? i0 : i0 - half;
-            const float sign = i0 < half ? -1.0f : 1.0f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float4 cv = __ldg(reinterpret_cast<const float4 *>(row + j) + h);
-                const float4 sv = __ldg(reinterpret_cast<const float4 *>(row + half + j) + h);
-                c[4 * h] = cv.x, c[4 * h + 1] = cv.y, c[4 * h + 2] = cv.z, c[4 * h + 3] = cv.w;
-                s[4 * h] = sign * sv.x, s[4 * h + 1] = sign * sv.y, s[4 * h + 2] = sign * sv.z, s[4 * h + 3] = sign * sv.w;
-            }
-        }
+        const bool turns = !value && 8 * g < p.R, apart = turns && !INTER;
+        return {{apart ? 4 * g : 8 * g, apart ? p.R / 2 + 4 * g : 8 * g + 4}, turns};
     }
-    // The other elements of the pairs, from the words as they were loaded; zero
-    // where nothing turns (there 0 times an infinity would be NaN).
-    __device__ __forceinline__ uint4 others(const HeadParams &p, const uint4 &v) const
+    __device__ __forceinline__ Raw load(const __nv_bfloat16 *x) const
     {
-        uint4 o;
-        if (p.interleaved) {
-            o = make_uint4(__byte_perm(v.x, 0, 0x1032), __byte_perm(v.y, 0, 0x1032), __byte_perm(v.z, 0, 0x1032),
-                           __byte_perm(v.w, 0, 0x1032));
-        } else {
-            o.x = __shfl_sync(0xffffffffu, v.x, partner);
-            o.y = __shfl_sync(0xffffffffu, v.y, partner);
-            o.z = __shfl_sync(0xffffffffu, v.z, partner);
-            o.w = __shfl_sync(0xffffffffu, v.w, partner);
-        }
-        return in ? o : make_uint4(0, 0, 0, 0);
+        // not through the read-only path: an output may take its input's place
+        return {{*reinterpret_cast<const uint2 *>(x + at[0]), *reinterpret_cast<const uint2 *>(x + at[1])}};
+    }
+    __device__ __forceinline__ void store(__nv_bfloat16 *y, const Raw &r) const
+    {
+        *reinterpret_cast<uint2 *>(y + at[0]) = r.v[0];
+        *reinterpret_cast<uint2 *>(y + at[1]) = r.v[1];
     }
 };
+
+// Cosines and sines of a lane's pairs.
+struct Turn {
+    uint64_t c[2], s[2];
+
+    template <bool INTER>
+    __device__ __forceinline__ void load(const HeadParams &p, const Place &pl, int64_t position, int g)
+    {
+        float4 cv = make_float4(1.0f, 1.0f, 1.0f, 1.0f), sv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (pl.turns) {
+            const float *row = p.table + position * p.R + 4 * g;
+            cv = __ldg(reinterpret_cast<const float4 *>(row));
+            sv = __ldg(reinterpret_cast<const float4 *>(row + p.R / 2));
+        }
+        c[0] = INTER ? f2_pack(cv.x, cv.y) : f2_pack(cv.x, cv.z);
+        c[1] = INTER ? f2_pack(cv.z, cv.w) : f2_pack(cv.y, cv.w);
+        s[0] = INTER ? f2_pack(sv.x, sv.y) : f2_pack(sv.x, sv.z);
+        s[1] = INTER ? f2_pack(sv.z, sv.w) : f2_pack(sv.y, sv.w);
+    }
+};
+
+__device__ __forceinline__ uint64_t f2_neg(uint64_t v) { return v ^ 0x8000000080000000ull; }
+
+__device__ __forceinline__ float f2_sum(uint64_t v)
+{
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return lo + hi;
+}
+
+__device__ __forceinline__ Raw ones()
+{
+    return {{make_uint2(0x3F803F80u, 0x3F803F80u), make_uint2(0x3F803F80u, 0x3F803F80u)}};
+}
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
 {
@@ -217,97 +246,164 @@ __device__ __forceinline__ void store_cached(const HeadParams &p, int half, int6
     }
 }
 
-// Vectors per group of lanes: four 16-byte loads in flight per lane.
-constexpr int kVectors = 4;
+// The eight neighbouring elements 8 g .. of a vector whose pieces lie apart: from
+// the lanes that hold them.
+template <int LANES>
+__device__ __forceinline__ void gather(const HeadParams &p, const Place &pl, int lane, float (&e)[8])
+{
+    const int g = lane % LANES, i = 8 * g, second = i >= p.R / 2;
+    const int from = pl.turns ? lane - g + (second ? i - p.R / 2 : i) / 4 : lane;
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float a0 = __shfl_sync(0xffffffffu, e[k], from), b0 = __shfl_sync(0xffffffffu, e[4 + k], from);
+        const float a1 = __shfl_sync(0xffffffffu, e[k], from + 1), b1 = __shfl_sync(0xffffffffu, e[4 + k], from + 1);
+        y[k] = second ? b0 : a0;
+        y[4 + k] = second ? b1 : a1;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = pl.turns ? y[k] : e[k];
+}
 
-template <int LANES, int CACHE>
-__global__ void __launch_bounds__(kThreads) head_kernel(const HeadParams p)
+// Vectors that a group of lanes works on at a time, with as many loads ahead.
+constexpr int kVectors = 2;
+
+// CTAs per SM that the kernels' registers are sized for.
+constexpr int kHeadCtas = 4, kBackCtas = 2;
+
+// Piece of the line of (token, block of heads of a kind) that a warp takes: as
+// many blocks for each, whatever the tokens and heads.
+struct Piece {
+    int64_t begin;
+    int count;
+
+    __device__ __forceinline__ Piece(int64_t items)
+    {
+        const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
+        const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+        begin = w * items / warps;
+        count = static_cast<int>((w + 1) * items / warps - begin);
+    }
+};
+
+template <int LANES, int CACHE, bool INTER>
+__global__ void __launch_bounds__(kThreads, kHeadCtas) head_kernel(const HeadParams p)
 {
     constexpr int GROUPS = 32 / LANES, BLOCK = GROUPS * kVectors;
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, g = lane % LANES, sub = lane / LANES;
     const int per_token = p.blocks[0] + p.blocks[1] + p.blocks[2];
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t t = item / per_token;
-    if (t >= p.T) return;
-    int block = static_cast<int>(item - t * per_token), kind = kQuery;
-    if (block >= p.blocks[0]) {
-        block -= p.blocks[0];
-        kind = kKey;
-        if (block >= p.blocks[1]) {
-            block -= p.blocks[1];
-            kind = kValue;
-        }
-    }
+    const Piece piece(p.T * per_token);
+    if (piece.count == 0) return;
     const bool lane_in = 8 * g < p.D;
-    const __nv_bfloat16 *x = p.x[kind] + t * p.ldx[kind] + 8 * g;
-    const int heads = p.heads[kind];
-    uint4 v[kVectors];      // not through the read-only path: the output may take the input's place
+    int64_t t = piece.begin / per_token;
+    int block = static_cast<int>(piece.begin - t * per_token);
+    int position_next = p.positions ? p.positions[t] : 0;
+    int slot_next = CACHE != kNoCache ? p.c.slots[t] : 0;
+    float gs[2] = {1.0f, 1.0f}, inv_gs[2] = {1.0f, 1.0f};
+    if (CACHE == QFP4_CACHE_NVFP4) {
 #pragma unroll
-    for (int i = 0; i < kVectors; ++i) {
-        const int head = block * BLOCK + i * GROUPS + sub;
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (lane_in && head < heads) v[i] = *reinterpret_cast<const uint4 *>(x + static_cast<int64_t>(head) * p.D);
-    }
-    // tokens without a position are padding: nothing of theirs is written
-    const int64_t position = p.positions ? p.positions[t] : 0;
-    const bool far = p.R > 0 && position >= p.table_rows;
-    int64_t slot = 0;
-    bool bad = far;
-    if (CACHE != kNoCache) {
-        slot = p.c.slots[t];
-        bad |= slot >= p.c.slot_count;
-    }
-    if (bad && lane == 0) atomicOr(&g_status_heads, kStatusBadGroup);
-    if (position < 0 || far) return;
-    if (CACHE != kNoCache && kind != kQuery && (slot < 0 || slot >= p.c.slot_count)) return;
-
-    Turn turn;
-    float a[8], b[8];
-    if (kind != kValue) {
-        turn.load<LANES>(p, position, lane);
-        uint4 w = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);      // ones
-        if (p.w[kind] && lane_in) w = __ldg(reinterpret_cast<const uint4 *>(p.w[kind] + 8 * g));
-        const uint4 wo = turn.others(p, w);
-        unpack8(w, a);
-        unpack8(wo, b);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            a[e] *= turn.c[e];
-            b[e] *= turn.s[e];
+        for (int h = 0; h < 2; ++h) {
+            gs[h] = *p.c.gs[h];
+            inv_gs[h] = __frcp_rn(gs[h]);
         }
     }
-    float gs = 1.0f, inv_gs = 1.0f;
-    if (CACHE == QFP4_CACHE_NVFP4 && kind != kQuery) {
-        gs = *p.c.gs[kind == kValue];
-        inv_gs = __frcp_rn(gs);
-    }
-#pragma unroll
-    for (int i = 0; i < kVectors; ++i) {
-        const int head = block * BLOCK + i * GROUPS + sub;
-        const bool live = lane_in && head < heads;
-        float y[8];
-        unpack8(v[i], y);
-        if (kind != kValue) {
-            float r = 1.0f;
-            if (p.norm) {
-                float ss = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-                r = rsqrtf(group_sum<LANES>(ss) / static_cast<float>(p.D) + p.eps);
+#pragma unroll 1
+    for (int left = piece.count, run = 0; left > 0; left -= run) {
+        int c = block, kind = kQuery;
+        if (c >= p.blocks[0]) {
+            c -= p.blocks[0];
+            kind = kKey;
+            if (c >= p.blocks[1]) {
+                c -= p.blocks[1];
+                kind = kValue;
             }
-            float o[8];
-            unpack8(turn.others(p, v[i]), o);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = fmaf(b[e], o[e], a[e] * y[e]) * r;
         }
-        if (CACHE == kNoCache || kind == kQuery) {
-            if (live)
-                *reinterpret_cast<uint4 *>(p.out[kind] + t * p.ldo[kind] + static_cast<int64_t>(head) * p.D + 8 * g) =
-                    pack8(y);
-        } else {
-            store_cached<CACHE, LANES>(p, kind == kValue, slot, min(head, heads - 1), lane, y, live, gs, inv_gs);
+        run = min(left, p.blocks[kind] - c);        // blocks of this token and kind
+        const int head_end = min(p.heads[kind], (c + run) * BLOCK), head0 = c * BLOCK + sub;
+        const Place pl = Place::of<LANES, INTER>(p, g, kind == kValue);
+        const __nv_bfloat16 *x = p.x[kind] + t * p.ldx[kind] + static_cast<int64_t>(head0) * p.D;
+        Raw next[kVectors] = {};
+#pragma unroll
+        for (int i = 0; i < kVectors; ++i)
+            if (lane_in && head0 + i * GROUPS < head_end) next[i] = pl.load(x + i * GROUPS * p.D);
+        int position = position_next, slot = slot_next;
+        const int64_t tok = t;
+        block += run;
+        if (block == per_token) {
+            block = 0;
+            if (++t < p.T) {
+                position_next = p.positions ? p.positions[t] : 0;
+                slot_next = CACHE != kNoCache ? p.c.slots[t] : 0;
+            }
+        }
+        // tokens without a position are padding: nothing of theirs is written
+        bool bad = p.R > 0 && position >= p.table_rows;
+        if (bad) position = -1;
+        if (CACHE != kNoCache && slot >= p.c.slot_count) {
+            bad = true;
+            slot = -1;
+        }
+        if (bad && lane == 0) atomicOr(&g_status_heads, kStatusBadGroup);
+        if (position < 0 || (CACHE != kNoCache && kind != kQuery && slot < 0)) continue;      // uniform over the warp
+
+        // y = r (a ac + b bs, b bc + a as), the weights in the cosines and sines
+        uint64_t ac[2], as[2], bc[2], bs[2];
+        if (kind != kValue) {
+            Turn turn;
+            turn.load<INTER>(p, pl, position, g);
+            Raw wr = ones();
+            if (p.w[kind] && lane_in) wr = pl.load(p.w[kind]);
+            const Eight w = unpack<INTER>(wr);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                ac[i] = f2_mul(w.a[i], turn.c[i]);
+                as[i] = f2_mul(w.a[i], turn.s[i]);
+                bc[i] = f2_mul(w.b[i], turn.c[i]);
+                bs[i] = f2_neg(f2_mul(w.b[i], turn.s[i]));
+            }
+        }
+#pragma unroll 1
+        for (int head = head0; head - sub < head_end; head += BLOCK) {
+            Raw now[kVectors];
+            x += BLOCK * p.D;
+#pragma unroll
+            for (int i = 0; i < kVectors; ++i) {
+                now[i] = next[i];
+                if (lane_in && head + (kVectors + i) * GROUPS < head_end) next[i] = pl.load(x + i * GROUPS * p.D);
+            }
+#pragma unroll
+            for (int i = 0; i < kVectors; ++i) {
+                const int h = head + i * GROUPS;
+                const bool live = lane_in && h < head_end;
+                Eight v = unpack<INTER>(now[i]);
+                if (kind != kValue) {
+                    float r = 1.0f;
+                    if (p.norm) {
+                        const uint64_t ss = f2_fma(v.b[1], v.b[1], f2_fma(v.b[0], v.b[0], f2_fma(v.a[1], v.a[1], f2_mul(v.a[0], v.a[0]))));
+                        r = rsqrtf(group_sum<LANES>(f2_sum(ss)) * p.inv_D + p.eps);
+                    }
+                    const uint64_t r2 = f2_pack(r, r);
+                    Eight o = v;        // the pairs' other elements
+                    if (p.R < p.D && !pl.turns) o = Eight{{0, 0}, {0, 0}};     // 0 times an infinity would be NaN
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint64_t ya = f2_fma(o.b[k], bs[k], f2_mul(v.a[k], ac[k]));
+                        v.b[k] = f2_mul(f2_fma(o.a[k], as[k], f2_mul(v.b[k], bc[k])), r2);
+                        v.a[k] = f2_mul(ya, r2);
+                    }
+                }
+                if (CACHE == kNoCache || kind == kQuery) {
+                    if (live) pl.store(p.out[kind] + tok * p.ldo[kind] + static_cast<int64_t>(h) * p.D, pack<INTER>(v));
+                } else {
+                    float e[8];
+                    elements<INTER>(v, e);
+                    if (!INTER && kind == kKey) gather<LANES>(p, pl, lane, e);
+                    const int half = kind == kValue;
+                    store_cached<CACHE, LANES>(p, half, slot, min(h, head_end - 1), lane, e, live, gs[half], inv_gs[half]);
+                }
+            }
         }
     }
 }
@@ -323,129 +419,232 @@ struct BackParams {
     float *partial;                     // [gridDim.x][2][D]
 };
 
-// Vectors per group of lanes in the gradient: two loads each.
-constexpr int kBackVectors = 2;
+// The gradient's vectors per group of lanes, and a warp's ring of stages in shared
+// memory, filled by bulk copies: a block of x and one of dy each, 16 bytes per lane,
+// vector and tensor.
+constexpr int kBackVectors = 4, kStages = 3, kHalfStage = 512 * kBackVectors, kStage = 2 * kHalfStage;
+constexpr int kRing = kWarps * kStages * kStage;
 
-template <int LANES>
-__global__ void __launch_bounds__(kThreads) head_backward_kernel(const BackParams q)
+// As head_kernel, but the queries of all tokens come before the keys, so that
+// nearly every warp sums the weights' gradient of one kind; and with the loads
+// through a ring.  What bounds it is the chain of each vector's sums and roots: four
+// vectors at a time with two CTAs per SM take 96 us for 16384 tokens x 40 heads x
+// 128 (5.3 TB/s, 0.78 of the copy bandwidth), two at a time 112, and 143 with
+// three CTAs, whose registers do not suffice; loads into registers instead of the
+// ring 116.
+template <int LANES, bool INTER>
+__global__ void __launch_bounds__(kThreads, kBackCtas) head_backward_kernel(const BackParams q)
 {
     constexpr int GROUPS = 32 / LANES, BLOCK = GROUPS * kBackVectors;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t s_bar[kWarps * kStages];
     __shared__ float s_dw[kWarps][2][LANES * 8];
     const HeadParams &p = q.f;
+    const int lane = threadIdx.x & 31, g = lane % LANES, sub = lane / LANES, warp = threadIdx.x >> 5;
+    const uint32_t bars = smem_u32(s_bar + warp * kStages);
+    uint8_t *ring = smem + warp * kStages * kStage;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, g = lane % LANES, sub = lane / LANES, warp = threadIdx.x >> 5;
-    const int per_token = p.blocks[0] + p.blocks[1];
-    const int64_t items = p.T * per_token;
+    const int64_t items_q = p.T * p.blocks[0];
+    const Piece piece(items_q + p.T * p.blocks[1]);
     const bool lane_in = 8 * g < p.D;
-    float dw[2][8];
+    const Place pl = Place::of<LANES, INTER>(p, g, false);
+    if (p.norm && sub == 0) {       // by the lanes that add the warp's sums later
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[0][e] = dw[1][e] = 0.0f;
-    for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < items;
-         item += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t t = item / per_token;
-        int block = static_cast<int>(item - t * per_token);
-        const int kind = block >= p.blocks[0] ? kKey : kQuery;
-        if (kind == kKey) block -= p.blocks[0];
-        const int heads = p.heads[kind];
-        const __nv_bfloat16 *x = p.x[kind] + t * p.ldx[kind] + 8 * g;
-        const __nv_bfloat16 *dy = q.dy[kind] + t * q.ldy[kind] + 8 * g;
-        __nv_bfloat16 *dx = q.dx[kind] + t * q.lddx[kind] + 8 * g;
-        const int64_t position = p.positions ? p.positions[t] : 0;
-        const bool far = p.R > 0 && position >= p.table_rows;
-        if (far && lane == 0) atomicOr(&g_status_heads, kStatusBadGroup);
-        const bool alive = position >= 0 && !far;
-        uint4 xv[kBackVectors], dv[kBackVectors];
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int i = 0; i < kBackVectors; ++i) {
-            const int64_t head = block * BLOCK + i * GROUPS + sub;
-            xv[i] = dv[i] = make_uint4(0, 0, 0, 0);
-            if (alive && lane_in && head < heads) {
-                // not through the read-only path: dx may take the place of either
-                dv[i] = *reinterpret_cast<const uint4 *>(dy + head * p.D);
-                if (p.norm) xv[i] = *reinterpret_cast<const uint4 *>(x + head * p.D);
+            for (int e = 0; e < 8; ++e) s_dw[warp][k][8 * g + e] = 0.0f;
+    }
+    int kind = piece.begin >= items_q ? kKey : kQuery;
+    const int64_t in_kind = kind == kKey ? piece.begin - items_q : piece.begin;
+    int64_t t = in_kind / p.blocks[kind];
+    int block = static_cast<int>(in_kind - t * p.blocks[kind]);
+
+    // ---- the ring's producer: the same walk, ahead
+    int64_t ahead_t = t;
+    int ahead_block = block, ahead_kind = kind, to_issue = piece.count;
+    auto issue = [&](int stage) {
+        if (lane == 0) {
+            const int k = ahead_kind, head = ahead_block * BLOCK;
+            const uint32_t bytes = static_cast<uint32_t>(min(BLOCK, p.heads[k] - head) * p.D) * 2u;
+            const uint32_t bar = bars + 8 * stage, dst = smem_u32(ring) + stage * kStage;
+            const int64_t from = static_cast<int64_t>(head) * p.D;
+            mbar_arrive_expect_tx(bar, p.norm ? 2 * bytes : bytes);
+            bulk_load(dst, q.dy[k] + ahead_t * q.ldy[k] + from, bytes, bar);
+            if (p.norm) bulk_load(dst + kHalfStage, p.x[k] + ahead_t * p.ldx[k] + from, bytes, bar);
+        }
+        --to_issue;
+        if (++ahead_block == p.blocks[ahead_kind]) {
+            ahead_block = 0;
+            if (++ahead_t == p.T && ahead_kind == kQuery) {
+                ahead_t = 0;
+                ahead_kind = kKey;
             }
         }
-        Turn turn;
-        if (alive) turn.load<LANES>(p, position, lane);
-        float w[8];
-        uint4 wv = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-        if (p.w[kind] && lane_in) wv = __ldg(reinterpret_cast<const uint4 *>(p.w[kind] + 8 * g));
-        unpack8(wv, w);
+    };
+    int position_next = piece.count > 0 && p.positions ? p.positions[t] : 0;
 #pragma unroll
-        for (int i = 0; i < kBackVectors; ++i) {
-            const int64_t head = block * BLOCK + i * GROUPS + sub;
-            float dz[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (alive) {        // uniform over the warp
-                float o[8];
-                unpack8(dv[i], dz);
-                unpack8(turn.others(p, dv[i]), o);
+    for (int i = 0; i < kStages; ++i)
+        if (to_issue > 0) issue(i);
+
+    Eight w, dw = {{0, 0}, {0, 0}};
+    // the groups of a warp hold the same elements: added up in a fixed order
+    auto flush = [&](int k) {
+        float e[8];
+        elements<INTER>(dw, e);
+        dw = Eight{{0, 0}, {0, 0}};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dz[e] = fmaf(-turn.s[e], o[e], turn.c[e] * dz[e]);
-                if (p.norm) {
-                    float h[8], ss = 0.0f, dot = 0.0f;
-                    unpack8(xv[i], h);
+        for (int i = 0; i < 8; ++i) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        ss = fmaf(h[e], h[e], ss);
-                        dot = fmaf(dz[e] * w[e], h[e], dot);
+            for (int o = 16; o >= LANES; o >>= 1) e[i] += __shfl_xor_sync(0xffffffffu, e[i], o);
+            if (sub == 0) s_dw[warp][k][8 * g + i] += e[i];
+        }
+    };
+    int stage = 0;
+    uint32_t phase = 0;
+    bool new_kind = true, dead = false;
+#pragma unroll 1
+    for (int left = piece.count, run = 0; left > 0; left -= run) {
+        run = min(left, p.blocks[kind] - block);        // blocks of this token and kind
+        const int heads = p.heads[kind], head0 = block * BLOCK + sub;
+        __nv_bfloat16 *dx = q.dx[kind] + t * q.lddx[kind] + static_cast<int64_t>(head0) * p.D;
+        int position = position_next;
+        const int was = kind;
+        block += run;
+        if (block == p.blocks[kind]) {
+            block = 0;
+            if (++t == p.T && kind == kQuery) {
+                t = 0;
+                kind = kKey;
+            }
+        }
+        if (left > run && p.positions) position_next = p.positions[t];
+        if (new_kind) {
+            Raw wr = ones();
+            if (p.w[was] && lane_in) wr = pl.load(p.w[was]);
+            w = unpack<INTER>(wr);
+        }
+        if (p.R > 0 && position >= p.table_rows) {
+            position = -1;
+            if (lane == 0) atomicOr(&g_status_heads, kStatusBadGroup);
+        }
+        const bool alive = position >= 0;       // uniform over the warp
+        Turn turn = {};
+        if (alive) turn.load<INTER>(p, pl, position, g);
+        const uint64_t back[2] = {f2_neg(turn.s[0]), f2_neg(turn.s[1])};
+#pragma unroll 1
+        for (int n = 0; n < run; ++n) {
+            if (!mbar_wait(bars + 8 * stage, phase)) {
+                if (lane == 0) atomicOr(&g_status_heads, kStatusTimeout);
+                dead = true;
+            }
+            const uint8_t *buf = ring + stage * kStage + sub * p.D * 2;
+            Raw xv[kBackVectors], dv[kBackVectors];
+#pragma unroll
+            for (int i = 0; i < kBackVectors; ++i) {
+                const __nv_bfloat16 *src = reinterpret_cast<const __nv_bfloat16 *>(buf + i * GROUPS * p.D * 2);
+                dv[i] = pl.load(src);
+                if (p.norm) xv[i] = pl.load(src + kHalfStage / 2);
+            }
+            __syncwarp();
+            if (to_issue > 0) issue(stage);
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+#pragma unroll
+            for (int i = 0; i < kBackVectors; ++i) {
+                const bool live = lane_in && head0 + n * BLOCK + i * GROUPS < heads;
+                if (!live) xv[i] = dv[i] = Raw{};       // other vectors' elements, or none
+                Eight d = {{0, 0}, {0, 0}};
+                if (alive) {
+                    const Eight v = unpack<INTER>(dv[i]);
+                    Eight o = v;
+                    if (p.R < p.D && !pl.turns) o = Eight{{0, 0}, {0, 0}};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        d.a[k] = f2_fma(o.b[k], turn.s[k], f2_mul(v.a[k], turn.c[k]));
+                        d.b[k] = f2_fma(o.a[k], back[k], f2_mul(v.b[k], turn.c[k]));
                     }
-                    const float n = static_cast<float>(p.D);
-                    const float r = rsqrtf(group_sum<LANES>(ss) / n + p.eps);
-                    const float mean = group_sum<LANES>(dot) * r / n;
+                    if (p.norm) {
+                        Eight h = unpack<INTER>(xv[i]), gw;
+                        uint64_t ss = 0, dot = 0;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        h[e] *= r;
-                        const float d = dz[e] * h[e];
-                        dw[0][e] += kind == kQuery ? d : 0.0f;
-                        dw[1][e] += kind == kKey ? d : 0.0f;
-                        dz[e] = r * fmaf(-h[e], mean, dz[e] * w[e]);
+                        for (int k = 0; k < 2; ++k) {
+                            gw.a[k] = f2_mul(d.a[k], w.a[k]);
+                            gw.b[k] = f2_mul(d.b[k], w.b[k]);
+                            ss = f2_fma(h.b[k], h.b[k], f2_fma(h.a[k], h.a[k], ss));
+                            dot = f2_fma(gw.b[k], h.b[k], f2_fma(gw.a[k], h.a[k], dot));
+                        }
+                        const float r = rsqrtf(group_sum<LANES>(f2_sum(ss)) * p.inv_D + p.eps);
+                        const float mean = group_sum<LANES>(f2_sum(dot)) * r * p.inv_D;
+                        const uint64_t r2 = f2_pack(r, r), m2 = f2_pack(-mean * r, -mean * r);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            h.a[k] = f2_mul(h.a[k], r2);
+                            h.b[k] = f2_mul(h.b[k], r2);
+                            dw.a[k] = f2_fma(d.a[k], h.a[k], dw.a[k]);
+                            dw.b[k] = f2_fma(d.b[k], h.b[k], dw.b[k]);
+                            d.a[k] = f2_fma(h.a[k], m2, f2_mul(gw.a[k], r2));
+                            d.b[k] = f2_fma(h.b[k], m2, f2_mul(gw.b[k], r2));
+                        }
                     }
                 }
+                if (live) pl.store(dx + i * GROUPS * p.D, pack<INTER>(d));
             }
-            if (lane_in && head < heads) *reinterpret_cast<uint4 *>(dx + head * p.D) = pack8(dz);
+            dx += BLOCK * p.D;
+        }
+        new_kind = kind != was;
+        if (p.norm && (new_kind || left == run)) flush(was);
+    }
+    if (dead) {     // copies in flight have time to land before the shared memory goes to another CTA
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 1000000ull) {
         }
     }
     if (!p.norm) return;
-    // the groups of a warp hold the same elements: added up in a fixed order
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            float v = dw[k][e];
-#pragma unroll
-            for (int o = 16; o >= LANES; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-            if (sub == 0) s_dw[warp][k][8 * g + e] = v;
-        }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * p.D; i += kThreads) {
-        const int k = i >= p.D, d = i - k * p.D;
+    // place i of a lane's eight back to the element that it holds
+    for (int i = threadIdx.x; i < 2 * LANES * 8; i += kThreads) {
+        const int k = i >= LANES * 8, in = i - k * LANES * 8, gi = in / 8, e = in % 8;
+        if (8 * gi >= p.D) continue;
+        const Place at = Place::of<LANES, INTER>(p, gi, false);
         float v = 0.0f;
 #pragma unroll
-        for (int wi = 0; wi < kWarps; ++wi) v += s_dw[wi][k][d];
-        q.partial[static_cast<int64_t>(blockIdx.x) * 2 * p.D + i] = v;
+        for (int j = 0; j < kWarps; ++j) v += s_dw[j][k][in];
+        q.partial[static_cast<int64_t>(blockIdx.x) * 2 * p.D + k * p.D + (e < 4 ? at.at[0] + e : at.at[1] + e - 4)] = v;
     }
 }
 
-// Weight gradients from the CTAs' partial sums, in 64 bits: 32 columns per CTA.
+// Weight gradients from the CTAs' partial sums: 32 columns per CTA, each added up
+// by 32 threads side by side and then by a tree (sums of 64 bits take 14 us here).
 __global__ void __launch_bounds__(1024) head_weight_kernel(const float *partial, int rows, int D, float *dq, float *dk)
 {
-    __shared__ double s_sum[32][33];
+    __shared__ float s_sum[32][33];
     pdl_wait();
     pdl_launch_dependents();
     const int c = threadIdx.x & 31, r = threadIdx.x >> 5;
     const int i = blockIdx.x * 32 + c;
-    double v = 0.0;
-    if (i < 2 * D)
-        for (int k = r; k < rows; k += 32) v += static_cast<double>(partial[static_cast<int64_t>(k) * 2 * D + i]);
+    float v = 0.0f;
+    if (i < 2 * D) {
+#pragma unroll 8
+        for (int k = r; k < rows; k += 32) v += partial[static_cast<int64_t>(k) * 2 * D + i];
+    }
     s_sum[r][c] = v;
     __syncthreads();
-    if (r != 0 || i >= 2 * D) return;
-    v = 0.0;
+    v = s_sum[c][r];        // lane c of warp r: part c of column r
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v += s_sum[k][c];
-    float *out = i < D ? dq : dk;
-    if (out) out[i < D ? i : i - D] = static_cast<float>(v);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int column = blockIdx.x * 32 + r;
+    if (c != 0 || column >= 2 * D) return;
+    float *out = column < D ? dq : dk;
+    if (out) out[column < D ? column : column - D] = v;
 }
 
 // ------------------------------------------------------------- cache's read
@@ -551,38 +750,34 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p
 
 int lanes_of(int64_t D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
-template <int LANES>
+// Cuts the tokens' heads into blocks; CTAs of the grid: one wave at most.
+int64_t plan_blocks(HeadParams &p, int lanes, int vectors, int per_sm)
+{
+    const int block = 32 / lanes * vectors;
+    int64_t per_token = 0;
+    for (int k = 0; k < 3; ++k) per_token += p.blocks[k] = (p.heads[k] + block - 1) / block;
+    const int64_t want = (p.T * per_token + kWarps - 1) / kWarps;
+    return want < per_sm * 152 ? want : per_sm * 152;
+}
+
+template <int LANES, bool INTER>
 int launch_heads(HeadParams &p, int cache, cudaStream_t s)
 {
-    constexpr int BLOCK = 32 / LANES * kVectors;
-    int64_t per_token = 0;
-    for (int k = 0; k < 3; ++k) per_token += p.blocks[k] = (p.heads[k] + BLOCK - 1) / BLOCK;
-    const int64_t grid = (p.T * per_token + kWarps - 1) / kWarps;
-    if (grid > INT32_MAX) return QFP4_ERR_UNSUPPORTED;
-    auto kernel = cache == kNoCache ? head_kernel<LANES, kNoCache>
-                : cache == QFP4_CACHE_BF16 ? head_kernel<LANES, QFP4_CACHE_BF16>
-                : cache == QFP4_CACHE_E4M3 ? head_kernel<LANES, QFP4_CACHE_E4M3>
-                                           : head_kernel<LANES, QFP4_CACHE_NVFP4>;
+    const int64_t grid = plan_blocks(p, LANES, kVectors, kHeadCtas);
+    auto kernel = cache == kNoCache ? head_kernel<LANES, kNoCache, INTER>
+                : cache == QFP4_CACHE_BF16 ? head_kernel<LANES, QFP4_CACHE_BF16, INTER>
+                : cache == QFP4_CACHE_E4M3 ? head_kernel<LANES, QFP4_CACHE_E4M3, INTER>
+                                           : head_kernel<LANES, QFP4_CACHE_NVFP4, INTER>;
     return launch_status(launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, p));
 }
 
 int launch_heads_any(HeadParams &p, int cache, cudaStream_t s)
 {
     switch (lanes_of(p.D)) {
-    case 8: return launch_heads<8>(p, cache, s);
-    case 16: return launch_heads<16>(p, cache, s);
-    default: return launch_heads<32>(p, cache, s);
+    case 8: return p.interleaved ? launch_heads<8, true>(p, cache, s) : launch_heads<8, false>(p, cache, s);
+    case 16: return p.interleaved ? launch_heads<16, true>(p, cache, s) : launch_heads<16, false>(p, cache, s);
+    default: return p.interleaved ? launch_heads<32, true>(p, cache, s) : launch_heads<32, false>(p, cache, s);
     }
-}
-
-// CTAs of the gradient's grid, whose partial sums of the weights' gradients
-// the workspace holds: four per SM, no more than there is work for.
-int64_t back_grid(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D)
-{
-    const int block = 32 / lanes_of(D) * kBackVectors;
-    const int64_t items = T * ((q_heads + block - 1) / block + (kv_heads + block - 1) / block);
-    const int64_t want = (items + kWarps - 1) / kWarps, most = 4 * 152;
-    return want < most ? want : most;
 }
 
 constexpr int64_t kMaxTokens = int64_t{1} << 30, kMaxHeads = 4096;
@@ -635,6 +830,7 @@ int fill_common(HeadParams &p, const void *QKV, int64_t ld, int64_t T, int64_t q
     p.interleaved = interleaved;
     p.norm = q_weight != nullptr;
     p.eps = eps;
+    p.inv_D = 1.0f / static_cast<float>(D);
     return QFP4_OK;
 }
 
@@ -785,7 +981,12 @@ extern "C" size_t qfp4_qk_norm_rope_backward_workspace_bytes(int64_t T, int64_t 
                                                              int64_t head_dim)
 {
     if (T < 0 || q_heads < 1 || kv_heads < 1 || !head_sizes_ok(T, q_heads, kv_heads, head_dim, 0)) return 0;
-    return static_cast<size_t>(back_grid(T, q_heads, kv_heads, head_dim)) * 2 * head_dim * sizeof(float);
+    HeadParams p = {};
+    p.T = T;
+    p.heads[0] = static_cast<int32_t>(q_heads);
+    p.heads[1] = static_cast<int32_t>(kv_heads);
+    // partial sums of the weights' gradients, a pair of vectors per CTA
+    return static_cast<size_t>(plan_blocks(p, lanes_of(head_dim), kBackVectors, kBackCtas)) * 2 * head_dim * sizeof(float);
 }
 
 extern "C" int qfp4_qk_norm_rope_backward(const void *QKV_bf16, int64_t ld, int64_t T, int64_t q_heads,
@@ -823,12 +1024,13 @@ extern "C" int qfp4_qk_norm_rope_backward(const void *QKV_bf16, int64_t ld, int6
         b.dx[1] = b.dx[0] + q_heads * head_dim;
         b.lddx[0] = b.lddx[1] = lddqkv;
         b.partial = static_cast<float *>(workspace);
-        const int lanes = lanes_of(head_dim), block = 32 / lanes * kBackVectors;
-        for (int k = 0; k < 2; ++k) b.f.blocks[k] = (b.f.heads[k] + block - 1) / block;
-        const dim3 grid(static_cast<unsigned>(back_grid(T, q_heads, kv_heads, head_dim)));
-        auto kernel = lanes == 8 ? head_backward_kernel<8>
-                    : lanes == 16 ? head_backward_kernel<16> : head_backward_kernel<32>;
-        const int st = launch_status(launch_pdl(kernel, grid, dim3(kThreads), 0, s, b));
+        const int lanes = lanes_of(head_dim);
+        const dim3 grid(static_cast<unsigned>(plan_blocks(b.f, lanes, kBackVectors, kBackCtas)));
+        auto kernel = lanes == 8 ? (interleaved ? head_backward_kernel<8, true> : head_backward_kernel<8, false>)
+                    : lanes == 16 ? (interleaved ? head_backward_kernel<16, true> : head_backward_kernel<16, false>)
+                                  : (interleaved ? head_backward_kernel<32, true> : head_backward_kernel<32, false>);
+        int st = ensure_smem_attr(reinterpret_cast<const void *>(kernel), kRing);
+        if (st == QFP4_OK) st = launch_status(launch_pdl(kernel, grid, dim3(kThreads), kRing, s, b));
         if (st != QFP4_OK || !norm) return st;
         return launch_status(launch_pdl(head_weight_kernel, dim3(columns), dim3(1024), 0, s, b.partial,
                                         static_cast<int>(grid.x), D, dq_weight, dk_weight));

@@ -548,14 +548,16 @@ def moe_route_backward(logits, ids, counts, n_valid, dgates, dloss, dlogits, val
           _at(dloss, _F32, 1), _at(dlogits, logits.dtype, T * E), _stream(stream))
 
 
-def _rows(t, width, rows, dtype=torch.bfloat16):
-    """(address, elements from row to row) of `rows` rows of `width` elements
+def _rows(t, width, rows):
+    """(address, elements from row to row) of `rows` BF16 rows of `width` elements
     that lie together: a contiguous matrix, or some columns of one (the heads of
-    one kind in a projection's output)."""
+    one kind in a projection's output).  The usual path asks each question once."""
     if t is None:
         return 0, width
-    if t.dtype is not dtype or not t.is_cuda:
-        raise ValueError(f"qfp4: expected {dtype} on the GPU, got {t.dtype} on {t.device}")
+    if t.dtype is _BF16 and t.is_cuda and t.numel() == rows * width and t.is_contiguous():
+        return t.data_ptr(), width
+    if t.dtype is not _BF16 or not t.is_cuda:
+        raise ValueError(f"qfp4: expected {_BF16} on the GPU, got {t.dtype} on {t.device}")
     shape, stride = t.shape, t.stride()
     if len(shape) == 3:
         if shape[2] != 1 and stride[2] != 1 or shape[1] != 1 and stride[1] != shape[2]:
@@ -638,15 +640,16 @@ def kv_cache_page_bytes(type: int, kv_heads: int, head_dim: int, page_size: int)
     return int(load().qfp4_kv_cache_page_bytes(type, kv_heads, head_dim, page_size))
 
 
-_CACHE_TOKEN_BITS = {CACHE_BF16: lambda D: 32 * D, CACHE_E4M3: lambda D: 16 * D + 64, CACHE_NVFP4: lambda D: 9 * D}
+_CACHE_TOKEN = {CACHE_BF16: (32, 0), CACHE_E4M3: (16, 64), CACHE_NVFP4: (9, 0)}     # bits per element and more
 
 
 def _cache(type, cache, kv_heads, D, page_size):
     """(address, pages) of a cache whose pages have that layout's size."""
-    token = _CACHE_TOKEN_BITS[type](D) // 8 if type in _CACHE_TOKEN_BITS else 1
-    pages, page = cache.shape[0], token * kv_heads * page_size
-    if type in _CACHE_TOKEN_BITS and cache.numel() != pages * page:
-        raise ValueError(f"qfp4: a page of this cache has {page} bytes, got {tuple(cache.shape)}")
+    pages, token = cache.shape[0], _CACHE_TOKEN.get(type)
+    if token is not None:
+        page = (token[0] * D + token[1]) // 8 * kv_heads * page_size
+        if cache.numel() != pages * page:
+            raise ValueError(f"qfp4: a page of this cache has {page} bytes, got {tuple(cache.shape)}")
     return _at(cache, _U8), pages
 
 
