@@ -2,21 +2,24 @@
 //   D[m,n] = gs_w * sum_k x[m,k] * w[n,k],  w = E2M1(W) * SF,
 // the weights packed and their scales in the MMA layout as qfp4_gemm_nt's B.
 //
-// Bound by the weights' bytes.  A CTA takes 128 rows of W (one tile of the
-// scales' layout), each of its eight warps 16 of them as the rows of a tensor
-// core product (m16n8k16) whose columns are the rows of x.  The codes become
-// FP16 exactly; NVFP4's scales join them there (a product of E2M1 and UE4M3 has
-// at most 6 significant bits), MXFP4's powers of two multiply the fp32 sums of a
-// block, so that their whole range counts.  x becomes FP16 in shared memory,
-// each row of a slice of K multiplied by the power of two that takes its largest
-// element there to [2^8, 2^9): an element loses bits only 2^22 below that,
-// 2^-34 of the largest at most.
+// Bound by the weights' bytes.  A warp takes 16 rows of W as the rows of tensor
+// core products (m16n8k16) whose columns are the rows of x.  The codes become FP16
+// exactly; NVFP4's scales join them there (a product of E2M1 and UE4M3 has at most
+// 6 significant bits), MXFP4's powers of two multiply the fp32 sums of a block, so
+// that their whole range counts.  x becomes FP16 in shared memory, each row of a
+// slice of K multiplied by the power of two that takes its largest element there to
+// [2^8, 2^9): an element loses bits only 2^22 below that, 2^-34 of the largest at
+// most.
 //
-// A warp brings its own rows and scales with 16-byte asynchronous copies into a
-// ring of stages of its own, 128 elements of K per stage, and waits for no other
-// warp but where a slice of x ends.  ldmatrix gives a lane eight neighbouring
-// codes of a block.  K is split over the CTAs of a cluster, whose sums are added
-// through distributed shared memory in a fixed order: results repeat bit for bit.
+// One CTA of 16 warps per SM, and one wave of them: the groups of 16 rows are dealt
+// out over the clusters, K over the CTAs of a cluster, so that a CTA converts its
+// part of x once and its warps stream their rows without a pause: each brings its own
+// rows and scales with 16-byte asynchronous copies into a ring of stages, 256 elements
+// of K per stage, across the groups' borders.  ldmatrix gives a lane eight
+// neighbouring codes of a block.  The cluster's sums are added through distributed
+// shared memory in a fixed order: results repeat bit for bit.
+#include <algorithm>
+#include <atomic>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -24,6 +27,7 @@
 
 #include "qfp4_attention.cuh"
 #include "qfp4_common.cuh"
+#include "qfp4_fp4_codes.cuh"
 #include "sm103_ptx.cuh"
 
 namespace qfp4 {
@@ -32,11 +36,11 @@ namespace {
 
 using namespace attn;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kRows = 128;              // rows of W per CTA
-constexpr int kStep = 128;              // elements of K per stage
-constexpr int kStages = 8;
-constexpr int kSlice = 1024;            // elements of K of x in shared memory at once
+constexpr int kStep = 128;              // elements of K that the scales' layout and K go by
+constexpr int kUnit = 256, kUnitSteps = 2;              // elements of K of a stage
+constexpr int kSlice = 512, kSliceUnits = 2;            // of x with a scale of their own
+constexpr int kRowSlices = 64;          // slices of rows of x in shared memory at once
+constexpr int kGroups = 32;             // groups of 16 rows whose sums are
 constexpr int kMaxRowsX = 16, kMaxSplits = 8;
 
 struct GemvParams {
@@ -50,16 +54,20 @@ struct GemvParams {
     int32_t M, N, K;
 };
 
+// NT: blocks of eight rows of x
 template <int FMT, int NT>
 struct GemvCfg {
-    static constexpr int SF = FMT == QFP4_NVFP4 ? 128 : 64;         // scale bytes of a warp's stage
-    static constexpr int STAGE = 16 * kStep / 2 + SF;
+    static constexpr int COLS4 = FMT == QFP4_NVFP4 ? 2 : 1;         // tiles of four scale columns per step
+    static constexpr int ROWS = 16 * kUnit / 2, STAGE = ROWS + kUnitSteps * COLS4 * 64;
+    // 24 warps of 80 registers are no faster than 16 (1 x 28672 x 8192: 32 us, 29)
+    static constexpr int WARPS = 16, THREADS = 32 * WARPS, STAGES = 3;
     static constexpr int PITCH = (kSlice + 32) * 2;                 // bytes of a row of x: two rows fall on different halves of the banks
-    static constexpr int RING = kWarps * kStages * STAGE;
-    static constexpr int X = 8 * NT * PITCH;
-    static constexpr int OUT = 8 * NT * (kRows + 4) * 4;            // the CTA's sums, over the ring
-    static constexpr int SMEM = RING + X + 8 * NT * 4;
-    static_assert(OUT <= RING, "the sums take the ring's place");
+    static constexpr int RING = WARPS * STAGES * STAGE;
+    static constexpr int X = kRowSlices * PITCH, BACK = (kRowSlices + 8 * NT) * 4;
+    static constexpr int SUMS = 8 * NT * 16;                        // of a group: [row of x][row of W]
+    static constexpr int OUT = kGroups * SUMS * 4;
+    static constexpr int SMEM = RING + X + BACK + OUT;
+    static_assert(SMEM <= 227 * 1024, "one CTA per SM");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
@@ -96,215 +104,362 @@ __device__ __forceinline__ float ue8m0(uint32_t c)
     return __uint_as_float(c == 255u ? 0x7FFFFFFFu : c == 0u ? 0x00400000u : c << 23);
 }
 
+__device__ __forceinline__ void mma_f16_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Whether a byte of w is 0 or 255.
+__device__ __forceinline__ bool has_end_byte(uint32_t w)
+{
+    return (((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w) & 0x80808080u) & 0x80808080u;
+}
+
 template <int FMT, int NT>
-__global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvParams p, const int splits)
+__global__ void __launch_bounds__(GemvCfg<FMT, NT>::THREADS, 1) gemv_kernel(const GemvParams p, const int splits)
 {
     using C = GemvCfg<FMT, NT>;
+    constexpr int STAGES = C::STAGES, COLS4 = C::COLS4, SUMS = C::SUMS, WARPS = C::WARPS, THREADS = C::THREADS;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    const int rank = blockIdx.x % splits, tile = blockIdx.x / splits;
-    const int row0 = tile * kRows;
-    const int steps_all = p.K / kStep;
-    const int step0 = static_cast<int>(static_cast<int64_t>(rank) * steps_all / splits);
-    const int steps = static_cast<int>(static_cast<int64_t>(rank + 1) * steps_all / splits) - step0;
-    const uint32_t ring = smem_u32(smem) + warp * kStages * C::STAGE;
+    const int rank = blockIdx.x % splits, cluster = blockIdx.x / splits, clusters = gridDim.x / splits;
+    // this CTA's part of K, in units
+    const int steps_all = p.K / kStep, units_all = (steps_all + 1) / 2;
+    const int unit0 = static_cast<int>(static_cast<int64_t>(rank) * units_all / splits);
+    const int units = static_cast<int>(static_cast<int64_t>(rank + 1) * units_all / splits) - unit0;
     uint8_t *xs = smem + C::RING;
-    float *s_back = reinterpret_cast<float *>(smem + C::RING + C::X);
+    float *s_back = reinterpret_cast<float *>(xs + C::X);           // [slice][row of x]
+    float *s_out = reinterpret_cast<float *>(xs + C::X + C::BACK);  // [group][row of x][row of W]
 
-    // A warp's row lr is row 4 warp + lr % 4 + 32 (lr / 4) of the tile: its scales
-    // then lie together, 64 bytes per tile of four columns.  Lane copies rows
-    // lane / 4 and 8 more, chunk lane % 4 of each; chunk c of row r goes to place
-    // c ^ (r / 2 % 4), so that the eight rows of an ldmatrix fall on all banks.
-    const uint8_t *src[2];
-    uint32_t dst[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int lr = 8 * h + g;
-        const int row = min(row0 + 4 * warp + (lr & 3) + 32 * (lr >> 2), p.N - 1);
-        src[h] = p.w + (static_cast<int64_t>(row) * p.K + static_cast<int64_t>(step0) * kStep) / 2 + 16 * t;
-        dst[h] = ring + lr * 64 + ((t ^ (lr >> 1 & 3)) << 4);
-    }
-    constexpr int COLS4 = FMT == QFP4_NVFP4 ? 2 : 1;        // tiles of four scale columns per step
-    const uint8_t *sf = p.sf + (static_cast<int64_t>(tile) * steps_all + step0) * (512 * COLS4) + 64 * warp + (lane >> 2) * 512 + (lane & 3) * 16;
-    const bool sf_lane = lane < 4 * COLS4;
-    const uint32_t sf_dst = ring + 1024 + lane * 16;
-    auto issue = [&](int step, int stage) {
-        if (step < steps) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) cp_async16(dst[h] + stage * C::STAGE, src[h] + step * (kStep / 2));
-            if (sf_lane) cp_async16(sf_dst + stage * C::STAGE, sf + static_cast<int64_t>(step) * (512 * COLS4));
+    // The cluster's groups of 16 rows.  Group q is part q % 8 of the scales' tile
+    // q / 8, its row lr row 4 (q % 8) + lr % 4 + 32 (lr / 4) there: its scales then
+    // lie together, 64 bytes per tile of four columns.
+    const int all = (p.N + 127) / 128 * 8;
+    const int q0 = static_cast<int>(static_cast<int64_t>(cluster) * all / clusters);
+    const int q1 = static_cast<int>(static_cast<int64_t>(cluster + 1) * all / clusters);
+
+    // a pass over K: what of x lies in shared memory at once
+    const int most = kRowSlices / p.M * kSliceUnits;
+    auto pass_units = [&](int u0) { return min(most, units - u0); };
+
+    // ---- the ring's producer.  Lane copies chunk lane % 8 of rows lane / 8 + 4 j;
+    // chunk c of row r goes to place c ^ r % 8, so that the eight rows of an ldmatrix
+    // fall on all banks.
+    const int64_t row_bytes = p.K / 2;
+    // It stands at a unit of group in_q, in the pass over K from
+    // in_u0 and over kGroups groups from in_base; in_left units of the group are left.
+    int in_base = q0, in_u0 = 0, in_q = q0 + warp, in_left = 0, in_last = 0, stage_in = 0;
+    const uint8_t *src[4] = {}, *sf = nullptr;
+    auto open = [&] {       // the group in_q, or the next that there is for this warp
+        while (in_q >= min(q1, in_base + kGroups)) {
+            if ((in_u0 += most) >= units) {
+                in_u0 = 0;
+                if ((in_base += kGroups) >= q1) return;
+            }
+            in_q = in_base + warp;
         }
+        const int tile = in_q >> 3, part = in_q & 7, unit = unit0 + in_u0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int row = min(tile * 128 + 4 * part + (lane >> 3) + 32 * j, p.N - 1);
+            src[j] = p.w + row * row_bytes + static_cast<int64_t>(unit) * (kUnit / 2) + 16 * (lane & 7);
+        }
+        sf = p.sf + (static_cast<int64_t>(tile) * steps_all + 2 * unit) * (512 * COLS4) + 64 * part + (lane >> 2) * 512 + (lane & 3) * 16;
+        in_left = pass_units(in_u0);
+        // steps of the group's last unit: one where K ends in the middle of it
+        in_last = min(2, steps_all - 2 * (unit + in_left - 1));
+    };
+    const uint32_t ring = smem_u32(smem) + warp * STAGES * C::STAGE;
+    const uint32_t dst = ring + (lane >> 3) * 128;
+    const uint32_t place0 = ((lane & 7) ^ (lane >> 3)) << 4, place1 = ((lane & 7) ^ ((lane >> 3) + 4)) << 4;
+    auto issue = [&] {
+        if (in_left > 0) {
+            const uint32_t off = stage_in * C::STAGE;
+            const bool both = in_left > 1 || in_last > 1;
+            if (both || (lane & 7) < 4) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) cp_async16(dst + off + j * 512 + (j & 1 ? place1 : place0), src[j]);
+            }
+            if (lane < (both ? 8 : 4) * COLS4) cp_async16(ring + off + C::ROWS + lane * 16, sf);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) src[j] += kUnit / 2;
+            sf += 2 * 512 * COLS4;
+            if (--in_left == 0) {
+                in_q += WARPS;
+                open();
+            }
+        }
+        if (++stage_in == STAGES) stage_in = 0;
         cp_async_commit();
     };
     pdl_wait();
     pdl_launch_dependents();
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) issue(i, i);
+    if (units > 0) open();
+#pragma unroll 1
+    for (int i = 0; i < STAGES - 1; ++i) issue();
 
-    float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[n][k] = 0.0f;
-
-    int stage = 0;
-    for (int s0 = 0; s0 < steps; s0 += kSlice / kStep) {
-        const int n_steps = min(kSlice / kStep, steps - s0), width = n_steps * kStep;
-        // ---- this slice of x: a warp converts rows warp and warp + 8
-        if (s0 > 0) __syncthreads();
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int m = 8 * n + warp;
+    // ---- x, [slice][row]: a warp converts a slice of a row at a time
+    auto convert = [&](int u0, int n) {
+#pragma unroll 1
+        for (int i = warp; i < p.M * n; i += WARPS) {
+            const int m = i % p.M, sl = i / p.M;
+            const int64_t k0 = static_cast<int64_t>(unit0 + u0) * kUnit + sl * kSlice;
+            const int64_t end = min(static_cast<int64_t>(p.K), static_cast<int64_t>(unit0 + units) * kUnit);
             uint4 v[kSlice / 256];
             float amax = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kSlice / 256; ++i) {
-                const int k = 256 * i + 8 * lane;
-                v[i] = make_uint4(0, 0, 0, 0);
-                if (m < p.M && k < width)
-                    v[i] = __ldg(reinterpret_cast<const uint4 *>(p.x + m * p.ldx + static_cast<int64_t>(step0 + s0) * kStep + k));
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            for (int j = 0; j < kSlice / 256; ++j) {
+                const int64_t k = k0 + 256 * j + 8 * lane;
+                v[j] = make_uint4(0, 0, 0, 0);
+                if (k < end) v[j] = __ldg(reinterpret_cast<const uint4 *>(p.x + m * p.ldx + k));
+            }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+            for (int j = 0; j < kSlice / 256; ++j) {
+                const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[u] << 16)), fabsf(__uint_as_float(w[u] & 0xFFFF0000u))));
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             int e = 8 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127);
             e = amax == 0.0f || !(amax < 3.4e38f) ? 0 : max(-126, min(126, e));
             const float up = pow2(e);
-            if (lane == 0) s_back[m] = pow2(-e);
+            if (lane == 0) s_back[sl * p.M + m] = pow2(-e);
 #pragma unroll
-            for (int i = 0; i < kSlice / 256; ++i) {
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            for (int j = 0; j < kSlice / 256; ++j) {
+                const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
                 uint32_t h[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h[j] = pack_f16(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xFFFF0000u) * up);
-                *reinterpret_cast<uint4 *>(xs + m * C::PITCH + (256 * i + 8 * lane) * 2) = make_uint4(h[0], h[1], h[2], h[3]);
+                for (int u = 0; u < 4; ++u) h[u] = pack_f16(__uint_as_float(w[u] << 16) * up, __uint_as_float(w[u] & 0xFFFF0000u) * up);
+                *reinterpret_cast<uint4 *>(xs + (sl * p.M + m) * C::PITCH + (256 * j + 8 * lane) * 2) = make_uint4(h[0], h[1], h[2], h[3]);
             }
         }
-        __syncthreads();
-        float part[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) part[n][k] = 0.0f;
+    };
+
+    // this lane's row of an ldmatrix and the chunk that it starts from, swizzled
+    const uint32_t rows_at = ring + (lane & 15) * 128, chunk_x = static_cast<uint32_t>((lane >> 4) ^ (lane & 7)) << 4;
+    const uint8_t *sf_at = smem + warp * STAGES * C::STAGE + C::ROWS + (g & 3) * 16 + (g >> 2) * 4;
+    const float gs = p.gs ? *p.gs : 1.0f;
+    int stage = 0;
 #pragma unroll 1
-        for (int s = 0; s < n_steps; ++s) {
-            cp_async_wait<kStages - 2>();
-            __syncwarp();
-            const uint32_t buf = ring + stage * C::STAGE;
-            const int next = stage == 0 ? kStages - 1 : stage - 1;
-            uint32_t code[2][4];        // [pair of chunks][rows 0..7 and 8..15 of the first, of the second]
-#pragma unroll
-            for (int c2 = 0; c2 < 2; ++c2) {
-                const int lr = lane & 15, c = 2 * c2 + (lane >> 4);
-                ldmatrix_x4(code[c2], buf + lr * 64 + ((c ^ (lr >> 1 & 3)) << 4));
+    for (int base = q0; base < q1; base += kGroups) {
+        const int groups = min(kGroups, q1 - base);
+#pragma unroll 1
+        for (int u0 = 0; u0 < units; u0 += most) {
+            const int n_units = pass_units(u0);
+            if (base == q0 || units > most) {        // else x is there from the groups before
+                if (u0 > 0) __syncthreads();
+                convert(u0, (n_units + 1) / 2);
+                __syncthreads();
             }
-            uint32_t sw[COLS4][2];      // four columns' scales of rows g and g + 8
+#pragma unroll 1
+            for (int group = warp; group < groups; group += WARPS) {
+                // pairs of sums: columns 2t and 2t + 1 of rows g (0) and g + 8 (1)
+                uint64_t acc[NT][2];
 #pragma unroll
-            for (int c4 = 0; c4 < COLS4; ++c4)
+                for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = 0;
+#pragma unroll 1
+                for (int slice = 0; slice * kSliceUnits < n_units; ++slice) {
+                    // of the slice, whose x has one scale: a chain for each step of a unit
+                    float sum[2][NT][4];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    sw[c4][h] = *reinterpret_cast<const uint32_t *>(smem + (buf - smem_u32(smem)) + 1024 + c4 * 64 + (g & 3) * 16 + ((g >> 2) + 2 * h) * 4);
-            uint4 xb[NT][4];
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+                        for (int k = 0; k < 4; ++k) sum[0][n][k] = sum[1][n][k] = 0.0f;
+                    const uint8_t *xb = xs + (slice * p.M + g) * C::PITCH + 16 * t;      // rows that x does not have: columns that nobody reads
+                    const int last = min(kSliceUnits, n_units - slice * kSliceUnits);
+#pragma unroll 1
+                    for (int unit = 0; unit < last; ++unit, xb += 2 * kUnit) {
+                        cp_async_wait<STAGES - 2>();
+                        __syncwarp();
+                        const uint32_t rows = rows_at + stage * C::STAGE;
+                        const uint8_t *sfs = sf_at + stage * C::STAGE;
+                        const bool both = 2 * (unit0 + u0 + slice * kSliceUnits + unit) + 1 < steps_all;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    xb[n][c] = *reinterpret_cast<const uint4 *>(xs + (8 * n + g) * C::PITCH + (s * kStep + 32 * c + 8 * t) * 2);
-            __syncwarp();
-            // the stage read last time round is free: its loads were waited for above
-            issue(s0 + s + kStages - 1, next);
+                        for (int s = 0; s < 2; ++s) {
+                            if (s == 1 && !both) break;
+                            uint32_t code[2][4];        // [pair of chunks][rows 0..7 and 8..15 of the first, of the second]
+                            uint32_t sw[COLS4][2];      // four columns' scales of rows g and g + 8
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t w0 = code[c >> 1][2 * (c & 1)], w1 = code[c >> 1][2 * (c & 1) + 1];
-                uint32_t a[2][4] = {{fp4x2<0>(w0), fp4x2<0>(w1), fp4x2<1>(w0), fp4x2<1>(w1)},
-                                    {fp4x2<2>(w0), fp4x2<2>(w1), fp4x2<3>(w0), fp4x2<3>(w1)}};
-                if constexpr (FMT == QFP4_NVFP4) {
-                    // this lane's codes belong to block 2 c + t / 2: its scales of rows g and g + 8
-                    const uint32_t sel = 2 * (c & 1) + (t >> 1);
-                    const uint32_t both = fp8x2<0>(__byte_perm(sw[c >> 1][0], sw[c >> 1][1], sel | (sel + 4) << 4));
-                    const uint32_t sg = __byte_perm(both, 0, 0x1010), sh = __byte_perm(both, 0, 0x3232);
+                            for (int c2 = 0; c2 < 2; ++c2) ldmatrix_x4(code[c2], rows + (chunk_x ^ ((4 * s + 2 * c2) << 4)));
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        a[u][0] = mul_f16x2(a[u][0], sg);
-                        a[u][1] = mul_f16x2(a[u][1], sh);
-                        a[u][2] = mul_f16x2(a[u][2], sg);
-                        a[u][3] = mul_f16x2(a[u][3], sh);
+                            for (int c4 = 0; c4 < COLS4; ++c4)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) sw[c4][h] = *reinterpret_cast<const uint32_t *>(sfs + (s * COLS4 + c4) * 64 + h * 8);
+                            float f[4][2];      // MXFP4: the chunks' scales of rows g and g + 8
+                            if (FMT == QFP4_MXFP4) {
+                                // the exponent field of 2^(byte - 127); 0 and 255 apart
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                    for (int h = 0; h < 2; ++h)
+                                        f[c][h] = __uint_as_float((c == 3 ? sw[0][h] >> 1 : sw[0][h] << (23 - 8 * c)) & 0x7F800000u);
+                                if (__any_sync(0xffffffffu, has_end_byte(sw[0][0]) || has_end_byte(sw[0][1]))) {
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                                        for (int h = 0; h < 2; ++h) f[c][h] = ue8m0(sw[0][h] >> (8 * c) & 255u);
+                                }
+                            }
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                uint4 x[NT];
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) x[n] = *reinterpret_cast<const uint4 *>(xb + n * 8 * C::PITCH + (s * kStep + 32 * c) * 2);
+                                const uint32_t w0 = code[c >> 1][2 * (c & 1)], w1 = code[c >> 1][2 * (c & 1) + 1];
+                                uint32_t a[2][4] = {{fp4x2<0>(w0), fp4x2<0>(w1), fp4x2<1>(w0), fp4x2<1>(w1)},
+                                                    {fp4x2<2>(w0), fp4x2<2>(w1), fp4x2<3>(w0), fp4x2<3>(w1)}};
+                                if constexpr (FMT == QFP4_NVFP4) {
+                                    // this lane's codes belong to block 2 c + t / 2: its scales of rows g and g + 8
+                                    const uint32_t sel = 2 * (c & 1) + (t >> 1);
+                                    const uint32_t two = fp8x2<0>(__byte_perm(sw[c >> 1][0], sw[c >> 1][1], sel | (sel + 4) << 4));
+                                    const uint32_t sg = __byte_perm(two, 0, 0x1010), sh = __byte_perm(two, 0, 0x3232);
+#pragma unroll
+                                    for (int u = 0; u < 2; ++u) {
+                                        a[u][0] = mul_f16x2(a[u][0], sg);
+                                        a[u][1] = mul_f16x2(a[u][1], sh);
+                                        a[u][2] = mul_f16x2(a[u][2], sg);
+                                        a[u][3] = mul_f16x2(a[u][3], sh);
+                                    }
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n) {
+                                        mma_f16(sum[s][n], a[0], x[n].x, x[n].y);
+                                        mma_f16(sum[s][n], a[1], x[n].z, x[n].w);
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n) {
+                                        float block[4];
+                                        mma_f16_zero(block, a[0], x[n].x, x[n].y);
+                                        mma_f16(block, a[1], x[n].z, x[n].w);
+                                        sum[s][n][0] = fmaf(f[c][0], block[0], sum[s][n][0]);
+                                        sum[s][n][1] = fmaf(f[c][0], block[1], sum[s][n][1]);
+                                        sum[s][n][2] = fmaf(f[c][1], block[2], sum[s][n][2]);
+                                        sum[s][n][3] = fmaf(f[c][1], block[3], sum[s][n][3]);
+                                    }
+                                }
+                            }
+                        }
+                        __syncwarp();
+                        issue();        // into the stage that was read last time round
+                        if (++stage == STAGES) stage = 0;
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        mma_f16(part[n], a[0], xb[n][c].x, xb[n][c].y);
-                        mma_f16(part[n], a[1], xb[n][c].z, xb[n][c].w);
-                    }
-                } else {
-                    const float sg = ue8m0(sw[0][0] >> (8 * c) & 255u), sh = ue8m0(sw[0][1] >> (8 * c) & 255u);
+                        const float *b = s_back + slice * p.M + 8 * n + 2 * t;
+                        const uint64_t b2 = f2_pack(b[0], b[1]);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                        mma_f16(sum, a[0], xb[n][c].x, xb[n][c].y);
-                        mma_f16(sum, a[1], xb[n][c].z, xb[n][c].w);
-                        part[n][0] = fmaf(sg, sum[0], part[n][0]);
-                        part[n][1] = fmaf(sg, sum[1], part[n][1]);
-                        part[n][2] = fmaf(sh, sum[2], part[n][2]);
-                        part[n][3] = fmaf(sh, sum[3], part[n][3]);
+                        for (int h = 0; h < 2; ++h)
+                            acc[n][h] = f2_fma(f2_add(f2_pack(sum[0][n][2 * h], sum[0][n][2 * h + 1]), f2_pack(sum[1][n][2 * h], sum[1][n][2 * h + 1])), b2, acc[n][h]);
                     }
                 }
+                // this lane's places of the group's sums: its own in every pass over K
+                float *out = s_out + group * SUMS + 2 * t * 16 + g;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float v0, v1;
+                        f2_unpack(acc[n][h], v0, v1);
+                        float *there = out + n * 8 * 16 + 8 * h;
+                        there[0] = u0 > 0 ? there[0] + v0 : v0;
+                        there[16] = u0 > 0 ? there[16] + v1 : v1;
+                    }
             }
-            if (++stage == kStages) stage = 0;
         }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const float b0 = s_back[8 * n + 2 * t], b1 = s_back[8 * n + 2 * t + 1];
-            acc[n][0] = fmaf(part[n][0], b0, acc[n][0]);
-            acc[n][1] = fmaf(part[n][1], b1, acc[n][1]);
-            acc[n][2] = fmaf(part[n][2], b0, acc[n][2]);
-            acc[n][3] = fmaf(part[n][3], b1, acc[n][3]);
+        if (units == 0)
+            for (int i = tid; i < groups * SUMS; i += THREADS) s_out[i] = 0.0f;
+        // ---- the cluster's sums: row by row of the scales' tiles
+        if (splits > 1) cluster_sync_all();
+        else __syncthreads();
+        const int tile0 = base >> 3, tiles = ((base + groups - 1) >> 3) - tile0 + 1;
+        for (int i = tid + rank * THREADS; i < p.M * tiles * 128; i += THREADS * splits) {
+            const int r = i & 127, rest = i >> 7, tile = tile0 + rest % tiles, m = rest / tiles;
+            const int q = tile * 8 + (r & 31) / 4 - base, lr = (r & 3) + 4 * (r >> 5), row = tile * 128 + r;
+            if (q < 0 || q >= groups || row >= p.N) continue;
+            const float *there = s_out + q * SUMS + m * 16 + lr;
+            float v = 0.0f;
+            if (splits == 1) {
+                v = *there;
+            } else {
+                for (int k = 0; k < splits; ++k) v += ld_cluster_f32(mapa_shared(smem_u32(there), k));
+            }
+            p.d[m * p.ldd + row] = __float2bfloat16_rn(v * gs);
         }
+        if (splits > 1) cluster_sync_all();     // a CTA's sums stay until the others have read them
+        else __syncthreads();
     }
-    // ---- the CTA's sums by row of x, then the cluster's
     cp_async_wait<0>();
-    __syncthreads();
-    constexpr int PITCH = kRows + 4;
-    float *out = reinterpret_cast<float *>(smem);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int lr = g + 8 * (k >> 1), r = 4 * warp + (lr & 3) + 32 * (lr >> 2);
-            out[(8 * n + 2 * t + (k & 1)) * PITCH + r] = acc[n][k];
-        }
-    if (splits > 1) cluster_sync_all();
-    else __syncthreads();
-    const float gs = p.gs ? *p.gs : 1.0f;
-    // rank takes its share of the rows of W
-    const int share = kRows / splits, first = rank * share;
-    for (int i = tid; i < p.M * share; i += kThreads) {
-        const int m = i / share, r = first + i % share;
-        if (row0 + r >= p.N) continue;
-        float v = 0.0f;
-        if (splits == 1) {
-            v = out[m * PITCH + r];
-        } else {
-            const uint32_t at = smem_u32(out + m * PITCH + r);
-            for (int q = 0; q < splits; ++q) v += ld_cluster_f32(mapa_shared(at, q));
-        }
-        p.d[m * p.ldd + row0 + r] = __float2bfloat16_rn(v * gs);
+}
+
+// Clusters of so many CTAs that the GPU holds at once, asked once; 0: none.
+template <int FMT, int NT>
+int clusters_at_once(int splits)
+{
+    static std::atomic<int> known[kMaxSplits + 1];
+    int n = known[splits].load(std::memory_order_relaxed);
+    if (n > 0) return n - 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(152 / splits * splits);
+    cfg.blockDim = dim3(GemvCfg<FMT, NT>::THREADS);
+    cfg.dynamicSmemBytes = GemvCfg<FMT, NT>::SMEM;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (splits == 1) {
+        n = sm_count();
+    } else if (cudaOccupancyMaxActiveClusters(&n, gemv_kernel<FMT, NT>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
     }
-    if (splits > 1) cluster_sync_all();     // a CTA's sums stay until the others have read them
+    known[splits].store(n + 1, std::memory_order_relaxed);
+    return n;
 }
 
 template <int FMT, int NT>
-int launch(const GemvParams &p, int64_t tiles, int splits, cudaStream_t s)
+int launch(const GemvParams &p, cudaStream_t s)
 {
     using C = GemvCfg<FMT, NT>;
     auto kernel = gemv_kernel<FMT, NT>;
     const int rc = ensure_smem_attr(reinterpret_cast<const void *>(kernel), C::SMEM);
     if (rc != QFP4_OK) return rc;
+    // The split of K whose busiest CTA has the least to do, counted in units: a
+    // group's part of K, the chain of the busiest warp (four times as long each), the
+    // join (as long as 12), and a pause for x (24).
+    const int64_t groups = (static_cast<int64_t>(p.N) + 127) / 128 * 8, units = (p.K + kUnit - 1) / kUnit;
+    const int64_t most = kRowSlices / p.M * kSliceUnits;
+    int splits = 0, clusters = 0;
+    int64_t best = 0;
+    for (int n = 1; n <= kMaxSplits && (n == 1 || units >= n); ++n) {
+        const int64_t c = std::min<int64_t>(clusters_at_once<FMT, NT>(n), groups);
+        if (c < 1) continue;
+        const int64_t per = (groups + c - 1) / c, part = (units + n - 1) / n;
+        const int64_t joins = (per + kGroups - 1) / kGroups, passes = part > most ? joins * ((part + most - 1) / most) : 1;
+        const int64_t cost = per * part + (per + C::WARPS - 1) / C::WARPS * part * 4 + 12 * joins * (n > 1) + 24 * (passes - 1);
+        if (splits == 0 || cost < best) {
+            best = cost;
+            splits = n;
+            clusters = static_cast<int>(c);
+        }
+    }
+    if (splits == 0) return QFP4_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * splits));
+    cfg.blockDim = dim3(GemvCfg<FMT, NT>::THREADS);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -319,13 +474,10 @@ int launch(const GemvParams &p, int64_t tiles, int splits, cudaStream_t s)
     return launch_status(cudaLaunchKernelEx(&cfg, kernel, p, splits));
 }
 
-// K is split while the CTAs do not fill the GPU three times over and each keeps
-// two steps.
-int plan_splits(int64_t tiles, int64_t steps)
+template <int FMT>
+int launch_any(const GemvParams &p, cudaStream_t s)
 {
-    int splits = 1;
-    while (splits < kMaxSplits && tiles * splits < 3 * sm_count() && steps >= 4 * splits) splits *= 2;
-    return splits;
+    return p.M <= 8 ? launch<FMT, 1>(p, s) : launch<FMT, 2>(p, s);
 }
 
 }  // namespace
@@ -350,9 +502,6 @@ extern "C" int qfp4_gemv_nt(int fmt, int64_t M, int64_t N, int64_t K, const void
                        static_cast<const uint8_t *>(W_sf), fmt == QFP4_NVFP4 ? gs_w : nullptr,
                        static_cast<__nv_bfloat16 *>(D_bf16), ldd, static_cast<int32_t>(M), static_cast<int32_t>(N),
                        static_cast<int32_t>(K)};
-    const int64_t tiles = (N + kRows - 1) / kRows;
-    const int splits = plan_splits(tiles, K / kStep);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (fmt == QFP4_NVFP4) return M <= 8 ? launch<QFP4_NVFP4, 1>(p, tiles, splits, s) : launch<QFP4_NVFP4, 2>(p, tiles, splits, s);
-    return M <= 8 ? launch<QFP4_MXFP4, 1>(p, tiles, splits, s) : launch<QFP4_MXFP4, 2>(p, tiles, splits, s);
+    return fmt == QFP4_NVFP4 ? launch_any<QFP4_NVFP4>(p, s) : launch_any<QFP4_MXFP4>(p, s);
 }
