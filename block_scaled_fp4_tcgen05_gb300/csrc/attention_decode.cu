@@ -51,7 +51,7 @@ extern "C" int qfp4_attention_decode(int type, const void *Q_bf16, int64_t ldq, 
     if (!cache_type_ok(type) || B < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1 || pages < 0 || page_size < 1 ||
         max_pages < 0 || window < 0 || ldq < q_heads * head_dim || !(scale > -3.0e38f && scale < 3.0e38f))
         return QFP4_ERR_INVALID_ARG;
-    if (!sizes_ok(B, q_heads, kv_heads, head_dim) || page_size % 16 != 0 || page_size > 65536 || pages > INT32_MAX ||
+    if (!sizes_ok(B, q_heads, kv_heads, head_dim) || page_size % 16 != 0 || page_size > 16384 || pages > INT32_MAX ||
         max_pages > kMaxLength / page_size || ldq % 8 != 0)
         return QFP4_ERR_UNSUPPORTED;
     if (B == 0) return QFP4_OK;
@@ -72,7 +72,9 @@ extern "C" int qfp4_attention_decode(int type, const void *Q_bf16, int64_t ldq, 
     p.blocks = (p.group + 8 * nt - 1) / (8 * nt);
     p.cache = static_cast<const uint8_t *>(cache);
     p.pages = pages;
-    p.page_size = static_cast<int32_t>(page_size);
+    p.page_units = static_cast<int32_t>(page_size / 16);
+    // exact for every unit of a sequence: fewer than 2^26 of them, at most 2^10 in a page
+    p.page_magic = ((uint64_t{1} << 36) + p.page_units - 1) / p.page_units;
     p.max_pages = static_cast<int32_t>(max_pages);
     p.window = static_cast<int32_t>(window < kMaxLength ? window : 0);
     p.page_table = page_table;

@@ -791,7 +791,7 @@ bool head_sizes_ok(int64_t T, int64_t q_heads, int64_t kv_heads, int64_t D, int6
 int check_cache(int type, int64_t kv_heads, int64_t D, int64_t pages, int64_t page_size)
 {
     if (!cache_type_ok(type) || kv_heads < 1 || D < 1 || pages < 0 || page_size < 1) return QFP4_ERR_INVALID_ARG;
-    if ((D != 64 && D != 128 && D != 256) || page_size % 16 != 0 || page_size > 65536 || kv_heads > kMaxHeads ||
+    if ((D != 64 && D != 128 && D != 256) || page_size % 16 != 0 || page_size > 16384 || kv_heads > kMaxHeads ||
         pages > INT32_MAX || pages * page_size > INT32_MAX)
         return QFP4_ERR_UNSUPPORTED;
     return QFP4_OK;

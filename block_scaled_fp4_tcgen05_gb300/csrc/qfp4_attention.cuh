@@ -47,7 +47,8 @@ struct AttnParams {
     int32_t blocks;             // blocks of query heads in a group
     const uint8_t *cache;
     int64_t pages;
-    int32_t page_size, max_pages, window;
+    int32_t page_units, max_pages, window;      // page_units: page_size / 16
+    uint64_t page_magic;        // ceil(2^36 / page_units): what a division by it is done with
     const int32_t *page_table, *lengths;
     float scale_log2;           // scale * log2(e)
     const float *gs_k, *gs_v;
@@ -62,17 +63,18 @@ struct AttnParams {
 __host__ __device__ constexpr int attn_piece_floats(int queries, int D) { return queries * (D + 2); }
 
 constexpr int kAttnWarps = 4, kAttnThreads = 32 * kAttnWarps;
-// tokens of a warp's stage, and stages of its ring
+// Tokens of a warp's stage, stages of its ring, and CTAs per SM that the registers
+// are sized for.
 constexpr int attn_stage_tokens(int type, int D)
 {
-    return type == QFP4_CACHE_NVFP4 ? (D == 64 ? 64 : D == 128 ? 32 : 16)
-         : type == QFP4_CACHE_E4M3  ? (D == 64 ? 32 : 16) : 16;
+    return type == QFP4_CACHE_BF16 ? (D == 64 ? 32 : 16) : D == 64 ? 64 : D == 128 ? 32 : 16;
 }
-constexpr int attn_stages(int type, int D) { return type == QFP4_CACHE_BF16 && D == 256 ? 2 : 3; }
+constexpr int kAttnStages = 2;
+constexpr int attn_ctas(int D, int nt) { return D == 256 || nt == 2 ? 2 : 4; }
 
 template <int TYPE, int D, int NT>
 struct AttnCfg {
-    static constexpr int TOKENS = attn_stage_tokens(TYPE, D), STAGES = attn_stages(TYPE, D), UNITS = TOKENS / 16;
+    static constexpr int TOKENS = attn_stage_tokens(TYPE, D), STAGES = kAttnStages, UNITS = TOKENS / 16;
     static constexpr int UNIT = cache_unit_bytes(TYPE, D), STAGE = UNITS * UNIT;
     static constexpr int TILE = TOKENS * kAttnWarps;
     static constexpr int QUERIES = 8 * NT;
@@ -104,6 +106,13 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
     if constexpr (TYPE == QFP4_CACHE_BF16) mma_bf16(c, a, b0, b1);
     else mma_f16(c, a, b0, b1);
 }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
 {
@@ -188,7 +197,7 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cas
 
 // Where a CTA stands on the line of tiles: sequence, (key head, query block) and tile.
 struct Cursor {
-    int b, item, tile, tiles;
+    int b, head, block, tile, tiles;
     int first, len;             // tokens that the sequence's tiles begin at (a multiple of 16) and end before
 
     template <int TILE>
@@ -201,7 +210,7 @@ struct Cursor {
     }
     __device__ static __forceinline__ void extent(const AttnParams &p, int length, int &first, int &len)
     {
-        const int64_t most = static_cast<int64_t>(p.max_pages) * p.page_size;
+        const int64_t most = static_cast<int64_t>(p.max_pages) * p.page_units * 16;
         len = length < 0 ? 0 : length > most ? static_cast<int>(most) : length;
         first = p.window > 0 && len > p.window ? (len - p.window) & ~15 : 0;
     }
@@ -217,8 +226,10 @@ struct Cursor {
     {
         if (++tile < tiles) return;
         tile = 0;
-        if (++item < p.kv_heads * p.blocks) return;
-        item = 0;
+        if (++block < p.blocks) return;
+        block = 0;
+        if (++head < p.kv_heads) return;
+        head = 0;
         ++b;
         load<TILE>(p);
     }
@@ -227,7 +238,7 @@ struct Cursor {
 }  // namespace attn
 
 template <int TYPE, int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads) attention_decode_kernel(const AttnParams p)
+__global__ void __launch_bounds__(kAttnThreads, attn_ctas(D, NT)) attention_decode_kernel(const AttnParams p)
 {
     using namespace attn;
     using C = AttnCfg<TYPE, D, NT>;
@@ -300,66 +311,78 @@ __global__ void __launch_bounds__(kAttnThreads) attention_decode_kernel(const At
     Cursor cur;
     cur.b = static_cast<int>(s_start[0]);
     cur.load<TILE>(p);
-    cur.item = static_cast<int>(s_start[1] / cur.tiles);
-    cur.tile = static_cast<int>(s_start[1] - static_cast<int64_t>(cur.item) * cur.tiles);
+    const int item0 = static_cast<int>(s_start[1] / cur.tiles);
+    cur.head = item0 / p.blocks;
+    cur.block = item0 - cur.head * p.blocks;
+    cur.tile = static_cast<int>(s_start[1] - static_cast<int64_t>(item0) * cur.tiles);
 
     // ---- the warp's ring
     Cursor ahead = cur;
     int64_t to_issue = hi - lo;
-    // page of this lane's unit in the tile that `ahead` stands at
-    auto page_of = [&](const Cursor &c) {
-        const int token = c.first + c.tile * TILE + warp * C::TOKENS + 16 * lane;
-        int page = -1;
-        if (lane < UNITS && token < c.len) page = p.page_table[static_cast<int64_t>(c.b) * p.max_pages + token / p.page_size];
-        return page;
+    // This lane's unit of the tile that a cursor stands at: its page (-1: none) and
+    // place there.
+    struct Unit {
+        int page, place;
     };
-    auto issue = [&](const Cursor &c, int page, int stage) {
+    auto unit_of = [&](const Cursor &c) {
         const int token = c.first + c.tile * TILE + warp * C::TOKENS + 16 * lane;
-        const bool has = lane < UNITS && token < c.len;
+        Unit u{-1, -1};
+        if (lane < UNITS && token < c.len) {
+            const uint32_t n = static_cast<uint32_t>(token) / 16;
+            const uint32_t page = static_cast<uint32_t>(n * p.page_magic >> 36);
+            u.page = p.page_table[static_cast<int64_t>(c.b) * p.max_pages + page];
+            u.place = static_cast<int>(n - page * p.page_units);
+        }
+        return u;
+    };
+    auto issue = [&](int head, Unit u, int stage) {
+        const bool has = u.place >= 0;
         const uint32_t n = __popc(__ballot_sync(0xffffffffu, has));
-        if (has && (page < 0 || page >= p.pages)) {
+        if (has && static_cast<uint32_t>(u.page) >= static_cast<uint32_t>(p.pages)) {
             atomicOr(p.status, kStatusBadGroup);
-            page = 0;
+            u.page = 0;
         }
         if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, n * C::UNIT);
         __syncwarp();
         if (has) {
-            const int64_t unit = (static_cast<int64_t>(page) * p.kv_heads + c.item / p.blocks) * (p.page_size / 16) +
-                                 token % p.page_size / 16;
+            const int64_t unit = (static_cast<int64_t>(u.page) * p.kv_heads + head) * p.page_units + u.place;
             bulk_load(smem_u32(ring + stage * C::STAGE + lane * C::UNIT), p.cache + unit * C::UNIT, C::UNIT, bars + 8 * stage);
         }
     };
-    {
-        Cursor c[STAGES];
-        int page[STAGES];
-        int n = 0;
+    {       // the first stages: all page numbers are on their way before the first is waited for
+        int head[STAGES], n = 0;
+        Unit u[STAGES];
 #pragma unroll
         for (int i = 0; i < STAGES; ++i) {
-            c[i] = ahead;
-            page[i] = -1;
+            head[i] = ahead.head;
             if (i < to_issue) {
-                page[i] = page_of(ahead);
+                u[i] = unit_of(ahead);
                 ahead.next<TILE>(p);
                 n = i + 1;
             }
         }
 #pragma unroll
         for (int i = 0; i < STAGES; ++i)
-            if (i < n) issue(c[i], page[i], i);
+            if (i < n) issue(head[i], u[i], i);
         to_issue -= n;
     }
-    int page_next = to_issue > 0 ? page_of(ahead) : -1;
+    Unit next{-1, -1};
+    if (to_issue > 0) next = unit_of(ahead);
 
     int stage = 0;
     uint32_t phase = 0;
     bool dead = false;
     const float gs_k = TYPE == QFP4_CACHE_NVFP4 ? *p.gs_k : 1.0f, gs_v = TYPE == QFP4_CACHE_NVFP4 ? *p.gs_v : 1.0f;
     int64_t at = lo;
+    // items that lie across CTAs and whose last piece this CTA wrote
+    struct Late {
+        int b, head, block, c0, n;
+    };
+    Late late[2] = {};
 
     while (at < hi) {
         // ---- a segment: the CTA's tiles of one (sequence, key head, query block)
-        const int b = cur.b, item = cur.item, seg_first = cur.tile, seg_tiles = cur.tiles, len = cur.len, first = cur.first;
-        const int head = item / p.blocks, qblock = item - head * p.blocks;
+        const int b = cur.b, head = cur.head, qblock = cur.block, seg_first = cur.tile, seg_tiles = cur.tiles, len = cur.len, first = cur.first;
         const int visible = p.window > 0 && len > p.window ? len - p.window : 0;      // first token that counts
         const int queries = min(QUERIES, p.group - qblock * QUERIES);
         const int64_t q_head0 = static_cast<int64_t>(head) * p.group + qblock * QUERIES;
@@ -655,23 +678,19 @@ __global__ void __launch_bounds__(kAttnThreads) attention_decode_kernel(const At
                                 uint32_t sw = *reinterpret_cast<const uint32_t *>(unit + U.v_scales + blk * 16 + 4 * t);
                                 if (part) sw &= __byte_perm(0x0000FF00u, 0, (live & 1) | (live & 2) << 3 | (live & 4) << 6 | (live & 8) << 9);
                                 const uint32_t s01 = fp8x2<0>(sw), s23 = fp8x2<1>(sw);
-                                const uint32_t sc[4] = {__byte_perm(s01, 0, 0x1010), __byte_perm(s01, 0, 0x3232),
-                                                        __byte_perm(s23, 0, 0x1010), __byte_perm(s23, 0, 0x3232)};
-                                uint32_t v[4][4];       // [token][pair of dims]
+                                // a byte of two tokens' codes of a dim: the even dims, the odd ones
+                                constexpr uint32_t LOW = 0x0F0F0F0Fu;
+                                const uint32_t e01 = (w[0][y] & LOW) | (w[1][y] << 4 & ~LOW), o01 = (w[0][y] >> 4 & LOW) | (w[1][y] & ~LOW);
+                                const uint32_t e23 = (w[2][y] & LOW) | (w[3][y] << 4 & ~LOW), o23 = (w[2][y] >> 4 & LOW) | (w[3][y] & ~LOW);
+                                const uint32_t a[4][4] = {
+                                    {mul_f16x2(fp4x2<0>(e01), s01), mul_f16x2(fp4x2<0>(o01), s01), mul_f16x2(fp4x2<0>(e23), s23), mul_f16x2(fp4x2<0>(o23), s23)},
+                                    {mul_f16x2(fp4x2<1>(e01), s01), mul_f16x2(fp4x2<1>(o01), s01), mul_f16x2(fp4x2<1>(e23), s23), mul_f16x2(fp4x2<1>(o23), s23)},
+                                    {mul_f16x2(fp4x2<2>(e01), s01), mul_f16x2(fp4x2<2>(o01), s01), mul_f16x2(fp4x2<2>(e23), s23), mul_f16x2(fp4x2<2>(o23), s23)},
+                                    {mul_f16x2(fp4x2<3>(e01), s01), mul_f16x2(fp4x2<3>(o01), s01), mul_f16x2(fp4x2<3>(e23), s23), mul_f16x2(fp4x2<3>(o23), s23)}};
 #pragma unroll
-                                for (int s = 0; s < 4; ++s) {
-                                    v[s][0] = mul_f16x2(fp4x2<0>(w[s][y]), sc[s]);
-                                    v[s][1] = mul_f16x2(fp4x2<1>(w[s][y]), sc[s]);
-                                    v[s][2] = mul_f16x2(fp4x2<2>(w[s][y]), sc[s]);
-                                    v[s][3] = mul_f16x2(fp4x2<3>(w[s][y]), sc[s]);
-                                }
+                                for (int k = 0; k < 4; ++k)
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const uint32_t a[4] = {__byte_perm(v[0][k], v[1][k], 0x5410), __byte_perm(v[0][k], v[1][k], 0x7632),
-                                                           __byte_perm(v[2][k], v[3][k], 0x5410), __byte_perm(v[2][k], v[3][k], 0x7632)};
-#pragma unroll
-                                    for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * (y0 + y) + k], a, pf[n][0], pf[n][1]);
-                                }
+                                    for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * (y0 + y) + k], a[k], pf[n][0], pf[n][1]);
                             } else if constexpr (TYPE == QFP4_CACHE_E4M3) {
                                 const uint32_t lo0 = __byte_perm(w[0][y], w[1][y], 0x5140), hi0 = __byte_perm(w[0][y], w[1][y], 0x7362);
                                 const uint32_t lo1 = __byte_perm(w[2][y], w[3][y], 0x5140), hi1 = __byte_perm(w[2][y], w[3][y], 0x7362);
@@ -697,9 +716,9 @@ __global__ void __launch_bounds__(kAttnThreads) attention_decode_kernel(const At
             }
             __syncwarp();
             if (to_issue > 0) {
-                issue(ahead, page_next, stage);
+                issue(ahead.head, next, stage);
                 ahead.next<TILE>(p);
-                page_next = --to_issue > 0 ? page_of(ahead) : -1;
+                if (--to_issue > 0) next = unit_of(ahead);
             }
             if (++stage == STAGES) {
                 stage = 0;
@@ -707,10 +726,10 @@ __global__ void __launch_bounds__(kAttnThreads) attention_decode_kernel(const At
             }
             ++at;
             cur.next<TILE>(p);
-        } while (at < hi && cur.b == b && cur.item == item);
+        } while (at < hi && cur.b == b && cur.head == head && cur.block == qblock);
 
         // ---- the warps' results joined: o relative to the CTA's maximum, added up in the warps' order
-        const int seg_n = static_cast<int>(cur.b == b && cur.item == item ? cur.tile : seg_tiles) - seg_first;
+        const int seg_n = static_cast<int>(cur.b == b && cur.head == head && cur.block == qblock ? cur.tile : seg_tiles) - seg_first;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -769,8 +788,20 @@ __global__ void __launch_bounds__(kAttnThreads) attention_decode_kernel(const At
             const float4 v = *reinterpret_cast<const float4 *>(s_o + q * (D + 4) + d0 + 4 * PER * i);
             acc[4 * i] = v.x, acc[4 * i + 1] = v.y, acc[4 * i + 2] = v.z, acc[4 * i + 3] = v.w;
         }
-        bool write = whole;
-        if (!whole) {
+        auto write_out = [&](int seq, int hd, int block, float m_, float l_) {
+            if (q >= min(QUERIES, p.group - block * QUERIES)) return;
+            // no token: zeros
+            const float inv = m_ == -INFINITY ? 0.0f : gs_v / l_;
+            const int64_t row = (static_cast<int64_t>(seq) * p.kv_heads + hd) * p.group + block * QUERIES + q;
+#pragma unroll
+            for (int i = 0; i < DIMS / 4; ++i)
+                *reinterpret_cast<uint2 *>(p.out + row * D + d0 + 4 * PER * i) =
+                    make_uint2(pack_bf16(acc[4 * i] * inv, acc[4 * i + 1] * inv), pack_bf16(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
+            if (p.lse && tid % PER == 0) p.lse[row] = m_ == -INFINITY ? -INFINITY : (m_ + log2f(l_)) * 0.693147180559945309f;
+        };
+        if (whole) {
+            write_out(b, head, qblock, m_all, l_all);
+        } else {
 #pragma unroll
             for (int i = 0; i < DIMS / 4; ++i)
                 *reinterpret_cast<float4 *>(piece + q * D + d0 + 4 * PER * i) =
@@ -783,45 +814,64 @@ __global__ void __launch_bounds__(kAttnThreads) attention_decode_kernel(const At
             __syncthreads();
             if (tid == 0) s_last = atom_add_acq_rel_gpu(p.counters + c0, 1u) == static_cast<uint32_t>(c1 - c0);
             __syncthreads();
-            write = s_last != 0;
-            if (write) {
-                __threadfence();
+            if (s_last) {       // all pieces are there: joined when this CTA's own tiles are done
                 if (tid == 0) p.counters[c0] = 0;
-                m_all = -INFINITY;
-                l_all = 0.0f;
-#pragma unroll
-                for (int i = 0; i < DIMS; ++i) acc[i] = 0.0f;
-                for (int64_t c = c0; c <= c1; ++c) {
-                    const float *from = p.partial + (2 * c + (c == c0)) * PIECE;
-                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(from + QUERIES * D + 2 * q));
-                    const float top = max_nan(m_all, ml.x);
-                    const float fa = m_all == -INFINITY ? 0.0f : exp2_fast(m_all - top);
-                    const float fb = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - top);
-                    m_all = top;
-                    l_all = l_all * fa + ml.y * fb;
-#pragma unroll
-                    for (int i = 0; i < DIMS / 4; ++i) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(from + q * D + d0 + 4 * PER * i));
-                        acc[4 * i] = acc[4 * i] * fa + v.x * fb;
-                        acc[4 * i + 1] = acc[4 * i + 1] * fa + v.y * fb;
-                        acc[4 * i + 2] = acc[4 * i + 2] * fa + v.z * fb;
-                        acc[4 * i + 3] = acc[4 * i + 3] * fa + v.w * fb;
-                    }
-                }
+                const int which = seg_first != 0 ? 0 : 1;       // a CTA has two items in pieces at most
+                late[which] = Late{b, head, qblock, static_cast<int>(c0), static_cast<int>(c1 - c0) + 1};
             }
         }
-        if (write && q < queries) {
-            // no token: zeros
-            const float inv = m_all == -INFINITY ? 0.0f : gs_v / l_all;
-            const int64_t row = static_cast<int64_t>(b) * p.kv_heads * p.group + q_head0 + q;
-#pragma unroll
-            for (int i = 0; i < DIMS / 4; ++i)
-                *reinterpret_cast<uint2 *>(p.out + row * D + d0 + 4 * PER * i) =
-                    make_uint2(pack_bf16(acc[4 * i] * inv, acc[4 * i + 1] * inv), pack_bf16(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
-            if (p.lse && tid % PER == 0)
-                p.lse[row] = m_all == -INFINITY ? -INFINITY : (m_all + log2f(l_all)) * 0.693147180559945309f;
-        }
         __syncthreads();
+        if (at < hi) continue;
+
+        // ---- joins: the pieces come to the rings' place, so many at a time that their
+        // loads do not wait for one another
+        constexpr int CHUNKS = PIECE / 4, BATCH = C::RING / (PIECE * 4);
+        static_assert(PIECE % 4 == 0 && BATCH >= 1, "pieces are copied 16 bytes at a time");
+        float *s_pieces = reinterpret_cast<float *>(smem);
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+            const Late w = late[which];
+            if (w.n == 0) continue;
+            __threadfence();
+            float m_ = -INFINITY, l_ = 0.0f;
+#pragma unroll
+            for (int i = 0; i < DIMS; ++i) acc[i] = 0.0f;
+#pragma unroll 1
+            for (int first_c = 0; first_c < w.n; first_c += BATCH) {
+                const int n = min(BATCH, w.n - first_c);
+                for (int i = tid; i < n * CHUNKS; i += kAttnThreads) {
+                    const int c = i / CHUNKS, pc = first_c + c;
+                    cp_async16(smem_u32(s_pieces + i * 4),
+                               p.partial + (2 * static_cast<int64_t>(w.c0 + pc) + (pc == 0)) * PIECE + (i - c * CHUNKS) * 4);
+                }
+                cp_async_wait_all();
+                __syncthreads();
+                float top = m_;
+                for (int c = 0; c < n; ++c) top = max_nan(top, s_pieces[c * PIECE + QUERIES * D + 2 * q]);
+                const float f0 = m_ == -INFINITY ? 0.0f : exp2_fast(m_ - top);
+                m_ = top;
+                l_ *= f0;
+#pragma unroll
+                for (int i = 0; i < DIMS; ++i) acc[i] *= f0;
+#pragma unroll 2
+                for (int c = 0; c < n; ++c) {
+                    const float *pc = s_pieces + c * PIECE;
+                    const float2 ml = *reinterpret_cast<const float2 *>(pc + QUERIES * D + 2 * q);
+                    const float f = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - top);
+                    l_ += ml.y * f;
+#pragma unroll
+                    for (int i = 0; i < DIMS / 4; ++i) {
+                        const float4 v = *reinterpret_cast<const float4 *>(pc + q * D + d0 + 4 * PER * i);
+                        acc[4 * i] += v.x * f;
+                        acc[4 * i + 1] += v.y * f;
+                        acc[4 * i + 2] += v.z * f;
+                        acc[4 * i + 3] += v.w * f;
+                    }
+                }
+                __syncthreads();
+            }
+            write_out(w.b, w.head, w.block, m_, l_);
+        }
     }
     if (dead) {     // copies in flight have time to land before the shared memory goes to another CTA
         const uint64_t t0 = globaltimer_ns();

@@ -777,7 +777,7 @@ enum { QFP4_CACHE_BF16 = 0, QFP4_CACHE_E4M3 = 1, QFP4_CACHE_NVFP4 = 2 };
  *   scales    E4M3: fp32 [token]; NVFP4: K [token][head_dim / 16], V
  *             [head_dim / 16][t][h][e]
  * so that a warp reads them as operands of the tensor cores' products.
- * head_dim is 64, 128 or 256, page_size a multiple of 16 up to 65536, and
+ * head_dim is 64, 128 or 256, page_size a multiple of 16 up to 16384, and
  * pages * page_size <= 2^31 - 1.  0 for sizes that no cache has. */
 size_t qfp4_kv_cache_page_bytes(int type, int64_t kv_heads, int64_t head_dim, int64_t page_size);
 
