@@ -62,7 +62,6 @@ struct AttnParams {
 // Space of a piece in the workspace: o, then m and l of each query.
 __host__ __device__ constexpr int attn_piece_floats(int queries, int D) { return queries * (D + 2); }
 
-constexpr int kAttnWarps = 4, kAttnThreads = 32 * kAttnWarps;
 // Tokens of a warp's stage, stages of its ring, and CTAs per SM that the registers
 // are sized for.
 constexpr int attn_stage_tokens(int type, int D)
@@ -70,17 +69,21 @@ constexpr int attn_stage_tokens(int type, int D)
     return type == QFP4_CACHE_BF16 ? (D == 64 ? 32 : 16) : D == 64 ? 64 : D == 128 ? 32 : 16;
 }
 constexpr int kAttnStages = 2;
-constexpr int attn_ctas(int D, int nt) { return D == 256 || nt == 2 ? 2 : 4; }
+constexpr int attn_ctas(int D, int nt, int warps) { return (D == 256 || nt == 2 ? 8 : 16) / warps; }
 
-template <int TYPE, int D, int NT>
+template <int TYPE, int D, int NT, int WARPS_>
 struct AttnCfg {
     static constexpr int TOKENS = attn_stage_tokens(TYPE, D), STAGES = kAttnStages, UNITS = TOKENS / 16;
     static constexpr int UNIT = cache_unit_bytes(TYPE, D), STAGE = UNITS * UNIT;
-    static constexpr int TILE = TOKENS * kAttnWarps;
+    static constexpr int WARPS = WARPS_, THREADS = 32 * WARPS;
+    static constexpr int TILE = TOKENS * WARPS;
     static constexpr int QUERIES = 8 * NT;
-    static constexpr int RING = kAttnWarps * STAGES * STAGE;
-    static constexpr int JOIN = QUERIES * (D + 4) * 4 + kAttnWarps * QUERIES * 8;
-    static constexpr int BARS = kAttnWarps * STAGES * 8;
+    static constexpr int RING = WARPS * STAGES * STAGE;
+    // Where the warps' results meet: half of them side by side, or one after the
+    // other where more would cost a CTA per SM.
+    static constexpr int SUMS = TYPE == QFP4_CACHE_NVFP4 && D <= 128 ? WARPS / 2 : 1, SUM = QUERIES * (D + 4);
+    static constexpr int JOIN = SUMS * SUM * 4 + WARPS * QUERIES * 8;
+    static constexpr int BARS = WARPS * STAGES * 8;
     static constexpr int SMEM = RING + JOIN + BARS;
 };
 
@@ -224,7 +227,13 @@ struct Cursor {
     template <int TILE>
     __device__ __forceinline__ void next(const AttnParams &p)
     {
-        if (++tile < tiles) return;
+        skip<TILE>(p, 1);
+    }
+    // n tiles on, to the next item at most
+    template <int TILE>
+    __device__ __forceinline__ void skip(const AttnParams &p, int n)
+    {
+        if ((tile += n) < tiles) return;
         tile = 0;
         if (++block < p.blocks) return;
         block = 0;
@@ -237,20 +246,20 @@ struct Cursor {
 
 }  // namespace attn
 
-template <int TYPE, int D, int NT>
-__global__ void __launch_bounds__(kAttnThreads, attn_ctas(D, NT)) attention_decode_kernel(const AttnParams p)
+template <int TYPE, int D, int NT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, attn_ctas(D, NT, WARPS)) attention_decode_kernel(const AttnParams p)
 {
     using namespace attn;
-    using C = AttnCfg<TYPE, D, NT>;
+    using C = AttnCfg<TYPE, D, NT, WARPS>;
     constexpr CacheUnit U(TYPE, D);
     constexpr int UNITS = C::UNITS, STAGES = C::STAGES, TILE = C::TILE, QUERIES = C::QUERIES;
     constexpr int KSTEPS = D / 16, MTILES = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_sum[kAttnWarps];
+    __shared__ int64_t s_sum[C::WARPS];
     __shared__ int64_t s_start[2];      // the CTA's first tile: sequence, tile within it
     __shared__ uint32_t s_last;
     float *s_o = reinterpret_cast<float *>(smem + C::RING);                     // [QUERIES][D + 4]
-    float2 *s_ml = reinterpret_cast<float2 *>(s_o + QUERIES * (D + 4));         // [warps][QUERIES]
+    float2 *s_ml = reinterpret_cast<float2 *>(s_o + C::SUMS * C::SUM);         // [warps][QUERIES]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const uint32_t bars = smem_u32(smem + C::RING + C::JOIN) + warp * STAGES * 8;
     uint8_t *ring = smem + warp * STAGES * C::STAGE;
@@ -265,7 +274,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas(D, NT)) attention_deco
     // ---- the CTA's piece of the line of tiles
     const int items = p.kv_heads * p.blocks;
     int64_t mine = 0;
-    for (int b = tid; b < p.B; b += kAttnThreads) {
+    for (int b = tid; b < p.B; b += C::THREADS) {
         int first, len;
         const int length = p.lengths[b];
         Cursor::extent(p, length, first, len);
@@ -278,7 +287,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas(D, NT)) attention_deco
     __syncthreads();
     int64_t total = 0;
 #pragma unroll
-    for (int i = 0; i < kAttnWarps; ++i) total += s_sum[i];
+    for (int i = 0; i < C::WARPS; ++i) total += s_sum[i];
     const int64_t ctas = total < gridDim.x ? total : gridDim.x;
     if (blockIdx.x >= ctas) return;
     const int64_t lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
@@ -445,8 +454,10 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas(D, NT)) attention_deco
             }
         }
 
-        do {
-            const int token0 = first + cur.tile * TILE + warp * C::TOKENS;
+        const int seg_n = static_cast<int>(hi - at < seg_tiles - seg_first ? hi - at : seg_tiles - seg_first);
+        int token0 = first + seg_first * TILE + warp * C::TOKENS;
+#pragma unroll 1
+        for (int n_tile = 0; n_tile < seg_n; ++n_tile, token0 += TILE) {
             if (!mbar_wait(bars + 8 * stage, phase)) {
                 if (lane == 0) atomicOr(p.status, kStatusTimeout);
                 dead = true;
@@ -724,12 +735,11 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas(D, NT)) attention_deco
                 stage = 0;
                 phase ^= 1;
             }
-            ++at;
-            cur.next<TILE>(p);
-        } while (at < hi && cur.b == b && cur.head == head && cur.block == qblock);
+        }
+        at += seg_n;
+        cur.skip<TILE>(p, seg_n);
 
         // ---- the warps' results joined: o relative to the CTA's maximum, added up in the warps' order
-        const int seg_n = static_cast<int>(cur.b == b && cur.head == head && cur.block == qblock ? cur.tile : seg_tiles) - seg_first;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -739,9 +749,10 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas(D, NT)) attention_deco
                 if (g == 0) s_ml[warp * QUERIES + 8 * n + 2 * t + k] = make_float2(m[n][k], l[n][k]);
             }
         __syncthreads();
+        constexpr int TURNS = C::WARPS / C::SUMS;
 #pragma unroll
-        for (int turn = 0; turn < kAttnWarps; ++turn) {
-            if (turn == warp) {
+        for (int turn = 0; turn < TURNS; ++turn) {
+            if (turn == warp / C::SUMS) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -749,11 +760,11 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas(D, NT)) attention_deco
                         const int q = 8 * n + 2 * t + k;
                         float top = -INFINITY;
 #pragma unroll
-                        for (int w = 0; w < kAttnWarps; ++w) top = max_nan(top, s_ml[w * QUERIES + q].x);
+                        for (int w = 0; w < C::WARPS; ++w) top = max_nan(top, s_ml[w * QUERIES + q].x);
                         const float own = TYPE == QFP4_CACHE_E4M3 ? mw[n][k] : m[n][k];
                         const float f = own == -INFINITY ? 0.0f : exp2_fast(own - top);
                         // dims g D / 8 + 2 i and the next
-                        float *dst = s_o + q * (D + 4) + g * (D / 8);
+                        float *dst = s_o + (warp % C::SUMS) * C::SUM + q * (D + 4) + g * (D / 8);
 #pragma unroll
                         for (int i = 0; i < MTILES; ++i) {
                             float2 v = make_float2(o[n][i][k] * f, o[n][i][2 + k] * f);
@@ -771,25 +782,33 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas(D, NT)) attention_deco
         const bool whole = seg_first == 0 && seg_n == seg_tiles;
         constexpr int PIECE = attn_piece_floats(QUERIES, D);
         float *piece = p.partial + (2 * static_cast<int64_t>(blockIdx.x) + (seg_first == 0)) * PIECE;
-        // thread -> query tid / (threads per query), dims
-        constexpr int PER = kAttnThreads / QUERIES, DIMS = D / PER;     // 16 or 8 threads per query
-        const int q = tid / PER, d0 = (tid % PER) * 4;
+        // a thread's query and dims
+        constexpr int ALL = C::THREADS / QUERIES, PER = ALL < D / 4 ? ALL : D / 4, DIMS = D / PER;
+        static_assert(DIMS % 4 == 0 && PER * QUERIES <= C::THREADS, "a thread has whole fours of one query's dims");
+        const bool mine = tid < PER * QUERIES;
+        const int q = mine ? tid / PER : 0, d0 = (tid % PER) * 4;
         float m_all = -INFINITY, l_all = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) m_all = max_nan(m_all, s_ml[w * QUERIES + q].x);
+        for (int w = 0; w < C::WARPS; ++w) m_all = max_nan(m_all, s_ml[w * QUERIES + q].x);
 #pragma unroll
-        for (int w = 0; w < kAttnWarps; ++w) {
+        for (int w = 0; w < C::WARPS; ++w) {
             const float2 v = s_ml[w * QUERIES + q];
             if (v.x != -INFINITY) l_all += v.y * exp2_fast(v.x - m_all);
         }
         float acc[DIMS];
 #pragma unroll
         for (int i = 0; i < DIMS / 4; ++i) {
-            const float4 v = *reinterpret_cast<const float4 *>(s_o + q * (D + 4) + d0 + 4 * PER * i);
+            const float *src = s_o + q * (D + 4) + d0 + 4 * PER * i;
+            float4 v = *reinterpret_cast<const float4 *>(src);
+#pragma unroll
+            for (int k = 1; k < C::SUMS; ++k) {
+                const float4 u = *reinterpret_cast<const float4 *>(src + k * C::SUM);
+                v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+            }
             acc[4 * i] = v.x, acc[4 * i + 1] = v.y, acc[4 * i + 2] = v.z, acc[4 * i + 3] = v.w;
         }
         auto write_out = [&](int seq, int hd, int block, float m_, float l_) {
-            if (q >= min(QUERIES, p.group - block * QUERIES)) return;
+            if (!mine || q >= min(QUERIES, p.group - block * QUERIES)) return;
             // no token: zeros
             const float inv = m_ == -INFINITY ? 0.0f : gs_v / l_;
             const int64_t row = (static_cast<int64_t>(seq) * p.kv_heads + hd) * p.group + block * QUERIES + q;
@@ -802,16 +821,18 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas(D, NT)) attention_deco
         if (whole) {
             write_out(b, head, qblock, m_all, l_all);
         } else {
+            if (mine) {
 #pragma unroll
-            for (int i = 0; i < DIMS / 4; ++i)
-                *reinterpret_cast<float4 *>(piece + q * D + d0 + 4 * PER * i) =
-                    make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-            if (tid % PER == 0) *reinterpret_cast<float2 *>(piece + QUERIES * D + 2 * q) = make_float2(m_all, l_all);
+                for (int i = 0; i < DIMS / 4; ++i)
+                    *reinterpret_cast<float4 *>(piece + q * D + d0 + 4 * PER * i) =
+                        make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+                if (tid % PER == 0) *reinterpret_cast<float2 *>(piece + QUERIES * D + 2 * q) = make_float2(m_all, l_all);
+            }
             // CTAs that hold the item's first and last tile
             const int64_t i0 = at - seg_n - seg_first, i1 = i0 + seg_tiles - 1;
             const int64_t c0 = ((i0 + 1) * ctas - 1) / total, c1 = ((i1 + 1) * ctas - 1) / total;
-            __threadfence();
             __syncthreads();
+            if (tid == 0) __threadfence();      // for all: they have met at the barrier
             if (tid == 0) s_last = atom_add_acq_rel_gpu(p.counters + c0, 1u) == static_cast<uint32_t>(c1 - c0);
             __syncthreads();
             if (s_last) {       // all pieces are there: joined when this CTA's own tiles are done
@@ -839,7 +860,7 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas(D, NT)) attention_deco
 #pragma unroll 1
             for (int first_c = 0; first_c < w.n; first_c += BATCH) {
                 const int n = min(BATCH, w.n - first_c);
-                for (int i = tid; i < n * CHUNKS; i += kAttnThreads) {
+                for (int i = tid; i < n * CHUNKS; i += C::THREADS) {
                     const int c = i / CHUNKS, pc = first_c + c;
                     cp_async16(smem_u32(s_pieces + i * 4),
                                p.partial + (2 * static_cast<int64_t>(w.c0 + pc) + (pc == 0)) * PIECE + (i - c * CHUNKS) * 4);
@@ -881,14 +902,14 @@ __global__ void __launch_bounds__(kAttnThreads, attn_ctas(D, NT)) attention_deco
 }
 
 // CTAs of this kernel that an SM holds, no more than `most`; asked once.
-template <int TYPE, int D, int NT>
+template <int TYPE, int D, int NT, int WARPS>
 int attn_per_sm(int most)
 {
     static std::atomic<int> known{0};
     int n = known.load(std::memory_order_relaxed);
     if (n == 0) {
-        using C = AttnCfg<TYPE, D, NT>;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attention_decode_kernel<TYPE, D, NT>, kAttnThreads,
+        using C = AttnCfg<TYPE, D, NT, WARPS>;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, attention_decode_kernel<TYPE, D, NT, WARPS>, C::THREADS,
                                                           C::SMEM) != cudaSuccess ||
             n < 1)
             return 0;
@@ -899,16 +920,30 @@ int attn_per_sm(int most)
 
 // The grid is what the GPU holds at once, whatever the lengths, which only the
 // device knows: 152 SMs times the CTAs of each, at most per_sm.
+template <int TYPE, int D, int NT, int WARPS>
+int attn_launch_one(const AttnParams &p, int per_sm, cudaStream_t s)
+{
+    using C = AttnCfg<TYPE, D, NT, WARPS>;
+    auto kernel = attention_decode_kernel<TYPE, D, NT, WARPS>;
+    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(kernel), C::SMEM);
+    if (rc != QFP4_OK) return rc;
+    const int n = attn_per_sm<TYPE, D, NT, WARPS>(per_sm);
+    if (n == 0) return QFP4_ERR_CUDA;
+    return launch_status(launch_pdl(kernel, dim3(152 * n), dim3(C::THREADS), C::SMEM, s, p));
+}
+
+// NVFP4's CTAs have eight warps, two of them on an SM, where the items (sequences x
+// key heads x blocks of queries) are few: half as many pieces to join (1 x 4096
+// tokens x 8 heads 11 us, 16 with four warps; 1 x 131072 48, 55).  Where they are
+// many, four smaller CTAs hide one another's joins (64 ragged sequences 83 us, 95 with
+// eight warps; 256 short ones 32, 43).
 template <int TYPE, int D, int NT>
 int attn_launch(const AttnParams &p, int per_sm, cudaStream_t s)
 {
-    using C = AttnCfg<TYPE, D, NT>;
-    auto kernel = attention_decode_kernel<TYPE, D, NT>;
-    const int rc = ensure_smem_attr(reinterpret_cast<const void *>(kernel), C::SMEM);
-    if (rc != QFP4_OK) return rc;
-    const int n = attn_per_sm<TYPE, D, NT>(per_sm);
-    if (n == 0) return QFP4_ERR_CUDA;
-    return launch_status(launch_pdl(kernel, dim3(152 * n), dim3(kAttnThreads), C::SMEM, s, p));
+    if constexpr (TYPE == QFP4_CACHE_NVFP4 && D <= 128) {
+        if (static_cast<int64_t>(p.B) * p.kv_heads * p.blocks <= 2 * 152) return attn_launch_one<TYPE, D, NT, 8>(p, per_sm, s);
+    }
+    return attn_launch_one<TYPE, D, NT, 4>(p, per_sm, s);
 }
 
 // Of attention_decode_<type>.cu.
