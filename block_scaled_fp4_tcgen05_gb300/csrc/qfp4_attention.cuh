@@ -69,6 +69,7 @@ constexpr int attn_stage_tokens(int type, int D)
     return type == QFP4_CACHE_BF16 ? (D == 64 ? 32 : 16) : D == 64 ? 64 : D == 128 ? 32 : 16;
 }
 constexpr int kAttnStages = 2;
+constexpr float kSlack = 8.0f;
 constexpr int attn_ctas(int D, int nt, int warps) { return (D == 256 || nt == 2 ? 8 : 16) / warps; }
 
 template <int TYPE, int D, int NT, int WARPS_>
@@ -333,10 +334,11 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(D, NT, WARPS)) attention
     struct Unit {
         int page, place;
     };
+    const int lane_token = lane < UNITS ? warp * C::TOKENS + 16 * lane : INT32_MAX / 2;
     auto unit_of = [&](const Cursor &c) {
-        const int token = c.first + c.tile * TILE + warp * C::TOKENS + 16 * lane;
+        const int token = c.first + c.tile * TILE + lane_token;
         Unit u{-1, -1};
-        if (lane < UNITS && token < c.len) {
+        if (token < c.len) {
             const uint32_t n = static_cast<uint32_t>(token) / 16;
             const uint32_t page = static_cast<uint32_t>(n * p.page_magic >> 36);
             u.page = p.page_table[static_cast<int64_t>(c.b) * p.max_pages + page];
@@ -440,7 +442,8 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(D, NT, WARPS)) attention
             qmul[n][1] = __shfl_sync(0xffffffffu, back, 8 * t + 4);
         }
 
-        float o[NT][MTILES][4], m[NT][2], mw[NT][2], l[NT][2];
+        // m, mw: what l and o are relative to, base and base_w the same or 0 for none
+        float o[NT][MTILES][4], m[NT][2], mw[NT][2], base[NT][2], base_w[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(D, NT, WARPS)) attention
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 m[n][k] = mw[n][k] = -INFINITY;
-                l[n][k] = 0.0f;
+                base[n][k] = base_w[n][k] = l[n][k] = 0.0f;
             }
         }
 
@@ -570,50 +573,60 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(D, NT, WARPS)) attention
                             }
                         }
                 }
-                // ---- running maxima; with value scales, those of x + log2 s as well
-                float base[NT][2], base_w[NT][2];
-                bool moved = false;
-                float alpha[NT][2];
+                // ---- what the exponents are taken relative to.  It moves only when a logit
+                // lies more than kSlack above it (weights up to 2^kSlack are as exact in
+                // FP16 as those up to 1), to the maximum of the logits so far; with value
+                // scales, that of x + log2 s as well.  A NaN moves it too.
+                bool above = false;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float top = -INFINITY, top_w = -INFINITY;
+                    for (int k = 0; k < 2; ++k)
 #pragma unroll
-                        for (int un = 0; un < UNITS; ++un) {
-                            top = max_nan(top, max_nan(x[un][n][k], x[un][n][2 + k]));
-                            if (TYPE == QFP4_CACHE_E4M3)
-                                top_w = max_nan(top_w, max_nan(x[un][n][k] + ls[un][0], x[un][n][2 + k] + ls[un][1]));
-                        }
+                        for (int un = 0; un < UNITS; ++un)
 #pragma unroll
-                        for (int s = 4; s < 32; s <<= 1) {
-                            top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, s));
-                            if (TYPE == QFP4_CACHE_E4M3) top_w = max_nan(top_w, __shfl_xor_sync(0xffffffffu, top_w, s));
-                        }
-                        const float m_new = max_nan(m[n][k], top);
-                        base[n][k] = m_new == -INFINITY ? 0.0f : m_new;
-                        const float a = exp2_fast(m[n][k] - base[n][k]);
-                        l[n][k] *= a;
-                        m[n][k] = m_new;
-                        alpha[n][k] = a;
-                        if (TYPE == QFP4_CACHE_E4M3) {
-                            const float w_new = max_nan(mw[n][k], top_w);
-                            base_w[n][k] = w_new == -INFINITY ? 0.0f : w_new;
-                            alpha[n][k] = exp2_fast(mw[n][k] - base_w[n][k]);
-                            mw[n][k] = w_new;
-                        }
-                        moved |= alpha[n][k] != 1.0f;
-                    }
-                if (__any_sync(0xffffffffu, moved)) {
+                            for (int h = 0; h < 2; ++h) {
+                                above |= !(x[un][n][2 * h + k] <= m[n][k] + kSlack);
+                                if (TYPE == QFP4_CACHE_E4M3) above |= !(x[un][n][2 * h + k] + ls[un][h] <= mw[n][k] + kSlack);
+                            }
+                if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n) {
+                        float alpha[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float top = -INFINITY, top_w = -INFINITY;
+#pragma unroll
+                            for (int un = 0; un < UNITS; ++un) {
+                                top = max_nan(top, max_nan(x[un][n][k], x[un][n][2 + k]));
+                                if (TYPE == QFP4_CACHE_E4M3)
+                                    top_w = max_nan(top_w, max_nan(x[un][n][k] + ls[un][0], x[un][n][2 + k] + ls[un][1]));
+                            }
+#pragma unroll
+                            for (int s = 4; s < 32; s <<= 1) {
+                                top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, s));
+                                if (TYPE == QFP4_CACHE_E4M3) top_w = max_nan(top_w, __shfl_xor_sync(0xffffffffu, top_w, s));
+                            }
+                            const float m_new = max_nan(m[n][k], top);
+                            base[n][k] = m_new == -INFINITY ? 0.0f : m_new;
+                            alpha[k] = exp2_fast(m[n][k] - base[n][k]);
+                            l[n][k] *= alpha[k];
+                            m[n][k] = m_new;
+                            if (TYPE == QFP4_CACHE_E4M3) {
+                                const float w_new = max_nan(mw[n][k], top_w);
+                                base_w[n][k] = w_new == -INFINITY ? 0.0f : w_new;
+                                alpha[k] = exp2_fast(mw[n][k] - base_w[n][k]);
+                                mw[n][k] = w_new;
+                            }
+                        }
 #pragma unroll
                         for (int i = 0; i < MTILES; ++i) {
-                            o[n][i][0] *= alpha[n][0];
-                            o[n][i][1] *= alpha[n][1];
-                            o[n][i][2] *= alpha[n][0];
-                            o[n][i][3] *= alpha[n][1];
+                            o[n][i][0] *= alpha[0];
+                            o[n][i][1] *= alpha[1];
+                            o[n][i][2] *= alpha[0];
+                            o[n][i][3] *= alpha[1];
                         }
+                    }
                 }
                 // ---- weights and their products with the values
 #pragma unroll
