@@ -844,8 +844,9 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(D, NT, WARPS)) attention
             // CTAs that hold the item's first and last tile
             const int64_t i0 = at - seg_n - seg_first, i1 = i0 + seg_tiles - 1;
             const int64_t c0 = ((i0 + 1) * ctas - 1) / total, c1 = ((i1 + 1) * ctas - 1) / total;
+            // one thread releases the piece for all, who have met at the barrier, and
+            // acquires the others' for all who meet at the next
             __syncthreads();
-            if (tid == 0) __threadfence();      // for all: they have met at the barrier
             if (tid == 0) s_last = atom_add_acq_rel_gpu(p.counters + c0, 1u) == static_cast<uint32_t>(c1 - c0);
             __syncthreads();
             if (s_last) {       // all pieces are there: joined when this CTA's own tiles are done
@@ -866,7 +867,6 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(D, NT, WARPS)) attention
         for (int which = 0; which < 2; ++which) {
             const Late w = late[which];
             if (w.n == 0) continue;
-            __threadfence();
             float m_ = -INFINITY, l_ = 0.0f;
 #pragma unroll
             for (int i = 0; i < DIMS; ++i) acc[i] = 0.0f;
@@ -881,13 +881,14 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(D, NT, WARPS)) attention
                 cp_async_wait_all();
                 __syncthreads();
                 float top = m_;
+#pragma unroll 8
                 for (int c = 0; c < n; ++c) top = max_nan(top, s_pieces[c * PIECE + QUERIES * D + 2 * q]);
                 const float f0 = m_ == -INFINITY ? 0.0f : exp2_fast(m_ - top);
                 m_ = top;
                 l_ *= f0;
 #pragma unroll
                 for (int i = 0; i < DIMS; ++i) acc[i] *= f0;
-#pragma unroll 2
+#pragma unroll 4
                 for (int c = 0; c < n; ++c) {
                     const float *pc = s_pieces + c * PIECE;
                     const float2 ml = *reinterpret_cast<const float2 *>(pc + QUERIES * D + 2 * q);
