@@ -46,7 +46,15 @@ struct CacheParams {
     const int32_t *slots;       // [T]
     const float *gs[2];         // NVFP4's global scales of K and V
     int64_t slot_count;         // pages * page_size
-    int32_t page_size, kv_heads;
+    uint64_t page_magic;        // ceil(2^37 / page_units): what a division by it is done with
+    int32_t page_units, kv_heads;       // page_units: page_size / 16
+
+    // Number of the unit of a slot for key head 0; head h's lies h page_units on.
+    __device__ __forceinline__ int64_t unit_of(int slot) const
+    {
+        const uint32_t n = static_cast<uint32_t>(slot) >> 4, page = static_cast<uint32_t>(n * page_magic >> 37);
+        return static_cast<int64_t>(page) * kv_heads * page_units + (n - page * page_units);
+    }
 };
 
 struct HeadParams {
@@ -200,21 +208,32 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
     return r;
 }
 
-// Writes a lane's eight elements of a key (half 0) or value (half 1) to the
-// cache: the quantisers' rules, with one scale per vector (E4M3) or per 16
-// elements (NVFP4).  Every lane of the group takes part.
+// Where a lane's eight elements of a token's keys (half 0) or values (half 1) lie
+// in a unit, and their scale.
 template <int TYPE, int LANES>
-__device__ __forceinline__ void store_cached(const HeadParams &p, int half, int64_t slot, int head, int lane,
+struct CachePlace {
+    static constexpr int UNIT = cache_unit_bytes(TYPE, LANES * 8);
+    int code, scale;
+
+    __device__ __forceinline__ CachePlace(int half, int j, int g)
+    {
+        constexpr CacheUnit U(TYPE, LANES * 8);
+        const int x = g * (U.row / LANES);
+        code = half == 0 ? U.k_code(j, x) : U.v_code(j, x);
+        scale = TYPE == QFP4_CACHE_E4M3 ? (half == 0 ? U.k_token_scale(j) : U.v_token_scale(j))
+                                        : (half == 0 ? U.k_block_scale(j, g / 2) : U.v_block_scale(j, g / 2));
+    }
+};
+
+// Writes a lane's eight elements to the cache: the quantisers' rules, with one
+// scale per vector (E4M3) or per 16 elements (NVFP4).  Every lane of the group takes
+// part.
+template <int TYPE, int LANES>
+__device__ __forceinline__ void store_cached(uint8_t *unit, const CachePlace<TYPE, LANES> &place, int lane,
                                              const float (&y)[8], bool live, float gs, float inv_gs)
 {
-    const CacheParams &c = p.c;
-    const CacheUnit u(TYPE, LANES * 8);
     const int g = lane % LANES;
-    const int64_t page = slot / c.page_size;
-    const int in_page = static_cast<int>(slot - page * c.page_size), j = in_page & 15;
-    uint8_t *unit = c.cache + ((page * c.kv_heads + head) * (c.page_size / 16) + in_page / 16) * u.bytes;
-    const int x = g * (u.row / LANES);
-    uint8_t *at = unit + (half == 0 ? u.k_code(j, x) : u.v_code(j, x));
+    uint8_t *at = unit + place.code;
     if (TYPE == QFP4_CACHE_BF16) {
         if (live) *reinterpret_cast<uint4 *>(at) = pack8(y);
         return;
@@ -230,9 +249,7 @@ __device__ __forceinline__ void store_cached(const HeadParams &p, int half, int6
         q.y = e4m3x2(y[4] * inv, y[5] * inv) | (e4m3x2(y[6] * inv, y[7] * inv) << 16);
         if (live) {
             *reinterpret_cast<uint2 *>(at) = q;
-            if (g == 0)
-                *reinterpret_cast<float *>(unit + (half == 0 ? u.k_token_scale(j) : u.v_token_scale(j))) =
-                    __fdiv_rn(a, 448.0f);
+            if (g == 0) *reinterpret_cast<float *>(unit + place.scale) = __fdiv_rn(a, 448.0f);
         }
     } else {
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
@@ -240,8 +257,7 @@ __device__ __forceinline__ void store_cached(const HeadParams &p, int half, int6
         const uint32_t q = encode8_f32<QFP4_NVFP4>(y, b);
         if (live) {
             *reinterpret_cast<uint32_t *>(at) = q;
-            if ((g & 1) == 0)
-                unit[half == 0 ? u.k_block_scale(j, g / 2) : u.v_block_scale(j, g / 2)] = static_cast<uint8_t>(b.code);
+            if ((g & 1) == 0) unit[place.scale] = static_cast<uint8_t>(b.code);
         }
     }
 }
@@ -269,7 +285,8 @@ __device__ __forceinline__ void gather(const HeadParams &p, const Place &pl, int
 constexpr int kVectors = 2;
 
 // CTAs per SM that the kernels' registers are sized for.
-constexpr int kHeadCtas = 4, kBackCtas = 2;
+constexpr int kHeadCtas = 4, kCacheCtas = 2, kBackCtas = 2;
+constexpr int head_ctas(int cache) { return cache == kNoCache ? kHeadCtas : kCacheCtas; }
 
 // Piece of the line of (token, block of heads of a kind) that a warp takes: as
 // many blocks for each, whatever the tokens and heads.
@@ -287,7 +304,7 @@ struct Piece {
 };
 
 template <int LANES, int CACHE, bool INTER>
-__global__ void __launch_bounds__(kThreads, kHeadCtas) head_kernel(const HeadParams p)
+__global__ void __launch_bounds__(kThreads, head_ctas(CACHE)) head_kernel(const HeadParams p)
 {
     constexpr int GROUPS = 32 / LANES, BLOCK = GROUPS * kVectors;
     pdl_wait();
@@ -348,6 +365,12 @@ __global__ void __launch_bounds__(kThreads, kHeadCtas) head_kernel(const HeadPar
         if (bad && lane == 0) atomicOr(&g_status_heads, kStatusBadGroup);
         if (position < 0 || (CACHE != kNoCache && kind != kQuery && slot < 0)) continue;      // uniform over the warp
 
+        constexpr int TYPE = CACHE == kNoCache ? 0 : CACHE;
+        const CachePlace<TYPE, LANES> place(kind == kValue, slot & 15, g);
+        uint8_t *units = nullptr;       // of head 0
+        if (CACHE != kNoCache && kind != kQuery)
+            units = p.c.cache + p.c.unit_of(slot) * CachePlace<TYPE, LANES>::UNIT;
+
         // y = r (a ac + b bs, b bc + a as), the weights in the cosines and sines
         uint64_t ac[2], as[2], bc[2], bs[2];
         if (kind != kValue) {
@@ -401,7 +424,8 @@ __global__ void __launch_bounds__(kThreads, kHeadCtas) head_kernel(const HeadPar
                     elements<INTER>(v, e);
                     if (!INTER && kind == kKey) gather<LANES>(p, pl, lane, e);
                     const int half = kind == kValue;
-                    store_cached<CACHE, LANES>(p, half, slot, min(h, head_end - 1), lane, e, live, gs[half], inv_gs[half]);
+                    uint8_t *unit = units + static_cast<int64_t>(min(h, head_end - 1)) * p.c.page_units * place.UNIT;
+                    store_cached<TYPE, LANES>(unit, place, lane, e, live, gs[half], inv_gs[half]);
                 }
             }
         }
@@ -657,21 +681,36 @@ struct ReadParams {
     int64_t ldo[2];
 };
 
-// A warp takes eight tokens of one head: where their slots follow one another
+// A warp takes four tokens of one head: where their slots follow one another
 // (a prefix), every 32-byte sector that it reads is used whole.
-constexpr int kReadTokens = 8;
+constexpr int kReadTokens = 4;
 
+// The places of a token's codes and scales in a unit are those of token 0, which a
+// lane knows, plus what depends on the token alone.
 template <int TYPE, int LANES>
-__device__ __forceinline__ uint4 cached8(const uint8_t *unit, int half, int j, int g, float gs)
+struct TokenPlace {
+    int code[2], scale[2];      // keys, values
+
+    __device__ __forceinline__ explicit TokenPlace(int j)
+    {
+        constexpr CacheUnit U(TYPE, LANES * 8);
+        constexpr int PIECE = U.row < 64 ? U.row : 64, W = U.row / 8;
+        const int quad = (j >> 3) * 2 + (j & 1), t = (j >> 1) & 3;
+        code[0] = (j >> 3) * (U.row / PIECE * 8 * PIECE) + (j & 7) * PIECE;
+        code[1] = W >= 16 ? quad * (W / 16 * 512) + t * 16 : (quad * W >> 4) * 512 + t * 16 + (quad * W & 15);
+        scale[0] = j * U.scale;
+        scale[1] = TYPE == QFP4_CACHE_E4M3 ? 4 * j : 4 * t + quad;
+    }
+};
+
+template <int TYPE>
+__device__ __forceinline__ uint4 cached8(const uint8_t *at, const uint8_t *scale, float gs)
 {
-    const CacheUnit u(TYPE, LANES * 8);
-    const int x = g * (u.row / LANES);
-    const uint8_t *at = unit + (half == 0 ? u.k_code(j, x) : u.v_code(j, x));
     if (TYPE == QFP4_CACHE_BF16) return __ldg(reinterpret_cast<const uint4 *>(at));
     float y[8];
     if (TYPE == QFP4_CACHE_E4M3) {
         const uint2 q = __ldg(reinterpret_cast<const uint2 *>(at));
-        const float s = __ldg(reinterpret_cast<const float *>(unit + (half == 0 ? u.k_token_scale(j) : u.v_token_scale(j))));
+        const float s = __ldg(reinterpret_cast<const float *>(scale));
         const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -683,7 +722,9 @@ __device__ __forceinline__ uint4 cached8(const uint8_t *unit, int half, int j, i
         }
     } else {
         const uint32_t q = __ldg(reinterpret_cast<const uint32_t *>(at));
-        const float s = ue4m3_decode(__ldg(unit + (half == 0 ? u.k_block_scale(j, g / 2) : u.v_block_scale(j, g / 2)))) * gs;
+        uint32_t sh;        // exact, as every E4M3 value is in FP16
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(sh) : "h"(static_cast<uint16_t>(__ldg(scale))));
+        const float s = __low2float(*reinterpret_cast<const __half2 *>(&sh)) * gs;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t h;
@@ -706,15 +747,15 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, g = lane % LANES, sub = lane / LANES;
     const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t t0 = item / p.heads * kReadTokens;
-    const int head = static_cast<int>(item % p.heads);
+    const int64_t block = item / p.heads, t0 = block * kReadTokens;
+    const int head = static_cast<int>(item - block * p.heads);
     if (t0 >= p.T) return;
     float gs[2] = {1.0f, 1.0f};
     if (TYPE == QFP4_CACHE_NVFP4) {
         gs[0] = *p.c.gs[0];
         gs[1] = *p.c.gs[1];
     }
-    int64_t slot[N];
+    int slot[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int64_t t = t0 + i * GROUPS + sub;
@@ -724,16 +765,16 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p
             slot[i] = -1;
         }
     }
+    const CachePlace<TYPE, LANES> k0(0, 0, g), v0(1, 0, g);
     uint4 v[2][N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         v[0][i] = v[1][i] = make_uint4(0, 0, 0, 0);
         if (slot[i] < 0) continue;
-        const int64_t page = slot[i] / p.c.page_size;
-        const int in_page = static_cast<int>(slot[i] - page * p.c.page_size);
-        const uint8_t *unit = p.c.cache + ((page * p.heads + head) * (p.c.page_size / 16) + in_page / 16) * UNIT;
-        v[0][i] = cached8<TYPE, LANES>(unit, 0, in_page & 15, g, gs[0]);
-        v[1][i] = cached8<TYPE, LANES>(unit, 1, in_page & 15, g, gs[1]);
+        const uint8_t *unit = p.c.cache + (p.c.unit_of(slot[i]) + static_cast<int64_t>(head) * p.c.page_units) * UNIT;
+        const TokenPlace<TYPE, LANES> tp(slot[i] & 15);
+        v[0][i] = cached8<TYPE>(unit + k0.code + tp.code[0], unit + k0.scale + tp.scale[0], gs[0]);
+        v[1][i] = cached8<TYPE>(unit + v0.code + tp.code[1], unit + v0.scale + tp.scale[1], gs[1]);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -763,7 +804,7 @@ int64_t plan_blocks(HeadParams &p, int lanes, int vectors, int per_sm)
 template <int LANES, bool INTER>
 int launch_heads(HeadParams &p, int cache, cudaStream_t s)
 {
-    const int64_t grid = plan_blocks(p, LANES, kVectors, kHeadCtas);
+    const int64_t grid = plan_blocks(p, LANES, kVectors, head_ctas(cache));
     auto kernel = cache == kNoCache ? head_kernel<LANES, kNoCache, INTER>
                 : cache == QFP4_CACHE_BF16 ? head_kernel<LANES, QFP4_CACHE_BF16, INTER>
                 : cache == QFP4_CACHE_E4M3 ? head_kernel<LANES, QFP4_CACHE_E4M3, INTER>
@@ -844,7 +885,9 @@ int fill_cache(CacheParams &c, int type, void *cache, int64_t kv_heads, int64_t 
     c.gs[0] = gs_k;
     c.gs[1] = gs_v;
     c.slot_count = pages * page_size;
-    c.page_size = static_cast<int32_t>(page_size);
+    c.page_units = static_cast<int32_t>(page_size / 16);
+    // exact for every unit number below 2^27, at most 2^10 units in a page
+    c.page_magic = ((uint64_t{1} << 37) + c.page_units - 1) / c.page_units;
     c.kv_heads = static_cast<int32_t>(kv_heads);
     return QFP4_OK;
 }
