@@ -1,5 +1,6 @@
 // attention_decode.cu -- entry points of the attention of one new token per
 // sequence over the paged cache (kernel: qfp4_attention.cuh).
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -87,6 +88,9 @@ extern "C" int qfp4_attention_decode(int type, const void *Q_bf16, int64_t ldq, 
     p.counters = static_cast<uint32_t *>(workspace);
     p.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + kCounterBytes);
     if (status_word_attention(&p.status) != QFP4_OK) return QFP4_ERR_CUDA;
+#ifdef QFP4_FAULT_INJECTION
+    p.skip_copy = inject_skip_copy();
+#endif
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (type) {
     case QFP4_CACHE_BF16: return attn_launch_bf16(p, D, nt, kMaxPerSm, s);
@@ -94,3 +98,16 @@ extern "C" int qfp4_attention_decode(int type, const void *Q_bf16, int64_t ldq, 
     default: return attn_launch_nvfp4(p, D, nt, kMaxPerSm, s);
     }
 }
+
+#ifdef QFP4_FAULT_INJECTION
+namespace qfp4 {
+static std::atomic<int> g_skip_copy{0};
+bool inject_skip_copy() { return g_skip_copy.load() != 0; }
+}  // namespace qfp4
+
+extern "C" int qfp4_test_inject_skip_copy(int on)
+{
+    qfp4::g_skip_copy.store(on);
+    return QFP4_OK;
+}
+#endif

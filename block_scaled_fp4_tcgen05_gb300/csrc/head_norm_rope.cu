@@ -441,12 +441,15 @@ struct BackParams {
     __nv_bfloat16 *dx[2];
     int64_t lddx[2];
     float *partial;                     // [gridDim.x][2][D]
+#ifdef QFP4_FAULT_INJECTION
+    bool skip_copy;
+#endif
 };
 
 // The gradient's vectors per group of lanes, and a warp's ring of stages in shared
 // memory, filled by bulk copies: a block of x and one of dy each, 16 bytes per lane,
 // vector and tensor.
-constexpr int kBackVectors = 4, kStages = 3, kHalfStage = 512 * kBackVectors, kStage = 2 * kHalfStage;
+constexpr int kBackVectors = 4, kStages = 2, kHalfStage = 512 * kBackVectors, kStage = 2 * kHalfStage;
 constexpr int kRing = kWarps * kStages * kStage;
 
 // As head_kernel, but the queries of all tokens come before the keys, so that
@@ -500,6 +503,9 @@ __global__ void __launch_bounds__(kThreads, kBackCtas) head_backward_kernel(cons
             const uint32_t bar = bars + 8 * stage, dst = smem_u32(ring) + stage * kStage;
             const int64_t from = static_cast<int64_t>(head) * p.D;
             mbar_arrive_expect_tx(bar, p.norm ? 2 * bytes : bytes);
+#ifdef QFP4_FAULT_INJECTION
+            if (!(q.skip_copy && blockIdx.x == 0 && warp == 0))
+#endif
             bulk_load(dst, q.dy[k] + ahead_t * q.ldy[k] + from, bytes, bar);
             if (p.norm) bulk_load(dst + kHalfStage, p.x[k] + ahead_t * p.ldx[k] + from, bytes, bar);
         }
@@ -559,14 +565,15 @@ __global__ void __launch_bounds__(kThreads, kBackCtas) head_backward_kernel(cons
             if (lane == 0) atomicOr(&g_status_heads, kStatusBadGroup);
         }
         const bool alive = position >= 0;       // uniform over the warp
-        Turn turn = {};
-        if (alive) turn.load<INTER>(p, pl, position, g);
+        Turn turn;      // of row 0, and not used, where there is no position
+        turn.load<INTER>(p, pl, max(position, 0), g);
         const uint64_t back[2] = {f2_neg(turn.s[0]), f2_neg(turn.s[1])};
 #pragma unroll 1
         for (int n = 0; n < run; ++n) {
-            if (!mbar_wait(bars + 8 * stage, phase)) {
+            if (!dead && !mbar_wait(bars + 8 * stage, phase)) {     // what comes out is undefined, but it ends
                 if (lane == 0) atomicOr(&g_status_heads, kStatusTimeout);
                 dead = true;
+                to_issue = 0;
             }
             const uint8_t *buf = ring + stage * kStage + sub * p.D * 2;
             Raw xv[kBackVectors], dv[kBackVectors];
@@ -1067,6 +1074,9 @@ extern "C" int qfp4_qk_norm_rope_backward(const void *QKV_bf16, int64_t ld, int6
         b.dx[1] = b.dx[0] + q_heads * head_dim;
         b.lddx[0] = b.lddx[1] = lddqkv;
         b.partial = static_cast<float *>(workspace);
+#ifdef QFP4_FAULT_INJECTION
+        b.skip_copy = inject_skip_copy();
+#endif
         const int lanes = lanes_of(head_dim);
         const dim3 grid(static_cast<unsigned>(plan_blocks(b.f, lanes, kBackVectors, kBackCtas)));
         auto kernel = lanes == 8 ? (interleaved ? head_backward_kernel<8, true> : head_backward_kernel<8, false>)

@@ -57,6 +57,9 @@ struct AttnParams {
     uint32_t *counters;         // [grid], zero before and after
     float *partial;             // [grid][2] pieces
     uint32_t *status;
+#ifdef QFP4_FAULT_INJECTION
+    bool skip_copy;
+#endif
 };
 
 // Space of a piece in the workspace: o, then m and l of each query.
@@ -70,7 +73,10 @@ constexpr int attn_stage_tokens(int type, int D)
 }
 constexpr int kAttnStages = 2;
 constexpr float kSlack = 8.0f;
-constexpr int attn_ctas(int D, int nt, int warps) { return (D == 256 || nt == 2 ? 8 : 16) / warps; }
+constexpr int attn_ctas(int type, int D, int nt, int warps)
+{
+    return (D == 256 ? (type == QFP4_CACHE_NVFP4 ? 12 : 8) : nt == 2 ? 8 : 16) / warps;
+}
 
 template <int TYPE, int D, int NT, int WARPS_>
 struct AttnCfg {
@@ -248,7 +254,7 @@ struct Cursor {
 }  // namespace attn
 
 template <int TYPE, int D, int NT, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, attn_ctas(D, NT, WARPS)) attention_decode_kernel(const AttnParams p)
+__global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) attention_decode_kernel(const AttnParams p)
 {
     using namespace attn;
     using C = AttnCfg<TYPE, D, NT, WARPS>;
@@ -355,6 +361,9 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(D, NT, WARPS)) attention
         }
         if (lane == 0) mbar_arrive_expect_tx(bars + 8 * stage, n * C::UNIT);
         __syncwarp();
+#ifdef QFP4_FAULT_INJECTION
+        if (p.skip_copy && blockIdx.x == 0 && warp == 0 && lane == 0) return;
+#endif
         if (has) {
             const int64_t unit = (static_cast<int64_t>(u.page) * p.kv_heads + head) * p.page_units + u.place;
             bulk_load(smem_u32(ring + stage * C::STAGE + lane * C::UNIT), p.cache + unit * C::UNIT, C::UNIT, bars + 8 * stage);
@@ -461,9 +470,10 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(D, NT, WARPS)) attention
         int token0 = first + seg_first * TILE + warp * C::TOKENS;
 #pragma unroll 1
         for (int n_tile = 0; n_tile < seg_n; ++n_tile, token0 += TILE) {
-            if (!mbar_wait(bars + 8 * stage, phase)) {
+            if (!dead && !mbar_wait(bars + 8 * stage, phase)) {     // what comes out is undefined, but it ends
                 if (lane == 0) atomicOr(p.status, kStatusTimeout);
                 dead = true;
+                to_issue = 0;
             }
             const uint8_t *buf = ring + stage * C::STAGE;
             const int units = min(UNITS, max(0, (len - token0 + 15) >> 4));

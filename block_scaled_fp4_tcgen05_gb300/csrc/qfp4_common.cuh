@@ -115,4 +115,10 @@ int status_word_fp8_quant(uint32_t **word);
 int status_word_heads(uint32_t **word);
 int status_word_attention(uint32_t **word);
 
+#ifdef QFP4_FAULT_INJECTION
+// Test build: a warp of the attention and of the head norms' gradient leaves out a
+// bulk copy that it then waits for (qfp4_test_inject_skip_copy).
+bool inject_skip_copy();
+#endif
+
 }  // namespace qfp4

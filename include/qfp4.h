@@ -836,9 +836,9 @@ int qfp4_qk_norm_rope_cache(const void *QKV_bf16, int64_t ld, int64_t T, int64_t
  *              without tokens
  *   workspace  DEVICE scratch, 16-byte aligned, of ws_bytes >=
  *              qfp4_attention_decode_workspace_bytes(...), ZERO-FILLED before
- *              its first use; every call leaves its counters at zero again.
- *              One call at a time per workspace, graphs that captured one
- *              included.
+ *              its first use; every call leaves its counters at zero again (zero
+ *              it anew after a reported timeout).  One call at a time per
+ *              workspace, graphs that captured one included.
  * Products and sums in fp32.  The queries enter the products in FP16 (E4M3,
  * NVFP4 cache), scaled so that an element loses bits only 2^28 below the largest
  * of its head; the weights are rounded to FP16 (2^-11 of each, 2^-25 of the
