@@ -18,6 +18,16 @@
 // of K per stage, across the groups' borders.  ldmatrix gives a lane eight
 // neighbouring codes of a block.  The cluster's sums are added through distributed
 // shared memory in a fixed order: results repeat bit for bit.
+//
+// Measured with the weights in HBM: 1 x 14336 x 4096 10.1 us (floor 4.9), 1 x 28672 x
+// 8192 27 us (19.5); more weights add 0.9 of the copy bandwidth, so what is above the
+// floor is the call's beginning and end, about 5 us.  Nine rows of x and more double
+// the products and bind it by instructions: 16 x 28672 x 8192 41 us (NVFP4), 48 us
+// (MXFP4), 2.1 a cycle.  Other forms, 16 and 1 rows of that size (MXFP4): CTAs of eight
+// warps and 128 rows with the CTA's slice of x converted for each 52 and 38 us; the
+// weights by TMA in stages of 128 rows 56 and 43; the line of groups and K shared
+// evenly between the warps 47 and 30 (more work around each stage); a group's K shared
+// by several warps 51 and 31.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -25,16 +35,16 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include "qfp4_attention.cuh"
 #include "qfp4_common.cuh"
 #include "qfp4_fp4_codes.cuh"
+#include "qfp4_lane_ops.cuh"
 #include "sm103_ptx.cuh"
 
 namespace qfp4 {
 
 namespace {
 
-using namespace attn;
+using namespace lane_ops;
 
 constexpr int kStep = 128;              // elements of K that the scales' layout and K go by
 constexpr int kUnit = 256, kUnitSteps = 2;              // elements of K of a stage

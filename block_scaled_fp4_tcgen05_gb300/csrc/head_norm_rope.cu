@@ -15,8 +15,11 @@
 // 8, 16 or 32 lanes hold a vector, eight elements each, in two pieces of four
 // that hold both elements of their pairs (4 g .. and R/2 + 4 g .., or eight
 // neighbours): no lane needs another's elements but for the sums.  The arithmetic
-// is on packed pairs of fp32.  A warp takes one token's heads of a kind one after
-// the other, the next ones' loads ahead, with the angles and weights in registers.
+// is on packed pairs of fp32.  Every warp of one wave walks an equal piece of the
+// line of (token, heads), the next heads' loads ahead, with the angles and weights in
+// registers.  16384 tokens x 40 heads x 128 take 59 us (5.8 TB/s, 0.86 of the copy
+// bandwidth); with a warp for every eight heads that reads them once 74, with the
+// pairs' elements exchanged between lanes 63, through a ring of bulk copies 70.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -172,7 +175,7 @@ struct Turn {
     uint64_t c[2], s[2];
 
     template <bool INTER>
-    __device__ __forceinline__ void load(const HeadParams &p, const Place &pl, int64_t position, int g)
+    __device__ __forceinline__ static Turn of(const HeadParams &p, const Place &pl, int64_t position, int g)
     {
         float4 cv = make_float4(1.0f, 1.0f, 1.0f, 1.0f), sv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (pl.turns) {
@@ -180,10 +183,8 @@ struct Turn {
             cv = __ldg(reinterpret_cast<const float4 *>(row));
             sv = __ldg(reinterpret_cast<const float4 *>(row + p.R / 2));
         }
-        c[0] = INTER ? f2_pack(cv.x, cv.y) : f2_pack(cv.x, cv.z);
-        c[1] = INTER ? f2_pack(cv.z, cv.w) : f2_pack(cv.y, cv.w);
-        s[0] = INTER ? f2_pack(sv.x, sv.y) : f2_pack(sv.x, sv.z);
-        s[1] = INTER ? f2_pack(sv.z, sv.w) : f2_pack(sv.y, sv.w);
+        return INTER ? Turn{{f2_pack(cv.x, cv.y), f2_pack(cv.z, cv.w)}, {f2_pack(sv.x, sv.y), f2_pack(sv.z, sv.w)}}
+                     : Turn{{f2_pack(cv.x, cv.z), f2_pack(cv.y, cv.w)}, {f2_pack(sv.x, sv.z), f2_pack(sv.y, sv.w)}};
     }
 };
 
@@ -374,8 +375,7 @@ __global__ void __launch_bounds__(kThreads, head_ctas(CACHE)) head_kernel(const 
         // y = r (a ac + b bs, b bc + a as), the weights in the cosines and sines
         uint64_t ac[2], as[2], bc[2], bs[2];
         if (kind != kValue) {
-            Turn turn;
-            turn.load<INTER>(p, pl, position, g);
+            const Turn turn = Turn::of<INTER>(p, pl, position, g);
             Raw wr = ones();
             if (p.w[kind] && lane_in) wr = pl.load(p.w[kind]);
             const Eight w = unpack<INTER>(wr);
@@ -455,10 +455,10 @@ constexpr int kRing = kWarps * kStages * kStage;
 // As head_kernel, but the queries of all tokens come before the keys, so that
 // nearly every warp sums the weights' gradient of one kind; and with the loads
 // through a ring.  What bounds it is the chain of each vector's sums and roots: four
-// vectors at a time with two CTAs per SM take 96 us for 16384 tokens x 40 heads x
-// 128 (5.3 TB/s, 0.78 of the copy bandwidth), two at a time 112, and 143 with
-// three CTAs, whose registers do not suffice; loads into registers instead of the
-// ring 116.
+// vectors at a time with two CTAs per SM take 95 us for 16384 tokens x 40 heads x
+// 128 (5.4 TB/s, 0.79 of the copy bandwidth), two at a time 112, eight 114, and 143
+// with three CTAs, whose registers do not suffice; loads into registers instead of
+// the ring 116.
 template <int LANES, bool INTER>
 __global__ void __launch_bounds__(kThreads, kBackCtas) head_backward_kernel(const BackParams q)
 {
@@ -565,8 +565,7 @@ __global__ void __launch_bounds__(kThreads, kBackCtas) head_backward_kernel(cons
             if (lane == 0) atomicOr(&g_status_heads, kStatusBadGroup);
         }
         const bool alive = position >= 0;       // uniform over the warp
-        Turn turn;      // of row 0, and not used, where there is no position
-        turn.load<INTER>(p, pl, max(position, 0), g);
+        const Turn turn = Turn::of<INTER>(p, pl, max(position, 0), g);      // not used without a position
         const uint64_t back[2] = {f2_neg(turn.s[0]), f2_neg(turn.s[1])};
 #pragma unroll 1
         for (int n = 0; n < run; ++n) {
@@ -688,7 +687,8 @@ struct ReadParams {
     int64_t ldo[2];
 };
 
-// A warp takes four tokens of one head: where their slots follow one another
+// A warp takes four tokens of one head (32768 tokens x 8 heads x 128 in NVFP4: 36 us,
+// floor 25; eight tokens 40, sixteen 62): where their slots follow one another
 // (a prefix), every 32-byte sector that it reads is used whole.
 constexpr int kReadTokens = 4;
 

@@ -2,9 +2,10 @@
 // cache (see qfp4_kv_cache.cuh for the cache's layout).  One translation unit
 // per cache type instantiates the kernel.
 //
-//   x_j = scale q . k_j (in units of log 2),  p_j = 2^(x_j - m),  m = max x_j,
+//   x_j = scale q . k_j (in units of log 2),  p_j = 2^(x_j - m),
 //   o = sum p_j v_j / sum p_j,  lse = ln 2 (m + log2 sum p_j)
-// in one pass over the cache, with the running m, sums and o in fp32 registers.
+// in one pass over the cache, with m (the largest x_j, or up to kSlack below it), the
+// sums and o in fp32 registers.
 //
 // Bound by the cache's bytes.  A warp takes 16 tokens as the rows of a tensor
 // core product with up to 8 (or 16) query heads that share the key head as its
@@ -16,9 +17,9 @@
 // become FP16 too, each multiplied by the power of two that takes its largest
 // element to [2^14, 2^15): what lies 2^28 below that loses bits, 2^-39 of the
 // largest at most.  p is rounded to FP16 (2^-11 of it at most); an E4M3 token's value
-// scale s joins it as 2^(x + log2 s - m'), m' the maximum of that exponent, so
-// that no range of scales is lost.  With a BF16 cache the operands are BF16 and p is the sum
-// of two (2^-16).
+// scale s joins it as 2^(x + log2 s - m'), m' the like of m for that exponent, so that
+// no range of scales is lost.  With a BF16 cache the operands are BF16 and p is the
+// sum of two (2^-16).
 //
 // The tokens of all sequences and heads are one line of tiles; each CTA takes an
 // equal piece of it, whatever the lengths, and the pieces of a head that lies
@@ -26,6 +27,16 @@
 // pieces: results repeat bit for bit.  Each warp brings its own tokens with bulk
 // copies into a ring of stages of its own, ahead of the tile that it works on and
 // across the heads' borders; no other warp waits for it until a head ends.
+//
+// Measured (of the copy bandwidth, head_dim 128): BF16 64 ragged sequences of up to
+// 8192 x 8 heads 185 us (0.91), E4M3 105 us (0.83); NVFP4 4 x 131072 x 8 heads 125 us
+// (0.71).  What is left of NVFP4 are instructions: a unit of 16 tokens takes about 330,
+// 64 conversions and 64 multiplications by scales among them, at 2.4 a cycle.  16 warps
+// per SM of 128 registers beat 12 of 168 (131 us against 159 at that time); stages of
+// 64 tokens, which halve the work around each, leave room for 12 warps only (147 us).
+// Short calls are a chain of latencies: length, page number, tokens, first products,
+// warps' join, pieces' join; 1 x 4096 tokens x 8 heads take 10.5 us, 3 of them the
+// pieces'.
 #pragma once
 
 #include <atomic>
@@ -36,6 +47,7 @@
 
 #include "qfp4_common.cuh"
 #include "qfp4_kv_cache.cuh"
+#include "qfp4_lane_ops.cuh"
 #include "sm103_ptx.cuh"
 
 namespace qfp4 {
@@ -96,19 +108,7 @@ struct AttnCfg {
 
 namespace attn {
 
-__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
+using namespace lane_ops;
 
 template <int TYPE>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -116,94 +116,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
     if constexpr (TYPE == QFP4_CACHE_BF16) mma_bf16(c, a, b0, b1);
     else mma_f16(c, a, b0, b1);
 }
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
-{
-    uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
-    return r;
-}
-
-// Two E2M1 codes (byte I of w) as FP16, the low code in the low half.
-template <int I>
-__device__ __forceinline__ uint32_t fp4x2(uint32_t w)
-{
-    uint32_t r;
-    if constexpr (I == 0)
-        asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %1;\ncvt.rn.f16x2.e2m1x2 %0, a;\n}" : "=r"(r) : "r"(w));
-    else if constexpr (I == 1)
-        asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %1;\ncvt.rn.f16x2.e2m1x2 %0, b;\n}" : "=r"(r) : "r"(w));
-    else if constexpr (I == 2)
-        asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %1;\ncvt.rn.f16x2.e2m1x2 %0, c;\n}" : "=r"(r) : "r"(w));
-    else
-        asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %1;\ncvt.rn.f16x2.e2m1x2 %0, d;\n}" : "=r"(r) : "r"(w));
-    return r;
-}
-
-// Two E4M3 codes (half I of w) as FP16.
-template <int I>
-__device__ __forceinline__ uint32_t fp8x2(uint32_t w)
-{
-    uint32_t r;
-    if constexpr (I == 0)
-        asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %1;\ncvt.rn.f16x2.e4m3x2 %0, a;\n}" : "=r"(r) : "r"(w));
-    else
-        asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %1;\ncvt.rn.f16x2.e4m3x2 %0, b;\n}" : "=r"(r) : "r"(w));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ float log2_fast(float x)
-{
-    float r;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// The larger one; NaN where either is: a NaN must not pass for "no token".
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-// 2^e for -126 <= e <= 127
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // Where a CTA stands on the line of tiles: sequence, (key head, query block) and tile.
 struct Cursor {
