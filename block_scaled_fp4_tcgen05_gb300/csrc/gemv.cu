@@ -69,7 +69,7 @@ template <int FMT, int NT>
 struct GemvCfg {
     static constexpr int COLS4 = FMT == QFP4_NVFP4 ? 2 : 1;         // tiles of four scale columns per step
     static constexpr int ROWS = 16 * kUnit / 2, STAGE = ROWS + kUnitSteps * COLS4 * 64;
-    // 24 warps of 80 registers are no faster than 16 (1 x 28672 x 8192: 32 us, 29)
+    // 24 warps of 80 registers are no faster than 16 (1 x 28672 x 8192: 32 us, 29 at that time)
     static constexpr int WARPS = 16, THREADS = 32 * WARPS, STAGES = 3;
     static constexpr int PITCH = (kSlice + 32) * 2;                 // bytes of a row of x: two rows fall on different halves of the banks
     static constexpr int RING = WARPS * STAGES * STAGE;

@@ -687,7 +687,7 @@ struct ReadParams {
     int64_t ldo[2];
 };
 
-// A warp takes four tokens of one head (32768 tokens x 8 heads x 128 in NVFP4: 36 us,
+// A warp takes four tokens of one head (32768 tokens x 8 heads x 128 in NVFP4: 35 us,
 // floor 25; eight tokens 40, sixteen 62): where their slots follow one another
 // (a prefix), every 32-byte sector that it reads is used whole.
 constexpr int kReadTokens = 4;

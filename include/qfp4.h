@@ -692,7 +692,7 @@ int qfp4_moe_route_backward(int logits_type, const void *logits, int64_t T, int6
  * repeat bit for bit.
  * Accuracy: |D - exact| <= 2^-8 |exact| + (K/16 + 16) 2^-23 sum_k |x_k w_k| +
  * 2^-33 max|x| sum_k |w_k| (elements of x below 2^-22 of their row's largest in
- * a slice of 1024 lose bits), where no sum leaves fp32's range (scales up to
+ * a slice of 512 lose bits), where no sum leaves fp32's range (scales up to
  * 2^100). */
 int qfp4_gemv_nt(int fmt, int64_t M, int64_t N, int64_t K, const void *X_bf16, int64_t ldx,
                  const void *W_packed, const void *W_sf, const float *gs_w, void *D_bf16, int64_t ldd,
@@ -726,7 +726,8 @@ int qfp4_gemv_nt(int fmt, int64_t M, int64_t N, int64_t K, const void *X_bf16, i
  * <= 256, at most 4096 heads of a kind, T <= 2^30, eps >= 0 and finite, ld, ldq,
  * ldk multiples of 8, the last a row's length at least; positions 4-byte
  * aligned, the rest 16-byte.  T == 0 launches nothing.
- * Accuracy: |y - exact| <= 2^-8 |exact| + 2^-20 (|z_a| + |z_b|) of the pair. */
+ * Accuracy: |y - exact| <= 2^-8 |exact| + 2^-20 (|z_a| + |z_b|) of the pair, where
+ * the head vector's sum of squares stays within fp32 (2^-126 to 2^127). */
 int qfp4_qk_norm_rope(const void *QKV_bf16, int64_t ld, int64_t T, int64_t q_heads, int64_t kv_heads,
                       int64_t head_dim, const void *q_weight, const void *k_weight, float eps,
                       const float *cos_sin, int64_t table_rows, int64_t rotary_dim, int interleaved,
@@ -843,6 +844,8 @@ int qfp4_qk_norm_rope_cache(const void *QKV_bf16, int64_t ld, int64_t T, int64_t
  * NVFP4 cache), scaled so that an element loses bits only 2^28 below the largest
  * of its head; the weights are rounded to FP16 (2^-11 of each, 2^-25 of the
  * largest at least) or, with a BF16 cache, to 16 bits.  Results repeat bit for bit.
+ * An infinite value that counts gives NaN (a weight times it is added in two parts),
+ * as infinite logits do.
  * Requirements: cache sizes as above, q_heads a multiple of kv_heads, at most
  * 4096, B <= 2^20, max_pages * page_size <= 2^30, ldq a multiple of 8, Q / cache /
  * O / workspace 16-byte aligned, the rest 4-byte.  B == 0 launches nothing. */

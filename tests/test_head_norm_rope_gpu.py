@@ -79,7 +79,7 @@ def forward64(s, H, KV, D, R, inter):
 
 
 SHAPES = [  # T, H, KV, D, R
-    (1, 1, 1, 64, 64), (3, 5, 1, 64, 32), (7, 8, 8, 128, 128), (64, 32, 8, 128, 128), (33, 3, 2, 96, 96), (9, 7, 1, 80, 16), (5, 4, 2, 192, 64),
+    (1, 1, 1, 64, 64), (3, 5, 1, 64, 32), (7, 9, 9, 128, 128), (64, 32, 8, 128, 128), (33, 3, 2, 96, 96), (9, 7, 1, 80, 16), (5, 4, 2, 192, 64),
     (17, 6, 2, 256, 256), (2, 16, 1, 256, 240), (40, 2, 1, 16, 16), (11, 9, 3, 112, 112), (6, 4, 4, 128, 0), (300, 12, 4, 48, 32),
 ]
 
