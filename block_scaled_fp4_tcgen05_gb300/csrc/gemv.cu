@@ -22,7 +22,7 @@
 // Measured with the weights in HBM: 1 x 14336 x 4096 10.1 us (floor 4.9), 1 x 28672 x
 // 8192 27 us (19.5); more weights add 0.9 of the copy bandwidth, so what is above the
 // floor is the call's beginning and end, about 5 us.  Nine rows of x and more double
-// the products and bind it by instructions: 16 x 28672 x 8192 41 us (NVFP4), 48 us
+// the products and bind it by instructions: 16 x 28672 x 8192 41 us (NVFP4), 43 us
 // (MXFP4), 2.1 a cycle.  Other forms, 16 and 1 rows of that size (MXFP4): CTAs of eight
 // warps and 128 rows with the CTA's slice of x converted for each 52 and 38 us; the
 // weights by TMA in stages of 128 rows 56 and 43; the line of groups and K shared
@@ -50,7 +50,7 @@ constexpr int kStep = 128;              // elements of K that the scales' layout
 constexpr int kUnit = 256, kUnitSteps = 2;              // elements of K of a stage
 constexpr int kSlice = 512, kSliceUnits = 2;            // of x with a scale of their own
 constexpr int kRowSlices = 64;          // slices of rows of x in shared memory at once
-constexpr int kGroups = 32;             // groups of 16 rows whose sums are
+constexpr int kGroups = 48;             // groups of 16 rows whose sums are
 constexpr int kMaxRowsX = 16, kMaxSplits = 8;
 
 struct GemvParams {
@@ -69,7 +69,8 @@ template <int FMT, int NT>
 struct GemvCfg {
     static constexpr int COLS4 = FMT == QFP4_NVFP4 ? 2 : 1;         // tiles of four scale columns per step
     static constexpr int ROWS = 16 * kUnit / 2, STAGE = ROWS + kUnitSteps * COLS4 * 64;
-    // 24 warps of 80 registers are no faster than 16 (1 x 28672 x 8192: 32 us, 29 at that time)
+    // 24 warps of 80 registers are no faster than 16 (1 x 28672 x 8192: 32 us, 29 at that
+    // time), nor 12 of 168 (16 x 28672 x 8192 MXFP4: 46 us, 44)
     static constexpr int WARPS = 16, THREADS = 32 * WARPS, STAGES = 3;
     static constexpr int PITCH = (kSlice + 32) * 2;                 // bytes of a row of x: two rows fall on different halves of the banks
     static constexpr int RING = WARPS * STAGES * STAGE;
@@ -275,12 +276,15 @@ __global__ void __launch_bounds__(GemvCfg<FMT, NT>::THREADS, 1) gemv_kernel(cons
                 for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = 0;
 #pragma unroll 1
                 for (int slice = 0; slice * kSliceUnits < n_units; ++slice) {
-                    // of the slice, whose x has one scale: a chain for each step of a unit
-                    float sum[2][NT][4];
+                    // of the slice, whose x has one scale: for NVFP4 a chain of products for
+                    // each step of a unit; MXFP4's blocks are chains of their own (one sum
+                    // and packed fp32 44 us for 16 x 28672 x 8192, two sums 46)
+                    constexpr int SUMS_OF = FMT == QFP4_NVFP4 ? 2 : 1;
+                    float sum[SUMS_OF][NT][4];
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) sum[0][n][k] = sum[1][n][k] = 0.0f;
+                        for (int k = 0; k < 4; ++k) sum[0][n][k] = sum[SUMS_OF - 1][n][k] = 0.0f;
                     const uint8_t *xb = xs + (slice * p.M + g) * C::PITCH + 16 * t;      // rows that x does not have: columns that nobody reads
                     const int last = min(kSliceUnits, n_units - slice * kSliceUnits);
 #pragma unroll 1
@@ -338,8 +342,8 @@ __global__ void __launch_bounds__(GemvCfg<FMT, NT>::THREADS, 1) gemv_kernel(cons
                                     }
 #pragma unroll
                                     for (int n = 0; n < NT; ++n) {
-                                        mma_f16(sum[s][n], a[0], x[n].x, x[n].y);
-                                        mma_f16(sum[s][n], a[1], x[n].z, x[n].w);
+                                        mma_f16(sum[s % SUMS_OF][n], a[0], x[n].x, x[n].y);
+                                        mma_f16(sum[s % SUMS_OF][n], a[1], x[n].z, x[n].w);
                                     }
                                 } else {
 #pragma unroll
@@ -347,10 +351,11 @@ __global__ void __launch_bounds__(GemvCfg<FMT, NT>::THREADS, 1) gemv_kernel(cons
                                         float block[4];
                                         mma_f16_zero(block, a[0], x[n].x, x[n].y);
                                         mma_f16(block, a[1], x[n].z, x[n].w);
-                                        sum[s][n][0] = fmaf(f[c][0], block[0], sum[s][n][0]);
-                                        sum[s][n][1] = fmaf(f[c][0], block[1], sum[s][n][1]);
-                                        sum[s][n][2] = fmaf(f[c][1], block[2], sum[s][n][2]);
-                                        sum[s][n][3] = fmaf(f[c][1], block[3], sum[s][n][3]);
+                                        float *d = sum[0][n];
+                                        const uint64_t lo = f2_fma(f2_pack(f[c][0], f[c][0]), f2_pack(block[0], block[1]), f2_pack(d[0], d[1]));
+                                        const uint64_t hi = f2_fma(f2_pack(f[c][1], f[c][1]), f2_pack(block[2], block[3]), f2_pack(d[2], d[3]));
+                                        f2_unpack(lo, d[0], d[1]);
+                                        f2_unpack(hi, d[2], d[3]);
                                     }
                                 }
                             }
@@ -364,8 +369,11 @@ __global__ void __launch_bounds__(GemvCfg<FMT, NT>::THREADS, 1) gemv_kernel(cons
                         const float *b = s_back + slice * p.M + 8 * n + 2 * t;
                         const uint64_t b2 = f2_pack(b[0], b[1]);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            acc[n][h] = f2_fma(f2_add(f2_pack(sum[0][n][2 * h], sum[0][n][2 * h + 1]), f2_pack(sum[1][n][2 * h], sum[1][n][2 * h + 1])), b2, acc[n][h]);
+                        for (int h = 0; h < 2; ++h) {
+                            uint64_t v = f2_pack(sum[0][n][2 * h], sum[0][n][2 * h + 1]);
+                            if constexpr (SUMS_OF == 2) v = f2_add(v, f2_pack(sum[1][n][2 * h], sum[1][n][2 * h + 1]));
+                            acc[n][h] = f2_fma(v, b2, acc[n][h]);
+                        }
                     }
                 }
                 // this lane's places of the group's sums: its own in every pass over K
