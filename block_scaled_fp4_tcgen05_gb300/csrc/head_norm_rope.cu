@@ -17,7 +17,7 @@
 // neighbours): no lane needs another's elements but for the sums.  The arithmetic
 // is on packed pairs of fp32.  Every warp of one wave walks an equal piece of the
 // line of (token, heads), the next heads' loads ahead, with the angles and weights in
-// registers.  16384 tokens x 40 heads x 128 take 59 us (5.8 TB/s, 0.86 of the copy
+// registers.  16384 tokens x 40 heads x 128 take 58 us (5.9 TB/s, 0.87 of the copy
 // bandwidth); with a warp for every eight heads that reads them once 74, with the
 // pairs' elements exchanged between lanes 63, through a ring of bulk copies 70.
 #include <cstdint>
@@ -28,6 +28,7 @@
 #include "qfp4_common.cuh"
 #include "qfp4_fp4_codes.cuh"
 #include "qfp4_kv_cache.cuh"
+#include "qfp4_lane_ops.cuh"
 #include "sm103_ptx.cuh"
 
 namespace qfp4 {
@@ -71,6 +72,7 @@ struct HeadParams {
     int64_t T, table_rows;
     int32_t heads[3];
     int32_t blocks[3];          // of each kind in a token; a block is what a warp works on at a time
+    uint32_t share, more;       // blocks of a warp; so many first warps have one more
     int32_t D, R, interleaved, norm;
     float eps, inv_D;
     CacheParams c;
@@ -290,17 +292,17 @@ constexpr int kHeadCtas = 4, kCacheCtas = 2, kBackCtas = 2;
 constexpr int head_ctas(int cache) { return cache == kNoCache ? kHeadCtas : kCacheCtas; }
 
 // Piece of the line of (token, block of heads of a kind) that a warp takes: as
-// many blocks for each, whatever the tokens and heads.
+// many blocks for each, whatever the tokens and heads.  In 32 bits, and divided on the
+// host: three 64-bit divisions per warp cost 0.6 us of a short call.
 struct Piece {
-    int64_t begin;
+    uint32_t begin;
     int count;
 
-    __device__ __forceinline__ Piece(int64_t items)
+    __device__ __forceinline__ explicit Piece(const HeadParams &p)
     {
-        const int64_t warps = static_cast<int64_t>(gridDim.x) * kWarps;
-        const int64_t w = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-        begin = w * items / warps;
-        count = static_cast<int>((w + 1) * items / warps - begin);
+        const uint32_t w = blockIdx.x * kWarps + (threadIdx.x >> 5);
+        begin = w * p.share + min(w, p.more);
+        count = static_cast<int>(p.share + (w < p.more));
     }
 };
 
@@ -311,12 +313,13 @@ __global__ void __launch_bounds__(kThreads, head_ctas(CACHE)) head_kernel(const 
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, g = lane % LANES, sub = lane / LANES;
-    const int per_token = p.blocks[0] + p.blocks[1] + p.blocks[2];
-    const Piece piece(p.T * per_token);
+    const uint32_t per_token = p.blocks[0] + p.blocks[1] + p.blocks[2];
+    const Piece piece(p);
     if (piece.count == 0) return;
     const bool lane_in = 8 * g < p.D;
-    int64_t t = piece.begin / per_token;
-    int block = static_cast<int>(piece.begin - t * per_token);
+    const uint32_t t_first = piece.begin / per_token;
+    int64_t t = t_first;
+    int block = static_cast<int>(piece.begin - t_first * per_token);
     int position_next = p.positions ? p.positions[t] : 0;
     int slot_next = CACHE != kNoCache ? p.c.slots[t] : 0;
     float gs[2] = {1.0f, 1.0f}, inv_gs[2] = {1.0f, 1.0f};
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, head_ctas(CACHE)) head_kernel(const 
         int position = position_next, slot = slot_next;
         const int64_t tok = t;
         block += run;
-        if (block == per_token) {
+        if (block == static_cast<int>(per_token)) {
             block = 0;
             if (++t < p.T) {
                 position_next = p.positions ? p.positions[t] : 0;
@@ -455,10 +458,10 @@ constexpr int kRing = kWarps * kStages * kStage;
 // As head_kernel, but the queries of all tokens come before the keys, so that
 // nearly every warp sums the weights' gradient of one kind; and with the loads
 // through a ring.  What bounds it is the chain of each vector's sums and roots: four
-// vectors at a time with two CTAs per SM take 95 us for 16384 tokens x 40 heads x
-// 128 (5.4 TB/s, 0.79 of the copy bandwidth), two at a time 112, eight 114, and 143
-// with three CTAs, whose registers do not suffice; loads into registers instead of
-// the ring 116.
+// vectors at a time with two CTAs per SM take 93 us for 16384 tokens x 40 heads x
+// 128 (5.5 TB/s, 0.81 of the copy bandwidth); before a step that took 2 us off, two at
+// a time 112, eight 114, 143 with three CTAs, whose registers do not suffice, and 116
+// with loads into registers instead of the ring.
 template <int LANES, bool INTER>
 __global__ void __launch_bounds__(kThreads, kBackCtas) head_backward_kernel(const BackParams q)
 {
@@ -478,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, kBackCtas) head_backward_kernel(cons
     __syncwarp();
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t items_q = p.T * p.blocks[0];
-    const Piece piece(items_q + p.T * p.blocks[1]);
+    const uint32_t items_q = static_cast<uint32_t>(p.T * p.blocks[0]);
+    const Piece piece(p);
     const bool lane_in = 8 * g < p.D;
     const Place pl = Place::of<LANES, INTER>(p, g, false);
     if (p.norm && sub == 0) {       // by the lanes that add the warp's sums later
@@ -489,9 +492,9 @@ __global__ void __launch_bounds__(kThreads, kBackCtas) head_backward_kernel(cons
             for (int e = 0; e < 8; ++e) s_dw[warp][k][8 * g + e] = 0.0f;
     }
     int kind = piece.begin >= items_q ? kKey : kQuery;
-    const int64_t in_kind = kind == kKey ? piece.begin - items_q : piece.begin;
-    int64_t t = in_kind / p.blocks[kind];
-    int block = static_cast<int>(in_kind - t * p.blocks[kind]);
+    const uint32_t in_kind = kind == kKey ? piece.begin - items_q : piece.begin, t_first = in_kind / p.blocks[kind];
+    int64_t t = t_first;
+    int block = static_cast<int>(in_kind - t_first * p.blocks[kind]);
 
     // ---- the ring's producer: the same walk, ahead
     int64_t ahead_t = t;
@@ -677,20 +680,123 @@ __global__ void __launch_bounds__(1024) head_weight_kernel(const float *partial,
     if (out) out[column < D ? column : column - D] = v;
 }
 
+// ------------------------------------------------------------ cache's write
+
+struct WriteParams {
+    CacheParams c;
+    const __nv_bfloat16 *in[2];     // K, V
+    int64_t ld[2];
+    uint32_t vectors, heads;        // vectors: tokens * heads
+};
+
+// N neighbouring bytes of codes, N = 4, 8 or 16, from the registers that hold them.
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t *at, const uint32_t *w)
+{
+    if constexpr (N == 4) *reinterpret_cast<uint32_t *>(at) = w[0];
+    else if constexpr (N == 8) *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A lane takes 16 elements of a token's key and value vector of a head: a block of
+// NVFP4 whole, so that its scale, as much work as its codes, is found once: 32768 tokens
+// x 8 heads x 128 take 40 us in NVFP4 (floor 25; bound by the quotients' instructions),
+// 32 in E4M3 (30) and 55 in BF16 (40; the pieces of 16 and 64 bytes); head_kernel, whose
+// lanes hold eight elements, takes 99, 71 and 75.
+template <int TYPE, int LANES>
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteParams p)
+{
+    constexpr int D = 16 * LANES, GROUPS = 32 / LANES;
+    constexpr CacheUnit U(TYPE, D);
+    constexpr int CODES = U.row / LANES, WORDS = CODES / 4;         // of a lane
+    constexpr int V_RUN = CODES < 16 ? (U.row / 8 < CODES ? U.row / 8 : CODES) : (U.row / 8 < 16 ? U.row / 8 : 16);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31, g = lane % LANES;
+    const uint32_t first = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * GROUPS, mine = first + lane / LANES;
+    if (first >= p.vectors) return;
+    const uint32_t v = min(mine, p.vectors - 1), t = v / p.heads, head = v - t * p.heads;
+    int slot = p.c.slots[t];
+    uint4 x[2][2];
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            x[half][i] = reinterpret_cast<const uint4 *>(p.in[half] + t * p.ld[half] + static_cast<int64_t>(head) * D + 16 * g)[i];
+    float gs[2] = {1.0f, 1.0f};
+    if (TYPE == QFP4_CACHE_NVFP4) {
+        gs[0] = *p.c.gs[0];
+        gs[1] = *p.c.gs[1];
+    }
+    if (slot >= p.c.slot_count) {
+        if (g == 0) atomicOr(&g_status_heads, kStatusBadGroup);
+        slot = -1;
+    }
+    const bool live = mine < p.vectors && slot >= 0;
+    slot = max(slot, 0);
+    uint8_t *unit = p.c.cache + (p.c.unit_of(slot) + static_cast<int64_t>(head) * p.c.page_units) * U.bytes;
+    const int j = slot & 15;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint32_t w[8] = {x[half][0].x, x[half][0].y, x[half][0].z, x[half][0].w,
+                               x[half][1].x, x[half][1].y, x[half][1].z, x[half][1].w};
+        uint32_t code[WORDS];
+        uint8_t *const k_at = unit + U.k_code(j, g * CODES);
+        if constexpr (TYPE == QFP4_CACHE_BF16) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) code[i] = w[i];
+        } else {
+            float y[16], amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                y[2 * i] = bf16_lo(w[i]);
+                y[2 * i + 1] = bf16_hi(w[i]);
+                amax = fmaxf(amax, fmaxf(fabsf(y[2 * i]), fabsf(y[2 * i + 1])));
+            }
+            if constexpr (TYPE == QFP4_CACHE_E4M3) {
+                const float a = fmaxf(group_max<LANES>(amax), kFloor), inv = __fdiv_rn(448.0f, a);
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i)
+                    code[i] = e4m3x2(y[4 * i] * inv, y[4 * i + 1] * inv) | (e4m3x2(y[4 * i + 2] * inv, y[4 * i + 3] * inv) << 16);
+                if (live && g == 0) *reinterpret_cast<float *>(unit + (half == 0 ? U.k_token_scale(j) : U.v_token_scale(j))) = __fdiv_rn(a, 448.0f);
+            } else {
+                const BlockScale b = block_scale<QFP4_NVFP4>(amax, gs[half], __frcp_rn(gs[half]));
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i) code[i] = encode8_f32<QFP4_NVFP4>(y + 8 * i, b);
+                if (live) unit[half == 0 ? U.k_block_scale(j, g) : U.v_block_scale(j, g)] = static_cast<uint8_t>(b.code);
+            }
+        }
+        if (!live) continue;
+        if (half == 0) {
+            constexpr int RUN = CODES < 16 ? CODES : 16;
+#pragma unroll
+            for (int i = 0; i < CODES; i += RUN) store_codes<RUN>(k_at + i, code + i / 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < CODES; i += V_RUN) store_codes<V_RUN>(unit + U.v_code(j, g * CODES + i), code + i / 4);
+        }
+    }
+}
+
 // ------------------------------------------------------------- cache's read
 
 struct ReadParams {
     CacheParams c;
     int64_t T;
-    int32_t heads;
+    uint32_t heads, warp_heads, parts;      // heads that a warp takes, and how many such parts there are
     __nv_bfloat16 *out[2];      // K, V
     int64_t ldo[2];
 };
 
-// A warp takes four tokens of one head (32768 tokens x 8 heads x 128 in NVFP4: 35 us,
-// floor 25; eight tokens 40, sixteen 62): where their slots follow one another
-// (a prefix), every 32-byte sector that it reads is used whole.
-constexpr int kReadTokens = 4;
+// A warp takes four tokens and as many heads as leave 48 warps for each SM: what a
+// token's place costs is paid once for them (32768 tokens x 8 heads x 128 in NVFP4:
+// 31 us, floor 25; a warp for each head, without the next head's loads ahead, 36; as many
+// registers as five CTAs per SM have 40).  Where the tokens' slots follow one
+// another (a prefix), every 32-byte sector of codes that it reads is used whole.
+constexpr int kReadVectors = 2, kReadWarps = 48 * 152, kReadCtas = 4;
+
+// Tokens of a warp: two for each group of lanes that holds a vector.
+__host__ __device__ constexpr int read_tokens(int lanes) { return 32 / lanes * kReadVectors; }
 
 // The places of a token's codes and scales in a unit are those of token 0, which a
 // lane knows, plus what depends on the token alone.
@@ -710,87 +816,117 @@ struct TokenPlace {
     }
 };
 
+// Eight elements of a vector as they lie in the cache.
 template <int TYPE>
-__device__ __forceinline__ uint4 cached8(const uint8_t *at, const uint8_t *scale, float gs)
-{
-    if (TYPE == QFP4_CACHE_BF16) return __ldg(reinterpret_cast<const uint4 *>(at));
-    float y[8];
-    if (TYPE == QFP4_CACHE_E4M3) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2 *>(at));
-        const float s = __ldg(reinterpret_cast<const float *>(scale));
-        const uint32_t w[2] = {q.x, q.y};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t h;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)))));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            y[2 * i] = f.x * s;
-            y[2 * i + 1] = f.y * s;
-        }
-    } else {
-        const uint32_t q = __ldg(reinterpret_cast<const uint32_t *>(at));
-        uint32_t sh;        // exact, as every E4M3 value is in FP16
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(sh) : "h"(static_cast<uint16_t>(__ldg(scale))));
-        const float s = __low2float(*reinterpret_cast<const __half2 *>(&sh)) * gs;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t h;
-            asm("{\n.reg .b8 x0, x1, x2, x3;\nmov.b32 {x0, x1, x2, x3}, %1;\ncvt.rn.f16x2.e2m1x2 %0, x0;\n}"
-                : "=r"(h) : "r"(q >> (8 * i)));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            y[2 * i] = f.x * s;
-            y[2 * i + 1] = f.y * s;
+struct Cached {
+    uint32_t code[TYPE == QFP4_CACHE_BF16 ? 4 : TYPE == QFP4_CACHE_E4M3 ? 2 : 1], scale;
+
+    __device__ __forceinline__ void load(const uint8_t *at, const uint8_t *s)
+    {
+        if constexpr (TYPE == QFP4_CACHE_BF16) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(at));
+            code[0] = v.x, code[1] = v.y, code[2] = v.z, code[3] = v.w;
+        } else if constexpr (TYPE == QFP4_CACHE_E4M3) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(at));
+            code[0] = v.x, code[1] = v.y;
+            scale = __ldg(reinterpret_cast<const uint32_t *>(s));
+        } else {
+            code[0] = __ldg(reinterpret_cast<const uint32_t *>(at));
+            scale = __ldg(s);
         }
     }
-    return pack8(y);
-}
+    __device__ __forceinline__ uint4 bf16(float gs) const
+    {
+        if constexpr (TYPE == QFP4_CACHE_BF16) {
+            return make_uint4(code[0], code[1], code[2], code[3]);
+        } else {
+            uint32_t h[4];      // FP16 holds E2M1 and E4M3 values as they are
+            float f;
+            if constexpr (TYPE == QFP4_CACHE_E4M3) {
+                f = __uint_as_float(scale);
+                h[0] = lane_ops::fp8x2<0>(code[0]), h[1] = lane_ops::fp8x2<1>(code[0]);
+                h[2] = lane_ops::fp8x2<0>(code[1]), h[3] = lane_ops::fp8x2<1>(code[1]);
+            } else {
+                const uint32_t sh = lane_ops::fp8x2<0>(scale);
+                f = __low2float(*reinterpret_cast<const __half2 *>(&sh)) * gs;
+                h[0] = lane_ops::fp4x2<0>(code[0]), h[1] = lane_ops::fp4x2<1>(code[0]);
+                h[2] = lane_ops::fp4x2<2>(code[0]), h[3] = lane_ops::fp4x2<3>(code[0]);
+            }
+            const uint64_t f2 = f2_pack(f, f);
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 c = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+                f2_unpack(f2_mul(f2_pack(c.x, c.y), f2), y[2 * i], y[2 * i + 1]);
+            }
+            return pack8(y);
+        }
+    }
+};
 
 template <int TYPE, int LANES>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p)
+__global__ void __launch_bounds__(kThreads, kReadCtas) cache_read_kernel(const ReadParams p)
 {
-    constexpr int GROUPS = 32 / LANES, N = kReadTokens / GROUPS;
+    constexpr int GROUPS = 32 / LANES, N = kReadVectors;
     constexpr int D = 8 * LANES, UNIT = cache_unit_bytes(TYPE, D);
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, g = lane % LANES, sub = lane / LANES;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t block = item / p.heads, t0 = block * kReadTokens;
-    const int head = static_cast<int>(item - block * p.heads);
+    const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5), block = item / p.parts;
+    const int64_t t0 = static_cast<int64_t>(block) * read_tokens(LANES);
     if (t0 >= p.T) return;
+    const uint32_t head0 = (item - block * p.parts) * p.warp_heads;
+    int heads = static_cast<int>(min(p.heads - head0, p.warp_heads));
     float gs[2] = {1.0f, 1.0f};
     if (TYPE == QFP4_CACHE_NVFP4) {
         gs[0] = *p.c.gs[0];
         gs[1] = *p.c.gs[1];
     }
-    int slot[N];
+    const CachePlace<TYPE, LANES> k0(0, 0, g), v0(1, 0, g);
+    const uint8_t *unit[N];     // NULL: none
+    int code[2][N], scale[2][N];
+    __nv_bfloat16 *out[2][N];   // NULL: not wanted
+    Cached<TYPE> next[2][N] = {};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const int64_t t = t0 + i * GROUPS + sub;
-        slot[i] = t < p.T ? p.c.slots[t] : -1;
-        if (slot[i] >= p.c.slot_count) {
+        int slot = t < p.T ? p.c.slots[t] : -1;
+        if (slot >= p.c.slot_count) {
             atomicOr(&g_status_heads, kStatusBadGroup);
-            slot[i] = -1;
+            slot = -1;
+        }
+        unit[i] = slot < 0 ? nullptr : p.c.cache + (p.c.unit_of(slot) + static_cast<int64_t>(head0) * p.c.page_units) * UNIT;
+        const TokenPlace<TYPE, LANES> tp(slot & 15);
+        code[0][i] = k0.code + tp.code[0], scale[0][i] = k0.scale + tp.scale[0];
+        code[1][i] = v0.code + tp.code[1], scale[1][i] = v0.scale + tp.scale[1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            out[h][i] = t < p.T && p.out[h] ? p.out[h] + t * p.ldo[h] + static_cast<int64_t>(head0) * D + 8 * g : nullptr;
+            if (unit[i]) next[h][i].load(unit[i] + code[h][i], unit[i] + scale[h][i]);
         }
     }
-    const CachePlace<TYPE, LANES> k0(0, 0, g), v0(1, 0, g);
-    uint4 v[2][N];
+    const int64_t step = static_cast<int64_t>(p.c.page_units) * UNIT;
+#pragma unroll 1
+    for (; heads > 0; --heads) {
+        Cached<TYPE> now[2][N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        v[0][i] = v[1][i] = make_uint4(0, 0, 0, 0);
-        if (slot[i] < 0) continue;
-        const uint8_t *unit = p.c.cache + (p.c.unit_of(slot[i]) + static_cast<int64_t>(head) * p.c.page_units) * UNIT;
-        const TokenPlace<TYPE, LANES> tp(slot[i] & 15);
-        v[0][i] = cached8<TYPE>(unit + k0.code + tp.code[0], unit + k0.scale + tp.scale[0], gs[0]);
-        v[1][i] = cached8<TYPE>(unit + v0.code + tp.code[1], unit + v0.scale + tp.scale[1], gs[1]);
-    }
+        for (int i = 0; i < N; ++i) {
+            now[0][i] = next[0][i];
+            now[1][i] = next[1][i];
+            if (unit[i] && heads > 1) {
+                unit[i] += step;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int64_t t = t0 + i * GROUPS + sub;
-        if (t >= p.T) continue;
+                for (int h = 0; h < 2; ++h) next[h][i].load(unit[i] + code[h][i], unit[i] + scale[h][i]);
+            }
+        }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (p.out[h])
-                *reinterpret_cast<uint4 *>(p.out[h] + t * p.ldo[h] + static_cast<int64_t>(head) * D + 8 * g) = v[h][i];
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (out[h][i]) {
+                    *reinterpret_cast<uint4 *>(out[h][i]) = now[h][i].bf16(gs[h]);
+                    out[h][i] += D;
+                }
     }
 }
 
@@ -798,20 +934,28 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const ReadParams p
 
 int lanes_of(int64_t D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
-// Cuts the tokens' heads into blocks; CTAs of the grid: one wave at most.
+// Cuts the tokens' heads into blocks and these into the warps' pieces; CTAs of the
+// grid: one wave at most, -1 for more blocks than 32 bits count.
 int64_t plan_blocks(HeadParams &p, int lanes, int vectors, int per_sm)
 {
     const int block = 32 / lanes * vectors;
     int64_t per_token = 0;
     for (int k = 0; k < 3; ++k) per_token += p.blocks[k] = (p.heads[k] + block - 1) / block;
-    const int64_t want = (p.T * per_token + kWarps - 1) / kWarps;
-    return want < per_sm * 152 ? want : per_sm * 152;
+    const int64_t items = p.T * per_token;
+    if (items > UINT32_MAX) return -1;
+    const int64_t want = (items + kWarps - 1) / kWarps, grid = want < per_sm * 152 ? want : per_sm * 152;
+    if (grid > 0) {
+        p.share = static_cast<uint32_t>(items / (grid * kWarps));
+        p.more = static_cast<uint32_t>(items % (grid * kWarps));
+    }
+    return grid;
 }
 
 template <int LANES, bool INTER>
 int launch_heads(HeadParams &p, int cache, cudaStream_t s)
 {
     const int64_t grid = plan_blocks(p, LANES, kVectors, head_ctas(cache));
+    if (grid < 0) return QFP4_ERR_UNSUPPORTED;
     auto kernel = cache == kNoCache ? head_kernel<LANES, kNoCache, INTER>
                 : cache == QFP4_CACHE_BF16 ? head_kernel<LANES, QFP4_CACHE_BF16, INTER>
                 : cache == QFP4_CACHE_E4M3 ? head_kernel<LANES, QFP4_CACHE_E4M3, INTER>
@@ -957,6 +1101,20 @@ extern "C" int qfp4_qk_norm_rope_cache(const void *QKV_bf16, int64_t ld, int64_t
     return launch_heads_any(p, type, static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+template <int LANES>
+int launch_write(const WriteParams &p, int type, cudaStream_t s)
+{
+    constexpr uint32_t CTA = kWarps * 32 / LANES;
+    auto kernel = type == QFP4_CACHE_BF16 ? cache_write_kernel<QFP4_CACHE_BF16, LANES>
+                : type == QFP4_CACHE_E4M3 ? cache_write_kernel<QFP4_CACHE_E4M3, LANES>
+                                          : cache_write_kernel<QFP4_CACHE_NVFP4, LANES>;
+    return launch_status(launch_pdl(kernel, dim3((p.vectors + CTA - 1) / CTA), dim3(kThreads), 0, s, p));
+}
+
+}  // namespace
+
 extern "C" int qfp4_kv_cache_write(int type, const void *K_bf16, int64_t ldk, const void *V_bf16, int64_t ldv,
                                    int64_t T, int64_t kv_heads, int64_t head_dim, const int32_t *slots,
                                    const float *gs_k, const float *gs_v, void *cache, int64_t pages,
@@ -965,30 +1123,37 @@ extern "C" int qfp4_kv_cache_write(int type, const void *K_bf16, int64_t ldk, co
     int rc = check_cache(type, kv_heads, head_dim, pages, page_size);
     if (rc == QFP4_ERR_INVALID_ARG || T < 0 || ldk < kv_heads * head_dim || ldv < kv_heads * head_dim)
         return QFP4_ERR_INVALID_ARG;
-    if (rc != QFP4_OK || T > kMaxTokens || ldk % 8 != 0 || ldv % 8 != 0) return QFP4_ERR_UNSUPPORTED;
+    if (rc != QFP4_OK || T > kMaxTokens || T * kv_heads > INT32_MAX || ldk % 8 != 0 || ldv % 8 != 0)
+        return QFP4_ERR_UNSUPPORTED;
     if (T == 0) return QFP4_OK;
     if (!K_bf16 || !V_bf16) return QFP4_ERR_INVALID_ARG;
-    HeadParams p = {};
+    WriteParams p = {};
     rc = fill_cache(p.c, type, cache, kv_heads, pages, page_size, slots, gs_k, gs_v);
     if (rc != QFP4_OK) return rc;
     if (!aligned16(K_bf16) || !aligned16(V_bf16)) return QFP4_ERR_MISALIGNED;
-    p.x[1] = static_cast<const __nv_bfloat16 *>(K_bf16);
-    p.x[2] = static_cast<const __nv_bfloat16 *>(V_bf16);
-    p.ldx[1] = ldk;
-    p.ldx[2] = ldv;
-    p.T = T;
-    p.heads[1] = p.heads[2] = static_cast<int32_t>(kv_heads);
-    p.D = static_cast<int32_t>(head_dim);
-    return launch_heads_any(p, type, static_cast<cudaStream_t>(stream));
+    p.in[0] = static_cast<const __nv_bfloat16 *>(K_bf16);
+    p.in[1] = static_cast<const __nv_bfloat16 *>(V_bf16);
+    p.ld[0] = ldk;
+    p.ld[1] = ldv;
+    p.vectors = static_cast<uint32_t>(T * kv_heads);
+    p.heads = static_cast<uint32_t>(kv_heads);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    switch (head_dim) {
+    case 64: return launch_write<4>(p, type, s);
+    case 128: return launch_write<8>(p, type, s);
+    default: return launch_write<16>(p, type, s);
+    }
 }
 
 namespace {
 
 template <int LANES>
-int launch_read(const ReadParams &p, int type, cudaStream_t s)
+int launch_read(ReadParams &p, int type, cudaStream_t s)
 {
-    const int64_t items = (p.T + kReadTokens - 1) / kReadTokens * p.heads, grid = (items + kWarps - 1) / kWarps;
-    if (grid > INT32_MAX) return QFP4_ERR_UNSUPPORTED;
+    const int64_t blocks = (p.T + read_tokens(LANES) - 1) / read_tokens(LANES), share = blocks * p.heads / kReadWarps;
+    p.warp_heads = share < 1 ? 1 : share < p.heads ? static_cast<uint32_t>(share) : p.heads;
+    p.parts = (p.heads + p.warp_heads - 1) / p.warp_heads;
+    const int64_t grid = (blocks * p.parts + kWarps - 1) / kWarps;
     auto kernel = type == QFP4_CACHE_BF16 ? cache_read_kernel<QFP4_CACHE_BF16, LANES>
                 : type == QFP4_CACHE_E4M3 ? cache_read_kernel<QFP4_CACHE_E4M3, LANES>
                                           : cache_read_kernel<QFP4_CACHE_NVFP4, LANES>;
@@ -1005,7 +1170,7 @@ extern "C" int qfp4_kv_cache_read(int type, const void *cache, int64_t pages, in
     if (rc == QFP4_ERR_INVALID_ARG || T < 0 || (K_out && ldk < kv_heads * head_dim) ||
         (V_out && ldv < kv_heads * head_dim))
         return QFP4_ERR_INVALID_ARG;
-    if (rc != QFP4_OK || T > kMaxTokens || (K_out && ldk % 8 != 0) || (V_out && ldv % 8 != 0))
+    if (rc != QFP4_OK || T > kMaxTokens || T * kv_heads > INT32_MAX || (K_out && ldk % 8 != 0) || (V_out && ldv % 8 != 0))
         return QFP4_ERR_UNSUPPORTED;
     if (T == 0) return QFP4_OK;
     if (!K_out && !V_out) return QFP4_ERR_INVALID_ARG;
@@ -1014,7 +1179,7 @@ extern "C" int qfp4_kv_cache_read(int type, const void *cache, int64_t pages, in
     if (rc != QFP4_OK) return rc;
     if (!aligned16(K_out) || !aligned16(V_out)) return QFP4_ERR_MISALIGNED;
     p.T = T;
-    p.heads = static_cast<int32_t>(kv_heads);
+    p.heads = static_cast<uint32_t>(kv_heads);
     p.out[0] = static_cast<__nv_bfloat16 *>(K_out);
     p.out[1] = static_cast<__nv_bfloat16 *>(V_out);
     p.ldo[0] = ldk;
@@ -1036,7 +1201,8 @@ extern "C" size_t qfp4_qk_norm_rope_backward_workspace_bytes(int64_t T, int64_t 
     p.heads[0] = static_cast<int32_t>(q_heads);
     p.heads[1] = static_cast<int32_t>(kv_heads);
     // partial sums of the weights' gradients, a pair of vectors per CTA
-    return static_cast<size_t>(plan_blocks(p, lanes_of(head_dim), kBackVectors, kBackCtas)) * 2 * head_dim * sizeof(float);
+    const int64_t ctas = plan_blocks(p, lanes_of(head_dim), kBackVectors, kBackCtas);
+    return ctas < 0 ? 0 : static_cast<size_t>(ctas) * 2 * head_dim * sizeof(float);
 }
 
 extern "C" int qfp4_qk_norm_rope_backward(const void *QKV_bf16, int64_t ld, int64_t T, int64_t q_heads,
@@ -1063,6 +1229,9 @@ extern "C" int qfp4_qk_norm_rope_backward(const void *QKV_bf16, int64_t ld, int6
     if (T > 0) {
         if (!dQ || !dK || !dQKV) return QFP4_ERR_INVALID_ARG;
         if (!aligned16(dQ) || !aligned16(dK) || !aligned16(dQKV) || !aligned16(workspace)) return QFP4_ERR_MISALIGNED;
+        const int lanes = lanes_of(head_dim);
+        const int64_t ctas = plan_blocks(b.f, lanes, kBackVectors, kBackCtas);
+        if (ctas < 0) return QFP4_ERR_UNSUPPORTED;
         if (norm && (!workspace ||
                      ws_bytes < qfp4_qk_norm_rope_backward_workspace_bytes(T, q_heads, kv_heads, head_dim)))
             return QFP4_ERR_WORKSPACE;
@@ -1077,8 +1246,7 @@ extern "C" int qfp4_qk_norm_rope_backward(const void *QKV_bf16, int64_t ld, int6
 #ifdef QFP4_FAULT_INJECTION
         b.skip_copy = inject_skip_copy();
 #endif
-        const int lanes = lanes_of(head_dim);
-        const dim3 grid(static_cast<unsigned>(plan_blocks(b.f, lanes, kBackVectors, kBackCtas)));
+        const dim3 grid(static_cast<unsigned>(ctas));
         auto kernel = lanes == 8 ? (interleaved ? head_backward_kernel<8, true> : head_backward_kernel<8, false>)
                     : lanes == 16 ? (interleaved ? head_backward_kernel<16, true> : head_backward_kernel<16, false>)
                                   : (interleaved ? head_backward_kernel<32, true> : head_backward_kernel<32, false>);

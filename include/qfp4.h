@@ -723,7 +723,8 @@ int qfp4_gemv_nt(int fmt, int64_t M, int64_t N, int64_t K, const void *X_bf16, i
  *              elements from token to token; they may be the heads' own places
  *              in QKV
  * Requirements: head_dim and rotary_dim multiples of 16, rotary_dim <= head_dim
- * <= 256, at most 4096 heads of a kind, T <= 2^30, eps >= 0 and finite, ld, ldq,
+ * <= 256, at most 4096 heads of a kind, T <= 2^30, fewer than 2^32 heads in all
+ * (those of values counted with a cache), eps >= 0 and finite, ld, ldq,
  * ldk multiples of 8, the last a row's length at least; positions 4-byte
  * aligned, the rest 16-byte.  T == 0 launches nothing.
  * Accuracy: |y - exact| <= 2^-8 |exact| + 2^-20 (|z_a| + |z_b|) of the pair, where
@@ -790,8 +791,8 @@ size_t qfp4_kv_cache_page_bytes(int type, int64_t kv_heads, int64_t head_dim, in
  *           slot (it would keep a mixture of both).
  *   gs_k, gs_v  DEVICE fp32 (NVFP4 only)
  * Bit-exact to the types' rules.  Requirements: ldk, ldv multiples of 8, T <=
- * 2^30, K / V / cache 16-byte aligned, the rest 4-byte.  T == 0 launches
- * nothing. */
+ * 2^30, T * kv_heads < 2^31, K / V / cache 16-byte aligned, the rest 4-byte.
+ * T == 0 launches nothing. */
 int qfp4_kv_cache_write(int type, const void *K_bf16, int64_t ldk, const void *V_bf16, int64_t ldv, int64_t T,
                         int64_t kv_heads, int64_t head_dim, const int32_t *slots, const float *gs_k,
                         const float *gs_v, void *cache, int64_t pages, int64_t page_size, void *stream);

@@ -114,6 +114,24 @@ def test_cache_write_and_read(lib):
     assert write(K=None) == INVALID and write(V=None) == INVALID and read(K=None, V=None) == INVALID
 
 
+def test_more_heads_than_32_bits_count(lib):
+    wide = dict(T=1 << 30, q_heads=2048, kv_heads=2048, ld=1 << 19)
+    forward = caller(lib.qfp4_qk_norm_rope, **HEADS, Q=FAKE, ldq=1 << 18, K=FAKE, ldk=1 << 18, stream=None)
+    assert forward(**wide) == UNSUPPORTED
+    fused = caller(lib.qfp4_qk_norm_rope_cache, **HEADS, Q=FAKE, ldq=1 << 18, type=2, cache=FAKE, pages=4, page_size=16, slots=FAKE, gs_k=FAKE, gs_v=FAKE,
+                   stream=None)
+    assert fused(**{**wide, "ld": 3 << 18}) == UNSUPPORTED
+    backward = caller(lib.qfp4_qk_norm_rope_backward, **HEADS, dQ=FAKE, lddq=1 << 18, dK=FAKE, lddk=1 << 18, dQKV=FAKE, lddqkv=1 << 19, dq_weight=FAKE,
+                      dk_weight=FAKE, workspace=FAKE, ws_bytes=1 << 40, stream=None)
+    assert backward(**wide) == UNSUPPORTED
+    assert lib.qfp4_qk_norm_rope_backward_workspace_bytes(1 << 30, 2048, 2048, 128) == 0
+    write = caller(lib.qfp4_kv_cache_write, type=2, K=FAKE, ldk=512, V=FAKE, ldv=512, T=1 << 29, kv_heads=4, head_dim=128, slots=FAKE, gs_k=FAKE, gs_v=FAKE,
+                   cache=FAKE, pages=4, page_size=16, stream=None)
+    read = caller(lib.qfp4_kv_cache_read, type=2, cache=FAKE, pages=4, page_size=16, kv_heads=4, head_dim=128, slots=FAKE, T=1 << 29, gs_k=FAKE, gs_v=FAKE,
+                  K=FAKE, ldk=512, V=FAKE, ldv=512, stream=None)
+    assert write() == UNSUPPORTED and read() == UNSUPPORTED
+
+
 def test_attention(lib):
     need = lib.qfp4_attention_decode_workspace_bytes(2, 8, 2, 128)
     assert need > 0

@@ -174,6 +174,32 @@ def test_norm_rope_cache_padding():
     assert torch.equal(cache[~touched], before[~touched])
 
 
+@pytest.mark.parametrize("H,D", [(5, 64), (8, 128), (3, 256)])
+@pytest.mark.parametrize("type", _cache.TYPES)
+def test_read_of_many_tokens(type, H, D):
+    """More tokens than the GPU has warps for each head: a warp takes several heads.
+    The same slots many times, skipped and far ones among them, against small calls."""
+    page_size, pages, T = 48, 7, 20011
+    g = torch.Generator(device="cuda").manual_seed(H)
+    gs, cache = scales(type), _cache.empty(type, pages, H, D, page_size)
+    n = pages * page_size
+    qfp4.kv_cache_write(type, vectors(g, n, H, D), vectors(g, n, H, D), torch.arange(n, dtype=torch.int32, device="cuda"), cache, page_size, *gs)
+    k, v = (torch.empty(n, H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for at in range(0, n, 42):
+        qfp4.kv_cache_read(type, cache, page_size, torch.arange(at, at + 42, dtype=torch.int32, device="cuda"), k[at: at + 42], v[at: at + 42], *gs)
+    assert qfp4.poll_device_status() == 0
+    slots = torch.randint(-20, n, (T,), generator=g, device="cuda").int()
+    slots[11::1000] = n
+    slots[12::1000] = 2**31 - 1
+    known = (slots >= 0) & (slots < n)
+    at = torch.where(known, slots, 0).long()
+    ko, vo = (torch.full((T + 1, H, D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qfp4.kv_cache_read(type, cache, page_size, slots, ko[:T], vo[:T], *gs)
+    assert qfp4.poll_device_status() == -1
+    for got, want in ((ko, k), (vo, v)):
+        assert torch.equal(got[:T], torch.where(known[:, None, None], want[at], 0)) and (got[T] == 7).all()
+
+
 def test_offsets_beyond_32_bits():
     """A cache of more than 2^32 bytes: its last page."""
     type, H, D, page_size = qfp4.CACHE_BF16, 8, 128, 64
