@@ -117,6 +117,32 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
     else mma_f16(c, a, b0, b1);
 }
 
+// How the line of tiles is dealt out.  Evenly where there are more than two for each CTA
+// of the grid.  Else one for each, so that as many as can load, or two: where there are
+// more than CTAs, where an item has at least 32 (half as many pieces to join: BF16, 1 x
+// 4096 tokens x 8 heads 13.4 us, 15.9 with one), and where it has two (none to join:
+// NVFP4, 512 tokens 7.5 us, 8.9).  Three and four were slower.
+struct Shares {
+    int64_t total, ctas;
+    int fixed;          // tiles of a CTA; 0: evenly
+
+    __device__ __forceinline__ Shares(const AttnParams &p, int64_t tiles) : total(tiles)
+    {
+        const int64_t grid = gridDim.x, items = static_cast<int64_t>(p.B) * p.kv_heads * p.blocks;
+        const bool two = total > grid || total >= 32 * items || (total > items && total <= 2 * items);
+        fixed = total > 2 * grid ? 0 : two ? 2 : 1;
+        ctas = fixed ? (total + fixed - 1) >> (fixed - 1) : grid;
+    }
+    __device__ __forceinline__ int64_t begin_of(int64_t cta) const
+    {
+        return fixed ? min(cta * fixed, total) : cta * total / ctas;
+    }
+    __device__ __forceinline__ int64_t cta_of(int64_t tile) const
+    {
+        return fixed ? tile >> (fixed - 1) : ((tile + 1) * ctas - 1) / total;
+    }
+};
+
 // Where a CTA stands on the line of tiles: sequence, (key head, query block) and tile.
 struct Cursor {
     int b, head, block, tile, tiles;
@@ -176,6 +202,7 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t s_sum[C::WARPS];
     __shared__ int64_t s_start[2];      // the CTA's first tile: sequence, tile within it
+    __shared__ int64_t s_total;         // tiles of the whole line
     __shared__ uint32_t s_last;
     float *s_o = reinterpret_cast<float *>(smem + C::RING);                     // [QUERIES][D + 4]
     float2 *s_ml = reinterpret_cast<float2 *>(s_o + C::SUMS * C::SUM);         // [warps][QUERIES]
@@ -207,9 +234,14 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
     int64_t total = 0;
 #pragma unroll
     for (int i = 0; i < C::WARPS; ++i) total += s_sum[i];
-    const int64_t ctas = total < gridDim.x ? total : gridDim.x;
-    if (blockIdx.x >= ctas) return;
-    const int64_t lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
+    int64_t lo, hi;
+    {
+        const Shares shares(p, total);
+        if (blockIdx.x >= shares.ctas) return;
+        lo = shares.begin_of(blockIdx.x);
+        hi = shares.begin_of(blockIdx.x + 1);
+        if (tid == 0) s_total = total;
+    }
     if (warp == 0) {
         int64_t before = 0;
         for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -239,7 +271,7 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
     Cursor cur;
     cur.b = static_cast<int>(s_start[0]);
     cur.load<TILE>(p);
-    const int item0 = static_cast<int>(s_start[1] / cur.tiles);
+    const int item0 = s_start[1] <= UINT32_MAX ? static_cast<uint32_t>(s_start[1]) / static_cast<uint32_t>(cur.tiles) : static_cast<int>(s_start[1] / cur.tiles);
     cur.head = item0 / p.blocks;
     cur.block = item0 - cur.head * p.blocks;
     cur.tile = static_cast<int>(s_start[1] - static_cast<int64_t>(item0) * cur.tiles);
@@ -765,7 +797,8 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
             }
             // CTAs that hold the item's first and last tile
             const int64_t i0 = at - seg_n - seg_first, i1 = i0 + seg_tiles - 1;
-            const int64_t c0 = ((i0 + 1) * ctas - 1) / total, c1 = ((i1 + 1) * ctas - 1) / total;
+            const Shares shares(p, s_total);
+            const int64_t c0 = shares.cta_of(i0), c1 = shares.cta_of(i1);
             // one thread releases the piece for all, who have met at the barrier, and
             // acquires the others' for all who meet at the next
             __syncthreads();
