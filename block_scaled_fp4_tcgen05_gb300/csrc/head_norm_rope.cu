@@ -228,33 +228,76 @@ struct CachePlace {
     }
 };
 
+// Where the eight neighbouring elements 8 g .. of a vector lie whose pieces are apart:
+// its first four in lane `from`, the others in the next, in the pieces of the same place.
+struct Gather {
+    int from;
+    bool moves, second;
+
+    template <int LANES>
+    __device__ __forceinline__ static Gather of(const HeadParams &p, const Place &pl, int lane)
+    {
+        const int g = lane % LANES, i = 8 * g;
+        const bool second = i >= p.R / 2;
+        return {pl.turns ? lane - g + (second ? i - p.R / 2 : i) / 4 : lane, pl.turns, second};
+    }
+    // N words of two pieces
+    template <int N>
+    __device__ __forceinline__ void words(uint32_t (&w)[N]) const
+    {
+        uint32_t o[N];
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+            const uint32_t a0 = __shfl_sync(0xffffffffu, w[k], from), b0 = __shfl_sync(0xffffffffu, w[N / 2 + k], from);
+            const uint32_t a1 = __shfl_sync(0xffffffffu, w[k], from + 1), b1 = __shfl_sync(0xffffffffu, w[N / 2 + k], from + 1);
+            o[k] = second ? b0 : a0;
+            o[N / 2 + k] = second ? b1 : a1;
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) w[k] = moves ? o[k] : w[k];
+    }
+};
+
 // Writes a lane's eight elements to the cache: the quantisers' rules, with one
 // scale per vector (E4M3) or per 16 elements (NVFP4).  Every lane of the group takes
-// part.
+// part.  Elements that lie apart are brought together as narrow as the scale allows.
 template <int TYPE, int LANES>
 __device__ __forceinline__ void store_cached(uint8_t *unit, const CachePlace<TYPE, LANES> &place, int lane,
-                                             const float (&y)[8], bool live, float gs, float inv_gs)
+                                             float (&y)[8], bool live, float gs, float inv_gs, bool apart,
+                                             const Gather &gather)
 {
     const int g = lane % LANES;
     uint8_t *at = unit + place.code;
-    if (TYPE == QFP4_CACHE_BF16) {
-        if (live) *reinterpret_cast<uint4 *>(at) = pack8(y);
+    if constexpr (TYPE == QFP4_CACHE_BF16) {
+        uint32_t w[4] = {pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7])};
+        if (apart) gather.words(w);
+        if (live) *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
         return;
+    }
+    if constexpr (TYPE == QFP4_CACHE_NVFP4) {
+        if (apart) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(y[e]);
+            gather.words(w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(w[e]);
+        }
     }
     float amax = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));
-    if (TYPE == QFP4_CACHE_E4M3) {
+    if constexpr (TYPE == QFP4_CACHE_E4M3) {
         const float a = fmaxf(group_max<LANES>(amax), kFloor);
         const float inv = __fdiv_rn(448.0f, a);
-        uint2 q;
-        q.x = e4m3x2(y[0] * inv, y[1] * inv) | (e4m3x2(y[2] * inv, y[3] * inv) << 16);
-        q.y = e4m3x2(y[4] * inv, y[5] * inv) | (e4m3x2(y[6] * inv, y[7] * inv) << 16);
+        uint32_t w[2] = {e4m3x2(y[0] * inv, y[1] * inv) | (e4m3x2(y[2] * inv, y[3] * inv) << 16),
+                         e4m3x2(y[4] * inv, y[5] * inv) | (e4m3x2(y[6] * inv, y[7] * inv) << 16)};
+        if (apart) gather.words(w);
         if (live) {
-            *reinterpret_cast<uint2 *>(at) = q;
+            *reinterpret_cast<uint2 *>(at) = make_uint2(w[0], w[1]);
             if (g == 0) *reinterpret_cast<float *>(unit + place.scale) = __fdiv_rn(a, 448.0f);
         }
-    } else {
+    } else if constexpr (TYPE == QFP4_CACHE_NVFP4) {
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         const BlockScale b = block_scale<QFP4_NVFP4>(amax, gs, inv_gs);
         const uint32_t q = encode8_f32<QFP4_NVFP4>(y, b);
@@ -265,30 +308,12 @@ __device__ __forceinline__ void store_cached(uint8_t *unit, const CachePlace<TYP
     }
 }
 
-// The eight neighbouring elements 8 g .. of a vector whose pieces lie apart: from
-// the lanes that hold them.
-template <int LANES>
-__device__ __forceinline__ void gather(const HeadParams &p, const Place &pl, int lane, float (&e)[8])
-{
-    const int g = lane % LANES, i = 8 * g, second = i >= p.R / 2;
-    const int from = pl.turns ? lane - g + (second ? i - p.R / 2 : i) / 4 : lane;
-    float y[8];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float a0 = __shfl_sync(0xffffffffu, e[k], from), b0 = __shfl_sync(0xffffffffu, e[4 + k], from);
-        const float a1 = __shfl_sync(0xffffffffu, e[k], from + 1), b1 = __shfl_sync(0xffffffffu, e[4 + k], from + 1);
-        y[k] = second ? b0 : a0;
-        y[4 + k] = second ? b1 : a1;
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) e[k] = pl.turns ? y[k] : e[k];
-}
-
 // Vectors that a group of lanes works on at a time, with as many loads ahead.
 constexpr int kVectors = 2;
 
-// CTAs per SM that the kernels' registers are sized for.
-constexpr int kHeadCtas = 4, kCacheCtas = 2, kBackCtas = 2;
+// CTAs per SM that the kernels' registers are sized for (with an E4M3 cache, 16384 tokens
+// x (32 + 8 + 8) heads x 128: three 79 us, two 91, four 84; floor 56).
+constexpr int kHeadCtas = 4, kCacheCtas = 3, kBackCtas = 2;
 constexpr int head_ctas(int cache) { return cache == kNoCache ? kHeadCtas : kCacheCtas; }
 
 // Piece of the line of (token, block of heads of a kind) that a warp takes: as
@@ -371,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, head_ctas(CACHE)) head_kernel(const 
 
         constexpr int TYPE = CACHE == kNoCache ? 0 : CACHE;
         const CachePlace<TYPE, LANES> place(kind == kValue, slot & 15, g);
+        const Gather gather = Gather::of<LANES>(p, pl, lane);
         uint8_t *units = nullptr;       // of head 0
         if (CACHE != kNoCache && kind != kQuery)
             units = p.c.cache + p.c.unit_of(slot) * CachePlace<TYPE, LANES>::UNIT;
@@ -425,10 +451,9 @@ __global__ void __launch_bounds__(kThreads, head_ctas(CACHE)) head_kernel(const 
                 } else {
                     float e[8];
                     elements<INTER>(v, e);
-                    if (!INTER && kind == kKey) gather<LANES>(p, pl, lane, e);
                     const int half = kind == kValue;
                     uint8_t *unit = units + static_cast<int64_t>(min(h, head_end - 1)) * p.c.page_units * place.UNIT;
-                    store_cached<TYPE, LANES>(unit, place, lane, e, live, gs[half], inv_gs[half]);
+                    store_cached<TYPE, LANES>(unit, place, lane, e, live, gs[half], inv_gs[half], !INTER && kind == kKey, gather);
                 }
             }
         }
@@ -702,7 +727,7 @@ __device__ __forceinline__ void store_codes(uint8_t *at, const uint32_t *w)
 // NVFP4 whole, so that its scale, as much work as its codes, is found once: 32768 tokens
 // x 8 heads x 128 take 40 us in NVFP4 (floor 25; bound by the quotients' instructions),
 // 32 in E4M3 (30) and 55 in BF16 (40; the pieces of 16 and 64 bytes); head_kernel, whose
-// lanes hold eight elements, takes 99, 71 and 75.
+// lanes hold eight elements, took 99, 71 and 75.
 template <int TYPE, int LANES>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteParams p)
 {
