@@ -124,10 +124,10 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b)
     return r;
 }
 
-// Whether a byte of w is 0 or 255.
-__device__ __forceinline__ bool has_end_byte(uint32_t w)
+// Whether the bytes of a and b all lie in 64..191 (their two top bits differ).
+__device__ __forceinline__ bool all_middling(uint32_t a, uint32_t b)
 {
-    return (((w - 0x01010101u) & ~w) | ((~w - 0x01010101u) & w) & 0x80808080u) & 0x80808080u;
+    return ((a ^ a << 1) & (b ^ b << 1) & 0x80808080u) == 0x80808080u;
 }
 
 template <int FMT, int NT>
@@ -307,13 +307,14 @@ __global__ void __launch_bounds__(GemvCfg<FMT, NT>::THREADS, 1) gemv_kernel(cons
                                 for (int h = 0; h < 2; ++h) sw[c4][h] = *reinterpret_cast<const uint32_t *>(sfs + (s * COLS4 + c4) * 64 + h * 8);
                             float f[4][2];      // MXFP4: the chunks' scales of rows g and g + 8
                             if (FMT == QFP4_MXFP4) {
-                                // the exponent field of 2^(byte - 127); 0 and 255 apart
+                                // the exponent field of 2^(byte - 127); 0 and 255 are not that, and are
+                                // looked for beyond 2^-63 and 2^64 only
 #pragma unroll
                                 for (int c = 0; c < 4; ++c)
 #pragma unroll
                                     for (int h = 0; h < 2; ++h)
                                         f[c][h] = __uint_as_float((c == 3 ? sw[0][h] >> 1 : sw[0][h] << (23 - 8 * c)) & 0x7F800000u);
-                                if (__any_sync(0xffffffffu, has_end_byte(sw[0][0]) || has_end_byte(sw[0][1]))) {
+                                if (!__all_sync(0xffffffffu, all_middling(sw[0][0], sw[0][1]))) {
 #pragma unroll
                                     for (int c = 0; c < 4; ++c)
 #pragma unroll

@@ -95,6 +95,22 @@ def test_range_of_scales():
     assert torch.isnan(d[:, 5]).all() and torch.isfinite(d[:, :5]).all() and torch.isfinite(d[:, 6:]).all()
 
 
+@pytest.mark.parametrize("K", [128, 384])
+def test_every_scale_byte(K):
+    """Rows of weights 1 with one MXFP4 scale byte each, in order and spread over the rows' groups: powers of two, exact."""
+    for order in (torch.arange(228), torch.randperm(228, generator=torch.Generator().manual_seed(K))):
+        sf = order.to(torch.uint8).cuda()[:, None].expand(228, K // 32).contiguous()
+        mma = torch.empty(qfp4.sf_mma_bytes(228, K // 32), dtype=torch.uint8, device="cuda")
+        qfp4.sf_interleave(sf, 228, K // 32, mma)
+        code = torch.full((228, K // 2), 0x22, dtype=torch.uint8, device="cuda")
+        x = torch.zeros(9, K, dtype=torch.bfloat16, device="cuda")
+        x[torch.arange(9), torch.arange(9) * 14 + K - 128] = 1.0
+        d = torch.empty(9, 228, dtype=torch.bfloat16, device="cuda")
+        qfp4.gemv_nt(MX, x, code, mma, None, d)
+        want = torch.ldexp(torch.ones(228, dtype=torch.float64), order - 127)
+        assert torch.equal(d.double().cpu(), want.expand(9, 228))
+
+
 def test_range_of_activations():
     """Rows of any size, and elements far below the largest."""
     g = torch.Generator(device="cuda").manual_seed(4)
