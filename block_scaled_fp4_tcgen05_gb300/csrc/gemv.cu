@@ -23,7 +23,7 @@
 // 8192 27 us (19.5); more weights add 0.9 of the copy bandwidth, so what is above the
 // floor is the call's beginning and end, about 5 us.  Nine rows of x and more double
 // the products and bind it by instructions: 16 x 28672 x 8192 41 us (NVFP4), 43 us
-// (MXFP4), 2.1 a cycle.  Other forms, 16 and 1 rows of that size (MXFP4): CTAs of eight
+// (MXFP4), 1.9 a cycle.  Other forms, 16 and 1 rows of that size (MXFP4): CTAs of eight
 // warps and 128 rows with the CTA's slice of x converted for each 52 and 38 us; the
 // weights by TMA in stages of 128 rows 56 and 43; the line of groups and K shared
 // evenly between the warps 47 and 30 (more work around each stage); a group's K shared

@@ -29,7 +29,7 @@
 // across the heads' borders; no other warp waits for it until a head ends.
 //
 // Measured (of the copy bandwidth, head_dim 128): BF16 64 ragged sequences of up to
-// 8192 x 8 heads 185 us (0.91), E4M3 105 us (0.83); NVFP4 4 x 131072 x 8 heads 125 us
+// 8192 x 8 heads 182 us (0.93), E4M3 103 us (0.84); NVFP4 4 x 131072 x 8 heads 125 us
 // (0.71).  What is left of NVFP4 are instructions: a unit of 16 tokens takes about 330,
 // 64 conversions and 64 multiplications by scales among them, at 2.4 a cycle.  16 warps
 // per SM of 128 registers beat 12 of 168 (131 us against 159 at that time); stages of
