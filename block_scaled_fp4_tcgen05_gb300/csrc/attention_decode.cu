@@ -14,10 +14,7 @@ int status_word_attention(uint32_t **word) { return status_word(g_status_attenti
 
 namespace {
 
-// CTAs that the workspace is sized for: 152 SMs, at most this many on each.
-constexpr int kMaxPerSm = 4, kMaxCtas = 152 * kMaxPerSm;
-constexpr size_t kCounterBytes = 4096;
-static_assert(kMaxCtas * sizeof(uint32_t) <= kCounterBytes, "a counter per CTA");
+constexpr size_t kCounterBytes = 8192;      // a counter per CTA, at the same place for all sizes
 
 constexpr int64_t kMaxHeads = 4096, kMaxBatch = 1 << 20, kMaxLength = int64_t{1} << 30;
 
@@ -26,10 +23,13 @@ bool sizes_ok(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D)
     return (D == 64 || D == 128 || D == 256) && q_heads <= kMaxHeads && B <= kMaxBatch && q_heads % kv_heads == 0;
 }
 
-size_t workspace_bytes(int64_t group, int D)
+// Counters and two pieces for each CTA that the GPU holds at once.
+size_t workspace_bytes(int64_t B, int64_t kv_heads, int64_t group, int D)
 {
-    return kCounterBytes + static_cast<size_t>(kMaxCtas) * 2 * attn_piece_floats(8 * attn_tiles(group, D), D) * sizeof(float);
+    const int queries = 8 * attn_tiles(group, D), ctas = 152 * attn_most_per_sm(B * kv_heads * ((group + queries - 1) / queries));
+    return kCounterBytes + static_cast<size_t>(ctas) * 2 * attn_piece_floats(queries, D) * sizeof(float);
 }
+static_assert(152 * 8 * sizeof(uint32_t) <= kCounterBytes, "8: the most that attn_most_per_sm gives");
 
 }  // namespace
 }  // namespace qfp4
@@ -39,7 +39,7 @@ using namespace qfp4;
 extern "C" size_t qfp4_attention_decode_workspace_bytes(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim)
 {
     if (B < 0 || q_heads < 1 || kv_heads < 1 || !sizes_ok(B, q_heads, kv_heads, head_dim)) return 0;
-    return workspace_bytes(q_heads / kv_heads, static_cast<int>(head_dim));
+    return workspace_bytes(B, kv_heads, q_heads / kv_heads, static_cast<int>(head_dim));
 }
 
 extern "C" int qfp4_attention_decode(int type, const void *Q_bf16, int64_t ldq, int64_t B, int64_t q_heads,
@@ -63,7 +63,7 @@ extern "C" int qfp4_attention_decode(int type, const void *Q_bf16, int64_t ldq, 
         !aligned4(page_table) || !aligned4(lengths) || !aligned4(gs_k) || !aligned4(gs_v) || !aligned4(lse))
         return QFP4_ERR_MISALIGNED;
     const int D = static_cast<int>(head_dim), nt = attn_tiles(q_heads / kv_heads, D);
-    if (!workspace || ws_bytes < workspace_bytes(q_heads / kv_heads, D)) return QFP4_ERR_WORKSPACE;
+    if (!workspace || ws_bytes < workspace_bytes(B, kv_heads, q_heads / kv_heads, D)) return QFP4_ERR_WORKSPACE;
     AttnParams p = {};
     p.q = static_cast<const __nv_bfloat16 *>(Q_bf16);
     p.ldq = ldq;
@@ -93,9 +93,9 @@ extern "C" int qfp4_attention_decode(int type, const void *Q_bf16, int64_t ldq, 
 #endif
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (type) {
-    case QFP4_CACHE_BF16: return attn_launch_bf16(p, D, nt, kMaxPerSm, s);
-    case QFP4_CACHE_E4M3: return attn_launch_e4m3(p, D, nt, kMaxPerSm, s);
-    default: return attn_launch_nvfp4(p, D, nt, kMaxPerSm, s);
+    case QFP4_CACHE_BF16: return attn_launch_bf16(p, D, nt, s);
+    case QFP4_CACHE_E4M3: return attn_launch_e4m3(p, D, nt, s);
+    default: return attn_launch_nvfp4(p, D, nt, s);
     }
 }
 

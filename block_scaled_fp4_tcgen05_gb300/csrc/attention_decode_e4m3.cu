@@ -4,9 +4,9 @@
 
 namespace qfp4 {
 
-int attn_launch_e4m3(const AttnParams &p, int D, int nt, int per_sm, cudaStream_t s)
+int attn_launch_e4m3(const AttnParams &p, int D, int nt, cudaStream_t s)
 {
-    return attn_launch_type<QFP4_CACHE_E4M3>(p, D, nt, per_sm, s);
+    return attn_launch_type<QFP4_CACHE_E4M3>(p, D, nt, s);
 }
 
 }  // namespace qfp4

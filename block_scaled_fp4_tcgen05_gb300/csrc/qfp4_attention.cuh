@@ -344,22 +344,17 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
     };
     Late late[2] = {};
 
-    while (at < hi) {
-        // ---- a segment: the CTA's tiles of one (sequence, key head, query block)
-        const int b = cur.b, head = cur.head, qblock = cur.block, seg_first = cur.tile, seg_tiles = cur.tiles, len = cur.len, first = cur.first;
-        const int visible = p.window > 0 && len > p.window ? len - p.window : 0;      // first token that counts
-        const int queries = min(QUERIES, p.group - qblock * QUERIES);
-        const int64_t q_head0 = static_cast<int64_t>(head) * p.group + qblock * QUERIES;
-
-        uint32_t qf[NT][KSTEPS][2];
-        float qmul[NT][2];
+    // The queries of the cursor's head as they are in memory: on their way while the
+    // segment before is joined.
+    uint32_t qf[NT][KSTEPS][2];
+    auto load_q = [&] {
+        const int queries = min(QUERIES, p.group - cur.block * QUERIES);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const bool has = 8 * n + g < queries;
-            const __nv_bfloat16 *src = p.q + b * p.ldq + (q_head0 + 8 * n + g) * D;
+            const __nv_bfloat16 *src = p.q + cur.b * p.ldq + (static_cast<int64_t>(cur.head) * p.group + cur.block * QUERIES + 8 * n + g) * D;
             // k step (chunk i, u): lane t's dims are four of chunk 4 i + t of the row
             constexpr int EC = U.row / 4 >= 16 ? 16 * D / U.row : D / 4;    // elements of a chunk
-            float amax = 0.0f;
 #pragma unroll
             for (int ks = 0; ks < KSTEPS; ++ks) {
                 const int i = ks / (EC / 4), u = ks % (EC / 4);
@@ -367,13 +362,26 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
                 if (has) v = *reinterpret_cast<const uint2 *>(src + (4 * i + t) * EC + 4 * u);
                 qf[n][ks][0] = v.x;
                 qf[n][ks][1] = v.y;
-                if (TYPE != QFP4_CACHE_BF16) {
-                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v.x << 16)), fabsf(__uint_as_float(v.x & 0xFFFF0000u))));
-                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v.y << 16)), fabsf(__uint_as_float(v.y & 0xFFFF0000u))));
-                }
             }
+        }
+    };
+    load_q();
+    while (at < hi) {
+        // ---- a segment: the CTA's tiles of one (sequence, key head, query block)
+        const int b = cur.b, head = cur.head, qblock = cur.block, seg_first = cur.tile, seg_tiles = cur.tiles, len = cur.len, first = cur.first;
+        const int visible = p.window > 0 && len > p.window ? len - p.window : 0;      // first token that counts
+
+        float qmul[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
             float back = 1.0f;      // what the products of this lane's query are multiplied by
             if (TYPE != QFP4_CACHE_BF16) {
+                float amax = 0.0f;
+#pragma unroll
+                for (int ks = 0; ks < KSTEPS; ++ks)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(qf[n][ks][r] << 16)), fabsf(__uint_as_float(qf[n][ks][r] & 0xFFFF0000u))));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 // the exponent that takes amax to [2^14, 2^15); none for zeros and infinities
@@ -705,6 +713,7 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
         }
         at += seg_n;
         cur.skip<TILE>(p, seg_n);
+        if (at < hi) load_q();
 
         // ---- the warps' results joined: o relative to the CTA's maximum, added up in the warps' order
 #pragma unroll
@@ -888,48 +897,58 @@ int attn_per_sm(int most)
 }
 
 // The grid is what the GPU holds at once, whatever the lengths, which only the
-// device knows: 152 SMs times the CTAs of each, at most per_sm.
+// device knows: 152 SMs times the CTAs of each, as many as `most` at most.
 template <int TYPE, int D, int NT, int WARPS>
-int attn_launch_one(const AttnParams &p, int per_sm, cudaStream_t s)
+int attn_launch_one(const AttnParams &p, int most, cudaStream_t s)
 {
     using C = AttnCfg<TYPE, D, NT, WARPS>;
     auto kernel = attention_decode_kernel<TYPE, D, NT, WARPS>;
     const int rc = ensure_smem_attr(reinterpret_cast<const void *>(kernel), C::SMEM);
     if (rc != QFP4_OK) return rc;
-    const int n = attn_per_sm<TYPE, D, NT, WARPS>(per_sm);
+    const int n = attn_per_sm<TYPE, D, NT, WARPS>(most);
     if (n == 0) return QFP4_ERR_CUDA;
     return launch_status(launch_pdl(kernel, dim3(152 * n), dim3(C::THREADS), C::SMEM, s, p));
 }
 
-// NVFP4's CTAs have eight warps, two of them on an SM, where the items (sequences x
-// key heads x blocks of queries) are few: half as many pieces to join (1 x 4096
-// tokens x 8 heads 11 us, 16 with four warps; 1 x 131072 48, 55).  Where they are
-// many, four smaller CTAs hide one another's joins (64 ragged sequences 83 us, 95 with
-// eight warps; 256 short ones 32, 43).
+// Items (sequences x key heads x blocks of queries), above which the CTAs have two warps.
+constexpr int64_t kManyItems = 4 * 152;
+
+// CTAs that an SM takes at most.
+inline int attn_most_per_sm(int64_t items) { return items > kManyItems ? 8 : 4; }
+
+// Four warps a CTA, four CTAs on an SM.  Many items: two warps and twice as many CTAs,
+// which hide one another's joins (256 ragged sequences up to 300 tokens x 8 heads: NVFP4
+// 26.4 us, 29.2 with four; E4M3 32.3, 36.2; up to 2000 tokens 81, 86 and 105, 109; one
+// warp 28, 36, 83, 109; 512 items up to 300 tokens 14.4, 13.5).  Few items in NVFP4: eight
+// warps, two CTAs on an SM, half as many pieces to join (1 x 4096 tokens x 8 heads 11 us, 16
+// with four warps; 1 x 131072 48, 55).
 template <int TYPE, int D, int NT>
-int attn_launch(const AttnParams &p, int per_sm, cudaStream_t s)
+int attn_launch(const AttnParams &p, cudaStream_t s)
 {
+    const int64_t items = static_cast<int64_t>(p.B) * p.kv_heads * p.blocks;
+    const int most = attn_most_per_sm(items);
+    if (items > kManyItems) return attn_launch_one<TYPE, D, NT, 2>(p, most, s);
     if constexpr (TYPE == QFP4_CACHE_NVFP4 && D <= 128) {
-        if (static_cast<int64_t>(p.B) * p.kv_heads * p.blocks <= 2 * 152) return attn_launch_one<TYPE, D, NT, 8>(p, per_sm, s);
+        if (items <= 2 * 152) return attn_launch_one<TYPE, D, NT, 8>(p, most, s);
     }
-    return attn_launch_one<TYPE, D, NT, 4>(p, per_sm, s);
+    return attn_launch_one<TYPE, D, NT, 4>(p, most, s);
 }
 
 // Of attention_decode_<type>.cu.
-int attn_launch_bf16(const AttnParams &p, int D, int nt, int per_sm, cudaStream_t s);
-int attn_launch_e4m3(const AttnParams &p, int D, int nt, int per_sm, cudaStream_t s);
-int attn_launch_nvfp4(const AttnParams &p, int D, int nt, int per_sm, cudaStream_t s);
+int attn_launch_bf16(const AttnParams &p, int D, int nt, cudaStream_t s);
+int attn_launch_e4m3(const AttnParams &p, int D, int nt, cudaStream_t s);
+int attn_launch_nvfp4(const AttnParams &p, int D, int nt, cudaStream_t s);
 
 // Query heads of a block: those of a group, 8 or 16; 8 where 16 would not fit
 // in the registers (D = 256).
 inline int attn_tiles(int64_t group, int D) { return group > 8 && D <= 128 ? 2 : 1; }
 
 template <int TYPE>
-int attn_launch_type(const AttnParams &p, int D, int nt, int per_sm, cudaStream_t s)
+int attn_launch_type(const AttnParams &p, int D, int nt, cudaStream_t s)
 {
-    if (D == 64) return nt == 1 ? attn_launch<TYPE, 64, 1>(p, per_sm, s) : attn_launch<TYPE, 64, 2>(p, per_sm, s);
-    if (D == 128) return nt == 1 ? attn_launch<TYPE, 128, 1>(p, per_sm, s) : attn_launch<TYPE, 128, 2>(p, per_sm, s);
-    return attn_launch<TYPE, 256, 1>(p, per_sm, s);
+    if (D == 64) return nt == 1 ? attn_launch<TYPE, 64, 1>(p, s) : attn_launch<TYPE, 64, 2>(p, s);
+    if (D == 128) return nt == 1 ? attn_launch<TYPE, 128, 1>(p, s) : attn_launch<TYPE, 128, 2>(p, s);
+    return attn_launch<TYPE, 256, 1>(p, s);
 }
 
 }  // namespace qfp4
