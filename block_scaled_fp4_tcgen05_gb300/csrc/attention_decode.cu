@@ -14,7 +14,8 @@ int status_word_attention(uint32_t **word) { return status_word(g_status_attenti
 
 namespace {
 
-constexpr size_t kCounterBytes = 8192;      // a counter per CTA, at the same place for all sizes
+constexpr size_t kCounterBytes = 16384;     // at the same place for all sizes
+static_assert(3 * kAttnMaxCtas * sizeof(uint32_t) <= kCounterBytes, "three counters per CTA");
 
 constexpr int64_t kMaxHeads = 4096, kMaxBatch = 1 << 20, kMaxLength = int64_t{1} << 30;
 
@@ -26,10 +27,10 @@ bool sizes_ok(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D)
 // Counters and two pieces for each CTA that the GPU holds at once.
 size_t workspace_bytes(int64_t B, int64_t kv_heads, int64_t group, int D)
 {
-    const int queries = 8 * attn_tiles(group, D), ctas = 152 * attn_most_per_sm(B * kv_heads * ((group + queries - 1) / queries));
+    const int nt = attn_tiles(group, D), queries = 8 * nt;
+    const int ctas = 152 * attn_most_per_sm(B * kv_heads * ((group + queries - 1) / queries), nt);
     return kCounterBytes + static_cast<size_t>(ctas) * 2 * attn_piece_floats(queries, D) * sizeof(float);
 }
-static_assert(152 * 8 * sizeof(uint32_t) <= kCounterBytes, "8: the most that attn_most_per_sm gives");
 
 }  // namespace
 }  // namespace qfp4

@@ -23,13 +23,13 @@
 //
 // The tokens of all sequences and heads are one line of tiles; each CTA takes an
 // equal piece of it, whatever the lengths, and the pieces of a head that lies
-// across CTAs are joined by the one that finishes last, in the order of the
-// pieces: results repeat bit for bit.  Each warp brings its own tokens with bulk
+// across CTAs are joined by the one that finishes last (many pieces in groups, and then
+// the groups), in the order of the pieces: results repeat bit for bit.  Each warp brings its own tokens with bulk
 // copies into a ring of stages of its own, ahead of the tile that it works on and
 // across the heads' borders; no other warp waits for it until a head ends.
 //
 // Measured (of the copy bandwidth, head_dim 128): BF16 64 ragged sequences of up to
-// 8192 x 8 heads 182 us (0.93), E4M3 103 us (0.84); NVFP4 4 x 131072 x 8 heads 125 us
+// 8192 x 8 heads 180 us (0.94), E4M3 102 us (0.85); NVFP4 4 x 131072 x 8 heads 125 us
 // (0.71).  What is left of NVFP4 are instructions: a unit of 16 tokens takes about 330,
 // 64 conversions and 64 multiplications by scales among them, at 2.4 a cycle.  16 warps
 // per SM of 128 registers beat 12 of 168 (131 us against 159 at that time); stages of
@@ -66,13 +66,21 @@ struct AttnParams {
     const float *gs_k, *gs_v;
     __nv_bfloat16 *out;         // [B, q_heads, D]
     float *lse;                 // [B, q_heads] or NULL
-    uint32_t *counters;         // [grid], zero before and after
+    uint32_t *counters;         // [3][kAttnMaxCtas], zero before and after
     float *partial;             // [grid][2] pieces
     uint32_t *status;
 #ifdef QFP4_FAULT_INJECTION
     bool skip_copy;
 #endif
 };
+
+// CTAs that the workspace is sized for at most: 152 SMs, eight on each.
+constexpr int kAttnMaxCtas = 152 * 8;
+
+// Pieces that are joined at a time: an item's all, or groups of them whose joined pieces
+// are joined in turn (one sequence of 131072 tokens with one key head, 304 to 608 pieces:
+// NVFP4 16 us, 38 all at once; BF16 26, 78).
+__device__ __forceinline__ int attn_join_group(int pieces) { return pieces <= 24 ? pieces : pieces <= 256 ? 16 : 32; }
 
 // Space of a piece in the workspace: o, then m and l of each query.
 __host__ __device__ constexpr int attn_piece_floats(int queries, int D) { return queries * (D + 2); }
@@ -204,6 +212,12 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
     __shared__ int64_t s_start[2];      // the CTA's first tile: sequence, tile within it
     __shared__ int64_t s_total;         // tiles of the whole line
     __shared__ uint32_t s_last;
+    // items that lie across CTAs and a group of whose pieces this CTA completed: CTAs of the
+    // pieces, and the first of the group; n = 0 for none
+    struct Late {
+        int b, head, block, c0, n, first;
+    };
+    __shared__ Late s_late[2];
     float *s_o = reinterpret_cast<float *>(smem + C::RING);                     // [QUERIES][D + 4]
     float2 *s_ml = reinterpret_cast<float2 *>(s_o + C::SUMS * C::SUM);         // [warps][QUERIES]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -241,6 +255,7 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
         lo = shares.begin_of(blockIdx.x);
         hi = shares.begin_of(blockIdx.x + 1);
         if (tid == 0) s_total = total;
+        if (tid < 2) s_late[tid].n = 0;
     }
     if (warp == 0) {
         int64_t before = 0;
@@ -338,11 +353,6 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
     bool dead = false;
     const float gs_k = TYPE == QFP4_CACHE_NVFP4 ? *p.gs_k : 1.0f, gs_v = TYPE == QFP4_CACHE_NVFP4 ? *p.gs_v : 1.0f;
     int64_t at = lo;
-    // items that lie across CTAs and whose last piece this CTA wrote
-    struct Late {
-        int b, head, block, c0, n;
-    };
-    Late late[2] = {};
 
     // The queries of the cursor's head as they are in memory: on their way while the
     // segment before is joined.
@@ -794,29 +804,36 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
                     make_uint2(pack_bf16(acc[4 * i] * inv, acc[4 * i + 1] * inv), pack_bf16(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
             if (p.lse && tid % PER == 0) p.lse[row] = m_ == -INFINITY ? -INFINITY : (m_ + log2f(l_)) * 0.693147180559945309f;
         };
+        auto write_piece = [&](float *to, float m_, float l_) {
+            if (!mine) return;
+#pragma unroll
+            for (int i = 0; i < DIMS / 4; ++i)
+                *reinterpret_cast<float4 *>(to + q * D + d0 + 4 * PER * i) =
+                    make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+            if (tid % PER == 0) *reinterpret_cast<float2 *>(to + QUERIES * D + 2 * q) = make_float2(m_, l_);
+        };
         if (whole) {
             write_out(b, head, qblock, m_all, l_all);
         } else {
-            if (mine) {
-#pragma unroll
-                for (int i = 0; i < DIMS / 4; ++i)
-                    *reinterpret_cast<float4 *>(piece + q * D + d0 + 4 * PER * i) =
-                        make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-                if (tid % PER == 0) *reinterpret_cast<float2 *>(piece + QUERIES * D + 2 * q) = make_float2(m_all, l_all);
-            }
+            write_piece(piece, m_all, l_all);
             // CTAs that hold the item's first and last tile
             const int64_t i0 = at - seg_n - seg_first, i1 = i0 + seg_tiles - 1;
             const Shares shares(p, s_total);
             const int64_t c0 = shares.cta_of(i0), c1 = shares.cta_of(i1);
+            const int pieces = static_cast<int>(c1 - c0) + 1, size = attn_join_group(pieces);
+            const int group = static_cast<int>(blockIdx.x - c0) / size, first = static_cast<int>(c0) + group * size;
+            // an item's first group has the counter of its first CTA, the others one of the
+            // second row: the last CTA of an item may be the first of the next
+            uint32_t *counter = p.counters + (group > 0 ? kAttnMaxCtas : 0) + first;
             // one thread releases the piece for all, who have met at the barrier, and
             // acquires the others' for all who meet at the next
             __syncthreads();
-            if (tid == 0) s_last = atom_add_acq_rel_gpu(p.counters + c0, 1u) == static_cast<uint32_t>(c1 - c0);
+            if (tid == 0) s_last = atom_add_acq_rel_gpu(counter, 1u) + 1 == static_cast<uint32_t>(min(size, pieces - group * size));
             __syncthreads();
-            if (s_last) {       // all pieces are there: joined when this CTA's own tiles are done
-                if (tid == 0) p.counters[c0] = 0;
-                const int which = seg_first != 0 ? 0 : 1;       // a CTA has two items in pieces at most
-                late[which] = Late{b, head, qblock, static_cast<int>(c0), static_cast<int>(c1 - c0) + 1};
+            if (s_last && tid == 0) {       // the group's pieces are there: joined when this CTA's own tiles are done
+                *counter = 0;
+                // a CTA has two items in pieces at most
+                s_late[seg_first == 0] = Late{b, head, qblock, static_cast<int>(c0), pieces, first};
             }
         }
         __syncthreads();
@@ -829,47 +846,65 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
         float *s_pieces = reinterpret_cast<float *>(smem);
 #pragma unroll 1
         for (int which = 0; which < 2; ++which) {
-            const Late w = late[which];
+            const Late w = s_late[which];
             if (w.n == 0) continue;
-            float m_ = -INFINITY, l_ = 0.0f;
-#pragma unroll
-            for (int i = 0; i < DIMS; ++i) acc[i] = 0.0f;
+            const int size = attn_join_group(w.n), groups = (w.n + size - 1) / size;
+            // a group's pieces; then, by the CTA that finishes last, the groups'
+            int first = w.first, count = min(size, w.c0 + w.n - w.first), step = 1;
 #pragma unroll 1
-            for (int first_c = 0; first_c < w.n; first_c += BATCH) {
-                const int n = min(BATCH, w.n - first_c);
-                for (int i = tid; i < n * CHUNKS; i += C::THREADS) {
-                    const int c = i / CHUNKS, pc = first_c + c;
-                    cp_async16(smem_u32(s_pieces + i * 4),
-                               p.partial + (2 * static_cast<int64_t>(w.c0 + pc) + (pc == 0)) * PIECE + (i - c * CHUNKS) * 4);
-                }
-                cp_async_wait_all();
-                __syncthreads();
-                float top = m_;
-#pragma unroll 8
-                for (int c = 0; c < n; ++c) top = max_nan(top, s_pieces[c * PIECE + QUERIES * D + 2 * q]);
-                const float f0 = m_ == -INFINITY ? 0.0f : exp2_fast(m_ - top);
-                m_ = top;
-                l_ *= f0;
+            for (;;) {
+                float m_ = -INFINITY, l_ = 0.0f;
 #pragma unroll
-                for (int i = 0; i < DIMS; ++i) acc[i] *= f0;
-#pragma unroll 4
-                for (int c = 0; c < n; ++c) {
-                    const float *pc = s_pieces + c * PIECE;
-                    const float2 ml = *reinterpret_cast<const float2 *>(pc + QUERIES * D + 2 * q);
-                    const float f = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - top);
-                    l_ += ml.y * f;
-#pragma unroll
-                    for (int i = 0; i < DIMS / 4; ++i) {
-                        const float4 v = *reinterpret_cast<const float4 *>(pc + q * D + d0 + 4 * PER * i);
-                        acc[4 * i] += v.x * f;
-                        acc[4 * i + 1] += v.y * f;
-                        acc[4 * i + 2] += v.z * f;
-                        acc[4 * i + 3] += v.w * f;
+                for (int i = 0; i < DIMS; ++i) acc[i] = 0.0f;
+#pragma unroll 1
+                for (int done = 0; done < count; done += BATCH) {
+                    const int n = min(BATCH, count - done);
+                    for (int i = tid; i < n * CHUNKS; i += C::THREADS) {
+                        const int c = i / CHUNKS, cta = first + (done + c) * step;
+                        cp_async16(smem_u32(s_pieces + i * 4),
+                                   p.partial + (2 * static_cast<int64_t>(cta) + (cta == w.c0)) * PIECE + (i - c * CHUNKS) * 4);
                     }
+                    cp_async_wait_all();
+                    __syncthreads();
+                    float top = m_;
+#pragma unroll 8
+                    for (int c = 0; c < n; ++c) top = max_nan(top, s_pieces[c * PIECE + QUERIES * D + 2 * q]);
+                    const float f0 = m_ == -INFINITY ? 0.0f : exp2_fast(m_ - top);
+                    m_ = top;
+                    l_ *= f0;
+#pragma unroll
+                    for (int i = 0; i < DIMS; ++i) acc[i] *= f0;
+#pragma unroll 4
+                    for (int c = 0; c < n; ++c) {
+                        const float *pc = s_pieces + c * PIECE;
+                        const float2 ml = *reinterpret_cast<const float2 *>(pc + QUERIES * D + 2 * q);
+                        const float f = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - top);
+                        l_ += ml.y * f;
+#pragma unroll
+                        for (int i = 0; i < DIMS / 4; ++i) {
+                            const float4 v = *reinterpret_cast<const float4 *>(pc + q * D + d0 + 4 * PER * i);
+                            acc[4 * i] += v.x * f;
+                            acc[4 * i + 1] += v.y * f;
+                            acc[4 * i + 2] += v.z * f;
+                            acc[4 * i + 3] += v.w * f;
+                        }
+                    }
+                    __syncthreads();
                 }
+                if (step > 1 || groups == 1) {
+                    write_out(w.b, w.head, w.block, m_, l_);
+                    break;
+                }
+                // in the place of the group's first piece, which has been read
+                write_piece(p.partial + (2 * static_cast<int64_t>(first) + (first == w.c0)) * PIECE, m_, l_);
+                uint32_t *counter = p.counters + 2 * kAttnMaxCtas + w.c0;
                 __syncthreads();
+                if (tid == 0) s_last = atom_add_acq_rel_gpu(counter, 1u) + 1 == static_cast<uint32_t>(groups);
+                __syncthreads();
+                if (!s_last) break;
+                if (tid == 0) *counter = 0;
+                first = w.c0, count = groups, step = size;
             }
-            write_out(w.b, w.head, w.block, m_, l_);
         }
     }
     if (dead) {     // copies in flight have time to land before the shared memory goes to another CTA
@@ -910,24 +945,24 @@ int attn_launch_one(const AttnParams &p, int most, cudaStream_t s)
     return launch_status(launch_pdl(kernel, dim3(152 * n), dim3(C::THREADS), C::SMEM, s, p));
 }
 
-// Items (sequences x key heads x blocks of queries), above which the CTAs have two warps.
-constexpr int64_t kManyItems = 4 * 152;
-
-// CTAs that an SM takes at most.
-inline int attn_most_per_sm(int64_t items) { return items > kManyItems ? 8 : 4; }
+// CTAs that an SM takes at most: twice as many, of two warps, for many items (sequences
+// x key heads x blocks of queries).
+inline bool attn_many(int64_t items, int nt) { return items > (nt == 2 ? 2 : 4) * 152; }
+inline int attn_most_per_sm(int64_t items, int nt) { return attn_many(items, nt) ? 8 : 4; }
 
 // Four warps a CTA, four CTAs on an SM.  Many items: two warps and twice as many CTAs,
 // which hide one another's joins (256 ragged sequences up to 300 tokens x 8 heads: NVFP4
 // 26.4 us, 29.2 with four; E4M3 32.3, 36.2; up to 2000 tokens 81, 86 and 105, 109; one
-// warp 28, 36, 83, 109; 512 items up to 300 tokens 14.4, 13.5).  Few items in NVFP4: eight
+// warp 28, 36, 83, 109; 512 items up to 300 tokens 14.4, 13.5; 512 items of 16 query heads
+// up to 1000 tokens E4M3 30, 41, and 128 of up to 16384 as long with either).  Few items in NVFP4: eight
 // warps, two CTAs on an SM, half as many pieces to join (1 x 4096 tokens x 8 heads 11 us, 16
 // with four warps; 1 x 131072 48, 55).
 template <int TYPE, int D, int NT>
 int attn_launch(const AttnParams &p, cudaStream_t s)
 {
     const int64_t items = static_cast<int64_t>(p.B) * p.kv_heads * p.blocks;
-    const int most = attn_most_per_sm(items);
-    if (items > kManyItems) return attn_launch_one<TYPE, D, NT, 2>(p, most, s);
+    const int most = attn_most_per_sm(items, NT);
+    if (attn_many(items, NT)) return attn_launch_one<TYPE, D, NT, 2>(p, most, s);
     if constexpr (TYPE == QFP4_CACHE_NVFP4 && D <= 128) {
         if (items <= 2 * 152) return attn_launch_one<TYPE, D, NT, 8>(p, most, s);
     }

@@ -152,6 +152,19 @@ def test_long(type):
     Case(type, [33000, 5, 20011], 16, 2, 128, 64, seed=5).check()
 
 
+@pytest.mark.parametrize("H,KV,D,lens", [(8, 1, 128, [131072]), (16, 1, 128, [50000, 3, 0, 70001]), (3, 1, 256, [60000, 20000]), (8, 2, 64, [40000, 40000, 17]),
+                                         (12, 1, 64, [1] * 700 + [30000, 9000])])
+@pytest.mark.parametrize("type", _cache.TYPES)
+def test_many_pieces(type, H, KV, D, lens):
+    """Heads that hundreds of CTAs share, whose pieces are joined in groups; the same bits every time, and every counter at zero again."""
+    c = Case(type, lens, H, KV, D, 16, seed=len(lens) + H)
+    o, lse = c.check()
+    for _ in range(3):
+        o2, lse2 = c.run()
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert not c.ws[:16384].any()
+
+
 @pytest.mark.parametrize("garbage", [0x00, 0x7F, 0x7E, 0xFF])
 @pytest.mark.parametrize("type", _cache.TYPES)
 def test_what_lies_beyond_the_length_does_not_count(type, garbage):
