@@ -233,17 +233,29 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
 
     // ---- the CTA's piece of the line of tiles
     const int items = p.kv_heads * p.blocks;
+    // `per` neighbouring sequences for each thread: its tiles, and where they begin in its warp's
+    const int per = (p.B + C::THREADS - 1) / C::THREADS;
     int64_t mine = 0;
-    for (int b = tid; b < p.B; b += C::THREADS) {
+    bool bad = false;
+#pragma unroll 4
+    for (int b = tid * per; b < min(p.B, (tid + 1) * per); ++b) {
         int first, len;
-        const int length = p.lengths[b];
+        const int length = __ldg(p.lengths + b);
         Cursor::extent(p, length, first, len);
-        if (length != len && blockIdx.x == 0) atomicOr(p.status, kStatusBadGroup);
+        bad |= length != len;
         mine += static_cast<int64_t>(items) * Cursor::count<TILE>(first, len);
     }
+    if (bad && blockIdx.x == 0) atomicOr(p.status, kStatusBadGroup);
+    auto sums_up_to = [lane](int64_t v) {       // of the warp's lanes
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    if (lane == 0) s_sum[warp] = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        return v;
+    };
+    const int64_t mine_upto = sums_up_to(mine);
+    if (lane == 31) s_sum[warp] = mine_upto;
     __syncthreads();
     int64_t total = 0;
 #pragma unroll
@@ -257,29 +269,33 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
         if (tid == 0) s_total = total;
         if (tid < 2) s_late[tid].n = 0;
     }
-    if (warp == 0) {
-        int64_t before = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
+    // the thread whose sequences hold the first tile; then the sequence, by its warp
+    int64_t from = mine_upto - mine;
+    for (int i = 0; i < warp; ++i) from += s_sum[i];
+    const bool here = lo >= from && lo < from + mine;
+    const uint32_t holds = __ballot_sync(0xffffffffu, here);
+    if (here && per == 1) {
+        s_start[0] = tid;
+        s_start[1] = lo - from;
+    }
+    if (holds && per > 1) {
+        const int which = __ffs(static_cast<int>(holds)) - 1, b1 = min(p.B, (warp * 32 + which + 1) * per);
+        from = __shfl_sync(0xffffffffu, from, which);
+        for (int b0 = (warp * 32 + which) * per; b0 < b1; b0 += 32) {
             const int b = b0 + lane;
             int64_t n = 0;
-            if (b < p.B) {
+            if (b < b1) {
                 int first, len;
-                Cursor::extent(p, p.lengths[b], first, len);
+                Cursor::extent(p, __ldg(p.lengths + b), first, len);
                 n = static_cast<int64_t>(items) * Cursor::count<TILE>(first, len);
             }
-            int64_t upto = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += v;
-            }
-            upto += before;
+            const int64_t upto = from + sums_up_to(n);
             if (n > 0 && lo >= upto - n && lo < upto) {
                 s_start[0] = b;
                 s_start[1] = lo - (upto - n);
             }
-            before = __shfl_sync(0xffffffffu, upto, 31);
-            if (before > lo) break;
+            from = __shfl_sync(0xffffffffu, upto, 31);
+            if (from > lo) break;
         }
     }
     __syncthreads();

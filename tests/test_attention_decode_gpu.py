@@ -146,6 +146,16 @@ def test_many_sequences(type):
     Case(type, lens, 8, 2, 64, 16, seed=4).check()
 
 
+@pytest.mark.parametrize("KV,window", [(1, 0), (2, 9)])
+def test_thousands_of_sequences(KV, window):
+    """Many sequences for each thread that looks for a CTA's first tile, long runs of empty ones among them."""
+    g = torch.Generator().manual_seed(KV)
+    lens = torch.randint(0, 40, (1501,), generator=g)
+    lens[100:700] = 0
+    lens[-3:] = torch.tensor([700, 0, 333])
+    Case(qfp4.CACHE_E4M3, lens.tolist(), 4, KV, 64, 16, seed=KV).check(window)
+
+
 @pytest.mark.parametrize("type", _cache.TYPES)
 def test_long(type):
     """Few sequences, each split over many CTAs."""
