@@ -580,20 +580,26 @@ def gemv_nt(fmt, X, W, W_sf, gs_w, D, stream=None) -> None:
     """D = X W^T: up to 16 BF16 rows X [M, K] times 4-bit weights W [N, K/2] with
     scales in the MMA layout (B of gemm_nt); gs_w may be None."""
     M, K = X.shape
-    N = W.shape[0]
-    if W.shape[1] * 2 != K:
-        raise ValueError(f"qfp4: W has {W.shape[1] * 2} columns, X {K}")
+    N, row = W.shape
+    if row * 2 != K:
+        raise ValueError(f"qfp4: W has {row * 2} columns, X {K}")
     x, ldx = _rows(X, K, M)
     d, ldd = _rows(D, N, M)
     g = 16 if fmt == NVFP4 else 32
-    _call("qfp4_gemv_nt", fmt, M, N, K, x, ldx, _at(W, _U8, N * K // 2),
+    _call("qfp4_gemv_nt", fmt, M, N, K, x, ldx, _at(W, _U8, N * row),
           _at(W_sf, _U8, (N + 127) // 128 * 128 * ((K // g + 3) // 4 * 4)), _at(gs_w, _F32, 1), d, ldd, _stream(stream))
 
 
-def _head_args(QKV, q_heads, kv_heads, head_dim, value_heads, q_weight, k_weight, cos_sin, positions, eps,
+def _space(t):
+    """(address, bytes) of a workspace, of whatever type."""
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError("qfp4: tensors must be contiguous and on the GPU")
+    return t.data_ptr(), t.nbytes
+
+
+def _head_args(QKV, T, width, q_heads, kv_heads, head_dim, value_heads, q_weight, k_weight, cos_sin, positions, eps,
                interleaved):
     """What the calls on query and key heads share, in the C ABI's order."""
-    T, width = QKV.shape
     if width < (q_heads + kv_heads + value_heads) * head_dim:
         raise ValueError(f"qfp4: {q_heads} + {kv_heads} heads of {head_dim} do not fit in rows of {width}")
     x, ld = _rows(QKV, width, T)
@@ -608,8 +614,8 @@ def qk_norm_rope(QKV, q_heads, kv_heads, Q_out, K_out, q_weight=None, k_weight=N
     by cos_sin [positions, rotary_dim] (None: none), from the QKV projection's
     output [T, (q_heads + kv_heads + ...) * head_dim].  Q_out [T, q_heads,
     head_dim] and K_out [T, kv_heads, head_dim] may be views of QKV itself."""
-    T, D = QKV.shape[0], Q_out.shape[2]
-    args = _head_args(QKV, q_heads, kv_heads, D, 0, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    (T, width), D = QKV.shape, Q_out.shape[2]
+    args = _head_args(QKV, T, width, q_heads, kv_heads, D, 0, q_weight, k_weight, cos_sin, positions, eps, interleaved)
     q, ldq = _rows(Q_out, q_heads * D, T)
     k, ldk = _rows(K_out, kv_heads * D, T)
     _call("qfp4_qk_norm_rope", *args, q, ldq, k, ldk, _stream(stream))
@@ -625,14 +631,12 @@ def qk_norm_rope_backward(QKV, q_heads, kv_heads, dQ, dK, dQKV, dq_weight, dk_we
     """Gradient of qk_norm_rope: the query and key heads of dQKV (its value heads
     stay) and, fp32 [head_dim], those of the weights; without weights they and
     the workspace may be None."""
-    T, D = QKV.shape[0], dQ.shape[2]
-    args = _head_args(QKV, q_heads, kv_heads, D, 0, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    (T, width), D = QKV.shape, dQ.shape[2]
+    args = _head_args(QKV, T, width, q_heads, kv_heads, D, 0, q_weight, k_weight, cos_sin, positions, eps, interleaved)
     q, ldq = _rows(dQ, q_heads * D, T)
     k, ldk = _rows(dK, kv_heads * D, T)
-    if dQKV.shape != QKV.shape:
-        raise ValueError(f"qfp4: dQKV is {tuple(dQKV.shape)}, QKV {tuple(QKV.shape)}")
-    dx, ldx = _rows(dQKV, QKV.shape[1], T)
-    ws, nbytes = (0, 0) if workspace is None else (_at(workspace, workspace.dtype), workspace.nbytes)
+    dx, ldx = _rows(dQKV, width, T)
+    ws, nbytes = (0, 0) if workspace is None else _space(workspace)
     _call("qfp4_qk_norm_rope_backward", *args, q, ldq, k, ldk, dx, ldx, _at(dq_weight, _F32, D),
           _at(dk_weight, _F32, D), ws, nbytes, _stream(stream))
 
@@ -648,10 +652,9 @@ _CACHE_TOKEN = {CACHE_BF16: (32, 0), CACHE_E4M3: (16, 64), CACHE_NVFP4: (9, 0)} 
 def _cache(type, cache, kv_heads, D, page_size):
     """(address, pages) of a cache whose pages have that layout's size."""
     pages, token = cache.shape[0], _CACHE_TOKEN.get(type)
-    if token is not None:
-        page = (token[0] * D + token[1]) // 8 * kv_heads * page_size
-        if cache.numel() != pages * page:
-            raise ValueError(f"qfp4: a page of this cache has {page} bytes, got {tuple(cache.shape)}")
+    page = (token[0] * D + token[1]) // 8 * kv_heads * page_size if token else 0
+    if cache.numel() != pages * page and token:
+        raise ValueError(f"qfp4: a page of this cache has {page} bytes, got {tuple(cache.shape)}")
     return _at(cache, _U8), pages
 
 
@@ -683,8 +686,8 @@ def qk_norm_rope_cache(QKV, q_heads, kv_heads, Q_out, type, cache, page_size, sl
                        stream=None) -> None:
     """qk_norm_rope with the keys and the value heads behind them quantised
     straight into the cache."""
-    T, D = QKV.shape[0], Q_out.shape[2]
-    args = _head_args(QKV, q_heads, kv_heads, D, kv_heads, q_weight, k_weight, cos_sin, positions, eps, interleaved)
+    (T, width), D = QKV.shape, Q_out.shape[2]
+    args = _head_args(QKV, T, width, q_heads, kv_heads, D, kv_heads, q_weight, k_weight, cos_sin, positions, eps, interleaved)
     q, ldq = _rows(Q_out, q_heads * D, T)
     c, pages = _cache(type, cache, kv_heads, D, page_size)
     _call("qfp4_qk_norm_rope_cache", *args, q, ldq, type, c, pages, page_size, _at(slots, _I32, T),
@@ -705,9 +708,9 @@ def attention_decode(type, Q, cache, page_size, page_table, lengths, scale, O, w
     heads = cache.shape[1] if kv_heads is None else kv_heads
     q, ldq = _rows(Q, H * D, B)
     c, pages = _cache(type, cache, heads, D, page_size)
-    if page_table.shape[0] != B:
-        raise ValueError(f"qfp4: page_table has {page_table.shape[0]} rows for {B} sequences")
+    rows, max_pages = page_table.shape
+    if rows != B:
+        raise ValueError(f"qfp4: page_table has {rows} rows for {B} sequences")
     _call("qfp4_attention_decode", type, q, ldq, B, H, heads, D, c, pages, page_size, _at(page_table, _I32),
-          page_table.shape[1], _at(lengths, _I32, B), window, scale, _at(gs_k, _F32, 1), _at(gs_v, _F32, 1),
-          _at(O, _BF16, B * H * D), _at(lse, _F32, B * H), _at(workspace, workspace.dtype), workspace.nbytes,
-          _stream(stream))
+          max_pages, _at(lengths, _I32, B), window, scale, _at(gs_k, _F32, 1), _at(gs_v, _F32, 1),
+          _at(O, _BF16, B * H * D), _at(lse, _F32, B * H), *_space(workspace), _stream(stream))
