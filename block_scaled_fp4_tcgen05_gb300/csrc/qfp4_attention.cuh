@@ -315,11 +315,11 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
     struct Unit {
         int page, place;
     };
-    const int lane_token = lane < UNITS ? warp * C::TOKENS + 16 * lane : INT32_MAX / 2;
+    const int lane_token = warp * C::TOKENS + 16 * lane;
     auto unit_of = [&](const Cursor &c) {
         const int token = c.first + c.tile * TILE + lane_token;
         Unit u{-1, -1};
-        if (token < c.len) {
+        if (lane < UNITS && token < c.len) {        // a stage has room for UNITS
             const uint32_t n = static_cast<uint32_t>(token) / 16;
             const uint32_t page = static_cast<uint32_t>(n * p.page_magic >> 36);
             u.page = p.page_table[static_cast<int64_t>(c.b) * p.max_pages + page];
