@@ -640,7 +640,8 @@ __global__ void __launch_bounds__(kThreads, kBackCtas) head_backward_kernel(cons
                             ss = f2_fma(h.b[k], h.b[k], f2_fma(h.a[k], h.a[k], ss));
                             dot = f2_fma(gw.b[k], h.b[k], f2_fma(gw.a[k], h.a[k], dot));
                         }
-                        const float r = rsqrtf(group_sum<LANES>(f2_sum(ss)) * p.inv_D + p.eps);
+                        // no vector: with eps = 0 its root would be that of 0, and the weights' sums NaN
+                        const float sum = group_sum<LANES>(f2_sum(ss)), r = live ? rsqrtf(sum * p.inv_D + p.eps) : 0.0f;
                         const float mean = group_sum<LANES>(f2_sum(dot)) * r * p.inv_D;
                         const uint64_t r2 = f2_pack(r, r), m2 = f2_pack(-mean * r, -mean * r);
 #pragma unroll
