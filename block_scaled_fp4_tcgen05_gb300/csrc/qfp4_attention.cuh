@@ -564,7 +564,8 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
                 // ---- what the exponents are taken relative to.  It moves only when a logit
                 // lies more than kSlack above it (weights up to 2^kSlack are as exact in
                 // FP16 as those up to 1), to the maximum of the logits so far; with value
-                // scales, that of x + log2 s as well.  A NaN moves it too.
+                // scales, that of x + log2 s as well.  A NaN moves it too.  The limit is rounded
+                // down: at logits whose last bit is 16 it would be 16 above, beyond FP16.
                 bool above = false;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -574,8 +575,8 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
                         for (int un = 0; un < UNITS; ++un)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                above |= !(x[un][n][2 * h + k] <= m[n][k] + kSlack);
-                                if (TYPE == QFP4_CACHE_E4M3) above |= !(x[un][n][2 * h + k] + ls[un][h] <= mw[n][k] + kSlack);
+                                above |= !(x[un][n][2 * h + k] <= __fadd_rd(m[n][k], kSlack));
+                                if (TYPE == QFP4_CACHE_E4M3) above |= !(x[un][n][2 * h + k] + ls[un][h] <= __fadd_rd(mw[n][k], kSlack));
                             }
                 if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
