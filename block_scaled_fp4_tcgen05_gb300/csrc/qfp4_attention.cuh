@@ -4,8 +4,8 @@
 //
 //   x_j = scale q . k_j (in units of log 2),  p_j = 2^(x_j - m),
 //   o = sum p_j v_j / sum p_j,  lse = ln 2 (m + log2 sum p_j)
-// in one pass over the cache, with m (the largest x_j, or up to kSlack below it), the
-// sums and o in fp32 registers.
+// in one pass over the cache, with m, the sums and o in fp32 registers.  m follows the
+// largest x_j (attn_headroom below it, and up to kSlack more).
 //
 // Bound by the cache's bytes.  A warp takes 16 tokens as the rows of a tensor
 // core product with up to 8 (or 16) query heads that share the key head as its
@@ -16,9 +16,10 @@
 // UE4M3 scales have at most 6 significant bits and are exact in FP16.  Queries
 // become FP16 too, each multiplied by the power of two that takes its largest
 // element to [2^14, 2^15): what lies 2^28 below that loses bits, 2^-39 of the
-// largest at most.  p is rounded to FP16 (2^-11 of it at most); an E4M3 token's value
-// scale s joins it as 2^(x + log2 s - m'), m' the like of m for that exponent, so that
-// no range of scales is lost.  With a BF16 cache the operands are BF16 and p is the
+// largest at most.  p is rounded to FP16: 2^-11 of it, or 2^-25, 2^-32 of the largest
+// p at most, which lies between 2^7 and 2^15.  An E4M3 token's value scale s joins it as
+// 2^(x + log2 s - m'), m' the like of m for that exponent, so that no range of scales
+// is lost.  With a BF16 cache the operands are BF16 and p is the
 // sum of two (2^-16).
 //
 // The tokens of all sequences and heads are one line of tiles; each CTA takes an
@@ -92,7 +93,11 @@ constexpr int attn_stage_tokens(int type, int D)
     return type == QFP4_CACHE_BF16 ? (D == 64 ? 32 : 16) : D == 64 ? 64 : D == 128 ? 32 : 16;
 }
 constexpr int kAttnStages = 2;
+// How far the largest exponent lies above its base when that moves, and how much further
+// it may rise before it moves again: weights of 2^7 to 2^15 leave FP16 the range below for
+// the small ones.  A BF16 cache's weights have BF16's range.
 constexpr float kSlack = 8.0f;
+constexpr float attn_headroom(int type) { return type == QFP4_CACHE_BF16 ? 0.0f : 7.0f; }
 constexpr int attn_ctas(int type, int D, int nt, int warps)
 {
     return (D == 256 ? (type == QFP4_CACHE_NVFP4 ? 12 : 8) : nt == 2 ? 8 : 16) / warps;
@@ -105,6 +110,7 @@ struct AttnCfg {
     static constexpr int WARPS = WARPS_, THREADS = 32 * WARPS;
     static constexpr int TILE = TOKENS * WARPS;
     static constexpr int QUERIES = 8 * NT;
+    static constexpr float HEADROOM = attn_headroom(TYPE);
     static constexpr int RING = WARPS * STAGES * STAGE;
     // Where the warps' results meet: half of them side by side, or one after the
     // other where more would cost a CTA per SM.
@@ -562,10 +568,12 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
                         }
                 }
                 // ---- what the exponents are taken relative to.  It moves only when a logit
-                // lies more than kSlack above it (weights up to 2^kSlack are as exact in
-                // FP16 as those up to 1), to the maximum of the logits so far; with value
-                // scales, that of x + log2 s as well.  A NaN moves it too.  The limit is rounded
-                // down: at logits whose last bit is 16 it would be 16 above, beyond FP16.
+                // lies more than the headroom and kSlack above it (the weights are as exact in
+                // FP16 there), to the headroom below the maximum of the logits so far; with
+                // value scales it is that of x + log2 s which matters for FP16, and moves so.  A
+                // NaN moves it too.  The limit is rounded down: at logits whose last bit is 16 it
+                // would be 16 above, beyond FP16.
+                constexpr float HEAD_W = C::HEADROOM, HEAD = TYPE == QFP4_CACHE_E4M3 ? 0.0f : HEAD_W;
                 bool above = false;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -575,8 +583,8 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
                         for (int un = 0; un < UNITS; ++un)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                above |= !(x[un][n][2 * h + k] <= __fadd_rd(m[n][k], kSlack));
-                                if (TYPE == QFP4_CACHE_E4M3) above |= !(x[un][n][2 * h + k] + ls[un][h] <= __fadd_rd(mw[n][k], kSlack));
+                                above |= !(x[un][n][2 * h + k] <= __fadd_rd(m[n][k], HEAD + kSlack));
+                                if (TYPE == QFP4_CACHE_E4M3) above |= !(x[un][n][2 * h + k] + ls[un][h] <= __fadd_rd(mw[n][k], HEAD_W + kSlack));
                             }
                 if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
@@ -596,13 +604,13 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
                                 top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, s));
                                 if (TYPE == QFP4_CACHE_E4M3) top_w = max_nan(top_w, __shfl_xor_sync(0xffffffffu, top_w, s));
                             }
-                            const float m_new = max_nan(m[n][k], top);
+                            const float m_new = max_nan(m[n][k], top - HEAD);
                             base[n][k] = m_new == -INFINITY ? 0.0f : m_new;
                             alpha[k] = exp2_fast(m[n][k] - base[n][k]);
                             l[n][k] *= alpha[k];
                             m[n][k] = m_new;
                             if (TYPE == QFP4_CACHE_E4M3) {
-                                const float w_new = max_nan(mw[n][k], top_w);
+                                const float w_new = max_nan(mw[n][k], top_w - HEAD_W);
                                 base_w[n][k] = w_new == -INFINITY ? 0.0f : w_new;
                                 alpha[k] = exp2_fast(mw[n][k] - base_w[n][k]);
                                 mw[n][k] = w_new;

@@ -843,8 +843,9 @@ int qfp4_qk_norm_rope_cache(const void *QKV_bf16, int64_t ld, int64_t T, int64_t
  *              workspace, graphs that captured one included.
  * Products and sums in fp32.  The queries enter the products in FP16 (E4M3,
  * NVFP4 cache), scaled so that an element loses bits only 2^28 below the largest
- * of its head; the weights are rounded to FP16 (2^-11 of each, 2^-25 of the
- * largest at least) or, with a BF16 cache, to 16 bits.  Results repeat bit for bit.
+ * of its head; the weights are rounded to FP16 (2^-11 of each, or up to 2^-32 of
+ * the largest; E4M3: of the weights times their values' scales) or, with a BF16
+ * cache, to 16 bits.  Results repeat bit for bit.
  * An infinite value that counts gives NaN (a weight times it is added in two parts),
  * as infinite logits do.
  * Requirements: cache sizes as above, q_heads a multiple of kv_heads, at most

@@ -1,4 +1,11 @@
-"""Attention of one new token where its arithmetic has little room."""
+"""Attention of one new token where its arithmetic has little room: logits whose
+last bit is 16, weights far below a sequence's largest.
+
+Bounds as in test_attention_decode_gpu.py: half a step of BF16, 2^-8 |o|; the
+logits' error twice over and the rounding of each weight to FP16, (2^-11 + 2^-17
+(1 + T)) sum p|v| / S; and 2^-32 of the largest weight for each weight that lies
+below FP16's normal range, with its value: 2^-32 sum |v| / S (E4M3: each weight
+has its value's scale in it, so 2^-32 n max(p |v|) / S)."""
 import math
 
 import numpy as np
@@ -59,3 +66,34 @@ def test_logits_whose_last_bit_is_16(type, period):
     assert (vv == v).all()
     assert ((o - v[0].double()).abs() <= (2.0 ** -8 + 2.0 ** -11) * v[0].double()).all(), o
     assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("every,n", [(64, 17), (64, 32), (16, 5000)])
+@pytest.mark.parametrize("below", [12, 18, 21, 23, 25])
+@pytest.mark.parametrize("type", _cache.TYPES)
+def test_values_far_below_the_largest_weight(type, below, every, n):
+    """A token in every so many whose weight is 2^below times that of the others, and
+    whose value is zero: the others' values alone make up the result."""
+    g = torch.Generator(device="cuda").manual_seed(n + below)
+    H, D = 8, 128
+    q = torch.randn(H, D, generator=g, device="cuda").sign().bfloat16().float()
+    q[:, :64] = 1.0
+    k = torch.zeros(n, 1, D, device="cuda")
+    k[::every, 0, :64] = 1.0
+    v = torch.randn(n, 1, D, generator=g, device="cuda")
+    v[::every] = 0.0
+    scale = below * math.log(2.0) / 64
+    o, lse, kv, vv = attend(type, q, k, v.bfloat16().float(), scale, 0.01 if type == qfp4.CACHE_NVFP4 else 1.0)
+    kv, vv = kv[:, 0], vv[:, 0]
+    x = q.double() @ kv.t() * float(np.float32(scale))
+    T = (q.double().abs() @ kv.abs().t() * float(np.float32(scale))).amax(-1, keepdim=True)
+    p = torch.exp(x - x.amax(-1, keepdim=True))
+    S = p.sum(-1, keepdim=True)
+    want, size = p @ vv / S, p @ vv.abs() / S
+    if type == qfp4.CACHE_E4M3:
+        lost = 2.0 ** -32 * n * (p * vv.abs().amax(-1)).amax(-1, keepdim=True) / S
+    else:
+        lost = 2.0 ** -32 * vv.abs().sum(0) / S
+    bound = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -17 * (1 + T)) * size + lost
+    assert ((o - want).abs() <= bound).all(), float(((o - want).abs() / bound).max())
+    assert ((lse - torch.logsumexp(x, -1)).abs() <= 2.0 ** -18 * T[:, 0] + 2.0 ** -20 + 2.0 ** -22 * lse.abs()).all()
