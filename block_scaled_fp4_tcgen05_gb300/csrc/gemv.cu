@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(GemvCfg<FMT, NT>::THREADS, 1) gemv_kernel(cons
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            int e = 8 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127);
-            e = amax == 0.0f || !(amax < 3.4e38f) ? 0 : max(-126, min(126, e));
+            // an infinity takes everything beside it into FP16's range, so that it alone counts
+            const int e = min(126, 8 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127));
             const float up = pow2(e);
             if (lane == 0) s_back[sl * p.M + m] = pow2(-e);
 #pragma unroll
