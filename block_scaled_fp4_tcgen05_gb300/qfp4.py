@@ -550,24 +550,24 @@ def moe_route_backward(logits, ids, counts, n_valid, dgates, dloss, dlogits, val
           _at(dloss, _F32, 1), _at(dlogits, logits.dtype, T * E), _stream(stream))
 
 
-def _rows(t, want):
-    """(address, elements from row to row) of BF16 rows that lie together, of the
-    shape [rows, width] or [rows, heads, elements]: a contiguous matrix, or some
-    columns of one (the heads of one kind in a projection's output).  The heads may
-    also be given as one row.  The usual path asks each question once."""
-    rows, width = want[0], want[1] if len(want) == 2 else want[1] * want[2]
+def _rows(t, width, want=None):
+    """(address, elements from row to row) of BF16 rows of `width` elements that lie
+    together: a contiguous matrix, or some columns of one (the heads of one kind in a
+    projection's output).  want: (rows, width) or (rows, heads, elements of each); the
+    heads may also be given as one row.  None: the shape that the tensor has, where the
+    call's sizes were taken from it.  The usual path asks each question once."""
     if t is None:
         return 0, width
-    shape = t.shape
-    if t.dtype is _BF16 and t.is_cuda and shape == want and t.is_contiguous():
+    if t.dtype is _BF16 and t.is_cuda and (want is None or t.shape == want) and t.is_contiguous():
         return t.data_ptr(), width
     if t.dtype is not _BF16 or not t.is_cuda:
         raise ValueError(f"qfp4: expected {_BF16} on the GPU, got {t.dtype} on {t.device}")
-    stride = t.stride()
+    shape, stride = t.shape, t.stride()
+    rows = shape[0] if want is None else want[0]
     if len(shape) == 3:
         if shape[2] != 1 and stride[2] != 1 or shape[1] != 1 and stride[1] != shape[2]:
             raise ValueError("qfp4: the heads of a row must lie together")
-        if len(want) == 3 and shape[2] != want[2]:
+        if want is not None and len(want) == 3 and shape[2] != want[2]:
             raise ValueError(f"qfp4: expected heads of {want[2]} elements, got {tuple(shape)}")
         got = shape[1] * shape[2]
     elif len(shape) == 2:
@@ -588,8 +588,8 @@ def gemv_nt(fmt, X, W, W_sf, gs_w, D, stream=None) -> None:
     N, row = W.shape
     if row * 2 != K:
         raise ValueError(f"qfp4: W has {row * 2} columns, X {K}")
-    x, ldx = _rows(X, (M, K))
-    d, ldd = _rows(D, (M, N))
+    x, ldx = _rows(X, K)
+    d, ldd = _rows(D, N, (M, N))
     g = 16 if fmt == NVFP4 else 32
     _call("qfp4_gemv_nt", fmt, M, N, K, x, ldx, _at(W, _U8, N * row),
           _at(W_sf, _U8, (N + 127) // 128 * 128 * ((K // g + 3) // 4 * 4)), _at(gs_w, _F32, 1), d, ldd, _stream(stream))
@@ -607,7 +607,7 @@ def _head_args(QKV, T, width, q_heads, kv_heads, head_dim, value_heads, q_weight
     """What the calls on query and key heads share, in the C ABI's order."""
     if width < (q_heads + kv_heads + value_heads) * head_dim:
         raise ValueError(f"qfp4: {q_heads} + {kv_heads} heads of {head_dim} do not fit in rows of {width}")
-    x, ld = _rows(QKV, (T, width))
+    x, ld = _rows(QKV, width)
     rows, rotary = (0, 0) if cos_sin is None else cos_sin.shape
     return (x, ld, T, q_heads, kv_heads, head_dim, _at(q_weight, _BF16, head_dim), _at(k_weight, _BF16, head_dim), eps,
             _at(cos_sin, _F32), rows, rotary, 1 if interleaved else 0, _at(positions, _I32, T))
@@ -621,8 +621,8 @@ def qk_norm_rope(QKV, q_heads, kv_heads, Q_out, K_out, q_weight=None, k_weight=N
     head_dim] and K_out [T, kv_heads, head_dim] may be views of QKV itself."""
     (T, width), D = QKV.shape, Q_out.shape[2]
     args = _head_args(QKV, T, width, q_heads, kv_heads, D, 0, q_weight, k_weight, cos_sin, positions, eps, interleaved)
-    q, ldq = _rows(Q_out, (T, q_heads, D))
-    k, ldk = _rows(K_out, (T, kv_heads, D))
+    q, ldq = _rows(Q_out, q_heads * D, (T, q_heads, D))
+    k, ldk = _rows(K_out, kv_heads * D, (T, kv_heads, D))
     _call("qfp4_qk_norm_rope", *args, q, ldq, k, ldk, _stream(stream))
 
 
@@ -638,9 +638,9 @@ def qk_norm_rope_backward(QKV, q_heads, kv_heads, dQ, dK, dQKV, dq_weight, dk_we
     the workspace may be None."""
     (T, width), D = QKV.shape, dQ.shape[2]
     args = _head_args(QKV, T, width, q_heads, kv_heads, D, 0, q_weight, k_weight, cos_sin, positions, eps, interleaved)
-    q, ldq = _rows(dQ, (T, q_heads, D))
-    k, ldk = _rows(dK, (T, kv_heads, D))
-    dx, ldx = _rows(dQKV, (T, width))
+    q, ldq = _rows(dQ, q_heads * D, (T, q_heads, D))
+    k, ldk = _rows(dK, kv_heads * D, (T, kv_heads, D))
+    dx, ldx = _rows(dQKV, width, (T, width))
     ws, nbytes = (0, 0) if workspace is None else _space(workspace)
     _call("qfp4_qk_norm_rope_backward", *args, q, ldq, k, ldk, dx, ldx, _at(dq_weight, _F32, D),
           _at(dk_weight, _F32, D), ws, nbytes, _stream(stream))
@@ -668,8 +668,8 @@ def kv_cache_write(type, K, V, slots, cache, page_size, gs_k=None, gs_v=None, st
     output, or whole) into the slots (int32 [T], negative: skipped) of the cache
     [pages, ...] (uint8, kv_cache_page_bytes per page)."""
     T, H, D = K.shape
-    k, ldk = _rows(K, (T, H, D))
-    v, ldv = _rows(V, (T, H, D))
+    k, ldk = _rows(K, H * D)
+    v, ldv = _rows(V, H * D, (T, H, D))
     c, pages = _cache(type, cache, H, D, page_size)
     _call("qfp4_kv_cache_write", type, k, ldk, v, ldv, T, H, D, _at(slots, _I32, T), _at(gs_k, _F32, 1),
           _at(gs_v, _F32, 1), c, pages, page_size, _stream(stream))
@@ -679,8 +679,8 @@ def kv_cache_read(type, cache, page_size, slots, K_out, V_out, gs_k=None, gs_v=N
     """The tokens at these slots in BF16, K_out and V_out [T, kv_heads, head_dim]
     (either may be None); a negative slot gives zeros."""
     T, H, D = (V_out if K_out is None else K_out).shape
-    k, ldk = _rows(K_out, (T, H, D))
-    v, ldv = _rows(V_out, (T, H, D))
+    k, ldk = _rows(K_out, H * D, (T, H, D))
+    v, ldv = _rows(V_out, H * D, (T, H, D))
     c, pages = _cache(type, cache, H, D, page_size)
     _call("qfp4_kv_cache_read", type, c, pages, page_size, H, D, _at(slots, _I32, T), T, _at(gs_k, _F32, 1),
           _at(gs_v, _F32, 1), k, ldk, v, ldv, _stream(stream))
@@ -693,7 +693,7 @@ def qk_norm_rope_cache(QKV, q_heads, kv_heads, Q_out, type, cache, page_size, sl
     straight into the cache."""
     (T, width), D = QKV.shape, Q_out.shape[2]
     args = _head_args(QKV, T, width, q_heads, kv_heads, D, kv_heads, q_weight, k_weight, cos_sin, positions, eps, interleaved)
-    q, ldq = _rows(Q_out, (T, q_heads, D))
+    q, ldq = _rows(Q_out, q_heads * D, (T, q_heads, D))
     c, pages = _cache(type, cache, kv_heads, D, page_size)
     _call("qfp4_qk_norm_rope_cache", *args, q, ldq, type, c, pages, page_size, _at(slots, _I32, T),
           _at(gs_k, _F32, 1), _at(gs_v, _F32, 1), _stream(stream))
@@ -711,7 +711,7 @@ def attention_decode(type, Q, cache, page_size, page_table, lengths, scale, O, w
     workspace is zeroed once, before its first use."""
     B, H, D = Q.shape
     heads = cache.shape[1] if kv_heads is None else kv_heads
-    q, ldq = _rows(Q, (B, H, D))
+    q, ldq = _rows(Q, H * D)
     c, pages = _cache(type, cache, heads, D, page_size)
     rows, max_pages = page_table.shape
     if rows != B:
