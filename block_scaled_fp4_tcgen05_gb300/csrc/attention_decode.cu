@@ -1,6 +1,7 @@
 // attention_decode.cu -- entry points of the attention of one new token per
 // sequence over the paged cache (kernel: qfp4_attention.cuh).
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -50,8 +51,9 @@ extern "C" int qfp4_attention_decode(int type, const void *Q_bf16, int64_t ldq, 
                                      const float *gs_v, void *O_bf16, float *lse, void *workspace, size_t ws_bytes,
                                      void *stream)
 {
+    const float scale_log2 = scale * 1.44269504088896341f;
     if (!cache_type_ok(type) || B < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1 || pages < 0 || page_size < 1 ||
-        max_pages < 0 || window < 0 || ldq < q_heads * head_dim || !(scale > -3.0e38f && scale < 3.0e38f))
+        max_pages < 0 || window < 0 || ldq < q_heads * head_dim || !std::isfinite(scale_log2))
         return QFP4_ERR_INVALID_ARG;
     if (!sizes_ok(B, q_heads, kv_heads, head_dim) || page_size % 16 != 0 || page_size > 16384 || pages > INT32_MAX ||
         max_pages > kMaxLength / page_size || ldq % 8 != 0)
@@ -81,7 +83,7 @@ extern "C" int qfp4_attention_decode(int type, const void *Q_bf16, int64_t ldq, 
     p.window = static_cast<int32_t>(window < kMaxLength ? window : 0);
     p.page_table = page_table;
     p.lengths = lengths;
-    p.scale_log2 = scale * 1.44269504088896341f;
+    p.scale_log2 = scale_log2;
     p.gs_k = gs_k;
     p.gs_v = gs_v;
     p.out = static_cast<__nv_bfloat16 *>(O_bf16);

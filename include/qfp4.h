@@ -833,6 +833,7 @@ int qfp4_qk_norm_rope_cache(const void *QKV_bf16, int64_t ld, int64_t T, int64_t
  *              that range and report.  What the pages hold beyond a sequence's
  *              length does not count, whatever it is.
  *   window     0, or how many of the last tokens are seen
+ *   scale      any sign; scale * log2(e) must be finite in fp32
  *   O_bf16     [B, q_heads, head_dim]; a sequence without tokens gets zeros
  *   lse        fp32 [B, q_heads] or NULL: ln sum_j exp(scale * q . k_j), -inf
  *              without tokens

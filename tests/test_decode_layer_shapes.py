@@ -1,5 +1,5 @@
-"""Tensors of the right size and the wrong order of axes: the binding of the decoding
-attention layer refuses them (no GPU needed)."""
+"""Refusals of the decoding attention layer beside those of test_decode_layer_abi.py (no
+GPU needed): tensors of the right size and the wrong order of axes, scales of no use."""
 import pytest
 import torch
 
@@ -40,3 +40,18 @@ def test_queries_of_the_attention(calls):  # noqa: F811
         with pytest.raises(ValueError):
             fn(**{**args, "Q": Tensor(BF16, *shape)})
     assert len(calls) == 1
+
+
+def test_scale_of_the_attention():
+    """The kernel works in units of log 2: a scale that is infinite there gives NaN for logits of 0."""
+    lib = qfp4.load()
+    need = lib.qfp4_attention_decode_workspace_bytes(0, 8, 2, 128)
+
+    def call(scale):
+        return lib.qfp4_attention_decode(2, 1 << 40, 1024, 0, 8, 2, 128, 1 << 40, 4, 16, 1 << 40, 2, 1 << 40, 0, scale, 1 << 40, 1 << 40, 1 << 40, None, 1 << 40,
+                                         need, None)
+
+    for scale in (0.0, -1.0, 2.3e38, -2.3e38):
+        assert call(scale) == 0, scale
+    for scale in (2.4e38, -2.9e38, 3.3e38, float("inf"), float("nan")):
+        assert call(scale) == -1, scale
