@@ -693,7 +693,8 @@ int qfp4_moe_route_backward(int logits_type, const void *logits, int64_t T, int6
  * Accuracy: |D - exact| <= 2^-8 |exact| + (K/16 + 16) 2^-23 sum_k |x_k w_k| +
  * 2^-33 max|x| sum_k |w_k| (elements of x below 2^-22 of their row's largest in
  * a slice of 512 lose bits), where no sum leaves fp32's range (scales up to
- * 2^100). */
+ * 2^100).  An infinite element of x gives the infinity of its product's sign, or
+ * NaN where its weight is zero. */
 int qfp4_gemv_nt(int fmt, int64_t M, int64_t N, int64_t K, const void *X_bf16, int64_t ldx,
                  const void *W_packed, const void *W_sf, const float *gs_w, void *D_bf16, int64_t ldd,
                  void *stream);
@@ -848,7 +849,8 @@ int qfp4_qk_norm_rope_cache(const void *QKV_bf16, int64_t ld, int64_t T, int64_t
  * the largest; E4M3: of the weights times their values' scales) or, with a BF16
  * cache, to 16 bits.  Results repeat bit for bit.
  * An infinite value that counts gives NaN (a weight times it is added in two parts),
- * as infinite logits do.
+ * as a logit of +inf does.  One of -inf has no weight; a sequence that has no others
+ * counts as one without tokens.
  * Requirements: cache sizes as above, q_heads a multiple of kv_heads, at most
  * 4096, B <= 2^20, max_pages * page_size <= 2^30, ldq a multiple of 8, Q / cache /
  * O / workspace 16-byte aligned, the rest 4-byte.  B == 0 launches nothing. */

@@ -1,5 +1,5 @@
 """Attention of one new token where its arithmetic has little room: logits whose
-last bit is 16, weights far below a sequence's largest.
+last bit is 16, weights far below a sequence's largest, logits of -inf.
 
 Bounds as in test_attention_decode_gpu.py: half a step of BF16, 2^-8 |o|; the
 logits' error twice over and the rounding of each weight to FP16, (2^-11 + 2^-17
@@ -97,3 +97,25 @@ def test_values_far_below_the_largest_weight(type, below, every, n):
     bound = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -17 * (1 + T)) * size + lost
     assert ((o - want).abs() <= bound).all(), float(((o - want).abs() / bound).max())
     assert ((lse - torch.logsumexp(x, -1)).abs() <= 2.0 ** -18 * T[:, 0] + 2.0 ** -20 + 2.0 ** -22 * lse.abs()).all()
+
+
+def test_logits_of_minus_infinity():
+    """Keys of -inf: their tokens have no weight; where all are such, the sequence counts as one without tokens."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n, D = 300, 64
+    q = torch.rand(4, D, generator=g, device="cuda").bfloat16().float() + 0.5
+    q = q.bfloat16().float()
+    k, v = (torch.randn(n, 1, D, generator=g, device="cuda").bfloat16().float() for _ in range(2))
+    gone = torch.rand(n, generator=g, device="cuda") < 0.7
+    k[gone, 0, 5] = -math.inf
+    o, lse, kv, vv = attend(qfp4.CACHE_BF16, q, k, v, 0.125)
+    keep = ~gone
+    x = q.double() @ kv[keep, 0].t() * 0.125
+    p = torch.softmax(x, -1)
+    want, size = p @ vv[keep, 0], p @ vv[keep, 0].abs()
+    T = (q.double().abs() @ kv[keep, 0].abs().t() * 0.125).max()
+    assert ((o - want).abs() <= 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -17 * (1 + T)) * size).all()
+    assert ((lse - torch.logsumexp(x, -1)).abs() <= 2.0 ** -18 * T + 2.0 ** -20 + 2.0 ** -22 * lse.abs()).all()
+    k[:, 0, 5] = -math.inf
+    o, lse, *_ = attend(qfp4.CACHE_BF16, q, k, v, 0.125)
+    assert (o == 0).all() and (lse == -math.inf).all()
