@@ -8,7 +8,7 @@
 // 6 significant bits), MXFP4's powers of two multiply the fp32 sums of a block, so
 // that their whole range counts.  x becomes FP16 in shared memory, each row of a
 // slice of K multiplied by the power of two that takes its largest element there to
-// [2^8, 2^9): an element loses bits only 2^22 below that, 2^-34 of the largest at
+// [2^8, 2^9): an element loses bits only 2^22 below that, 2^-33 of the largest at
 // most.
 //
 // One CTA of 16 warps per SM, and one wave of them: the groups of 16 rows are dealt
