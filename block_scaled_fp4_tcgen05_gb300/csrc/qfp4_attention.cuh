@@ -30,11 +30,13 @@
 // across the heads' borders; no other warp waits for it until a head ends.
 //
 // Measured (of the copy bandwidth, head_dim 128): BF16 64 ragged sequences of up to
-// 8192 x 8 heads 180 us (0.94), E4M3 102 us (0.85); NVFP4 4 x 131072 x 8 heads 125 us
-// (0.71).  What is left of NVFP4 are instructions: a unit of 16 tokens takes about 330,
-// 64 conversions and 64 multiplications by scales among them, at 2.4 a cycle.  16 warps
-// per SM of 128 registers beat 12 of 168 (131 us against 159 at that time); stages of
-// 64 tokens, which halve the work around each, leave room for 12 warps only (147 us).
+// 8192 x 8 heads 181 us (0.93), E4M3 103 us (0.84); NVFP4 4 x 131072 x 8 heads 123 us
+// (0.73).  What is left of NVFP4 are instructions: a unit of 16 tokens takes about 330,
+// 64 conversions and 64 multiplications by scales among them, at 2.4 a cycle.  Its 16
+// warps per SM of 128 registers beat 12 of 168 (131 us against 159 at that time); stages
+// of 64 tokens, which halve the work around each, leave room for 12 warps only (147 us).
+// With up to 16 queries per key head it has 8 warps of 232 registers (104 us for 16 x
+// 16384 x 8 heads, floor 45).
 // Short calls are a chain of latencies: length, page number, tokens, first products,
 // warps' join, pieces' join; 1 x 4096 tokens x 8 heads take 10.5 us, 3 of them the
 // pieces'.
@@ -87,7 +89,9 @@ __device__ __forceinline__ int attn_join_group(int pieces) { return pieces <= 24
 __host__ __device__ constexpr int attn_piece_floats(int queries, int D) { return queries * (D + 2); }
 
 // Tokens of a warp's stage, stages of its ring, and CTAs per SM that the registers
-// are sized for.
+// are sized for.  Shared memory holds fewer of some: of four warps three in E4M3 and BF16
+// (one in BF16 with 256 elements), of two warps five in E4M3 and six in BF16.  That those
+// forms would gain by registers for what fits is not measured.
 constexpr int attn_stage_tokens(int type, int D)
 {
     return type == QFP4_CACHE_BF16 ? (D == 64 ? 32 : 16) : D == 64 ? 64 : D == 128 ? 32 : 16;
@@ -975,8 +979,8 @@ int attn_launch_one(const AttnParams &p, int most, cudaStream_t s)
 inline bool attn_many(int64_t items, int nt) { return items > (nt == 2 ? 2 : 4) * 152; }
 inline int attn_most_per_sm(int64_t items, int nt) { return attn_many(items, nt) ? 8 : 4; }
 
-// Four warps a CTA, four CTAs on an SM.  Many items: two warps and twice as many CTAs,
-// which hide one another's joins (256 ragged sequences up to 300 tokens x 8 heads: NVFP4
+// Four warps a CTA, up to four CTAs on an SM (three in E4M3 and BF16).  Many items: two
+// warps and up to twice as many CTAs, which hide one another's joins (256 ragged sequences up to 300 tokens x 8 heads: NVFP4
 // 26.4 us, 29.2 with four; E4M3 32.3, 36.2; up to 2000 tokens 81, 86 and 105, 109; one
 // warp 28, 36, 83, 109; 512 items up to 300 tokens 14.4, 13.5; 512 items of 16 query heads
 // up to 1000 tokens E4M3 30, 41, and 128 of up to 16384 as long with either).  Few items in NVFP4: eight

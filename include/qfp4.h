@@ -810,7 +810,9 @@ int qfp4_kv_cache_read(int type, const void *cache, int64_t pages, int64_t page_
  * QKV, unchanged) quantised straight into the cache, from the fp32 values
  * without a rounding to BF16 between.  A row without a position writes nothing;
  * one whose slot is negative or beyond the cache writes its queries only (and
- * reports the latter). */
+ * reports the latter).  Made for new tokens: from about 512 tokens of an NVFP4 cache
+ * and some thousands of an E4M3 one on, qfp4_qk_norm_rope and qfp4_kv_cache_write one
+ * after the other are faster. */
 int qfp4_qk_norm_rope_cache(const void *QKV_bf16, int64_t ld, int64_t T, int64_t q_heads, int64_t kv_heads,
                             int64_t head_dim, const void *q_weight, const void *k_weight, float eps,
                             const float *cos_sin, int64_t table_rows, int64_t rotary_dim, int interleaved,
