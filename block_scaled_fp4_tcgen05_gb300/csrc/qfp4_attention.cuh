@@ -420,9 +420,9 @@ __global__ void __launch_bounds__(32 * WARPS, attn_ctas(TYPE, D, NT, WARPS)) att
                         amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(qf[n][ks][r] << 16)), fabsf(__uint_as_float(qf[n][ks][r] & 0xFFFF0000u))));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                // the exponent that takes amax to [2^14, 2^15); none for zeros and infinities
-                int e = 14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127);
-                e = amax == 0.0f || !(amax < 3.4e38f) ? 0 : max(-126, min(126, e));
+                // the exponent that takes amax to [2^14, 2^15); an infinity takes everything
+                // beside it into FP16's range, so that it alone counts
+                const int e = min(126, 14 - (static_cast<int>(__float_as_uint(amax) >> 23) - 127));
                 const float up = pow2(e);
                 back = pow2(-e);
 #pragma unroll

@@ -1,5 +1,6 @@
 """Attention of one new token where its arithmetic has little room: logits whose
-last bit is 16, weights far below a sequence's largest, logits of -inf.
+last bit is 16, weights far below a sequence's largest, logits of -inf, infinite
+queries.
 
 Bounds as in test_attention_decode_gpu.py: half a step of BF16, 2^-8 |o|; the
 logits' error twice over and the rounding of each weight to FP16, (2^-11 + 2^-17
@@ -119,3 +120,17 @@ def test_logits_of_minus_infinity():
     k[:, 0, 5] = -math.inf
     o, lse, *_ = attend(qfp4.CACHE_BF16, q, k, v, 0.125)
     assert (o == 0).all() and (lse == -math.inf).all()
+
+
+@pytest.mark.parametrize("type", _cache.TYPES)
+def test_infinite_query_beside_large_elements(type):
+    """Every logit is -inf by the one infinite element, whatever the others add: no token counts.  With the other sign they are +inf: NaN."""
+    n, D = 100, 64
+    q = torch.full((2, D), 1e6, device="cuda")
+    q[0, 3], q[1, 3] = math.inf, -math.inf
+    k = torch.ones(n, 1, D, device="cuda")
+    k[:, 0, 3] = -1.0
+    o, lse, kv, _ = attend(type, q, k, torch.ones(n, 1, D, device="cuda"), 0.125, 0.01)
+    assert (kv[:, 0, 3] < 0).all()
+    assert (o[0] == 0).all() and lse[0] == -math.inf
+    assert torch.isnan(o[1]).all() and torch.isnan(lse[1])
