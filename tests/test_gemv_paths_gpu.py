@@ -71,3 +71,24 @@ def test_several_rounds_of_rows(fmt, M, K):
         bound = 2.0 ** -8 * want.abs() + (K / 16 + 16) * 2.0 ** -23 * size + 2.0 ** -33 * far
         assert ((d[:, lo: lo + step].double() - want).abs() <= bound).all(), lo
     assert qfp4.poll_device_status() == 0
+
+
+@pytest.mark.parametrize("fmt", [MX, NV])
+def test_weights_beyond_32_bits(fmt):
+    """4.6 GB of weights, all zero but the last rows."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    N, K, tail, block = 140000, 65536, 200, qfp4.block_size(fmt)
+    code = torch.zeros(N, K // 2, dtype=torch.uint8, device="cuda")
+    sf = torch.full((N, K // block), 127 if fmt == MX else 0x38, dtype=torch.uint8, device="cuda")
+    mma = torch.zeros(qfp4.sf_mma_bytes(N, K // block), dtype=torch.uint8, device="cuda")
+    qfp4.sf_interleave(sf, N, K // block, mma)
+    code[-tail:] = torch.randint(0, 256, (tail, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    x = torch.randn(2, K, generator=g, device="cuda").bfloat16()
+    d = torch.full((2, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    qfp4.gemv_nt(fmt, x, code, mma, None, d)
+    table, c = torch.cat([GRID, -GRID]).cuda(), code[-tail:]
+    w = torch.stack([table[(c & 15).int()], table[(c >> 4).int()]], -1).flatten(1)         # scales of 1
+    want, size = x.double() @ w.t(), x.double().abs() @ w.abs().t()
+    far = x.double().abs().amax(1, keepdim=True) * w.abs().sum(1)
+    assert (d[:, :-tail] == 0).all()
+    assert ((d[:, -tail:].double() - want).abs() <= 2.0 ** -8 * want.abs() + (K / 16 + 16) * 2.0 ** -23 * size + 2.0 ** -33 * far).all()

@@ -77,3 +77,21 @@ def test_sums_of_any_terms(T, H, KV, D, inter):
     _, _, a, b, ma, mb = heads.backward64(s, H, KV, D, D, inter, s["dq"], s["dk"], 1.0)
     for got, want, size in ((dqw, a, ma), (dkw, b, mb)):
         assert ((got.double() - want).abs() <= (chain(T, H, KV, D) + 64) * 2.0 ** -24 * size).all()
+
+
+def test_gradient_offsets_beyond_32_bits():
+    """Rows of every tensor far apart: the last one's offset passes 2^31 elements."""
+    T, H, KV, D, ld = 3, 2, 1, 64, 1 << 30
+    s = heads.inputs(T, H, KV, D, D, True, 3)
+    want, dqw, dkw = heads.check_backward(s, T, H, KV, D, D, False)
+    flat = [torch.zeros(2 * ld + 4 * D, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    qkv, grads, out = (f.as_strided((T, (H + 2 * KV) * D), (ld, 1)) for f in flat)
+    qkv.copy_(s["qkv"])
+    dq, dk = grads[:, : H * D].unflatten(1, (H, D)), grads[:, H * D: (H + KV) * D].unflatten(1, (KV, D))
+    dq.copy_(s["dq"])
+    dk.copy_(s["dk"])
+    a, b = torch.empty(D, device="cuda"), torch.empty(D, device="cuda")
+    ws = torch.empty(qfp4.qk_norm_rope_backward_workspace_bytes(T, H, KV, D), dtype=torch.uint8, device="cuda")
+    qfp4.qk_norm_rope_backward(qkv, H, KV, dq, dk, out, a, b, ws, s["qw"], s["kw"], s["table"], s["pos"], eps=heads.EPS)
+    assert torch.equal(out[:, : (H + KV) * D], want[:, : (H + KV) * D]) and torch.equal(a, dqw) and torch.equal(b, dkw)
+    assert qfp4.poll_device_status() == 0
